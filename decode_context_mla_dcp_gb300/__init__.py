@@ -10,7 +10,9 @@ are buffers on one GPU and one kernel reads them in place.
 The C ABI (include/dcp_lse_reduce.h) is the product; this package is its thin
 binding: ``dcp_lse_reduce`` / ``dcp_lse_reduce_ex`` take raw pointers (or
 tensors) exactly like the C calls, and ``merge`` derives the sizes and strides
-from torch tensors and allocates the outputs.
+from torch tensors and allocates the outputs. ``mla_cache8_append``,
+``mla_cache8_read``, ``mla_cache8_decode`` and ``mla_rope`` (cache8.py) work on an
+8-bit latent cache.
 """
 from __future__ import annotations
 
@@ -26,7 +28,11 @@ from ._binding import (DCP_DTYPE_BF16, DCP_DTYPE_F16, DCP_FLAG_LSE_FIRST, DCP_FL
                        dcp_lse_reduce, dcp_lse_reduce_ex, dcp_lse_reduce_strerror, dcp_lse_reduce_version,
                        DCP_MLA_NOALLOC_SCRATCH_BYTES, dcp_mla_decode, dcp_mla_decode_noalloc,
                        dcp_mla_decode_partial, dcp_mla_decode_smem_bytes,
-                       dcp_mla_decode_workspace_bytes, library_path, load)
+                       dcp_mla_decode_workspace_bytes, library_path, load,
+                       DCP_DTYPE_F32, DCP_MLA_CACHE8_BLOCK_MAX, DCP_MLA_CACHE8_CP_MAX, dcp_mla_rope,
+                       dcp_mla_cache8_append, dcp_mla_cache8_read, dcp_mla_cache8_decode,
+                       dcp_mla_cache8_decode_workspace_bytes, dcp_mla_cache8_strerror)
+from .cache8 import mla_cache8_append, mla_cache8_decode, mla_cache8_read, mla_rope, mla_rope_inv_freq
 
 __all__ = ["dcp_lse_reduce", "dcp_lse_reduce_ex", "dcp_lse_reduce_strerror", "dcp_lse_reduce_version", "merge",
            "dcp_mla_decode_partial", "dcp_mla_decode_smem_bytes", "mla_decode_partial", "DCP_MLA_SPLIT_MAX",
@@ -37,7 +43,11 @@ __all__ = ["dcp_lse_reduce", "dcp_lse_reduce_ex", "dcp_lse_reduce_strerror", "dc
            "DCP_DTYPE_BF16", "DCP_DTYPE_F16", "DCP_FLAG_PDL", "DCP_FLAG_PRELOAD", "DCP_FLAG_LSE_FIRST",
            "DCP_FLAG_PREFETCH",
            "DCP_LSE_REDUCE_CP_MAX", "dcp_mla_decode_kernel", "DCP_MLA_KERNEL_TCGEN05", "DCP_MLA_KERNEL_MMA_SYNC",
-           "dcp_mla_decode_pick_split"]
+           "dcp_mla_decode_pick_split",
+           "mla_rope", "mla_rope_inv_freq", "mla_cache8_append", "mla_cache8_read", "mla_cache8_decode",
+           "dcp_mla_rope", "dcp_mla_cache8_append", "dcp_mla_cache8_read", "dcp_mla_cache8_decode",
+           "dcp_mla_cache8_decode_workspace_bytes", "dcp_mla_cache8_strerror", "DCP_DTYPE_F32",
+           "DCP_MLA_CACHE8_BLOCK_MAX", "DCP_MLA_CACHE8_CP_MAX"]
 
 
 def algorithmic_bytes(cp: int, B: int, H: int, D: int, elem: int = 2, skipped_payload_rows: int = 0) -> int:

@@ -18,6 +18,7 @@ from . import build as _build
 DCP_LSE_REDUCE_CP_MAX = 16
 DCP_DTYPE_BF16 = 0
 DCP_DTYPE_F16 = 1
+DCP_DTYPE_F32 = 2
 DCP_FLAG_PDL = 1
 DCP_FLAG_PRELOAD = 2
 DCP_FLAG_LSE_FIRST = 4
@@ -25,7 +26,11 @@ DCP_FLAG_PREFETCH = 8
 
 EXPORTED_SYMBOLS = ("dcp_lse_reduce", "dcp_lse_reduce_ex", "dcp_lse_reduce_strerror", "dcp_lse_reduce_version",
                     "dcp_mla_decode_partial", "dcp_mla_decode_smem_bytes", "dcp_mla_decode_workspace_bytes",
-                    "dcp_mla_decode", "dcp_mla_decode_noalloc", "dcp_mla_decode_kernel", "dcp_mla_decode_pick_split")
+                    "dcp_mla_decode", "dcp_mla_decode_noalloc", "dcp_mla_decode_kernel", "dcp_mla_decode_pick_split",
+                    "dcp_mla_rope", "dcp_mla_cache8_append", "dcp_mla_cache8_read", "dcp_mla_cache8_decode",
+                    "dcp_mla_cache8_decode_workspace_bytes", "dcp_mla_cache8_strerror")
+DCP_MLA_CACHE8_BLOCK_MAX = 128
+DCP_MLA_CACHE8_CP_MAX = 16
 DCP_MLA_NOALLOC_SCRATCH_BYTES = 32 << 20
 DCP_MLA_SPLIT_MAX = 16
 DCP_MLA_FLAG_MMA_SYNC = 2
@@ -102,6 +107,21 @@ def load(path: str | None = None):
                                                ctypes.c_float, ci, ci, ctypes.POINTER(vp), ctypes.POINTER(vp), vp,
                                                ctypes.c_uint, vp]
         lib.dcp_mla_decode_noalloc.restype = ci
+        cf, pv = ctypes.c_float, ctypes.POINTER(vp)
+        lib.dcp_mla_rope.argtypes = [vp, i64, i64, vp, ci, vp, i64, ci, ci, ci, ci, ci, cf, ci, vp, i64, i64, vp]
+        lib.dcp_mla_rope.restype = ci
+        lib.dcp_mla_cache8_append.argtypes = [vp, i64, vp, i64, ci, i64, i64, ci, vp, vp, pv, pv, ci, i64, ci, ci, vp,
+                                              ci, cf, vp]
+        lib.dcp_mla_cache8_append.restype = ci
+        lib.dcp_mla_cache8_read.argtypes = [pv, pv, ci, i64, i64, ci, ci, ci, vp, vp, i64, vp, i64, ci, vp]
+        lib.dcp_mla_cache8_read.restype = ci
+        lib.dcp_mla_cache8_decode.argtypes = [vp, i64, i64, pv, pv, vp, ci, i64, ci, ci, ci, i64, ci, ci, i64, i64, cf,
+                                              ci, vp, i64, vp, vp, vp, ctypes.c_uint, vp]
+        lib.dcp_mla_cache8_decode.restype = ci
+        lib.dcp_mla_cache8_decode_workspace_bytes.argtypes = [i64, ci, ci]
+        lib.dcp_mla_cache8_decode_workspace_bytes.restype = i64
+        lib.dcp_mla_cache8_strerror.argtypes = [ci]
+        lib.dcp_mla_cache8_strerror.restype = ctypes.c_char_p
         if path is None:
             _lib = lib
         return lib
@@ -234,3 +254,56 @@ def dcp_mla_decode_noalloc(q, kv_ptrs, kv_len_ptrs, cp: int, B: int, H: int, Dk:
                                       int(n_split), _ptr_array(dst_ptrs, cp),
                                       _ptr_array(lse_out_ptrs, cp, allow_none=True), _ptr(status), int(flags),
                                       _stream(stream)))
+
+
+def dcp_mla_rope(x, x_row: int, x_head: int, positions, pos64: bool, inv_freq, N: int, H: int, D: int, start: int,
+                 rot: int, interleaved: bool, mscale: float, dtype: int, out, out_row: int, out_head: int,
+                 stream=None) -> None:
+    """Rotary positions on part of each head (see include/dcp_mla_cache8.h)."""
+    _check8(load().dcp_mla_rope(_ptr(x), int(x_row), int(x_head), _ptr(positions), 1 if pos64 else 0, _ptr(inv_freq),
+                                int(N), int(H), int(D), int(start), int(rot), 1 if interleaved else 0, float(mscale),
+                                int(dtype), _ptr(out), int(out_row), int(out_head), _stream(stream)))
+
+
+def dcp_mla_cache8_append(latent, latent_row: int, k_rope, rope_row: int, dtype: int, N: int, B: int, Dk: int, cu_new,
+                          seq_lens, kv_ptrs, scale_ptrs, cp: int, T: int, block: int = 1, interleave: int = 1,
+                          inv_freq=None, interleaved: bool = True, mscale: float = 1.0, stream=None) -> None:
+    """Quantise new tokens into the 8-bit cache (see include/dcp_mla_cache8.h)."""
+    _check8(load().dcp_mla_cache8_append(_ptr(latent), int(latent_row), _ptr(k_rope), int(rope_row), int(dtype),
+                                         int(N), int(B), int(Dk), _ptr(cu_new), _ptr(seq_lens),
+                                         _ptr_array(kv_ptrs, cp), _ptr_array(scale_ptrs, cp), int(cp), int(T),
+                                         int(block), int(interleave), _ptr(inv_freq), 1 if interleaved else 0,
+                                         float(mscale), _stream(stream)))
+
+
+def dcp_mla_cache8_read(kv_ptrs, scale_ptrs, cp: int, B: int, T: int, Dk: int, block: int, interleave: int, starts, cu,
+                        N: int, out, out_row: int, dtype: int, stream=None) -> None:
+    """Read cached tokens back (see include/dcp_mla_cache8.h)."""
+    _check8(load().dcp_mla_cache8_read(_ptr_array(kv_ptrs, cp), _ptr_array(scale_ptrs, cp), int(cp), int(B), int(T),
+                                       int(Dk), int(block), int(interleave), _ptr(starts), _ptr(cu), int(N),
+                                       _ptr(out), int(out_row), int(dtype), _stream(stream)))
+
+
+def dcp_mla_cache8_decode(q, q_row: int, q_head: int, kv_ptrs, scale_ptrs, seq_lens, cp: int, B: int, H: int, Dk: int,
+                          Dv: int, T: int, block: int, interleave: int, window: int, sinks: int, scale: float,
+                          lse_base_e: bool, workspace, workspace_bytes: int, out, lse=None, status=None,
+                          flags: int = 0, stream=None) -> None:
+    """Single-token attention over the 8-bit cache (see include/dcp_mla_cache8.h)."""
+    _check8(load().dcp_mla_cache8_decode(_ptr(q), int(q_row), int(q_head), _ptr_array(kv_ptrs, cp),
+                                         _ptr_array(scale_ptrs, cp), _ptr(seq_lens), int(cp), int(B), int(H), int(Dk),
+                                         int(Dv), int(T), int(block), int(interleave), int(window), int(sinks),
+                                         float(scale), 1 if lse_base_e else 0, _ptr(workspace), int(workspace_bytes),
+                                         _ptr(out), _ptr(lse), _ptr(status), int(flags), _stream(stream)))
+
+
+def dcp_mla_cache8_decode_workspace_bytes(B: int, H: int, num_sms: int) -> int:
+    return int(load().dcp_mla_cache8_decode_workspace_bytes(int(B), int(H), int(num_sms)))
+
+
+def dcp_mla_cache8_strerror(status: int) -> str:
+    return load().dcp_mla_cache8_strerror(int(status)).decode()
+
+
+def _check8(status: int) -> None:
+    if status != 0:
+        raise DcpError(status, dcp_mla_cache8_strerror(status))

@@ -3,7 +3,7 @@
     python -m decode_context_mla_dcp_gb300.build [--force]
 
 The library lands in decode_context_mla_dcp_gb300/_build/ (git-ignored). It is
-one translation unit compiled for sm_103a only; the CUDA runtime is linked
+a few translation units compiled for sm_103a only; the CUDA runtime is linked
 statically so the library needs nothing beyond the driver at run time.
 """
 from __future__ import annotations
@@ -15,8 +15,10 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SOURCES = [os.path.join(PKG, "csrc", name) for name in ("dcp_lse_reduce.cu", "mla_decode_partial.cu")]
-HEADERS = [os.path.join(ROOT, "include", "dcp_lse_reduce.h"), os.path.join(ROOT, "include", "dcp_mla_decode.h")]
+SOURCES = [os.path.join(PKG, "csrc", name)
+           for name in ("dcp_lse_reduce.cu", "mla_decode_partial.cu", "mla_cache8.cu", "mla_cache8_decode.cu")]
+HEADERS = [os.path.join(ROOT, "include", name)
+           for name in ("dcp_lse_reduce.h", "dcp_mla_decode.h", "dcp_mla_cache8.h")]
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libdcp_lse_reduce.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)

@@ -1,0 +1,310 @@
+"""The 8-bit latent cache from torch tensors: rotary positions, the quantising
+append, the read-back and single-token attention (include/dcp_mla_cache8.h).
+
+A row's cache is [T, 512 latent + 64 rotary] e4m3 (or 512 alone) with one fp32
+scale for each ``block`` consecutive tokens. Under context parallelism position
+p is held by shard (p / interleave) mod cp; calls take one cache and one scale
+tensor per shard, None for a shard that this device does not hold ("[DCP]
+Optimize shared Output, Query, and Indexer/Top-K via peer memory", sglang
+#32851, commit notes on the interleaved KV shards). A serving step chains them:
+
+    mla_rope(q_pe, positions, inv_freq, out=q[..., 512:])
+    mla_cache8_append(latent, k_pe, caches, scales, seq_lens, inv_freq=inv_freq)
+    out, lse = mla_cache8_decode(q, caches, scales, seq_lens + 1, scale)
+
+Streams: everything runs on ``stream`` (default: the current stream of the
+tensors' device); what a call allocates is allocated for that stream. Wrong
+arguments raise ValueError, TypeError or DcpError before anything is launched.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import math
+
+from . import _binding as _b
+
+_DTYPES = None  # torch dtype -> library dtype, filled on first use (torch is imported late)
+_SMS: dict = {}
+
+
+def _types():
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.bfloat16: _b.DCP_DTYPE_BF16, torch.float16: _b.DCP_DTYPE_F16,
+                   torch.float32: _b.DCP_DTYPE_F32}
+    return _DTYPES
+
+
+def _on(device, stream):
+    """(raw stream, context): the stream to launch on, and what to be inside of
+    while allocating and launching (None where that is the present state)."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError("the tensors must be CUDA tensors")
+    here = torch.cuda.current_device() == device.index
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
+        return raw, (None if here else torch.cuda.device(device))
+    if isinstance(stream, int):
+        raw = stream
+        stream = torch.cuda.default_stream(device) if raw == 0 else torch.cuda.ExternalStream(raw, device=device)
+    else:
+        raw = int(stream.cuda_stream)
+        if stream.device != device:
+            raise ValueError("the stream is on another device than the tensors")
+    both = contextlib.ExitStack()
+    both.enter_context(torch.cuda.device(device))
+    both.enter_context(torch.cuda.stream(stream))
+    return raw, both
+
+
+def _sms(device) -> int:
+    n = _SMS.get(device.index)
+    if n is None:
+        import torch
+        n = _SMS[device.index] = int(torch.cuda.get_device_properties(device).multi_processor_count)
+    return n
+
+
+def _ints(name, t, n, device):
+    """A contiguous int32 tensor of n entries (or None)."""
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on the caches' device")
+    return t.data_ptr()
+
+
+def _shards(caches, scales, block):
+    """Check the shards' tensors; (device, B, T, Dk, cache pointers, scale pointers)."""
+    import torch
+    cp = len(caches)
+    if cp < 1 or cp > _b.DCP_MLA_CACHE8_CP_MAX or len(scales) != cp:
+        raise ValueError(f"need 1 to {_b.DCP_MLA_CACHE8_CP_MAX} caches (None for a shard that is not held) and as "
+                         "many scale tensors")
+    if block < 1 or block > _b.DCP_MLA_CACHE8_BLOCK_MAX or block & (block - 1):
+        raise ValueError(f"block must be a power of two, at most {_b.DCP_MLA_CACHE8_BLOCK_MAX}")
+    device = shape = None
+    kv, sc = (ctypes.c_void_p * cp)(), (ctypes.c_void_p * cp)()
+    for j in range(cp):
+        c, s = caches[j], scales[j]
+        if c is None or s is None:
+            if c is not s:
+                raise ValueError("a shard has both a cache and scales, or neither")
+            continue
+        if shape is None:
+            device, shape = c.device, c.shape
+            if len(shape) != 3 or shape[2] not in (512, 576):
+                raise ValueError("a cache must be [B, T, 512] or [B, T, 576]")
+            sshape = (shape[0], -(-shape[1] // block))
+        if c.dtype not in (torch.float8_e4m3fn, torch.uint8) or s.dtype != torch.float32:
+            raise TypeError("caches must be float8_e4m3fn (or uint8 codes) and scales float32")
+        if c.shape != shape or s.shape != sshape or c.device != device or s.device != device:
+            raise ValueError("shards must have one shape and device, and scales [B, ceil(T / block)]")
+        if not (c.is_contiguous() and s.is_contiguous()):
+            raise ValueError("caches and scales must be contiguous")
+        kv[j], sc[j] = c.data_ptr(), s.data_ptr()
+    if shape is None:
+        raise ValueError("no shard is held here")
+    return device, shape[0], shape[1], shape[2], kv, sc
+
+
+def mla_rope_inv_freq(rot: int = 64, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
+                      original_len: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                      mscale: float = 1.0, mscale_all_dim: float = 0.0, device="cuda"):
+    """Radians per position of each rotated pair, and the factor for cos and sin.
+
+    scaling "none": base^(-2i / rot). "linear": divided by ``factor``. "yarn":
+    pairs that turn more than ``beta_fast`` times over ``original_len`` positions
+    keep their frequency, those below ``beta_slow`` turns are divided by
+    ``factor``, those between are blended linearly over the pair index; the
+    factor is (0.1 mscale ln(factor) + 1) / (0.1 mscale_all_dim ln(factor) + 1).
+    Returns (float64 tensor [rot / 2] on ``device``, float), for mla_rope and
+    mla_cache8_append."""
+    import torch
+    if rot < 2 or rot % 2 or base <= 0 or factor < 1 or original_len < 1:
+        raise ValueError("rot must be even and positive, base positive, factor >= 1, original_len >= 1")
+    i = torch.arange(0, rot, 2, dtype=torch.float64)
+    f = base ** (-i / rot)
+    amp = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        if base == 1:
+            raise ValueError("base must not be 1 with yarn")
+        at = [rot * math.log(original_len / (b * 2 * math.pi)) / (2 * math.log(base)) for b in (beta_fast, beta_slow)]
+        lo, hi = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rot - 1)
+        keep = 1 - ((torch.arange(rot // 2, dtype=torch.float64) - lo) / max(hi - lo, 0.001)).clamp(0, 1)
+        f = f / factor * (1 - keep) + f * keep
+        amp = (0.1 * mscale * math.log(factor) + 1) / (0.1 * mscale_all_dim * math.log(factor) + 1)
+    elif scaling != "none":
+        raise ValueError("scaling must be 'none', 'linear' or 'yarn'")
+    return f.to(device), amp
+
+
+def mla_rope(x, positions, inv_freq, *, start: int = 0, interleaved: bool = True, mscale: float = 1.0, out=None,
+             stream=None):
+    """Rotary positions on dims [start, start + 2 len(inv_freq)) of every head.
+
+    x: CUDA bf16, fp16 or fp32 [N, H, D] (unit stride along D). positions: int32
+    or int64 [N]. inv_freq: float64 [rot / 2] (mla_rope_inv_freq). ``interleaved``
+    pairs dims (2i, 2i + 1), otherwise (i, i + rot / 2). out: None allocates
+    [N, H, D]; x itself rotates in place; another tensor or view (unit stride
+    along D, not overlapping x) also receives the dims that are not rotated.
+    Returns out."""
+    import torch
+    if x.dim() != 3:
+        raise ValueError("x must be [N, H, D]")
+    n, h, d = x.shape
+    dtype = _types().get(x.dtype)
+    if dtype is None:
+        raise TypeError("x must be bf16, fp16 or fp32")
+    device = x.device
+    if x.stride(2) != 1 and d > 1:
+        raise ValueError("x needs unit stride along D")
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous() or \
+            inv_freq.device != device:
+        raise ValueError("inv_freq must be a contiguous float64 tensor on x's device")
+    if positions.dtype not in (torch.int64, torch.int32) or positions.shape != (n,) or \
+            not positions.is_contiguous() or positions.device != device:
+        raise ValueError("positions must be a contiguous int32 or int64 tensor [N] on x's device")
+    raw, inside = _on(device, stream)
+    with inside or contextlib.nullcontext():
+        if out is None:
+            out = torch.empty((n, h, d), dtype=x.dtype, device=device)
+        elif out is not x:
+            if out.shape != x.shape or out.dtype != x.dtype or out.device != device or (out.stride(2) != 1 and d > 1):
+                raise ValueError("out must have x's shape, dtype and device, and unit stride along D")
+            gap = abs(out.data_ptr() - x.data_ptr()) // x.element_size()
+            if 0 < gap < d and n * h > 0 and x.untyped_storage().data_ptr() == out.untyped_storage().data_ptr():
+                raise ValueError("out overlaps x: pass x itself to rotate in place")
+        _b._check8(_b.load().dcp_mla_rope(x.data_ptr(), x.stride(0), x.stride(1), positions.data_ptr(),
+                                      positions.dtype == torch.int64, inv_freq.data_ptr(), n, h, d, start,
+                                      2 * inv_freq.shape[0], interleaved, mscale, dtype, out.data_ptr(),
+                                      out.stride(0), out.stride(1), raw))
+    return out
+
+
+def mla_cache8_append(latent, k_rope, caches, scales, seq_lens, *, cu_new=None, block: int = 1, interleave: int = 1,
+                      inv_freq=None, interleaved: bool = True, mscale: float = 1.0, stream=None) -> None:
+    """Quantise new tokens into the caches, in place.
+
+    latent: bf16 or fp16 [N, 512]; k_rope: [N, 64] of the same type, or None for
+    512-wide caches (unit inner strides, row strides multiples of 8). Row b's new
+    tokens are latent[cu_new[b]:cu_new[b + 1]] (int32 [B + 1]; None: N / B each),
+    at positions seq_lens[b], ... (int32 [B]: the lengths before the call). With
+    inv_freq (float64 [32]) k_rope is rotated on the way. A block's scale is the
+    smallest power of two that holds its values; a block that already holds
+    tokens is requantised where its scale grows."""
+    import torch
+    device, B, T, dk, kv, sc = _shards(caches, scales, block)
+    dtype = _types().get(latent.dtype)
+    if dtype is None or dtype == _b.DCP_DTYPE_F32:
+        raise TypeError("latent must be bf16 or fp16")
+    n = latent.shape[0]
+    if latent.dim() != 2 or latent.shape[1] != 512 or latent.stride(1) != 1 or latent.device != device:
+        raise ValueError("latent must be [N, 512] with unit inner stride, on the caches' device")
+    rope_ptr, rope_row = None, 0
+    if dk == 576:
+        if k_rope is None or k_rope.shape != (n, 64) or k_rope.dtype != latent.dtype or k_rope.stride(1) != 1 or \
+                k_rope.device != device:
+            raise ValueError("k_rope must be [N, 64] of latent's dtype with unit inner stride, on the caches' device")
+        rope_ptr, rope_row = k_rope.data_ptr(), k_rope.stride(0)
+    elif k_rope is not None or inv_freq is not None:
+        raise ValueError("512-wide caches have no rotary part: k_rope and inv_freq must be None")
+    freq_ptr = None
+    if inv_freq is not None:
+        if inv_freq.dtype != torch.float64 or inv_freq.shape != (32,) or not inv_freq.is_contiguous() or \
+                inv_freq.device != device:
+            raise ValueError("inv_freq must be a contiguous float64 tensor [32] on the caches' device")
+        freq_ptr = inv_freq.data_ptr()
+    lens = _ints("seq_lens", seq_lens, B, device)
+    if lens is None:
+        raise ValueError("seq_lens is required")
+    cu = _ints("cu_new", cu_new, B + 1, device)
+    raw, inside = _on(device, stream)
+    with inside or contextlib.nullcontext():
+        _b._check8(_b.load().dcp_mla_cache8_append(latent.data_ptr(), latent.stride(0), rope_ptr, rope_row, dtype, n, B,
+                                               dk, cu, lens, kv, sc, len(caches), T, block, interleave, freq_ptr,
+                                               interleaved, mscale, raw))
+
+
+def mla_cache8_read(caches, scales, total: int, *, starts=None, cu=None, block: int = 1, interleave: int = 1,
+                    dtype=None, out=None, stream=None):
+    """Cached tokens as numbers: out[cu[b] + i] is position starts[b] + i of row b.
+
+    total: packed tokens in all; cu: int32 [B + 1] (None: total / B each); starts:
+    int32 [B] (None: 0). dtype: bf16 (default), fp16 or fp32. out: None allocates
+    [total, Dk]; or a tensor of that shape, unit inner stride, rows and base on
+    16-byte boundaries. Tokens that no held shard has are left as they were.
+    Returns out."""
+    import torch
+    device, B, T, dk, kv, sc = _shards(caches, scales, block)
+    if total < 0:
+        raise ValueError("total must not be negative")
+    dtype = (torch.bfloat16 if out is None else out.dtype) if dtype is None else dtype
+    code = _types().get(dtype)
+    if code is None:
+        raise TypeError("dtype must be bf16, fp16 or fp32")
+    start_ptr, cu_ptr = _ints("starts", starts, B, device), _ints("cu", cu, B + 1, device)
+    raw, inside = _on(device, stream)
+    with inside or contextlib.nullcontext():
+        if out is None:
+            out = torch.empty((total, dk), dtype=dtype, device=device)
+        elif out.shape != (total, dk) or out.dtype != dtype or out.device != device or out.stride(1) != 1:
+            raise ValueError("out must be [total, Dk] of dtype with unit inner stride, on the caches' device")
+        _b._check8(_b.load().dcp_mla_cache8_read(kv, sc, len(caches), B, T, dk, block, interleave, start_ptr, cu_ptr,
+                                             total, out.data_ptr(), out.stride(0), code, raw))
+    return out
+
+
+def mla_cache8_decode(q, caches, scales, seq_lens, scale: float, *, block: int = 1, interleave: int = 1,
+                      window: int = 0, sinks: int = 0, lse_base_e: bool = True, out=None, lse=None, workspace=None,
+                      status=None, flags: int = 0, stream=None):
+    """Single-token attention over the cached positions of each row.
+
+    q: CUDA bf16 [B, H, Dk] (unit stride along Dk, even row and head strides);
+    seq_lens: int32 [B] cached positions over all shards. window > 0 limits a row
+    to its last ``window`` positions and its first ``sinks``. Returns (out, lse):
+    bf16 [B, H, 512] and fp32 [B, H] (base e, or 2); heads [r H/cp, (r + 1) H/cp)
+    of out are what destination r of mla_decode_dcp receives. With some shards
+    None the result is the partial over the held ones, for ``merge``. workspace: a
+    uint8 CUDA tensor of dcp_mla_cache8_decode_workspace_bytes, allocated when not
+    given. status: None, or an int32 CUDA tensor (see the C header)."""
+    import torch
+    device, B, T, dk, kv, sc = _shards(caches, scales, block)
+    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != dk or q.dtype != torch.bfloat16 or q.stride(2) != 1 or \
+            q.device != device:
+        raise ValueError("q must be bf16 [B, H, Dk] with unit inner stride, on the caches' device")
+    H = q.shape[1]
+    lens = _ints("seq_lens", seq_lens, B, device)
+    if lens is None:
+        raise ValueError("seq_lens is required")
+    lib = _b.load()
+    raw, inside = _on(device, stream)
+    with inside or contextlib.nullcontext():
+        if out is None:
+            out = torch.empty((B, H, 512), dtype=torch.bfloat16, device=device)
+        elif out.shape != (B, H, 512) or out.dtype != torch.bfloat16 or out.device != device or \
+                not out.is_contiguous():
+            raise ValueError("out must be a contiguous bf16 tensor [B, H, 512] on the caches' device")
+        if lse is None:
+            lse = torch.empty((B, H), dtype=torch.float32, device=device)
+        elif lse.shape != (B, H) or lse.dtype != torch.float32 or lse.device != device or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous fp32 tensor [B, H] on the caches' device")
+        if workspace is None:
+            need = lib.dcp_mla_cache8_decode_workspace_bytes(B, H, _sms(device))
+            workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=device)
+        elif workspace.device != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the caches' device")
+        if status is not None and (status.dtype != torch.int32 or status.device != device or status.numel() < 1):
+            raise ValueError("status must be an int32 tensor on the caches' device")
+        _b._check8(lib.dcp_mla_cache8_decode(q.data_ptr(), q.stride(0), q.stride(1), kv, sc, lens, len(caches), B, H, dk,
+                                         512, T, block, interleave, window, sinks, scale, lse_base_e,
+                                         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                         out.data_ptr(), lse.data_ptr(),
+                                         None if status is None else status.data_ptr(), flags, raw))
+    return out, lse

@@ -1,0 +1,755 @@
+// The 8-bit latent cache's elementwise operators, sm_103a: rotary positions, the
+// quantising append and the read-back. What they compute, and the cache's
+// format, are stated in include/dcp_mla_cache8.h; the attention over the cache
+// is in mla_cache8_decode.cu.
+//
+// All three move bytes and compute little: a few operations per element
+// against 2 to 4 bytes. Their floors are DRAM time for large calls and one
+// launch plus a few dependent memory round trips for small ones. So loads are
+// 8 or 16 bytes a lane and issued before any is used, and everything that a
+// token needs (its row, shard, place, angles) is found once and shared.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "dcp_lse_reduce.h"
+#include "dcp_mla_cache8.h"
+
+namespace {
+
+constexpr int kLatent = 512;
+constexpr int kCpMax = DCP_MLA_CACHE8_CP_MAX;
+constexpr int kMinExp = -60;              // a scale is at least 2^-60
+constexpr int64_t kMaxInterleave = 1 << 24;
+
+// ---- element types -------------------------------------------------------------
+
+struct Bf16 {
+    using T = uint16_t;
+    __device__ static float get(T v) { return __uint_as_float((uint32_t)v << 16); }
+    __device__ static T put(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+};
+struct F16 {
+    using T = uint16_t;
+    __device__ static float get(T v) { return __half2float(__ushort_as_half(v)); }
+    __device__ static T put(float x) { return __half_as_ushort(__float2half_rn(x)); }
+};
+struct F32 {
+    using T = float;
+    __device__ static float get(T v) { return v; }
+    __device__ static T put(float x) { return x; }
+};
+
+// The low and high 16-bit element of a 32-bit word.
+template <class E>
+__device__ __forceinline__ float get_lo(uint32_t w) { return E::get((uint16_t)(w & 0xffffu)); }
+template <class E>
+__device__ __forceinline__ float get_hi(uint32_t w) { return E::get((uint16_t)(w >> 16)); }
+
+// ---- angles --------------------------------------------------------------------
+
+// Turns per position as a 64-bit fraction of a turn: multiplying it by a
+// position wraps at whole turns exactly, so a far position loses nothing but
+// what the double held (2^-53 of the frequency).
+__device__ __forceinline__ uint64_t turns_of(double inv_freq) {
+    const double u = inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
+    return (uint64_t)((u - floor(u)) * 18446744073709551616.0);
+}
+
+// cos and sin of position * frequency, from the top 32 bits of the wrapped
+// product read as half turns in [-1, 1).
+__device__ __forceinline__ void angle_of(int64_t pos, uint64_t turns, float* c, float* s) {
+    const uint64_t phase = (uint64_t)pos * turns;
+    sincospif((float)(int32_t)(uint32_t)(phase >> 32) * 4.656612873077393e-10f, s, c);  // 2^-31
+}
+
+// ---- rotary positions ------------------------------------------------------------
+
+struct RopeParams {
+    const void* x;
+    void* out;
+    const void* positions;
+    const double* inv_freq;
+    int64_t x_row, x_head, out_row, out_head;  // elements
+    int64_t N;
+    int H, start, half;      // half = rot / 2
+    int interleaved, pos64, copy;
+    float mscale;
+    int tokens;              // tokens of a CTA
+    int heads;               // heads of a CTA
+    int rot_units, units;    // work units of a head: rotating ones first, then copied ones
+    uint32_t units_magic;    // ceil(2^32 / units): idx / units for idx * units < 2^32
+    uint32_t heads_magic;
+    int copy_lead;           // copied units before the rotated dims
+};
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeAngles = 2048;  // cos/sin pairs a CTA holds
+
+// One CTA: `tokens` tokens x `heads` heads. Their angles (64-bit multiply,
+// sincos) are computed once into shared memory and used by every head; a unit is
+// then kV elements (16 bytes): kV/2 interleaved pairs, or kV pairs of the two
+// halves, or kV copied elements. kV = 1 is the form for sizes or strides that are
+// not multiples of 16 bytes: a unit is one pair or one copied element.
+template <class E, int kV>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+    using T = typename E::T;
+    __shared__ float2 cs[kRopeAngles];
+    const int64_t n0 = (int64_t)blockIdx.x * p.tokens;
+    const int ntok = (int)(p.N - n0 < p.tokens ? p.N - n0 : p.tokens);
+    const int h0 = blockIdx.y * p.heads;
+    const int nh = p.H - h0 < p.heads ? p.H - h0 : p.heads;
+    for (int i = threadIdx.x; i < ntok * p.half; i += kRopeThreads) {
+        const int t = i / p.half, f = i - t * p.half;
+        const int64_t pos = p.pos64 ? static_cast<const int64_t*>(p.positions)[n0 + t]
+                                    : (int64_t) static_cast<const int32_t*>(p.positions)[n0 + t];
+        float c, s;
+        angle_of(pos, turns_of(p.inv_freq[f]), &c, &s);
+        cs[i] = make_float2(c * p.mscale, s * p.mscale);
+    }
+    __syncthreads();
+    const int total = ntok * nh * p.units;
+    struct alignas(kV * sizeof(T)) Vec { T e[kV]; };
+    const T* const x = static_cast<const T*>(p.x);
+    T* const out = static_cast<T*>(p.out);
+#pragma unroll 2
+    for (int i = threadIdx.x; i < total; i += kRopeThreads) {
+        const int th = p.units == 1 ? i : (int)__umulhi((uint32_t)i, p.units_magic);
+        const int u = i - th * p.units;
+        const int t = nh == 1 ? th : (int)__umulhi((uint32_t)th, p.heads_magic), h = th - t * nh;
+        const T* const xr = x + (n0 + t) * p.x_row + (h0 + h) * p.x_head;
+        T* const orow = out + (n0 + t) * p.out_row + (h0 + h) * p.out_head;
+        const float2* const a = cs + t * p.half;
+        if (u >= p.rot_units) {  // a copied unit, before or behind the rotated dims
+            const int c = u - p.rot_units;
+            const int d = c < p.copy_lead ? c * kV : p.start + 2 * p.half + (c - p.copy_lead) * kV;
+            *reinterpret_cast<Vec*>(orow + d) = *reinterpret_cast<const Vec*>(xr + d);
+        } else if (p.interleaved) {
+            constexpr int kP = kV > 1 ? kV / 2 : 1;  // pairs of the unit
+            struct alignas(kV > 1 ? sizeof(T) * kV : sizeof(T)) Pairs { T e[2 * kP]; };
+            const int d = p.start + u * 2 * kP;
+            Pairs v = *reinterpret_cast<const Pairs*>(xr + d), w;
+#pragma unroll
+            for (int k = 0; k < kP; ++k) {
+                const float2 r = a[u * kP + k];
+                const float f = E::get(v.e[2 * k]), g = E::get(v.e[2 * k + 1]);
+                w.e[2 * k] = E::put(f * r.x - g * r.y);
+                w.e[2 * k + 1] = E::put(g * r.x + f * r.y);
+            }
+            *reinterpret_cast<Pairs*>(orow + d) = w;
+        } else {
+            const int d = p.start + u * kV;
+            Vec v0 = *reinterpret_cast<const Vec*>(xr + d), v1 = *reinterpret_cast<const Vec*>(xr + d + p.half);
+#pragma unroll
+            for (int k = 0; k < kV; ++k) {
+                const float2 r = a[u * kV + k];
+                const float f = E::get(v0.e[k]), g = E::get(v1.e[k]);
+                v0.e[k] = E::put(f * r.x - g * r.y);
+                v1.e[k] = E::put(g * r.x + f * r.y);
+            }
+            *reinterpret_cast<Vec*>(orow + d) = v0;
+            *reinterpret_cast<Vec*>(orow + d + p.half) = v1;
+        }
+    }
+}
+
+// ---- rows of packed tokens ----------------------------------------------------------
+
+// Row of packed token n: a b with cu[b] <= n < cu[b + 1], whatever cu holds; -1
+// before cu[0] or past cu[B].
+__device__ __forceinline__ int row_of(const int32_t* cu, int B, int64_t n) {
+    if (n < cu[0] || n >= cu[B]) return -1;
+    int lo = 0, hi = B;  // cu[lo] <= n < cu[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cu[mid] <= n) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// Shard j's share of the first L positions of a row.
+__device__ __forceinline__ uint32_t held_tokens(uint32_t L, int j, uint32_t cp, uint32_t interleave) {
+    if (cp == 1) return L;
+    const uint32_t round = cp * interleave, q = L / round, r = L - q * round, lo = (uint32_t)j * interleave;
+    const uint32_t part = r > lo ? r - lo : 0;
+    return q * interleave + (part < interleave ? part : interleave);
+}
+
+// ---- quantising ----------------------------------------------------------------------
+
+// Exponent k of the smallest power of two with a <= 448 * 2^k, at least -60.
+// 448 = 1.75 * 2^8: a = m * 2^e with 1 <= m < 2 needs k = e - 8, or e - 7 above 1.75.
+__device__ __forceinline__ int scale_exp(float a) {
+    const uint32_t u = __float_as_uint(a);
+    const int e = (int)(u >> 23) - 127;
+    const int k = e - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return k < kMinExp ? kMinExp : k;  // (a subnormal or zero a has e = -127)
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
+// |x| of a finite x, 0 of a NaN or an infinity
+__device__ __forceinline__ float mag(float x) { return finite(x) ? fabsf(x) : 0.f; }
+// Two e4m3 codes (first in the low byte), round to nearest even; NaN where x is not finite.
+__device__ __forceinline__ uint32_t codes2(float x, float y, float inv) {
+    const float a = finite(x) ? x * inv : __uint_as_float(0x7fffffffu);
+    const float b = finite(y) ? y * inv : __uint_as_float(0x7fffffffu);
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 values2(uint32_t codes) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xffffu), __NV_E4M3);
+    return __half22float2(__half2(h));
+}
+
+struct AppendParams {
+    const uint8_t* latent;
+    const uint8_t* k_rope;
+    int64_t latent_row, rope_row;  // bytes
+    const int32_t* cu;             // or NULL: `even` tokens a row
+    const int32_t* seq_lens;
+    const double* inv_freq;
+    uint8_t* kv[kCpMax];
+    float* scales[kCpMax];
+    int64_t N, T, blocks;          // blocks: scales of a row
+    int B, Dk, even;
+    uint32_t cp, interleave;
+    int block_log2, interleaved;
+    float mscale;
+};
+
+// A token in a warp's registers: lane l holds latent dims 8l .. 8l+7 and
+// 256 + 8l .. 256 + 8l + 7 as they are, and the rotated rotary pair l.
+struct Token {
+    uint4 v[2];
+    float r0, r1;
+};
+
+template <class E>
+__device__ __forceinline__ void load_token(const AppendParams& p, int64_t src, int lane, Token* t, uint32_t* rope) {
+    const uint4* const row = reinterpret_cast<const uint4*>(p.latent + src * p.latent_row);
+    t->v[0] = __ldg(row + lane);
+    t->v[1] = __ldg(row + 32 + lane);
+    if (p.Dk > kLatent) {
+        const uint8_t* const r = p.k_rope + src * p.rope_row;
+        if (p.interleaved) {
+            *rope = __ldg(reinterpret_cast<const uint32_t*>(r) + lane);
+        } else {
+            const uint16_t* const e = reinterpret_cast<const uint16_t*>(r);
+            *rope = (uint32_t)__ldg(e + lane) | ((uint32_t)__ldg(e + 32 + lane) << 16);
+        }
+    }
+}
+
+template <class E>
+__device__ __forceinline__ void turn_token(const AppendParams& p, uint32_t rope, bool rotate, uint64_t turns,
+                                           int64_t pos, Token* t) {
+    t->r0 = t->r1 = 0.f;
+    if (p.Dk > kLatent) {
+        t->r0 = get_lo<E>(rope);
+        t->r1 = get_hi<E>(rope);
+        if (rotate) {
+            float c, s;
+            angle_of(pos, turns, &c, &s);
+            c *= p.mscale;
+            s *= p.mscale;
+            const float a = t->r0, b = t->r1;
+            t->r0 = a * c - b * s;
+            t->r1 = b * c + a * s;
+        }
+    }
+}
+
+template <class E>
+__device__ __forceinline__ float token_peak(const Token& t) {
+    float a = fmaxf(mag(t.r0), mag(t.r1));
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t w[4] = {t.v[k].x, t.v[k].y, t.v[k].z, t.v[k].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a = fmaxf(a, fmaxf(mag(get_lo<E>(w[i])), mag(get_hi<E>(w[i]))));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    return a;
+}
+
+template <class E>
+__device__ __forceinline__ void store_token(const AppendParams& p, const Token& t, uint8_t* dst, int lane, float inv) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t w[4] = {t.v[k].x, t.v[k].y, t.v[k].z, t.v[k].w};
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = codes2(get_lo<E>(w[i]), get_hi<E>(w[i]), inv);
+        *reinterpret_cast<uint2*>(dst + 256 * k + 8 * lane) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    }
+    if (p.Dk > kLatent) {
+        const uint32_t c = codes2(t.r0, t.r1, inv);
+        if (p.interleaved) {
+            *reinterpret_cast<uint16_t*>(dst + kLatent + 2 * lane) = (uint16_t)c;
+        } else {
+            dst[kLatent + lane] = (uint8_t)c;
+            dst[kLatent + 32 + lane] = (uint8_t)(c >> 8);
+        }
+    }
+}
+
+// Where packed token n goes. False: nowhere.
+struct Place {
+    int row, shard;
+    uint32_t first, count, len;  // the row's first packed token, its new tokens, its length before
+    uint32_t pos, loc;
+};
+__device__ __forceinline__ bool place_of(const AppendParams& p, const int32_t* cu, int64_t n, Place* w) {
+    if (p.cu != nullptr) {
+        w->row = row_of(cu, p.B, n);
+        if (w->row < 0) return false;
+        const int64_t first = cu[w->row], last = cu[w->row + 1] < p.N ? cu[w->row + 1] : p.N;
+        if (first < 0) return false;
+        w->first = (uint32_t)first;
+        w->count = (uint32_t)(last - first);
+    } else {
+        w->row = (int)((uint32_t)n / (uint32_t)p.even);
+        w->first = (uint32_t)w->row * (uint32_t)p.even;
+        w->count = (uint32_t)p.even;
+    }
+    const int32_t len = p.seq_lens[w->row];
+    w->len = len < 0 ? 0u : (uint32_t)len;
+    w->pos = w->len + ((uint32_t)n - w->first);
+    if (p.cp == 1) {
+        w->shard = 0;
+        w->loc = w->pos;
+    } else {
+        const uint32_t turn = w->pos / p.interleave, q = turn / p.cp;
+        w->shard = (int)(turn - q * p.cp);
+        w->loc = q * p.interleave + (w->pos - turn * p.interleave);
+    }
+    return true;
+}
+
+// Each token its own scale: a warp takes a token, one round trip for its data.
+template <class E>
+__global__ void __launch_bounds__(128) append_token_kernel(const __grid_constant__ AppendParams p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t n = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (n >= p.N) return;
+    Token t;
+    uint32_t rope = 0;
+    load_token<E>(p, n, lane, &t, &rope);  // the packed inputs have N rows, whether the token has a place or not
+    const bool rotate = p.inv_freq != nullptr;
+    const double f = rotate ? p.inv_freq[lane] : 0.0;
+    Place w;
+    if (!place_of(p, p.cu, n, &w) || (int64_t)w.loc >= p.T) return;
+    uint8_t* const kv = p.kv[w.shard];
+    if (kv == nullptr) return;
+    turn_token<E>(p, rope, rotate, turns_of(f), (int64_t)w.pos, &t);
+    const int k = scale_exp(token_peak<E>(t));
+    const int64_t at = (int64_t)w.row * p.T + w.loc;
+    store_token<E>(p, t, kv + at * p.Dk, lane, pow2(-k));
+    if (lane == 0) p.scales[w.shard][at] = pow2(k);
+}
+
+// Blocks of tokens. The first new token of a block (of a row, on a shard) stands
+// for it; the CTA that looks at that token writes the whole block: the block's
+// new tokens in registers (kTok a warp, every load in flight at once), their
+// peak, the scale, the tokens that the block held before if the scale grows, and
+// the new codes. CTA c looks at tokens c, c + G, c + 2G, ... with G odd, so that
+// first tokens, which stand a power of two apart, spread over all CTAs.
+constexpr int kBlockWarps = 16;
+constexpr int kCuShared = 1024;
+constexpr int kAppendGrid = 1217;  // odd, about eight CTAs a multiprocessor
+
+template <class E, int kTok>
+__global__ void __launch_bounds__(32 * kBlockWarps) append_block_kernel(const __grid_constant__ AppendParams p) {
+    __shared__ int32_t cu_s[kCuShared + 1];
+    __shared__ int32_t list[32 * kBlockWarps];
+    __shared__ int found;
+    __shared__ float peak_s[kBlockWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int32_t* cu = p.cu;
+    if (cu != nullptr && p.B <= kCuShared) {
+        for (int i = tid; i <= p.B; i += 32 * kBlockWarps) cu_s[i] = cu[i];
+        cu = cu_s;
+    }
+    const bool rotate = p.inv_freq != nullptr;
+    const uint64_t turns = rotate ? turns_of(p.inv_freq[lane]) : 0;
+    const uint32_t block = 1u << p.block_log2;
+    for (int64_t base = blockIdx.x; base < p.N; base += (int64_t)gridDim.x * (32 * kBlockWarps)) {
+        __syncthreads();
+        if (tid == 0) found = 0;
+        __syncthreads();
+        const int64_t n = base + (int64_t)tid * gridDim.x;
+        Place w;
+        if (n < p.N && place_of(p, cu, n, &w) && (int64_t)w.loc < p.T && p.kv[w.shard] != nullptr) {
+            const uint32_t held = held_tokens(w.len, w.shard, p.cp, p.interleave);
+            if (w.loc == held || (w.loc & (block - 1)) == 0) list[atomicAdd(&found, 1)] = tid;
+        }
+        __syncthreads();
+        const int nfound = found;
+        for (int i = 0; i < nfound; ++i) {  // (in any order: blocks are independent of each other)
+            (void)place_of(p, cu, base + (int64_t)list[i] * gridDim.x, &w);
+            uint8_t* const kv = p.kv[w.shard] + (int64_t)w.row * p.T * p.Dk;
+            float* const scale = p.scales[w.shard] + (int64_t)w.row * p.blocks + (w.loc >> p.block_log2);
+            const uint32_t b0 = w.loc & ~(block - 1);
+            uint32_t end = held_tokens(w.len + w.count, w.shard, p.cp, p.interleave);
+            if (end > b0 + block) end = b0 + block;
+            if ((int64_t)end > p.T) end = (uint32_t)p.T;
+            const float old = b0 < w.loc ? *scale : 0.f;  // the present scale counts where the block holds tokens
+            Token t[kTok];
+            uint32_t rope[kTok], pos[kTok];
+#pragma unroll
+            for (int k = 0; k < kTok; ++k) {
+                const uint32_t loc = w.loc + warp + k * kBlockWarps;
+                if (loc < end) {
+                    pos[k] = p.cp == 1 ? loc
+                                       : (loc / p.interleave * p.cp + w.shard) * p.interleave + loc % p.interleave;
+                    load_token<E>(p, (int64_t)w.first + (pos[k] - w.len), lane, &t[k], &rope[k]);
+                }
+            }
+            float peak = 0.f;
+#pragma unroll
+            for (int k = 0; k < kTok; ++k)
+                if (w.loc + warp + k * kBlockWarps < end) {
+                    turn_token<E>(p, rope[k], rotate, turns, (int64_t)pos[k], &t[k]);
+                    peak = fmaxf(peak, token_peak<E>(t[k]));
+                }
+            if (lane == 0) peak_s[warp] = peak;
+            __syncthreads();
+            peak = 0.f;
+#pragma unroll
+            for (int k = 0; k < kBlockWarps; ++k) peak = fmaxf(peak, peak_s[k]);
+            const int e = scale_exp(peak);
+            float s = pow2(e);
+            if (old > s) s = old;
+            const float inv = 1.0f / s;
+#pragma unroll
+            for (int k = 0; k < kTok; ++k) {
+                const uint32_t loc = w.loc + warp + k * kBlockWarps;
+                if (loc < end) store_token<E>(p, t[k], kv + (int64_t)loc * p.Dk, lane, inv);
+            }
+            if (b0 < w.loc && s > old) {  // requantise what the block held
+                const float ratio = old / s;
+                for (uint32_t loc = b0 + warp; loc < w.loc; loc += kBlockWarps) {
+                    uint32_t* const row = reinterpret_cast<uint32_t*>(kv + (int64_t)loc * p.Dk);
+                    for (int c = lane; c < p.Dk / 4; c += 32) {
+                        const uint32_t u = row[c];
+                        const float2 a = values2(u), b = values2(u >> 16);
+                        row[c] = codes2(a.x, a.y, ratio) | (codes2(b.x, b.y, ratio) << 16);
+                    }
+                }
+            }
+            if (tid == 0) *scale = s;
+            __syncthreads();  // peak_s is used again
+        }
+    }
+}
+
+// ---- read-back -------------------------------------------------------------------------
+
+struct ReadParams {
+    const uint8_t* kv[kCpMax];
+    const float* scales[kCpMax];
+    const int32_t* starts;
+    const int32_t* cu;
+    uint8_t* out;
+    int64_t out_row;  // bytes
+    int64_t N, T, blocks;
+    int B, even, block_log2;
+    uint32_t cp, interleave;
+    int tokens;       // tokens of a CTA
+};
+
+constexpr int kReadThreads = 288;  // 72 x 4: with 8 codes a thread, four tokens of 576 a sweep
+constexpr int kReadTokens = 32;
+
+// A CTA finds its tokens' places once, then moves 8 codes a thread: 8-byte
+// loads, 16-byte stores of 16-bit values, both contiguous over the token.
+template <class E, int kDk>
+__global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadParams p) {
+    using T = typename E::T;
+    constexpr int kUnits = kDk / 8;
+    __shared__ const uint8_t* src_s[kReadTokens];
+    __shared__ float scale_s[kReadTokens];
+    const int64_t n0 = (int64_t)blockIdx.x * p.tokens;
+    const int ntok = (int)(p.N - n0 < p.tokens ? p.N - n0 : p.tokens);
+    if ((int)threadIdx.x < ntok) {
+        const int64_t n = n0 + threadIdx.x;
+        const uint8_t* src = nullptr;
+        float s = 0.f;
+        int row = -1;
+        uint32_t i = 0;
+        if (p.cu != nullptr) {
+            row = row_of(p.cu, p.B, n);
+            if (row >= 0) i = (uint32_t)(n - p.cu[row]);
+        } else {
+            row = (int)((uint32_t)n / (uint32_t)p.even);
+            i = (uint32_t)n - (uint32_t)row * (uint32_t)p.even;
+        }
+        if (row >= 0) {
+            const int32_t start = p.starts != nullptr ? p.starts[row] : 0;
+            const int64_t pos64 = (int64_t)start + i;
+            if (pos64 >= 0) {
+                const uint32_t pos = (uint32_t)pos64;
+                int shard = 0;
+                uint32_t loc = pos;
+                if (p.cp > 1) {
+                    const uint32_t turn = pos / p.interleave, q = turn / p.cp;
+                    shard = (int)(turn - q * p.cp);
+                    loc = q * p.interleave + (pos - turn * p.interleave);
+                }
+                if ((int64_t)loc < p.T && p.kv[shard] != nullptr) {
+                    src = p.kv[shard] + ((int64_t)row * p.T + loc) * kDk;
+                    s = p.scales[shard][(int64_t)row * p.blocks + (loc >> p.block_log2)];
+                }
+            }
+        }
+        src_s[threadIdx.x] = src;
+        scale_s[threadIdx.x] = s;
+    }
+    __syncthreads();
+    const int total = ntok * kUnits;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < total; i += kReadThreads) {
+        const int t = i / kUnits, u = i - t * kUnits;
+        const uint8_t* const src = src_s[t];
+        if (src == nullptr) continue;
+        const uint2 c = __ldg(reinterpret_cast<const uint2*>(src) + u);
+        const float s = scale_s[t];
+        const float2 a = values2(c.x), b = values2(c.x >> 16), d = values2(c.y), e = values2(c.y >> 16);
+        struct alignas(16) Vec { T e[8]; } v = {{E::put(a.x * s), E::put(a.y * s), E::put(b.x * s), E::put(b.y * s),
+                                                 E::put(d.x * s), E::put(d.y * s), E::put(e.x * s), E::put(e.y * s)}};
+        *reinterpret_cast<Vec*>(p.out + (n0 + t) * p.out_row + (int64_t)u * sizeof(Vec)) = v;
+    }
+}
+
+// ---- host side ---------------------------------------------------------------------------
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int launched() {
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? 0 : (int)e;
+}
+
+int log2_of(int block) {
+    for (int k = 0; (1 << k) <= DCP_MLA_CACHE8_BLOCK_MAX; ++k)
+        if (block == 1 << k) return k;
+    return -1;
+}
+
+int check_shards(const void* const* kv, const float* const* scales, int cp, int64_t interleave) {
+    if (cp < 1 || cp > kCpMax || interleave < 1 || interleave > kMaxInterleave) return DCP_MLA_CACHE8_ERR_BAD_CP;
+    if (kv == nullptr || scales == nullptr) return DCP_MLA_CACHE8_ERR_NULL_POINTER;
+    bool any = false;
+    for (int j = 0; j < cp; ++j) {
+        if ((kv[j] == nullptr) != (scales[j] == nullptr)) return DCP_MLA_CACHE8_ERR_NULL_POINTER;
+        if (!aligned(kv[j], 16) || !aligned(scales[j], 4)) return DCP_MLA_CACHE8_ERR_MISALIGNED;
+        any |= kv[j] != nullptr;
+    }
+    return any ? 0 : DCP_MLA_CACHE8_ERR_NULL_POINTER;
+}
+
+template <class E>
+int launch_rope(RopeParams& p, int D, int64_t esize, cudaStream_t st) {
+    // 16-byte units where every address that a unit can take allows it
+    const int v = (int)(16 / esize);
+    const bool al = (reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.out)) % 16 == 0 &&
+                    (p.x_row | p.x_head | p.out_row | p.out_head) % v == 0 && p.start % v == 0 &&
+                    (p.interleaved ? 2 * p.half : p.half) % v == 0 && (!p.copy || D % v == 0);
+    const int kv = al ? v : 1;
+    p.rot_units = p.interleaved ? (kv > 1 ? 2 * p.half / kv : p.half) : p.half / kv;
+    p.copy_lead = p.copy ? p.start / kv : 0;
+    p.units = p.rot_units + (p.copy ? (D - 2 * p.half) / kv : 0);
+    // Tokens and heads of a CTA: about 1024 units (4 a thread), fewer where the
+    // call is small, so that it still fills the GPU.
+    const int64_t all = p.N * p.H * p.units;
+    int64_t want = all / (152 * 8);
+    want = want < 256 ? 256 : (want > 1024 ? 1024 : want);
+    int64_t heads = want / p.units;
+    heads = heads < 1 ? 1 : (heads > p.H ? p.H : heads);
+    p.heads = (int)heads;
+    int64_t tokens = heads < p.H ? 1 : want / (heads * p.units);
+    if (tokens > kRopeAngles / p.half) tokens = kRopeAngles / p.half;
+    tokens = tokens < 1 ? 1 : (tokens > p.N ? p.N : tokens);
+    p.tokens = (int)tokens;
+    p.units_magic = p.units > 1 ? (uint32_t)(((uint64_t(1) << 32) + p.units - 1) / p.units) : 0;
+    const int64_t gx = (p.N + tokens - 1) / tokens, gy = (p.H + heads - 1) / heads;
+    if (gx > 0x7fffffff || gy > 65535) return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
+    // every CTA of a row of CTAs has `heads` heads but the last, which divides by its own count:
+    // with more than one head block a CTA has one token, so the quotient is always 0
+    p.heads_magic = p.heads > 1 ? (uint32_t)(((uint64_t(1) << 32) + p.heads - 1) / p.heads) : 0;
+    const dim3 grid((unsigned)gx, (unsigned)gy);
+    if (kv > 1) rope_kernel<E, 16 / sizeof(typename E::T)><<<grid, kRopeThreads, 0, st>>>(p);
+    else rope_kernel<E, 1><<<grid, kRopeThreads, 0, st>>>(p);
+    return launched();
+}
+
+template <class E>
+int launch_append(const AppendParams& p, int block, cudaStream_t st) {
+    if (block == 1) {
+        append_token_kernel<E><<<(unsigned)((p.N + 3) / 4), 128, 0, st>>>(p);
+        return launched();
+    }
+    const unsigned grid = (unsigned)(p.N < kAppendGrid ? p.N : kAppendGrid);
+    const int threads = 32 * kBlockWarps;
+    if (block <= 16) append_block_kernel<E, 1><<<grid, threads, 0, st>>>(p);
+    else if (block == 32) append_block_kernel<E, 2><<<grid, threads, 0, st>>>(p);
+    else if (block == 64) append_block_kernel<E, 4><<<grid, threads, 0, st>>>(p);
+    else append_block_kernel<E, 8><<<grid, threads, 0, st>>>(p);
+    return launched();
+}
+
+template <class E>
+int launch_read(const ReadParams& p, int Dk, cudaStream_t st) {
+    const unsigned grid = (unsigned)((p.N + p.tokens - 1) / p.tokens);
+    if (Dk == 576) read_kernel<E, 576><<<grid, kReadThreads, 0, st>>>(p);
+    else read_kernel<E, 512><<<grid, kReadThreads, 0, st>>>(p);
+    return launched();
+}
+
+}  // namespace
+
+extern "C" const char* dcp_mla_cache8_strerror(int status) {
+    switch (status) {
+        case DCP_MLA_CACHE8_ERR_NULL_POINTER: return "a required pointer is NULL, or every shard's";
+        case DCP_MLA_CACHE8_ERR_BAD_SHAPE: return "a size is out of range";
+        case DCP_MLA_CACHE8_ERR_BAD_BLOCK: return "block must be a power of two in [1, 128]";
+        case DCP_MLA_CACHE8_ERR_BAD_CP: return "cp must be in [1, 16] and interleave in [1, 2^24]";
+        case DCP_MLA_CACHE8_ERR_MISALIGNED: return "a pointer or a stride is not aligned as the call asks";
+        case DCP_MLA_CACHE8_ERR_BAD_DTYPE: return "a dtype that the call does not take";
+        case DCP_MLA_CACHE8_ERR_BAD_FLAGS: return "unknown flag bits";
+        case DCP_MLA_CACHE8_ERR_WORKSPACE:
+            return "the workspace is NULL, not 256-byte aligned, or smaller than dcp_mla_cache8_decode_workspace_bytes";
+        case DCP_MLA_CACHE8_ERR_BAD_WINDOW: return "window and sinks must not be negative, and sinks need a window";
+        case DCP_MLA_CACHE8_ERR_TENSOR_MAP: return "a TMA tensor map of a cache could not be encoded";
+        default: return dcp_lse_reduce_strerror(status);
+    }
+}
+
+extern "C" int dcp_mla_rope(const void* x, int64_t x_row, int64_t x_head, const void* positions, int pos64,
+                            const double* inv_freq, int64_t N, int H, int D, int start, int rot, int interleaved,
+                            float mscale, int dtype, void* out, int64_t out_row, int64_t out_head, void* stream) {
+    if (N < 0 || N > 0x7fffffff || H < 1 || H > 65535 || D < 1 || D > 65536 || rot < 2 || rot > 256 || rot % 2 != 0 ||
+        start < 0 || start > D - rot)
+        return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
+    if (dtype != DCP_DTYPE_BF16 && dtype != DCP_DTYPE_F16 && dtype != DCP_DTYPE_F32)
+        return DCP_MLA_CACHE8_ERR_BAD_DTYPE;
+    if (N == 0) return 0;
+    if (x == nullptr || out == nullptr || positions == nullptr || inv_freq == nullptr)
+        return DCP_MLA_CACHE8_ERR_NULL_POINTER;
+    const int64_t esize = dtype == DCP_DTYPE_F32 ? 4 : 2;
+    if (!aligned(x, esize) || !aligned(out, esize) || !aligned(positions, pos64 ? 8 : 4) || !aligned(inv_freq, 8))
+        return DCP_MLA_CACHE8_ERR_MISALIGNED;
+    if (x == out && (x_row != out_row || x_head != out_head)) return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
+    RopeParams p = {};
+    p.x = x;
+    p.out = out;
+    p.positions = positions;
+    p.inv_freq = inv_freq;
+    p.x_row = x_row;
+    p.x_head = x_head;
+    p.out_row = out_row;
+    p.out_head = out_head;
+    p.N = N;
+    p.H = H;
+    p.start = start;
+    p.half = rot / 2;
+    p.interleaved = interleaved != 0;
+    p.pos64 = pos64 != 0;
+    p.copy = x != out && D > rot;
+    p.mscale = mscale;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dtype == DCP_DTYPE_BF16) return launch_rope<Bf16>(p, D, esize, st);
+    if (dtype == DCP_DTYPE_F16) return launch_rope<F16>(p, D, esize, st);
+    return launch_rope<F32>(p, D, esize, st);
+}
+
+extern "C" int dcp_mla_cache8_append(const void* latent, int64_t latent_row, const void* k_rope, int64_t rope_row,
+                                     int dtype, int64_t N, int64_t B, int Dk, const int32_t* cu_new,
+                                     const int32_t* seq_lens, void* const* kv_ptrs, float* const* scale_ptrs, int cp,
+                                     int64_t T, int block, int interleave, const double* inv_freq, int interleaved,
+                                     float mscale, void* stream) {
+    if (N < 0 || N > 0x7fffffff || B < 0 || B > 65535 || T < 0 || T > 0x7fffffff || (Dk != 512 && Dk != 576) ||
+        (cu_new == nullptr && B > 0 && N % B != 0) || (B == 0 && N > 0))
+        return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
+    if (dtype != DCP_DTYPE_BF16 && dtype != DCP_DTYPE_F16) return DCP_MLA_CACHE8_ERR_BAD_DTYPE;
+    const int lg = log2_of(block);
+    if (lg < 0) return DCP_MLA_CACHE8_ERR_BAD_BLOCK;
+    if (const int rc = check_shards(kv_ptrs, scale_ptrs, cp, interleave)) return rc;
+    if (N == 0 || T == 0) return 0;
+    if (latent == nullptr || seq_lens == nullptr || (Dk == 576 && k_rope == nullptr))
+        return DCP_MLA_CACHE8_ERR_NULL_POINTER;
+    if (!aligned(latent, 16) || !aligned(k_rope, 16) || latent_row % 8 != 0 || (Dk == 576 && rope_row % 8 != 0) ||
+        !aligned(seq_lens, 4) || !aligned(cu_new, 4) || !aligned(inv_freq, 8))
+        return DCP_MLA_CACHE8_ERR_MISALIGNED;
+    AppendParams p = {};
+    p.latent = static_cast<const uint8_t*>(latent);
+    p.k_rope = static_cast<const uint8_t*>(k_rope);
+    p.latent_row = latent_row * 2;
+    p.rope_row = rope_row * 2;
+    p.cu = cu_new;
+    p.seq_lens = seq_lens;
+    p.inv_freq = Dk == 576 ? inv_freq : nullptr;
+    for (int j = 0; j < cp; ++j) {
+        p.kv[j] = static_cast<uint8_t*>(kv_ptrs[j]);
+        p.scales[j] = scale_ptrs[j];
+    }
+    p.N = N;
+    p.T = T;
+    p.blocks = (T + block - 1) / block;
+    p.B = (int)B;
+    p.Dk = Dk;
+    p.even = cu_new == nullptr ? (int)(N / B) : 0;
+    p.cp = (uint32_t)cp;
+    p.interleave = (uint32_t)interleave;
+    p.block_log2 = lg;
+    p.interleaved = interleaved != 0;
+    p.mscale = mscale;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return dtype == DCP_DTYPE_BF16 ? launch_append<Bf16>(p, block, st) : launch_append<F16>(p, block, st);
+}
+
+extern "C" int dcp_mla_cache8_read(const void* const* kv_ptrs, const float* const* scale_ptrs, int cp, int64_t B,
+                                   int64_t T, int Dk, int block, int interleave, const int32_t* starts,
+                                   const int32_t* cu, int64_t N, void* out, int64_t out_row, int dtype,
+                                   void* stream) {
+    if (N < 0 || N > 0x7fffffff || B < 0 || B > 65535 || T < 0 || T > 0x7fffffff || (Dk != 512 && Dk != 576) ||
+        (cu == nullptr && B > 0 && N % B != 0) || (B == 0 && N > 0))
+        return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
+    if (dtype != DCP_DTYPE_BF16 && dtype != DCP_DTYPE_F16 && dtype != DCP_DTYPE_F32)
+        return DCP_MLA_CACHE8_ERR_BAD_DTYPE;
+    const int lg = log2_of(block);
+    if (lg < 0) return DCP_MLA_CACHE8_ERR_BAD_BLOCK;
+    if (const int rc = check_shards(kv_ptrs, scale_ptrs, cp, interleave)) return rc;
+    if (N == 0 || T == 0) return 0;
+    if (out == nullptr) return DCP_MLA_CACHE8_ERR_NULL_POINTER;
+    const int64_t esize = dtype == DCP_DTYPE_F32 ? 4 : 2;
+    if (!aligned(out, 16) || (out_row * esize) % 16 != 0 || !aligned(starts, 4) || !aligned(cu, 4))
+        return DCP_MLA_CACHE8_ERR_MISALIGNED;
+    ReadParams p = {};
+    for (int j = 0; j < cp; ++j) {
+        p.kv[j] = static_cast<const uint8_t*>(kv_ptrs[j]);
+        p.scales[j] = scale_ptrs[j];
+    }
+    p.starts = starts;
+    p.cu = cu;
+    p.out = static_cast<uint8_t*>(out);
+    p.out_row = out_row * esize;
+    p.N = N;
+    p.T = T;
+    p.blocks = (T + block - 1) / block;
+    p.B = (int)B;
+    p.even = cu == nullptr ? (int)(N / B) : 0;
+    p.block_log2 = lg;
+    p.cp = (uint32_t)cp;
+    p.interleave = (uint32_t)interleave;
+    // 32 tokens a CTA, 8 where that would leave multiprocessors idle
+    p.tokens = N >= 152 * 4 * kReadTokens ? kReadTokens : 8;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dtype == DCP_DTYPE_BF16) return launch_read<Bf16>(p, Dk, st);
+    if (dtype == DCP_DTYPE_F16) return launch_read<F16>(p, Dk, st);
+    return launch_read<F32>(p, Dk, st);
+}
