@@ -32,6 +32,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
+#include <limits.h>
+#include <stddef.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -43,7 +45,9 @@ namespace {
 constexpr int kDv = 512;
 constexpr int kTile = 128;                 // tokens of a tile: the MMA's M
 constexpr int kSlice = kTile * 128;        // bytes of a 128-dim slice of a tile
-constexpr int kThreads = 512;
+constexpr int kSoftWarps = 16, kSoftThreads = 32 * kSoftWarps;
+constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
+constexpr int kThreads = kSoftThreads + 64;
 constexpr int kCpMax = DCP_MLA_CACHE8_CP_MAX;
 constexpr int64_t kMaxInterleave = 1 << 24;
 constexpr long long kWaitLimitNs = 2000000000LL;  // every wait gives up after this
@@ -59,7 +63,7 @@ struct DecodeParams {
     const int* seq_lens;
     float* part;                           // [2 x CTAs][heads of a block][512], normalised
     float* part_lse;                       // [2 x CTAs][heads of a block], base 2
-    int* row_info;                         // [B] tiles before the row; [B]: tiles of a CTA
+    int2* row_info;                        // [B] a row's first range of CTAs and its segments
     uint8_t* out;
     float* lse;
     int* status;
@@ -128,12 +132,21 @@ __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity, long 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// 4 bytes from global to shared memory, asynchronously; `bytes` = 0 writes zeros.
+__device__ __forceinline__ void copy_word(uint32_t dst, const uint8_t* src, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* tm, int x, int y, int z, uint64_t* bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
             smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* tm, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(tm)),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
 }
 constexpr uint32_t kSwizzle128 = 2, kSwizzle64 = 4, kSwizzleNone = 0;
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
@@ -149,14 +162,22 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
         : "memory");
 }
 // the same with one ue8m0 scale for 32 products of a row of A and of B
+// (kKeep: A stays in the tensor core's collector; kKept: it is there from the MMA before)
+enum Collect { kPlain, kKeep, kKept };
+template <Collect kC>
 __device__ __forceinline__ void mma_f8_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                               uint32_t sfb, uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(
-            d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
-        : "memory");
+#define DCP_MMA_SCALED(collector)                                                                                 \
+    asm volatile(                                                                                                 \
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"                                                             \
+        " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X" collector                            \
+        " [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),                                                        \
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)                                                  \
+        : "memory")
+    if constexpr (kC == kPlain) DCP_MMA_SCALED("");
+    else if constexpr (kC == kKeep) DCP_MMA_SCALED(".collector::a::fill");
+    else DCP_MMA_SCALED(".collector::a::lastuse");
+#undef DCP_MMA_SCALED
 }
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
@@ -227,9 +248,11 @@ __device__ __forceinline__ uint32_t share(const DecodeParams& p, Prefix x, uint3
 struct RowView {
     Prefix len, win, sink;
 };
-__device__ __forceinline__ RowView row_view(const DecodeParams& p, int b) {
+__device__ __forceinline__ uint32_t row_length(const DecodeParams& p, int b) {
     const int n = p.seq_lens[b];
-    const uint32_t L = n < 0 ? 0u : (uint32_t)n;
+    return n < 0 ? 0u : (uint32_t)n;
+}
+__device__ __forceinline__ RowView row_view(const DecodeParams& p, uint32_t L) {
     const uint32_t w = p.window > 0 && L > p.window ? L - p.window : 0u;
     RowView v;
     v.len = prefix_of(p, L);
@@ -255,9 +278,10 @@ __device__ __forceinline__ ShardView shard_view(const DecodeParams& p, const Row
     s.tiles = s.tiles_first + (int)((s.end - s.start + kTile - 1) / kTile);
     return s;
 }
-__device__ __forceinline__ int row_tiles(const DecodeParams& p, int b) {
-    const RowView v = row_view(p, b);
+__device__ __forceinline__ int row_tiles(const DecodeParams& p, uint32_t L) {
+    const RowView v = row_view(p, L);
     int n = 0;
+#pragma unroll 1
     for (uint32_t j = 0; j < p.cp; ++j) n += shard_view(p, v, j).tiles;
     return n;
 }
@@ -267,8 +291,8 @@ struct Cursor {
     ShardView s;
     uint32_t j;
     int i;  // tile of the shard
-    __device__ __forceinline__ void seek(const DecodeParams& p, int b, int tile) {
-        row = row_view(p, b);
+    __device__ __forceinline__ void seek(const DecodeParams& p, uint32_t L, int tile) {
+        row = row_view(p, L);
         j = 0;
         s = shard_view(p, row, 0);
         i = tile;
@@ -293,6 +317,14 @@ struct Cursor {
     }
 };
 
+// What the join needs of a row: its first CTA range and its number of segments. Written by the CTA that has the
+// row's first tile; for a row without a tile by the first CTA.
+__device__ __forceinline__ void tell_row(const DecodeParams& p, int b, int n, int pre, int g, int g_end, int per,
+                                         int range) {
+    if (n == 0 && range == 0) p.row_info[b] = make_int2(0, 0);
+    else if (n > 0 && pre >= g && pre < g_end) p.row_info[b] = make_int2(range, (pre + n - 1) / per - range + 1);
+}
+
 // ---- the kernel ------------------------------------------------------------------
 
 template <int kDk, int kNH>
@@ -307,16 +339,183 @@ struct Shape {
     // With 64 heads P's lo part takes the rope slice of its tile, which is done with once the scores are there.
     static constexpr bool kLoInRope = !kStacked && kHasRope;
     static constexpr int kPBytes = kStacked || !kLoInRope ? kRows * 128 : kNH * 128;
-    static constexpr int kMisc = 1024 + 128 + 4 * kNH * 4;
+    static constexpr int kMisc = 1024 + 8 * kNH * 4;
     static constexpr int kSmem = 2 * kStage + kQBytes + kPBytes + kMisc;
     static constexpr int kHW = kNH / 4;                      // heads of a thread
     static constexpr int kO = kRows;                         // TMEM: S [0, rows), O 4 x kOB columns, scales
     static constexpr int kOB = kStacked ? kRows : kNH;
     static constexpr int kSf = kO + 4 * kOB;
-    static constexpr int kCols = kSf + 12 <= 256 ? 256 : 512;
-    static_assert(kSmem <= 232448 && kSf + 12 <= 512, "");
+    static constexpr int kCols = kSf + 8 <= 256 ? 256 : 512;
+    static_assert(kSmem <= 232448 && kSf + 8 <= 512, "");
 };
 
+// What the loading warp tells the others about a tile.
+struct alignas(16) TileInfo {
+    uint32_t token;  // first token
+    int valid;       // tokens; 0: no more tiles
+    uint32_t what;   // shard, and kFirst ...
+    int row;
+};
+constexpr uint32_t kFirst = 256, kLast = 512;  // the first, the last tile of a segment (a run of tiles of one row)
+constexpr uint32_t kWhole = 1024;              // the segment is the whole row
+constexpr uint32_t kStarts = 2048;             // the segment has the row's first tile
+
+struct Shared {  // barriers and small things, behind the scale atom
+    uint64_t info_full[4];    // a tile's description is there
+    uint64_t kv_full[2][4];   // a slice of a tile has landed (the last one with the rope slice)
+    uint64_t kv_free[2][4];   // it has been multiplied for the last time
+    uint64_t s_full, s_free;  // scores are in TMEM; they have been read
+    uint64_t p_full;          // probabilities (and zeroed rows, scales) are in shared memory
+    uint64_t o_done;          // a tile's values are added
+    uint64_t q_full;          // a segment's q is in shared memory
+    uint64_t drained;         // every MMA of the CTA is done
+    uint64_t voted[4];        // a group's warps know how far their scores are above the references
+    uint64_t met[4];          // a group's warps have come to the same place
+    int moved[4][2];          // too far, in the group's even and odd tiles
+    int armed[2][4];          // how often each slice's barrier has been armed, less one
+    uint32_t tmem;
+    int abort;
+    int find[4];
+    int wsum[16];
+    TileInfo info[4];
+};
+static_assert(sizeof(Shared) <= 512 && offsetof(Shared, s_full) == 160, "");
+
+// Scores ride on 1.5 * 2^23: x + kMagic rounds x to an integer that the low bits
+// of the sum hold, so that integer maxima and differences of the sums' bits are
+// those of the rounded scores (for |x| < 2^22).
+constexpr float kMagic = 12582912.f;
+constexpr int kMagicBits = 0x4B400000;
+constexpr int kRange = 1 << 21;  // scores beyond this (base-2 units) give NaN
+
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+    f32x2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Four e4m3 codes, the first in the low byte.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+// Barrier, and vote, of all softmax warps.
+__device__ __forceinline__ void soft_sync() {
+    asm volatile("barrier.cta.sync.aligned 5, %0;" ::"n"(kSoftThreads) : "memory");
+}
+__device__ __forceinline__ bool soft_any(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 q, %2, 0;\n barrier.cta.red.or.pred.aligned p, 5, %1, q;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(r)
+        : "n"(kSoftThreads), "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
+
+// The scores' MMAs over slices [s, to) of the tile at `ka`, with the last slice those over the rope slice.
+// (Loops are kept rolled where code runs once or rarely: a call is short, its
+// instructions come from L2, and unrolled they cost more than they compute.)
+template <class S>
+__device__ __forceinline__ void issue_scores(uint32_t ka, uint32_t qa, uint32_t tmem, uint32_t idesc, int s, int to,
+                                             uint64_t* done) {
+    if (elect_one()) {
+        uint64_t a0 = smem_desc(ka + s * kSlice, 16, 1024, kSwizzle128);
+        uint64_t b0 = smem_desc(qa + s * S::kQSlice, 16, 1024, kSwizzle128);
+#pragma unroll 1
+        for (; s < to; ++s) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mma_f8(tmem, a0 + (uint32_t)(2 * k), b0 + (uint32_t)(2 * k), idesc, s | k);
+            a0 += kSlice >> 4;
+            b0 += S::kQSlice >> 4;
+        }
+        if (to == 4) {
+            if constexpr (S::kHasRope) {
+                const uint64_t a1 = smem_desc(ka + 4 * kSlice, 16, 512, kSwizzle64);
+                const uint64_t b1 = smem_desc(qa + 4 * S::kQSlice, 16, 512, kSwizzle64);
+                mma_f8(tmem, a1, b1, idesc, 1);
+                mma_f8(tmem, a1 + 2, b1 + 2, idesc, 1);
+            }
+            mma_commit(done);
+        }
+    }
+    __syncwarp();
+}
+
+// Its values: per 128 latent dims 4 MMAs (8 where P's parts are two operands); each slice of the tile is
+// given back as soon as it has been used.
+template <class S>
+__device__ __forceinline__ void issue_values(uint32_t ka, uint32_t pa, uint32_t tmem, uint32_t idesc, uint32_t go_on,
+                                             uint64_t* slice_free, uint64_t* done) {
+    if (elect_one()) {
+        const uint64_t a0 = smem_desc(ka, kSlice, 1024, kSwizzle128), b0 = smem_desc(pa, 16, 1024, kSwizzle128);
+        const uint64_t b1 = smem_desc(S::kLoInRope ? ka + 4 * kSlice : pa + (S::kRows / 2) * 128, 16, 1024, kSwizzle128);
+        copy_scales(tmem + S::kSf + 4, pa + S::kPBytes);
+#pragma unroll 1
+        for (int m = 0; m < 4; ++m) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t d = tmem + S::kO + m * S::kOB, id = idesc | ((uint32_t)k << 4) | ((uint32_t)k << 29);
+                const uint64_t a = a0 + (uint32_t)(m * (kSlice >> 4) + 256 * k);
+                mma_f8_scaled<S::kStacked ? kPlain : kKeep>(d, a, b0 + (uint32_t)(2 * k), id, tmem + S::kSf,
+                                                            tmem + S::kSf + 4, k > 0 ? 1u : go_on);
+                if constexpr (!S::kStacked)
+                    mma_f8_scaled<kKept>(d, a, b1 + (uint32_t)(2 * k), id, tmem + S::kSf, tmem + S::kSf + 4, 1u);
+            }
+            mma_commit(slice_free + m);
+        }
+        mma_commit(done);
+    }
+    __syncwarp();
+}
+
+// Roles. Sixteen warps do the softmax, in four groups of four: a group has a
+// quarter of the heads, a warp of it 32 of the tile's tokens (its TMEM lanes), a
+// thread one token. One warp walks the tiles and loads them (TMA, two stages,
+// each slice as soon as the values of the tile before last have used it), one
+// issues the MMAs: whichever is ready first, the next tile's scores or this
+// tile's values, so that scores and softmax of one tile run beside the values of
+// another.
 template <int kDk, int kNH>
 __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ DecodeParams p) {
     using S = Shape<kDk, kNH>;
@@ -327,56 +526,49 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* const q_s = smem + 2 * S::kStage;
     uint8_t* const p_s = q_s + S::kQBytes;
-    uint8_t* const sf_s = p_s + S::kPBytes;                       // two 512-byte scale atoms
-    uint64_t* const bar_kv = reinterpret_cast<uint64_t*>(sf_s + 1024);  // [2] a tile has landed
-    uint64_t* const bar_s = bar_kv + 2;                           // a tile's scores are there
-    uint64_t* const bar_o = bar_kv + 3;                           // a tile's values are added
-    uint32_t* const tslot = reinterpret_cast<uint32_t*>(bar_kv + 4);
-    volatile int* const abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-    int* const find_s = reinterpret_cast<int*>(tslot + 2);        // [4]
-    int* const wsum = reinterpret_cast<int*>(tslot + 6);          // [16]
-    int* const m_s = reinterpret_cast<int*>(sf_s + 1024 + 128);   // reference exponents
-    int* const mn_s = m_s + kNH;
-    float* const a_s = reinterpret_cast<float*>(mn_s + kNH);      // rescale factors, then 1 / sums
-    float* const g_s = a_s + kNH;                                 // q's scales
+    uint8_t* const sf_s = p_s + S::kPBytes;                       // a 512-byte scale atom
+    Shared* const sh = reinterpret_cast<Shared*>(sf_s + 512);
+    int* const m_s = reinterpret_cast<int*>(sf_s + 1024);         // reference exponents (as bits of x + kMagic)
+    float* const g_s = reinterpret_cast<float*>(m_s + kNH);       // q's scales
+    float* const a_s = g_s + kNH;                                 // factors of a moved reference, 1 / sums
+    int* const up_s = reinterpret_cast<int*>(a_s + kNH);          // how far it moved
+    float* const red = a_s + 2 * kNH;                             // [4][kNH]: a warp's own words
+    int* const red_i = reinterpret_cast<int*>(red);
+    volatile int* const abort_flag = &sh->abort;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hblk = blockIdx.x % p.head_blocks, range = blockIdx.x / p.head_blocks;
     const int h0 = hblk * kNH;
     const int nh = p.H - h0 < kNH ? p.H - h0 : kNH;
 
-    if (tid == 0) {
-        for (int i = 0; i < 4; ++i) mbar_init(bar_kv + i, 1);
+    if (warp == kLoadWarp) {
+        // barriers, one per lane: those that one thread or one MMA completes, then those of 16 warps, then of 4
+        if (lane < 24) mbar_init(&sh->info_full[0] + lane, lane == 21 || lane == 22 ? kSoftWarps : 1);
+        else if (lane == 24) mbar_init(&sh->q_full, kSoftWarps);
+        else if (lane == 25) mbar_init(&sh->drained, 1);
+        if (lane < 8) mbar_init(&sh->voted[0] + lane, 4);
+        if (lane >= 24) (&sh->moved[0][0])[lane - 24] = 0;
+        if (lane >= 16 && lane < 24) (&sh->armed[0][0])[lane - 16] = -1;
+        if (lane == 0) *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        *abort_flag = 0;
     }
-    if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)),
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh->tmem)),
                      "r"(S::kCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    for (int i = tid; i < 256; i += kThreads) reinterpret_cast<uint32_t*>(sf_s)[i] = 0;
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tslot;
-    const int quad = warp & 3, tok = quad * 32 + lane, hb = (warp >> 2) * kHW;
-    const uint32_t tlane = tmem + ((uint32_t)(32 * quad) << 16);
-    if (warp < 4) {  // the cached tile's scale is 1 everywhere: its own scale went into the probabilities
-        const float one[4] = {__uint_as_float(0x7f7f7f7fu), __uint_as_float(0x7f7f7f7fu), __uint_as_float(0x7f7f7f7fu),
-                              __uint_as_float(0x7f7f7f7fu)};
-        tmem_st4(tlane + S::kSf, one);
-        tmem_wait_st();
-    }
+    if (tid < 128) reinterpret_cast<uint32_t*>(sf_s)[tid] = 0;
 
     pdl_wait();
     pdl_launch_dependents();
+    uint32_t length = 0;  // the loading warp's row's; with few rows, first a lane's row's
+    if (warp == kLoadWarp && lane < p.B) length = row_length(p, lane);
 
-    // ---- this CTA's tiles: [g, g_end) of all rows' tiles, from tile `tile` of row `row`
-    int row = range, tile = 0, g = 0, g_end = 0;
-    if (!p.row_mode) {
-        int total = 0, n_mine = 0, pre_mine = 0;
+    // ---- this CTA's tiles: [g, g_end) of all rows' tiles, from tile `tile` of row `row` (or whole rows)
+    int row = range, tile = 0, n_row = 0, g = 0, g_end = 0;
+    if (!p.row_mode && p.B > 32) {
+        int total = 0, n_mine = 0, pre_mine = 0, per_cta = 0;
         for (int pass = 0; pass < 2; ++pass) {
             int base = 0;
             if (pass == 1) {
@@ -385,26 +577,22 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 const int64_t lo = (int64_t)range * per, hi = lo + per;
                 g = lo < total ? (int)lo : total;
                 g_end = hi < total ? (int)hi : total;
-                if (blockIdx.x == 0 && tid == 0) p.row_info[p.B] = per;
-                if (tid == 0) find_s[0] = p.B;
-                __syncthreads();
+                per_cta = per;
             }
-            for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-                if (pass == 0 || p.B > kThreads) {
-                    const int n = b0 + tid < p.B ? row_tiles(p, b0 + tid) : 0;
+            for (int b0 = 0; b0 < p.B; b0 += kSoftThreads) {
+                if (pass == 0 || p.B > kSoftThreads) {
+                    const int n = tid < kSoftThreads && b0 + tid < p.B ? row_tiles(p, row_length(p, b0 + tid)) : 0;
                     int x = n;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
                         const int y = __shfl_up_sync(0xffffffffu, x, o);
                         if (lane >= o) x += y;
                     }
-                    if (lane == 31) wsum[warp] = x;
+                    if (lane == 31 && warp < kSoftWarps) sh->wsum[warp] = x;
                     __syncthreads();
-                    int before = 0, all = 0;
-                    for (int w = 0; w < kThreads / 32; ++w) {
-                        before += w < warp ? wsum[w] : 0;
-                        all += wsum[w];
-                    }
+                    const int ws = lane < kSoftWarps ? sh->wsum[lane] : 0;
+                    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0);
+                    const int all = __reduce_add_sync(0xffffffffu, ws);
                     __syncthreads();
                     n_mine = n;
                     pre_mine = base + before + x - n;
@@ -412,329 +600,556 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 }
                 if (pass == 1) {
                     if (n_mine > 0 && pre_mine <= g && g < pre_mine + n_mine && g < g_end) {
-                        find_s[0] = b0 + tid;
-                        find_s[1] = g - pre_mine;
+                        sh->find[0] = b0 + tid;
+                        sh->find[1] = g - pre_mine;
+                        sh->find[2] = n_mine;
                     }
-                    // the CTA that has a row's first tile says where the row lies
-                    if (n_mine > 0 && hblk == 0 && pre_mine >= g && pre_mine < g_end)
-                        p.row_info[b0 + tid] = pre_mine;
+                    if (hblk == 0 && tid < kSoftThreads && b0 + tid < p.B)
+                        tell_row(p, b0 + tid, n_mine, pre_mine, g, g_end, per_cta, range);
                 }
             }
             if (pass == 0) total = base;
         }
-        __syncthreads();
-        row = find_s[0];
-        tile = find_s[1];
-    }
-
-    uint32_t it = 0;        // tiles of this CTA so far: stage it & 1
-    bool aborted = false;
-    while (row < p.B && (p.row_mode || g < g_end)) {
-        // ---- a segment: tiles [tile, tile + n) of this row
-        const int n_row = row_tiles(p, row);
-        const int n = p.row_mode || n_row - tile < g_end - g ? n_row - tile : g_end - g;
-        if (n_row == 0) {
-            if (p.row_mode) {
-                uint4* const o = reinterpret_cast<uint4*>(p.out + ((int64_t)row * p.H + h0) * (kDv * 2));
-                for (int i = tid; i < nh * (kDv / 8); i += kThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (p.lse != nullptr && tid < nh) p.lse[(int64_t)row * p.H + h0 + tid] = -INFINITY;
-            }
-            row += p.row_mode ? p.ranges : 1;
-            tile = 0;
-            continue;
-        }
-        Cursor cur, ahead;
-        cur.seek(p, row, tile);
-        ahead = cur;
-        auto load = [&](const Cursor& c, uint32_t k) {  // one thread: tile k of this CTA into its stage
-            uint8_t* const kv = smem + (k & 1) * S::kStage;
-            uint64_t* const bar = bar_kv + (k & 1);
-            const int t0 = (int)c.token();
-            mbar_expect_tx(bar, S::kStage);
-#pragma unroll
-            for (int a = 0; a < 4; ++a) tma_load_3d(kv + a * kSlice, &p.tm_latent[c.j], a * 128, t0, row, bar);
-            if constexpr (S::kHasRope) tma_load_3d(kv + 4 * kSlice, &p.tm_rope[c.j], kDv, t0, row, bar);
-        };
-        if (tid == 0) load(ahead, it);
-
-        // ---- q: hi and lo e4m3 parts of each head at its own power-of-two scale
-        for (int h = warp; h < kNH; h += kThreads / 32) {
-            uint32_t w[kDk / 64];
-            const uint32_t* const src = reinterpret_cast<const uint32_t*>(p.q + row * p.q_row + (h0 + h) * p.q_head);
-#pragma unroll
-            for (int i = 0; i < kDk / 64; ++i) w[i] = h < nh ? __ldg(src + i * 32 + lane) : 0u;
-            float top = 0.f;
-#pragma unroll
-            for (int i = 0; i < kDk / 64; ++i)
-                top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const uint32_t u = __float_as_uint(top);
-            int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);  // top <= 448 * 2^e
-            e = e < -120 ? -120 : e;
-            const bool bad = u >= 0x7f800000u;  // an infinity: the whole head is NaN (a NaN stays one by itself)
-            const float inv = bad ? __uint_as_float(0x7fffffffu) : __uint_as_float((uint32_t)(127 - e) << 23);
-            if (lane == 0) g_s[h] = bad ? 1.f : __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-            for (int i = 0; i < kDk / 64; ++i) {
-                const float x = __uint_as_float(w[i] << 16) * inv, y = __uint_as_float(w[i] & 0xffff0000u) * inv;
-                const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
-                const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(hi, __NV_E4M3)));
-                const __nv_fp8x2_storage_t lo =
-                    __nv_cvt_float2_to_fp8x2(make_float2(x - back.x, y - back.y), __NV_SATFINITE, __NV_E4M3);
-                const int d = 64 * i + 2 * lane, c = (d & 127) >> 4;
-#pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                    const int r = h + part * kNH;
-                    uint8_t* dst;
-                    if (S::kHasRope && i == kDv / 64)
-                        dst = q_s + 4 * S::kQSlice + r * 64 + ((c ^ ((r >> 1) & 3)) << 4) + (d & 15);
-                    else
-                        dst = q_s + (d >> 7) * S::kQSlice + r * 128 + ((c ^ (r & 7)) << 4) + (d & 15);
-                    *reinterpret_cast<__nv_fp8x2_storage_t*>(dst) = part ? lo : hi;
-                }
-            }
-        }
-        if (tid < kNH) m_s[tid] = -kFar;
-        if (tid < kNH) mn_s[tid] = -kFar;
-        async_fence();
-        __syncthreads();
-
-        float l_part[kHW];
-#pragma unroll
-        for (int h = 0; h < kHW; ++h) l_part[h] = 0.f;
-
-        for (int i = 0; i < n; ++i, ++it) {
-            if (__syncthreads_or(*abort_flag != 0)) {
-                aborted = true;
-                break;
-            }
-            uint8_t* const kv = smem + (it & 1) * S::kStage;
-            const int valid = cur.valid();
-            // this thread's token's scale, in flight beside the tile
-            const uint32_t t_loc = cur.token() + (uint32_t)(tok < valid ? tok : valid - 1);
-            const float u = fmaxf(p.scales[cur.j][(int64_t)row * p.blocks + (t_loc >> p.block_log2)], 7.888609e-31f);
-            (void)mbar_wait(bar_kv + (it & 1), (it >> 1) & 1, abort_flag, p.status, p.wait_ns);
-            if (tid == 0 && !*abort_flag) {  // scores
-                tc_fence_after();
-                const uint32_t ka = smem_u32(kv), qa = smem_u32(q_s);
-#pragma unroll
-                for (int a = 0; a < 4; ++a)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f8(tmem, smem_desc(ka + a * kSlice + k * 32, 16, 1024, kSwizzle128),
-                               smem_desc(qa + a * S::kQSlice + k * 32, 16, 1024, kSwizzle128), kIdS, (a | k) != 0);
-                if constexpr (S::kHasRope) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        mma_f8(tmem, smem_desc(ka + 4 * kSlice + k * 32, 16, 512, kSwizzle64),
-                               smem_desc(qa + 4 * S::kQSlice + k * 32, 16, 512, kSwizzle64), kIdS, 1);
-                }
-                mma_commit(bar_s);
-            }
-            (void)mbar_wait(bar_s, it & 1, abort_flag, p.status, p.wait_ns);
-            tc_fence_after();
-            // (every MMA before these is done too: the other stage is free)
-            if (tid == 0 && i + 1 < n && !*abort_flag) {
-                ahead.next(p);
-                load(ahead, it + 1);
-            }
-
-            float sv[kHW];
-            {
-                float lo[kHW];
-                tmem_ld<kHW>(tlane + hb, sv);
-                tmem_ld<kHW>(tlane + kNH + hb, lo);
-                tmem_wait_ld();
-#pragma unroll
-                for (int h = 0; h < kHW; ++h) sv[h] += lo[h];
-            }
-            const bool live = tok < valid;
-            const float c = u * p.scale_log2, lu = log2f(u), ru = 1.0f / u;
-            int e[kHW];
-            bool over = false;
-#pragma unroll
-            for (int h = 0; h < kHW; ++h) {
-                sv[h] = live ? fmaf(sv[h] * g_s[hb + h], c, lu) : -INFINITY;
-                int x = __float2int_ru(sv[h]);
-                x = __reduce_max_sync(0xffffffffu, x < -kFar ? -kFar : (x > kFar ? kFar : x));
-                e[h] = x;
-                over |= x - m_s[hb + h] > kLazy;
-            }
-            // a token that is not visible may hold anything: its value row must not (0 x NaN)
-            if (!live) {
-                uint4* const r = reinterpret_cast<uint4*>(kv + (warp >> 2) * kSlice + tok * 128);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) r[(k + tok) & 7] = make_uint4(0u, 0u, 0u, 0u);
-            }
-            const bool move = __syncthreads_or(over);
-            if (move) {
-#pragma unroll
-                for (int h = 0; h < kHW; ++h)
-                    if (lane == 0) atomicMax(&mn_s[hb + h], e[h]);
-                __syncthreads();
-                if (tid < kNH) {
-                    const int m = m_s[tid], mn = mn_s[tid] > m ? mn_s[tid] : m;
-                    a_s[tid] = ex2((float)(m - mn));
-                    m_s[tid] = mn;
-                }
-                __syncthreads();
-#pragma unroll
-                for (int h = 0; h < kHW; ++h) l_part[h] *= a_s[hb + h];
-                if (i > 0) {
-#pragma unroll 1
-                    for (int b = 0; b < 4 * (S::kStacked ? 2 : 1); ++b) {
-                        const uint32_t col = tlane + S::kO + (S::kStacked ? (b >> 1) * S::kOB + (b & 1) * kNH : b * S::kOB) + hb;
-#pragma unroll
-                        for (int h = 0; h < kHW; h += 4) {
-                            float o[4];
-                            tmem_ld<4>(col + h, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) o[k] *= a_s[hb + h + k];
-                            tmem_st4(col + h, o);
-                        }
-                    }
-                    tmem_wait_st();
-                }
-            }
-            uint8_t* const p_lo = S::kStacked ? p_s + kNH * 128 : (S::kLoInRope ? kv + 4 * kSlice : p_s + kNH * 128);
-            int sf = 0;
-#pragma unroll
-            for (int h = 0; h < kHW; h += 2) {
-                float hi[2], lo[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float x = ex2(sv[h + k] - (float)(e[h + k] - 8));
-                    int f = e[h + k] - m_s[hb + h + k] - 8 + 127;
-                    f = f < 0 ? 0 : f;
-                    if (lane == h + k) sf = f;
-                    l_part[h + k] = fmaf(x * ru, __int_as_float(f << 23), l_part[h + k]);
-                    // the nearest number of 4 significand bits, and the rest
-                    hi[k] = __uint_as_float((__float_as_uint(x) + 0x80000u) & 0xfff00000u);
-                    lo[k] = (x - hi[k]) * 32.f;
-                }
-                const uint32_t ch = __nv_cvt_float2_to_fp8x2(make_float2(hi[0], hi[1]), __NV_SATFINITE, __NV_E4M3);
-                const uint32_t cl = __nv_cvt_float2_to_fp8x2(make_float2(lo[0], lo[1]), __NV_SATFINITE, __NV_E4M3);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int r = hb + h + k;
-                    const int at = r * 128 + (((tok >> 4) ^ (r & 7)) << 4) + (tok & 15);
-                    const int at_lo = S::kStacked ? r * 128 + (((tok >> 4) ^ ((r + kNH) & 7)) << 4) + (tok & 15) : at;
-                    p_s[at] = (uint8_t)(ch >> (8 * k));
-                    p_lo[at_lo] = (uint8_t)(cl >> (8 * k));
-                }
-            }
-            if (lane < kHW) {
-                const int r = hb + lane, r2 = S::kStacked ? r + kNH : r;
-                const int lo = sf - 5;
-                sf_s[(r & 31) * 16 + (r >> 5) * 4 + quad] = (uint8_t)sf;
-                sf_s[(S::kStacked ? 0 : 512) + (r2 & 31) * 16 + (r2 >> 5) * 4 + quad] = (uint8_t)(lo < 0 ? 0 : lo);
-            }
-            async_fence();
-            tc_fence_before();
-            __syncthreads();
-            if (tid == 0 && !*abort_flag) {  // values
-                tc_fence_after();
-                copy_scales(tmem + S::kSf + 4, smem_u32(sf_s));
-                if constexpr (!S::kStacked) copy_scales(tmem + S::kSf + 8, smem_u32(sf_s + 512));
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-#pragma unroll
-                    for (int part = 0; part < (S::kStacked ? 1 : 2); ++part)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_f8_scaled(tmem + S::kO + m * S::kOB,
-                                          smem_desc(smem_u32(kv + m * kSlice) + k * 4096, kSlice, 1024, kSwizzle128),
-                                          smem_desc(smem_u32(part ? p_lo : p_s) + k * 32, 16, 1024, kSwizzle128),
-                                          kIdO | ((uint32_t)k << 4) | ((uint32_t)k << 29), tmem + S::kSf,
-                                          tmem + S::kSf + 4 + 4 * part, (i > 0 || part > 0 || k > 0) ? 1u : 0u);
-                mma_commit(bar_o);
-            }
-            cur.next(p);
-        }
-        if (aborted) break;
-
-        // ---- the segment's end: sums, then O / l
-        (void)mbar_wait(bar_o, (it - 1) & 1, abort_flag, p.status, p.wait_ns);
-        if (__syncthreads_or(*abort_flag != 0)) {
-            aborted = true;
-            break;
-        }
-        tc_fence_after();
-        float* const red = reinterpret_cast<float*>(p_s);  // [4][kNH]
-#pragma unroll
-        for (int h = 0; h < kHW; ++h) {
-            float x = l_part[h];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-            if (lane == 0) red[quad * kNH + hb + h] = x;
-        }
-        __syncthreads();
-        const bool whole = tile == 0 && n == n_row;  // the row's only segment
-        const int64_t slot = (int64_t)blockIdx.x * 2 + (tile == 0 ? 1 : 0);
-        if (tid < kNH) {
-            const float l = (red[tid] + red[kNH + tid]) + (red[2 * kNH + tid] + red[3 * kNH + tid]);
-            a_s[tid] = 1.0f / l;
-            const float lse2 = (float)m_s[tid] + log2f(l);
-            if (!whole) p.part_lse[slot * kNH + tid] = lse2;
-            else if (p.lse != nullptr && tid < nh) p.lse[(int64_t)row * p.H + h0 + tid] = lse2 * p.lse_scale;
-        }
-        __syncthreads();
-#pragma unroll 1
-        for (int m = 0; m < 4; ++m) {
-            float o[kHW];
-            tmem_ld<kHW>(tlane + S::kO + m * S::kOB + hb, o);
-            if constexpr (S::kStacked) {
-                float lo[kHW];
-                tmem_ld<kHW>(tlane + S::kO + m * S::kOB + kNH + hb, lo);
-                tmem_wait_ld();
-#pragma unroll
-                for (int h = 0; h < kHW; ++h) o[h] += lo[h];
-            }
-            tmem_wait_ld();
-            const int d = 128 * m + tok;  // lane = latent dim
-#pragma unroll
-            for (int h = 0; h < kHW; ++h) {
-                const float x = o[h] * a_s[hb + h];
-                if (whole) reinterpret_cast<__nv_bfloat16*>(smem)[(hb + h) * kDv + d] = __float2bfloat16_rn(x);
-                else reinterpret_cast<float*>(smem)[(hb + h) * kDv + d] = x;
-            }
-        }
-        async_fence();
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        if (tid == 0) {
-            void* const dst = whole ? static_cast<void*>(p.out + ((int64_t)row * p.H + h0) * (kDv * 2))
-                                    : static_cast<void*>(p.part + slot * (kNH * kDv));
-            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
-                         "r"(smem_u32(smem)), "r"((uint32_t)(nh * kDv * (whole ? 2 : 4)))
-                         : "memory");
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        }
-        __syncthreads();
-        g += n;
-        row += p.row_mode ? p.ranges : 1;
-        tile = 0;
-    }
-    if (aborted) {
-        // A wait gave up. Before the CTA leaves, wait (bounded) for what may still
-        // be in flight: the tile loads and MMAs of the last two tiles.
-        __syncthreads();
-        if (tid == 0) {
-            for (uint32_t k = 0; k < 2; ++k) {
-                mbar_drain(bar_kv + k, 0, p.wait_ns);
-                mbar_drain(bar_kv + k, 1, p.wait_ns);
-            }
-            mbar_drain(bar_s, it & 1, p.wait_ns);
-            mbar_drain(bar_o, it & 1, p.wait_ns);
-        }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0)
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem;
+
+    if (warp == kLoadWarp) {
+        // ---- loads (the warp walks together, lane 0 issues)
+        if (!p.row_mode) {
+            if (p.B > 32) {
+                row = p.B;
+                if (g < g_end) {  // (a range of no tiles has found no row)
+                    row = sh->find[0];
+                    tile = sh->find[1];
+                    n_row = sh->find[2];
+                    length = row_length(p, row);
+                }
+            } else {  // few rows: a lane a row
+                const int n = lane < p.B ? row_tiles(p, length) : 0;
+                int x = n;
+#pragma unroll 1
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o) x += y;
+                }
+                const int total = __shfl_sync(0xffffffffu, x, 31), pre = x - n;
+                int per = (total + p.ranges - 1) / p.ranges;
+                if (per < p.min_tiles) per = p.min_tiles;
+                const int64_t lo = (int64_t)range * per, hi = lo + per;
+                g = lo < total ? (int)lo : total;
+                g_end = hi < total ? (int)hi : total;
+                const uint32_t here = __ballot_sync(0xffffffffu, n > 0 && pre <= g && g < pre + n);
+                row = here ? __ffs(here) - 1 : 0;
+                tile = g - __shfl_sync(0xffffffffu, pre, row);
+                n_row = __shfl_sync(0xffffffffu, n, row);
+                length = __shfl_sync(0xffffffffu, length, row);
+                if (hblk == 0 && lane < p.B) tell_row(p, lane, n, pre, g, g_end, per, range);
+            }
+        }
+        uint32_t t = 0;
+        bool ok = true, known = !p.row_mode;
+        while (ok && row < p.B && (p.row_mode || g < g_end)) {
+            if (!known) {
+                length = row_length(p, row);
+                n_row = row_tiles(p, length);
+            }
+            known = false;
+            if (n_row == 0 && p.row_mode) {  // a row that sees nothing
+                uint4* const o = reinterpret_cast<uint4*>(p.out + ((int64_t)row * p.H + h0) * (kDv * 2));
+                for (int i = lane; i < nh * (kDv / 8); i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (p.lse != nullptr)
+                    for (int i = lane; i < nh; i += 32) p.lse[(int64_t)row * p.H + h0 + i] = -INFINITY;
+            }
+            const int n = p.row_mode || n_row - tile < g_end - g ? n_row - tile : g_end - g;
+            if (n > 0) {
+                Cursor c;
+                c.seek(p, length, tile);
+                const uint32_t about = (tile == 0 ? kStarts : 0u) | (tile == 0 && n == n_row ? kWhole : 0u);
+                for (int i = 0; i < n; ++i, ++t) {
+                    const uint32_t st = t & 1, par = ((t >> 1) + 1) & 1;
+                    uint8_t* const kv = smem + st * S::kStage;
+                    const int tok0 = (int)c.token();
+                    if (lane == 0) {
+                        sh->info[t & 3] = {(uint32_t)tok0, c.valid(),
+                                           c.j | about | (i == 0 ? kFirst : 0u) | (i == n - 1 ? kLast : 0u), row};
+                        mbar_arrive(&sh->info_full[t & 3]);
+                    }
+#pragma unroll 1
+                    for (int a = 0; a < 4; ++a) {
+                        if (t >= 2) ok = mbar_wait(&sh->kv_free[st][a], par, abort_flag, p.status, p.wait_ns);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            uint64_t* const bar = &sh->kv_full[st][a];
+                            mbar_expect_tx(bar, kSlice + (a == 3 ? S::kRopeSlice : 0));
+                            tma_load_3d(kv + a * kSlice, &p.tm_latent[c.j], a * 128, tok0, row, bar);
+                            if (S::kHasRope && a == 3)
+                                tma_load_3d(kv + 4 * kSlice, &p.tm_rope[c.j], kDv, tok0, row, bar);
+                            sh->armed[st][a] = (int)(t >> 1);
+                        }
+                    }
+                    if (!ok) break;
+                    c.next(p);
+                    if (i + 1 < n && t >= 1 && lane == 0) {  // the next tile's stage is still in use: to L2 meanwhile
+#pragma unroll 1
+                        for (int a = 0; a < 4; ++a) tma_prefetch_3d(&p.tm_latent[c.j], a * 128, (int)c.token(), row);
+                        if constexpr (S::kHasRope) tma_prefetch_3d(&p.tm_rope[c.j], kDv, (int)c.token(), row);
+                    }
+                }
+            }
+            g += n;
+            row += p.row_mode ? p.ranges : 1;
+            tile = 0;
+        }
+        if (lane == 0) {
+            if (ok) {  // no more tiles: a tile of no tokens
+                if (t >= 4) ok = mbar_wait(&sh->kv_free[t & 1][3], ((t >> 1) + 1) & 1, abort_flag, p.status, p.wait_ns);
+                sh->info[t & 3] = {0u, 0, 0u, 0};
+                mbar_arrive(&sh->info_full[t & 3]);
+            }
+            // after a wait that gave up, what was armed still lands before the CTA leaves
+            if (*abort_flag)
+                for (int k = 0; k < 8; ++k) {
+                    const int n = sh->armed[k >> 2][k & 3];
+                    if (n >= 0) mbar_drain(&sh->kv_full[k >> 2][k & 3], (uint32_t)(n & 1), p.wait_ns);
+                }
+        }
+    } else if (warp == kMmaWarp) {
+        // ---- MMAs: scores of tile a and values of tile b, b <= a <= b + 1, whichever is ready. The whole warp
+        // walks the loop on values that are the same in every lane (so that descriptors live in uniform
+        // registers, and an MMA costs one instruction), and one elected lane issues.
+        uint32_t a = 0, b = 0, segs = 0, idle = 0;
+        int slice = -1;  // of tile a: -1 not looked at
+        bool more = true;
+        long long t0 = 0;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), base = smem_u32(smem);
+        while (more || b < a) {
+            bool did = false;
+            if (more && slice < 0 && a - b < 2 &&
+                __all_sync(0xffffffffu, mbar_test(&sh->info_full[a & 3], (a >> 2) & 1) &&
+                                            (a == 0 || mbar_test(&sh->s_free, (a - 1) & 1)))) {
+                const int valid = __shfl_sync(0xffffffffu, sh->info[a & 3].valid, 0);
+                const uint32_t first = __shfl_sync(0xffffffffu, sh->info[a & 3].what, 0) & kFirst;
+                if (valid == 0) {
+                    more = false;
+                } else if (!first || __all_sync(0xffffffffu, mbar_test(&sh->q_full, segs & 1))) {
+                    segs += first ? 1 : 0;
+                    slice = 0;
+                }
+            }
+            if (slice >= 0 && __all_sync(0xffffffffu, mbar_test(&sh->kv_full[a & 1][slice], (a >> 1) & 1))) {
+                // (slices land in order: with the last one there, all are)
+                const int to =
+                    __all_sync(0xffffffffu, mbar_test(&sh->kv_full[a & 1][3], (a >> 1) & 1)) ? 4 : slice + 1;
+                tc_fence_after();
+                issue_scores<S>(base + (a & 1) * S::kStage, base + 2 * S::kStage, tm, kIdS, slice, to, &sh->s_full);
+                slice = to;
+                if (slice == 4) {
+                    slice = -1;
+                    ++a;
+                }
+                did = true;
+            } else if (b < a && __all_sync(0xffffffffu, mbar_test(&sh->p_full, b & 1))) {
+                const uint32_t go_on = __shfl_sync(0xffffffffu, sh->info[b & 3].what, 0) & kFirst ? 0u : 1u;
+                tc_fence_after();
+                issue_values<S>(base + (b & 1) * S::kStage, base + 2 * S::kStage + S::kQBytes, tm, kIdO, go_on,
+                                sh->kv_free[b & 1], &sh->o_done);
+                ++b;
+                did = true;
+            }
+            if (did) {
+                idle = 0;
+            } else if (++idle == 64) {
+                t0 = global_ns();
+            } else if (idle > 64 && (idle & 63) == 0) {
+                bool stop = *abort_flag != 0;
+                if (!stop && global_ns() - t0 > p.wait_ns) {
+                    stop = true;
+                    *abort_flag = 1;
+                    if (p.status != nullptr) atomicOr(p.status, 1);
+                }
+                if (__any_sync(0xffffffffu, stop)) break;
+            }
+        }
+        if (elect_one()) mma_commit(&sh->drained);
+        mbar_drain(&sh->drained, 0, p.wait_ns);
+    } else {
+        // ---- softmax
+        const int group = warp >> 2, quad = warp & 3, tok = quad * 32 + lane, hb = group * kHW;
+        const uint32_t tlane = tmem + ((uint32_t)(32 * quad) << 16);
+        // 4 x 4 bytes are transposed between neighbouring lanes: each stage's byte selectors
+        const uint32_t sel1 = (lane & 1) ? 0x3715u : 0x6240u, sel2 = (lane & 2) ? 0x3276u : 0x5410u;
+        if (warp < 4) {  // the cached tile's scale is 1 everywhere: its own scale goes into the probabilities
+            const float one[4] = {__uint_as_float(0x7f7f7f7fu), __uint_as_float(0x7f7f7f7fu),
+                                  __uint_as_float(0x7f7f7f7fu), __uint_as_float(0x7f7f7f7fu)};
+            tmem_st4(tlane + S::kSf, one);
+            tmem_wait_st();  // (ordered before the first values by the probabilities' barrier)
+        }
+        uint32_t t = 0, met = 0;
+        bool aborted = false;
+        // the four warps of the group meet (a bounded wait, as every wait of this kernel)
+        auto meet = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->met[group]);
+            return (bool)__all_sync(0xffffffffu,
+                                    mbar_wait(&sh->met[group], met++ & 1, abort_flag, p.status, p.wait_ns));
+        };
+        while (!aborted) {  // segments
+            bool ok = mbar_wait(&sh->info_full[t & 3], (t >> 2) & 1, abort_flag, p.status, p.wait_ns);
+            const int row = sh->info[t & 3].row;
+            // (all warps agree: this is also where they leave together)
+            if (soft_any(!ok)) break;
+            if (sh->info[t & 3].valid == 0) break;
+
+            // q: hi and lo e4m3 parts of each head at its own power-of-two scale. A head's bf16 values come into the
+            // place of its two parts first (128 dims of a slice are 256 bytes either way), all of a warp's heads in
+            // flight at once; a lane then has dims 4l .. 4l + 3 of each slice and 2l, 2l + 1 of the rotary part.
+            constexpr int kWords = kDk / 64;
+#pragma unroll 1
+            for (int h = warp; h < kNH; h += kSoftWarps) {
+                const uint8_t* const src = p.q + row * p.q_row + (h0 + (h < nh ? h : 0)) * p.q_head + 4 * lane;
+                const uint32_t dst = smem_u32(q_s) + h * 128 + 4 * lane, bytes = h < nh ? 4u : 0u;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    copy_word(dst + (i >> 1) * S::kQSlice + (i & 1) * kNH * 128, src + 128 * i, bytes);
+                if constexpr (S::kHasRope)
+                    copy_word(smem_u32(q_s) + 4 * S::kQSlice + (h + (lane >> 4) * kNH) * 64 + 4 * (lane & 15),
+                              src + 1024, bytes);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
+#pragma unroll 1
+            for (int h = warp; h < kNH; h += kSoftWarps) {
+                uint32_t w[kWords];
+                {
+                    const uint8_t* const at = q_s + (h + (lane >> 4) * kNH) * 128 + 8 * (lane & 15);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint2 v = *reinterpret_cast<const uint2*>(at + i * S::kQSlice);
+                        w[2 * i] = v.x;
+                        w[2 * i + 1] = v.y;
+                    }
+                    if constexpr (S::kHasRope)
+                        w[8] = *reinterpret_cast<const uint32_t*>(q_s + 4 * S::kQSlice + (h + (lane >> 4) * kNH) * 64 +
+                                                                  4 * (lane & 15));
+                    __syncwarp();
+                }
+                uint32_t u = 0;  // the largest magnitude (their bits order like integers)
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) u = max(u, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
+                u = __reduce_max_sync(0xffffffffu, u);
+                int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);  // top <= 448 * 2^e
+                e = e < -120 ? -120 : e;
+                const bool bad = u >= 0x7f800000u;  // a NaN or an infinity: the whole head is NaN
+                const float inv = bad ? __uint_as_float(0x7fffffffu) : __uint_as_float((uint32_t)(127 - e) << 23);
+                if (lane == 0) g_s[h] = bad ? 1.f : __uint_as_float((uint32_t)(127 + e) << 23);
+                // hi: x to 4 significand bits (halves away from zero), nothing of what e4m3 has as a subnormal;
+                // lo: the rest, at most 4 bits of it above 2^-9
+                uint32_t hi[kWords], lo[kWords];
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) {
+                    const float x = __uint_as_float(w[i] << 16) * inv, y = __uint_as_float(w[i] & 0xffff0000u) * inv;
+                    const float xh = fabsf(x) < 0.015625f ? 0.f
+                                                          : __uint_as_float((__float_as_uint(x) + 0x80000u) & 0xfff00000u);
+                    const float yh = fabsf(y) < 0.015625f ? 0.f
+                                                          : __uint_as_float((__float_as_uint(y) + 0x80000u) & 0xfff00000u);
+                    hi[i] = __nv_cvt_float2_to_fp8x2(make_float2(xh, yh), __NV_SATFINITE, __NV_E4M3);
+                    lo[i] = __nv_cvt_float2_to_fp8x2(make_float2(x - xh, y - yh), __NV_SATFINITE, __NV_E4M3);
+                }
+                // (kNH is a multiple of 8: the rows of both parts are swizzled alike)
+                uint8_t* const at = q_s + h * 128 + (((lane >> 2) ^ (h & 7)) << 4) + ((4 * lane) & 15);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    *reinterpret_cast<uint32_t*>(at + i * S::kQSlice) = hi[2 * i] | (hi[2 * i + 1] << 16);
+                    *reinterpret_cast<uint32_t*>(at + i * S::kQSlice + kNH * 128) = lo[2 * i] | (lo[2 * i + 1] << 16);
+                }
+                if constexpr (S::kHasRope) {
+                    uint8_t* const ar = q_s + 4 * S::kQSlice + h * 64 + (((lane >> 3) ^ ((h >> 1) & 3)) << 4) +
+                                        ((2 * lane) & 15);
+                    *reinterpret_cast<uint16_t*>(ar) = (uint16_t)hi[8];
+                    *reinterpret_cast<uint16_t*>(ar + kNH * 64) = (uint16_t)lo[8];
+                }
+            }
+            if (tid < kNH) m_s[tid] = kMagicBits - kFar;
+            async_fence();
+            soft_sync();  // (every group reads scales and references that all warps wrote)
+            if (lane == 0) mbar_arrive(&sh->q_full);
+
+            f32x2 l2[kHW / 2];
+#pragma unroll
+            for (int h = 0; h < kHW / 2; ++h) l2[h] = 0ull;
+
+            TileInfo ti;
+            for (bool first = true;; first = false, ++t) {
+                ok = mbar_wait(&sh->info_full[t & 3], (t >> 2) & 1, abort_flag, p.status, p.wait_ns);
+                ti = sh->info[t & 3];
+                // this thread's token's scale, in flight beside the scores
+                float u = 1.f;
+                const int valid = ti.valid;
+                if (ok) {
+                    const uint32_t loc = ti.token + (uint32_t)(tok < valid ? tok : valid - 1);
+                    u = p.scales[ti.what & 255u][(int64_t)row * p.blocks + (loc >> p.block_log2)];
+                }
+                ok = ok && mbar_wait(&sh->s_full, t & 1, abort_flag, p.status, p.wait_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();
+                float sv[kHW];
+                f32x2 ru2;
+                {
+                    float lo[kHW];
+                    tmem_ld<kHW>(tlane + hb, sv);
+                    tmem_ld<kHW>(tlane + kNH + hb, lo);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    if (lane == 0) mbar_arrive(&sh->s_free);
+                    u = fmaxf(u, 7.888609e-31f);  // 2^-100: a scale of 0 is that of zeros
+                    const float c = u * p.scale_log2, lu = __log2f(u);
+                    const float ru = __fdividef(1.0f, u);
+                    ru2 = pack2(ru, ru);
+                    const f32x2 c2 = pack2(c, c), lu2 = pack2(lu, lu);
+#pragma unroll
+                    for (int h = 0; h < kHW; h += 4) {
+                        const float4 g = *reinterpret_cast<const float4*>(g_s + hb + h);
+                        unpack2(fma2(add2(pack2(sv[h], sv[h + 1]), pack2(lo[h], lo[h + 1])),
+                                     mul2(pack2(g.x, g.y), c2), lu2),
+                                sv[h], sv[h + 1]);
+                        unpack2(fma2(add2(pack2(sv[h + 2], sv[h + 3]), pack2(lo[h + 2], lo[h + 3])),
+                                     mul2(pack2(g.z, g.w), c2), lu2),
+                                sv[h + 2], sv[h + 3]);
+                    }
+                }
+                if (valid < kTile && tok >= valid) {
+                    // a token that is not visible may hold anything: probability 0 (2^-kRange, and with a whole
+                    // warp of them scale 2^-127), and a value row of zeros (0 x NaN)
+#pragma unroll
+                    for (int h = 0; h < kHW; ++h) sv[h] = -(float)kRange;
+                    uint4* const r = reinterpret_cast<uint4*>(smem + (t & 1) * S::kStage + group * kSlice + tok * 128);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) r[(k + tok) & 7] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                // E, the 32 tokens' largest score rounded to an integer, per head; how far it lies from the reference;
+                // and P = 2^(s - E + 8) in (0, 2^8.5], which does not depend on the reference
+                int d[kHW], far = INT_MIN;
+                uint32_t wh[kHW / 4], wl[kHW / 4];
+                const f32x2 neg = pack2(-1.f, -1.f);
+#pragma unroll
+                for (int h = 0; h < kHW; h += kHW < 8 ? 4 : 8) {
+                    constexpr int kB = kHW < 8 ? 4 : 8;
+                    float hi[kB], lo[kB];
+#pragma unroll
+                    for (int k = 0; k < kB; k += 2) {
+                        const f32x2 s2 = pack2(sv[h + k], sv[h + k + 1]);
+                        float e0, e1;
+                        unpack2(add2(s2, pack2(kMagic, kMagic)), e0, e1);
+                        const int i0 = __reduce_max_sync(0xffffffffu, __float_as_int(e0));
+                        const int i1 = __reduce_max_sync(0xffffffffu, __float_as_int(e1));
+                        const int2 m = *reinterpret_cast<const int2*>(m_s + hb + h + k);
+                        d[h + k] = i0 - m.x;
+                        d[h + k + 1] = i1 - m.y;
+                        far = max(far, max(d[h + k], d[h + k + 1]));
+                        const f32x2 e8 = fma2(pack2(__int_as_float(i0), __int_as_float(i1)), neg,
+                                              pack2(kMagic + 8.f, kMagic + 8.f));
+                        float x, y;
+                        unpack2(add2(s2, e8), x, y);
+                        sv[h + k] = ex2(x);
+                        sv[h + k + 1] = ex2(y);
+                        // the nearest numbers of 4 significand bits, and the rest
+                        hi[k] = __uint_as_float((__float_as_uint(sv[h + k]) + 0x80000u) & 0xfff00000u);
+                        hi[k + 1] = __uint_as_float((__float_as_uint(sv[h + k + 1]) + 0x80000u) & 0xfff00000u);
+                        unpack2(fma2(pack2(hi[k], hi[k + 1]), neg, pack2(sv[h + k], sv[h + k + 1])), lo[k], lo[k + 1]);
+                    }
+                    // A word is four heads of this token (every other head: their rows lie on different banks);
+                    // transposed between four lanes it is four tokens of one head.
+#pragma unroll
+                    for (int w = 0; w < kB / 4; ++w) {
+                        constexpr int kS = kB / 4;
+                        uint32_t vh = codes4(hi[w], hi[w + kS], hi[w + 2 * kS], hi[w + 3 * kS]);
+                        uint32_t vl = codes4(lo[w], lo[w + kS], lo[w + 2 * kS], lo[w + 3 * kS]);
+                        vh = __byte_perm(vh, __shfl_xor_sync(0xffffffffu, vh, 1), sel1);
+                        vl = __byte_perm(vl, __shfl_xor_sync(0xffffffffu, vl, 1), sel1);
+                        wh[h / 4 + w] = __byte_perm(vh, __shfl_xor_sync(0xffffffffu, vh, 2), sel2);
+                        wl[h / 4 + w] = __byte_perm(vl, __shfl_xor_sync(0xffffffffu, vl, 2), sel2);
+                    }
+                }
+                // Did the reference of some head fall behind? Each warp says so now and hears the others below. The
+                // scales 2^(E - M - 8) and P's share of the sums take the present reference: if it moves by `up`,
+                // everything is multiplied by 2^-up.
+                if (lane == 0) {
+                    if (far > kLazy) sh->moved[group][t & 1] = 1;
+                    mbar_arrive(&sh->voted[group]);
+                }
+                int* const mine = red_i + quad * kNH + hb;  // this warp's words
+#pragma unroll
+                for (int h = 0; h < kHW; h += 2) {
+                    d[h] = max(d[h] + 119, 0);
+                    d[h + 1] = max(d[h + 1] + 119, 0);
+                    l2[h / 2] = fma2(mul2(pack2(sv[h], sv[h + 1]), ru2),
+                                     pack2(__int_as_float(d[h] << 23), __int_as_float(d[h + 1] << 23)), l2[h / 2]);
+                }
+                if (lane == 0) {
+#pragma unroll
+                    for (int h = 0; h < kHW; h += 4)
+                        *reinterpret_cast<int4*>(mine + h) = make_int4(d[h], d[h + 1], d[h + 2], d[h + 3]);
+                }
+                __syncwarp();
+                int sf = lane < kHW ? mine[lane] : 0;
+                const bool heard =
+                    __all_sync(0xffffffffu, mbar_wait(&sh->voted[group], t & 1, abort_flag, p.status, p.wait_ns));
+                ok = ok && heard;
+                if (heard && *(volatile int*)&sh->moved[group][t & 1]) {
+                    ok = meet() && ok;
+                    if (quad == 0 && lane < kHW) {
+                        const int r = hb + lane;
+                        int up = 0;
+#pragma unroll 1
+                        for (int k = 0; k < 4; ++k) up = max(up, red_i[k * kNH + r] - 119);
+                        const int m = m_s[r] + up;
+                        // out of range, or NaN: the head's sums become NaN
+                        const bool bad = m >= kMagicBits + kRange || m <= kMagicBits - kRange;
+                        a_s[r] = bad ? __int_as_float(0x7fffffff) : up > 100 ? 0.f : ex2(-(float)up);
+                        m_s[r] = m;
+                        up_s[r] = up;
+                        if (lane == 0) sh->moved[group][t & 1] = 0;
+                    }
+                    ok = meet() && ok;
+                    if (lane < kHW) sf = max(sf - up_s[hb + lane], 0);
+#pragma unroll
+                    for (int h = 0; h < kHW; h += 2) {
+                        // (a move by more than 2^100 leaves nothing of the sums before, and 2^E was out of range)
+                        const float2 f = *reinterpret_cast<const float2*>(a_s + hb + h);
+                        const int2 up = *reinterpret_cast<const int2*>(up_s + hb + h);
+                        const f32x2 z = mul2(mul2(pack2(sv[h], sv[h + 1]), ru2),
+                                             pack2(__int_as_float(max(d[h] - up.x, 0) << 23),
+                                                   __int_as_float(max(d[h + 1] - up.y, 0) << 23)));
+                        float x, y, zx, zy;
+                        unpack2(mul2(l2[h / 2], pack2(f.x, f.y)), x, y);
+                        unpack2(z, zx, zy);
+                        l2[h / 2] = pack2(up.x > 100 ? zx + f.x : x, up.y > 100 ? zy + f.y : y);
+                    }
+                    if (!first) {  // O as well, once the values before are added
+                        ok = mbar_wait(&sh->o_done, (t - 1) & 1, abort_flag, p.status, p.wait_ns) && ok;
+                        __syncwarp();
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < 4 * (S::kStacked ? 2 : 1) * (kHW / 4); ++c) {
+                            const int h = (c % (kHW / 4)) * 4, b = c / (kHW / 4);
+                            const uint32_t col =
+                                tlane + S::kO + (S::kStacked ? (b >> 1) * S::kOB + (b & 1) * kNH : b * S::kOB) + hb + h;
+                            float o[4];
+                            tmem_ld<4>(col, o);
+                            const float4 f = *reinterpret_cast<const float4*>(a_s + hb + h);
+                            tmem_wait_ld();
+                            o[0] *= f.x;
+                            o[1] *= f.y;
+                            o[2] *= f.z;
+                            o[3] *= f.w;
+                            tmem_st4(col, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                // the buffer of P is free once the values before are added
+                if (t > 0) ok = mbar_wait(&sh->o_done, (t - 1) & 1, abort_flag, p.status, p.wait_ns) && ok;
+                // (warps of a group leave at one place: at the end of a tile, when a wait gave up anywhere)
+                uint8_t* const p_lo =
+                    S::kLoInRope ? smem + (t & 1) * S::kStage + 4 * kSlice : p_s + kNH * 128;
+#pragma unroll
+                for (int w = 0; w < kHW / 4; ++w) {
+                    constexpr int kS = kHW < 8 ? 1 : 2;
+                    const int r = hb + (w / kS) * 4 * kS + (w % kS) + (lane & 3) * kS;  // this lane's head
+                    const int at = r * 128 + (((tok >> 4) ^ (r & 7)) << 4) + (tok & 12);
+                    *reinterpret_cast<uint32_t*>(p_s + at) = wh[w];
+                    *reinterpret_cast<uint32_t*>(p_lo + at) = wl[w];
+                }
+                if (lane < kHW) {
+                    const int r = hb + lane;
+                    sf_s[(r & 31) * 16 + (r >> 5) * 4 + quad] = (uint8_t)sf;
+                    if constexpr (S::kStacked)
+                        sf_s[((r + kNH) & 31) * 16 + ((r + kNH) >> 5) * 4 + quad] = (uint8_t)sf;
+                }
+                async_fence();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->p_full);
+                aborted = __any_sync(0xffffffffu, !ok);
+                if (aborted || (ti.what & kLast)) break;
+            }
+            ++t;
+            // ---- the segment's end: sums, then O / l
+            if (!aborted) {
+                const bool ok =
+                    __all_sync(0xffffffffu, mbar_wait(&sh->o_done, (t - 1) & 1, abort_flag, p.status, p.wait_ns));
+                tc_fence_after();
+                // sums over the warp's tokens: halves of the heads to halves of the lanes until a lane has one head
+                float l[kHW];
+#pragma unroll
+                for (int h = 0; h < kHW; h += 2) unpack2(l2[h / 2], l[h], l[h + 1]);
+                int off = 16;
+#pragma unroll
+                for (int k = kHW / 2; k >= 1; k /= 2, off /= 2) {
+                    const bool upper = (lane & off) != 0;
+#pragma unroll
+                    for (int h = 0; h < k; ++h) {
+                        const float give = upper ? l[h] : l[h + k], keep = upper ? l[h + k] : l[h];
+                        l[h] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+                    }
+                }
+#pragma unroll
+                for (; off >= 1; off /= 2) l[0] += __shfl_xor_sync(0xffffffffu, l[0], off);
+                if ((lane & (32 / kHW - 1)) == 0) red[quad * kNH + hb + lane / (32 / kHW)] = l[0];
+                aborted = !meet() || !ok;
+                const bool whole = (ti.what & kWhole) != 0;  // the row's only segment
+                const int64_t slot = (int64_t)blockIdx.x * 2 + ((ti.what & kStarts) ? 1 : 0);
+                if (quad == 0 && lane < kHW) {
+                    const int r = hb + lane;
+                    const float l = (red[r] + red[kNH + r]) + (red[2 * kNH + r] + red[3 * kNH + r]);
+                    a_s[r] = __fdividef(1.0f, l);
+                    const float lse2 = (float)(m_s[r] - kMagicBits) + log2f(l);
+                    if (!whole) p.part_lse[slot * kNH + r] = lse2;
+                    else if (p.lse != nullptr && r < nh) p.lse[(int64_t)row * p.H + h0 + r] = lse2 * p.lse_scale;
+                }
+                aborted = !meet() || aborted;
+                float inv[kHW];
+#pragma unroll
+                for (int h = 0; h < kHW; h += 4) *reinterpret_cast<float4*>(inv + h) = *reinterpret_cast<const float4*>(a_s + hb + h);
+#pragma unroll 1
+                for (int m = 0; m < 4; ++m) {
+                    float o[kHW];
+                    tmem_ld<kHW>(tlane + S::kO + m * S::kOB + hb, o);
+                    if constexpr (S::kStacked) {
+                        float lo[kHW];
+                        tmem_ld<kHW>(tlane + S::kO + m * S::kOB + kNH + hb, lo);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int h = 0; h < kHW; ++h) o[h] += lo[h];
+                    }
+                    tmem_wait_ld();
+                    const int d = 128 * m + tok;  // lane = latent dim: a warp's store is contiguous
+                    if (whole) {
+                        __nv_bfloat16* const dst =
+                            reinterpret_cast<__nv_bfloat16*>(p.out) + ((int64_t)row * p.H + h0 + hb) * kDv + d;
+#pragma unroll
+                        for (int h = 0; h < kHW; ++h)
+                            if (hb + h < nh) dst[h * kDv] = __float2bfloat16_rn(o[h] * inv[h]);
+                    } else {
+                        float* const dst = p.part + slot * (kNH * kDv) + hb * kDv + d;
+#pragma unroll
+                        for (int h = 0; h < kHW; ++h) dst[h * kDv] = o[h] * inv[h];
+                    }
+                }
+                tc_fence_before();
+            }
+            // (the next segment writes what this one's threads have read; all warps leave together)
+            aborted = soft_any(aborted);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kCols) : "memory");
 }
 
@@ -752,10 +1167,10 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Decod
     const int64_t unit = (int64_t)blockIdx.x * (8 / kWarps) + warp / kWarps;
     if (unit >= (int64_t)p.B * p.H) return;
     const int b = (int)(unit / p.H), h = (int)(unit - (int64_t)b * p.H);
-    const int n = row_tiles(p, b);
+    const int2 row = p.row_info[b];
     uint4* const out = reinterpret_cast<uint4*>(p.out + unit * (kDv * 2));
     const int w = warp % kWarps;
-    if (n == 0) {
+    if (row.y == 0) {
         if (w == 0) {
             out[lane] = make_uint4(0u, 0u, 0u, 0u);
             out[32 + lane] = make_uint4(0u, 0u, 0u, 0u);
@@ -763,9 +1178,8 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Decod
         }
         return;
     }
-    const int per = p.row_info[p.B], pre = p.row_info[b];
-    const int k0 = pre / per, k1 = (pre + n - 1) / per;
-    if (k0 == k1) return;
+    if (row.y == 1) return;
+    const int k0 = row.x, k1 = k0 + row.y - 1;
     const int hblk = h / heads_of_block, hh = h - hblk * heads_of_block;
     auto slot = [&](int k) { return ((int64_t)k * p.head_blocks + hblk) * 2 + (k == k0 ? 1 : 0); };
     float m = -INFINITY;
@@ -885,7 +1299,7 @@ Workspace workspace_of(int64_t B, int H, int num_sms) {
     w.part = 0;
     w.part_lse = w.part + round_up(2 * ctas * nh * kDv * 4);
     w.row_info = w.part_lse + round_up(2 * ctas * nh * 4);
-    w.bytes = w.row_info + round_up((B + 1) * 4);
+    w.bytes = w.row_info + round_up(B * 8);
     return w;
 }
 
@@ -930,7 +1344,8 @@ cudaError_t launch_decode(const DecodeParams& p, unsigned flags, cudaStream_t st
     if (e != cudaSuccess || p.row_mode) return e;
     // the join overlaps its launch with the decode's tail and waits for it on the device
     const int64_t units = (int64_t)p.B * p.H;
-    const bool few = units <= 512;
+    // eight warps a (row, head) where a row has four segments or more on average, else one
+    const bool few = p.ranges >= 4 * p.B;
     cfg.gridDim = dim3((unsigned)(few ? units : (units + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
@@ -1014,7 +1429,7 @@ extern "C" int dcp_mla_cache8_decode(const void* q, int64_t q_row, int64_t q_hea
     p.seq_lens = seq_lens;
     p.part = reinterpret_cast<float*>(w + ws.part);
     p.part_lse = reinterpret_cast<float*>(w + ws.part_lse);
-    p.row_info = reinterpret_cast<int*>(w + ws.row_info);
+    p.row_info = reinterpret_cast<int2*>(w + ws.row_info);
     p.out = static_cast<uint8_t*>(out);
     p.lse = lse;
     p.status = status;
