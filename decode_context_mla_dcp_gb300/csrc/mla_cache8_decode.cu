@@ -415,15 +415,6 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
 // Four e4m3 codes, the first in the low byte.
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -718,61 +709,45 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 }
         }
     } else if (warp == kMmaWarp) {
-        // ---- MMAs: scores of tile a and values of tile b, b <= a <= b + 1, whichever is ready. The whole warp
-        // walks the loop on values that are the same in every lane (so that descriptors live in uniform
-        // registers, and an MMA costs one instruction), and one elected lane issues.
-        uint32_t a = 0, b = 0, segs = 0, idle = 0;
-        int slice = -1;  // of tile a: -1 not looked at
+        // ---- MMAs, in turn: the scores of a tile, slice by slice as they land, then the values of the tile before.
+        // The whole warp walks the loop on values that are the same in every lane (so that descriptors live in
+        // uniform registers, and an MMA costs one instruction), and one elected lane issues.
+        uint32_t t = 0, segs = 0;
         bool more = true;
-        long long t0 = 0;
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), base = smem_u32(smem);
-        while (more || b < a) {
-            bool did = false;
-            if (more && slice < 0 && a - b < 2 &&
-                __all_sync(0xffffffffu, mbar_test(&sh->info_full[a & 3], (a >> 2) & 1) &&
-                                            (a == 0 || mbar_test(&sh->s_free, (a - 1) & 1)))) {
-                const int valid = __shfl_sync(0xffffffffu, sh->info[a & 3].valid, 0);
-                const uint32_t first = __shfl_sync(0xffffffffu, sh->info[a & 3].what, 0) & kFirst;
-                if (valid == 0) {
-                    more = false;
-                } else if (!first || __all_sync(0xffffffffu, mbar_test(&sh->q_full, segs & 1))) {
-                    segs += first ? 1 : 0;
-                    slice = 0;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, p.wait_ns));
+        };
+        bool began = false;  // tile t - 1 is the first of a segment
+        auto values = [&](uint32_t v) {
+            if (!wait(&sh->p_full, v & 1)) return false;
+            tc_fence_after();
+            issue_values<S>(base + (v & 1) * S::kStage, base + 2 * S::kStage + S::kQBytes, tm, kIdO, began ? 0u : 1u,
+                            sh->kv_free[v & 1], &sh->o_done);
+            return true;
+        };
+        while (more) {
+            if (!wait(&sh->info_full[t & 3], (t >> 2) & 1)) break;
+            const bool first = (__shfl_sync(0xffffffffu, sh->info[t & 3].what, 0) & kFirst) != 0;
+            more = __shfl_sync(0xffffffffu, sh->info[t & 3].valid, 0) != 0;
+            // (a new segment's q comes after the sums of the last one, and they after its values)
+            const bool turn = t > 0 && (first || !more);
+            if (turn && !values(t - 1)) break;
+            if (more) {
+                if (t > 0 && !wait(&sh->s_free, (t - 1) & 1)) break;
+                if (first && !wait(&sh->q_full, segs++ & 1)) break;
+                bool ok = true;
+#pragma unroll 1
+                for (int s = 0; s < 4 && ok; ++s) {
+                    ok = wait(&sh->kv_full[t & 1][s], (t >> 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_scores<S>(base + (t & 1) * S::kStage, base + 2 * S::kStage, tm, kIdS, s, s + 1, &sh->s_full);
                 }
+                if (!ok || (t > 0 && !turn && !values(t - 1))) break;
             }
-            if (slice >= 0 && __all_sync(0xffffffffu, mbar_test(&sh->kv_full[a & 1][slice], (a >> 1) & 1))) {
-                // (slices land in order: with the last one there, all are)
-                const int to =
-                    __all_sync(0xffffffffu, mbar_test(&sh->kv_full[a & 1][3], (a >> 1) & 1)) ? 4 : slice + 1;
-                tc_fence_after();
-                issue_scores<S>(base + (a & 1) * S::kStage, base + 2 * S::kStage, tm, kIdS, slice, to, &sh->s_full);
-                slice = to;
-                if (slice == 4) {
-                    slice = -1;
-                    ++a;
-                }
-                did = true;
-            } else if (b < a && __all_sync(0xffffffffu, mbar_test(&sh->p_full, b & 1))) {
-                const uint32_t go_on = __shfl_sync(0xffffffffu, sh->info[b & 3].what, 0) & kFirst ? 0u : 1u;
-                tc_fence_after();
-                issue_values<S>(base + (b & 1) * S::kStage, base + 2 * S::kStage + S::kQBytes, tm, kIdO, go_on,
-                                sh->kv_free[b & 1], &sh->o_done);
-                ++b;
-                did = true;
-            }
-            if (did) {
-                idle = 0;
-            } else if (++idle == 64) {
-                t0 = global_ns();
-            } else if (idle > 64 && (idle & 63) == 0) {
-                bool stop = *abort_flag != 0;
-                if (!stop && global_ns() - t0 > p.wait_ns) {
-                    stop = true;
-                    *abort_flag = 1;
-                    if (p.status != nullptr) atomicOr(p.status, 1);
-                }
-                if (__any_sync(0xffffffffu, stop)) break;
-            }
+            began = first;
+            ++t;
         }
         if (elect_one()) mma_commit(&sh->drained);
         mbar_drain(&sh->drained, 0, p.wait_ns);
