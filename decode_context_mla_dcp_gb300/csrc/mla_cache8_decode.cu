@@ -415,6 +415,13 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ __nv_bfloat162 as_bf16x2(uint32_t x) { return *reinterpret_cast<__nv_bfloat162*>(&x); }
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpret_cast<uint32_t*>(&x); }
+// Two e4m3 codes of a pair of bf16, in its order.
+__device__ __forceinline__ uint32_t codes2(uint32_t x) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)),
+                                    __NV_SATFINITE, __NV_E4M3);
+}
 // Four e4m3 codes, the first in the low byte.
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -772,17 +779,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             return (bool)__all_sync(0xffffffffu,
                                     mbar_wait(&sh->met[group], met++ & 1, abort_flag, p.status, p.wait_ns));
         };
-        while (!aborted) {  // segments
-            bool ok = mbar_wait(&sh->info_full[t & 3], (t >> 2) & 1, abort_flag, p.status, p.wait_ns);
-            const int row = sh->info[t & 3].row;
-            // (all warps agree: this is also where they leave together)
-            if (soft_any(!ok)) break;
-            if (sh->info[t & 3].valid == 0) break;
-
-            // q: hi and lo e4m3 parts of each head at its own power-of-two scale. A head's bf16 values come into the
-            // place of its two parts first (128 dims of a slice are 256 bytes either way), all of a warp's heads in
-            // flight at once; a lane then has dims 4l .. 4l + 3 of each slice and 2l, 2l + 1 of the rotary part.
-            constexpr int kWords = kDk / 64;
+        // A segment's q, raw: a head's bf16 values into the place of its two parts (128 dims of a slice are 256 bytes
+        // either way), all of a warp's heads in flight at once.
+        auto fetch_q = [&](int row) {
 #pragma unroll 1
             for (int h = warp; h < kNH; h += kSoftWarps) {
                 const uint8_t* const src = p.q + row * p.q_row + (h0 + (h < nh ? h : 0)) * p.q_head + 4 * lane;
@@ -794,45 +793,55 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     copy_word(smem_u32(q_s) + 4 * S::kQSlice + (h + (lane >> 4) * kNH) * 64 + 4 * (lane & 15),
                               src + 1024, bytes);
             }
+        };
+        // The next tile's description; a tile of no tokens (or a wait that gave up, in any warp) ends the loop.
+        TileInfo ti = {0u, 0, 0u, 0};
+        auto next_segment = [&]() {
+            const bool ok = mbar_wait(&sh->info_full[t & 3], (t >> 2) & 1, abort_flag, p.status, p.wait_ns);
+            ti = sh->info[t & 3];
+            return !soft_any(!ok) && ti.valid > 0;  // (all warps agree)
+        };
+        bool going = next_segment();
+        if (going) fetch_q(ti.row);
+        while (going) {  // segments
+            const int row = ti.row;
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
+            // q: hi and lo e4m3 parts of each head at its own power-of-two scale. A lane has dims 4l .. 4l + 3 of each
+            // slice and 2l, 2l + 1 of the rotary part; the arithmetic is on pairs of bf16, and exact.
+            constexpr int kWords = kDk / 64;
 #pragma unroll 1
             for (int h = warp; h < kNH; h += kSoftWarps) {
                 uint32_t w[kWords];
-                {
-                    const uint8_t* const at = q_s + (h + (lane >> 4) * kNH) * 128 + 8 * (lane & 15);
+                const uint8_t* const raw = q_s + (h + (lane >> 4) * kNH) * 128 + 8 * (lane & 15);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint2 v = *reinterpret_cast<const uint2*>(at + i * S::kQSlice);
-                        w[2 * i] = v.x;
-                        w[2 * i + 1] = v.y;
-                    }
-                    if constexpr (S::kHasRope)
-                        w[8] = *reinterpret_cast<const uint32_t*>(q_s + 4 * S::kQSlice + (h + (lane >> 4) * kNH) * 64 +
-                                                                  4 * (lane & 15));
-                    __syncwarp();
+                for (int i = 0; i < 4; ++i) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(raw + i * S::kQSlice);
+                    w[2 * i] = v.x;
+                    w[2 * i + 1] = v.y;
                 }
-                uint32_t u = 0;  // the largest magnitude (their bits order like integers)
+                if constexpr (S::kHasRope)
+                    w[8] = *reinterpret_cast<const uint32_t*>(q_s + 4 * S::kQSlice + (h + (lane >> 4) * kNH) * 64 +
+                                                              4 * (lane & 15));
+                __syncwarp();
+                __nv_bfloat162 top = __habs2(as_bf16x2(w[0]));  // (the larger of two numbers: a NaN is passed over)
 #pragma unroll
-                for (int i = 0; i < kWords; ++i) u = max(u, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
-                u = __reduce_max_sync(0xffffffffu, u);
+                for (int i = 1; i < kWords; ++i) top = __hmax2(top, __habs2(as_bf16x2(w[i])));
+                uint32_t u = as_u32(top);
+                u = __reduce_max_sync(0xffffffffu, max(u & 0xffff0000u, u << 16));
                 int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);  // top <= 448 * 2^e
                 e = e < -120 ? -120 : e;
-                const bool bad = u >= 0x7f800000u;  // a NaN or an infinity: the whole head is NaN
-                const float inv = bad ? __uint_as_float(0x7fffffffu) : __uint_as_float((uint32_t)(127 - e) << 23);
+                const bool bad = u >= 0x7f800000u;  // an infinity: the whole head is NaN (a NaN stays one by itself)
+                const uint32_t inv = bad ? 0x7fff7fffu : (uint32_t)(127 - e) * 0x00800080u;
                 if (lane == 0) g_s[h] = bad ? 1.f : __uint_as_float((uint32_t)(127 + e) << 23);
-                // hi: x to 4 significand bits (halves away from zero), nothing of what e4m3 has as a subnormal;
-                // lo: the rest, at most 4 bits of it above 2^-9
                 uint32_t hi[kWords], lo[kWords];
 #pragma unroll
                 for (int i = 0; i < kWords; ++i) {
-                    const float x = __uint_as_float(w[i] << 16) * inv, y = __uint_as_float(w[i] & 0xffff0000u) * inv;
-                    const float xh = fabsf(x) < 0.015625f ? 0.f
-                                                          : __uint_as_float((__float_as_uint(x) + 0x80000u) & 0xfff00000u);
-                    const float yh = fabsf(y) < 0.015625f ? 0.f
-                                                          : __uint_as_float((__float_as_uint(y) + 0x80000u) & 0xfff00000u);
-                    hi[i] = __nv_cvt_float2_to_fp8x2(make_float2(xh, yh), __NV_SATFINITE, __NV_E4M3);
-                    lo[i] = __nv_cvt_float2_to_fp8x2(make_float2(x - xh, y - yh), __NV_SATFINITE, __NV_E4M3);
+                    // hi: to 4 significand bits (halves away from zero); lo: the rest, at most 4 bits
+                    const __nv_bfloat162 x = __hmul2(as_bf16x2(w[i]), as_bf16x2(inv));
+                    const uint32_t xh = (as_u32(x) + 0x00080008u) & 0xfff0fff0u;
+                    hi[i] = codes2(xh);
+                    lo[i] = codes2(as_u32(__hsub2(x, as_bf16x2(xh))));
                 }
                 // (kNH is a multiple of 8: the rows of both parts are swizzled alike)
                 uint8_t* const at = q_s + h * 128 + (((lane >> 2) ^ (h & 7)) << 4) + ((4 * lane) & 15);
@@ -857,9 +866,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 #pragma unroll
             for (int h = 0; h < kHW / 2; ++h) l2[h] = 0ull;
 
-            TileInfo ti;
+            const uint32_t about = ti.what;  // (of the first tile: how the segment lies in its row)
             for (bool first = true;; first = false, ++t) {
-                ok = mbar_wait(&sh->info_full[t & 3], (t >> 2) & 1, abort_flag, p.status, p.wait_ns);
+                bool ok = mbar_wait(&sh->info_full[t & 3], (t >> 2) & 1, abort_flag, p.status, p.wait_ns);
                 ti = sh->info[t & 3];
                 // this thread's token's scale, in flight beside the scores
                 float u = 1.f;
@@ -1053,6 +1062,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 if (aborted || (ti.what & kLast)) break;
             }
             ++t;
+            // The next segment's q is on its way while this one ends (its scores are all done: q's place is free).
+            going = next_segment();
+            if (going) fetch_q(ti.row);
             // ---- the segment's end: sums, then O / l
             if (!aborted) {
                 const bool ok =
@@ -1076,8 +1088,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 for (; off >= 1; off /= 2) l[0] += __shfl_xor_sync(0xffffffffu, l[0], off);
                 if ((lane & (32 / kHW - 1)) == 0) red[quad * kNH + hb + lane / (32 / kHW)] = l[0];
                 aborted = !meet() || !ok;
-                const bool whole = (ti.what & kWhole) != 0;  // the row's only segment
-                const int64_t slot = (int64_t)blockIdx.x * 2 + ((ti.what & kStarts) ? 1 : 0);
+                const bool whole = (about & kWhole) != 0;  // the row's only segment
+                const int64_t slot = (int64_t)blockIdx.x * 2 + ((about & kStarts) ? 1 : 0);
                 if (quad == 0 && lane < kHW) {
                     const int r = hb + lane;
                     const float l = (red[r] + red[kNH + r]) + (red[2 * kNH + r] + red[3 * kNH + r]);
@@ -1118,8 +1130,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 tc_fence_before();
             }
             // (the next segment writes what this one's threads have read; all warps leave together)
-            aborted = soft_any(aborted);
+            going = !soft_any(aborted) && going;
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");  // (of a segment that was given up)
     }
     __syncwarp();
     tc_fence_before();

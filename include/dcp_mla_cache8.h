@@ -153,7 +153,7 @@ int dcp_mla_cache8_read(const void* const* kv_ptrs, const float* const* scale_pt
  *            0 <= T < 2^31, window and sinks >= 0
  * Numerics. The codes go to the tensor cores as they are. q is split into two
  * e4m3 parts at a power-of-two scale per head, which holds every value above
- * 2^-10 of the head's largest exactly (and the others to 2^-19 of it).
+ * 2^-9 of the head's largest exactly (and the others to 2^-16 of it).
  * Probabilities are split the same way at a power-of-two scale for each head and
  * 32 tokens, to 2^-8 relative like bf16. Products accumulate in fp32; output
  * rounded once to bf16. A NaN code that is visible, or a NaN or infinity in q,

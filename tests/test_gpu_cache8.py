@@ -7,7 +7,9 @@ Tolerances, derived:
   can move a value across a rounding boundary: within half a step of the code plus that.
 * attention: a probability keeps 2^-8 of itself (two e4m3 parts: half a step of 2^-4 of half a step of 2^-4) and what
   lies below 2^-18 of its 32-token block's largest; the output half a step of bf16. Scores are fp32 sums of exact
-  products: 2^-21 of the sum of their magnitudes; a q element below 2^-10 of its head's largest is held to 2^-19 of it.
+  products: 2^-21 of the sum of their magnitudes. q's head is scaled so that its largest lies in (224, 448]; a bf16 is two
+  e4m3 numbers exactly if its last bit is at least e4m3's smallest step, 2^-9: from 2^-2 up, which is 2^-2 / 224 < 2^-9 of
+  the largest. Below that each of the two parts errs by at most half that step: 2 * 2^-10 / 224 < 2^-16 of the largest.
 """
 import math
 
@@ -369,9 +371,9 @@ def check_decode(q, kv, sc, lens, scale, cp, il, block, window, sinks, out, lse,
         # what the split may lose: 2^-18 of the largest p u of 32 tokens, at most 32 of them for each maximum
         lost = 2.0 ** -18 * 32 * (p * u).sum(1, keepdim=True) * codes[:, :512].abs().amax()
         top = qb.abs().amax(1, keepdim=True)
-        small = qb.abs() < 2.0 ** -10 * top
+        small = qb.abs() < 2.0 ** -9 * top
         ds = abs(scale) * (2.0 ** -21 * (qb.abs() @ k.abs().T) +
-                           2.0 ** -19 * top * (small.double() @ k.abs().T)).amax(1, keepdim=True) + \
+                           2.0 ** -16 * top * (small.double() @ k.abs().T)).amax(1, keepdim=True) + \
             2.0 ** -22 * (s.abs().amax(1, keepdim=True) + 1)
         err = (out[b].double() - want).abs()
         tol = 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2 * ds + 2.0 ** -18) * mass + lost
