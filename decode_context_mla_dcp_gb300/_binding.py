@@ -118,7 +118,7 @@ def load(path: str | None = None):
         lib.dcp_mla_cache8_decode.argtypes = [vp, i64, i64, pv, pv, vp, ci, i64, ci, ci, ci, i64, ci, ci, i64, i64, cf,
                                               ci, vp, i64, vp, vp, vp, ctypes.c_uint, vp]
         lib.dcp_mla_cache8_decode.restype = ci
-        lib.dcp_mla_cache8_decode_workspace_bytes.argtypes = [i64, ci, ci]
+        lib.dcp_mla_cache8_decode_workspace_bytes.argtypes = [ci, i64, ci, i64, i64, i64, ci]
         lib.dcp_mla_cache8_decode_workspace_bytes.restype = i64
         lib.dcp_mla_cache8_strerror.argtypes = [ci]
         lib.dcp_mla_cache8_strerror.restype = ctypes.c_char_p
@@ -296,8 +296,11 @@ def dcp_mla_cache8_decode(q, q_row: int, q_head: int, kv_ptrs, scale_ptrs, seq_l
                                          _ptr(out), _ptr(lse), _ptr(status), int(flags), _stream(stream)))
 
 
-def dcp_mla_cache8_decode_workspace_bytes(B: int, H: int, num_sms: int) -> int:
-    return int(load().dcp_mla_cache8_decode_workspace_bytes(int(B), int(H), int(num_sms)))
+def dcp_mla_cache8_decode_workspace_bytes(cp: int, B: int, H: int, T: int, window: int, sinks: int,
+                                          num_sms: int) -> int:
+    """Bytes of workspace a decode of these sizes needs, 0 for none (host only)."""
+    return int(load().dcp_mla_cache8_decode_workspace_bytes(int(cp), int(B), int(H), int(T), int(window), int(sinks),
+                                                            int(num_sms)))
 
 
 def dcp_mla_cache8_strerror(status: int) -> str:

@@ -24,63 +24,64 @@ import math
 
 from . import _binding as _b
 
-_DTYPES = None  # torch dtype -> library dtype, filled on first use (torch is imported late)
+_torch = None
+_DTYPES: dict = {}  # torch dtype -> library dtype
 _SMS: dict = {}
 
 
-def _types():
-    global _DTYPES
-    if _DTYPES is None:
+def _ready():
+    """The library and torch (imported on first use)."""
+    global _torch
+    if _torch is None:
         import torch
-        _DTYPES = {torch.bfloat16: _b.DCP_DTYPE_BF16, torch.float16: _b.DCP_DTYPE_F16,
-                   torch.float32: _b.DCP_DTYPE_F32}
-    return _DTYPES
+        _DTYPES.update({torch.bfloat16: _b.DCP_DTYPE_BF16, torch.float16: _b.DCP_DTYPE_F16,
+                        torch.float32: _b.DCP_DTYPE_F32})
+        _torch = torch
+    return _b._lib or _b.load(), _torch
 
 
 def _on(device, stream):
     """(raw stream, context): the stream to launch on, and what to be inside of
-    while allocating and launching (None where that is the present state)."""
-    import torch
+    while allocating and launching (None where that is the present state, which
+    the small calls' host time is mostly made of)."""
     if device.type != "cuda":
         raise ValueError("the tensors must be CUDA tensors")
-    here = torch.cuda.current_device() == device.index
+    cuda, index = _torch.cuda, device.index
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(device.index)
-        return raw, (None if here else torch.cuda.device(device))
+        # (the raw handle: building a torch.cuda.Stream for it costs as much as a launch)
+        return _torch._C._cuda_getCurrentRawStream(index), \
+            None if cuda.current_device() == index else cuda.device(device)
     if isinstance(stream, int):
         raw = stream
-        stream = torch.cuda.default_stream(device) if raw == 0 else torch.cuda.ExternalStream(raw, device=device)
+        stream = cuda.default_stream(device) if raw == 0 else cuda.ExternalStream(raw, device=device)
     else:
         raw = int(stream.cuda_stream)
         if stream.device != device:
             raise ValueError("the stream is on another device than the tensors")
     both = contextlib.ExitStack()
-    both.enter_context(torch.cuda.device(device))
-    both.enter_context(torch.cuda.stream(stream))
+    both.enter_context(cuda.device(device))
+    both.enter_context(cuda.stream(stream))
     return raw, both
 
 
 def _sms(device) -> int:
     n = _SMS.get(device.index)
     if n is None:
-        import torch
-        n = _SMS[device.index] = int(torch.cuda.get_device_properties(device).multi_processor_count)
+        n = _SMS[device.index] = int(_torch.cuda.get_device_properties(device).multi_processor_count)
     return n
 
 
 def _ints(name, t, n, device):
-    """A contiguous int32 tensor of n entries (or None)."""
-    import torch
+    """The address of a contiguous int32 tensor of n entries (None for None)."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or t.device != device:
+    if t.dtype != _torch.int32 or t.dim() != 1 or len(t) != n or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on the caches' device")
     return t.data_ptr()
 
 
 def _shards(caches, scales, block):
     """Check the shards' tensors; (device, B, T, Dk, cache pointers, scale pointers)."""
-    import torch
     cp = len(caches)
     if cp < 1 or cp > _b.DCP_MLA_CACHE8_CP_MAX or len(scales) != cp:
         raise ValueError(f"need 1 to {_b.DCP_MLA_CACHE8_CP_MAX} caches (None for a shard that is not held) and as "
@@ -89,6 +90,7 @@ def _shards(caches, scales, block):
         raise ValueError(f"block must be a power of two, at most {_b.DCP_MLA_CACHE8_BLOCK_MAX}")
     device = shape = None
     kv, sc = (ctypes.c_void_p * cp)(), (ctypes.c_void_p * cp)()
+    e4m3, codes, f32 = _torch.float8_e4m3fn, _torch.uint8, _torch.float32
     for j in range(cp):
         c, s = caches[j], scales[j]
         if c is None or s is None:
@@ -100,7 +102,7 @@ def _shards(caches, scales, block):
             if len(shape) != 3 or shape[2] not in (512, 576):
                 raise ValueError("a cache must be [B, T, 512] or [B, T, 576]")
             sshape = (shape[0], -(-shape[1] // block))
-        if c.dtype not in (torch.float8_e4m3fn, torch.uint8) or s.dtype != torch.float32:
+        if (c.dtype != e4m3 and c.dtype != codes) or s.dtype != f32:
             raise TypeError("caches must be float8_e4m3fn (or uint8 codes) and scales float32")
         if c.shape != shape or s.shape != sshape or c.device != device or s.device != device:
             raise ValueError("shards must have one shape and device, and scales [B, ceil(T / block)]")
@@ -109,7 +111,8 @@ def _shards(caches, scales, block):
         kv[j], sc[j] = c.data_ptr(), s.data_ptr()
     if shape is None:
         raise ValueError("no shard is held here")
-    return device, shape[0], shape[1], shape[2], kv, sc
+    B, T, dk = shape
+    return device, B, T, dk, kv, sc
 
 
 def mla_rope_inv_freq(rot: int = 64, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
@@ -155,36 +158,46 @@ def mla_rope(x, positions, inv_freq, *, start: int = 0, interleaved: bool = True
     [N, H, D]; x itself rotates in place; another tensor or view (unit stride
     along D, not overlapping x) also receives the dims that are not rotated.
     Returns out."""
-    import torch
+    lib, torch = _ready()
     if x.dim() != 3:
         raise ValueError("x must be [N, H, D]")
     n, h, d = x.shape
-    dtype = _types().get(x.dtype)
+    row, head, unit = x.stride()
+    dtype = _DTYPES.get(x.dtype)
     if dtype is None:
         raise TypeError("x must be bf16, fp16 or fp32")
     device = x.device
-    if x.stride(2) != 1 and d > 1:
+    if unit != 1 and d > 1:
         raise ValueError("x needs unit stride along D")
     if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous() or \
             inv_freq.device != device:
         raise ValueError("inv_freq must be a contiguous float64 tensor on x's device")
-    if positions.dtype not in (torch.int64, torch.int32) or positions.shape != (n,) or \
-            not positions.is_contiguous() or positions.device != device:
+    wide = positions.dtype == torch.int64
+    if not (wide or positions.dtype == torch.int32) or positions.dim() != 1 or len(positions) != n or \
+            positions.device != device or not positions.is_contiguous():
         raise ValueError("positions must be a contiguous int32 or int64 tensor [N] on x's device")
     raw, inside = _on(device, stream)
-    with inside or contextlib.nullcontext():
-        if out is None:
-            out = torch.empty((n, h, d), dtype=x.dtype, device=device)
-        elif out is not x:
-            if out.shape != x.shape or out.dtype != x.dtype or out.device != device or (out.stride(2) != 1 and d > 1):
-                raise ValueError("out must have x's shape, dtype and device, and unit stride along D")
-            gap = abs(out.data_ptr() - x.data_ptr()) // x.element_size()
-            if 0 < gap < d and n * h > 0 and x.untyped_storage().data_ptr() == out.untyped_storage().data_ptr():
-                raise ValueError("out overlaps x: pass x itself to rotate in place")
-        _b._check8(_b.load().dcp_mla_rope(x.data_ptr(), x.stride(0), x.stride(1), positions.data_ptr(),
-                                      positions.dtype == torch.int64, inv_freq.data_ptr(), n, h, d, start,
-                                      2 * inv_freq.shape[0], interleaved, mscale, dtype, out.data_ptr(),
-                                      out.stride(0), out.stride(1), raw))
+    if inside is not None:
+        with inside:
+            return mla_rope(x, positions, inv_freq, start=start, interleaved=interleaved, mscale=mscale, out=out)
+    src = x.data_ptr()
+    if out is None:
+        out = torch.empty((n, h, d), dtype=x.dtype, device=device)
+        dst, orow, ohead = out.data_ptr(), h * d, d
+    elif out is x:
+        dst, orow, ohead = src, row, head
+    else:
+        orow, ohead, unit = out.stride() if out.dim() == 3 else (0, 0, 0)
+        if out.shape != x.shape or out.dtype != x.dtype or out.device != device or (unit != 1 and d > 1):
+            raise ValueError("out must have x's shape, dtype and device, and unit stride along D")
+        dst = out.data_ptr()
+        gap = abs(dst - src) // x.element_size()
+        if 0 < gap < d and n * h > 0 and x.untyped_storage().data_ptr() == out.untyped_storage().data_ptr():
+            raise ValueError("out overlaps x: pass x itself to rotate in place")
+    rc = lib.dcp_mla_rope(src, row, head, positions.data_ptr(), wide, inv_freq.data_ptr(), n, h, d, start,
+                          2 * len(inv_freq), interleaved, mscale, dtype, dst, orow, ohead, raw)
+    if rc:
+        _b._check8(rc)
     return out
 
 
@@ -199,12 +212,12 @@ def mla_cache8_append(latent, k_rope, caches, scales, seq_lens, *, cu_new=None, 
     inv_freq (float64 [32]) k_rope is rotated on the way. A block's scale is the
     smallest power of two that holds its values; a block that already holds
     tokens is requantised where its scale grows."""
-    import torch
+    lib, torch = _ready()
     device, B, T, dk, kv, sc = _shards(caches, scales, block)
-    dtype = _types().get(latent.dtype)
+    dtype = _DTYPES.get(latent.dtype)
     if dtype is None or dtype == _b.DCP_DTYPE_F32:
         raise TypeError("latent must be bf16 or fp16")
-    n = latent.shape[0]
+    n = len(latent)
     if latent.dim() != 2 or latent.shape[1] != 512 or latent.stride(1) != 1 or latent.device != device:
         raise ValueError("latent must be [N, 512] with unit inner stride, on the caches' device")
     rope_ptr, rope_row = None, 0
@@ -227,9 +240,11 @@ def mla_cache8_append(latent, k_rope, caches, scales, seq_lens, *, cu_new=None, 
     cu = _ints("cu_new", cu_new, B + 1, device)
     raw, inside = _on(device, stream)
     with inside or contextlib.nullcontext():
-        _b._check8(_b.load().dcp_mla_cache8_append(latent.data_ptr(), latent.stride(0), rope_ptr, rope_row, dtype, n, B,
-                                               dk, cu, lens, kv, sc, len(caches), T, block, interleave, freq_ptr,
-                                               interleaved, mscale, raw))
+        rc = lib.dcp_mla_cache8_append(latent.data_ptr(), latent.stride(0), rope_ptr, rope_row, dtype, n, B, dk, cu,
+                                       lens, kv, sc, len(caches), T, block, interleave, freq_ptr, interleaved, mscale,
+                                       raw)
+    if rc:
+        _b._check8(rc)
 
 
 def mla_cache8_read(caches, scales, total: int, *, starts=None, cu=None, block: int = 1, interleave: int = 1,
@@ -241,23 +256,27 @@ def mla_cache8_read(caches, scales, total: int, *, starts=None, cu=None, block: 
     [total, Dk]; or a tensor of that shape, unit inner stride, rows and base on
     16-byte boundaries. Tokens that no held shard has are left as they were.
     Returns out."""
-    import torch
+    lib, torch = _ready()
     device, B, T, dk, kv, sc = _shards(caches, scales, block)
     if total < 0:
         raise ValueError("total must not be negative")
     dtype = (torch.bfloat16 if out is None else out.dtype) if dtype is None else dtype
-    code = _types().get(dtype)
+    code = _DTYPES.get(dtype)
     if code is None:
         raise TypeError("dtype must be bf16, fp16 or fp32")
     start_ptr, cu_ptr = _ints("starts", starts, B, device), _ints("cu", cu, B + 1, device)
     raw, inside = _on(device, stream)
     with inside or contextlib.nullcontext():
         if out is None:
-            out = torch.empty((total, dk), dtype=dtype, device=device)
+            out, row = torch.empty((total, dk), dtype=dtype, device=device), dk
         elif out.shape != (total, dk) or out.dtype != dtype or out.device != device or out.stride(1) != 1:
             raise ValueError("out must be [total, Dk] of dtype with unit inner stride, on the caches' device")
-        _b._check8(_b.load().dcp_mla_cache8_read(kv, sc, len(caches), B, T, dk, block, interleave, start_ptr, cu_ptr,
-                                             total, out.data_ptr(), out.stride(0), code, raw))
+        else:
+            row = out.stride(0)
+        rc = lib.dcp_mla_cache8_read(kv, sc, len(caches), B, T, dk, block, interleave, start_ptr, cu_ptr, total,
+                                     out.data_ptr(), row, code, raw)
+    if rc:
+        _b._check8(rc)
     return out
 
 
@@ -272,18 +291,21 @@ def mla_cache8_decode(q, caches, scales, seq_lens, scale: float, *, block: int =
     bf16 [B, H, 512] and fp32 [B, H] (base e, or 2); heads [r H/cp, (r + 1) H/cp)
     of out are what destination r of mla_decode_dcp receives. With some shards
     None the result is the partial over the held ones, for ``merge``. workspace: a
-    uint8 CUDA tensor of dcp_mla_cache8_decode_workspace_bytes, allocated when not
-    given. status: None, or an int32 CUDA tensor (see the C header)."""
-    import torch
+    contiguous CUDA tensor of at least dcp_mla_cache8_decode_workspace_bytes bytes,
+    256-byte aligned, allocated when not given and needed. status: None, or an
+    int32 CUDA tensor (see the C header)."""
+    lib, torch = _ready()
     device, B, T, dk, kv, sc = _shards(caches, scales, block)
-    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != dk or q.dtype != torch.bfloat16 or q.stride(2) != 1 or \
-            q.device != device:
+    if q.dim() != 3 or q.dtype != torch.bfloat16 or q.device != device:
         raise ValueError("q must be bf16 [B, H, Dk] with unit inner stride, on the caches' device")
-    H = q.shape[1]
+    qb, H, qd = q.shape
+    row, head, unit = q.stride()
+    if qb != B or qd != dk or unit != 1:
+        raise ValueError("q must be bf16 [B, H, Dk] with unit inner stride, on the caches' device")
     lens = _ints("seq_lens", seq_lens, B, device)
     if lens is None:
         raise ValueError("seq_lens is required")
-    lib = _b.load()
+    cp = len(caches)
     raw, inside = _on(device, stream)
     with inside or contextlib.nullcontext():
         if out is None:
@@ -296,15 +318,19 @@ def mla_cache8_decode(q, caches, scales, seq_lens, scale: float, *, block: int =
         elif lse.shape != (B, H) or lse.dtype != torch.float32 or lse.device != device or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous fp32 tensor [B, H] on the caches' device")
         if workspace is None:
-            need = lib.dcp_mla_cache8_decode_workspace_bytes(B, H, _sms(device))
-            workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=device)
+            size = lib.dcp_mla_cache8_decode_workspace_bytes(cp, B, H, T, window, sinks, _sms(device))
+            if size > 0:
+                workspace = torch.empty((size,), dtype=torch.uint8, device=device)
         elif workspace.device != device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the caches' device")
+        else:
+            size = workspace.numel() * workspace.element_size()
         if status is not None and (status.dtype != torch.int32 or status.device != device or status.numel() < 1):
             raise ValueError("status must be an int32 tensor on the caches' device")
-        _b._check8(lib.dcp_mla_cache8_decode(q.data_ptr(), q.stride(0), q.stride(1), kv, sc, lens, len(caches), B, H, dk,
-                                         512, T, block, interleave, window, sinks, scale, lse_base_e,
-                                         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                         out.data_ptr(), lse.data_ptr(),
-                                         None if status is None else status.data_ptr(), flags, raw))
+        rc = lib.dcp_mla_cache8_decode(q.data_ptr(), row, head, kv, sc, lens, cp, B, H, dk, 512, T, block, interleave,
+                                       window, sinks, scale, lse_base_e,
+                                       None if workspace is None else workspace.data_ptr(), size, out.data_ptr(),
+                                       lse.data_ptr(), None if status is None else status.data_ptr(), flags, raw)
+    if rc:
+        _b._check8(rc)
     return out, lse

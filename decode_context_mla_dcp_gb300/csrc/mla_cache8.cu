@@ -28,11 +28,22 @@ constexpr int64_t kMaxInterleave = 1 << 24;
 // ---- element types -------------------------------------------------------------
 
 struct Bf16 {
+    // the larger magnitudes of two pairs; NaN loses to a number
+    __device__ static uint32_t top2(uint32_t a, uint32_t b) {
+        const __nv_bfloat162 m = __hmax2(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&a)),
+                                         __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    }
     using T = uint16_t;
     __device__ static float get(T v) { return __uint_as_float((uint32_t)v << 16); }
     __device__ static T put(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 };
 struct F16 {
+    __device__ static uint32_t top2(uint32_t a, uint32_t b) {
+        const __half2 m = __hmax2(__habs2(*reinterpret_cast<const __half2*>(&a)),
+                                  __habs2(*reinterpret_cast<const __half2*>(&b)));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    }
     using T = uint16_t;
     __device__ static float get(T v) { return __half2float(__ushort_as_half(v)); }
     __device__ static T put(float x) { return __half_as_ushort(__float2half_rn(x)); }
@@ -81,78 +92,131 @@ struct RopeParams {
     int tokens;              // tokens of a CTA
     int heads;               // heads of a CTA
     int rot_units, units;    // work units of a head: rotating ones first, then copied ones
-    uint32_t units_magic;    // ceil(2^32 / units): idx / units for idx * units < 2^32
-    uint32_t heads_magic;
     int copy_lead;           // copied units before the rotated dims
 };
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeAngles = 2048;  // cos/sin pairs a CTA holds
+constexpr int kRopeBatch = 4;      // 16-byte vectors a thread has in flight
 
-// One CTA: `tokens` tokens x `heads` heads. Their angles (64-bit multiply,
-// sincos) are computed once into shared memory and used by every head; a unit is
-// then kV elements (16 bytes): kV/2 interleaved pairs, or kV pairs of the two
-// halves, or kV copied elements. kV = 1 is the form for sizes or strides that are
-// not multiples of 16 bytes: a unit is one pair or one copied element.
-template <class E, int kV>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+// A unit is kV elements (16 bytes) of a head, or with halves two of them (kV
+// pairs); kV = 1 is the form for sizes or strides that are not multiples of 16
+// bytes: a unit is one pair or one copied element.
+template <class E, int kV, bool kInter>
+struct RopeUnit {
     using T = typename E::T;
-    __shared__ float2 cs[kRopeAngles];
+    static constexpr int kE = kInter && kV == 1 ? 2 : kV;  // elements of a vector
+    static constexpr int kA = kInter ? kE / 2 : kE;        // angles
+    struct alignas(kV * sizeof(T)) Vec { T e[kE]; };
+    Vec v, w;
+    __device__ __forceinline__ void load(const T* src, int half, bool turn) {
+        if (kE == kV) {
+            v = *reinterpret_cast<const Vec*>(src);
+        } else {
+            v.e[0] = src[0];
+            if (turn) v.e[kE - 1] = src[1];
+        }
+        if (!kInter && turn) w = *reinterpret_cast<const Vec*>(src + half);
+    }
+    __device__ __forceinline__ void turn_by(const float2* a) {
+#pragma unroll
+        for (int j = 0; j < kA; ++j) {
+            T& p = v.e[kInter ? 2 * j : j];
+            T& q = kInter ? v.e[kInter ? 2 * j + 1 : 0] : w.e[j];
+            const float f = E::get(p), g = E::get(q);
+            p = E::put(f * a[j].x - g * a[j].y);
+            q = E::put(g * a[j].x + f * a[j].y);
+        }
+    }
+    __device__ __forceinline__ void store(T* dst, int half, bool turn) const {
+        if (kE == kV) {
+            *reinterpret_cast<Vec*>(dst) = v;
+        } else {
+            dst[0] = v.e[0];
+            if (turn) dst[1] = v.e[kE - 1];
+        }
+        if (!kInter && turn) *reinterpret_cast<Vec*>(dst + half) = w;
+    }
+};
+
+// One CTA: `tokens` tokens x `heads` heads, the rows. A thread keeps one unit of
+// the row and walks the rows in steps of `slots` (the rows that the CTA's threads
+// cover side by side), so that its place in the row, its kind, its step and (with
+// one token a CTA, !kMany) its angles are found once. It loads its first rows,
+// then the CTA computes its tokens' angles (64-bit multiply, sincos) once into
+// shared memory, then the rows are turned and stored: the angles cost their
+// latency beside the loads'.
+template <class E, int kV, bool kInter, bool kMany>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+    using Unit = RopeUnit<E, kV, kInter>;
+    using T = typename E::T;
+    constexpr int kB = kInter ? kRopeBatch : kRopeBatch / 2;
+    __shared__ alignas(16) float2 cs[kRopeAngles];
     const int64_t n0 = (int64_t)blockIdx.x * p.tokens;
-    const int ntok = (int)(p.N - n0 < p.tokens ? p.N - n0 : p.tokens);
+    const int ntok = kMany ? (int)(p.N - n0 < p.tokens ? p.N - n0 : p.tokens) : 1;
     const int h0 = blockIdx.y * p.heads;
     const int nh = p.H - h0 < p.heads ? p.H - h0 : p.heads;
-    for (int i = threadIdx.x; i < ntok * p.half; i += kRopeThreads) {
-        const int t = i / p.half, f = i - t * p.half;
-        const int64_t pos = p.pos64 ? static_cast<const int64_t*>(p.positions)[n0 + t]
-                                    : (int64_t) static_cast<const int32_t*>(p.positions)[n0 + t];
-        float c, s;
-        angle_of(pos, turns_of(p.inv_freq[f]), &c, &s);
-        cs[i] = make_float2(c * p.mscale, s * p.mscale);
-    }
-    __syncthreads();
-    const int total = ntok * nh * p.units;
-    struct alignas(kV * sizeof(T)) Vec { T e[kV]; };
-    const T* const x = static_cast<const T*>(p.x);
-    T* const out = static_cast<T*>(p.out);
-#pragma unroll 2
-    for (int i = threadIdx.x; i < total; i += kRopeThreads) {
-        const int th = p.units == 1 ? i : (int)__umulhi((uint32_t)i, p.units_magic);
-        const int u = i - th * p.units;
-        const int t = nh == 1 ? th : (int)__umulhi((uint32_t)th, p.heads_magic), h = th - t * nh;
-        const T* const xr = x + (n0 + t) * p.x_row + (h0 + h) * p.x_head;
-        T* const orow = out + (n0 + t) * p.out_row + (h0 + h) * p.out_head;
-        const float2* const a = cs + t * p.half;
-        if (u >= p.rot_units) {  // a copied unit, before or behind the rotated dims
-            const int c = u - p.rot_units;
-            const int d = c < p.copy_lead ? c * kV : p.start + 2 * p.half + (c - p.copy_lead) * kV;
-            *reinterpret_cast<Vec*>(orow + d) = *reinterpret_cast<const Vec*>(xr + d);
-        } else if (p.interleaved) {
-            constexpr int kP = kV > 1 ? kV / 2 : 1;  // pairs of the unit
-            struct alignas(kV > 1 ? sizeof(T) * kV : sizeof(T)) Pairs { T e[2 * kP]; };
-            const int d = p.start + u * 2 * kP;
-            Pairs v = *reinterpret_cast<const Pairs*>(xr + d), w;
+    const int rows = ntok * nh;
+    const bool narrow = p.units < kRopeThreads;
+    const int slots = narrow ? kRopeThreads / p.units : 1;
+    const int slot = narrow ? (int)threadIdx.x / p.units : 0;
+    const int64_t x_step = slots * p.x_head, out_step = slots * p.out_head;
+    bool angles = false;
+    for (int u = (int)threadIdx.x - slot * p.units;; u += kRopeThreads) {
+        const bool turn = u < p.rot_units;
+        const int c = u - p.rot_units;  // a copied unit lies before or behind the rotated dims
+        const int d = turn ? p.start + u * Unit::kE
+                           : (c < p.copy_lead ? c * kV : p.start + 2 * p.half + (c - p.copy_lead) * kV);
+        const T* src = static_cast<const T*>(p.x) + (n0 * p.x_row + (h0 + slot) * p.x_head + d);
+        T* dst = static_cast<T*>(p.out) + (n0 * p.out_row + (h0 + slot) * p.out_head + d);
+        const float2* at = cs + u * Unit::kA;
+        int r = slot < slots && u < p.units ? slot : rows, h = slot, ht = slot;
+        float2 mine[Unit::kA];
+        do {
+            Unit v[kB];
 #pragma unroll
-            for (int k = 0; k < kP; ++k) {
-                const float2 r = a[u * kP + k];
-                const float f = E::get(v.e[2 * k]), g = E::get(v.e[2 * k + 1]);
-                w.e[2 * k] = E::put(f * r.x - g * r.y);
-                w.e[2 * k + 1] = E::put(g * r.x + f * r.y);
+            for (int k = 0; k < kB; ++k) {
+                if (r + k * slots < rows) {
+                    if (kMany)
+                        for (; h >= nh; h -= nh) src += p.x_row - nh * p.x_head;  // on to the next token
+                    v[k].load(src, p.half, turn);
+                    src += x_step;
+                    h += slots;
+                }
             }
-            *reinterpret_cast<Pairs*>(orow + d) = w;
-        } else {
-            const int d = p.start + u * kV;
-            Vec v0 = *reinterpret_cast<const Vec*>(xr + d), v1 = *reinterpret_cast<const Vec*>(xr + d + p.half);
+            if (!angles) {
+                for (int i = threadIdx.x; i < ntok * p.half; i += kRopeThreads) {
+                    const int tok = kMany ? i / p.half : 0, f = i - tok * p.half;
+                    const int64_t pos = p.pos64 ? static_cast<const int64_t*>(p.positions)[n0 + tok]
+                                                : (int64_t) static_cast<const int32_t*>(p.positions)[n0 + tok];
+                    float co, si;
+                    angle_of(pos, turns_of(p.inv_freq[f]), &co, &si);
+                    cs[i] = make_float2(co * p.mscale, si * p.mscale);
+                }
+                __syncthreads();  // (every thread comes here once, with its first rows)
+                angles = true;
+            }
+            if (!kMany && turn) {
 #pragma unroll
-            for (int k = 0; k < kV; ++k) {
-                const float2 r = a[u * kV + k];
-                const float f = E::get(v0.e[k]), g = E::get(v1.e[k]);
-                v0.e[k] = E::put(f * r.x - g * r.y);
-                v1.e[k] = E::put(g * r.x + f * r.y);
+                for (int j = 0; j < Unit::kA; ++j) mine[j] = at[j];
             }
-            *reinterpret_cast<Vec*>(orow + d) = v0;
-            *reinterpret_cast<Vec*>(orow + d + p.half) = v1;
-        }
+#pragma unroll
+            for (int k = 0; k < kB; ++k) {
+                if (r + k * slots < rows) {
+                    if (kMany)
+                        for (; ht >= nh; ht -= nh) {
+                            dst += p.out_row - nh * p.out_head;
+                            at += p.half;
+                        }
+                    if (turn) v[k].turn_by(kMany ? at : mine);
+                    v[k].store(dst, p.half, turn);
+                    dst += out_step;
+                    ht += slots;
+                }
+            }
+            r += kB * slots;
+        } while (r < rows);
+        if (narrow || u + kRopeThreads >= p.units) break;
     }
 }
 
@@ -193,10 +257,12 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)
 __device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 // |x| of a finite x, 0 of a NaN or an infinity
 __device__ __forceinline__ float mag(float x) { return finite(x) ? fabsf(x) : 0.f; }
-// Two e4m3 codes (first in the low byte), round to nearest even; NaN where x is not finite.
+// Two e4m3 codes (first in the low byte), round to nearest even. kOdd: NaN for an infinity too (the conversion gives
+// the largest number).
+template <bool kOdd>
 __device__ __forceinline__ uint32_t codes2(float x, float y, float inv) {
-    const float a = finite(x) ? x * inv : __uint_as_float(0x7fffffffu);
-    const float b = finite(y) ? y * inv : __uint_as_float(0x7fffffffu);
+    const float a = !kOdd || finite(x) ? x * inv : __uint_as_float(0x7fffffffu);
+    const float b = !kOdd || finite(y) ? y * inv : __uint_as_float(0x7fffffffu);
     return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 __device__ __forceinline__ float2 values2(uint32_t codes) {
@@ -262,32 +328,42 @@ __device__ __forceinline__ void turn_token(const AppendParams& p, uint32_t rope,
     }
 }
 
+// The largest finite magnitude of a token. `odd`: it has NaNs or infinities, found
+// out cheaply (a maximum that is no finite number, or a NaN among the rotated),
+// and its values are then looked at one by one.
 template <class E>
-__device__ __forceinline__ float token_peak(const Token& t) {
-    float a = fmaxf(mag(t.r0), mag(t.r1));
+__device__ __forceinline__ float token_peak(const Token& t, bool* odd) {
+    const uint32_t w[8] = {t.v[0].x, t.v[0].y, t.v[0].z, t.v[0].w, t.v[1].x, t.v[1].y, t.v[1].z, t.v[1].w};
+    uint32_t m = E::top2(w[0], w[1]);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const uint32_t w[4] = {t.v[k].x, t.v[k].y, t.v[k].z, t.v[k].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a = fmaxf(a, fmaxf(mag(get_lo<E>(w[i])), mag(get_hi<E>(w[i]))));
+    for (int i = 2; i < 8; ++i) m = E::top2(m, w[i]);
+    float a = fmaxf(fmaxf(get_lo<E>(m), get_hi<E>(m)), fmaxf(fabsf(t.r0), fabsf(t.r1)));
+    *odd = __any_sync(0xffffffffu, !finite(a) || !finite(t.r0) || !finite(t.r1));
+    if (*odd) {
+        a = fmaxf(mag(t.r0), mag(t.r1));
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+            const uint4 v = i < 4 ? t.v[0] : t.v[1];
+            const uint32_t x = (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
+            a = fmaxf(a, fmaxf(mag(get_lo<E>(x)), mag(get_hi<E>(x))));
+        }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    return a;
+    // (magnitudes: their bits order like integers)
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
 }
 
-template <class E>
-__device__ __forceinline__ void store_token(const AppendParams& p, const Token& t, uint8_t* dst, int lane, float inv) {
+template <class E, bool kOdd>
+__device__ __forceinline__ void store_codes(const AppendParams& p, const Token& t, uint8_t* dst, int lane, float inv) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const uint32_t w[4] = {t.v[k].x, t.v[k].y, t.v[k].z, t.v[k].w};
         uint32_t c[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = codes2(get_lo<E>(w[i]), get_hi<E>(w[i]), inv);
+        for (int i = 0; i < 4; ++i) c[i] = codes2<kOdd>(get_lo<E>(w[i]), get_hi<E>(w[i]), inv);
         *reinterpret_cast<uint2*>(dst + 256 * k + 8 * lane) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
     }
     if (p.Dk > kLatent) {
-        const uint32_t c = codes2(t.r0, t.r1, inv);
+        const uint32_t c = codes2<kOdd>(t.r0, t.r1, inv);
         if (p.interleaved) {
             *reinterpret_cast<uint16_t*>(dst + kLatent + 2 * lane) = (uint16_t)c;
         } else {
@@ -295,6 +371,12 @@ __device__ __forceinline__ void store_token(const AppendParams& p, const Token& 
             dst[kLatent + 32 + lane] = (uint8_t)(c >> 8);
         }
     }
+}
+template <class E>
+__device__ __forceinline__ void store_token(const AppendParams& p, const Token& t, bool odd, uint8_t* dst, int lane,
+                                            float inv) {
+    if (odd) store_codes<E, true>(p, t, dst, lane, inv);
+    else store_codes<E, false>(p, t, dst, lane, inv);
 }
 
 // Where packed token n goes. False: nowhere.
@@ -346,9 +428,10 @@ __global__ void __launch_bounds__(128) append_token_kernel(const __grid_constant
     uint8_t* const kv = p.kv[w.shard];
     if (kv == nullptr) return;
     turn_token<E>(p, rope, rotate, turns_of(f), (int64_t)w.pos, &t);
-    const int k = scale_exp(token_peak<E>(t));
+    bool odd;
+    const int k = scale_exp(token_peak<E>(t, &odd));
     const int64_t at = (int64_t)w.row * p.T + w.loc;
-    store_token<E>(p, t, kv + at * p.Dk, lane, pow2(-k));
+    store_token<E>(p, t, odd, kv + at * p.Dk, lane, pow2(-k));
     if (lane == 0) p.scales[w.shard][at] = pow2(k);
 }
 
@@ -356,94 +439,97 @@ __global__ void __launch_bounds__(128) append_token_kernel(const __grid_constant
 // for it; the CTA that looks at that token writes the whole block: the block's
 // new tokens in registers (kTok a warp, every load in flight at once), their
 // peak, the scale, the tokens that the block held before if the scale grows, and
-// the new codes. CTA c looks at tokens c, c + G, c + 2G, ... with G odd, so that
-// first tokens, which stand a power of two apart, spread over all CTAs.
-constexpr int kBlockWarps = 16;
+// the new codes. A CTA has as many warps as a block needs, so that small blocks
+// take small CTAs and all CTAs of a call are resident at once. CTA c looks at
+// tokens c, c + G, c + 2G, ... with G odd, so that first tokens, which stand a
+// power of two apart, spread over all CTAs.
+constexpr int kTok = 4;
 constexpr int kCuShared = 1024;
-constexpr int kAppendGrid = 1217;  // odd, about eight CTAs a multiprocessor
 
-template <class E, int kTok>
-__global__ void __launch_bounds__(32 * kBlockWarps) append_block_kernel(const __grid_constant__ AppendParams p) {
+template <class E, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) append_block_kernel(const __grid_constant__ AppendParams p) {
     __shared__ int32_t cu_s[kCuShared + 1];
-    __shared__ int32_t list[32 * kBlockWarps];
+    __shared__ Place list[32 * kWarps];
     __shared__ int found;
-    __shared__ float peak_s[kBlockWarps];
+    __shared__ float peak_s[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int32_t* cu = p.cu;
+    if (tid == 0) found = 0;
     if (cu != nullptr && p.B <= kCuShared) {
-        for (int i = tid; i <= p.B; i += 32 * kBlockWarps) cu_s[i] = cu[i];
+        for (int i = tid; i <= p.B; i += 32 * kWarps) cu_s[i] = cu[i];
         cu = cu_s;
     }
     const bool rotate = p.inv_freq != nullptr;
-    const uint64_t turns = rotate ? turns_of(p.inv_freq[lane]) : 0;
+    const double freq = rotate ? p.inv_freq[lane] : 0.0;
     const uint32_t block = 1u << p.block_log2;
-    for (int64_t base = blockIdx.x; base < p.N; base += (int64_t)gridDim.x * (32 * kBlockWarps)) {
-        __syncthreads();
-        if (tid == 0) found = 0;
+    for (int64_t base = blockIdx.x; base < p.N; base += (int64_t)gridDim.x * (32 * kWarps)) {
         __syncthreads();
         const int64_t n = base + (int64_t)tid * gridDim.x;
         Place w;
         if (n < p.N && place_of(p, cu, n, &w) && (int64_t)w.loc < p.T && p.kv[w.shard] != nullptr) {
             const uint32_t held = held_tokens(w.len, w.shard, p.cp, p.interleave);
-            if (w.loc == held || (w.loc & (block - 1)) == 0) list[atomicAdd(&found, 1)] = tid;
+            if (w.loc == held || (w.loc & (block - 1)) == 0) list[atomicAdd(&found, 1)] = w;
         }
         __syncthreads();
         const int nfound = found;
         for (int i = 0; i < nfound; ++i) {  // (in any order: blocks are independent of each other)
-            (void)place_of(p, cu, base + (int64_t)list[i] * gridDim.x, &w);
+            w = list[i];
             uint8_t* const kv = p.kv[w.shard] + (int64_t)w.row * p.T * p.Dk;
             float* const scale = p.scales[w.shard] + (int64_t)w.row * p.blocks + (w.loc >> p.block_log2);
             const uint32_t b0 = w.loc & ~(block - 1);
             uint32_t end = held_tokens(w.len + w.count, w.shard, p.cp, p.interleave);
             if (end > b0 + block) end = b0 + block;
             if ((int64_t)end > p.T) end = (uint32_t)p.T;
-            const float old = b0 < w.loc ? *scale : 0.f;  // the present scale counts where the block holds tokens
             Token t[kTok];
             uint32_t rope[kTok], pos[kTok];
 #pragma unroll
             for (int k = 0; k < kTok; ++k) {
-                const uint32_t loc = w.loc + warp + k * kBlockWarps;
+                const uint32_t loc = w.loc + warp + k * kWarps;
                 if (loc < end) {
                     pos[k] = p.cp == 1 ? loc
                                        : (loc / p.interleave * p.cp + w.shard) * p.interleave + loc % p.interleave;
                     load_token<E>(p, (int64_t)w.first + (pos[k] - w.len), lane, &t[k], &rope[k]);
                 }
             }
+            const float old = b0 < w.loc ? *scale : 0.f;  // the present scale counts where the block holds tokens
+            const uint64_t turns = turns_of(freq);
             float peak = 0.f;
+            bool odd[kTok];
 #pragma unroll
             for (int k = 0; k < kTok; ++k)
-                if (w.loc + warp + k * kBlockWarps < end) {
+                if (w.loc + warp + k * kWarps < end) {
                     turn_token<E>(p, rope[k], rotate, turns, (int64_t)pos[k], &t[k]);
-                    peak = fmaxf(peak, token_peak<E>(t[k]));
+                    peak = fmaxf(peak, token_peak<E>(t[k], &odd[k]));
                 }
             if (lane == 0) peak_s[warp] = peak;
             __syncthreads();
-            peak = 0.f;
+            peak = peak_s[lane & (kWarps - 1)];
 #pragma unroll
-            for (int k = 0; k < kBlockWarps; ++k) peak = fmaxf(peak, peak_s[k]);
+            for (int o = 16; o > 0; o >>= 1) peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, o));
             const int e = scale_exp(peak);
             float s = pow2(e);
             if (old > s) s = old;
             const float inv = 1.0f / s;
 #pragma unroll
             for (int k = 0; k < kTok; ++k) {
-                const uint32_t loc = w.loc + warp + k * kBlockWarps;
-                if (loc < end) store_token<E>(p, t[k], kv + (int64_t)loc * p.Dk, lane, inv);
+                const uint32_t loc = w.loc + warp + k * kWarps;
+                if (loc < end) store_token<E>(p, t[k], odd[k], kv + (int64_t)loc * p.Dk, lane, inv);
             }
             if (b0 < w.loc && s > old) {  // requantise what the block held
                 const float ratio = old / s;
-                for (uint32_t loc = b0 + warp; loc < w.loc; loc += kBlockWarps) {
+                for (uint32_t loc = b0 + warp; loc < w.loc; loc += kWarps) {
                     uint32_t* const row = reinterpret_cast<uint32_t*>(kv + (int64_t)loc * p.Dk);
                     for (int c = lane; c < p.Dk / 4; c += 32) {
                         const uint32_t u = row[c];
                         const float2 a = values2(u), b = values2(u >> 16);
-                        row[c] = codes2(a.x, a.y, ratio) | (codes2(b.x, b.y, ratio) << 16);
+                        row[c] = codes2<false>(a.x, a.y, ratio) | (codes2<false>(b.x, b.y, ratio) << 16);
                     }
                 }
             }
             if (tid == 0) *scale = s;
             __syncthreads();  // peak_s is used again
         }
+        if (tid == 0) found = 0;
     }
 }
 
@@ -462,15 +548,21 @@ struct ReadParams {
     int tokens;       // tokens of a CTA
 };
 
-constexpr int kReadThreads = 288;  // 72 x 4: with 8 codes a thread, four tokens of 576 a sweep
+constexpr int kReadThreads = 256;
 constexpr int kReadTokens = 32;
+
+__device__ __forceinline__ uint2 load_once(const uint8_t* src) {
+    uint2 v;
+    asm("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(src));
+    return v;
+}
 
 // A CTA finds its tokens' places once, then moves 8 codes a thread: 8-byte
 // loads, 16-byte stores of 16-bit values, both contiguous over the token.
 template <class E, int kDk>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadParams p) {
     using T = typename E::T;
-    constexpr int kUnits = kDk / 8;
+    constexpr int kUnits = kDk / 8;  // 8 codes: 72 or 64 a token, a whole number of sweeps for 32 tokens
     __shared__ const uint8_t* src_s[kReadTokens];
     __shared__ float scale_s[kReadTokens];
     const int64_t n0 = (int64_t)blockIdx.x * p.tokens;
@@ -510,18 +602,29 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
         scale_s[threadIdx.x] = s;
     }
     __syncthreads();
+    // eight loads of a thread in flight (a CTA's 32 tokens)
+    constexpr int kBatch = kReadTokens * kUnits / kReadThreads;
     const int total = ntok * kUnits;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < total; i += kReadThreads) {
-        const int t = i / kUnits, u = i - t * kUnits;
-        const uint8_t* const src = src_s[t];
-        if (src == nullptr) continue;
-        const uint2 c = __ldg(reinterpret_cast<const uint2*>(src) + u);
-        const float s = scale_s[t];
-        const float2 a = values2(c.x), b = values2(c.x >> 16), d = values2(c.y), e = values2(c.y >> 16);
-        struct alignas(16) Vec { T e[8]; } v = {{E::put(a.x * s), E::put(a.y * s), E::put(b.x * s), E::put(b.y * s),
-                                                 E::put(d.x * s), E::put(d.y * s), E::put(e.x * s), E::put(e.y * s)}};
-        *reinterpret_cast<Vec*>(p.out + (n0 + t) * p.out_row + (int64_t)u * sizeof(Vec)) = v;
+    uint2 c[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+        const int i = k * kReadThreads + (int)threadIdx.x, t = i / kUnits, u = i - t * kUnits;
+        c[k] = make_uint2(0u, 0u);
+        if (i < total && src_s[t] != nullptr) c[k] = load_once(src_s[t] + 8 * u);
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+        const int i = k * kReadThreads + (int)threadIdx.x, t = i / kUnits, u = i - t * kUnits;
+        if (i < total && src_s[t] != nullptr) {
+            const float s = scale_s[t];
+            const float2 a = values2(c[k].x), b = values2(c[k].x >> 16), d = values2(c[k].y), e = values2(c[k].y >> 16);
+            struct alignas(16) Vec { T e[8]; } v = {{E::put(a.x * s), E::put(a.y * s), E::put(b.x * s),
+                                                     E::put(b.y * s), E::put(d.x * s), E::put(d.y * s),
+                                                     E::put(e.x * s), E::put(e.y * s)}};
+            uint4* const to = reinterpret_cast<uint4*>(p.out + (n0 + t) * p.out_row + (int64_t)u * sizeof(Vec));
+#pragma unroll
+            for (int j = 0; j < (int)(sizeof(Vec) / 16); ++j) __stcs(to + j, reinterpret_cast<const uint4*>(&v)[j]);
+        }
     }
 }
 
@@ -563,27 +666,31 @@ int launch_rope(RopeParams& p, int D, int64_t esize, cudaStream_t st) {
     p.rot_units = p.interleaved ? (kv > 1 ? 2 * p.half / kv : p.half) : p.half / kv;
     p.copy_lead = p.copy ? p.start / kv : 0;
     p.units = p.rot_units + (p.copy ? (D - 2 * p.half) / kv : 0);
-    // Tokens and heads of a CTA: about 1024 units (4 a thread), fewer where the
-    // call is small, so that it still fills the GPU.
-    const int64_t all = p.N * p.H * p.units;
-    int64_t want = all / (152 * 8);
-    want = want < 256 ? 256 : (want > 1024 ? 1024 : want);
-    int64_t heads = want / p.units;
-    heads = heads < 1 ? 1 : (heads > p.H ? p.H : heads);
-    p.heads = (int)heads;
-    int64_t tokens = heads < p.H ? 1 : want / (heads * p.units);
+    // Tokens and heads of a CTA: at most about two batches of rows a thread, fewer where the call is small, so that it still
+    // spreads over the GPU. More than one token only with all their heads.
+    const int slots = p.units < kRopeThreads ? kRopeThreads / p.units : 1;
+    const int64_t batch = (int64_t)slots * (p.interleaved ? kRopeBatch : kRopeBatch / 2);
+    int64_t want = p.N * p.H / (152 * 4);  // rows
+    want = want < slots ? slots : (want > 2 * batch ? 2 * batch : want);
+    const int64_t parts = (p.H + want - 1) / want, heads = (p.H + parts - 1) / parts;
+    int64_t tokens = heads < p.H ? 1 : want / heads;
     if (tokens > kRopeAngles / p.half) tokens = kRopeAngles / p.half;
     tokens = tokens < 1 ? 1 : (tokens > p.N ? p.N : tokens);
+    p.heads = (int)heads;
     p.tokens = (int)tokens;
-    p.units_magic = p.units > 1 ? (uint32_t)(((uint64_t(1) << 32) + p.units - 1) / p.units) : 0;
     const int64_t gx = (p.N + tokens - 1) / tokens, gy = (p.H + heads - 1) / heads;
     if (gx > 0x7fffffff || gy > 65535) return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
-    // every CTA of a row of CTAs has `heads` heads but the last, which divides by its own count:
-    // with more than one head block a CTA has one token, so the quotient is always 0
-    p.heads_magic = p.heads > 1 ? (uint32_t)(((uint64_t(1) << 32) + p.heads - 1) / p.heads) : 0;
     const dim3 grid((unsigned)gx, (unsigned)gy);
-    if (kv > 1) rope_kernel<E, 16 / sizeof(typename E::T)><<<grid, kRopeThreads, 0, st>>>(p);
-    else rope_kernel<E, 1><<<grid, kRopeThreads, 0, st>>>(p);
+    constexpr int kWide = 16 / sizeof(typename E::T);
+    void (*kernel)(const RopeParams);
+    if (tokens > 1) {
+        if (p.interleaved) kernel = kv > 1 ? rope_kernel<E, kWide, true, true> : rope_kernel<E, 1, true, true>;
+        else kernel = kv > 1 ? rope_kernel<E, kWide, false, true> : rope_kernel<E, 1, false, true>;
+    } else {
+        if (p.interleaved) kernel = kv > 1 ? rope_kernel<E, kWide, true, false> : rope_kernel<E, 1, true, false>;
+        else kernel = kv > 1 ? rope_kernel<E, kWide, false, false> : rope_kernel<E, 1, false, false>;
+    }
+    kernel<<<grid, kRopeThreads, 0, st>>>(p);
     return launched();
 }
 
@@ -593,12 +700,12 @@ int launch_append(const AppendParams& p, int block, cudaStream_t st) {
         append_token_kernel<E><<<(unsigned)((p.N + 3) / 4), 128, 0, st>>>(p);
         return launched();
     }
-    const unsigned grid = (unsigned)(p.N < kAppendGrid ? p.N : kAppendGrid);
-    const int threads = 32 * kBlockWarps;
-    if (block <= 16) append_block_kernel<E, 1><<<grid, threads, 0, st>>>(p);
-    else if (block == 32) append_block_kernel<E, 2><<<grid, threads, 0, st>>>(p);
-    else if (block == 64) append_block_kernel<E, 4><<<grid, threads, 0, st>>>(p);
-    else append_block_kernel<E, 8><<<grid, threads, 0, st>>>(p);
+    // about as many CTAs as are resident at once (32 warps a multiprocessor), an odd number
+    const auto grid = [&](int64_t most) { return (unsigned)(p.N < most ? p.N : most); };
+    if (block <= 16) append_block_kernel<E, 4><<<grid(1217), 128, 0, st>>>(p);
+    else if (block == 32) append_block_kernel<E, 8><<<grid(609), 256, 0, st>>>(p);
+    else if (block == 64) append_block_kernel<E, 16><<<grid(305), 512, 0, st>>>(p);
+    else append_block_kernel<E, 32><<<grid(153), 1024, 0, st>>>(p);
     return launched();
 }
 

@@ -72,7 +72,6 @@ struct DecodeParams {
     uint32_t T, cp, interleave, window, sinks;
     int block_log2;
     int B, H, head_blocks, ranges;         // grid: head_blocks x ranges CTAs
-    int min_tiles;
     int row_mode;                          // a range is whole rows (no row is split)
     float scale_log2;
     float lse_scale;                       // ln 2 for a natural-log LSE, 1 for base 2
@@ -570,8 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         for (int pass = 0; pass < 2; ++pass) {
             int base = 0;
             if (pass == 1) {
-                int per = (total + p.ranges - 1) / p.ranges;
-                if (per < p.min_tiles) per = p.min_tiles;
+                const int per = max((total + p.ranges - 1) / p.ranges, 1);
                 const int64_t lo = (int64_t)range * per, hi = lo + per;
                 g = lo < total ? (int)lo : total;
                 g_end = hi < total ? (int)hi : total;
@@ -634,8 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     if (lane >= o) x += y;
                 }
                 const int total = __shfl_sync(0xffffffffu, x, 31), pre = x - n;
-                int per = (total + p.ranges - 1) / p.ranges;
-                if (per < p.min_tiles) per = p.min_tiles;
+                const int per = max((total + p.ranges - 1) / p.ranges, 1);
                 const int64_t lo = (int64_t)range * per, hi = lo + per;
                 g = lo < total ? (int)lo : total;
                 g_end = hi < total ? (int)hi : total;
@@ -1352,9 +1349,23 @@ cudaError_t launch_decode_dk(const DecodeParams& p, unsigned flags, cudaStream_t
 
 }  // namespace
 
-extern "C" int64_t dcp_mla_cache8_decode_workspace_bytes(int64_t B, int H, int num_sms) {
-    if (B < 0 || B > 65535 || H < 1 || H > 1024 || num_sms < 1 || num_sms > 4096) return -1;
-    return workspace_of(B, H, num_sms).bytes;
+namespace {
+
+// Rows of at most two tiles are not worth splitting: a join costs as much.
+bool whole_rows(int cp, int64_t T, int64_t window, int64_t sinks) {
+    const int64_t seen = window > 0 && window < T ? window : T, first = sinks < T ? sinks : T;
+    const int64_t most = (seen + kTile - 1) / kTile + (window > 0 ? (first + kTile - 1) / kTile : 0);
+    return cp * most <= 2;
+}
+
+}  // namespace
+
+extern "C" int64_t dcp_mla_cache8_decode_workspace_bytes(int cp, int64_t B, int H, int64_t T, int64_t window,
+                                                         int64_t sinks, int num_sms) {
+    if (cp < 1 || cp > kCpMax || B < 0 || B > 65535 || H < 1 || H > 1024 || T < 0 || T > 0x7fffffff || window < 0 ||
+        sinks < 0 || num_sms < 1 || num_sms > 4096)
+        return -1;
+    return B == 0 || whole_rows(cp, T, window, sinks) ? 0 : workspace_of(B, H, num_sms).bytes;
 }
 
 extern "C" int dcp_mla_cache8_decode(const void* q, int64_t q_row, int64_t q_head, const void* const* kv_ptrs,
@@ -1399,7 +1410,8 @@ extern "C" int dcp_mla_cache8_decode(const void* q, int64_t q_row, int64_t q_hea
         return DCP_ERR_DEVICE;
     }
     const Workspace ws = workspace_of(B, H, sms);
-    if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < ws.bytes)
+    p.row_mode = whole_rows(cp, T, window, sinks) ? 1 : 0;
+    if (!p.row_mode && (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < ws.bytes))
         return DCP_MLA_CACHE8_ERR_WORKSPACE;
     if (T == 0) p.held = 0;  // nothing is cached: every row is empty
     for (int j = 0; j < kCpMax; ++j) {
@@ -1432,14 +1444,9 @@ extern "C" int dcp_mla_cache8_decode(const void* q, int64_t q_row, int64_t q_hea
     p.H = H;
     p.head_blocks = (H + head_block(H) - 1) / head_block(H);
     p.ranges = grid_ranges(H, sms);
-    p.min_tiles = 1;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.lse_scale = lse_base_e ? 0.6931471805599453f : 1.0f;
     p.wait_ns = kWaitLimitNs;
-    // Rows of at most two tiles are not worth splitting: a join costs as much.
-    const int64_t span = window > 0 && window < T ? window + kTile - 1 : T;
-    const int64_t row_most = (int64_t)cp * ((span + kTile - 1) / kTile + (sinks > 0 ? (sinks + kTile - 1) / kTile : 0));
-    p.row_mode = row_most <= 2 ? 1 : 0;
     if (p.row_mode && p.ranges > B) p.ranges = (int)B;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = Dk == 576 ? launch_decode_dk<576>(p, flags, st) : launch_decode_dk<512>(p, flags, st);

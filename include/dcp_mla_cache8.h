@@ -142,9 +142,10 @@ int dcp_mla_cache8_read(const void* const* kv_ptrs, const float* const* scale_pt
  *            elements), 4-byte aligned
  *   out      [B, H, 512] bf16, contiguous, 16-byte aligned
  *   lse      [B, H] fp32, contiguous, base e or 2; may be NULL
- *   workspace at least dcp_mla_cache8_decode_workspace_bytes(B, H, num_sms)
- *            bytes, 256-byte aligned, owned by the caller; its contents on
- *            entry do not matter. Calls that share one must be ordered.
+ *   workspace at least dcp_mla_cache8_decode_workspace_bytes(...) bytes,
+ *            256-byte aligned, owned by the caller (NULL where that is 0); its
+ *            contents on entry do not matter. Calls that share one must be
+ *            ordered.
  *   status   as for dcp_mla_decode_partial: NULL, or a device int32 that the
  *            kernel ORs 1 into if a wait for its own copies or MMAs ever
  *            exceeds two seconds; the outputs are then not valid
@@ -166,10 +167,12 @@ int dcp_mla_cache8_decode(const void* q, int64_t q_row, int64_t q_head, const vo
                           int32_t* status, unsigned flags, void* stream);
 
 /*
- * Bytes of workspace dcp_mla_cache8_decode needs on a device with num_sms
- * multiprocessors (cudaDevAttrMultiProcessorCount); -1 for sizes out of range.
+ * Bytes of workspace dcp_mla_cache8_decode needs for these sizes on a device
+ * with num_sms multiprocessors (cudaDevAttrMultiProcessorCount); 0 where no row
+ * can be long enough to be split; -1 for sizes out of range. Host only.
  */
-int64_t dcp_mla_cache8_decode_workspace_bytes(int64_t B, int H, int num_sms);
+int64_t dcp_mla_cache8_decode_workspace_bytes(int cp, int64_t B, int H, int64_t T, int64_t window, int64_t sinks,
+                                              int num_sms);
 
 #ifdef __cplusplus
 }

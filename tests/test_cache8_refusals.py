@@ -93,9 +93,16 @@ def test_decode_of_no_rows_is_nothing():
 
 def test_workspace_bytes():
     ws = dcp.dcp_mla_cache8_decode_workspace_bytes
-    assert ws(8, 128, 152) >= 2 * 152 * 64 * 513 * 4
-    assert ws(65535, 1024, 152) >= 2 * 144 * 64 * 513 * 4 + 65536 * 4  # 16 head blocks x 9 ranges
-    for bad in ((-1, 16, 152), (65536, 16, 152), (1, 0, 152), (1, 1025, 152), (1, 16, 0)):
+    assert ws(1, 8, 128, 4096, 0, 0, 152) >= 2 * 152 * 64 * 513 * 4
+    assert ws(1, 65535, 1024, 4096, 0, 0, 152) >= 2 * 144 * 64 * 513 * 4 + 65535 * 8  # 16 head blocks x 9 ranges
+    # at most two tiles of 128 tokens a row: no row is split
+    for cp, T, window, sinks, none in ((1, 256, 0, 0, True), (1, 257, 0, 0, False), (2, 128, 0, 0, True),
+                                       (3, 100, 0, 0, False), (1, 10 ** 6, 128, 4, True), (1, 10 ** 6, 129, 4, False),
+                                       (1, 10 ** 6, 256, 0, True), (2, 10 ** 6, 128, 0, True), (1, 0, 0, 0, True)):
+        assert (ws(cp, 4, 16, T, window, sinks, 152) == 0) == none
+    for bad in ((0, 1, 16, 9, 0, 0, 152), (17, 1, 16, 9, 0, 0, 152), (1, -1, 16, 9, 0, 0, 152),
+                (1, 65536, 16, 9, 0, 0, 152), (1, 1, 0, 9, 0, 0, 152), (1, 1, 1025, 9, 0, 0, 152),
+                (1, 1, 16, -1, 0, 0, 152), (1, 1, 16, 9, -1, 0, 152), (1, 1, 16, 9, 0, 0, 0)):
         assert ws(*bad) == -1
 
 

@@ -575,7 +575,7 @@ def test_decode_strided_q_given_outputs_and_flags():
     out = torch.empty((B, H, 512), dtype=torch.bfloat16, device=DEV)
     lse = torch.empty((B, H), dtype=torch.float32, device=DEV)
     n = torch.cuda.get_device_properties(0).multi_processor_count
-    ws = torch.full((dcp.dcp_mla_cache8_decode_workspace_bytes(B, H, n),), 0xFF, dtype=torch.uint8, device=DEV)
+    ws = torch.full((dcp.dcp_mla_cache8_decode_workspace_bytes(1, B, H, T, 0, 0, n),), 0xFF, dtype=torch.uint8, device=DEV)
     codes = [x.view(torch.uint8) for x in kv]
     got = dcp.mla_cache8_decode(q, codes, sc, lens, SCALE, out=out, lse=lse, workspace=ws, flags=dcp.DCP_FLAG_PDL)
     assert got[0] is out and got[1] is lse
