@@ -40,55 +40,65 @@ def _ready():
     return _b._lib or _b.load(), _torch
 
 
-def _on(device, stream):
-    """(raw stream, context): the stream to launch on, and what to be inside of
-    while allocating and launching (None where that is the present state, which
-    the small calls' host time is mostly made of)."""
-    if device.type != "cuda":
+# A small call's time is its host time, and most of that is looking at tensors: the
+# checks use what is cheapest to ask (device indices, not device objects; shape[0],
+# not len()).
+
+
+def _on(index: int, stream):
+    """(raw stream, context) on CUDA device ``index``: the stream to launch on, and
+    what to be inside of while allocating and launching (None where that is the
+    present state)."""
+    if index < 0:
         raise ValueError("the tensors must be CUDA tensors")
-    cuda, index = _torch.cuda, device.index
     if stream is None:
         # (the raw handle: building a torch.cuda.Stream for it costs as much as a launch)
         return _torch._C._cuda_getCurrentRawStream(index), \
-            None if cuda.current_device() == index else cuda.device(device)
+            None if _torch._C._cuda_getDevice() == index else _torch.cuda.device(index)
+    cuda = _torch.cuda
     if isinstance(stream, int):
         raw = stream
-        stream = cuda.default_stream(device) if raw == 0 else cuda.ExternalStream(raw, device=device)
+        stream = cuda.default_stream(index) if raw == 0 else cuda.ExternalStream(raw, device=index)
     else:
         raw = int(stream.cuda_stream)
-        if stream.device != device:
+        if stream.device.index != index:
             raise ValueError("the stream is on another device than the tensors")
     both = contextlib.ExitStack()
-    both.enter_context(cuda.device(device))
+    both.enter_context(cuda.device(index))
     both.enter_context(cuda.stream(stream))
     return raw, both
 
 
-def _sms(device) -> int:
-    n = _SMS.get(device.index)
+def _sms(index: int) -> int:
+    n = _SMS.get(index)
     if n is None:
-        n = _SMS[device.index] = int(_torch.cuda.get_device_properties(device).multi_processor_count)
+        n = _SMS[index] = int(_torch.cuda.get_device_properties(index).multi_processor_count)
     return n
 
 
-def _ints(name, t, n, device):
+def _cuda(index: int):
+    return _torch.device("cuda", index)
+
+
+def _ints(name, t, n, index):
     """The address of a contiguous int32 tensor of n entries (None for None)."""
     if t is None:
         return None
-    if t.dtype != _torch.int32 or t.dim() != 1 or len(t) != n or t.device != device or not t.is_contiguous():
+    if t.dtype != _torch.int32 or t.dim() != 1 or t.shape[0] != n or t.get_device() != index or \
+            not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on the caches' device")
     return t.data_ptr()
 
 
 def _shards(caches, scales, block):
-    """Check the shards' tensors; (device, B, T, Dk, cache pointers, scale pointers)."""
+    """Check the shards' tensors; (device index, B, T, Dk, cache pointers, scale pointers)."""
     cp = len(caches)
     if cp < 1 or cp > _b.DCP_MLA_CACHE8_CP_MAX or len(scales) != cp:
         raise ValueError(f"need 1 to {_b.DCP_MLA_CACHE8_CP_MAX} caches (None for a shard that is not held) and as "
                          "many scale tensors")
     if block < 1 or block > _b.DCP_MLA_CACHE8_BLOCK_MAX or block & (block - 1):
         raise ValueError(f"block must be a power of two, at most {_b.DCP_MLA_CACHE8_BLOCK_MAX}")
-    device = shape = None
+    shape = None
     kv, sc = (ctypes.c_void_p * cp)(), (ctypes.c_void_p * cp)()
     e4m3, codes, f32 = _torch.float8_e4m3fn, _torch.uint8, _torch.float32
     for j in range(cp):
@@ -98,21 +108,23 @@ def _shards(caches, scales, block):
                 raise ValueError("a shard has both a cache and scales, or neither")
             continue
         if shape is None:
-            device, shape = c.device, c.shape
+            index, shape = c.get_device(), c.shape
             if len(shape) != 3 or shape[2] not in (512, 576):
                 raise ValueError("a cache must be [B, T, 512] or [B, T, 576]")
-            sshape = (shape[0], -(-shape[1] // block))
+            B, T, dk = shape
+            sshape = (B, -(-T // block))
+        elif c.shape != shape:
+            raise ValueError("the caches must have one shape")
         if (c.dtype != e4m3 and c.dtype != codes) or s.dtype != f32:
             raise TypeError("caches must be float8_e4m3fn (or uint8 codes) and scales float32")
-        if c.shape != shape or s.shape != sshape or c.device != device or s.device != device:
-            raise ValueError("shards must have one shape and device, and scales [B, ceil(T / block)]")
+        if s.shape != sshape or c.get_device() != index or s.get_device() != index:
+            raise ValueError("shards must be on one device, and scales [B, ceil(T / block)]")
         if not (c.is_contiguous() and s.is_contiguous()):
             raise ValueError("caches and scales must be contiguous")
         kv[j], sc[j] = c.data_ptr(), s.data_ptr()
     if shape is None:
         raise ValueError("no shard is held here")
-    B, T, dk = shape
-    return device, B, T, dk, kv, sc
+    return index, B, T, dk, kv, sc
 
 
 def mla_rope_inv_freq(rot: int = 64, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
@@ -166,36 +178,36 @@ def mla_rope(x, positions, inv_freq, *, start: int = 0, interleaved: bool = True
     dtype = _DTYPES.get(x.dtype)
     if dtype is None:
         raise TypeError("x must be bf16, fp16 or fp32")
-    device = x.device
+    index = x.get_device()
     if unit != 1 and d > 1:
         raise ValueError("x needs unit stride along D")
     if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous() or \
-            inv_freq.device != device:
+            inv_freq.get_device() != index:
         raise ValueError("inv_freq must be a contiguous float64 tensor on x's device")
     wide = positions.dtype == torch.int64
-    if not (wide or positions.dtype == torch.int32) or positions.dim() != 1 or len(positions) != n or \
-            positions.device != device or not positions.is_contiguous():
+    if not (wide or positions.dtype == torch.int32) or positions.dim() != 1 or positions.shape[0] != n or \
+            positions.get_device() != index or not positions.is_contiguous():
         raise ValueError("positions must be a contiguous int32 or int64 tensor [N] on x's device")
-    raw, inside = _on(device, stream)
+    raw, inside = _on(index, stream)
     if inside is not None:
         with inside:
             return mla_rope(x, positions, inv_freq, start=start, interleaved=interleaved, mscale=mscale, out=out)
     src = x.data_ptr()
     if out is None:
-        out = torch.empty((n, h, d), dtype=x.dtype, device=device)
+        out = torch.empty((n, h, d), dtype=x.dtype, device=x.device)
         dst, orow, ohead = out.data_ptr(), h * d, d
     elif out is x:
         dst, orow, ohead = src, row, head
     else:
         orow, ohead, unit = out.stride() if out.dim() == 3 else (0, 0, 0)
-        if out.shape != x.shape or out.dtype != x.dtype or out.device != device or (unit != 1 and d > 1):
+        if out.shape != x.shape or out.dtype != x.dtype or out.get_device() != index or (unit != 1 and d > 1):
             raise ValueError("out must have x's shape, dtype and device, and unit stride along D")
         dst = out.data_ptr()
         gap = abs(dst - src) // x.element_size()
         if 0 < gap < d and n * h > 0 and x.untyped_storage().data_ptr() == out.untyped_storage().data_ptr():
             raise ValueError("out overlaps x: pass x itself to rotate in place")
     rc = lib.dcp_mla_rope(src, row, head, positions.data_ptr(), wide, inv_freq.data_ptr(), n, h, d, start,
-                          2 * len(inv_freq), interleaved, mscale, dtype, dst, orow, ohead, raw)
+                          2 * inv_freq.shape[0], interleaved, mscale, dtype, dst, orow, ohead, raw)
     if rc:
         _b._check8(rc)
     return out
@@ -213,17 +225,20 @@ def mla_cache8_append(latent, k_rope, caches, scales, seq_lens, *, cu_new=None, 
     smallest power of two that holds its values; a block that already holds
     tokens is requantised where its scale grows."""
     lib, torch = _ready()
-    device, B, T, dk, kv, sc = _shards(caches, scales, block)
+    index, B, T, dk, kv, sc = _shards(caches, scales, block)
     dtype = _DTYPES.get(latent.dtype)
     if dtype is None or dtype == _b.DCP_DTYPE_F32:
         raise TypeError("latent must be bf16 or fp16")
-    n = len(latent)
-    if latent.dim() != 2 or latent.shape[1] != 512 or latent.stride(1) != 1 or latent.device != device:
+    if latent.dim() != 2 or latent.get_device() != index:
+        raise ValueError("latent must be [N, 512] with unit inner stride, on the caches' device")
+    n, width = latent.shape
+    row, unit = latent.stride()
+    if width != 512 or unit != 1:
         raise ValueError("latent must be [N, 512] with unit inner stride, on the caches' device")
     rope_ptr, rope_row = None, 0
     if dk == 576:
         if k_rope is None or k_rope.shape != (n, 64) or k_rope.dtype != latent.dtype or k_rope.stride(1) != 1 or \
-                k_rope.device != device:
+                k_rope.get_device() != index:
             raise ValueError("k_rope must be [N, 64] of latent's dtype with unit inner stride, on the caches' device")
         rope_ptr, rope_row = k_rope.data_ptr(), k_rope.stride(0)
     elif k_rope is not None or inv_freq is not None:
@@ -231,18 +246,20 @@ def mla_cache8_append(latent, k_rope, caches, scales, seq_lens, *, cu_new=None, 
     freq_ptr = None
     if inv_freq is not None:
         if inv_freq.dtype != torch.float64 or inv_freq.shape != (32,) or not inv_freq.is_contiguous() or \
-                inv_freq.device != device:
+                inv_freq.get_device() != index:
             raise ValueError("inv_freq must be a contiguous float64 tensor [32] on the caches' device")
         freq_ptr = inv_freq.data_ptr()
-    lens = _ints("seq_lens", seq_lens, B, device)
+    lens = _ints("seq_lens", seq_lens, B, index)
     if lens is None:
         raise ValueError("seq_lens is required")
-    cu = _ints("cu_new", cu_new, B + 1, device)
-    raw, inside = _on(device, stream)
-    with inside or contextlib.nullcontext():
-        rc = lib.dcp_mla_cache8_append(latent.data_ptr(), latent.stride(0), rope_ptr, rope_row, dtype, n, B, dk, cu,
-                                       lens, kv, sc, len(caches), T, block, interleave, freq_ptr, interleaved, mscale,
-                                       raw)
+    cu = _ints("cu_new", cu_new, B + 1, index)
+    raw, inside = _on(index, stream)
+    if inside is not None:
+        with inside:
+            return mla_cache8_append(latent, k_rope, caches, scales, seq_lens, cu_new=cu_new, block=block,
+                                     interleave=interleave, inv_freq=inv_freq, interleaved=interleaved, mscale=mscale)
+    rc = lib.dcp_mla_cache8_append(latent.data_ptr(), row, rope_ptr, rope_row, dtype, n, B, dk, cu, lens, kv, sc,
+                                   len(caches), T, block, interleave, freq_ptr, interleaved, mscale, raw)
     if rc:
         _b._check8(rc)
 
@@ -257,24 +274,28 @@ def mla_cache8_read(caches, scales, total: int, *, starts=None, cu=None, block: 
     16-byte boundaries. Tokens that no held shard has are left as they were.
     Returns out."""
     lib, torch = _ready()
-    device, B, T, dk, kv, sc = _shards(caches, scales, block)
+    index, B, T, dk, kv, sc = _shards(caches, scales, block)
     if total < 0:
         raise ValueError("total must not be negative")
     dtype = (torch.bfloat16 if out is None else out.dtype) if dtype is None else dtype
     code = _DTYPES.get(dtype)
     if code is None:
         raise TypeError("dtype must be bf16, fp16 or fp32")
-    start_ptr, cu_ptr = _ints("starts", starts, B, device), _ints("cu", cu, B + 1, device)
-    raw, inside = _on(device, stream)
-    with inside or contextlib.nullcontext():
-        if out is None:
-            out, row = torch.empty((total, dk), dtype=dtype, device=device), dk
-        elif out.shape != (total, dk) or out.dtype != dtype or out.device != device or out.stride(1) != 1:
-            raise ValueError("out must be [total, Dk] of dtype with unit inner stride, on the caches' device")
-        else:
-            row = out.stride(0)
-        rc = lib.dcp_mla_cache8_read(kv, sc, len(caches), B, T, dk, block, interleave, start_ptr, cu_ptr, total,
-                                     out.data_ptr(), row, code, raw)
+    start_ptr, cu_ptr = _ints("starts", starts, B, index), _ints("cu", cu, B + 1, index)
+    raw, inside = _on(index, stream)
+    if inside is not None:
+        with inside:
+            return mla_cache8_read(caches, scales, total, starts=starts, cu=cu, block=block, interleave=interleave,
+                                   dtype=dtype, out=out)
+    row = dk
+    if out is None:
+        out = torch.empty((total, dk), dtype=dtype, device=_cuda(index))
+    elif out.shape != (total, dk) or out.dtype != dtype or out.get_device() != index or out.stride(1) != 1:
+        raise ValueError("out must be [total, Dk] of dtype with unit inner stride, on the caches' device")
+    else:
+        row = out.stride(0)
+    rc = lib.dcp_mla_cache8_read(kv, sc, len(caches), B, T, dk, block, interleave, start_ptr, cu_ptr, total,
+                                 out.data_ptr(), row, code, raw)
     if rc:
         _b._check8(rc)
     return out
@@ -295,42 +316,49 @@ def mla_cache8_decode(q, caches, scales, seq_lens, scale: float, *, block: int =
     256-byte aligned, allocated when not given and needed. status: None, or an
     int32 CUDA tensor (see the C header)."""
     lib, torch = _ready()
-    device, B, T, dk, kv, sc = _shards(caches, scales, block)
-    if q.dim() != 3 or q.dtype != torch.bfloat16 or q.device != device:
+    index, B, T, dk, kv, sc = _shards(caches, scales, block)
+    if q.dim() != 3 or q.dtype != torch.bfloat16 or q.get_device() != index:
         raise ValueError("q must be bf16 [B, H, Dk] with unit inner stride, on the caches' device")
     qb, H, qd = q.shape
     row, head, unit = q.stride()
     if qb != B or qd != dk or unit != 1:
         raise ValueError("q must be bf16 [B, H, Dk] with unit inner stride, on the caches' device")
-    lens = _ints("seq_lens", seq_lens, B, device)
+    lens = _ints("seq_lens", seq_lens, B, index)
     if lens is None:
         raise ValueError("seq_lens is required")
     cp = len(caches)
-    raw, inside = _on(device, stream)
-    with inside or contextlib.nullcontext():
-        if out is None:
-            out = torch.empty((B, H, 512), dtype=torch.bfloat16, device=device)
-        elif out.shape != (B, H, 512) or out.dtype != torch.bfloat16 or out.device != device or \
-                not out.is_contiguous():
-            raise ValueError("out must be a contiguous bf16 tensor [B, H, 512] on the caches' device")
-        if lse is None:
-            lse = torch.empty((B, H), dtype=torch.float32, device=device)
-        elif lse.shape != (B, H) or lse.dtype != torch.float32 or lse.device != device or not lse.is_contiguous():
-            raise ValueError("lse must be a contiguous fp32 tensor [B, H] on the caches' device")
-        if workspace is None:
-            size = lib.dcp_mla_cache8_decode_workspace_bytes(cp, B, H, T, window, sinks, _sms(device))
-            if size > 0:
-                workspace = torch.empty((size,), dtype=torch.uint8, device=device)
-        elif workspace.device != device or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the caches' device")
-        else:
-            size = workspace.numel() * workspace.element_size()
-        if status is not None and (status.dtype != torch.int32 or status.device != device or status.numel() < 1):
+    raw, inside = _on(index, stream)
+    if inside is not None:
+        with inside:
+            return mla_cache8_decode(q, caches, scales, seq_lens, scale, block=block, interleave=interleave,
+                                     window=window, sinks=sinks, lse_base_e=lse_base_e, out=out, lse=lse,
+                                     workspace=workspace, status=status, flags=flags)
+    if out is None:
+        out = torch.empty((B, H, 512), dtype=torch.bfloat16, device=q.device)
+    elif out.shape != (B, H, 512) or out.dtype != torch.bfloat16 or out.get_device() != index or \
+            not out.is_contiguous():
+        raise ValueError("out must be a contiguous bf16 tensor [B, H, 512] on the caches' device")
+    if lse is None:
+        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+    elif lse.shape != (B, H) or lse.dtype != torch.float32 or lse.get_device() != index or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 tensor [B, H] on the caches' device")
+    room = None
+    if workspace is None:
+        size = lib.dcp_mla_cache8_decode_workspace_bytes(cp, B, H, T, window, sinks, _sms(index))
+        if size > 0:
+            workspace = torch.empty((size,), dtype=torch.uint8, device=q.device)
+            room = workspace.data_ptr()
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the caches' device")
+    else:
+        size, room = workspace.numel() * workspace.element_size(), workspace.data_ptr()
+    if status is not None:
+        if status.dtype != torch.int32 or status.get_device() != index or status.numel() < 1:
             raise ValueError("status must be an int32 tensor on the caches' device")
-        rc = lib.dcp_mla_cache8_decode(q.data_ptr(), row, head, kv, sc, lens, cp, B, H, dk, 512, T, block, interleave,
-                                       window, sinks, scale, lse_base_e,
-                                       None if workspace is None else workspace.data_ptr(), size, out.data_ptr(),
-                                       lse.data_ptr(), None if status is None else status.data_ptr(), flags, raw)
+        status = status.data_ptr()
+    rc = lib.dcp_mla_cache8_decode(q.data_ptr(), row, head, kv, sc, lens, cp, B, H, dk, 512, T, block, interleave,
+                                   window, sinks, scale, lse_base_e, room, size, out.data_ptr(), lse.data_ptr(),
+                                   status, flags, raw)
     if rc:
         _b._check8(rc)
     return out, lse
