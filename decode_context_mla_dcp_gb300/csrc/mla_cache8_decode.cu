@@ -60,6 +60,7 @@ struct DecodeParams {
     const float* scales[kCpMax];
     const uint8_t* q;
     int64_t q_row, q_head;                 // bytes
+    int q_wide;                            // q can be read 16 bytes at a time
     const int* seq_lens;
     float* part;                           // [2 x CTAs][heads of a block][512], normalised
     float* part_lse;                       // [2 x CTAs][heads of a block], base 2
@@ -134,6 +135,9 @@ __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.
 // 4 bytes from global to shared memory, asynchronously; `bytes` = 0 writes zeros.
 __device__ __forceinline__ void copy_word(uint32_t dst, const uint8_t* src, uint32_t bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_16(uint32_t dst, const uint8_t* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* tm, int x, int y, int z, uint64_t* bar) {
     asm volatile(
@@ -427,10 +431,7 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
     return lo | (hi << 16);
 }
-// Barrier, and vote, of all softmax warps.
-__device__ __forceinline__ void soft_sync() {
-    asm volatile("barrier.cta.sync.aligned 5, %0;" ::"n"(kSoftThreads) : "memory");
-}
+// A vote of all softmax warps (and a barrier).
 __device__ __forceinline__ bool soft_any(bool x) {
     uint32_t r;
     asm volatile(
@@ -777,38 +778,45 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                                     mbar_wait(&sh->met[group], met++ & 1, abort_flag, p.status, p.wait_ns));
         };
         // A segment's q, raw: a head's bf16 values into the place of its two parts (128 dims of a slice are 256 bytes
-        // either way), all of a warp's heads in flight at once.
+        // either way), all of a warp's heads (a quarter of its group's) in flight at once.
+        constexpr int kPer = kHW / 4;
+        const int hq = hb + quad * kPer;
         auto fetch_q = [&](int row) {
+            const uint8_t* const src = p.q + row * p.q_row + (h0 + hq) * p.q_head;
+            const uint32_t to = smem_u32(q_s);
+            if (p.q_wide) {
+                constexpr int kC = kDk / 8;  // 16-byte pieces of a head
 #pragma unroll 1
-            for (int h = warp; h < kNH; h += kSoftWarps) {
-                const uint8_t* const src = p.q + row * p.q_row + (h0 + (h < nh ? h : 0)) * p.q_head + 4 * lane;
-                const uint32_t dst = smem_u32(q_s) + h * 128 + 4 * lane, bytes = h < nh ? 4u : 0u;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    copy_word(dst + (i >> 1) * S::kQSlice + (i & 1) * kNH * 128, src + 128 * i, bytes);
-                if constexpr (S::kHasRope)
-                    copy_word(smem_u32(q_s) + 4 * S::kQSlice + (h + (lane >> 4) * kNH) * 64 + 4 * (lane & 15),
-                              src + 1024, bytes);
+                for (int i = lane; i < kPer * kC; i += 32) {
+                    const int k = i / kC, j = i - k * kC;
+                    const uint32_t dst = j < 64 ? (j >> 4) * S::kQSlice + (hq + k + ((j >> 3) & 1) * kNH) * 128 + (j & 7) * 16
+                                                : 4 * S::kQSlice + (hq + k + ((j - 64) >> 2) * kNH) * 64 + (j & 3) * 16;
+                    const bool is = hq + k < nh;
+                    copy_16(to + dst, is ? src + k * p.q_head + 16 * j : p.q, is ? 16u : 0u);
+                }
+            } else {
+#pragma unroll 1
+                for (int k = 0; k < kPer; ++k) {
+                    const bool is = hq + k < nh;
+                    const uint8_t* const from = is ? src + k * p.q_head + 4 * lane : p.q;
+                    const uint32_t dst = to + (hq + k) * 128 + 4 * lane, step = is ? 128u : 0u, bytes = is ? 4u : 0u;
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i)
+                        copy_word(dst + (i >> 1) * S::kQSlice + (i & 1) * kNH * 128, from + i * step, bytes);
+                    if constexpr (S::kHasRope)
+                        copy_word(to + 4 * S::kQSlice + (hq + k + (lane >> 4) * kNH) * 64 + 4 * (lane & 15),
+                                  from + 8 * step, bytes);
+                }
             }
         };
-        // The next tile's description; a tile of no tokens (or a wait that gave up, in any warp) ends the loop.
-        TileInfo ti = {0u, 0, 0u, 0};
-        auto next_segment = [&]() {
-            const bool ok = mbar_wait(&sh->info_full[t & 3], (t >> 2) & 1, abort_flag, p.status, p.wait_ns);
-            ti = sh->info[t & 3];
-            return !soft_any(!ok) && ti.valid > 0;  // (all warps agree)
-        };
-        bool going = next_segment();
-        if (going) fetch_q(ti.row);
-        while (going) {  // segments
-            const int row = ti.row;
+        // hi and lo e4m3 parts of each head at its own power-of-two scale. A lane has dims 4l .. 4l + 3 of each slice
+        // and 2l, 2l + 1 of the rotary part; the arithmetic is on pairs of bf16, and exact.
+        auto split_q = [&]() {
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
-            // q: hi and lo e4m3 parts of each head at its own power-of-two scale. A lane has dims 4l .. 4l + 3 of each
-            // slice and 2l, 2l + 1 of the rotary part; the arithmetic is on pairs of bf16, and exact.
             constexpr int kWords = kDk / 64;
 #pragma unroll 1
-            for (int h = warp; h < kNH; h += kSoftWarps) {
+            for (int h = hq; h < hq + kPer; ++h) {
                 uint32_t w[kWords];
                 const uint8_t* const raw = q_s + (h + (lane >> 4) * kNH) * 128 + 8 * (lane & 15);
 #pragma unroll
@@ -854,11 +862,27 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     *reinterpret_cast<uint16_t*>(ar + kNH * 64) = (uint16_t)lo[8];
                 }
             }
-            if (tid < kNH) m_s[tid] = kMagicBits - kFar;
+            if (lane < kPer) m_s[hq + lane] = kMagicBits - kFar;
             async_fence();
-            soft_sync();  // (every group reads scales and references that all warps wrote)
+            const bool ok = meet();  // (the group's warps use each other's heads)
             if (lane == 0) mbar_arrive(&sh->q_full);
-
+            return ok;
+        };
+        // The next tile's description; a tile of no tokens ends the loop, and so does a wait that gave up in any
+        // warp: all warps agree here.
+        TileInfo ti = {0u, 0, 0u, 0};
+        auto next_segment = [&](bool good) {
+            const bool ok = mbar_wait(&sh->info_full[t & 3], (t >> 2) & 1, abort_flag, p.status, p.wait_ns);
+            ti = sh->info[t & 3];
+            return !soft_any(!(ok && good)) && ti.valid > 0;
+        };
+        bool going = next_segment(true);
+        if (going) {
+            fetch_q(ti.row);
+            aborted = !split_q();
+        }
+        while (going) {  // segments
+            const int row = ti.row;
             f32x2 l2[kHW / 2];
 #pragma unroll
             for (int h = 0; h < kHW / 2; ++h) l2[h] = 0ull;
@@ -1055,18 +1079,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh->p_full);
-                aborted = __any_sync(0xffffffffu, !ok);
+                aborted = aborted || __any_sync(0xffffffffu, !ok);
                 if (aborted || (ti.what & kLast)) break;
             }
             ++t;
-            // The next segment's q is on its way while this one ends (its scores are all done: q's place is free).
-            going = next_segment();
+            // ---- the segment's end. The next one's q comes in meanwhile (this one's scores are all done: q's place
+            // is free) and is split before this one's output leaves, so that its first scores run beside that.
+            going = next_segment(!aborted);
             if (going) fetch_q(ti.row);
-            // ---- the segment's end: sums, then O / l
             if (!aborted) {
-                const bool ok =
-                    __all_sync(0xffffffffu, mbar_wait(&sh->o_done, (t - 1) & 1, abort_flag, p.status, p.wait_ns));
-                tc_fence_after();
                 // sums over the warp's tokens: halves of the heads to halves of the lanes until a lane has one head
                 float l[kHW];
 #pragma unroll
@@ -1084,7 +1105,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 #pragma unroll
                 for (; off >= 1; off /= 2) l[0] += __shfl_xor_sync(0xffffffffu, l[0], off);
                 if ((lane & (32 / kHW - 1)) == 0) red[quad * kNH + hb + lane / (32 / kHW)] = l[0];
-                aborted = !meet() || !ok;
+                aborted = !meet();
                 const bool whole = (about & kWhole) != 0;  // the row's only segment
                 const int64_t slot = (int64_t)blockIdx.x * 2 + ((about & kStarts) ? 1 : 0);
                 if (quad == 0 && lane < kHW) {
@@ -1098,7 +1119,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 aborted = !meet() || aborted;
                 float inv[kHW];
 #pragma unroll
-                for (int h = 0; h < kHW; h += 4) *reinterpret_cast<float4*>(inv + h) = *reinterpret_cast<const float4*>(a_s + hb + h);
+                for (int h = 0; h < kHW; h += 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(a_s + hb + h);
+                    inv[h] = x.x;
+                    inv[h + 1] = x.y;
+                    inv[h + 2] = x.z;
+                    inv[h + 3] = x.w;
+                }
+                if (going) aborted = !split_q() || aborted;
+                aborted = !__all_sync(0xffffffffu, mbar_wait(&sh->o_done, (t - 1) & 1, abort_flag, p.status,
+                                                             p.wait_ns)) || aborted;
+                tc_fence_after();
 #pragma unroll 1
                 for (int m = 0; m < 4; ++m) {
                     float o[kHW];
@@ -1126,8 +1157,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 }
                 tc_fence_before();
             }
-            // (the next segment writes what this one's threads have read; all warps leave together)
-            going = !soft_any(aborted) && going;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");  // (of a segment that was given up)
     }
@@ -1140,21 +1169,35 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 
 // ---- the rows that were split ---------------------------------------------------------
 
+struct JoinParams {
+    const float* part;
+    const float* part_lse;
+    const int2* row_info;
+    uint8_t* out;
+    float* lse;
+    int64_t units;       // rows x heads
+    int H, head_blocks, block_heads;
+    float lse_scale;
+};
+
 // One warp (or kWarps warps, where there are few rows and many segments of each)
 // per (row, head): the segments' outputs weighted by 2^(lse - max), and the row's
 // LSE. Rows with one segment have been written; rows without a tile get zeros.
+// Two round trips to memory: what the row has, then a warp's first segment and
+// all LSEs together.
 template <int kWarps>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ DecodeParams p, int heads_of_block) {
-    __shared__ float acc_s[8][kDv];
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinParams p) {
+    __shared__ float acc_s[kWarps > 1 ? 8 : 1][kDv];
     __shared__ float sum_s[8];
-    pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t unit = (int64_t)blockIdx.x * (8 / kWarps) + warp / kWarps;
-    if (unit >= (int64_t)p.B * p.H) return;
     const int b = (int)(unit / p.H), h = (int)(unit - (int64_t)b * p.H);
+    const int hblk = h / p.block_heads, hh = h - hblk * p.block_heads, w = warp % kWarps;
+    pdl_wait();
+    if (unit >= p.units) return;
     const int2 row = p.row_info[b];
+    if (row.y == 1) return;
     uint4* const out = reinterpret_cast<uint4*>(p.out + unit * (kDv * 2));
-    const int w = warp % kWarps;
     if (row.y == 0) {
         if (w == 0) {
             out[lane] = make_uint4(0u, 0u, 0u, 0u);
@@ -1163,39 +1206,41 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Decod
         }
         return;
     }
-    if (row.y == 1) return;
-    const int k0 = row.x, k1 = k0 + row.y - 1;
-    const int hblk = h / heads_of_block, hh = h - hblk * heads_of_block;
-    auto slot = [&](int k) { return ((int64_t)k * p.head_blocks + hblk) * 2 + (k == k0 ? 1 : 0); };
-    float m = -INFINITY;
+    // segment i of the row: the first one is its CTA's last, the others are their CTAs' first
+    const auto place = [&](int i) {
+        return (((int64_t)(row.x + i) * p.head_blocks + hblk) * 2 + (i == 0 ? 1 : 0)) * p.block_heads + hh;
+    };
+    float acc[16], sum = 0.f, m = -INFINITY;
     bool nan = false;
-    for (int k = k0 + lane; k <= k1; k += 32) {
-        const float x = p.part_lse[slot(k) * heads_of_block + hh];
-        nan |= isnan(x);
-        m = fmaxf(m, x);
+    float4 x[4];
+    const auto load = [&](int i) {
+        const float4* const src = reinterpret_cast<const float4*>(p.part + place(i) * kDv);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = src[k * 32 + lane];
+    };
+    if (w < row.y) load(w);
+    for (int i = lane; i < row.y; i += 32) {
+        const float l = p.part_lse[place(i)];
+        nan |= isnan(l);
+        m = fmaxf(m, l);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (__any_sync(0xffffffffu, nan)) m = __uint_as_float(0x7fffffffu);
-    float acc[16], sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-#pragma unroll 2
-    for (int k = k0 + w; k <= k1; k += kWarps) {
-        const int64_t s = slot(k);
-        const float4* const src = reinterpret_cast<const float4*>(p.part + (s * heads_of_block + hh) * kDv);
-        float4 x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = src[i * 32 + lane];
-        const float f = ex2(p.part_lse[s * heads_of_block + hh] - m);
+#pragma unroll 1
+    for (int i = w; i < row.y; i += kWarps) {
+        const float f = ex2(p.part_lse[place(i)] - m);
         sum += f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            acc[4 * i] = fmaf(f, x[i].x, acc[4 * i]);
-            acc[4 * i + 1] = fmaf(f, x[i].y, acc[4 * i + 1]);
-            acc[4 * i + 2] = fmaf(f, x[i].z, acc[4 * i + 2]);
-            acc[4 * i + 3] = fmaf(f, x[i].w, acc[4 * i + 3]);
+        for (int k = 0; k < 4; ++k) {
+            acc[4 * k] = fmaf(f, x[k].x, acc[4 * k]);
+            acc[4 * k + 1] = fmaf(f, x[k].y, acc[4 * k + 1]);
+            acc[4 * k + 2] = fmaf(f, x[k].z, acc[4 * k + 2]);
+            acc[4 * k + 3] = fmaf(f, x[k].w, acc[4 * k + 3]);
         }
+        if (i + kWarps < row.y) load(i + kWarps);
     }
     if constexpr (kWarps > 1) {
 #pragma unroll
@@ -1205,14 +1250,15 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Decod
         if (lane == 0) sum_s[warp] = sum;
         __syncthreads();  // (the whole CTA is one unit: no thread has left)
         sum = 0.f;
-        for (int v = 0; v < kWarps; ++v) sum += sum_s[v];
-        const float inv = 1.0f / sum;
-        const int d = threadIdx.x * 2;
         float a = 0.f, c = 0.f;
+#pragma unroll
         for (int v = 0; v < kWarps; ++v) {
-            a += acc_s[v][d];
-            c += acc_s[v][d + 1];
+            const float2 y = *reinterpret_cast<const float2*>(&acc_s[v][2 * threadIdx.x]);
+            sum += sum_s[v];
+            a += y.x;
+            c += y.y;
         }
+        const float inv = 1.0f / sum;
         reinterpret_cast<__nv_bfloat162*>(out)[threadIdx.x] = __floats2bfloat162_rn(a * inv, c * inv);
         if (p.lse != nullptr && threadIdx.x == 0) p.lse[unit] = (m + log2f(sum)) * p.lse_scale;
     } else {
@@ -1335,8 +1381,8 @@ cudaError_t launch_decode(const DecodeParams& p, unsigned flags, cudaStream_t st
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
-    return few ? cudaLaunchKernelEx(&cfg, join_kernel<8>, p, (int)kNH)
-               : cudaLaunchKernelEx(&cfg, join_kernel<1>, p, (int)kNH);
+    const JoinParams j = {p.part, p.part_lse, p.row_info, p.out, p.lse, units, p.H, p.head_blocks, kNH, p.lse_scale};
+    return few ? cudaLaunchKernelEx(&cfg, join_kernel<8>, j) : cudaLaunchKernelEx(&cfg, join_kernel<1>, j);
 }
 
 template <int kDk>
@@ -1426,6 +1472,7 @@ extern "C" int dcp_mla_cache8_decode(const void* q, int64_t q_row, int64_t q_hea
     p.q = static_cast<const uint8_t*>(q);
     p.q_row = q_row * 2;
     p.q_head = q_head * 2;
+    p.q_wide = aligned(q, 16) && q_row % 8 == 0 && q_head % 8 == 0;
     p.seq_lens = seq_lens;
     p.part = reinterpret_cast<float*>(w + ws.part);
     p.part_lse = reinterpret_cast<float*>(w + ws.part_lse);
