@@ -372,6 +372,7 @@ struct Shared {  // barriers and small things, behind the scale atom
     uint64_t o_done;          // a tile's values are added
     uint64_t q_full;          // a segment's q is in shared memory
     uint64_t drained;         // every MMA of the CTA is done
+    uint64_t q_asked;         // the first segment's q is on its way
     uint64_t voted[4];        // a group's warps know how far their scores are above the references
     uint64_t met[4];          // a group's warps have come to the same place
     int moved[4][2];          // too far, in the group's even and odd tiles
@@ -544,6 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         if (lane < 24) mbar_init(&sh->info_full[0] + lane, lane == 21 || lane == 22 ? kSoftWarps : 1);
         else if (lane == 24) mbar_init(&sh->q_full, kSoftWarps);
         else if (lane == 25) mbar_init(&sh->drained, 1);
+        else if (lane == 26) mbar_init(&sh->q_asked, kSoftWarps);
         if (lane < 8) mbar_init(&sh->voted[0] + lane, 4);
         if (lane >= 24) (&sh->moved[0][0])[lane - 24] = 0;
         if (lane >= 16 && lane < 24) (&sh->armed[0][0])[lane - 16] = -1;
@@ -565,7 +567,28 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 
     // ---- this CTA's tiles: [g, g_end) of all rows' tiles, from tile `tile` of row `row` (or whole rows)
     int row = range, tile = 0, n_row = 0, g = 0, g_end = 0;
-    if (!p.row_mode && p.B > 32) {
+    if (!p.row_mode && p.B <= 32) {
+        if (warp == kLoadWarp) {  // few rows: a lane a row, beside the others' set-up
+            const int n = lane < p.B ? row_tiles(p, length) : 0;
+            int x = n;
+#pragma unroll 1
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            const int total = __shfl_sync(0xffffffffu, x, 31), pre = x - n;
+            const int per = max((total + p.ranges - 1) / p.ranges, 1);
+            const int64_t lo = (int64_t)range * per, hi = lo + per;
+            g = lo < total ? (int)lo : total;
+            g_end = hi < total ? (int)hi : total;
+            const uint32_t here = __ballot_sync(0xffffffffu, n > 0 && pre <= g && g < pre + n);
+            row = here ? __ffs(here) - 1 : 0;
+            tile = g - __shfl_sync(0xffffffffu, pre, row);
+            n_row = __shfl_sync(0xffffffffu, n, row);
+            length = __shfl_sync(0xffffffffu, length, row);
+            if (hblk == 0 && lane < p.B) tell_row(p, lane, n, pre, g, g_end, per, range);
+        }
+    } else if (!p.row_mode) {
         int total = 0, n_mine = 0, pre_mine = 0, per_cta = 0;
         for (int pass = 0; pass < 2; ++pass) {
             int base = 0;
@@ -615,34 +638,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 
     if (warp == kLoadWarp) {
         // ---- loads (the warp walks together, lane 0 issues)
-        if (!p.row_mode) {
-            if (p.B > 32) {
-                row = p.B;
-                if (g < g_end) {  // (a range of no tiles has found no row)
-                    row = sh->find[0];
-                    tile = sh->find[1];
-                    n_row = sh->find[2];
-                    length = row_length(p, row);
-                }
-            } else {  // few rows: a lane a row
-                const int n = lane < p.B ? row_tiles(p, length) : 0;
-                int x = n;
-#pragma unroll 1
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, x, o);
-                    if (lane >= o) x += y;
-                }
-                const int total = __shfl_sync(0xffffffffu, x, 31), pre = x - n;
-                const int per = max((total + p.ranges - 1) / p.ranges, 1);
-                const int64_t lo = (int64_t)range * per, hi = lo + per;
-                g = lo < total ? (int)lo : total;
-                g_end = hi < total ? (int)hi : total;
-                const uint32_t here = __ballot_sync(0xffffffffu, n > 0 && pre <= g && g < pre + n);
-                row = here ? __ffs(here) - 1 : 0;
-                tile = g - __shfl_sync(0xffffffffu, pre, row);
-                n_row = __shfl_sync(0xffffffffu, n, row);
-                length = __shfl_sync(0xffffffffu, length, row);
-                if (hblk == 0 && lane < p.B) tell_row(p, lane, n, pre, g, g_end, per, range);
+        if (!p.row_mode && p.B > 32) {
+            row = p.B;
+            if (g < g_end) {  // (a range of no tiles has found no row)
+                row = sh->find[0];
+                tile = sh->find[1];
+                n_row = sh->find[2];
+                length = row_length(p, row);
             }
         }
         uint32_t t = 0;
@@ -673,6 +675,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                                            c.j | about | (i == 0 ? kFirst : 0u) | (i == n - 1 ? kLast : 0u), row};
                         mbar_arrive(&sh->info_full[t & 3]);
                     }
+                    // (q is needed first: the first tile's loads stand behind it)
+                    if (t == 0) ok = __all_sync(0xffffffffu, mbar_wait(&sh->q_asked, 0, abort_flag, p.status, p.wait_ns));
+                    if (!ok) break;
 #pragma unroll 1
                     for (int a = 0; a < 4; ++a) {
                         if (t >= 2) ok = mbar_wait(&sh->kv_free[st][a], par, abort_flag, p.status, p.wait_ns);
@@ -879,6 +884,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         bool going = next_segment(true);
         if (going) {
             fetch_q(ti.row);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->q_asked);
             aborted = !split_q();
         }
         while (going) {  // segments
