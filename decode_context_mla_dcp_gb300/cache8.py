@@ -27,6 +27,7 @@ from . import _binding as _b
 _torch = None
 _DTYPES: dict = {}  # torch dtype -> library dtype
 _SMS: dict = {}
+_ROOM: dict = {}  # sizes of a decode -> bytes of workspace
 
 
 def _ready():
@@ -344,7 +345,12 @@ def mla_cache8_decode(q, caches, scales, seq_lens, scale: float, *, block: int =
         raise ValueError("lse must be a contiguous fp32 tensor [B, H] on the caches' device")
     room = None
     if workspace is None:
-        size = lib.dcp_mla_cache8_decode_workspace_bytes(cp, B, H, T, window, sinks, _sms(index))
+        size = _ROOM.get((cp, B, H, T, window, sinks, index))
+        if size is None:
+            if len(_ROOM) > 4096:
+                _ROOM.clear()
+            size = lib.dcp_mla_cache8_decode_workspace_bytes(cp, B, H, T, window, sinks, _sms(index))
+            _ROOM[cp, B, H, T, window, sinks, index] = size
         if size > 0:
             workspace = torch.empty((size,), dtype=torch.uint8, device=q.device)
             room = workspace.data_ptr()

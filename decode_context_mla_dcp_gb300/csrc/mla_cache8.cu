@@ -77,6 +77,15 @@ __device__ __forceinline__ void angle_of(int64_t pos, uint64_t turns, float* c, 
     sincospif((float)(int32_t)(uint32_t)(phase >> 32) * 4.656612873077393e-10f, s, c);  // 2^-31
 }
 
+// The same for values that are then rounded to e4m3: the hardware's sine and
+// cosine, within 2^-21 of the true ones on [-pi, pi], against e4m3's 2^-4.
+__device__ __forceinline__ void coarse_angle_of(int64_t pos, uint64_t turns, float* c, float* s) {
+    const uint64_t phase = (uint64_t)pos * turns;
+    const float x = (float)(int32_t)(uint32_t)(phase >> 32) * 1.4629180792671596e-9f;  // pi 2^-31
+    *s = __sinf(x);
+    *c = __cosf(x);
+}
+
 // ---- rotary positions ------------------------------------------------------------
 
 struct RopeParams {
@@ -331,7 +340,7 @@ __device__ __forceinline__ void turn_token(const AppendParams& p, uint32_t rope,
         t->r1 = get_hi<E>(rope);
         if (rotate) {
             float c, s;
-            angle_of(pos, turns, &c, &s);
+            coarse_angle_of(pos, turns, &c, &s);
             c *= p.mscale;
             s *= p.mscale;
             const float a = t->r0, b = t->r1;
@@ -341,27 +350,29 @@ __device__ __forceinline__ void turn_token(const AppendParams& p, uint32_t rope,
     }
 }
 
-// The largest finite magnitude of a token. `odd`: it has NaNs or infinities, found
-// out cheaply (a maximum that is no finite number, or a NaN among the rotated),
-// and its values are then looked at one by one.
+// A lane's largest magnitude of a token, cheaply: packed maxima, in which a NaN
+// loses to a number. Where that or a rotated value is no finite number (`odd`) the
+// warp looks at its tokens again one value at a time.
 template <class E>
-__device__ __forceinline__ float token_peak(const Token& t, bool* odd) {
+__device__ __forceinline__ float lane_top(const Token& t, bool* odd) {
     const uint32_t w[8] = {t.v[0].x, t.v[0].y, t.v[0].z, t.v[0].w, t.v[1].x, t.v[1].y, t.v[1].z, t.v[1].w};
     uint32_t m = E::top2(w[0], w[1]);
 #pragma unroll
     for (int i = 2; i < 8; ++i) m = E::top2(m, w[i]);
-    float a = fmaxf(fmaxf(get_lo<E>(m), get_hi<E>(m)), fmaxf(fabsf(t.r0), fabsf(t.r1)));
-    *odd = __any_sync(0xffffffffu, !finite(a) || !finite(t.r0) || !finite(t.r1));
-    if (*odd) {
-        a = fmaxf(mag(t.r0), mag(t.r1));
-#pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-            const uint4 v = i < 4 ? t.v[0] : t.v[1];
-            const uint32_t x = (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
-            a = fmaxf(a, fmaxf(mag(get_lo<E>(x)), mag(get_hi<E>(x))));
-        }
-    }
-    // (magnitudes: their bits order like integers)
+    const float a = fmaxf(fmaxf(get_lo<E>(m), get_hi<E>(m)), fmaxf(fabsf(t.r0), fabsf(t.r1)));
+    *odd |= !finite(a) || !finite(t.r0 + t.r1);
+    return a;
+}
+template <class E>
+__device__ __forceinline__ float lane_finite_top(const Token& t) {
+    const uint32_t w[8] = {t.v[0].x, t.v[0].y, t.v[0].z, t.v[0].w, t.v[1].x, t.v[1].y, t.v[1].z, t.v[1].w};
+    float a = fmaxf(mag(t.r0), mag(t.r1));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = fmaxf(a, fmaxf(mag(get_lo<E>(w[i])), mag(get_hi<E>(w[i]))));
+    return a;
+}
+// (magnitudes: their bits order like integers)
+__device__ __forceinline__ float warp_top(float a) {
     return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
 }
 
@@ -396,7 +407,7 @@ __device__ __forceinline__ void store_token(const AppendParams& p, const Token& 
 struct Place {
     int row, shard;
     uint32_t first, count, len;  // the row's first packed token, its new tokens, its length before
-    uint32_t pos, loc;
+    uint32_t pos, loc, end;      // its position; its token of the shard; the shard's tokens after the call
 };
 __device__ __forceinline__ bool place_of(const AppendParams& p, const int32_t* cu, int64_t n, Place* w) {
     if (p.cu != nullptr) {
@@ -441,58 +452,152 @@ __global__ void __launch_bounds__(128) append_token_kernel(const __grid_constant
     uint8_t* const kv = p.kv[w.shard];
     if (kv == nullptr) return;
     turn_token<E>(p, rope, rotate, turns_of(f), (int64_t)w.pos, &t);
-    bool odd;
-    const int k = scale_exp(token_peak<E>(t, &odd));
+    bool odd = false;
+    float top = lane_top<E>(t, &odd);
+    odd = __any_sync(0xffffffffu, odd);
+    if (odd) top = lane_finite_top<E>(t);
+    const int k = scale_exp(warp_top(top));
     const int64_t at = (int64_t)w.row * p.T + w.loc;
     store_token<E>(p, t, odd, kv + at * p.Dk, lane, pow2(-k));
     if (lane == 0) p.scales[w.shard][at] = pow2(k);
 }
 
-// Blocks of tokens. The first new token of a block (of a row, on a shard) stands
-// for it; the CTA that looks at that token writes the whole block: the block's
-// new tokens in registers (kTok a warp, every load in flight at once), their
-// peak, the scale, the tokens that the block held before if the scale grows, and
-// the new codes. A CTA has as many warps as a block needs, so that small blocks
-// take small CTAs and all CTAs of a call are resident at once. CTA c looks at
-// tokens c, c + G, c + 2G, ... with G odd, so that first tokens, which stand a
-// power of two apart, spread over all CTAs.
+// Blocks of tokens. A CTA writes whole blocks: a block's new tokens in registers
+// (kTok a warp, every load in flight at once), their peak, the scale, the tokens
+// that the block held before if the scale grows, and the new codes. A CTA has as
+// many warps as a block needs, so that small blocks take small CTAs and all CTAs
+// of a call are resident at once.
+//
+// Which blocks. kCounted: CTA u takes block u of all rows' and shards' blocks in
+// order; the CTA's warps count the blocks of 32 (row, shard) pairs each, and then
+// every warp looks through the 32 that hold block u. That spreads any mix of rows
+// evenly and costs two round trips, but goes over all pairs: it is for up to
+// kCountedPairs. Beyond, the first new token of a block (of a row, on a shard)
+// stands for it: CTA c looks at tokens c, c + G, c + 2G, ... (a binary search
+// each) with G odd, so that first tokens, which stand a power of two apart, spread
+// over the CTAs. (16385 tokens of 5 rows in blocks of 64: 15.4 us by first tokens,
+// whose 257 blocks fall on 159 CTAs, up to three on one.)
 constexpr int kTok = 4;
 constexpr int kCuShared = 1024;
+constexpr int kCountedPairs = 256;
 
-template <class E, int kWarps>
+// Blocks of pair e = row * cp + shard that have new tokens, from block `b0` on.
+struct Pair {
+    int row, shard;
+    uint32_t first, len, before, after;
+    int blocks;
+};
+__device__ __forceinline__ Pair pair_of(const AppendParams& p, int e) {
+    Pair r;
+    r.row = (int)((uint32_t)e / p.cp);
+    r.shard = e - r.row * (int)p.cp;
+    r.blocks = 0;
+    if (r.row >= p.B || p.kv[r.shard] == nullptr) return r;
+    int64_t first = (int64_t)r.row * p.even, last = first + p.even;
+    if (p.cu != nullptr) {
+        first = p.cu[r.row];
+        last = p.cu[r.row + 1];
+    }
+    if (last > p.N) last = p.N;
+    if (first < 0 || last <= first) return r;
+    const int32_t len = p.seq_lens[r.row];
+    r.first = (uint32_t)first;
+    r.len = len < 0 ? 0u : (uint32_t)len;
+    r.before = held_tokens(r.len, r.shard, p.cp, p.interleave);
+    r.after = held_tokens(r.len + (uint32_t)(last - first), r.shard, p.cp, p.interleave);
+    if ((int64_t)r.after > p.T) r.after = (uint32_t)p.T;
+    if (r.after > r.before) r.blocks = (int)(((r.after - 1) >> p.block_log2) - (r.before >> p.block_log2)) + 1;
+    return r;
+}
+// Inclusive sum over the warp's lanes.
+__device__ __forceinline__ int lane_sums(int x, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+
+template <class E, int kWarps, bool kCounted>
 __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) append_block_kernel(const __grid_constant__ AppendParams p) {
-    __shared__ int32_t cu_s[kCuShared + 1];
-    __shared__ Place list[32 * kWarps];
+    __shared__ int32_t cu_s[kCounted ? kCountedPairs / 32 : kCuShared + 1];
+    __shared__ Place list[kCounted ? 1 : 32 * kWarps];
     __shared__ int found;
     __shared__ float peak_s[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int32_t* cu = p.cu;
-    if (tid == 0) found = 0;
-    if (cu != nullptr && p.B <= kCuShared) {
-        for (int i = tid; i <= p.B; i += 32 * kWarps) cu_s[i] = cu[i];
-        cu = cu_s;
-    }
     const bool rotate = p.inv_freq != nullptr;
     const double freq = rotate ? p.inv_freq[lane] : 0.0;
     const uint32_t block = 1u << p.block_log2;
-    for (int64_t base = blockIdx.x; base < p.N; base += (int64_t)gridDim.x * (32 * kWarps)) {
-        __syncthreads();
-        const int64_t n = base + (int64_t)tid * gridDim.x;
-        Place w;
-        if (n < p.N && place_of(p, cu, n, &w) && (int64_t)w.loc < p.T && p.kv[w.shard] != nullptr) {
-            const uint32_t held = held_tokens(w.len, w.shard, p.cp, p.interleave);
-            if (w.loc == held || (w.loc & (block - 1)) == 0) list[atomicAdd(&found, 1)] = w;
+    const int32_t* cu = p.cu;
+    if constexpr (!kCounted) {
+        if (tid == 0) found = 0;
+        if (cu != nullptr && p.B <= kCuShared) {
+            for (int i = tid; i <= p.B; i += 32 * kWarps) cu_s[i] = cu[i];
+            cu = cu_s;
         }
-        __syncthreads();
-        const int nfound = found;
+    }
+    for (int64_t base = blockIdx.x; base < p.N; base += (int64_t)gridDim.x * (kCounted ? 1 : 32 * kWarps)) {
+        Place w;
+        int nfound = 1;
+        if constexpr (kCounted) {
+            const int pairs = p.B * (int)p.cp, chunks = (pairs + 31) / 32;
+            int u = (int)base, chunk = 0;
+            if (chunks > 1) {
+                for (int c = warp; c < chunks; c += kWarps) {
+                    const int n = __reduce_add_sync(0xffffffffu, pair_of(p, c * 32 + lane).blocks);
+                    if (lane == 0) cu_s[c] = n;
+                }
+                __syncthreads();
+                chunk = chunks;
+                for (int c0 = 0; c0 < chunks; c0 += 32) {
+                    const int n = c0 + lane < chunks ? cu_s[c0 + lane] : 0, sum = lane_sums(n, lane);
+                    const uint32_t past = __ballot_sync(0xffffffffu, sum > u);
+                    if (past) {
+                        const int l = __ffs(past) - 1;
+                        chunk = c0 + l;
+                        u -= __shfl_sync(0xffffffffu, sum - n, l);
+                        break;
+                    }
+                    u -= __shfl_sync(0xffffffffu, sum, 31);
+                }
+                if (chunk == chunks) return;
+            }
+            const Pair r = pair_of(p, chunk * 32 + lane);
+            const int sum = lane_sums(r.blocks, lane);
+            const uint32_t past = __ballot_sync(0xffffffffu, sum > u);
+            if (!past) return;
+            const int l = __ffs(past) - 1;
+            u -= __shfl_sync(0xffffffffu, sum - r.blocks, l);
+            w.row = __shfl_sync(0xffffffffu, r.row, l);
+            w.shard = __shfl_sync(0xffffffffu, r.shard, l);
+            w.first = __shfl_sync(0xffffffffu, r.first, l);
+            w.len = __shfl_sync(0xffffffffu, r.len, l);
+            w.end = __shfl_sync(0xffffffffu, r.after, l);
+            const uint32_t before = __shfl_sync(0xffffffffu, r.before, l);
+            w.loc = ((before >> p.block_log2) + (uint32_t)u) << p.block_log2;
+            if (w.loc < before) w.loc = before;
+            if (u < 0 || w.loc >= w.end) return;  // (only with offsets that are not in order)
+        } else {
+            __syncthreads();
+            const int64_t n = base + (int64_t)tid * gridDim.x;
+            if (n < p.N && place_of(p, cu, n, &w) && (int64_t)w.loc < p.T && p.kv[w.shard] != nullptr) {
+                const uint32_t held = held_tokens(w.len, w.shard, p.cp, p.interleave);
+                if (w.loc == held || (w.loc & (block - 1)) == 0) {
+                    w.end = held_tokens(w.len + w.count, w.shard, p.cp, p.interleave);
+                    if ((int64_t)w.end > p.T) w.end = (uint32_t)p.T;
+                    list[atomicAdd(&found, 1)] = w;
+                }
+            }
+            __syncthreads();
+            nfound = found;
+        }
         for (int i = 0; i < nfound; ++i) {  // (in any order: blocks are independent of each other)
-            w = list[i];
+            if constexpr (!kCounted) w = list[i];
             uint8_t* const kv = p.kv[w.shard] + (int64_t)w.row * p.T * p.Dk;
             float* const scale = p.scales[w.shard] + (int64_t)w.row * p.blocks + (w.loc >> p.block_log2);
             const uint32_t b0 = w.loc & ~(block - 1);
-            uint32_t end = held_tokens(w.len + w.count, w.shard, p.cp, p.interleave);
-            if (end > b0 + block) end = b0 + block;
-            if ((int64_t)end > p.T) end = (uint32_t)p.T;
+            const uint32_t end = w.end < b0 + block ? w.end : b0 + block;
             Token t[kTok];
             uint32_t rope[kTok], pos[kTok];
 #pragma unroll
@@ -507,18 +612,24 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) append_block_kernel(
             const float old = b0 < w.loc ? *scale : 0.f;  // the present scale counts where the block holds tokens
             const uint64_t turns = turns_of(freq);
             float peak = 0.f;
-            bool odd[kTok];
+            bool odd = false;
 #pragma unroll
             for (int k = 0; k < kTok; ++k)
                 if (w.loc + warp + k * kWarps < end) {
                     turn_token<E>(p, rope[k], rotate, turns, (int64_t)pos[k], &t[k]);
-                    peak = fmaxf(peak, token_peak<E>(t[k], &odd[k]));
+                    peak = fmaxf(peak, lane_top<E>(t[k], &odd));
                 }
+            odd = __any_sync(0xffffffffu, odd);
+            if (odd) {
+                peak = 0.f;
+#pragma unroll
+                for (int k = 0; k < kTok; ++k)
+                    if (w.loc + warp + k * kWarps < end) peak = fmaxf(peak, lane_finite_top<E>(t[k]));
+            }
+            peak = warp_top(peak);
             if (lane == 0) peak_s[warp] = peak;
             __syncthreads();
-            peak = peak_s[lane & (kWarps - 1)];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, o));
+            peak = warp_top(peak_s[lane & (kWarps - 1)]);
             const int e = scale_exp(peak);
             float s = pow2(e);
             if (old > s) s = old;
@@ -526,7 +637,7 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) append_block_kernel(
 #pragma unroll
             for (int k = 0; k < kTok; ++k) {
                 const uint32_t loc = w.loc + warp + k * kWarps;
-                if (loc < end) store_token<E>(p, t[k], odd[k], kv + (int64_t)loc * p.Dk, lane, inv);
+                if (loc < end) store_token<E>(p, t[k], odd, kv + (int64_t)loc * p.Dk, lane, inv);
             }
             if (b0 < w.loc && s > old) {  // requantise what the block held
                 const float ratio = old / s;
@@ -542,7 +653,7 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) append_block_kernel(
             if (tid == 0) *scale = s;
             __syncthreads();  // peak_s is used again
         }
-        if (tid == 0) found = 0;
+        if (!kCounted && tid == 0) found = 0;
     }
 }
 
@@ -717,12 +828,22 @@ int launch_append(const AppendParams& p, int block, cudaStream_t st) {
         append_token_kernel<E><<<(unsigned)((p.N + 3) / 4), 128, 0, st>>>(p);
         return launched();
     }
+    const int64_t pairs = (int64_t)p.B * p.cp;
+    if (pairs <= kCountedPairs) {  // at most two blocks of a pair are not full of new tokens
+        const int64_t most = p.N / block + 2 * pairs;
+        const unsigned grid = (unsigned)(p.N < most ? p.N : most);
+        if (block <= 16) append_block_kernel<E, 4, true><<<grid, 128, 0, st>>>(p);
+        else if (block == 32) append_block_kernel<E, 8, true><<<grid, 256, 0, st>>>(p);
+        else if (block == 64) append_block_kernel<E, 16, true><<<grid, 512, 0, st>>>(p);
+        else append_block_kernel<E, 32, true><<<grid, 1024, 0, st>>>(p);
+        return launched();
+    }
     // about as many CTAs as are resident at once (32 warps a multiprocessor), an odd number
     const auto grid = [&](int64_t most) { return (unsigned)(p.N < most ? p.N : most); };
-    if (block <= 16) append_block_kernel<E, 4><<<grid(1217), 128, 0, st>>>(p);
-    else if (block == 32) append_block_kernel<E, 8><<<grid(609), 256, 0, st>>>(p);
-    else if (block == 64) append_block_kernel<E, 16><<<grid(305), 512, 0, st>>>(p);
-    else append_block_kernel<E, 32><<<grid(153), 1024, 0, st>>>(p);
+    if (block <= 16) append_block_kernel<E, 4, false><<<grid(1217), 128, 0, st>>>(p);
+    else if (block == 32) append_block_kernel<E, 8, false><<<grid(609), 256, 0, st>>>(p);
+    else if (block == 64) append_block_kernel<E, 16, false><<<grid(305), 512, 0, st>>>(p);
+    else append_block_kernel<E, 32, false><<<grid(153), 1024, 0, st>>>(p);
     return launched();
 }
 

@@ -276,28 +276,34 @@ def test_append_skips_shards_that_are_not_held(block):
         assert torch.equal(bits(part[j]), bits(full[j])) and torch.equal(sp[j], sf[j])
 
 
-def test_append_many_rows_and_a_broken_cu():
-    """More rows than the shared copy of cu holds; and offsets that a caller got wrong write nothing out of place."""
+@pytest.mark.parametrize("B,cp,T", [(1500, 1, 8), (100, 2, 8), (100, 3, 8), (9, 1, 8)])
+def test_append_many_rows_and_a_broken_cu(B, cp, T):
+    """More rows than the shared copy of cu holds, and few; and offsets that a caller got wrong write nothing out of
+    place."""
     g = gen(9)
-    B, T, block = 1500, 8, 4
+    block = 4
     counts = [(i * 7) % 3 for i in range(B)]
     n = sum(counts)
     latent = randn(g, n, 512).bfloat16()
-    kv, sc = blank(1, B, T, 512, block)
-    values, scales = [kv[0].double()], [sc[0].double()]
+    kv, sc = blank(cp, B, T, 512, block)
+    values, scales = [x.double() for x in kv], [x.double() for x in sc]
     starts = [i % 5 for i in range(B)]
     cu = torch.tensor([0] + counts, device=DEV).cumsum(0).int()
     dcp.mla_cache8_append(latent, None, kv, sc, torch.tensor(starts, device=DEV, dtype=torch.int32), cu_new=cu,
                           block=block)
-    ref.append(latent.double(), counts, starts, values, scales, 1, 1, block)
-    assert torch.equal(kv[0].double(), values[0]) and torch.equal(sc[0].double(), scales[0])
-    before = bits(kv[0]).clone()
-    for blk, scale in ((4, sc), (1, [torch.ones((B, T), device=DEV)])):
-        dcp.mla_cache8_append(latent, None, kv, scale, torch.full((B,), T, device=DEV, dtype=torch.int32), cu_new=cu,
-                              block=blk)
+    ref.append(latent.double(), counts, starts, values, scales, cp, 1, block)
+    for j in range(cp):
+        assert torch.equal(kv[j].double(), values[j]) and torch.equal(sc[j].double(), scales[j])
+    before = [bits(x).clone() for x in kv]
+    for blk, scale in ((4, sc), (1, [torch.ones((B, T), device=DEV) for _ in range(cp)])):
+        dcp.mla_cache8_append(latent, None, kv, scale, torch.full((B,), T * cp, device=DEV, dtype=torch.int32),
+                              cu_new=cu, block=blk)
         dcp.mla_cache8_append(latent, None, kv, scale, torch.full((B,), -3 - T, device=DEV, dtype=torch.int32),
                               cu_new=torch.full((B + 1,), n + 5, device=DEV, dtype=torch.int32), block=blk)
-    assert torch.equal(bits(kv[0]), before)
+        dcp.mla_cache8_append(latent, None, kv, scale, torch.full((B,), T * cp, device=DEV, dtype=torch.int32),
+                              cu_new=torch.arange(B + 1, device=DEV, dtype=torch.int32).flip(0) - 3, block=blk)
+    for j in range(cp):
+        assert torch.equal(bits(kv[j]), before[j])
 
 
 # ---- read-back --------------------------------------------------------------------
