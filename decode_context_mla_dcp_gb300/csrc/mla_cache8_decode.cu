@@ -54,10 +54,10 @@ constexpr long long kWaitLimitNs = 2000000000LL;  // every wait gives up after t
 constexpr int kFar = 1 << 28;              // beyond every exponent
 constexpr int kLazy = 32;                  // how far an exponent may pass the reference
 
-struct DecodeParams {
-    CUtensorMap tm_latent[kCpMax];         // boxes of 128 dims x 128 tokens, 128-byte swizzle
-    CUtensorMap tm_rope[kCpMax];           // boxes of 64 dims x 128 tokens, 64-byte swizzle
-    const float* scales[kCpMax];
+// The kernel's parameters but for what there is one of per shard. Those come in
+// room for 1, 4 or 16 shards: a launch copies its parameters, and with one shard
+// the compiler drops the arithmetic of several.
+struct DecodeBase {
     const uint8_t* q;
     int64_t q_row, q_head;                 // bytes
     int q_wide;                            // q can be read 16 bytes at a time
@@ -77,6 +77,13 @@ struct DecodeParams {
     float scale_log2;
     float lse_scale;                       // ln 2 for a natural-log LSE, 1 for base 2
     long long wait_ns;
+};
+template <int kShards>
+struct DecodeParams : DecodeBase {
+    CUtensorMap tm_latent[kShards];        // boxes of 128 dims x 128 tokens, 128-byte swizzle
+    CUtensorMap tm_rope[kShards];          // boxes of 64 dims x 128 tokens, 64-byte swizzle
+    const float* scales[kShards];
+    __device__ __forceinline__ uint32_t shards() const { return kShards == 1 ? 1u : cp; }
 };
 
 // ---- PTX helpers -------------------------------------------------------------
@@ -234,14 +241,16 @@ __device__ __forceinline__ float ex2(float x) {
 struct Prefix {
     uint32_t q, r;
 };
-__device__ __forceinline__ Prefix prefix_of(const DecodeParams& p, uint32_t L) {
-    if (p.cp == 1) return {0u, L};
-    const uint32_t round = p.cp * p.interleave, q = L / round;
+template <class P>
+__device__ __forceinline__ Prefix prefix_of(const P& p, uint32_t L) {
+    if (p.shards() == 1) return {0u, L};
+    const uint32_t round = p.shards() * p.interleave, q = L / round;
     return {q, L - q * round};
 }
-__device__ __forceinline__ uint32_t share(const DecodeParams& p, Prefix x, uint32_t j) {
+template <class P>
+__device__ __forceinline__ uint32_t share(const P& p, Prefix x, uint32_t j) {
     uint32_t n = x.r;
-    if (p.cp > 1) {
+    if (p.shards() > 1) {
         const uint32_t lo = j * p.interleave;
         n = x.r > lo ? x.r - lo : 0u;
         n = x.q * p.interleave + (n < p.interleave ? n : p.interleave);
@@ -251,11 +260,12 @@ __device__ __forceinline__ uint32_t share(const DecodeParams& p, Prefix x, uint3
 struct RowView {
     Prefix len, win, sink;
 };
-__device__ __forceinline__ uint32_t row_length(const DecodeParams& p, int b) {
+__device__ __forceinline__ uint32_t row_length(const DecodeBase& p, int b) {
     const int n = p.seq_lens[b];
     return n < 0 ? 0u : (uint32_t)n;
 }
-__device__ __forceinline__ RowView row_view(const DecodeParams& p, uint32_t L) {
+template <class P>
+__device__ __forceinline__ RowView row_view(const P& p, uint32_t L) {
     const uint32_t w = p.window > 0 && L > p.window ? L - p.window : 0u;
     RowView v;
     v.len = prefix_of(p, L);
@@ -268,7 +278,8 @@ struct ShardView {
     uint32_t first, start, end;
     int tiles_first, tiles;
 };
-__device__ __forceinline__ ShardView shard_view(const DecodeParams& p, const RowView& v, uint32_t j) {
+template <class P>
+__device__ __forceinline__ ShardView shard_view(const P& p, const RowView& v, uint32_t j) {
     ShardView s = {0u, 0u, 0u, 0, 0};
     if (!((p.held >> j) & 1u)) return s;
     s.end = share(p, v.len, j);
@@ -281,11 +292,12 @@ __device__ __forceinline__ ShardView shard_view(const DecodeParams& p, const Row
     s.tiles = s.tiles_first + (int)((s.end - s.start + kTile - 1) / kTile);
     return s;
 }
-__device__ __forceinline__ int row_tiles(const DecodeParams& p, uint32_t L) {
+template <class P>
+__device__ __forceinline__ int row_tiles(const P& p, uint32_t L) {
     const RowView v = row_view(p, L);
     int n = 0;
 #pragma unroll 1
-    for (uint32_t j = 0; j < p.cp; ++j) n += shard_view(p, v, j).tiles;
+    for (uint32_t j = 0; j < p.shards(); ++j) n += shard_view(p, v, j).tiles;
     return n;
 }
 // Walks a row's tiles over the shards.
@@ -294,20 +306,23 @@ struct Cursor {
     ShardView s;
     uint32_t j;
     int i;  // tile of the shard
-    __device__ __forceinline__ void seek(const DecodeParams& p, uint32_t L, int tile) {
+    template <class P>
+__device__ __forceinline__ void seek(const P& p, uint32_t L, int tile) {
         row = row_view(p, L);
         j = 0;
         s = shard_view(p, row, 0);
         i = tile;
         settle(p);
     }
-    __device__ __forceinline__ void settle(const DecodeParams& p) {
-        while (i >= s.tiles && j + 1 < p.cp) {
+    template <class P>
+__device__ __forceinline__ void settle(const P& p) {
+        while (i >= s.tiles && j + 1 < p.shards()) {
             i -= s.tiles;
             s = shard_view(p, row, ++j);
         }
     }
-    __device__ __forceinline__ void next(const DecodeParams& p) {
+    template <class P>
+__device__ __forceinline__ void next(const P& p) {
         ++i;
         settle(p);
     }
@@ -322,7 +337,7 @@ struct Cursor {
 
 // What the join needs of a row: its first CTA range and its number of segments. Written by the CTA that has the
 // row's first tile; for a row without a tile by the first CTA.
-__device__ __forceinline__ void tell_row(const DecodeParams& p, int b, int n, int pre, int g, int g_end, int per,
+__device__ __forceinline__ void tell_row(const DecodeBase& p, int b, int n, int pre, int g, int g_end, int per,
                                          int range) {
     if (n == 0 && range == 0) p.row_info[b] = make_int2(0, 0);
     else if (n > 0 && pre >= g && pre < g_end) p.row_info[b] = make_int2(range, (pre + n - 1) / per - range + 1);
@@ -515,8 +530,8 @@ __device__ __forceinline__ void issue_values(uint32_t ka, uint32_t pa, uint32_t 
 // issues the MMAs: whichever is ready first, the next tile's scores or this
 // tile's values, so that scores and softmax of one tile run beside the values of
 // another.
-template <int kDk, int kNH>
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ DecodeParams p) {
+template <int kDk, int kNH, int kShards>
+__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ DecodeParams<kShards> p) {
     using S = Shape<kDk, kNH>;
     constexpr int kHW = S::kHW;
     constexpr uint32_t kIdS = (1u << 4) | ((uint32_t)(S::kRows >> 3) << 17) | (8u << 24);
@@ -1201,6 +1216,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinP
     const int b = (int)(unit / p.H), h = (int)(unit - (int64_t)b * p.H);
     const int hblk = h / p.block_heads, hh = h - hblk * p.block_heads, w = warp % kWarps;
     pdl_wait();
+    pdl_launch_dependents();
     if (unit >= p.units) return;
     const int2 row = p.row_info[b];
     if (row.y == 1) return;
@@ -1356,15 +1372,15 @@ int multiprocessors() {
     return n;
 }
 
-template <int kDk, int kNH>
-cudaError_t launch_decode(const DecodeParams& p, unsigned flags, cudaStream_t st) {
+template <int kDk, int kNH, int kShards>
+cudaError_t launch_decode(const DecodeParams<kShards>& p, unsigned flags, cudaStream_t st) {
     constexpr int bytes = Shape<kDk, kNH>::kSmem;
     static int configured[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE)) {
-        e = cudaFuncSetAttribute(decode_kernel<kDk, kNH>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        e = cudaFuncSetAttribute(decode_kernel<kDk, kNH, kShards>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
     }
@@ -1378,7 +1394,7 @@ cudaError_t launch_decode(const DecodeParams& p, unsigned flags, cudaStream_t st
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = (flags & DCP_FLAG_PDL) ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, decode_kernel<kDk, kNH>, p);
+    e = cudaLaunchKernelEx(&cfg, decode_kernel<kDk, kNH, kShards>, p);
     if (e != cudaSuccess || p.row_mode) return e;
     // the join overlaps its launch with the decode's tail and waits for it on the device
     const int64_t units = (int64_t)p.B * p.H;
@@ -1392,12 +1408,30 @@ cudaError_t launch_decode(const DecodeParams& p, unsigned flags, cudaStream_t st
     return few ? cudaLaunchKernelEx(&cfg, join_kernel<8>, j) : cudaLaunchKernelEx(&cfg, join_kernel<1>, j);
 }
 
-template <int kDk>
-cudaError_t launch_decode_dk(const DecodeParams& p, unsigned flags, cudaStream_t st) {
-    const int nh = head_block(p.H);
-    if (nh == 16) return launch_decode<kDk, 16>(p, flags, st);
-    if (nh == 32) return launch_decode<kDk, 32>(p, flags, st);
-    return launch_decode<kDk, 64>(p, flags, st);
+// Encode the shards' tensor maps and launch. Returns the call's status.
+template <int kShards>
+int run_decode(const DecodeBase& base, const void* const* kv, const float* const* scales, int Dk, unsigned flags,
+               cudaStream_t st) {
+    DecodeParams<kShards> p;
+    static_cast<DecodeBase&>(p) = base;
+    for (uint32_t j = 0; j < (uint32_t)kShards; ++j) {
+        p.scales[j] = j < base.cp ? scales[j] : nullptr;
+        if (!((base.held >> j) & 1u)) continue;
+        if (!encode_cache(&p.tm_latent[j], kv[j], Dk, base.T, base.B, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            (Dk > kDv && !encode_cache(&p.tm_rope[j], kv[j], Dk, base.T, base.B, 64, CU_TENSOR_MAP_SWIZZLE_64B)))
+            return DCP_MLA_CACHE8_ERR_TENSOR_MAP;
+    }
+    const int nh = head_block(base.H);
+    cudaError_t e;
+    if (Dk > kDv) {
+        e = nh == 16 ? launch_decode<576, 16>(p, flags, st)
+                     : (nh == 32 ? launch_decode<576, 32>(p, flags, st) : launch_decode<576, 64>(p, flags, st));
+    } else {
+        e = nh == 16 ? launch_decode<512, 16>(p, flags, st)
+                     : (nh == 32 ? launch_decode<512, 32>(p, flags, st) : launch_decode<512, 64>(p, flags, st));
+    }
+    if (e != cudaSuccess) (void)cudaGetLastError();
+    return (int)e;
 }
 
 }  // namespace
@@ -1441,7 +1475,7 @@ extern "C" int dcp_mla_cache8_decode(const void* q, int64_t q_row, int64_t q_hea
     if (!aligned(q, 4) || q_row % 2 != 0 || q_head % 2 != 0 || !aligned(out, 16) || !aligned(lse, 4) ||
         !aligned(seq_lens, 4) || !aligned(status, 4))
         return DCP_MLA_CACHE8_ERR_MISALIGNED;
-    DecodeParams p;
+    DecodeBase p;
     int some = -1;
     p.held = 0;
     for (int j = 0; j < cp; ++j) {
@@ -1467,14 +1501,6 @@ extern "C" int dcp_mla_cache8_decode(const void* q, int64_t q_row, int64_t q_hea
     if (!p.row_mode && (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < ws.bytes))
         return DCP_MLA_CACHE8_ERR_WORKSPACE;
     if (T == 0) p.held = 0;  // nothing is cached: every row is empty
-    for (int j = 0; j < kCpMax; ++j) {
-        p.scales[j] = j < cp ? scale_ptrs[j] : nullptr;
-        if (T > 0 && j < cp && kv_ptrs[j] != nullptr) {
-            if (!encode_cache(&p.tm_latent[j], kv_ptrs[j], Dk, T, B, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-                (Dk > kDv && !encode_cache(&p.tm_rope[j], kv_ptrs[j], Dk, T, B, 64, CU_TENSOR_MAP_SWIZZLE_64B)))
-                return DCP_MLA_CACHE8_ERR_TENSOR_MAP;
-        }
-    }
     uint8_t* const w = static_cast<uint8_t*>(workspace);
     p.q = static_cast<const uint8_t*>(q);
     p.q_row = q_row * 2;
@@ -1503,10 +1529,7 @@ extern "C" int dcp_mla_cache8_decode(const void* q, int64_t q_row, int64_t q_hea
     p.wait_ns = kWaitLimitNs;
     if (p.row_mode && p.ranges > B) p.ranges = (int)B;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = Dk == 576 ? launch_decode_dk<576>(p, flags, st) : launch_decode_dk<512>(p, flags, st);
-    if (e != cudaSuccess) {
-        (void)cudaGetLastError();
-        return (int)e;
-    }
-    return 0;
+    if (cp == 1) return run_decode<1>(p, kv_ptrs, scale_ptrs, Dk, flags, st);
+    if (cp <= 4) return run_decode<4>(p, kv_ptrs, scale_ptrs, Dk, flags, st);
+    return run_decode<kCpMax>(p, kv_ptrs, scale_ptrs, Dk, flags, st);
 }
