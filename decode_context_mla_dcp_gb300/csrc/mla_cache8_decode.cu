@@ -51,8 +51,8 @@ constexpr int kThreads = kSoftThreads + 64;
 constexpr int kCpMax = DCP_MLA_CACHE8_CP_MAX;
 constexpr int64_t kMaxInterleave = 1 << 24;
 constexpr long long kWaitLimitNs = 2000000000LL;  // every wait gives up after this
-constexpr int kFar = 1 << 28;              // beyond every exponent
 constexpr int kLazy = 32;                  // how far an exponent may pass the reference
+constexpr int kLow = 60;                   // how far below it a segment's first ones may lie
 
 // The kernel's parameters but for what there is one of per shard. Those come in
 // room for 1, 4 or 16 shards: a launch copies its parameters, and with one shard
@@ -406,6 +406,9 @@ static_assert(sizeof(Shared) <= 512 && offsetof(Shared, s_full) == 160, "");
 constexpr float kMagic = 12582912.f;
 constexpr int kMagicBits = 0x4B400000;
 constexpr int kRange = 1 << 21;  // scores beyond this (base-2 units) give NaN
+constexpr int kBias = 127 - 8;   // P is 2^8 at the block's largest
+// 2^(d - 8), 0 below 2^-127 (d is at most kLazy, or what it gives is not used)
+__device__ __forceinline__ float scale_of(int d) { return __int_as_float(max(d + kBias, 0) << 23); }
 
 using f32x2 = unsigned long long;
 __device__ __forceinline__ f32x2 pack2(float a, float b) {
@@ -882,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     *reinterpret_cast<uint16_t*>(ar + kNH * 64) = (uint16_t)lo[8];
                 }
             }
-            if (lane < kPer) m_s[hq + lane] = kMagicBits - kFar;
+            if (lane < kPer) m_s[hq + lane] = kMagicBits;
             async_fence();
             const bool ok = meet();  // (the group's warps use each other's heads)
             if (lane == 0) mbar_arrive(&sh->q_full);
@@ -1001,21 +1004,25 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                         wl[h / 4 + w] = __byte_perm(vl, __shfl_xor_sync(0xffffffffu, vl, 2), sel2);
                     }
                 }
-                // Did the reference of some head fall behind? Each warp says so now and hears the others below. The
-                // scales 2^(E - M - 8) and P's share of the sums take the present reference: if it moves by `up`,
-                // everything is multiplied by 2^-up.
+                // Does the reference of some head have to move? Up when a score passes it by 2^kLazy; down only at
+                // once, when a segment's first scores lie far below the 0 that it begins at (sums would lose
+                // themselves below fp32's range). Each warp says so now and hears the others below. The scales
+                // 2^(E - M - 8) and P's share of the sums take the present reference: if it moves by `up`, everything
+                // is multiplied by 2^-up.
+                bool move = far > kLazy;
+                if (first && quad * 32 < valid) {
+#pragma unroll
+                    for (int h = 0; h < kHW; ++h) move |= d[h] < -kLow;
+                }
                 if (lane == 0) {
-                    if (far > kLazy) sh->moved[group][t & 1] = 1;
+                    if (move) sh->moved[group][t & 1] = 1;
                     mbar_arrive(&sh->voted[group]);
                 }
                 int* const mine = red_i + quad * kNH + hb;  // this warp's words
 #pragma unroll
-                for (int h = 0; h < kHW; h += 2) {
-                    d[h] = max(d[h] + 119, 0);
-                    d[h + 1] = max(d[h + 1] + 119, 0);
-                    l2[h / 2] = fma2(mul2(pack2(sv[h], sv[h + 1]), ru2),
-                                     pack2(__int_as_float(d[h] << 23), __int_as_float(d[h + 1] << 23)), l2[h / 2]);
-                }
+                for (int h = 0; h < kHW; h += 2)
+                    l2[h / 2] = fma2(mul2(pack2(sv[h], sv[h + 1]), ru2), pack2(scale_of(d[h]), scale_of(d[h + 1])),
+                                     l2[h / 2]);
                 if (lane == 0) {
 #pragma unroll
                     for (int h = 0; h < kHW; h += 4)
@@ -1030,31 +1037,32 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     ok = meet() && ok;
                     if (quad == 0 && lane < kHW) {
                         const int r = hb + lane;
-                        int up = 0;
+                        int up = INT_MIN;
 #pragma unroll 1
-                        for (int k = 0; k < 4; ++k) up = max(up, red_i[k * kNH + r] - 119);
+                        for (int k = 0; k < 4; ++k) up = max(up, red_i[k * kNH + r]);
+                        // (each head by its own scores: none is rounded differently for another's)
+                        up = up > kLazy || (first && up < -kLow) ? up : 0;
                         const int m = m_s[r] + up;
                         // out of range, or NaN: the head's sums become NaN
                         const bool bad = m >= kMagicBits + kRange || m <= kMagicBits - kRange;
-                        a_s[r] = bad ? __int_as_float(0x7fffffff) : up > 100 ? 0.f : ex2(-(float)up);
+                        a_s[r] = bad ? __int_as_float(0x7fffffff) : first || up > 100 ? 0.f : ex2(-(float)up);
                         m_s[r] = m;
                         up_s[r] = up;
                         if (lane == 0) sh->moved[group][t & 1] = 0;
                     }
                     ok = meet() && ok;
-                    if (lane < kHW) sf = max(sf - up_s[hb + lane], 0);
+                    if (lane < kHW) sf -= up_s[hb + lane];
 #pragma unroll
                     for (int h = 0; h < kHW; h += 2) {
-                        // (a move by more than 2^100 leaves nothing of the sums before, and 2^E was out of range)
+                        // (a first tile has no sums before it; a move by more than 2^100 leaves nothing of them, and
+                        // then 2^E was out of range)
                         const float2 f = *reinterpret_cast<const float2*>(a_s + hb + h);
                         const int2 up = *reinterpret_cast<const int2*>(up_s + hb + h);
-                        const f32x2 z = mul2(mul2(pack2(sv[h], sv[h + 1]), ru2),
-                                             pack2(__int_as_float(max(d[h] - up.x, 0) << 23),
-                                                   __int_as_float(max(d[h + 1] - up.y, 0) << 23)));
                         float x, y, zx, zy;
+                        unpack2(mul2(mul2(pack2(sv[h], sv[h + 1]), ru2),
+                                     pack2(scale_of(d[h] - up.x), scale_of(d[h + 1] - up.y))), zx, zy);
                         unpack2(mul2(l2[h / 2], pack2(f.x, f.y)), x, y);
-                        unpack2(z, zx, zy);
-                        l2[h / 2] = pack2(up.x > 100 ? zx + f.x : x, up.y > 100 ? zy + f.y : y);
+                        l2[h / 2] = pack2(first || up.x > 100 ? zx + f.x : x, first || up.y > 100 ? zy + f.y : y);
                     }
                     if (!first) {  // O as well, once the values before are added
                         ok = mbar_wait(&sh->o_done, (t - 1) & 1, abort_flag, p.status, p.wait_ns) && ok;
@@ -1093,6 +1101,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 }
                 if (lane < kHW) {
                     const int r = hb + lane;
+                    sf = max(sf + kBias, 0);
                     sf_s[(r & 31) * 16 + (r >> 5) * 4 + quad] = (uint8_t)sf;
                     if constexpr (S::kStacked)
                         sf_s[((r + kNH) & 31) * 16 + ((r + kNH) >> 5) * 4 + quad] = (uint8_t)sf;

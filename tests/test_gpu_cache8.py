@@ -529,6 +529,25 @@ def test_decode_rising_scores():
         check_decode(q, kv, sc, lens, SCALE, 1, 1, 1, 0, 0, out, lse)
 
 
+@pytest.mark.parametrize("level", [-3000.0, -200.0, -85.0, -40.0, 20.0, 60.0, 200.0, 3000.0])
+@pytest.mark.parametrize("H", [16, 64])
+def test_decode_scores_all_far_from_zero(level, H):
+    """Scores about `level` (base 2) from the first tile on, and one row whose second tile jumps back to zero."""
+    g = gen(int(level) + H)
+    T = 300
+    direction = randn(g, 576)
+    direction /= direction.norm()
+    a = torch.full((2, T, 1), level * math.log(2.0) / (8 * SCALE), device=DEV)
+    a[1, 128:] = 0
+    x = direction * a + randn(g, 2, T, 576) * 0.1
+    q = (direction * 8 + randn(g, 2, H, 576) * 0.1).bfloat16()
+    s = torch.exp2(torch.floor(torch.log2(x.abs().amax(-1) / 448)) + 1)
+    kv, sc = [(x / s[..., None]).to(E4M3)], [s]
+    lens = torch.tensor([T, T - 7], dtype=torch.int32, device=DEV)
+    out, lse = dcp.mla_cache8_decode(q, kv, sc, lens, SCALE)
+    check_decode(q, kv, sc, lens, SCALE, 1, 1, 1, 0, 0, out, lse)
+
+
 def test_decode_q_of_very_different_heads_and_dims():
     g = gen(13)
     H, T = 64, 300
