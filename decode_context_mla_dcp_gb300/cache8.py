@@ -91,7 +91,7 @@ def _ints(name, t, n, index):
     return t.data_ptr()
 
 
-def _shards(caches, scales, block):
+def _shards(caches, scales, block, interleave):
     """Check the shards' tensors; (device index, B, T, Dk, cache pointers, scale pointers)."""
     cp = len(caches)
     if cp < 1 or cp > _b.DCP_MLA_CACHE8_CP_MAX or len(scales) != cp:
@@ -99,6 +99,8 @@ def _shards(caches, scales, block):
                          "many scale tensors")
     if block < 1 or block > _b.DCP_MLA_CACHE8_BLOCK_MAX or block & (block - 1):
         raise ValueError(f"block must be a power of two, at most {_b.DCP_MLA_CACHE8_BLOCK_MAX}")
+    if interleave < 1 or interleave > 1 << 24:  # (here, for ctypes drops an int's high bits)
+        raise ValueError("interleave must be in [1, 2^24]")
     shape = None
     kv, sc = (ctypes.c_void_p * cp)(), (ctypes.c_void_p * cp)()
     e4m3, codes, f32 = _torch.float8_e4m3fn, _torch.uint8, _torch.float32
@@ -161,6 +163,17 @@ def mla_rope_inv_freq(rot: int = 64, base: float = 10000.0, *, scaling: str = "n
     return f.to(device), amp
 
 
+def _meet(gap, n, h, d, row, head, orow, ohead) -> bool:
+    """Whether x [n, h, d] and out, ``gap`` elements behind it, may share elements: if
+    their spans do, unless they are different dims of the same heads."""
+    if gap < 0:
+        gap, row, head, orow, ohead = -gap, orow, ohead, row, head
+    if gap >= (n - 1) * row + (h - 1) * head + d:
+        return False
+    step = math.gcd(row if n > 1 else 0, head if h > 1 else 0)
+    return (n > 1 and row != orow) or (h > 1 and head != ohead) or step == 0 or not d <= gap % step <= step - d
+
+
 def mla_rope(x, positions, inv_freq, *, start: int = 0, interleaved: bool = True, mscale: float = 1.0, out=None,
              stream=None):
     """Rotary positions on dims [start, start + 2 len(inv_freq)) of every head.
@@ -189,6 +202,8 @@ def mla_rope(x, positions, inv_freq, *, start: int = 0, interleaved: bool = True
     if not (wide or positions.dtype == torch.int32) or positions.dim() != 1 or positions.shape[0] != n or \
             positions.get_device() != index or not positions.is_contiguous():
         raise ValueError("positions must be a contiguous int32 or int64 tensor [N] on x's device")
+    if start < 0 or start > d:
+        raise ValueError("start must be in [0, D]")
     raw, inside = _on(index, stream)
     if inside is not None:
         with inside:
@@ -204,8 +219,10 @@ def mla_rope(x, positions, inv_freq, *, start: int = 0, interleaved: bool = True
         if out.shape != x.shape or out.dtype != x.dtype or out.get_device() != index or (unit != 1 and d > 1):
             raise ValueError("out must have x's shape, dtype and device, and unit stride along D")
         dst = out.data_ptr()
-        gap = abs(dst - src) // x.element_size()
-        if 0 < gap < d and n * h > 0 and x.untyped_storage().data_ptr() == out.untyped_storage().data_ptr():
+        if n > 1 and h > 1 and ohead < (n - 1) * orow + d and orow < (h - 1) * ohead + d or \
+                n > 1 and orow < d or h > 1 and ohead < d:
+            raise ValueError("out's rows or heads overlap each other")
+        if dst != src and n * h > 0 and _meet((dst - src) // x.element_size(), n, h, d, row, head, orow, ohead):
             raise ValueError("out overlaps x: pass x itself to rotate in place")
     rc = lib.dcp_mla_rope(src, row, head, positions.data_ptr(), wide, inv_freq.data_ptr(), n, h, d, start,
                           2 * inv_freq.shape[0], interleaved, mscale, dtype, dst, orow, ohead, raw)
@@ -226,7 +243,7 @@ def mla_cache8_append(latent, k_rope, caches, scales, seq_lens, *, cu_new=None, 
     smallest power of two that holds its values; a block that already holds
     tokens is requantised where its scale grows."""
     lib, torch = _ready()
-    index, B, T, dk, kv, sc = _shards(caches, scales, block)
+    index, B, T, dk, kv, sc = _shards(caches, scales, block, interleave)
     dtype = _DTYPES.get(latent.dtype)
     if dtype is None or dtype == _b.DCP_DTYPE_F32:
         raise TypeError("latent must be bf16 or fp16")
@@ -275,7 +292,7 @@ def mla_cache8_read(caches, scales, total: int, *, starts=None, cu=None, block: 
     16-byte boundaries. Tokens that no held shard has are left as they were.
     Returns out."""
     lib, torch = _ready()
-    index, B, T, dk, kv, sc = _shards(caches, scales, block)
+    index, B, T, dk, kv, sc = _shards(caches, scales, block, interleave)
     if total < 0:
         raise ValueError("total must not be negative")
     dtype = (torch.bfloat16 if out is None else out.dtype) if dtype is None else dtype
@@ -295,6 +312,8 @@ def mla_cache8_read(caches, scales, total: int, *, starts=None, cu=None, block: 
         raise ValueError("out must be [total, Dk] of dtype with unit inner stride, on the caches' device")
     else:
         row = out.stride(0)
+        if row < dk and total > 1:
+            raise ValueError("out's rows overlap each other")
     rc = lib.dcp_mla_cache8_read(kv, sc, len(caches), B, T, dk, block, interleave, start_ptr, cu_ptr, total,
                                  out.data_ptr(), row, code, raw)
     if rc:
@@ -317,7 +336,7 @@ def mla_cache8_decode(q, caches, scales, seq_lens, scale: float, *, block: int =
     256-byte aligned, allocated when not given and needed. status: None, or an
     int32 CUDA tensor (see the C header)."""
     lib, torch = _ready()
-    index, B, T, dk, kv, sc = _shards(caches, scales, block)
+    index, B, T, dk, kv, sc = _shards(caches, scales, block, interleave)
     if q.dim() != 3 or q.dtype != torch.bfloat16 or q.get_device() != index:
         raise ValueError("q must be bf16 [B, H, Dk] with unit inner stride, on the caches' device")
     qb, H, qd = q.shape
@@ -328,6 +347,8 @@ def mla_cache8_decode(q, caches, scales, seq_lens, scale: float, *, block: int =
     if lens is None:
         raise ValueError("seq_lens is required")
     cp = len(caches)
+    if window < 0 or sinks < 0 or max(window, sinks) >= 1 << 63:
+        raise ValueError("window and sinks must be in [0, 2^63)")
     raw, inside = _on(index, stream)
     if inside is not None:
         with inside:

@@ -862,7 +862,8 @@ extern "C" const char* dcp_mla_cache8_strerror(int status) {
         case DCP_MLA_CACHE8_ERR_NULL_POINTER: return "a required pointer is NULL, or every shard's";
         case DCP_MLA_CACHE8_ERR_BAD_SHAPE: return "a size is out of range";
         case DCP_MLA_CACHE8_ERR_BAD_BLOCK: return "block must be a power of two in [1, 128]";
-        case DCP_MLA_CACHE8_ERR_BAD_CP: return "cp must be in [1, 16] and interleave in [1, 2^24]";
+        case DCP_MLA_CACHE8_ERR_BAD_CP:
+            return "cp must be in [1, 16] and interleave in [1, 2^24], and two shards must not share what is written";
         case DCP_MLA_CACHE8_ERR_MISALIGNED: return "a pointer or a stride is not aligned as the call asks";
         case DCP_MLA_CACHE8_ERR_BAD_DTYPE: return "a dtype that the call does not take";
         case DCP_MLA_CACHE8_ERR_BAD_FLAGS: return "unknown flag bits";
@@ -924,6 +925,11 @@ extern "C" int dcp_mla_cache8_append(const void* latent, int64_t latent_row, con
     const int lg = log2_of(block);
     if (lg < 0) return DCP_MLA_CACHE8_ERR_BAD_BLOCK;
     if (const int rc = check_shards(kv_ptrs, scale_ptrs, cp, interleave)) return rc;
+    // (a cache that stands for two shards would be written by both at once)
+    for (int j = 0; j < cp; ++j)
+        for (int k = 0; k < j; ++k)
+            if (T > 0 && kv_ptrs[j] != nullptr && (kv_ptrs[j] == kv_ptrs[k] || scale_ptrs[j] == scale_ptrs[k]))
+                return DCP_MLA_CACHE8_ERR_BAD_CP;
     if (N == 0 || T == 0) return 0;
     if (latent == nullptr || seq_lens == nullptr || (Dk == 576 && k_rope == nullptr))
         return DCP_MLA_CACHE8_ERR_NULL_POINTER;

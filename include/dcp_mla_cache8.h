@@ -11,7 +11,8 @@
  * row of a shard share one fp32 scale: the cached value is code * scale.
  *   kv     [B, T, Dk] e4m3 codes (4 exponent, 3 mantissa bits, no infinity),
  *          contiguous, 16-byte aligned
- *   scales [B, ceil(T / block)] fp32, contiguous; positive
+ *   scales [B, ceil(T / block)] fp32, contiguous; positive (the append writes
+ *          powers of two; the decode takes any from 2^-60 to 2^32)
  * block is a power of two, at most DCP_MLA_CACHE8_BLOCK_MAX; 1 gives each token
  * its own scale.
  *
@@ -47,8 +48,8 @@ enum {
     DCP_MLA_CACHE8_ERR_NULL_POINTER = -201, /* a required pointer is NULL (or every shard's) */
     DCP_MLA_CACHE8_ERR_BAD_SHAPE = -202,    /* a size out of range (see each call) */
     DCP_MLA_CACHE8_ERR_BAD_BLOCK = -203,    /* block not a power of two in [1, DCP_MLA_CACHE8_BLOCK_MAX] */
-    DCP_MLA_CACHE8_ERR_BAD_CP = -204,       /* cp outside [1, DCP_MLA_CACHE8_CP_MAX] or interleave outside
-                                               [1, 2^24] */
+    DCP_MLA_CACHE8_ERR_BAD_CP = -204,       /* cp outside [1, DCP_MLA_CACHE8_CP_MAX], interleave outside
+                                               [1, 2^24], or an append whose shards share a cache or scales */
     DCP_MLA_CACHE8_ERR_MISALIGNED = -205,   /* a pointer or a stride is not aligned as the call asks */
     DCP_MLA_CACHE8_ERR_BAD_DTYPE = -206,    /* a dtype that the call does not take */
     DCP_MLA_CACHE8_ERR_BAD_FLAGS = -207,    /* unknown flag bits */
@@ -99,7 +100,8 @@ int dcp_mla_rope(const void* x, int64_t x_row, int64_t x_head, const void* posit
  *   k_rope   [N, 64] of the same type, row stride rope_row (a multiple of 8),
  *            16-byte aligned; NULL with Dk = 512
  *   inv_freq NULL: k_rope is taken as it is; or [32] doubles as for
- *            dcp_mla_rope: k_rope is rotated (fp32, not rounded in between)
+ *            dcp_mla_rope: k_rope is rotated (fp32, not rounded in between, the
+ *            sine and cosine to 2^-21)
  * Scales. A block's scale is the smallest power of two s with |x| <= 448 s over
  * the finite values of its new tokens, at least 2^-60. A block that already
  * holds tokens of the row keeps the larger of that and its present scale; where
@@ -129,11 +131,12 @@ int dcp_mla_cache8_read(const void* const* kv_ptrs, const float* const* scale_pt
                         void* out, int64_t out_row, int dtype, void* stream);
 
 /*
- * Single-token attention over the cache. For row b with L = seq_lens[b] cached
- * positions (clamped to what the shards can hold), every head attends to
+ * Single-token attention over the cache. For row b with L = seq_lens[b]
+ * positions (negative: 0), every head attends to
  *     all positions p < L                                   (window = 0)
  *     p < L with p >= L - window or p < sinks               (window > 0)
- * of the shards that are held:
+ * that a held shard has (a position past a shard's T tokens, which the append
+ * drops, counts in L but is not seen):
  *     s_p       = scale * <q[b, h, :Dk], kv[p, :Dk]>
  *     out[b, h] = sum_p softmax(s)_p * kv[p, :512]
  *     lse[b, h] = log_base sum_p exp(s_p)
@@ -157,8 +160,9 @@ int dcp_mla_cache8_read(const void* const* kv_ptrs, const float* const* scale_pt
  * 2^-9 of the head's largest exactly (and the others to 2^-16 of it).
  * Probabilities are split the same way at a power-of-two scale for each head and
  * 32 tokens, to 2^-8 relative like bf16. Products accumulate in fp32; output
- * rounded once to bf16. A NaN code that is visible, or a NaN or infinity in q,
- * makes the (row, head) NaN; tokens that are not visible may hold anything.
+ * rounded once to bf16. A NaN code that is visible, a NaN or infinity in q, or
+ * scores beyond 2^21 in units of ln 2 make the (row, head) NaN; tokens that are
+ * not visible may hold anything.
  */
 int dcp_mla_cache8_decode(const void* q, int64_t q_row, int64_t q_head, const void* const* kv_ptrs,
                           const float* const* scale_ptrs, const int32_t* seq_lens, int cp, int64_t B, int H, int Dk,

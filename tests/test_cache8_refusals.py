@@ -65,7 +65,8 @@ SHARDS = [
     (SHAPE, dict(N=-1)), (SHAPE, dict(cu_new=None, N=3)), (SHAPE, dict(B=0)), (DTYPE, dict(dtype=2)),
     (NULL, dict(latent=None)), (NULL, dict(k_rope=None)), (NULL, dict(seq_lens=None)), (ALIGN, dict(latent=A + 2)),
     (ALIGN, dict(latent_row=516)), (ALIGN, dict(rope_row=68)), (ALIGN, dict(k_rope=A + 8)), (ALIGN, dict(cu_new=A + 1)),
-    (ALIGN, dict(inv_freq=A + 4))])
+    (ALIGN, dict(inv_freq=A + 4)), (CP, dict(cp=2, kv_ptrs=[A, A], scale_ptrs=[A, 2 * A])),
+    (CP, dict(cp=3, kv_ptrs=[A, None, 2 * A], scale_ptrs=[A, None, A]))])
 def test_append(code, change):
     refused(code, dcp.dcp_mla_cache8_append, APPEND, **change)
 
@@ -157,6 +158,9 @@ def test_wrappers_check_shards():
                  ([kv.view(torch.uint8).view(torch.float8_e5m2)], [sc])]:
         with pytest.raises(TypeError):
             read(c, s)
+    for il in (0, (1 << 24) + 1, (1 << 32) + 1):
+        with pytest.raises(ValueError):
+            read([kv], [sc], interleave=il)
     with pytest.raises(ValueError):
         dcp.mla_cache8_read([kv], [sc], -1)
     with pytest.raises(TypeError):
@@ -192,7 +196,13 @@ def test_wrappers_check_the_rest():
             dcp.mla_cache8_decode(bad, [kv], [sc], lens, 1.0)
     with pytest.raises(ValueError):
         dcp.mla_cache8_decode(q, [kv], [sc], None, 1.0)
+    for kw in (dict(window=-1), dict(window=1 << 64), dict(window=4, sinks=-1), dict(window=4, sinks=1 << 63)):
+        with pytest.raises(ValueError, match="window"):
+            dcp.mla_cache8_decode(q, [kv], [sc], lens, 1.0, **kw)
     x, pos = torch.zeros((2, 3, 64)), torch.zeros((2,), dtype=torch.int64)
+    for start in (-1, 65, 1 << 32):
+        with pytest.raises(ValueError, match="start"):
+            dcp.mla_rope(x, pos, freq, start=start)
     for a in ((x[0], pos, freq), (x, pos[:1], freq), (x, pos.float(), freq), (x, pos, freq.float()),
               (x.transpose(1, 2), pos, freq)):
         with pytest.raises(ValueError):
@@ -214,3 +224,25 @@ def test_inv_freq_values():
     assert torch.allclose(f, 10000.0 ** (-torch.arange(32, dtype=torch.float64) / 32), rtol=1e-15, atol=0)
     y, amp = dcp.mla_rope_inv_freq(64, scaling="yarn", factor=40.0, mscale=1.0, mscale_all_dim=1.0, device="cpu")
     assert amp == 1.0 and (y <= f).all() and (y >= f / 40 * (1 - 1e-15)).all() and (y[:-1] > y[1:]).all()
+
+
+@pytest.mark.parametrize("n,h,d,x,out", [
+    # offset and strides of two views of one buffer
+    (3, 2, 4, (0, 8, 4), (4, 8, 4)), (3, 2, 4, (0, 16, 8), (4, 16, 8)), (3, 2, 4, (0, 16, 8), (3, 16, 8)),
+    (3, 2, 4, (0, 16, 8), (5, 16, 8)), (3, 2, 4, (20, 16, 8), (0, 16, 8)), (3, 2, 4, (0, 16, 8), (44, 16, 8)),
+    (3, 2, 4, (0, 16, 8), (43, 16, 8)), (1, 2, 4, (0, 5, 12), (4, 3, 12)), (1, 2, 4, (0, 5, 12), (4, 3, 8)),
+    (1, 1, 4, (0, 5, 12), (3, 3, 8)), (1, 1, 4, (0, 5, 12), (4, 3, 8)), (2, 3, 4, (0, 4, 8), (24, 4, 8)),
+    (2, 3, 4, (0, 4, 8), (8, 4, 8)), (2, 3, 4, (50, 4, 8), (8, 4, 8)), (4, 1, 4, (0, 10, 0), (6, 10, 0)),
+    (4, 1, 4, (0, 10, 0), (7, 10, 0)), (2, 2, 4, (0, 0, 8), (4, 8, 16))])
+def test_overlaps_of_rotated_views(n, h, d, x, out):
+    """Views that share an element are always found; views that do not are let through where they are different dims of
+    the same heads, or lie apart."""
+    from decode_context_mla_dcp_gb300 import cache8
+    elems = lambda v: {v[0] + i * v[1] + j * v[2] + k for i in range(n) for j in range(h) for k in range(d)}
+    said = cache8._meet(out[0] - x[0], n, h, d, *x[1:], *out[1:])
+    a, b = elems(x), elems(out)
+    if a & b:
+        assert said
+    elif x[1:] == out[1:] or max(a) < min(b) or max(b) < min(a):
+        aside = n > 1 and h > 1 and x[1] < x[2]  # (heads outside rows: told apart only where the spans are)
+        assert not said or aside

@@ -114,6 +114,25 @@ def test_rope_into_a_view_leaves_the_rest():
     assert torch.equal(buf2[..., :3], before[..., :3]) and torch.equal(buf2[..., 67:], before[..., 67:])
 
 
+def test_rope_refuses_overlaps():
+    x = torch.zeros((4, 2, 64), device=DEV)
+    pos = torch.zeros((4,), dtype=torch.int32, device=DEV)
+    inv_freq, _ = dcp.mla_rope_inv_freq(32)
+    whole = torch.zeros((4, 2, 128), device=DEV)
+    dcp.mla_rope(whole[..., :64], pos, inv_freq, out=whole[..., 64:])  # other dims of the same heads
+    for out in (x.expand(4, 2, 64)[:1].expand(4, 2, 64), torch.zeros((4, 1, 64), device=DEV).expand(4, 2, 64),
+                torch.zeros((400,), device=DEV).as_strided((4, 2, 64), (64, 64, 1))):
+        with pytest.raises(ValueError, match="overlap"):
+            dcp.mla_rope(x, pos, inv_freq, out=out)
+    with pytest.raises(ValueError, match="overlap"):
+        dcp.mla_rope(whole[..., :64], pos, inv_freq, out=whole[..., 32:96])
+    big = torch.zeros((5, 2, 64), device=DEV)
+    with pytest.raises(ValueError, match="overlap"):
+        dcp.mla_rope(big[:4], pos, inv_freq, out=big[1:])
+    heads_first = torch.zeros((2, 4, 64), device=DEV)
+    assert dcp.mla_rope(x, pos, inv_freq, out=heads_first.transpose(0, 1)).data_ptr() == heads_first.data_ptr()
+
+
 def test_rope_of_nothing():
     inv_freq, _ = dcp.mla_rope_inv_freq(64)
     x = torch.empty((0, 4, 64), device=DEV)
@@ -304,6 +323,57 @@ def test_append_many_rows_and_a_broken_cu(B, cp, T):
                               cu_new=torch.arange(B + 1, device=DEV, dtype=torch.int32).flip(0) - 3, block=blk)
     for j in range(cp):
         assert torch.equal(bits(kv[j]), before[j])
+
+
+@pytest.mark.parametrize("B,cp,il,block", [(300, 2, 1, 32), (70, 4, 3, 64), (130, 2, 16, 128), (257, 1, 1, 2),
+                                           (32, 8, 1, 16), (33, 8, 1, 16)])
+def test_append_more_pairs_of_rows_and_shards(B, cp, il, block):
+    """More than 256 pairs (256 themselves once), rows of no new token to several blocks, from inside a block on."""
+    g = gen(B)
+    T = 2 * block + 5
+    counts = [(i * 13) % 5 if i % 11 else cp * block + i % 7 for i in range(B)]
+    starts = [(i * 5) % (cp * T) for i in range(B)]
+    n = sum(counts)
+    latent = loud(g, n, 512, torch.bfloat16)
+    kv, sc = blank(cp, B, T, 512, block)
+    values, scales = [x.double() for x in kv], [x.double() for x in sc]
+    cu = torch.tensor([0] + counts, device=DEV).cumsum(0).int()
+    dcp.mla_cache8_append(latent, None, kv, sc, torch.tensor(starts, device=DEV, dtype=torch.int32), cu_new=cu,
+                          block=block, interleave=il)
+    ref.append(latent.double(), counts, starts, values, scales, cp, il, block)
+    for j in range(cp):
+        assert torch.equal(kv[j].double(), values[j]) and torch.equal(sc[j].double(), scales[j])
+
+
+@pytest.mark.parametrize("block", [1, 64])
+def test_a_cache_whose_offsets_pass_32_bits(block):
+    """Two rows of 4.3 GB: append, read back and attend behind 2^32 bytes and at the end of the last row."""
+    g = gen(12)
+    B, T, n, window = 2, 7_500_000, 300, 290
+    kv = [torch.zeros((B, T, 576), dtype=torch.uint8, device=DEV).view(E4M3)]
+    sc = [torch.ones((B, -(-T // block)), device=DEV)]
+    starts = torch.tensor([T - n - 17, T - n], dtype=torch.int32, device=DEV)
+    latent, rope = randn(g, B * n, 512).bfloat16(), randn(g, B * n, 64).bfloat16()
+    dcp.mla_cache8_append(latent, rope, kv, sc, starts, block=block)
+    got = dcp.mla_cache8_read(kv, sc, B * n, starts=starts, block=block, dtype=torch.float32)
+    x = torch.cat((latent, rope), 1).double()
+    for b in range(B):
+        rows = slice(int(starts[b]), int(starts[b]) + n)
+        scale = sc[0][b, torch.arange(rows.start, rows.stop, device=DEV) // block].double()[:, None]
+        mine = x[b * n:(b + 1) * n]
+        assert torch.equal(got[b * n:(b + 1) * n].double(), kv[0][b, rows].double() * scale)
+        assert ((got[b * n:(b + 1) * n].double() - mine).abs() <=
+                torch.maximum(2.0 ** -4 * mine.abs(), 2.0 ** -10 * scale)).all()
+        assert (kv[0][b, rows.start - 5:rows.start].view(torch.uint8) == 0).all()
+    q = randn(g, B, 16, 576).bfloat16()
+    lens = starts + n
+    out, lse = dcp.mla_cache8_decode(q, kv, sc, lens, SCALE, block=block, window=window)
+    first = (T - 600) // 128 * 128  # the same rows in a short cache (whole blocks of it)
+    short = [kv[0][:, first:].contiguous()]
+    short_sc = [sc[0][:, first // block:].contiguous()]
+    again = dcp.mla_cache8_decode(q, short, short_sc, lens - first, SCALE, block=block, window=window)
+    check_decode(q, short, short_sc, lens - first, SCALE, 1, 1, block, window, 0, *again)
+    check_decode(q, short, short_sc, lens - first, SCALE, 1, 1, block, window, 0, out, lse)
 
 
 # ---- read-back --------------------------------------------------------------------
@@ -527,6 +597,60 @@ def test_decode_rising_scores():
         lens = torch.full((1,), T, dtype=torch.int32, device=DEV)
         out, lse = dcp.mla_cache8_decode(q, kv, sc, lens, SCALE)
         check_decode(q, kv, sc, lens, SCALE, 1, 1, 1, 0, 0, out, lse)
+
+
+@pytest.mark.parametrize("B,cp,window,sinks", [(33, 3, 0, 0), (40, 2, 150, 5), (513, 2, 130, 0), (600, 1, 200, 3)])
+def test_decode_many_rows_with_shards_and_windows(B, cp, window, sinks):
+    g = gen(B)
+    H, T, block = 24, 330, 4
+    kv, sc = make_cache(g, cp, B, T, 576, block)
+    q = randn(g, B, H, 576).bfloat16()
+    lens = (torch.rand((B,), generator=g, device=DEV) * cp * (T + 30)).int()  # (some past the end)
+    lens[::5] = 0
+    out, lse = dcp.mla_cache8_decode(q, kv, sc, lens, SCALE, block=block, interleave=2, window=window, sinks=sinks)
+    check_decode(q, kv, sc, lens, SCALE, cp, 2, block, window, sinks, out, lse, rows=[0, 1, 2, 31, 32, B // 2, B - 1])
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_decode_scales_over_their_whole_range(H):
+    """Blocks of scales from 2^-60 to 2^32 in one row, small q."""
+    g = gen(H)
+    T, block = 500, 4
+    q = (randn(g, 1, H, 576) * 2.0 ** -36).bfloat16()
+    kv = [(randn(g, 1, T, 576) * 60).to(E4M3)]
+    lens = torch.tensor([T], dtype=torch.int32, device=DEV)
+    for lo, hi in ((-60, 33), (-60, -59), (32, 33), (-10, 33)):
+        sc = [torch.exp2(torch.randint(lo, hi, (1, T // block), generator=g, device=DEV).float())]
+        out, lse = dcp.mla_cache8_decode(q, kv, sc, lens, SCALE, block=block)
+        check_decode(q, kv, sc, lens, SCALE, 1, 1, block, 0, 0, out, lse)
+
+
+def test_decode_scores_out_of_range_are_nan():
+    """Beyond 2^21 in units of ln 2: NaN, not a wrong number; the other heads and rows keep their bits."""
+    g = gen(31)
+    kv, sc = make_cache(g, 1, 2, 300, 576, 1)
+    q = randn(g, 2, 32, 576).bfloat16()
+    lens = torch.tensor([300, 200], dtype=torch.int32, device=DEV)
+    clean = dcp.mla_cache8_decode(q, kv, sc, lens, SCALE)
+    q[0, 5] *= 2.0 ** 24
+    out, lse = dcp.mla_cache8_decode(q, kv, sc, lens, SCALE)
+    same = torch.ones((2, 32), dtype=torch.bool, device=DEV)
+    same[0, 5] = False
+    assert out[0, 5].isnan().all() and lse[0, 5].isnan()
+    assert torch.equal(out[same], clean[0][same]) and torch.equal(lse[same], clean[1][same])
+
+
+def test_decode_q_word_by_word():
+    """q whose heads are not on 16-byte boundaries, in each kernel form."""
+    g = gen(32)
+    for H in (5, 32, 64, 100):
+        for dk in (512, 576):
+            kv, sc = make_cache(g, 1, 2, 300, dk, 1)
+            q = randn(g, 2, H, dk + 2).bfloat16()[..., 2:]
+            lens = torch.tensor([300, 129], dtype=torch.int32, device=DEV)
+            a = dcp.mla_cache8_decode(q, kv, sc, lens, SCALE)
+            b = dcp.mla_cache8_decode(q.contiguous(), kv, sc, lens, SCALE)
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 @pytest.mark.parametrize("level", [-3000.0, -200.0, -85.0, -40.0, 20.0, 60.0, 200.0, 3000.0])
