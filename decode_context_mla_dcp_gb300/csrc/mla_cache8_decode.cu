@@ -469,24 +469,18 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
-// The scores' MMAs over slices [s, to) of the tile at `ka`, with the last slice those over the rope slice.
+// The scores' MMAs over slice s of the tile at `ka`, with the last slice those over the rope slice.
 // (Loops are kept rolled where code runs once or rarely: a call is short, its
 // instructions come from L2, and unrolled they cost more than they compute.)
 template <class S>
-__device__ __forceinline__ void issue_scores(uint32_t ka, uint32_t qa, uint32_t tmem, uint32_t idesc, int s, int to,
+__device__ __forceinline__ void issue_scores(uint32_t ka, uint32_t qa, uint32_t tmem, uint32_t idesc, int s,
                                              uint64_t* done) {
     if (elect_one()) {
-        uint64_t a0 = smem_desc(ka + s * kSlice, 16, 1024, kSwizzle128);
-        uint64_t b0 = smem_desc(qa + s * S::kQSlice, 16, 1024, kSwizzle128);
-#pragma unroll 1
-        for (; s < to; ++s) {
+        const uint64_t a0 = smem_desc(ka + s * kSlice, 16, 1024, kSwizzle128);
+        const uint64_t b0 = smem_desc(qa + s * S::kQSlice, 16, 1024, kSwizzle128);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                mma_f8(tmem, a0 + (uint32_t)(2 * k), b0 + (uint32_t)(2 * k), idesc, s | k);
-            a0 += kSlice >> 4;
-            b0 += S::kQSlice >> 4;
-        }
-        if (to == 4) {
+        for (int k = 0; k < 4; ++k) mma_f8(tmem, a0 + (uint32_t)(2 * k), b0 + (uint32_t)(2 * k), idesc, s | k);
+        if (s == 3) {
             if constexpr (S::kHasRope) {
                 const uint64_t a1 = smem_desc(ka + 4 * kSlice, 16, 512, kSwizzle64);
                 const uint64_t b1 = smem_desc(qa + 4 * S::kQSlice, 16, 512, kSwizzle64);
@@ -764,13 +758,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             if (more) {
                 if (t > 0 && !wait(&sh->s_free, (t - 1) & 1)) break;
                 if (first && !wait(&sh->q_full, segs++ & 1)) break;
-                bool ok = true;
-#pragma unroll 1
-                for (int s = 0; s < 4 && ok; ++s) {
-                    ok = wait(&sh->kv_full[t & 1][s], (t >> 1) & 1);
+                // (whether the next slice is there is asked before this one's MMAs are issued)
+                uint64_t* const full = sh->kv_full[t & 1];
+                const uint32_t par = (t >> 1) & 1;
+                bool ok = true, there = mbar_try_wait(full, par);
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    if (!__all_sync(0xffffffffu, there)) ok = wait(full + s, par);
                     if (!ok) break;
+                    if (s < 3) there = mbar_try_wait(full + s + 1, par);
                     tc_fence_after();
-                    issue_scores<S>(base + (t & 1) * S::kStage, base + 2 * S::kStage, tm, kIdS, s, s + 1, &sh->s_full);
+                    issue_scores<S>(base + (t & 1) * S::kStage, base + 2 * S::kStage, tm, kIdS, s, &sh->s_full);
                 }
                 if (!ok || (t > 0 && !turn && !values(t - 1))) break;
             }
