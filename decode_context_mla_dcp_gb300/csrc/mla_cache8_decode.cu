@@ -158,7 +158,7 @@ __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* tm, int x, in
                  "r"(x), "r"(y), "r"(z)
                  : "memory");
 }
-constexpr uint32_t kSwizzle128 = 2, kSwizzle64 = 4, kSwizzleNone = 0;
+constexpr uint32_t kSwizzle128 = 2, kSwizzle64 = 4, kSwizzle32 = 6, kSwizzleNone = 0;
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
     return (uint64_t)((addr >> 4) & 0x3fffu) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) |
            (1ull << 46) | ((uint64_t)swizzle << 61);
@@ -356,7 +356,8 @@ struct Shape {
     static constexpr int kQBytes = 4 * kQSlice + (kHasRope ? kRows * 64 : 0);
     // With 64 heads P's lo part takes the rope slice of its tile, which is done with once the scores are there.
     static constexpr bool kLoInRope = !kStacked && kHasRope;
-    static constexpr int kPBytes = kStacked || !kLoInRope ? kRows * 128 : kNH * 128;
+    static constexpr int kPRow = kStacked ? kRows : kNH;     // bytes of a token in P: 64, or 32 with 16 heads
+    static constexpr int kPBytes = kTile * kPRow * (kStacked || kLoInRope ? 1 : 2);
     static constexpr int kMisc = 1024 + 8 * kNH * 4;
     static constexpr int kSmem = 2 * kStage + kQBytes + kPBytes + kMisc;
     static constexpr int kHW = kNH / 4;                      // heads of a thread
@@ -499,8 +500,9 @@ template <class S>
 __device__ __forceinline__ void issue_values(uint32_t ka, uint32_t pa, uint32_t tmem, uint32_t idesc, uint32_t go_on,
                                              uint64_t* slice_free, uint64_t* done) {
     if (elect_one()) {
-        const uint64_t a0 = smem_desc(ka, kSlice, 1024, kSwizzle128), b0 = smem_desc(pa, 16, 1024, kSwizzle128);
-        const uint64_t b1 = smem_desc(S::kLoInRope ? ka + 4 * kSlice : pa + (S::kRows / 2) * 128, 16, 1024, kSwizzle128);
+        constexpr uint32_t kSw = S::kPRow == 64 ? kSwizzle64 : kSwizzle32;
+        const uint64_t a0 = smem_desc(ka, kSlice, 1024, kSwizzle128), b0 = smem_desc(pa, 16, 8 * S::kPRow, kSw);
+        const uint64_t b1 = smem_desc(S::kLoInRope ? ka + 4 * kSlice : pa + kTile * S::kPRow, 16, 8 * S::kPRow, kSw);
         copy_scales(tmem + S::kSf + 4, pa + S::kPBytes);
 #pragma unroll 1
         for (int m = 0; m < 4; ++m) {
@@ -508,10 +510,10 @@ __device__ __forceinline__ void issue_values(uint32_t ka, uint32_t pa, uint32_t 
             for (int k = 0; k < 4; ++k) {
                 const uint32_t d = tmem + S::kO + m * S::kOB, id = idesc | ((uint32_t)k << 4) | ((uint32_t)k << 29);
                 const uint64_t a = a0 + (uint32_t)(m * (kSlice >> 4) + 256 * k);
-                mma_f8_scaled<S::kStacked ? kPlain : kKeep>(d, a, b0 + (uint32_t)(2 * k), id, tmem + S::kSf,
+                mma_f8_scaled<S::kStacked ? kPlain : kKeep>(d, a, b0 + (uint32_t)(2 * S::kPRow * k), id, tmem + S::kSf,
                                                             tmem + S::kSf + 4, k > 0 ? 1u : go_on);
                 if constexpr (!S::kStacked)
-                    mma_f8_scaled<kKept>(d, a, b1 + (uint32_t)(2 * k), id, tmem + S::kSf, tmem + S::kSf + 4, 1u);
+                    mma_f8_scaled<kKept>(d, a, b1 + (uint32_t)(2 * S::kPRow * k), id, tmem + S::kSf, tmem + S::kSf + 4, 1u);
             }
             mma_commit(slice_free + m);
         }
@@ -533,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     constexpr int kHW = S::kHW;
     constexpr uint32_t kIdS = (1u << 4) | ((uint32_t)(S::kRows >> 3) << 17) | (8u << 24);
     constexpr uint32_t kIdO = ((uint32_t)((S::kStacked ? S::kRows : kNH) >> 3) << 17) | (1u << 23) | (8u << 24) |
-                              (1u << 15);  // ue8m0 scales, A read M-major
+                              (1u << 15) | (1u << 16);  // ue8m0 scales, A read M-major, B N-major
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* const q_s = smem + 2 * S::kStage;
     uint8_t* const p_s = q_s + S::kQBytes;
@@ -781,8 +783,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         // ---- softmax
         const int group = warp >> 2, quad = warp & 3, tok = quad * 32 + lane, hb = group * kHW;
         const uint32_t tlane = tmem + ((uint32_t)(32 * quad) << 16);
-        // 4 x 4 bytes are transposed between neighbouring lanes: each stage's byte selectors
-        const uint32_t sel1 = (lane & 1) ? 0x3715u : 0x6240u, sel2 = (lane & 2) ? 0x3276u : 0x5410u;
         if (warp < 4) {  // the cached tile's scale is 1 everywhere: its own scale goes into the probabilities
             const float one[4] = {__uint_as_float(0x7f7f7f7fu), __uint_as_float(0x7f7f7f7fu),
                                   __uint_as_float(0x7f7f7f7fu), __uint_as_float(0x7f7f7f7fu)};
@@ -989,17 +989,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                         hi[k + 1] = __uint_as_float((__float_as_uint(sv[h + k + 1]) + 0x80000u) & 0xfff00000u);
                         unpack2(fma2(pack2(hi[k], hi[k + 1]), neg, pack2(sv[h + k], sv[h + k + 1])), lo[k], lo[k + 1]);
                     }
-                    // A word is four heads of this token (every other head: their rows lie on different banks);
-                    // transposed between four lanes it is four tokens of one head.
 #pragma unroll
-                    for (int w = 0; w < kB / 4; ++w) {
-                        constexpr int kS = kB / 4;
-                        uint32_t vh = codes4(hi[w], hi[w + kS], hi[w + 2 * kS], hi[w + 3 * kS]);
-                        uint32_t vl = codes4(lo[w], lo[w + kS], lo[w + 2 * kS], lo[w + 3 * kS]);
-                        vh = __byte_perm(vh, __shfl_xor_sync(0xffffffffu, vh, 1), sel1);
-                        vl = __byte_perm(vl, __shfl_xor_sync(0xffffffffu, vl, 1), sel1);
-                        wh[h / 4 + w] = __byte_perm(vh, __shfl_xor_sync(0xffffffffu, vh, 2), sel2);
-                        wl[h / 4 + w] = __byte_perm(vl, __shfl_xor_sync(0xffffffffu, vl, 2), sel2);
+                    for (int k = 0; k < kB; k += 4) {
+                        wh[(h + k) / 4] = codes4(hi[k], hi[k + 1], hi[k + 2], hi[k + 3]);
+                        wl[(h + k) / 4] = codes4(lo[k], lo[k + 1], lo[k + 2], lo[k + 3]);
                     }
                 }
                 // Does the reference of some head have to move? Up when a score passes it by 2^kLazy; down only at
@@ -1087,15 +1080,22 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 // the buffer of P is free once the values before are added
                 if (t > 0) ok = mbar_wait(&sh->o_done, (t - 1) & 1, abort_flag, p.status, p.wait_ns) && ok;
                 // (warps of a group leave at one place: at the end of a tile, when a wait gave up anywhere)
+                // A token's heads side by side, as they lie in this thread (the MMA reads P along the heads).
                 uint8_t* const p_lo =
-                    S::kLoInRope ? smem + (t & 1) * S::kStage + 4 * kSlice : p_s + kNH * 128;
-#pragma unroll
-                for (int w = 0; w < kHW / 4; ++w) {
-                    constexpr int kS = kHW < 8 ? 1 : 2;
-                    const int r = hb + (w / kS) * 4 * kS + (w % kS) + (lane & 3) * kS;  // this lane's head
-                    const int at = r * 128 + (((tok >> 4) ^ (r & 7)) << 4) + (tok & 12);
-                    *reinterpret_cast<uint32_t*>(p_s + at) = wh[w];
-                    *reinterpret_cast<uint32_t*>(p_lo + at) = wl[w];
+                    S::kLoInRope ? smem + (t & 1) * S::kStage + 4 * kSlice : p_s + (S::kStacked ? 0 : kTile * S::kPRow);
+                const int swz = S::kPRow == 64 ? (tok >> 1) & 3 : (tok >> 2) & 1;
+                const int at_h = tok * S::kPRow + (((hb >> 4) ^ swz) << 4) + (hb & 15);
+                const int lo_c = (S::kStacked ? kNH >> 4 : 0) + (hb >> 4);
+                const int at_l = tok * S::kPRow + ((lo_c ^ swz) << 4) + (hb & 15);
+                if constexpr (kHW == 16) {
+                    *reinterpret_cast<uint4*>(p_s + at_h) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+                    *reinterpret_cast<uint4*>(p_lo + at_l) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
+                } else if constexpr (kHW == 8) {
+                    *reinterpret_cast<uint2*>(p_s + at_h) = make_uint2(wh[0], wh[1]);
+                    *reinterpret_cast<uint2*>(p_lo + at_l) = make_uint2(wl[0], wl[1]);
+                } else {
+                    *reinterpret_cast<uint32_t*>(p_s + at_h) = wh[0];
+                    *reinterpret_cast<uint32_t*>(p_lo + at_l) = wl[0];
                 }
                 if (lane < kHW) {
                     const int r = hb + lane;
