@@ -361,9 +361,15 @@ struct Shape {
     static constexpr int kMisc = 1024 + 8 * kNH * 4;
     static constexpr int kSmem = 2 * kStage + kQBytes + kPBytes + kMisc;
     static constexpr int kHW = kNH / 4;                      // heads of a thread
-    static constexpr int kO = kRows;                         // TMEM: S [0, rows), O 4 x kOB columns, scales
-    static constexpr int kOB = kStacked ? kRows : kNH;
-    static constexpr int kSf = kO + 4 * kOB;
+    // TMEM: S [0, rows), O in blocks of kNH columns, scales. A block of 128 latent dims has O's two parts side by side
+    // (one MMA of both parts of P) where there is room: with 64 heads that is the first one only.
+    static constexpr int kO = kRows;
+    static constexpr int kOBlocks = kStacked ? 8 : 5;
+    static constexpr int kSf = kO + kOBlocks * kNH;
+    __device__ __forceinline__ static bool wide(int m) { return kStacked || m == 0; }
+    __device__ __forceinline__ static uint32_t col(int m) {
+        return (uint32_t)(kO + (kStacked ? 2 * m : m + (m > 0 ? 1 : 0)) * kNH);
+    }
     static constexpr int kCols = kSf + 8 <= 256 ? 256 : 512;
     static_assert(kSmem <= 232448 && kSf + 8 <= 512, "");
 };
@@ -494,26 +500,42 @@ __device__ __forceinline__ void issue_scores(uint32_t ka, uint32_t qa, uint32_t 
     __syncwarp();
 }
 
-// Its values: per 128 latent dims 4 MMAs (8 where P's parts are two operands); each slice of the tile is
-// given back as soon as it has been used.
+// Its values: per 128 latent dims 4 MMAs with both parts of P side by side, or 8 with one part each (the cached tile
+// then stays in the collector for the second); each slice of the tile is given back as soon as it has been used.
 template <class S>
-__device__ __forceinline__ void issue_values(uint32_t ka, uint32_t pa, uint32_t tmem, uint32_t idesc, uint32_t go_on,
+__device__ __forceinline__ void issue_values(uint32_t ka, uint32_t pa, uint32_t tmem, uint32_t go_on,
                                              uint64_t* slice_free, uint64_t* done) {
+    // ue8m0 scales, A read M-major, B N-major
+    constexpr uint32_t kId = (1u << 23) | (8u << 24) | (1u << 15) | (1u << 16);
+    constexpr uint32_t kIdBoth = kId | ((uint32_t)(S::kRows >> 3) << 17), kIdPart = kId | ((uint32_t)(S::kRows >> 4) << 17);
+    constexpr uint32_t kSw = S::kPRow == 64 ? kSwizzle64 : kSwizzle32, kStep = 2 * S::kPRow;
     if (elect_one()) {
-        constexpr uint32_t kSw = S::kPRow == 64 ? kSwizzle64 : kSwizzle32;
-        const uint64_t a0 = smem_desc(ka, kSlice, 1024, kSwizzle128), b0 = smem_desc(pa, 16, 8 * S::kPRow, kSw);
-        const uint64_t b1 = smem_desc(S::kLoInRope ? ka + 4 * kSlice : pa + kTile * S::kPRow, 16, 8 * S::kPRow, kSw);
+        // the parts of P: in one row per token, or the low one in its tile's rope slice, or behind the other
+        const uint32_t lo = S::kLoInRope ? ka + 4 * kSlice : pa + kTile * S::kPRow;
+        const uint64_t a0 = smem_desc(ka, kSlice, 1024, kSwizzle128);
+        const uint64_t hi = smem_desc(pa, 16, 8 * S::kPRow, kSw), b1 = smem_desc(lo, 16, 8 * S::kPRow, kSw);
+        const uint64_t both = S::kStacked ? hi : (S::kLoInRope ? smem_desc(lo, pa - lo, 8 * S::kPRow, kSw)
+                                                               : smem_desc(pa, lo - pa, 8 * S::kPRow, kSw));
         copy_scales(tmem + S::kSf + 4, pa + S::kPBytes);
 #pragma unroll 1
         for (int m = 0; m < 4; ++m) {
+            const uint32_t d = tmem + S::col(m);
+            const uint64_t am = a0 + (uint32_t)(m * (kSlice >> 4));
+            if (S::wide(m)) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t d = tmem + S::kO + m * S::kOB, id = idesc | ((uint32_t)k << 4) | ((uint32_t)k << 29);
-                const uint64_t a = a0 + (uint32_t)(m * (kSlice >> 4) + 256 * k);
-                mma_f8_scaled<S::kStacked ? kPlain : kKeep>(d, a, b0 + (uint32_t)(2 * S::kPRow * k), id, tmem + S::kSf,
-                                                            tmem + S::kSf + 4, k > 0 ? 1u : go_on);
-                if constexpr (!S::kStacked)
-                    mma_f8_scaled<kKept>(d, a, b1 + (uint32_t)(2 * S::kPRow * k), id, tmem + S::kSf, tmem + S::kSf + 4, 1u);
+                for (int k = 0; k < 4; ++k)
+                    mma_f8_scaled<kPlain>(d, am + (uint32_t)(256 * k), both + kStep * k,
+                                          kIdBoth | ((uint32_t)k << 4) | ((uint32_t)k << 29), tmem + S::kSf,
+                                          tmem + S::kSf + 4, k > 0 ? 1u : go_on);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t id = kIdPart | ((uint32_t)k << 4) | ((uint32_t)k << 29);
+                    mma_f8_scaled<kKeep>(d, am + (uint32_t)(256 * k), hi + kStep * k, id, tmem + S::kSf,
+                                         tmem + S::kSf + 4, k > 0 ? 1u : go_on);
+                    mma_f8_scaled<kKept>(d, am + (uint32_t)(256 * k), b1 + kStep * k, id, tmem + S::kSf,
+                                         tmem + S::kSf + 4, 1u);
+                }
             }
             mma_commit(slice_free + m);
         }
@@ -534,8 +556,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     using S = Shape<kDk, kNH>;
     constexpr int kHW = S::kHW;
     constexpr uint32_t kIdS = (1u << 4) | ((uint32_t)(S::kRows >> 3) << 17) | (8u << 24);
-    constexpr uint32_t kIdO = ((uint32_t)((S::kStacked ? S::kRows : kNH) >> 3) << 17) | (1u << 23) | (8u << 24) |
-                              (1u << 15) | (1u << 16);  // ue8m0 scales, A read M-major, B N-major
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* const q_s = smem + 2 * S::kStage;
     uint8_t* const p_s = q_s + S::kQBytes;
@@ -746,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         auto values = [&](uint32_t v) {
             if (!wait(&sh->p_full, v & 1)) return false;
             tc_fence_after();
-            issue_values<S>(base + (v & 1) * S::kStage, base + 2 * S::kStage + S::kQBytes, tm, kIdO, began ? 0u : 1u,
+            issue_values<S>(base + (v & 1) * S::kStage, base + 2 * S::kStage + S::kQBytes, tm, began ? 0u : 1u,
                             sh->kv_free[v & 1], &sh->o_done);
             return true;
         };
@@ -1060,10 +1080,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                         __syncwarp();
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < 4 * (S::kStacked ? 2 : 1) * (kHW / 4); ++c) {
+                        for (int c = 0; c < S::kOBlocks * (kHW / 4); ++c) {
                             const int h = (c % (kHW / 4)) * 4, b = c / (kHW / 4);
-                            const uint32_t col =
-                                tlane + S::kO + (S::kStacked ? (b >> 1) * S::kOB + (b & 1) * kNH : b * S::kOB) + hb + h;
+                            const uint32_t col = tlane + S::kO + b * kNH + hb + h;
                             float o[4];
                             tmem_ld<4>(col, o);
                             const float4 f = *reinterpret_cast<const float4*>(a_s + hb + h);
@@ -1101,8 +1120,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     const int r = hb + lane;
                     sf = max(sf + kBias, 0);
                     sf_s[(r & 31) * 16 + (r >> 5) * 4 + quad] = (uint8_t)sf;
-                    if constexpr (S::kStacked)
-                        sf_s[((r + kNH) & 31) * 16 + ((r + kNH) >> 5) * 4 + quad] = (uint8_t)sf;
+                    sf_s[((r + kNH) & 31) * 16 + ((r + kNH) >> 5) * 4 + quad] = (uint8_t)sf;
                 }
                 async_fence();
                 tc_fence_before();
@@ -1162,10 +1180,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 #pragma unroll 1
                 for (int m = 0; m < 4; ++m) {
                     float o[kHW];
-                    tmem_ld<kHW>(tlane + S::kO + m * S::kOB + hb, o);
-                    if constexpr (S::kStacked) {
+                    tmem_ld<kHW>(tlane + S::col(m) + hb, o);
+                    if (S::wide(m)) {
                         float lo[kHW];
-                        tmem_ld<kHW>(tlane + S::kO + m * S::kOB + kNH + hb, lo);
+                        tmem_ld<kHW>(tlane + S::col(m) + kNH + hb, lo);
                         tmem_wait_ld();
 #pragma unroll
                         for (int h = 0; h < kHW; ++h) o[h] += lo[h];
