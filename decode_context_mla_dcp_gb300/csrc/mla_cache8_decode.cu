@@ -335,10 +335,17 @@ __device__ __forceinline__ void next(const P& p) {
     }
 };
 
+// The CTAs' shares. All rows' tiles lie in a line that is cut evenly, but a row that begins in a share costs its CTA
+// a change of segments (q, sums, output) of about kChange tiles' time, so that each row is kChange places longer than
+// its tiles, which come last. (64 ragged rows x 16K: the slowest CTA 135 -> 130 us.)
+constexpr int kChange = 2;
+__device__ __forceinline__ int places(int tiles) { return tiles > 0 ? tiles + kChange : 0; }
+
 // What the join needs of a row: its first CTA range and its number of segments. Written by the CTA that has the
-// row's first tile; for a row without a tile by the first CTA.
+// row's first tile (at place pre + kChange); for a row without a tile by the first CTA.
 __device__ __forceinline__ void tell_row(const DecodeBase& p, int b, int n, int pre, int g, int g_end, int per,
                                          int range) {
+    pre += kChange;
     if (n == 0 && range == 0) p.row_info[b] = make_int2(0, 0);
     else if (n > 0 && pre >= g && pre < g_end) p.row_info[b] = make_int2(range, (pre + n - 1) / per - range + 1);
 }
@@ -401,7 +408,7 @@ struct Shared {  // barriers and small things, behind the scale atom
     int armed[2][4];          // how often each slice's barrier has been armed, less one
     uint32_t tmem;
     int abort;
-    int find[4];
+    int find[4];              // the CTA's first row (-1: none), its first tile there, the row's tiles
     int wsum[16];
     TileInfo info[4];
 };
@@ -583,7 +590,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         if (lane < 8) mbar_init(&sh->voted[0] + lane, 4);
         if (lane >= 24) (&sh->moved[0][0])[lane - 24] = 0;
         if (lane >= 16 && lane < 24) (&sh->armed[0][0])[lane - 16] = -1;
-        if (lane == 0) *abort_flag = 0;
+        if (lane == 0) {
+            *abort_flag = 0;
+            sh->find[0] = p.row_mode ? range : -1;
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMmaWarp) {
@@ -604,22 +614,23 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     if (!p.row_mode && p.B <= 32) {
         if (warp == kLoadWarp) {  // few rows: a lane a row, beside the others' set-up
             const int n = lane < p.B ? row_tiles(p, length) : 0;
-            int x = n;
+            int x = places(n);
 #pragma unroll 1
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, x, o);
                 if (lane >= o) x += y;
             }
-            const int total = __shfl_sync(0xffffffffu, x, 31), pre = x - n;
+            const int total = __shfl_sync(0xffffffffu, x, 31), pre = x - places(n);
             const int per = max((total + p.ranges - 1) / p.ranges, 1);
             const int64_t lo = (int64_t)range * per, hi = lo + per;
             g = lo < total ? (int)lo : total;
             g_end = hi < total ? (int)hi : total;
-            const uint32_t here = __ballot_sync(0xffffffffu, n > 0 && pre <= g && g < pre + n);
+            const uint32_t here = __ballot_sync(0xffffffffu, pre <= g && g < x);
             row = here ? __ffs(here) - 1 : 0;
-            tile = g - __shfl_sync(0xffffffffu, pre, row);
+            tile = g - __shfl_sync(0xffffffffu, pre, row) - kChange;
             n_row = __shfl_sync(0xffffffffu, n, row);
             length = __shfl_sync(0xffffffffu, length, row);
+            if (lane == 0 && here) sh->find[0] = row;
             if (hblk == 0 && lane < p.B) tell_row(p, lane, n, pre, g, g_end, per, range);
         }
     } else if (!p.row_mode) {
@@ -636,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             for (int b0 = 0; b0 < p.B; b0 += kSoftThreads) {
                 if (pass == 0 || p.B > kSoftThreads) {
                     const int n = tid < kSoftThreads && b0 + tid < p.B ? row_tiles(p, row_length(p, b0 + tid)) : 0;
-                    int x = n;
+                    int x = places(n);
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
                         const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -649,13 +660,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     const int all = __reduce_add_sync(0xffffffffu, ws);
                     __syncthreads();
                     n_mine = n;
-                    pre_mine = base + before + x - n;
+                    pre_mine = base + before + x - places(n);
                     base += all;
                 }
                 if (pass == 1) {
-                    if (n_mine > 0 && pre_mine <= g && g < pre_mine + n_mine && g < g_end) {
+                    if (pre_mine <= g && g < pre_mine + places(n_mine) && g < g_end) {
                         sh->find[0] = b0 + tid;
-                        sh->find[1] = g - pre_mine;
+                        sh->find[1] = g - pre_mine - kChange;
                         sh->find[2] = n_mine;
                     }
                     if (hblk == 0 && tid < kSoftThreads && b0 + tid < p.B)
@@ -694,6 +705,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 for (int i = lane; i < nh * (kDv / 8); i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
                 if (p.lse != nullptr)
                     for (int i = lane; i < nh; i += 32) p.lse[(int64_t)row * p.H + h0 + i] = -INFINITY;
+            }
+            if (!p.row_mode && tile < 0) {  // (places of no tile)
+                g -= n_row > 0 ? tile : 0;
+                tile = 0;
             }
             const int n = p.row_mode || n_row - tile < g_end - g ? n_row - tile : g_end - g;
             if (n > 0) {
@@ -735,9 +750,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     }
                 }
             }
-            g += n;
+            g += n > 0 ? n : 0;
             row += p.row_mode ? p.ranges : 1;
-            tile = 0;
+            tile = p.row_mode ? 0 : -kChange;
         }
         if (lane == 0) {
             if (ok) {  // no more tiles: a tile of no tokens
@@ -917,11 +932,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             ti = sh->info[t & 3];
             return !soft_any(!(ok && good)) && ti.valid > 0;
         };
+        // q of the CTA's first row is asked for at once (with whole rows that row may turn out to see nothing)
+        const int asked = sh->find[0];
+        if (asked >= 0) fetch_q(asked);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->q_asked);
         bool going = next_segment(true);
         if (going) {
-            fetch_q(ti.row);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->q_asked);
+            if (ti.row != asked) {
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                __syncwarp();
+                fetch_q(ti.row);
+            }
             aborted = !split_q();
         }
         while (going) {  // segments
@@ -1227,19 +1249,19 @@ struct JoinParams {
     float lse_scale;
 };
 
-// One warp (or kWarps warps, where there are few rows and many segments of each)
-// per (row, head): the segments' outputs weighted by 2^(lse - max), and the row's
-// LSE. Rows with one segment have been written; rows without a tile get zeros.
-// Two round trips to memory: what the row has, then a warp's first segment and
-// all LSEs together.
+// One warp per (row, head), eight of them a CTA; or a CTA of kWarps warps, where there are few rows and many segments
+// of each (its 1024 CTAs for 8 rows x 128 heads are resident at once with four warps, not with eight). The segments'
+// outputs are weighted by 2^(lse - max), and the row's LSE comes of the same weights. Rows with one segment have been
+// written; rows without a tile get zeros. Bound by the partials' way from L2, so a warp asks for two segments at once,
+// together with the LSEs: two round trips, the first for what the row has.
 template <int kWarps>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinParams p) {
-    __shared__ float acc_s[kWarps > 1 ? 8 : 1][kDv];
-    __shared__ float sum_s[8];
+__global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 256) join_kernel(const __grid_constant__ JoinParams p) {
+    __shared__ float acc_s[kWarps > 1 ? kWarps : 1][kDv];
+    __shared__ float sum_s[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * (8 / kWarps) + warp / kWarps;
+    const int64_t unit = kWarps > 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 8 + warp;
     const int b = (int)(unit / p.H), h = (int)(unit - (int64_t)b * p.H);
-    const int hblk = h / p.block_heads, hh = h - hblk * p.block_heads, w = warp % kWarps;
+    const int hblk = h / p.block_heads, hh = h - hblk * p.block_heads, w = kWarps > 1 ? warp : 0;
     pdl_wait();
     pdl_launch_dependents();
     if (unit >= p.units) return;
@@ -1260,13 +1282,14 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinP
     };
     float acc[16], sum = 0.f, m = -INFINITY;
     bool nan = false;
-    float4 x[4];
-    const auto load = [&](int i) {
+    float4 x[2][4];
+    const auto load = [&](int i, float4* to) {
         const float4* const src = reinterpret_cast<const float4*>(p.part + place(i) * kDv);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = src[k * 32 + lane];
+        for (int k = 0; k < 4; ++k) to[k] = src[k * 32 + lane];
     };
-    if (w < row.y) load(w);
+    if (w < row.y) load(w, x[0]);
+    if (w + kWarps < row.y) load(w + kWarps, x[1]);
     for (int i = lane; i < row.y; i += 32) {
         const float l = p.part_lse[place(i)];
         nan |= isnan(l);
@@ -1278,17 +1301,22 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinP
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.f;
 #pragma unroll 1
-    for (int i = w; i < row.y; i += kWarps) {
-        const float f = ex2(p.part_lse[place(i)] - m);
-        sum += f;
+    for (int i0 = w; i0 < row.y; i0 += 2 * kWarps) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            acc[4 * k] = fmaf(f, x[k].x, acc[4 * k]);
-            acc[4 * k + 1] = fmaf(f, x[k].y, acc[4 * k + 1]);
-            acc[4 * k + 2] = fmaf(f, x[k].z, acc[4 * k + 2]);
-            acc[4 * k + 3] = fmaf(f, x[k].w, acc[4 * k + 3]);
+        for (int u = 0; u < 2; ++u) {
+            const int i = i0 + u * kWarps;
+            if (i >= row.y) break;
+            const float f = ex2(p.part_lse[place(i)] - m);
+            sum += f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                acc[4 * k] = fmaf(f, x[u][k].x, acc[4 * k]);
+                acc[4 * k + 1] = fmaf(f, x[u][k].y, acc[4 * k + 1]);
+                acc[4 * k + 2] = fmaf(f, x[u][k].z, acc[4 * k + 2]);
+                acc[4 * k + 3] = fmaf(f, x[u][k].w, acc[4 * k + 3]);
+            }
+            if (i + 2 * kWarps < row.y) load(i + 2 * kWarps, x[u]);
         }
-        if (i + kWarps < row.y) load(i + kWarps);
     }
     if constexpr (kWarps > 1) {
 #pragma unroll
@@ -1298,30 +1326,33 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinP
         if (lane == 0) sum_s[warp] = sum;
         __syncthreads();  // (the whole CTA is one unit: no thread has left)
         sum = 0.f;
-        float a = 0.f, c = 0.f;
+        float4 a = {0.f, 0.f, 0.f, 0.f};
+        static_assert(kWarps == 1 || kDv == 128 * kWarps, "");
 #pragma unroll
         for (int v = 0; v < kWarps; ++v) {
-            const float2 y = *reinterpret_cast<const float2*>(&acc_s[v][2 * threadIdx.x]);
+            const float4 y = *reinterpret_cast<const float4*>(&acc_s[v][4 * threadIdx.x]);
             sum += sum_s[v];
-            a += y.x;
-            c += y.y;
+            a.x += y.x;
+            a.y += y.y;
+            a.z += y.z;
+            a.w += y.w;
         }
-        const float inv = 1.0f / sum;
-        reinterpret_cast<__nv_bfloat162*>(out)[threadIdx.x] = __floats2bfloat162_rn(a * inv, c * inv);
-        if (p.lse != nullptr && threadIdx.x == 0) p.lse[unit] = (m + log2f(sum)) * p.lse_scale;
-    } else {
-        const float inv = 1.0f / sum;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint2 v;
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[4 * i] * inv, acc[4 * i + 1] * inv);
-            const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv);
-            v.x = *reinterpret_cast<const uint32_t*>(&lo);
-            v.y = *reinterpret_cast<const uint32_t*>(&hi);
-            reinterpret_cast<uint2*>(out)[i * 32 + lane] = v;
-        }
-        if (p.lse != nullptr && lane == 0) p.lse[unit] = (m + log2f(sum)) * p.lse_scale;
+        acc[0] = a.x;
+        acc[1] = a.y;
+        acc[2] = a.z;
+        acc[3] = a.w;
     }
+    const float inv = 1.0f / sum;
+#pragma unroll
+    for (int i = 0; i < (kWarps > 1 ? 1 : 4); ++i) {
+        uint2 v;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[4 * i] * inv, acc[4 * i + 1] * inv);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv);
+        v.x = *reinterpret_cast<const uint32_t*>(&lo);
+        v.y = *reinterpret_cast<const uint32_t*>(&hi);
+        reinterpret_cast<uint2*>(out)[kWarps > 1 ? (int)threadIdx.x : i * 32 + lane] = v;
+    }
+    if (p.lse != nullptr && lane == 0 && w == 0) p.lse[unit] = (m + log2f(sum)) * p.lse_scale;
 }
 
 // ---- host side -------------------------------------------------------------------------
@@ -1423,14 +1454,14 @@ cudaError_t launch_decode(const DecodeParams<kShards>& p, unsigned flags, cudaSt
     if (e != cudaSuccess || p.row_mode) return e;
     // the join overlaps its launch with the decode's tail and waits for it on the device
     const int64_t units = (int64_t)p.B * p.H;
-    // eight warps a (row, head) where a row has four segments or more on average, else one
+    // four warps a (row, head) where a row has four segments or more on average, else one
     const bool few = p.ranges >= 4 * p.B;
     cfg.gridDim = dim3((unsigned)(few ? units : (units + 7) / 8));
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(few ? 128 : 256);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
     const JoinParams j = {p.part, p.part_lse, p.row_info, p.out, p.lse, units, p.H, p.head_blocks, kNH, p.lse_scale};
-    return few ? cudaLaunchKernelEx(&cfg, join_kernel<8>, j) : cudaLaunchKernelEx(&cfg, join_kernel<1>, j);
+    return few ? cudaLaunchKernelEx(&cfg, join_kernel<4>, j) : cudaLaunchKernelEx(&cfg, join_kernel<1>, j);
 }
 
 // Encode the shards' tensor maps and launch. Returns the call's status.
