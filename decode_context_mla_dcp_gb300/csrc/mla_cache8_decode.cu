@@ -59,6 +59,7 @@
 
 #include "dcp_lse_reduce.h"
 #include "dcp_mla_cache8.h"
+#include "dcp_mla_decode.h"
 
 namespace {
 
@@ -70,7 +71,8 @@ constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
 constexpr int kThreads = kSoftThreads + 64;
 constexpr int kCpMax = DCP_MLA_CACHE8_CP_MAX;
 constexpr int64_t kMaxInterleave = 1 << 24;
-constexpr long long kWaitLimitNs = 2000000000LL;  // every wait gives up after this
+constexpr long long kWaitLimitNs = 2000000000LL;  // every wait gives up after this,
+constexpr long long kTestWaitLimitNs = 20000000LL;  // or after this, with DCP_MLA_FLAG_TEST_STALL
 constexpr int kLazy = 32;                  // how far an exponent may pass the reference
 constexpr int kLow = 60;                   // how far below it a segment's first ones may lie
 
@@ -97,6 +99,7 @@ struct DecodeBase {
     float scale_log2;
     float lse_scale;                       // ln 2 for a natural-log LSE, 1 for base 2
     long long wait_ns;
+    int stall;                             // DCP_MLA_FLAG_TEST_STALL: a CTA's first slice waits for 16 bytes more
 };
 template <int kShards>
 struct DecodeParams : DecodeBase {
@@ -763,7 +766,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                         if (!ok) break;
                         if (lane == 0) {
                             uint64_t* const bar = &sh->kv_full[st][a];
-                            mbar_expect_tx(bar, kSlice + (a == 3 ? S::kRopeSlice : 0));
+                            mbar_expect_tx(bar, kSlice + (a == 3 ? S::kRopeSlice : 0) +
+                                                    (p.stall && t == 0 && a == 0 ? 16 : 0));
                             tma_load_3d(kv + a * kSlice, &p.tm_latent[c.j], a * 128, tok0, row, bar);
                             if (S::kHasRope && a == 3)
                                 tma_load_3d(kv + 4 * kSlice, &p.tm_rope[c.j], kDv, tok0, row, bar);
@@ -789,12 +793,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 sh->info[t & 3] = {0u, 0, 0u, 0};
                 mbar_arrive(&sh->info_full[t & 3]);
             }
-            // after a wait that gave up, what was armed still lands before the CTA leaves
-            if (*abort_flag)
-                for (int k = 0; k < 8; ++k) {
-                    const int n = sh->armed[k >> 2][k & 3];
-                    if (n >= 0) mbar_drain(&sh->kv_full[k >> 2][k & 3], (uint32_t)(n & 1), p.wait_ns);
-                }
         }
     } else if (warp == kMmaWarp) {
         // ---- MMAs, in turn: the scores of a tile, slice by slice as they land, then the values of the tile before.
@@ -1262,6 +1260,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    // after a wait that gave up, what was armed still lands before the CTA leaves
+    if (warp == kLoadWarp && lane < 8 && *abort_flag) {
+        const int n = sh->armed[lane >> 2][lane & 3];
+        if (n >= 0) mbar_drain(&sh->kv_full[lane >> 2][lane & 3], (uint32_t)(n & 1), p.wait_ns);
+    }
     if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kCols) : "memory");
 }
@@ -1558,7 +1561,7 @@ extern "C" int dcp_mla_cache8_decode(const void* q, int64_t q_row, int64_t q_hea
     if (lg < 0) return DCP_MLA_CACHE8_ERR_BAD_BLOCK;
     if (cp < 1 || cp > kCpMax || interleave < 1 || interleave > kMaxInterleave) return DCP_MLA_CACHE8_ERR_BAD_CP;
     if (window < 0 || sinks < 0 || (sinks > 0 && window == 0)) return DCP_MLA_CACHE8_ERR_BAD_WINDOW;
-    if ((flags & ~(unsigned)DCP_FLAG_PDL) != 0) return DCP_MLA_CACHE8_ERR_BAD_FLAGS;
+    if ((flags & ~(DCP_FLAG_PDL | DCP_MLA_FLAG_TEST_STALL)) != 0) return DCP_MLA_CACHE8_ERR_BAD_FLAGS;
     if (q == nullptr || kv_ptrs == nullptr || scale_ptrs == nullptr || seq_lens == nullptr || out == nullptr)
         return DCP_MLA_CACHE8_ERR_NULL_POINTER;
     if (!aligned(q, 4) || q_row % 2 != 0 || q_head % 2 != 0 || !aligned(out, 16) || !aligned(lse, 4) ||
@@ -1615,7 +1618,8 @@ extern "C" int dcp_mla_cache8_decode(const void* q, int64_t q_row, int64_t q_hea
     p.ranges = grid_ranges(H, sms);
     p.scale_log2 = scale * 1.4426950408889634f;
     p.lse_scale = lse_base_e ? 0.6931471805599453f : 1.0f;
-    p.wait_ns = kWaitLimitNs;
+    p.stall = (flags & DCP_MLA_FLAG_TEST_STALL) ? 1 : 0;
+    p.wait_ns = p.stall ? kTestWaitLimitNs : kWaitLimitNs;
     if (p.row_mode && p.ranges > B) p.ranges = (int)B;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (cp == 1) return run_decode<1>(p, kv_ptrs, scale_ptrs, Dk, flags, st);

@@ -152,7 +152,9 @@ int dcp_mla_cache8_read(const void* const* kv_ptrs, const float* const* scale_pt
  *   status   as for dcp_mla_decode_partial: NULL, or a device int32 that the
  *            kernel ORs 1 into if a wait for its own copies or MMAs ever
  *            exceeds two seconds; the outputs are then not valid
- *   flags    0 or DCP_FLAG_PDL (1)
+ *   flags    0 or a combination of DCP_FLAG_PDL (1) and, for tests,
+ *            DCP_MLA_FLAG_TEST_STALL (32; see dcp_mla_decode.h: the first tile
+ *            of each CTA never counts as landed, waits give up after 20 ms)
  *   shapes   0 <= B <= 65535, 1 <= H <= 1024, Dk 512 or 576, Dv 512,
  *            0 <= T < 2^31, window and sinks >= 0
  * Numerics. The codes go to the tensor cores as they are. q is split into two

@@ -90,6 +90,7 @@ def test_decode(code, change):
 
 def test_decode_of_no_rows_is_nothing():
     dcp.dcp_mla_cache8_decode(**{**DECODE, "B": 0, "workspace": None})
+    dcp.dcp_mla_cache8_decode(**{**DECODE, "B": 0, "flags": dcp.DCP_FLAG_PDL | dcp.DCP_MLA_FLAG_TEST_STALL})
 
 
 def test_workspace_bytes():

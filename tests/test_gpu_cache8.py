@@ -755,6 +755,27 @@ def test_decode_partials_of_shards_merge_to_the_whole():
     assert (m[~torch.isinf(m)] - w[~torch.isinf(w)]).abs().max() <= 1e-5 * w[~torch.isinf(w)].abs().max()
 
 
+@pytest.mark.parametrize("B,H,T", [(3, 16, 200), (2, 64, 1000), (2, 128, 1000), (40, 32, 500), (700, 64, 256)])
+def test_decode_after_waits_that_gave_up(B, H, T):
+    """The first tile of every CTA never counts as landed: the status word reads 1 and the call ends; the next one is
+    right, in the same workspace."""
+    g = gen(B)
+    kv, sc = make_cache(g, 1, B, T, 576, 1)
+    q = randn(g, B, H, 576).bfloat16()
+    lens = torch.full((B,), T, dtype=torch.int32, device=DEV)
+    n = torch.cuda.get_device_properties(0).multi_processor_count
+    ws = torch.empty((max(dcp.dcp_mla_cache8_decode_workspace_bytes(1, B, H, T, 0, 0, n), 256),), dtype=torch.uint8,
+                     device=DEV)
+    status = torch.zeros((1,), dtype=torch.int32, device=DEV)
+    dcp.mla_cache8_decode(q, kv, sc, lens, SCALE, workspace=ws, status=status, flags=dcp.DCP_MLA_FLAG_TEST_STALL)
+    torch.cuda.synchronize()
+    assert int(status) == 1
+    status.zero_()
+    out, lse = dcp.mla_cache8_decode(q, kv, sc, lens, SCALE, workspace=ws, status=status)
+    check_decode(q, kv, sc, lens, SCALE, 1, 1, 1, 0, 0, out, lse, rows=[0, B - 1])
+    assert int(status) == 0
+
+
 def test_decode_of_an_empty_cache_and_no_rows():
     q = torch.zeros((2, 16, 576), dtype=torch.bfloat16, device=DEV)
     empty = torch.empty((2, 0, 576), dtype=E4M3, device=DEV)
