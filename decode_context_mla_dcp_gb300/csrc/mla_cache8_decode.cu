@@ -37,8 +37,8 @@
 // token (q's and P's two parts) against 576 bytes, so with 64 heads and more it is
 // the tensor cores and what feeds them, with 16 the cache's way from DRAM. A tile
 // of 64 heads takes 4,230 cycles at the 1.94 GHz that the call runs at. Its MMAs
-// alone take 2,958 (1,393 the scores, N = 128; 1,565 the values: N = 64 costs 59
-// cycles and N = 128 77, so both parts of P go into one MMA where TMEM has room
+// alone take 2,958 (1,393 the scores, N = 128; 1,565 the values: N = 64 costs 55
+// to 59 cycles and N = 128 77, so both parts of P go into one MMA where TMEM has room
 // for them, the first 128 dims). Shared memory's port is what they wait for: the
 // operands take 2,150 of its cycles a tile, the tile itself 580, the softmax some
 // 900. Two tiles, q and P fill shared memory, S, O and the scales TMEM (456 of 512
