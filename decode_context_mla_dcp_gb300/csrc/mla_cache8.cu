@@ -70,10 +70,17 @@ __device__ __forceinline__ float get_hi(uint32_t w) { return E::get((uint16_t)(w
 
 // Turns per position as a 64-bit fraction of a turn: multiplying it by a
 // position wraps at whole turns exactly, so a far position loses nothing but
-// what the double held (2^-53 of the frequency).
+// the fraction's last place. In integers, for 64-bit floating point is slow here
+// (30,000 tokens of one head of 288 dims: 26.6 us with it, 19.6 without): the
+// double is m 2^(e - 1075), and 1 / (2 pi) is kTurn 2^-66.
 __device__ __forceinline__ uint64_t turns_of(double inv_freq) {
-    const double u = inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
-    return (uint64_t)((u - floor(u)) * 18446744073709551616.0);
+    constexpr uint64_t kTurn = 0xa2f9836e4e44152aull;
+    const int64_t bits = __double_as_longlong(inv_freq);
+    const int s = 1077 - ((int)(bits >> 52) & 0x7ff);  // what the 117-bit product has to be shifted right by
+    const uint64_t m = ((uint64_t)bits & 0xfffffffffffffull) | (1ull << 52);
+    const uint64_t lo = m * kTurn, hi = __umul64hi(m, kTurn);
+    const uint64_t u = s >= 128 ? 0 : s >= 64 ? hi >> (s - 64) : s > 0 ? (lo >> s) | (hi << (64 - s)) : s > -64 ? lo << -s : 0;
+    return bits < 0 ? 0 - u : u;
 }
 
 // cos and sin of position * frequency, from the top 32 bits of the wrapped
@@ -113,6 +120,7 @@ struct RopeParams {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeAngles = 2048;  // cos/sin pairs a CTA holds
+constexpr int kRopeHalf = 128;     // pairs of a head, at most
 constexpr int kRopeBatch = 4;      // 16-byte vectors a thread has in flight
 
 // A unit is kV elements (16 bytes) of a head, or with halves two of them (kV
@@ -181,6 +189,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     using T = typename E::T;
     constexpr int kB = kInter ? kRopeBatch : kRopeBatch / 2;
     __shared__ alignas(16) float2 cs[kRopeAngles];
+    __shared__ uint64_t turn_s[kMany ? kRopeHalf : 1];
     const int64_t n0 = (int64_t)blockIdx.x * p.tokens;
     const int ntok = kMany ? (int)(p.N - n0 < p.tokens ? p.N - n0 : p.tokens) : 1;
     const int h0 = blockIdx.y * p.heads;
@@ -213,13 +222,25 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
                 }
             }
             if (!angles) {
+                // (with many tokens the frequencies are taken into turns once, and no angle costs a division)
+                if (kMany) {
+                    for (int f = threadIdx.x; f < p.half; f += threads) turn_s[f] = turns_of(p.inv_freq[f]);
+                    __syncthreads();
+                }
+                int tok = kMany ? (int)threadIdx.x / p.half : 0, f = (int)threadIdx.x - tok * p.half;
+                const int dtok = kMany ? threads / p.half : 0, df = threads - dtok * p.half;
                 for (int i = threadIdx.x; i < ntok * p.half; i += threads) {
-                    const int tok = kMany ? i / p.half : 0, f = i - tok * p.half;
                     const int64_t pos = p.pos64 ? static_cast<const int64_t*>(p.positions)[n0 + tok]
                                                 : (int64_t) static_cast<const int32_t*>(p.positions)[n0 + tok];
                     float co, si;
-                    angle_of(pos, turns_of(p.inv_freq[f]), &co, &si);
+                    angle_of(pos, kMany ? turn_s[f] : turns_of(p.inv_freq[f]), &co, &si);
                     cs[i] = make_float2(co * p.mscale, si * p.mscale);
+                    tok += dtok;
+                    f += df;
+                    if (kMany && f >= p.half) {
+                        f -= p.half;
+                        ++tok;
+                    }
                 }
                 __syncthreads();  // (every thread comes here once, with its first rows)
                 angles = true;
@@ -475,45 +496,64 @@ __global__ void __launch_bounds__(128) append_token_kernel(const __grid_constant
 // many warps as a block needs, so that small blocks take small CTAs and all CTAs
 // of a call are resident at once.
 //
-// Which blocks. kCounted: CTA u takes block u of all rows' and shards' blocks in
-// order; the CTA's warps count the blocks of 32 (row, shard) pairs each, and then
-// every warp looks through the 32 that hold block u. That spreads any mix of rows
-// evenly and costs two round trips, but goes over all pairs: it is for up to
-// kCountedPairs. Beyond, the first new token of a block (of a row, on a shard)
-// stands for it: CTA c looks at tokens c, c + G, c + 2G, ... (a binary search
-// each) with G odd, so that first tokens, which stand a power of two apart, spread
-// over the CTAs. (16385 tokens of 5 rows in blocks of 64: 15.4 us by first tokens,
-// whose 257 blocks fall on 159 CTAs, up to three on one.)
+// Which blocks. kCounted: the CTA's warps count the blocks of all rows, 32 rows
+// each in turn, once; then CTA c takes blocks c, c + G, ... of all rows' and
+// shards' blocks in order, and every warp looks through the 32 rows that hold one.
+// That spreads any mix of rows evenly and costs two round trips, but goes over all
+// rows. Otherwise the first new token of a block (of a row, on a shard) stands for
+// it: CTA c looks at tokens c, c + G, c + 2G, ... (a binary search each) with G odd,
+// so that first tokens, which stand a power of two apart, spread over the CTAs; yet
+// some CTAs find several. Counting is for up to kCountedRows rows and calls of more
+// tokens than CTAs are resident. (16,385 tokens of 5 rows in blocks of 64: 8.6 us
+// counted, 14.4 by first tokens; of 256 rows over four shards in blocks of 16 13.9
+// and 23.4; of 1,024 rows over two shards in blocks of 64 42.8 and 25.3; 256 x 4
+// tokens over four shards 6.3 and 5.6; 300 tokens of 256 rows 6.0 and 4.8.)
 constexpr int kTok = 4;
 constexpr int kCuShared = 1024;
-constexpr int kCountedPairs = 256;
+constexpr int kCountedRows = 512;
 
-// Blocks of pair e = row * cp + shard that have new tokens, from block `b0` on.
-struct Pair {
-    int row, shard;
-    uint32_t first, len, before, after;
+// A row's new tokens, and how many blocks of all its held shards get some. The first L positions lie in q whole
+// rounds over the shards and r positions of another, which cp shards ask for one division each.
+struct NewTokens {
+    uint32_t first, len, count;
     int blocks;
 };
-__device__ __forceinline__ Pair pair_of(const AppendParams& p, int e) {
-    Pair r;
-    r.row = (int)((uint32_t)e / p.cp);
-    r.shard = e - r.row * (int)p.cp;
-    r.blocks = 0;
-    if (r.row >= p.B || p.kv[r.shard] == nullptr) return r;
-    int64_t first = (int64_t)r.row * p.even, last = first + p.even;
+struct Part {
+    uint32_t before, after;  // the shard's tokens
+    int blocks;
+};
+__device__ __forceinline__ uint32_t part_of(const AppendParams& p, uint32_t L, uint32_t q, uint32_t j) {
+    const uint32_t r = L - q * p.cp * p.interleave, lo = j * p.interleave, n = r > lo ? r - lo : 0;
+    return q * p.interleave + (n < p.interleave ? n : p.interleave);
+}
+__device__ __forceinline__ Part shard_part(const AppendParams& p, uint32_t L0, uint32_t q0, uint32_t L1, uint32_t q1,
+                                           int j) {
+    Part s;
+    s.before = p.cp == 1 ? L0 : part_of(p, L0, q0, (uint32_t)j);
+    s.after = p.cp == 1 ? L1 : part_of(p, L1, q1, (uint32_t)j);
+    if ((int64_t)s.after > p.T) s.after = (uint32_t)p.T;
+    s.blocks = s.after > s.before && p.kv[j] != nullptr
+                   ? (int)(((s.after - 1) >> p.block_log2) - (s.before >> p.block_log2)) + 1
+                   : 0;
+    return s;
+}
+__device__ __forceinline__ NewTokens new_tokens(const AppendParams& p, int b) {
+    NewTokens r = {0u, 0u, 0u, 0};
+    if (b >= p.B) return r;
+    int64_t first = (int64_t)b * p.even, last = first + p.even;
     if (p.cu != nullptr) {
-        first = p.cu[r.row];
-        last = p.cu[r.row + 1];
+        first = p.cu[b];
+        last = p.cu[b + 1];
     }
+    const int32_t len = p.seq_lens[b];
     if (last > p.N) last = p.N;
     if (first < 0 || last <= first) return r;
-    const int32_t len = p.seq_lens[r.row];
     r.first = (uint32_t)first;
+    r.count = (uint32_t)(last - first);
     r.len = len < 0 ? 0u : (uint32_t)len;
-    r.before = held_tokens(r.len, r.shard, p.cp, p.interleave);
-    r.after = held_tokens(r.len + (uint32_t)(last - first), r.shard, p.cp, p.interleave);
-    if ((int64_t)r.after > p.T) r.after = (uint32_t)p.T;
-    if (r.after > r.before) r.blocks = (int)(((r.after - 1) >> p.block_log2) - (r.before >> p.block_log2)) + 1;
+    const uint32_t round = p.cp * p.interleave, end = r.len + r.count;
+    const uint32_t q0 = p.cp == 1 ? 0u : r.len / round, q1 = p.cp == 1 ? 0u : end / round;
+    for (int j = 0; j < (int)p.cp; ++j) r.blocks += shard_part(p, r.len, q0, end, q1, j).blocks;
     return r;
 }
 // Inclusive sum over the warp's lanes.
@@ -529,7 +569,7 @@ __device__ __forceinline__ int lane_sums(int x, int lane) {
 template <class E, int kWarps, bool kCounted>
 __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps)
 append_block_kernel(const __grid_constant__ AppendParams p) {
-    __shared__ int32_t cu_s[kCounted ? kCountedPairs / 32 : kCuShared + 1];
+    __shared__ int32_t cu_s[kCounted ? kCountedRows / 32 : kCuShared + 1];
     __shared__ Place list[kCounted ? 1 : 32 * kWarps];
     __shared__ int found;
     __shared__ float peak_s[kWarps];
@@ -545,44 +585,48 @@ append_block_kernel(const __grid_constant__ AppendParams p) {
             cu = cu_s;
         }
     }
+    const int chunks = (p.B + 31) / 32;  // of rows (counted: fewer than 32)
+    if constexpr (kCounted) {
+        for (int c = warp; c < chunks; c += kWarps) {
+            const int n = __reduce_add_sync(0xffffffffu, new_tokens(p, c * 32 + lane).blocks);
+            if (lane == 0) cu_s[c] = n;
+        }
+        __syncthreads();
+    }
     for (int64_t base = blockIdx.x; base < p.N; base += (int64_t)gridDim.x * (kCounted ? 1 : 32 * kWarps)) {
         Place w;
         int nfound = 1;
         if constexpr (kCounted) {
-            const int pairs = p.B * (int)p.cp, chunks = (pairs + 31) / 32;
-            int u = (int)base, chunk = 0;
-            if (chunks > 1) {
-                for (int c = warp; c < chunks; c += kWarps) {
-                    const int n = __reduce_add_sync(0xffffffffu, pair_of(p, c * 32 + lane).blocks);
-                    if (lane == 0) cu_s[c] = n;
-                }
-                __syncthreads();
-                chunk = chunks;
-                for (int c0 = 0; c0 < chunks; c0 += 32) {
-                    const int n = c0 + lane < chunks ? cu_s[c0 + lane] : 0, sum = lane_sums(n, lane);
-                    const uint32_t past = __ballot_sync(0xffffffffu, sum > u);
-                    if (past) {
-                        const int l = __ffs(past) - 1;
-                        chunk = c0 + l;
-                        u -= __shfl_sync(0xffffffffu, sum - n, l);
-                        break;
-                    }
-                    u -= __shfl_sync(0xffffffffu, sum, 31);
-                }
-                if (chunk == chunks) return;
-            }
-            const Pair r = pair_of(p, chunk * 32 + lane);
-            const int sum = lane_sums(r.blocks, lane);
-            const uint32_t past = __ballot_sync(0xffffffffu, sum > u);
+            int u = (int)base;
+            const int n = lane < chunks ? cu_s[lane] : 0;
+            int sum = lane_sums(n, lane);
+            uint32_t past = __ballot_sync(0xffffffffu, sum > u);
             if (!past) return;
-            const int l = __ffs(past) - 1;
+            const int chunk = __ffs(past) - 1;
+            u -= __shfl_sync(0xffffffffu, sum - n, chunk);
+            const NewTokens r = new_tokens(p, chunk * 32 + lane);
+            sum = lane_sums(r.blocks, lane);
+            past = __ballot_sync(0xffffffffu, sum > u);
+            if (!past) return;
+            int l = __ffs(past) - 1;
             u -= __shfl_sync(0xffffffffu, sum - r.blocks, l);
-            w.row = __shfl_sync(0xffffffffu, r.row, l);
-            w.shard = __shfl_sync(0xffffffffu, r.shard, l);
+            w.row = chunk * 32 + l;
             w.first = __shfl_sync(0xffffffffu, r.first, l);
             w.len = __shfl_sync(0xffffffffu, r.len, l);
-            w.end = __shfl_sync(0xffffffffu, r.after, l);
-            const uint32_t before = __shfl_sync(0xffffffffu, r.before, l);
+            const uint32_t end = w.len + __shfl_sync(0xffffffffu, r.count, l);
+            Part s = {0u, 0u, 0};  // a lane a shard
+            if (lane < (int)p.cp) {
+                const uint32_t round = p.cp * p.interleave;
+                s = shard_part(p, w.len, p.cp == 1 ? 0u : w.len / round, end, p.cp == 1 ? 0u : end / round, lane);
+            }
+            sum = lane_sums(s.blocks, lane);
+            past = __ballot_sync(0xffffffffu, sum > u);
+            if (!past) return;
+            l = __ffs(past) - 1;
+            u -= __shfl_sync(0xffffffffu, sum - s.blocks, l);
+            w.shard = l;
+            w.end = __shfl_sync(0xffffffffu, s.after, l);
+            const uint32_t before = __shfl_sync(0xffffffffu, s.before, l);
             w.loc = ((before >> p.block_log2) + (uint32_t)u) << p.block_log2;
             if (w.loc < before) w.loc = before;
             if (u < 0 || w.loc >= w.end) return;  // (only with offsets that are not in order)
@@ -836,22 +880,20 @@ int launch_append(const AppendParams& p, int block, cudaStream_t st) {
         append_token_kernel<E><<<(unsigned)((p.N + 3) / 4), 128, 0, st>>>(p);
         return launched();
     }
-    const int64_t pairs = (int64_t)p.B * p.cp;
-    if (pairs <= kCountedPairs) {  // at most two blocks of a pair are not full of new tokens
-        const int64_t most = p.N / block + 2 * pairs;
-        const unsigned grid = (unsigned)(p.N < most ? p.N : most);
-        if (block <= 16) append_block_kernel<E, 4, true><<<grid, 128, 0, st>>>(p);
-        else if (block == 32) append_block_kernel<E, 8, true><<<grid, 256, 0, st>>>(p);
-        else if (block == 64) append_block_kernel<E, 16, true><<<grid, 512, 0, st>>>(p);
-        else append_block_kernel<E, 32, true><<<grid, 1024, 0, st>>>(p);
-        return launched();
-    }
     // about as many CTAs as are resident at once (32 warps a multiprocessor), an odd number
-    const auto grid = [&](int64_t most) { return (unsigned)(p.N < most ? p.N : most); };
-    if (block <= 16) append_block_kernel<E, 4, false><<<grid(1217), 128, 0, st>>>(p);
-    else if (block == 32) append_block_kernel<E, 8, false><<<grid(609), 256, 0, st>>>(p);
-    else if (block == 64) append_block_kernel<E, 16, false><<<grid(305), 512, 0, st>>>(p);
-    else append_block_kernel<E, 32, false><<<grid(153), 1024, 0, st>>>(p);
+    const int warps = block <= 16 ? 4 : block / 4, resident = 152 * (32 / warps) + 1;
+    const unsigned grid = (unsigned)(p.N < resident ? p.N : resident);
+    if (p.N > resident && p.B <= kCountedRows) {
+        if (warps == 4) append_block_kernel<E, 4, true><<<grid, 128, 0, st>>>(p);
+        else if (warps == 8) append_block_kernel<E, 8, true><<<grid, 256, 0, st>>>(p);
+        else if (warps == 16) append_block_kernel<E, 16, true><<<grid, 512, 0, st>>>(p);
+        else append_block_kernel<E, 32, true><<<grid, 1024, 0, st>>>(p);
+    } else {
+        if (warps == 4) append_block_kernel<E, 4, false><<<grid, 128, 0, st>>>(p);
+        else if (warps == 8) append_block_kernel<E, 8, false><<<grid, 256, 0, st>>>(p);
+        else if (warps == 16) append_block_kernel<E, 16, false><<<grid, 512, 0, st>>>(p);
+        else append_block_kernel<E, 32, false><<<grid, 1024, 0, st>>>(p);
+    }
     return launched();
 }
 

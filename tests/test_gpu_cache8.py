@@ -345,6 +345,37 @@ def test_append_more_pairs_of_rows_and_shards(B, cp, il, block):
         assert torch.equal(kv[j].double(), values[j]) and torch.equal(sc[j].double(), scales[j])
 
 
+@pytest.mark.parametrize("B,cp,il,block,n", [
+    (5, 1, 1, 16, 1500), (300, 2, 3, 4, 1300), (512, 1, 1, 2, 1400), (513, 2, 1, 8, 1400), (40, 4, 16, 32, 900),
+    (33, 16, 2, 64, 700), (3, 1, 1, 128, 500), (1, 5, 1, 16, 1218), (64, 3, 7, 16, 1217)])
+def test_append_of_more_tokens_than_resident_ctas(B, cp, il, block, n):
+    """Uneven rows, some of no tokens, that begin inside a block; a shard that is not held; rows that the cache has no
+    room for; and offsets that a caller got wrong write nothing out of place."""
+    g = gen(B + n)
+    w = [(i * 29) % 7 if i % 6 else 40 for i in range(B)] if B > 1 else [1]
+    counts = [n * x // sum(w) for x in w]
+    counts[B // 2] += n - sum(counts)
+    starts = [(i * 37) % 90 for i in range(B)]
+    T = max(-(-(s + c) // cp) + 2 * il for s, c in zip(starts, counts)) - 9
+    latent = loud(g, n, 512, torch.bfloat16)
+    kv, sc = blank(cp, B, T, 512, block)
+    values, scales = [x.double() for x in kv], [x.double() for x in sc]
+    held = [j for j in range(cp) if cp == 1 or j != 1]
+    only = lambda x: [x[j] if j in held else None for j in range(cp)]
+    cu = torch.tensor([0] + counts, device=DEV).cumsum(0).int()
+    lens = torch.tensor(starts, device=DEV, dtype=torch.int32)
+    dcp.mla_cache8_append(latent, None, only(kv), only(sc), lens, cu_new=cu, block=block, interleave=il)
+    ref.append(latent.double(), counts, starts, values, scales, cp, il, block, held)
+    for j in range(cp):
+        assert torch.equal(kv[j].double(), values[j]) and torch.equal(sc[j].double(), scales[j])
+    before = [bits(x).clone() for x in kv]
+    full = torch.full((B,), T * cp + cp * il, device=DEV, dtype=torch.int32)
+    for bad in (cu, torch.full((B + 1,), n + 5, device=DEV, dtype=torch.int32), cu.flip(0) - 3, -cu):
+        dcp.mla_cache8_append(latent, None, kv, sc, full, cu_new=bad.contiguous(), block=block, interleave=il)
+    for j in range(cp):
+        assert torch.equal(bits(kv[j]), before[j])
+
+
 @pytest.mark.parametrize("block", [1, 64])
 def test_a_cache_whose_offsets_pass_32_bits(block):
     """Two rows of 4.3 GB: append, read back and attend behind 2^32 bytes and at the end of the last row."""
