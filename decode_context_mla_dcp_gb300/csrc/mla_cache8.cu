@@ -845,12 +845,12 @@ int launch_rope(RopeParams& p, int D, int64_t esize, cudaStream_t st) {
     // Rows side by side: a power of two, as counts of heads mostly are, so that no slot idles in the last step.
     // Tokens and heads of a CTA: at most about two batches of rows a thread, fewer where the call is small, so that
     // it still spreads over the GPU. More than one token only with all their heads.
+    int64_t want = p.N * p.H / (152 * 4);  // rows
     int slots = 1;
-    while (2 * slots * p.units <= kRopeThreads) slots *= 2;
+    while (2 * slots * p.units <= kRopeThreads && (slots < want || slots * p.units < 32)) slots *= 2;
     p.slots = slots;
     const int threads = slots * p.units < kRopeThreads ? (slots * p.units + 31) / 32 * 32 : kRopeThreads;
     const int64_t batch = (int64_t)slots * (p.interleaved ? kRopeBatch : kRopeBatch / 2);
-    int64_t want = p.N * p.H / (152 * 4);  // rows
     want = want < slots ? slots : (want > 2 * batch ? 2 * batch : want);
     const int64_t parts = (p.H + want - 1) / want, heads = (p.H + parts - 1) / parts;
     int64_t tokens = heads < p.H ? 1 : want / heads;
