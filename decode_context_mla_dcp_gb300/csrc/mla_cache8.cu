@@ -9,11 +9,12 @@
 // 8 or 16 bytes a lane and issued before any is used, and everything that a
 // token needs (its row, shard, place, angles) is found once and shared.
 // Measured, against a copy's 6.79 TB/s: rotating 64 of 192 dims of 8,192 x 64
-// heads 60.1 us (0.99), 128 x 128 heads x 64 into other rows 2.5 us; reading
+// heads 60.5 us (0.98), 128 x 128 heads x 64 into other rows 2.4 us; reading
 // 262,144 tokens back from four shards 68.7 us (0.97), 2,047 tokens 3.0 us;
-// appending 16,385 tokens in blocks of 64 9.5 us (0.44: two round trips before
-// the tokens' own, and a barrier), 256 x 4 tokens over four shards 6.0 us, one
-// token 2.0 us.
+// appending 16,385 tokens in blocks of 64 8.6 us (0.48: two round trips before
+// the tokens' own, and two barriers), 256 x 4 tokens over four shards 5.7 us, one
+// token 2.1 us. Many tokens of one head are bound by the angles' arithmetic
+// (30,000 tokens of 288 dims, 128 rotated: 15.3 us against 5.1).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -71,15 +72,20 @@ __device__ __forceinline__ float get_hi(uint32_t w) { return E::get((uint16_t)(w
 // Turns per position as a 64-bit fraction of a turn: multiplying it by a
 // position wraps at whole turns exactly, so a far position loses nothing but
 // the fraction's last place. In integers, for 64-bit floating point is slow here
-// (30,000 tokens of one head of 288 dims: 26.6 us with it, 19.6 without): the
-// double is m 2^(e - 1075), and 1 / (2 pi) is kTurn 2^-66.
+// (30,000 tokens of one head of 288 dims: 26.6 us with it, 19.6 without, 15.3 with
+// each CTA's frequencies taken into turns once): the double is m 2^(e - 1075), and
+// 1 / (2 pi) is kTurn 2^-66.
 __device__ __forceinline__ uint64_t turns_of(double inv_freq) {
     constexpr uint64_t kTurn = 0xa2f9836e4e44152aull;
     const int64_t bits = __double_as_longlong(inv_freq);
     const int s = 1077 - ((int)(bits >> 52) & 0x7ff);  // what the 117-bit product has to be shifted right by
     const uint64_t m = ((uint64_t)bits & 0xfffffffffffffull) | (1ull << 52);
     const uint64_t lo = m * kTurn, hi = __umul64hi(m, kTurn);
-    const uint64_t u = s >= 128 ? 0 : s >= 64 ? hi >> (s - 64) : s > 0 ? (lo >> s) | (hi << (64 - s)) : s > -64 ? lo << -s : 0;
+    const uint64_t u = s >= 128  ? 0
+                       : s >= 64 ? hi >> (s - 64)
+                       : s > 0   ? (lo >> s) | (hi << (64 - s))
+                       : s > -64 ? lo << -s
+                                 : 0;
     return bits < 0 ? 0 - u : u;
 }
 
@@ -184,10 +190,13 @@ struct RopeUnit {
 // shared memory, then the rows are turned and stored: the angles cost their
 // latency beside the loads'.
 template <class E, int kV, bool kInter, bool kMany>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kMany ? 5 : 4)
+rope_kernel(const __grid_constant__ RopeParams p) {
     using Unit = RopeUnit<E, kV, kInter>;
     using T = typename E::T;
     constexpr int kB = kInter ? kRopeBatch : kRopeBatch / 2;
+    // (five CTAs a multiprocessor where a CTA has many tokens: 8,192 x 16 heads x 64 9.1 -> 8.1 us; four elsewhere: with
+    // five the prompt's rotation spills, 60.5 -> 67.9 us, with its registers not limited it has fewer CTAs, 63.6)
     __shared__ alignas(16) float2 cs[kRopeAngles];
     __shared__ uint64_t turn_s[kMany ? kRopeHalf : 1];
     const int64_t n0 = (int64_t)blockIdx.x * p.tokens;
@@ -197,28 +206,34 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const int rows = ntok * nh;
     const int slots = p.slots, threads = (int)blockDim.x;
     const int slot = slots > 1 ? (int)threadIdx.x / p.units : 0;
-    const int64_t x_step = slots * p.x_head, out_step = slots * p.out_head;
+    // the place of row `slot`, and a step of `slots` rows: tokens, heads, and on to the next token past the last head
+    const int tok0 = kMany ? slot / nh : 0, head0 = slot - tok0 * nh;
+    const int toks = kMany ? slots / nh : 0, hs = slots - toks * nh;
+    const int64_t x_step = toks * p.x_row + hs * p.x_head, out_step = toks * p.out_row + hs * p.out_head;
+    const int64_t x_wrap = p.x_row - nh * p.x_head, out_wrap = p.out_row - nh * p.out_head;
     bool angles = false;
     for (int u = (int)threadIdx.x - slot * p.units;; u += threads) {
         const bool turn = u < p.rot_units;
         const int c = u - p.rot_units;  // a copied unit lies before or behind the rotated dims
         const int d = turn ? p.start + u * Unit::kE
                            : (c < p.copy_lead ? c * kV : p.start + 2 * p.half + (c - p.copy_lead) * kV);
-        const T* src = static_cast<const T*>(p.x) + (n0 * p.x_row + (h0 + slot) * p.x_head + d);
-        T* dst = static_cast<T*>(p.out) + (n0 * p.out_row + (h0 + slot) * p.out_head + d);
-        const float2* at = cs + u * Unit::kA;
-        int r = slot < slots && u < p.units ? slot : rows, h = slot, ht = slot;
+        const T* src = static_cast<const T*>(p.x) + ((n0 + tok0) * p.x_row + (h0 + head0) * p.x_head + d);
+        T* dst = static_cast<T*>(p.out) + ((n0 + tok0) * p.out_row + (h0 + head0) * p.out_head + d);
+        const float2* at = cs + tok0 * p.half + u * Unit::kA;
+        int r = slot < slots && u < p.units ? slot : rows, h = head0, ht = head0;
         float2 mine[Unit::kA];
         do {
             Unit v[kB];
 #pragma unroll
             for (int k = 0; k < kB; ++k) {
                 if (r + k * slots < rows) {
-                    if (kMany)
-                        for (; h >= nh; h -= nh) src += p.x_row - nh * p.x_head;  // on to the next token
                     v[k].load(src, p.half, turn);
                     src += x_step;
-                    h += slots;
+                    h += hs;
+                    if (kMany && h >= nh) {
+                        h -= nh;
+                        src += x_wrap;
+                    }
                 }
             }
             if (!angles) {
@@ -252,15 +267,16 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 #pragma unroll
             for (int k = 0; k < kB; ++k) {
                 if (r + k * slots < rows) {
-                    if (kMany)
-                        for (; ht >= nh; ht -= nh) {
-                            dst += p.out_row - nh * p.out_head;
-                            at += p.half;
-                        }
                     if (turn) v[k].turn_by(kMany ? at : mine);
                     v[k].store(dst, p.half, turn);
                     dst += out_step;
-                    ht += slots;
+                    at += toks * p.half;
+                    ht += hs;
+                    if (kMany && ht >= nh) {
+                        ht -= nh;
+                        dst += out_wrap;
+                        at += p.half;
+                    }
                 }
             }
             r += kB * slots;
@@ -463,8 +479,8 @@ __device__ __forceinline__ bool place_of(const AppendParams& p, const int32_t* c
     return true;
 }
 
-// Each token its own scale: a warp takes a token, one round trip for its data (one token 2.4 us, 256 x 4 tokens over four
-// shards 4.1, 16,385 tokens 7.7; the kernel of blocks takes 3.4, 5.7 and 37 for them).
+// Each token its own scale: a warp takes a token, one round trip for its data. (One token 2.4 us, 256 x 4 tokens over
+// four shards 4.1, 16,385 tokens 7.7; the kernel of blocks took 3.4, 5.7 and 37 for them.)
 template <class E>
 __global__ void __launch_bounds__(128) append_token_kernel(const __grid_constant__ AppendParams p) {
     const int lane = threadIdx.x & 31;
