@@ -911,6 +911,66 @@ def test_chain_captured_and_replayed():
         assert torch.equal(bits(a) if a.dtype == E4M3 else a, bits(b) if b.dtype == E4M3 else b)
 
 
+def test_two_graphs_share_a_workspace():
+    """Two captured decodes of different sizes in one workspace, replayed in turn on one stream."""
+    n = torch.cuda.get_device_properties(0).multi_processor_count
+    sizes = [(3, 64, 3000), (40, 16, 900)]
+    ws = torch.full((max(dcp.dcp_mla_cache8_decode_workspace_bytes(1, B, H, T, 0, 0, n) for B, H, T in sizes),), 0xFF,
+                    dtype=torch.uint8, device=DEV)
+    calls, want = [], []
+    for k, (B, H, T) in enumerate(sizes):
+        g = gen(50 + k)
+        kv, sc = make_cache(g, 1, B, T, 576, 1)
+        q = randn(g, B, H, 576).bfloat16()
+        lens = (torch.rand((B,), generator=g, device=DEV) * T).int()
+        want.append(dcp.mla_cache8_decode(q, kv, sc, lens, SCALE))
+        calls.append((q, kv, sc, lens))
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for c in calls:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(dcp.mla_cache8_decode(*c, SCALE, workspace=ws))
+        graphs.append(graph)
+    for _ in range(3):
+        for o, l in outs:
+            o.fill_(9.0)
+            l.fill_(9.0)
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for (o, l), (wo, wl) in zip(outs, want):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+def test_two_host_threads():
+    """The chain from two threads at once, each on a stream of its own, gives one thread's results."""
+    import threading
+    want = [chain(s, state) for state in [chain_state(16, 4, 2)] for s in range(3)]
+    states = [chain_state(16, 4, 2) for _ in range(2)]
+    torch.cuda.synchronize()
+    got, wrong = [None, None], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                got[i] = [chain(s, states[i]) for s in range(3)]
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # (seen by the main thread)
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not wrong, wrong
+    for mine in got:
+        for a, b in zip(mine, want):
+            for x, y in zip(a, b):
+                assert torch.equal(x, y)
+
+
 def test_on_other_streams():
     """The same decode and append on three streams at once, each with buffers of its own, as a stream object and as a
     raw handle; and outputs that are allocated on the stream that writes them."""
