@@ -359,16 +359,17 @@ struct Cursor {
 };
 
 // The CTAs' shares. All rows' tiles lie in a line that is cut evenly, but a row that begins in a share costs its CTA
-// a change of segments (q, sums, output) of about kChange tiles' time, so that each row is kChange places longer than
-// its tiles, which come last. (64 ragged rows x 16K: the slowest CTA 135 -> 130 us.)
-constexpr int kChange = 2;
-__device__ __forceinline__ int places(int tiles) { return tiles > 0 ? tiles + kChange : 0; }
+// a change of segments (q, sums, output) of `change` tiles' time, so that each row is `change` places longer than its
+// tiles, which come last. change is 2 with blocks of 64 heads, 1 with 32, 0 with 16. (128 heads, 64 ragged rows x 16K:
+// 154 us with 0, 150 with 1, 148 with 2 and with 3; 32 rows x 4096 42, 36, 34, 34. 32 heads, 250 ragged rows x 1024:
+// 40, 33, 34, 36. 16 heads, 64 rows x 16K: 66.9, 67.0, 67.9, 68.5.)
+__device__ __forceinline__ int places(int tiles, int change) { return tiles > 0 ? tiles + change : 0; }
 
 // What the join needs of a row: its first CTA range and its number of segments. Written by the CTA that has the
-// row's first tile (at place pre + kChange); for a row without a tile by the first CTA.
+// row's first tile (at place pre + change); for a row without a tile by the first CTA.
 __device__ __forceinline__ void tell_row(const DecodeBase& p, int b, int n, int pre, int g, int g_end, int per,
-                                         int range) {
-    pre += kChange;
+                                         int range, int change) {
+    pre += change;
     if (n == 0 && range == 0) p.row_info[b] = make_int2(0, 0);
     else if (n > 0 && pre >= g && pre < g_end) p.row_info[b] = make_int2(range, (pre + n - 1) / per - range + 1);
 }
@@ -592,7 +593,7 @@ __device__ __forceinline__ void issue_values(uint32_t ka, uint32_t pa, uint32_t 
 template <int kDk, int kNH, int kShards>
 __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ DecodeParams<kShards> p) {
     using S = Shape<kDk, kNH>;
-    constexpr int kHW = S::kHW;
+    constexpr int kHW = S::kHW, kChange = kNH / 32;
     constexpr uint32_t kIdS = (1u << 4) | ((uint32_t)(S::kRows >> 3) << 17) | (8u << 24);
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* const q_s = smem + 2 * S::kStage;
@@ -645,13 +646,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     if (!p.row_mode && p.B <= 32) {
         if (warp == kLoadWarp) {  // few rows: a lane a row, beside the others' set-up
             const int n = lane < p.B ? row_tiles(p, length) : 0;
-            int x = places(n);
+            int x = places(n, kChange);
 #pragma unroll 1
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, x, o);
                 if (lane >= o) x += y;
             }
-            const int total = __shfl_sync(0xffffffffu, x, 31), pre = x - places(n);
+            const int total = __shfl_sync(0xffffffffu, x, 31), pre = x - places(n, kChange);
             const int per = max((total + p.ranges - 1) / p.ranges, 1);
             const int64_t lo = (int64_t)range * per, hi = lo + per;
             g = lo < total ? (int)lo : total;
@@ -662,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             n_row = __shfl_sync(0xffffffffu, n, row);
             length = __shfl_sync(0xffffffffu, length, row);
             if (lane == 0 && here) sh->find[0] = row;
-            if (hblk == 0 && lane < p.B) tell_row(p, lane, n, pre, g, g_end, per, range);
+            if (hblk == 0 && lane < p.B) tell_row(p, lane, n, pre, g, g_end, per, range, kChange);
         }
     } else if (!p.row_mode) {
         int total = 0, n_mine = 0, pre_mine = 0, per_cta = 0;
@@ -678,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             for (int b0 = 0; b0 < p.B; b0 += kSoftThreads) {
                 if (pass == 0 || p.B > kSoftThreads) {
                     const int n = tid < kSoftThreads && b0 + tid < p.B ? row_tiles(p, row_length(p, b0 + tid)) : 0;
-                    int x = places(n);
+                    int x = places(n, kChange);
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
                         const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -691,17 +692,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     const int all = __reduce_add_sync(0xffffffffu, ws);
                     __syncthreads();
                     n_mine = n;
-                    pre_mine = base + before + x - places(n);
+                    pre_mine = base + before + x - places(n, kChange);
                     base += all;
                 }
                 if (pass == 1) {
-                    if (pre_mine <= g && g < pre_mine + places(n_mine) && g < g_end) {
+                    if (pre_mine <= g && g < pre_mine + places(n_mine, kChange) && g < g_end) {
                         sh->find[0] = b0 + tid;
                         sh->find[1] = g - pre_mine - kChange;
                         sh->find[2] = n_mine;
                     }
                     if (hblk == 0 && tid < kSoftThreads && b0 + tid < p.B)
-                        tell_row(p, b0 + tid, n_mine, pre_mine, g, g_end, per_cta, range);
+                        tell_row(p, b0 + tid, n_mine, pre_mine, g, g_end, per_cta, range, kChange);
                 }
             }
             if (pass == 0) total = base;
