@@ -77,6 +77,40 @@ def test_rope(dtype, interleaved, n, h, d, start, rot):
     assert torch.equal(y, got)
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_rope_random(seed):
+    """Random sizes, types, strides and places: into a new tensor, in place, or into a view of a wider one."""
+    import random
+    r = random.Random(seed)
+    g = gen(seed)
+    dtype = r.choice([torch.bfloat16, torch.bfloat16, torch.float16, torch.float32])
+    rot = r.choice([2, 6, 32, 64, 128, 256])
+    start, h = r.choice([0, 0, 8, 30, 128]), r.choice([1, 1, 2, 3, 7, 16, 40, 128])
+    d = start + rot + r.choice([0, 0, 8, 5])
+    n = min(r.choice([1, 2, 9, 100, 700, 5000]), max(1, 400000 // (h * d)))
+    pad, lead = r.choice([0, 0, 8, 3]), r.choice([0, 0, 16, 1])
+    buf = randn(g, n, h, lead + d + pad).to(dtype)
+    if r.random() < 0.3:  # heads outside tokens
+        buf = randn(g, h, n, lead + d + pad).to(dtype).transpose(0, 1)
+    x = buf[..., lead:lead + d]
+    pos = torch.randint(-1000, 200000, (n,), generator=g, device=DEV, dtype=r.choice([torch.int32, torch.int64]))
+    inv_freq, _ = dcp.mla_rope_inv_freq(rot)
+    kw = dict(start=start, interleaved=r.random() < 0.5, mscale=r.choice([1.0, 1.37]))
+    x0, whole = x.clone(), buf.clone()
+    how = r.choice(["new", "place", "view"])
+    if how == "new":
+        got = dcp.mla_rope(x, pos, inv_freq, **kw)
+        assert torch.equal(buf, whole)
+    elif how == "place":
+        got = dcp.mla_rope(x, pos, inv_freq, out=x, **kw)
+        assert torch.equal(buf[..., :lead], whole[..., :lead]) and torch.equal(buf[..., lead + d:], whole[..., lead + d:])
+    else:
+        other = torch.full((n, h, d + 24), 5.0, dtype=dtype, device=DEV)
+        got = dcp.mla_rope(x, pos, inv_freq, out=other[..., 8:8 + d], **kw)
+        assert (other[..., :8] == 5).all() and (other[..., 8 + d:] == 5).all()
+    check_rope(x0, pos, inv_freq, start, kw["interleaved"], kw["mscale"], got)
+
+
 def test_rope_far_and_negative_positions():
     x = randn(gen(0), 6, 4, 64)
     pos = torch.tensor([0, -1, (1 << 31) - 1, -(1 << 30), 10 ** 6 + 1, 163839], device=DEV)
