@@ -445,8 +445,16 @@ constexpr float kMagic = 12582912.f;
 constexpr int kMagicBits = 0x4B400000;
 constexpr int kRange = 1 << 21;  // scores beyond this (base-2 units) give NaN
 constexpr int kBias = 127 - 8;   // P is 2^8 at the block's largest
-// 2^(d - 8), 0 below 2^-127 (d is at most kLazy, or what it gives is not used)
-__device__ __forceinline__ float scale_of(int d) { return __int_as_float(max(d + kBias, 0) << 23); }
+// A token's weight in the sums is 2^(s - M) = P (1 / u) 2^(E - M - 8), of which the last two factors are taken 2^-kEven
+// and 2^kEven times. So no token whose score is within 29 of the row's largest is lost below fp32, whatever scales of
+// 2^-60 to 2^32 stand side by side: M is at most 93 above that score (kLow, and the largest scale), a factor of 0 has
+// E - M < -182, and s is at most E + 60.5.
+constexpr int kEven = 64;
+__device__ __forceinline__ float weight_of(int d) {  // (d is at most kLazy)
+    return __int_as_float(max(d + kBias + kEven, 0) << 23);
+}
+// 2^-x, for x > 126 zero (x >= -127)
+__device__ __forceinline__ float down_by(int x) { return __int_as_float(max(127 - x, 0) << 23); }
 
 using f32x2 = unsigned long long;
 __device__ __forceinline__ f32x2 pack2(float a, float b) {
@@ -1004,9 +1012,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     tmem_wait_ld();
                     tc_fence_before();
                     if (lane == 0) mbar_arrive(&sh->s_free);
-                    u = fmaxf(u, 7.888609e-31f);  // 2^-100: a scale of 0 is that of zeros
+                    // a scale of 0 is that of zeros, and counts as the smallest: a weight is at most 2^(kLazy + 60.5),
+                    // and fp32 holds the sum of as many as there can be tokens
+                    if (!(u >= 7.888609e-31f)) u = 8.6736174e-19f;  // 2^-100, 2^-60
                     const float c = u * p.scale_log2, lu = __log2f(u);
-                    const float ru = __fdividef(1.0f, u);
+                    const float ru = __fdividef(5.421010862e-20f, u);  // 2^-kEven / u
                     ru2 = pack2(ru, ru);
                     const f32x2 c2 = pack2(c, c), lu2 = pack2(lu, lu);
 #pragma unroll
@@ -1068,9 +1078,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 }
                 // Does the reference of some head have to move? Up when a score passes it by 2^kLazy; down only at
                 // once, when a segment's first scores lie far below the 0 that it begins at (sums would lose
-                // themselves below fp32's range). Each warp says so now and hears the others below. The scales
-                // 2^(E - M - 8) and P's share of the sums take the present reference: if it moves by `up`, everything
-                // is multiplied by 2^-up.
+                // themselves below fp32's range). Each warp says so now and hears the others below. If it moves by
+                // `up`, the scales 2^(E - M - 8) and what has been summed are multiplied by 2^-up. P's share of the
+                // sums waits for the reference that holds: M follows s + log2 u and the sums s alone, so that at the
+                // old one a token with a small scale can lie beyond fp32, and after a move by a large scale the sums
+                // before it can still count.
                 bool move = far > kLazy;
                 if (first && quad * 32 < valid) {
 #pragma unroll
@@ -1081,10 +1093,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     mbar_arrive(&sh->voted[group]);
                 }
                 int* const mine = red_i + quad * kNH + hb;  // this warp's words
-#pragma unroll
-                for (int h = 0; h < kHW; h += 2)
-                    l2[h / 2] = fma2(mul2(pack2(sv[h], sv[h + 1]), ru2), pack2(scale_of(d[h]), scale_of(d[h + 1])),
-                                     l2[h / 2]);
                 if (lane == 0) {
 #pragma unroll
                     for (int h = 0; h < kHW; h += 4)
@@ -1107,7 +1115,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                         const int m = m_s[r] + up;
                         // out of range, or NaN: the head's sums become NaN
                         const bool bad = m >= kMagicBits + kRange || m <= kMagicBits - kRange;
-                        a_s[r] = bad ? __int_as_float(0x7fffffff) : first || up > 100 ? 0.f : ex2(-(float)up);
+                        a_s[r] = bad ? __int_as_float(0x7fffffff) : down_by(max(up, 0));
                         m_s[r] = m;
                         up_s[r] = up;
                         if (lane == 0) sh->moved[group][t & 1] = 0;
@@ -1116,15 +1124,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     if (lane < kHW) sf -= up_s[hb + lane];
 #pragma unroll
                     for (int h = 0; h < kHW; h += 2) {
-                        // (a first tile has no sums before it; a move by more than 2^100 leaves nothing of them, and
-                        // then 2^E was out of range)
+                        // in two factors, for sums can be 2^93 and a move more than 2^126; a_s adds a NaN, or nothing
+                        // (a first tile has no sums before it)
                         const float2 f = *reinterpret_cast<const float2*>(a_s + hb + h);
                         const int2 up = *reinterpret_cast<const int2*>(up_s + hb + h);
-                        float x, y, zx, zy;
-                        unpack2(mul2(mul2(pack2(sv[h], sv[h + 1]), ru2),
-                                     pack2(scale_of(d[h] - up.x), scale_of(d[h + 1] - up.y))), zx, zy);
-                        unpack2(mul2(l2[h / 2], pack2(f.x, f.y)), x, y);
-                        l2[h / 2] = pack2(first || up.x > 100 ? zx + f.x : x, first || up.y > 100 ? zy + f.y : y);
+                        const int x = max(up.x, 0), y = max(up.y, 0);
+                        l2[h / 2] = fma2(pack2(f.x, f.y), 0ull,
+                                         mul2(mul2(l2[h / 2], pack2(down_by(x >> 1), down_by(y >> 1))),
+                                              pack2(down_by(x - (x >> 1)), down_by(y - (y >> 1)))));
+                        d[h] -= up.x;
+                        d[h + 1] -= up.y;
                     }
                     if (!first) {  // O as well, once the values before are added
                         ok = mbar_wait(&sh->o_done, (t - 1) & 1, abort_flag, p.status, p.wait_ns) && ok;
@@ -1147,6 +1156,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                         tmem_wait_st();
                     }
                 }
+#pragma unroll
+                for (int h = 0; h < kHW; h += 2)
+                    l2[h / 2] = fma2(mul2(pack2(sv[h], sv[h + 1]), ru2), pack2(weight_of(d[h]), weight_of(d[h + 1])),
+                                     l2[h / 2]);
                 // the buffer of P is free once the values before are added
                 if (t > 0) ok = mbar_wait(&sh->o_done, (t - 1) & 1, abort_flag, p.status, p.wait_ns) && ok;
                 // (warps of a group leave at one place: at the end of a tile, when a wait gave up anywhere)

@@ -12,7 +12,8 @@
  *   kv     [B, T, Dk] e4m3 codes (4 exponent, 3 mantissa bits, no infinity),
  *          contiguous, 16-byte aligned
  *   scales [B, ceil(T / block)] fp32, contiguous; positive (the append writes
- *          powers of two; the decode takes any from 2^-60 to 2^32)
+ *          powers of two; the decode takes any from 2^-60 to 2^32, in any order
+ *          along a row, and 0, which counts as 2^-60)
  * block is a power of two, at most DCP_MLA_CACHE8_BLOCK_MAX; 1 gives each token
  * its own scale.
  *

@@ -690,6 +690,119 @@ def test_decode_scales_over_their_whole_range(H):
         check_decode(q, kv, sc, lens, SCALE, 1, 1, block, 0, 0, out, lse)
 
 
+def levelled(g, levels, u, T, B=1):
+    """q [64 dims of 8 behind 512 zeros] and keys whose scores lie about levels[i] (base 2) in tile i of 128 tokens and
+    whose scale there is u[i]; latents of about 100 codes."""
+    lv = torch.tensor(levels, device=DEV, dtype=torch.float64).repeat_interleave(128)[:T]
+    us = torch.tensor(u, device=DEV, dtype=torch.float64).repeat_interleave(128)[:T]
+    codes = torch.cat((randn(g, B, T, 512) * 100, torch.zeros((B, T, 64), device=DEV)), 2).double()
+    top = max(float((lv.abs() / us).amax()) / 300, 2.0 ** -60)  # what q has to be for the largest code to be about 300
+    codes[..., 512:] = (lv / us / top)[:, None]
+    q = torch.zeros((B, 576), device=DEV, dtype=torch.float64)
+    q[:, 512:] = top / (64 * SCALE * math.log2(math.e))
+    kv = codes.clamp(-448, 448).float().to(E4M3)
+    return q, kv, us.float().expand(B, T).contiguous()
+
+
+def check_levelled(q, kv, sc, lens, out, lse, rows=(0,)):
+    """As check_decode for one shard in blocks of 1, where q splits exactly wherever a code is not zero: scores are fp32
+    sums of exact products, and nothing else moves the sums. A scale of 0 counts as 2^-60 among the 32 tokens of a
+    probability scale: its token has p u = p 2^-60 there (of codes of 0, or of 2^-60 times its codes), and the others
+    may lose 2^-18 of that like of any other token's."""
+    for b in rows:
+        n = int(lens[b])
+        codes, u = kv[b, :n].double(), sc[b, :n].double()
+        k, qb = codes * u[:, None], q[b].double()
+        want, wl = ref.attend(qb, k, SCALE)
+        s = SCALE * (qb @ k.T)
+        p = torch.exp(s - wl[:, None])
+        ds = SCALE * 2.0 ** -21 * (qb.abs() @ k.abs().T).amax(1, keepdim=True) + \
+            2.0 ** -22 * (s.abs().amax(1, keepdim=True) + 1)
+        lost = 2.0 ** -18 * 32 * (p * u.clamp(min=2.0 ** -60)).sum(1, keepdim=True) * codes[:, :512].abs().amax()
+        assert not out[b].isnan().any()
+        assert ((lse[b].double() - wl).abs() <= ds[:, 0] + 2.0 ** -20 * (wl.abs() + 1)).all(), f"row {b}"
+        tol = 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2 * ds + 2.0 ** -18) * (p @ k[:, :512].abs()) + lost
+        assert ((out[b].double() - want).abs() <= tol).all(), f"row {b}"
+
+
+@pytest.mark.parametrize("H", [16, 32, 64])
+@pytest.mark.parametrize("low", [-60.0, -91.0, -100.0, -128.0, -135.0, -150.0, -159.0, -161.0, -250.0])
+@pytest.mark.parametrize("scale", [2.0 ** -60, 0.0])
+def test_decode_a_zero_token_after_low_scores(H, low, scale):
+    """A tile whose largest score and scale lie about 2^low below the reference's start, then, in another tile of the
+    same segment, a token of zeros: score 0, and the scale that the append gives it. One row in one segment."""
+    g = gen(int(-low) + H)
+    q, kv, sc = levelled(g, [low + 7, low + 7], [2.0 ** -7] * 2, 256)
+    bits(kv)[0, 200] = 0
+    sc[0, 200] = scale
+    q = (q[:, None] * (1 + 0.02 * torch.rand((1, H, 1), generator=g, device=DEV))).bfloat16()
+    lens = torch.tensor([256], dtype=torch.int32, device=DEV)
+    out, lse = dcp.mla_cache8_decode(q, [kv], [sc], lens, SCALE)
+    check_levelled(q, kv, sc, lens, out, lse)
+
+
+@pytest.mark.parametrize("H,B", [(16, 16), (128, 16), (32, 40)])
+def test_decode_zero_tokens_among_low_scores_in_split_rows(H, B):
+    """The same in rows of many tiles that are split, a third of the tiles with a token of zeros; and over two shards,
+    whose partial results go through merge."""
+    g = gen(H)
+    n = 3000
+    tiles = -(-n // 128)
+    q, kv, sc = levelled(g, [-128.0] * tiles, [2.0 ** -7] * tiles, n, B)
+    zero = torch.arange(2 * 128 + 5, n, 3 * 128, device=DEV)
+    bits(kv)[:, zero] = 0
+    sc[:, zero] = 2.0 ** -60
+    q = q[:, None].expand(B, H, 576).bfloat16()
+    lens = torch.tensor([n - 7 * b for b in range(B)], dtype=torch.int32, device=DEV)
+    out, lse = dcp.mla_cache8_decode(q, [kv], [sc], lens, SCALE)
+    rows = [0, 1, B // 2, B - 1]
+    check_levelled(q, kv, sc, lens, out, lse, rows=rows)
+    two, two_sc = [kv, kv.clone()], [sc, sc.clone()]
+    parts = [dcp.mla_cache8_decode(q, [two[j] if j == k else None for j in range(2)],
+                                   [two_sc[j] if j == k else None for j in range(2)], 2 * lens, SCALE)
+             for k in range(2)]
+    merged, ml = dcp.merge([p[0] for p in parts], [p[1] for p in parts], True)
+    # the two halves are alike: the same output, rounded once more, and twice the sum
+    assert ((torch.cat(merged, 1).double() - out.double()).abs() <= 2.0 ** -7 * out.double().abs()).all()
+    assert ((torch.cat(ml, 1) - lse - math.log(2.0)).abs() <= 1e-4).all()
+
+
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("levels,exps", [
+    ((0.0, 8.0), (-60, -7)), ((0.0, 20.0), (-60, -7)), ((0.0, 20.0), (-60, 0)), ((-9.0, 0.0), (-60, 32)),
+    ((-9.0, 0.0), (-60, 31)), ((-40.0, 0.0), (-60, 32)), ((0.0, 133.0), (0, -60)), ((0.0, 160.0), (0, -60)),
+    ((0.0, 127.0), (0, -60)), ((0.0, 0.0), (-60, 32)), ((0.0, 0.0), (32, -60)), ((0.0, 30.0), (32, -30)),
+    ((0.0, 8.0), (-1000, -7)), ((0.0, 20.0), (-1000, 0)), ((-30.0, 0.0), (32, -1000))])
+def test_decode_a_move_of_scores_and_scales(H, levels, exps):
+    """Two tiles of one segment, each with its own score and its own scale: how far the reference moves goes by the one
+    times the other, the sums by the scores alone."""
+    g = gen(int(levels[1]) + exps[1] + H)
+    q, kv, sc = levelled(g, levels, [2.0 ** e for e in exps], 256)
+    q = q[:, None].expand(1, H, 576).bfloat16()
+    lens = torch.tensor([256], dtype=torch.int32, device=DEV)
+    out, lse = dcp.mla_cache8_decode(q, [kv], [sc], lens, SCALE)
+    check_levelled(q, kv, sc, lens, out, lse)
+
+
+@pytest.mark.parametrize("H,B", [(16, 64), (64, 40), (32, 1)])
+@pytest.mark.parametrize("order", ["up", "down", "steps"])
+def test_decode_scales_in_order_along_the_row(H, B, order):
+    """Scales over their whole range, one for each tile of 128 tokens: rising, falling, or the two ends in turn. All
+    scores are 0, so every token counts alike."""
+    g = gen(H + B)
+    exps = {"up": list(range(-60, 33, 8)), "down": list(range(32, -61, -8)),
+            "steps": [-60, 32, 31, -60, -59, 32] * 2}[order]
+    T = 128 * len(exps)
+    _, kv, sc = levelled(g, [0.0] * (len(exps) - 1) + [1.0], [2.0 ** e for e in exps], T, B)
+    bits(kv)[..., 512:] = 0
+    q = torch.zeros((B, H, 576), device=DEV)
+    q[..., 512:] = randn(g, B, H, 64)
+    q = q.bfloat16()
+    lens = torch.tensor([T - b for b in range(B)], dtype=torch.int32, device=DEV)
+    out, lse = dcp.mla_cache8_decode(q, [kv], [sc], lens, SCALE)
+    check_levelled(q, kv, sc, lens, out, lse, rows=sorted({0, 1 % B, B // 2, B - 1}))
+
+
 def test_decode_scores_out_of_range_are_nan():
     """Beyond 2^21 in units of ln 2: NaN, not a wrong number; the other heads and rows keep their bits."""
     g = gen(31)
