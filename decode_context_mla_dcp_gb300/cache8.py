@@ -174,6 +174,19 @@ def _meet(gap, n, h, d, row, head, orow, ohead) -> bool:
     return (n > 1 and row != orow) or (h > 1 and head != ohead) or step == 0 or not d <= gap % step <= step - d
 
 
+def _folded(n, h, d, row, head) -> bool:
+    """Whether [n, h, d] with strides (row, head, 1) has two elements in one place."""
+    if n > 1 and row < d or h > 1 and head < d:
+        return True
+    if n <= 1 or h <= 1 or head >= (n - 1) * row + d or row >= (h - 1) * head + d:
+        return False
+    # heads and rows interlock: a row i further meets the head whose place is next below or above its own
+    if n > h:
+        n, h, row, head = h, n, head, row
+    return any(i * row % head < d and i * row // head < h or
+               head - i * row % head < d and i * row // head + 1 < h for i in range(1, n))
+
+
 def mla_rope(x, positions, inv_freq, *, start: int = 0, interleaved: bool = True, mscale: float = 1.0, out=None,
              stream=None):
     """Rotary positions on dims [start, start + 2 len(inv_freq)) of every head.
@@ -183,7 +196,8 @@ def mla_rope(x, positions, inv_freq, *, start: int = 0, interleaved: bool = True
     pairs dims (2i, 2i + 1), otherwise (i, i + rot / 2). out: None allocates
     [N, H, D]; x itself rotates in place; another tensor or view (unit stride
     along D, not overlapping x) also receives the dims that are not rotated.
-    Returns out."""
+    What is written must not share elements between rows or heads (an expanded x
+    cannot be rotated in place). Returns out."""
     lib, torch = _ready()
     if x.dim() != 3:
         raise ValueError("x must be [N, H, D]")
@@ -204,26 +218,25 @@ def mla_rope(x, positions, inv_freq, *, start: int = 0, interleaved: bool = True
         raise ValueError("positions must be a contiguous int32 or int64 tensor [N] on x's device")
     if start < 0 or start > d:
         raise ValueError("start must be in [0, D]")
+    src = x.data_ptr()
+    if out is not None:
+        dst, orow, ohead = src, row, head
+        if out is not x:
+            orow, ohead, unit = out.stride() if out.dim() == 3 else (0, 0, 0)
+            if out.shape != x.shape or out.dtype != x.dtype or out.get_device() != index or (unit != 1 and d > 1):
+                raise ValueError("out must have x's shape, dtype and device, and unit stride along D")
+            dst = out.data_ptr()
+        if _folded(n, h, d, orow, ohead):
+            raise ValueError("out's rows or heads overlap each other")
+        if dst != src and n * h > 0 and _meet((dst - src) // x.element_size(), n, h, d, row, head, orow, ohead):
+            raise ValueError("out overlaps x: pass x itself to rotate in place")
     raw, inside = _on(index, stream)
     if inside is not None:
         with inside:
             return mla_rope(x, positions, inv_freq, start=start, interleaved=interleaved, mscale=mscale, out=out)
-    src = x.data_ptr()
     if out is None:
         out = torch.empty((n, h, d), dtype=x.dtype, device=x.device)
         dst, orow, ohead = out.data_ptr(), h * d, d
-    elif out is x:
-        dst, orow, ohead = src, row, head
-    else:
-        orow, ohead, unit = out.stride() if out.dim() == 3 else (0, 0, 0)
-        if out.shape != x.shape or out.dtype != x.dtype or out.get_device() != index or (unit != 1 and d > 1):
-            raise ValueError("out must have x's shape, dtype and device, and unit stride along D")
-        dst = out.data_ptr()
-        if n > 1 and h > 1 and ohead < (n - 1) * orow + d and orow < (h - 1) * ohead + d or \
-                n > 1 and orow < d or h > 1 and ohead < d:
-            raise ValueError("out's rows or heads overlap each other")
-        if dst != src and n * h > 0 and _meet((dst - src) // x.element_size(), n, h, d, row, head, orow, ohead):
-            raise ValueError("out overlaps x: pass x itself to rotate in place")
     rc = lib.dcp_mla_rope(src, row, head, positions.data_ptr(), wide, inv_freq.data_ptr(), n, h, d, start,
                           2 * inv_freq.shape[0], interleaved, mscale, dtype, dst, orow, ohead, raw)
     if rc:

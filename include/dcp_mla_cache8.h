@@ -72,7 +72,8 @@ const char* dcp_mla_cache8_strerror(int status);
  * with (a, b) = (start + 2i, start + 2i + 1) when `interleaved`, else
  * (start + i, start + i + rot / 2). The other dims are copied, or left alone
  * where out is x itself (rotating in place). out must either be x with the same
- * strides or not overlap it.
+ * strides or not overlap it, and no two rows or heads of out may overlap each
+ * other, in place neither (x that is only read may repeat rows or heads).
  *   inv_freq   [rot / 2] doubles on the device, radians per position. The angle
  *              is reduced to a fraction of a turn in 64-bit fixed point, so far
  *              positions keep what the double holds (2^-53 of the angle) and

@@ -247,3 +247,29 @@ def test_overlaps_of_rotated_views(n, h, d, x, out):
     elif x[1:] == out[1:] or max(a) < min(b) or max(b) < min(a):
         aside = n > 1 and h > 1 and x[1] < x[2]  # (heads outside rows: told apart only where the spans are)
         assert not said or aside
+
+
+@pytest.mark.parametrize("n,h,d,row,head", [
+    (4, 2, 64, 0, 64), (4, 2, 64, 128, 0), (1, 2, 64, 0, 64), (4, 1, 64, 64, 0), (1, 1, 64, 0, 0), (4, 2, 64, 64, 64),
+    (4, 2, 64, 128, 64), (2, 4, 64, 64, 128), (4, 2, 64, 63, 256), (4, 2, 64, 64, 256), (4, 2, 64, 64, 255),
+    (3, 2, 4, 8, 12), (2, 3, 4, 12, 8), (2, 2, 4, 12, 8), (2, 3, 4, 13, 8), (3, 3, 4, 20, 8), (3, 3, 4, 16, 8),
+    (3, 3, 4, 19, 8), (2, 5, 3, 7, 10), (5, 2, 3, 7, 10), (5, 5, 3, 7, 10), (4, 4, 1, 3, 4), (3, 4, 1, 4, 3),
+    (5, 4, 1, 4, 3), (0, 2, 4, 0, 4), (6, 7, 2, 11, 13), (12, 12, 2, 11, 13), (14, 12, 2, 11, 13)])
+def test_rows_and_heads_that_share_elements(n, h, d, row, head):
+    from decode_context_mla_dcp_gb300 import cache8
+    places = [i * row + j * head + k for i in range(n) for j in range(h) for k in range(d)]
+    assert cache8._folded(n, h, d, row, head) == (len(set(places)) < len(places))
+
+
+def test_rope_in_place_refuses_what_repeats_rows_or_heads():
+    """Every CTA would turn the same elements again: refused before anything looks at the device."""
+    freq, _ = dcp.mla_rope_inv_freq(64, device="cpu")
+    pos = torch.zeros((4,), dtype=torch.int64)
+    base = torch.zeros((400,))
+    for x in (torch.zeros((1, 2, 64)).expand(4, 2, 64), torch.zeros((4, 1, 64)).expand(4, 2, 64),
+              base.as_strided((4, 2, 64), (32, 192, 1)), base.as_strided((4, 2, 64), (64, 64, 1))):
+        with pytest.raises(ValueError, match="overlap"):
+            dcp.mla_rope(x, pos, freq, out=x)
+    for x in (base.as_strided((1, 2, 64), (0, 64, 1)), base.as_strided((4, 1, 64), (64, 0, 1))):
+        with pytest.raises(ValueError, match="CUDA"):  # (these share nothing: what is wrong is the device)
+            dcp.mla_rope(x, pos[:x.shape[0]], freq, out=x)
