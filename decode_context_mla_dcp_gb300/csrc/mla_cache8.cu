@@ -74,7 +74,10 @@ __device__ __forceinline__ float get_hi(uint32_t w) { return E::get((uint16_t)(w
 // the fraction's last place. In integers, for 64-bit floating point is slow here
 // (30,000 tokens of one head of 288 dims: 26.6 us with it, 19.6 without, 15.3 with
 // each CTA's frequencies taken into turns once): the double is m 2^(e - 1075), and
-// 1 / (2 pi) is kTurn 2^-66.
+// 1 / (2 pi) is kTurn 2^-66. A frequency that is not finite gives kNoTurns, whose
+// cosine and sine are NaN (a finite one that has these low bits is the last place off).
+constexpr uint32_t kNoTurns = 0x80000001u;
+constexpr float kNaN = __builtin_nanf("");
 __device__ __forceinline__ uint64_t turns_of(double inv_freq) {
     constexpr uint64_t kTurn = 0xa2f9836e4e44152aull;
     const int64_t bits = __double_as_longlong(inv_freq);
@@ -86,21 +89,25 @@ __device__ __forceinline__ uint64_t turns_of(double inv_freq) {
                        : s > 0   ? (lo >> s) | (hi << (64 - s))
                        : s > -64 ? lo << -s
                                  : 0;
-    return bits < 0 ? 0 - u : u;
+    const uint64_t turns = bits < 0 ? 0 - u : u;
+    if (s == 1077 - 0x7ff) return kNoTurns;
+    return (uint32_t)turns == kNoTurns ? turns - 1 : turns;
 }
 
 // cos and sin of position * frequency, from the top 32 bits of the wrapped
 // product read as half turns in [-1, 1).
 __device__ __forceinline__ void angle_of(int64_t pos, uint64_t turns, float* c, float* s) {
     const uint64_t phase = (uint64_t)pos * turns;
-    sincospif((float)(int32_t)(uint32_t)(phase >> 32) * 4.656612873077393e-10f, s, c);  // 2^-31
+    const float unit = (uint32_t)turns == kNoTurns ? kNaN : 4.656612873077393e-10f;  // 2^-31
+    sincospif((float)(int32_t)(uint32_t)(phase >> 32) * unit, s, c);
 }
 
 // The same for values that are then rounded to e4m3: the hardware's sine and
 // cosine, within 2^-21 of the true ones on [-pi, pi], against e4m3's 2^-4.
 __device__ __forceinline__ void coarse_angle_of(int64_t pos, uint64_t turns, float* c, float* s) {
     const uint64_t phase = (uint64_t)pos * turns;
-    const float x = (float)(int32_t)(uint32_t)(phase >> 32) * 1.4629180792671596e-9f;  // pi 2^-31
+    const float unit = (uint32_t)turns == kNoTurns ? kNaN : 1.4629180792671596e-9f;  // pi 2^-31
+    const float x = (float)(int32_t)(uint32_t)(phase >> 32) * unit;
     *s = __sinf(x);
     *c = __cosf(x);
 }

@@ -77,7 +77,7 @@ const char* dcp_mla_cache8_strerror(int status);
  *   inv_freq   [rot / 2] doubles on the device, radians per position. The angle
  *              is reduced to a fraction of a turn in 64-bit fixed point, so far
  *              positions keep what the double holds (2^-53 of the angle) and
- *              the rest is fp32.
+ *              the rest is fp32. An infinite or NaN one makes its pair NaN.
  *   positions  [N] int32, or int64 with pos64; any sign, below 2^31 in size
  *   dtype      DCP_DTYPE_BF16, DCP_DTYPE_F16 or DCP_DTYPE_F32; the arithmetic
  *              is fp32, rounded once
@@ -109,7 +109,8 @@ int dcp_mla_rope(const void* x, int64_t x_row, int64_t x_head, const void* posit
  * holds tokens of the row keeps the larger of that and its present scale; where
  * it grows, the tokens that it holds are requantised (exact but for values that
  * become subnormal, which round to nearest even). Codes round to nearest even;
- * NaN and infinities are stored as NaN.
+ * NaN and infinities are stored as NaN, and so is the pair of a frequency that is
+ * not finite.
  * Each block is written by one CTA in a fixed way: the result does not depend on
  * timing. One launch.
  *   shapes   0 <= N < 2^31, 0 <= B <= 65535, 0 <= T < 2^31, Dk 512 or 576

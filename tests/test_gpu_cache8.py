@@ -131,6 +131,30 @@ def test_rope_scaled_frequencies(scaling):
     check_rope(x, pos, f, 0, True, amp, dcp.mla_rope(x, pos, f, mscale=amp))
 
 
+@pytest.mark.parametrize("n,h", [(1, 3), (7, 40), (2000, 1)])
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_rope_of_frequencies_that_are_not_finite(n, h, interleaved):
+    """Their pairs are NaN, in the appended cache too; the other pairs keep their bits."""
+    g = gen(n)
+    x, latent = randn(g, n, h, 64).bfloat16(), randn(g, n, 512).bfloat16()
+    pos = torch.arange(n, device=DEV) + 5
+    good, _ = dcp.mla_rope_inv_freq(64)
+    bad = good.clone()
+    bad[3], bad[10], bad[31] = math.nan, math.inf, -math.inf
+    pairs = torch.arange(64, device=DEV)
+    odd = torch.isin(pairs // 2 if interleaved else pairs % 32, torch.tensor([3, 10, 31], device=DEV))
+    want = dcp.mla_rope(x, pos, good, interleaved=interleaved)
+    got = dcp.mla_rope(x, pos, bad, interleaved=interleaved)
+    assert got[..., odd].isnan().all() and torch.equal(got[..., ~odd], want[..., ~odd])
+    for block in (1, 16):
+        kv, sc = blank(1, 1, n + 5, 576, block)
+        lens = torch.full((1,), 5, dtype=torch.int32, device=DEV)
+        dcp.mla_cache8_append(latent, x[:, 0], kv, sc, lens, block=block, inv_freq=bad, interleaved=interleaved)
+        codes = kv[0][0, 5:].float()
+        assert codes[:, 512:][:, odd].isnan().all() and not codes[:, :512].isnan().any()
+        assert not codes[:, 512:][:, ~odd].isnan().any()
+
+
 def test_rope_into_a_view_leaves_the_rest():
     g = gen(2)
     buf = randn(g, 7, 12, 576).bfloat16()
