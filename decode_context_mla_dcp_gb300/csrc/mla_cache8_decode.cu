@@ -1013,8 +1013,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     tc_fence_before();
                     if (lane == 0) mbar_arrive(&sh->s_free);
                     // a scale of 0 is that of zeros, and counts as the smallest: a weight is at most 2^(kLazy + 60.5),
-                    // and fp32 holds the sum of as many as there can be tokens
-                    if (!(u >= 7.888609e-31f)) u = 8.6736174e-19f;  // 2^-100, 2^-60
+                    // and fp32 holds the sum of as many as there can be tokens (a NaN stays one)
+                    if (u < 7.888609e-31f) u = 8.6736174e-19f;  // 2^-100, 2^-60
                     const float c = u * p.scale_log2, lu = __log2f(u);
                     const float ru = __fdividef(5.421010862e-20f, u);  // 2^-kEven / u
                     ru2 = pack2(ru, ru);

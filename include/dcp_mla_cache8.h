@@ -165,9 +165,10 @@ int dcp_mla_cache8_read(const void* const* kv_ptrs, const float* const* scale_pt
  * 2^-9 of the head's largest exactly (and the others to 2^-16 of it).
  * Probabilities are split the same way at a power-of-two scale for each head and
  * 32 tokens, to 2^-8 relative like bf16. Products accumulate in fp32; output
- * rounded once to bf16. A NaN code that is visible, a NaN or infinity in q, or
- * scores beyond 2^21 in units of ln 2 make the (row, head) NaN; tokens that are
- * not visible may hold anything.
+ * rounded once to bf16. A NaN code or scale that is visible, or a NaN or infinity
+ * in q, makes the (row, head) NaN; tokens that are not visible may hold anything.
+ * In units of ln 2, scores above 2^21 make it NaN too, and one below -2^21 has
+ * weight 0 or makes it NaN.
  */
 int dcp_mla_cache8_decode(const void* q, int64_t q_row, int64_t q_head, const void* const* kv_ptrs,
                           const float* const* scale_ptrs, const int32_t* seq_lens, int cp, int64_t B, int H, int Dk,

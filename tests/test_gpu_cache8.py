@@ -915,6 +915,21 @@ def test_decode_nan_reaches_its_row_and_head_only():
     assert torch.equal(out[~bad], clean[0][~bad]) and torch.equal(lse[~bad], clean[1][~bad])
 
 
+@pytest.mark.parametrize("H,T,block", [(16, 200, 1), (64, 700, 16), (128, 256, 64)])
+def test_decode_a_visible_scale_that_is_nan(H, T, block):
+    """It reaches every head of its row (a NaN scale of what is not visible: test_decode)."""
+    g = gen(H)
+    kv, sc = make_cache(g, 1, 3, T, 576, block)
+    q = randn(g, 3, H, 576).bfloat16()
+    lens = torch.tensor([T, T - 1, T - 70], dtype=torch.int32, device=DEV)
+    clean = dcp.mla_cache8_decode(q, kv, sc, lens, SCALE, block=block)
+    sc[0][1, 100 // block] = math.nan
+    out, lse = dcp.mla_cache8_decode(q, kv, sc, lens, SCALE, block=block)
+    assert out[1].isnan().all() and lse[1].isnan().all()
+    for b in (0, 2):
+        assert torch.equal(out[b], clean[0][b]) and torch.equal(lse[b], clean[1][b])
+
+
 def test_decode_strided_q_given_outputs_and_flags():
     g = gen(16)
     B, H, T = 3, 40, 300
