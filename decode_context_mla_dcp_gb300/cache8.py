@@ -15,6 +15,8 @@ Optimize shared Output, Query, and Indexer/Top-K via peer memory", sglang
 Streams: everything runs on ``stream`` (default: the current stream of the
 tensors' device); what a call allocates is allocated for that stream. Wrong
 arguments raise ValueError, TypeError or DcpError before anything is launched.
+A batch of no rows is nothing to do; a cache of no tokens (T = 0) is refused, for
+its tensor has no address.
 """
 from __future__ import annotations
 
@@ -124,7 +126,8 @@ def _shards(caches, scales, block, interleave):
             raise ValueError("shards must be on one device, and scales [B, ceil(T / block)]")
         if not (c.is_contiguous() and s.is_contiguous()):
             raise ValueError("caches and scales must be contiguous")
-        kv[j], sc[j] = c.data_ptr(), s.data_ptr()
+        # (tensors of no rows have no address, and NULL is a shard that is not held: one that is never read stands in)
+        kv[j], sc[j] = (c.data_ptr(), s.data_ptr()) if B else (256 * (j + 1), 256 * (j + 1))
     if shape is None:
         raise ValueError("no shard is held here")
     return index, B, T, dk, kv, sc

@@ -1576,7 +1576,8 @@ extern "C" int dcp_mla_cache8_decode(const void* q, int64_t q_row, int64_t q_hea
     if (cp < 1 || cp > kCpMax || interleave < 1 || interleave > kMaxInterleave) return DCP_MLA_CACHE8_ERR_BAD_CP;
     if (window < 0 || sinks < 0 || (sinks > 0 && window == 0)) return DCP_MLA_CACHE8_ERR_BAD_WINDOW;
     if ((flags & ~(DCP_FLAG_PDL | DCP_MLA_FLAG_TEST_STALL)) != 0) return DCP_MLA_CACHE8_ERR_BAD_FLAGS;
-    if (q == nullptr || kv_ptrs == nullptr || scale_ptrs == nullptr || seq_lens == nullptr || out == nullptr)
+    if (kv_ptrs == nullptr || scale_ptrs == nullptr ||
+        (B > 0 && (q == nullptr || seq_lens == nullptr || out == nullptr)))
         return DCP_MLA_CACHE8_ERR_NULL_POINTER;
     if (!aligned(q, 4) || q_row % 2 != 0 || q_head % 2 != 0 || !aligned(out, 16) || !aligned(lse, 4) ||
         !aligned(seq_lens, 4) || !aligned(status, 4))

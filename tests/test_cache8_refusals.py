@@ -93,6 +93,14 @@ def test_decode_of_no_rows_is_nothing():
     dcp.dcp_mla_cache8_decode(**{**DECODE, "B": 0, "flags": dcp.DCP_FLAG_PDL | dcp.DCP_MLA_FLAG_TEST_STALL})
 
 
+def test_decode_of_no_rows_takes_null_for_what_rows_have():
+    """As empty tensors give it; what is wrong besides is refused all the same."""
+    empty = {**DECODE, "B": 0, "q": None, "seq_lens": None, "out": None, "lse": None, "workspace": None}
+    dcp.dcp_mla_cache8_decode(**empty)
+    refused(WINDOW, dcp.dcp_mla_cache8_decode, empty, sinks=4)
+    refused(NULL, dcp.dcp_mla_cache8_decode, empty, kv_ptrs=[None], scale_ptrs=[None])
+
+
 def test_workspace_bytes():
     ws = dcp.dcp_mla_cache8_decode_workspace_bytes
     assert ws(1, 8, 128, 4096, 0, 0, 152) >= 2 * 152 * 64 * 513 * 4

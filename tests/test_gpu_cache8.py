@@ -1005,6 +1005,42 @@ def test_decode_of_an_empty_cache_and_no_rows():
         dcp.mla_cache8_decode(q, [empty], [sc], torch.zeros((2,), dtype=torch.int32, device=DEV), SCALE)
 
 
+@pytest.mark.parametrize("cp,held", [(1, [0]), (3, [0, 1, 2]), (3, [1])])
+def test_a_batch_of_no_rows(cp, held):
+    """Every call over a cache of no rows does nothing and gives empty results."""
+    kv = [torch.empty((0, 64, 576), dtype=E4M3, device=DEV) if j in held else None for j in range(cp)]
+    sc = [torch.empty((0, 4), device=DEV) if j in held else None for j in range(cp)]
+    none = torch.empty((0,), dtype=torch.int32, device=DEV)
+    zero = torch.zeros((1,), dtype=torch.int32, device=DEV)
+    latent, rope = (torch.empty((0, w), dtype=torch.bfloat16, device=DEV) for w in (512, 64))
+    inv_freq, _ = dcp.mla_rope_inv_freq(64)
+    for cu in (None, zero):
+        dcp.mla_cache8_append(latent, rope, kv, sc, none, cu_new=cu, block=16, inv_freq=inv_freq)
+        assert dcp.mla_cache8_read(kv, sc, 0, starts=none, cu=cu, block=16).shape == (0, 576)
+    for kw in ({}, dict(window=9, sinks=2)):
+        out, lse = dcp.mla_cache8_decode(torch.empty((0, 16, 576), dtype=torch.bfloat16, device=DEV), kv, sc, none,
+                                         SCALE, block=16, **kw)
+        assert out.shape == (0, 16, 512) and lse.shape == (0, 16)
+    with pytest.raises(dcp.DcpError):  # packed tokens that belong to no row
+        dcp.mla_cache8_append(latent.new_zeros((3, 512)), rope.new_zeros((3, 64)), kv, sc, none, block=16)
+    with pytest.raises(dcp.DcpError):
+        dcp.mla_cache8_read(kv, sc, 3, block=16)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("what", ["append", "read"])
+def test_a_cache_of_no_tokens_is_refused(what):
+    """An empty tensor has no address, so that a shard without tokens cannot be told from one that is not held."""
+    kv, sc = [torch.empty((2, 0, 576), dtype=E4M3, device=DEV)], [torch.empty((2, 0), device=DEV)]
+    lens = torch.zeros((2,), dtype=torch.int32, device=DEV)
+    with pytest.raises(dcp.DcpError):
+        if what == "append":
+            dcp.mla_cache8_append(torch.zeros((2, 512), dtype=torch.bfloat16, device=DEV),
+                                  torch.zeros((2, 64), dtype=torch.bfloat16, device=DEV), kv, sc, lens)
+        else:
+            dcp.mla_cache8_read(kv, sc, 2)
+
+
 # ---- the chain, streams and graphs ------------------------------------------------------
 
 
