@@ -9,12 +9,15 @@
 // 8 or 16 bytes a lane and issued before any is used, and everything that a
 // token needs (its row, shard, place, angles) is found once and shared.
 // Measured, against a copy's 6.79 TB/s: rotating 64 of 192 dims of 8,192 x 64
-// heads 60.5 us (0.98), 128 x 128 heads x 64 into other rows 2.4 us; reading
-// 262,144 tokens back from four shards 68.7 us (0.97), 2,047 tokens 3.0 us;
-// appending 16,385 tokens in blocks of 64 8.6 us (0.48: two round trips before
+// heads 60.6 us (0.98), 128 x 128 heads x 64 into other rows 2.4 us; reading
+// 262,144 tokens back from four shards 68.4 us (0.97), 2,047 tokens 3.0 us;
+// appending 16,385 tokens in blocks of 64 8.7 us (0.48: two round trips before
 // the tokens' own, and two barriers), 256 x 4 tokens over four shards 5.7 us, one
-// token 2.1 us. Many tokens of one head are bound by the angles' arithmetic
-// (30,000 tokens of 288 dims, 128 rotated: 15.3 us against 5.1).
+// token 1.9 to 2.1 us. Many tokens of one head stay far from the floor: 30,000 of
+// 288 dims, 128 rotated, 15.3 us in halves and 12.7 interleaved against 5.1. A
+// CTA's loads, its angles and its stores follow one another. Moving the data alone
+// takes 9.2 and 6.7; the angles add 6 (without sine and cosine 4.6 and 3.4 of it
+// stay: positions, 64-bit products, shared memory).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -31,6 +34,7 @@ constexpr int kLatent = 512;
 constexpr int kCpMax = DCP_MLA_CACHE8_CP_MAX;
 constexpr int kMinExp = -60;              // a scale is at least 2^-60
 constexpr int64_t kMaxInterleave = 1 << 24;
+constexpr int kSms = 152;  // GB300's multiprocessors, for the launch rules below: with another count they cost time only
 
 // ---- element types -------------------------------------------------------------
 
@@ -486,8 +490,8 @@ __device__ __forceinline__ bool place_of(const AppendParams& p, const int32_t* c
     return true;
 }
 
-// Each token its own scale: a warp takes a token, one round trip for its data. (One token 2.4 us, 256 x 4 tokens over
-// four shards 4.1, 16,385 tokens 7.7; the kernel of blocks took 3.4, 5.7 and 37 for them.)
+// Each token its own scale: a warp takes a token, one round trip for its data. (One token 1.9 us, 256 x 4 tokens over
+// four shards 3.5, 16,385 tokens 7.1; the kernel of blocks took 3.0, 5.0 and 59 for them.)
 template <class E>
 __global__ void __launch_bounds__(128) append_token_kernel(const __grid_constant__ AppendParams p) {
     const int lane = threadIdx.x & 31;
@@ -801,7 +805,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
         scale_s[threadIdx.x] = s;
     }
     __syncthreads();
-    // eight loads of a thread in flight (a CTA's 32 tokens)
+    // all loads of a thread in flight (a CTA's 32 tokens: nine, or eight of a 512-wide cache)
     constexpr int kBatch = kReadTokens * kUnits / kReadThreads;
     const int total = ntok * kUnits;
     uint2 c[kBatch];
@@ -868,7 +872,7 @@ int launch_rope(RopeParams& p, int D, int64_t esize, cudaStream_t st) {
     // Rows side by side: a power of two, as counts of heads mostly are, so that no slot idles in the last step.
     // Tokens and heads of a CTA: at most about two batches of rows a thread, fewer where the call is small, so that
     // it still spreads over the GPU. More than one token only with all their heads.
-    int64_t want = p.N * p.H / (152 * 4);  // rows
+    int64_t want = p.N * p.H / (kSms * 4);  // rows
     int slots = 1;
     while (2 * slots * p.units <= kRopeThreads && (slots < want || slots * p.units < 32)) slots *= 2;
     p.slots = slots;
@@ -904,7 +908,7 @@ int launch_append(const AppendParams& p, int block, cudaStream_t st) {
         return launched();
     }
     // about as many CTAs as are resident at once (32 warps a multiprocessor), an odd number
-    const int warps = block <= 16 ? 4 : block / 4, resident = 152 * (32 / warps) + 1;
+    const int warps = block <= 16 ? 4 : block / 4, resident = kSms * (32 / warps) + 1;
     const unsigned grid = (unsigned)(p.N < resident ? p.N : resident);
     if (p.N > resident && p.B <= kCountedRows) {
         if (warps == 4) append_block_kernel<E, 4, true><<<grid, 128, 0, st>>>(p);
@@ -1072,7 +1076,7 @@ extern "C" int dcp_mla_cache8_read(const void* const* kv_ptrs, const float* cons
     p.interleave = (uint32_t)interleave;
     // 32 tokens a CTA, 8 where that would leave multiprocessors idle (2,047 tokens: 3.0 us with 8, 3.6 with 32; 8,192
     // tokens: 5.3 and 4.5; 262,144: 99 and 69)
-    p.tokens = N >= 152 * kReadTokens ? kReadTokens : 8;
+    p.tokens = N >= kSms * kReadTokens ? kReadTokens : 8;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dtype == DCP_DTYPE_BF16) return launch_read<Bf16>(p, Dk, st);
     if (dtype == DCP_DTYPE_F16) return launch_read<F16>(p, Dk, st);
