@@ -43,10 +43,19 @@
 // operands take 2,150 of its cycles a tile, the tile itself 580, the softmax some
 // 900. Two tiles, q and P fill shared memory, S, O and the scales TMEM (456 of 512
 // columns), so there is no third stage and one CTA a multiprocessor.
-//   measured, 128 heads: 64 ragged rows of up to 16K tokens 144 us (1.01 PFLOP/s as
-//   the operator counts them, twice that on the tensor cores); 8 rows x 4096 tokens
-//   23.2 us, of which 16.4 are the main kernel (4 tiles a CTA between 10,000 cycles
-//   to begin and 6,000 to end) and 6 the join; 16 heads, 200 tokens: 8.1 us.
+//   measured, 128 heads: 64 ragged rows of up to 16K tokens 142 to 151 us with their
+//   lengths, 280 to 286 us for 10^6 tokens (146.3 us, 1.00 PFLOP/s as the operator
+//   counts them, twice that on the tensor cores, over three sets of lengths; 148 for
+//   seconds on end, at the power limit); 8 rows x 4096 tokens 23.5 us, of which 16.4
+//   are the main kernel (4 tiles a CTA between 10,000 cycles to begin and 6,000 to
+//   end) and 6 the join; 16 heads, 200 tokens: 8.1 to 8.4 us. One shard of 8 held,
+//   8 rows x 4096 of its tokens: 24.0 us.
+// With 16 and 32 heads 64 ragged rows x 16K take 67 and 71 us against 45 of their
+// bytes; where the rest goes has not been measured.
+//
+// Rounding to fewer bits: q's and P's parts as above. log2 u, exp2 and the division by u
+// are the hardware's (two units of the last place, 2^-22, two units), far below P's
+// 2^-8; the sums are those of the P that is not rounded yet, in fp32.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -1544,7 +1553,9 @@ int run_decode(const DecodeBase& base, const void* const* kv, const float* const
 
 // Rows of at most two tiles are not worth splitting: a join costs as much. (128 heads x 256 tokens: 12.6 us whole, 15.3
 // split for 8 rows, 34 and 41 for 200. Of four tiles: 16.6 whole and 15.7 split for 8 rows x 512, 17.8 and 20.4 for 64;
-// the lengths are on the device, and a call with uneven ones wants the split.)
+// the lengths are on the device, and a call with uneven ones wants the split.) Shards that are not held count too: one
+// of 8 with 256 tokens a row is split, 16.2 us for 8 rows and 41.9 for 200, where the same tokens alone take 12.0 and
+// 33.1.
 bool whole_rows(int cp, int64_t T, int64_t window, int64_t sinks) {
     const int64_t seen = window > 0 && window < T ? window : T, first = sinks < T ? sinks : T;
     const int64_t most = (seen + kTile - 1) / kTile + (window > 0 ? (first + kTile - 1) / kTile : 0);

@@ -105,7 +105,9 @@ int dcp_mla_rope(const void* x, int64_t x_row, int64_t x_head, const void* posit
  *            dcp_mla_rope: k_rope is rotated (fp32, not rounded in between, the
  *            sine and cosine to 2^-21)
  * Scales. A block's scale is the smallest power of two s with |x| <= 448 s over
- * the finite values of its new tokens, at least 2^-60. A block that already
+ * the finite values of its new tokens, at least 2^-60 (and up to 2^120: values
+ * beyond 448 * 2^32 are cached and read back, but lie outside what the decode
+ * takes). A block that already
  * holds tokens of the row keeps the larger of that and its present scale; where
  * it grows, the tokens that it holds are requantised (exact but for values that
  * become subnormal, which round to nearest even). Codes round to nearest even;
