@@ -1041,6 +1041,83 @@ def test_a_cache_of_no_tokens_is_refused(what):
             dcp.mla_cache8_read(kv, sc, 2)
 
 
+@pytest.mark.parametrize("H,T,window", [(200, 300, 0), (1000, 300, 0), (1024, 900, 200), (1024, 128, 0)])
+def test_decode_many_heads(H, T, window):
+    g = gen(H + T)
+    kv, sc = make_cache(g, 1, 3, T, 576, 4)
+    q = randn(g, 3, H, 576).bfloat16()
+    lens = torch.tensor([T, 77, 0], dtype=torch.int32, device=DEV)
+    out, lse = dcp.mla_cache8_decode(q, kv, sc, lens, SCALE, block=4, window=window)
+    check_decode(q, kv, sc, lens, SCALE, 1, 1, 4, window, 0, out, lse)
+
+
+@pytest.mark.parametrize("scale", [0.0, -SCALE])
+@pytest.mark.parametrize("H", [16, 64])
+def test_decode_scale_of_zero_or_below(H, scale):
+    g = gen(H)
+    kv, sc = make_cache(g, 2, 2, 300, 576, 1)
+    q = randn(g, 1, 1, 576).bfloat16().expand(2, H, 576)  # (rows and heads that q repeats)
+    lens = torch.tensor([600, 131], dtype=torch.int32, device=DEV)
+    out, lse = dcp.mla_cache8_decode(q, kv, sc, lens, scale)
+    check_decode(q, kv, sc, lens, scale, 2, 1, 1, 0, 0, out, lse)
+
+
+def test_lengths_windows_and_places_at_their_limits():
+    """Positions up to 2^31 - 1 over caches that end long before: nothing is written or read there, and the decode sees
+    the first tokens alone."""
+    g = gen(77)
+    B, T, cp, big = 3, 300, 3, (1 << 31) - 1
+    kv, sc = make_cache(g, cp, B, T, 576, 4)
+    sc = [torch.exp2(torch.ceil(torch.log2(s))) for s in sc]
+    before = [bits(x).clone() for x in kv], [x.clone() for x in sc]
+    q = randn(g, B, 32, 576).bfloat16()
+    lens = torch.tensor([big, big - 100, 40], dtype=torch.int32, device=DEV)
+    for il in (1, 16, 1 << 24):
+        for window, sinks in ((5, 9), (1, 1 << 40), (1 << 40, 0), (big, 3), (1 << 62, 1 << 62)):
+            out, lse = dcp.mla_cache8_decode(q, kv, sc, lens, SCALE, block=4, interleave=il, window=window,
+                                             sinks=sinks)
+            for b in range(B):
+                n = int(lens[b])
+                rows, codes = [], []
+                for j in range(cp):  # what shard j holds, by position
+                    t = torch.arange(T, device=DEV)
+                    pos = (t // il * cp + j) * il + t % il
+                    see = (pos < n) & ((pos >= n - window) | (pos < sinks))
+                    rows.append(kv[j][b, see].double() * sc[j][b, t[see] // 4].double()[:, None])
+                k = torch.cat(rows)
+                want, wl = ref.attend(q[b].double(), k, SCALE)
+                if not len(k):
+                    assert (out[b] == 0).all() and (lse[b] == -math.inf).all()
+                    continue
+                # as in check_decode, with every rounding at its largest over these caches
+                mass = torch.exp(SCALE * (q[b].double() @ k.T) - wl[:, None]) @ k[:, :512].abs()
+                assert ((lse[b].double() - wl).abs() <= 1e-3).all()
+                assert ((out[b].double() - want).abs() <= 2.0 ** -7 * mass + 2.0 ** -8 * want.abs() + 1e-2).all()
+        latent, rope = randn(g, B * 50, 512).bfloat16(), randn(g, B * 50, 64).bfloat16()
+        far = torch.full((B,), big - 20, dtype=torch.int32, device=DEV)
+        for block in (1, 4):
+            scales = sc if block == 4 else [torch.ones((B, T), device=DEV) for _ in range(cp)]
+            dcp.mla_cache8_append(latent, rope, kv, scales, far, block=block, interleave=il)
+        got = torch.full((B * 50, 576), 3.0, device=DEV)
+        dcp.mla_cache8_read(kv, sc, B * 50, starts=far, block=4, interleave=il, dtype=torch.float32, out=got)
+        assert (got == 3).all()
+    for x, y in zip(kv + sc, before[0] + before[1]):
+        assert torch.equal(bits(x) if x.dtype == E4M3 else x, y)
+
+
+def test_decode_65535_rows():
+    g = gen(65535)
+    B, H, T = 65535, 16, 300
+    one = (randn(g, 1, T, 576) * 30).clamp(-448, 448).to(E4M3)
+    kv = [bits(one).expand(B, T, 576).contiguous().view(E4M3)]
+    sc = [(2.0 ** -5 * (1 + torch.rand((B, T), generator=g, device=DEV)))]
+    q = randn(g, 1, H, 576).bfloat16().expand(B, H, 576)
+    lens = (torch.arange(B, device=DEV) * 7919 % (T + 1)).int()
+    out, lse = dcp.mla_cache8_decode(q, kv, sc, lens, SCALE)
+    check_decode(q, kv, sc, lens, SCALE, 1, 1, 1, 0, 0, out, lse, rows=[0, 1, 2, 511, 512, 40000, 65533, 65534])
+    assert not out.isnan().any() and ((lse == -math.inf) == (lens == 0)[:, None]).all()
+
+
 # ---- the chain, streams and graphs ------------------------------------------------------
 
 
