@@ -305,8 +305,8 @@ def mla_cache8_read(caches, scales, total: int, *, starts=None, cu=None, block: 
     total: packed tokens in all; cu: int32 [B + 1] (None: total / B each); starts:
     int32 [B] (None: 0). dtype: bf16 (default), fp16 or fp32. out: None allocates
     [total, Dk]; or a tensor of that shape, unit inner stride, rows and base on
-    16-byte boundaries. Tokens that no held shard has are left as they were.
-    Returns out."""
+    16-byte boundaries. Tokens that no held shard has are left as they were (in
+    a tensor that the call allocates: undefined). Returns out."""
     lib, torch = _ready()
     index, B, T, dk, kv, sc = _shards(caches, scales, block, interleave)
     if total < 0:

@@ -166,8 +166,9 @@ int dcp_mla_cache8_read(const void* const* kv_ptrs, const float* const* scale_pt
  * e4m3 parts at a power-of-two scale per head, which holds every value above
  * 2^-9 of the head's largest exactly (and the others to 2^-16 of it).
  * Probabilities are split the same way at a power-of-two scale for each head and
- * 32 tokens, to 2^-8 relative like bf16. Products accumulate in fp32; output
- * rounded once to bf16. A NaN code or scale that is visible, or a NaN or infinity
+ * 32 tokens, to 2^-8 relative like bf16. Products accumulate in fp32, and log2 of
+ * a token's scale is added to its score in fp32 (so that scales near 2^-60 leave a
+ * score some 2^-18); output rounded once to bf16. A NaN code or scale that is visible, or a NaN or infinity
  * in q, makes the (row, head) NaN; tokens that are not visible may hold anything.
  * In units of ln 2, scores above 2^21 make it NaN too, and one below -2^21 has
  * weight 0 or makes it NaN.
