@@ -11,8 +11,8 @@
 // Measured, against a copy's 6.79 TB/s: rotating 64 of 192 dims of 8,192 x 64
 // heads 60.6 us (0.98), 128 x 128 heads x 64 into other rows 2.4 us; reading
 // 262,144 tokens back from four shards 68.4 us (0.97), 2,047 tokens 3.0 us;
-// appending 16,385 tokens in blocks of 64 8.7 us (0.48: two round trips before
-// the tokens' own, and two barriers), 256 x 4 tokens over four shards 5.7 us, one
+// appending 16,385 tokens in blocks of 64 9.2 us (0.45: two round trips before
+// the tokens' own, and two barriers), 256 x 4 tokens over four shards 5.6 us, one
 // token 1.9 to 2.1 us. Many tokens of one head stay far from the floor: 30,000 of
 // 288 dims, 128 rotated, 15.3 us in halves and 12.7 interleaved against 5.1. A
 // CTA's loads, its angles and its stores follow one another. Moving the data alone
@@ -106,14 +106,20 @@ __device__ __forceinline__ void angle_of(int64_t pos, uint64_t turns, float* c, 
     sincospif((float)(int32_t)(uint32_t)(phase >> 32) * unit, s, c);
 }
 
-// The same for values that are then rounded to e4m3: the hardware's sine and
-// cosine, within 2^-21 of the true ones on [-pi, pi], against e4m3's 2^-4.
-__device__ __forceinline__ void coarse_angle_of(int64_t pos, uint64_t turns, float* c, float* s) {
-    const uint64_t phase = (uint64_t)pos * turns;
-    const float unit = (uint32_t)turns == kNoTurns ? kNaN : 1.4629180792671596e-9f;  // pi 2^-31
-    const float x = (float)(int32_t)(uint32_t)(phase >> 32) * unit;
-    *s = __sinf(x);
-    *c = __cosf(x);
+// The same to fp32's last places, for values that are then rounded to a coarse grid, where a small error moves the few
+// that lie beside a boundary a whole step: the quarter of a turn is taken out of the integer first, so that its
+// conversion keeps 2^-27 of a half turn. (Keys on another code than in 64 bits: 1 to 4 in 260,000 to 1,050,000, the plain
+// form in 32 bits 0 to 8; 1 to 12 with the form above, 6 to 29 with the hardware's sine and cosine, which saved 4% of a
+// prompt's append in blocks of 64, 7% with a scale each.)
+__device__ __forceinline__ void fine_angle_of(int64_t pos, uint64_t turns, float* c, float* s) {
+    const uint32_t phase = (uint32_t)(((uint64_t)pos * turns) >> 32);
+    const float unit = (uint32_t)turns == kNoTurns ? kNaN : 4.656612873077393e-10f;  // 2^-31
+    const uint32_t quarter = (phase + 0x20000000u) >> 30;
+    float x, y;
+    sincospif((float)(int32_t)(phase - (quarter << 30)) * unit, &y, &x);
+    const float u = quarter & 1 ? y : x, v = quarter & 1 ? x : y;
+    *c = (quarter + 1) & 2 ? -u : u;
+    *s = quarter & 2 ? -v : v;
 }
 
 // ---- rotary positions ------------------------------------------------------------
@@ -394,7 +400,7 @@ __device__ __forceinline__ void turn_token(const AppendParams& p, uint32_t rope,
         t->r1 = get_hi<E>(rope);
         if (rotate) {
             float c, s;
-            coarse_angle_of(pos, turns, &c, &s);
+            fine_angle_of(pos, turns, &c, &s);
             c *= p.mscale;
             s *= p.mscale;
             const float a = t->r0, b = t->r1;
@@ -491,7 +497,7 @@ __device__ __forceinline__ bool place_of(const AppendParams& p, const int32_t* c
 }
 
 // Each token its own scale: a warp takes a token, one round trip for its data. (One token 1.9 us, 256 x 4 tokens over
-// four shards 3.5, 16,385 tokens 7.1; the kernel of blocks took 3.0, 5.0 and 59 for them.)
+// four shards 3.7, 16,385 tokens 7.5; the kernel of blocks took 3.0, 5.0 and 59 for them.)
 template <class E>
 __global__ void __launch_bounds__(128) append_token_kernel(const __grid_constant__ AppendParams p) {
     const int lane = threadIdx.x & 31;
@@ -531,10 +537,10 @@ __global__ void __launch_bounds__(128) append_token_kernel(const __grid_constant
 // it: CTA c looks at tokens c, c + G, c + 2G, ... (a binary search each) with G odd,
 // so that first tokens, which stand a power of two apart, spread over the CTAs; yet
 // some CTAs find several. Counting is for up to kCountedRows rows and calls of more
-// tokens than CTAs are resident. (16,385 tokens of 5 rows in blocks of 64: 8.6 us
-// counted, 14.4 by first tokens; of 256 rows over four shards in blocks of 16 13.9
-// and 23.4; of 1,024 rows over two shards in blocks of 64 42.8 and 25.3; 256 x 4
-// tokens over four shards 6.3 and 5.6; 300 tokens of 256 rows 6.0 and 4.8.)
+// tokens than CTAs are resident. (16,385 tokens of 5 rows in blocks of 64: 9.2 us
+// counted, 15.5 by first tokens; of 256 rows over four shards in blocks of 16 16.5
+// and 23.5; of 1,024 rows over two shards in blocks of 64 50.2 and 26.5; 256 x 4
+// tokens over four shards 6.1 and 5.6; 300 tokens of 256 rows 4.6 and 4.4.)
 constexpr int kTok = 4;
 constexpr int kCuShared = 1024;
 constexpr int kCountedRows = 512;

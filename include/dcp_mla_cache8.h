@@ -102,8 +102,7 @@ int dcp_mla_rope(const void* x, int64_t x_row, int64_t x_head, const void* posit
  *   k_rope   [N, 64] of the same type, row stride rope_row (a multiple of 8),
  *            16-byte aligned; NULL with Dk = 512
  *   inv_freq NULL: k_rope is taken as it is; or [32] doubles as for
- *            dcp_mla_rope: k_rope is rotated (fp32, not rounded in between, the
- *            sine and cosine to 2^-21)
+ *            dcp_mla_rope: k_rope is rotated (fp32, not rounded in between)
  * Scales. A block's scale is the smallest power of two s with |x| <= 448 s over
  * the finite values of its new tokens, at least 2^-60 (and up to 2^120: values
  * beyond 448 * 2^32 are cached and read back, but lie outside what the decode

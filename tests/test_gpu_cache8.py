@@ -280,6 +280,33 @@ def test_append(case):
         assert same.all()
 
 
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("block", [1, 64])
+def test_append_rotates_to_the_last_places(interleaved, block):
+    """Codes of rotated keys lie within half a step and 2^-22 of the pair of the 64-bit value. In units of 2^-24 of the
+    pair: the angle 0.41 (2^-27 of a half turn), sine and cosine 1, the factor 0.5, the products and their sum 1."""
+    g = gen(block)
+    n, mscale = 60000, 1.25
+    latent, rope = randn(g, n, 512).bfloat16(), (3 * randn(g, n, 64)).bfloat16()
+    inv_freq, _ = dcp.mla_rope_inv_freq(64)
+    kv, sc = blank(1, 1, n + 5, 576, block)
+    lens = torch.full((1,), 5, dtype=torch.int32, device=DEV)
+    sc[0][0, 0] = 1.0
+    dcp.mla_cache8_append(latent, rope, kv, sc, lens, block=block, inv_freq=inv_freq, interleaved=interleaved,
+                          mscale=mscale)
+    x = rope[:, None].double()
+    want = ref.rotate(x, torch.arange(5, n + 5, device=DEV), inv_freq, 0, interleaved, mscale)[:, 0]
+    a = x[:, 0].abs()
+    pair = a.unflatten(-1, (32, 2)).sum(-1).repeat_interleave(2, -1) if interleaved else \
+        (a[:, :32] + a[:, 32:]).repeat(1, 2)
+    scale = sc[0][0, torch.arange(5, n + 5, device=DEV) // block].double()[:, None]
+    codes = kv[0][0, 5:, 512:].double()
+    step = torch.exp2((torch.frexp(want.abs() / scale)[1] - 1).clamp(min=-6).double() - 3)
+    # (above a power of two the grid is coarser than below: the larger of the two steps where the code is one)
+    step = torch.maximum(step, torch.exp2((torch.frexp(codes.abs())[1] - 1).clamp(min=-6).double() - 3))
+    assert ((codes - want / scale).abs() <= step / 2 + 2.0 ** -22 * mscale * pair / scale).all()
+
+
 def test_append_even_and_cu_agree_and_strides():
     g = gen(5)
     B, per, T = 6, 3, 64
