@@ -12,7 +12,8 @@ binding: ``dcp_lse_reduce`` / ``dcp_lse_reduce_ex`` take raw pointers (or
 tensors) exactly like the C calls, and ``merge`` derives the sizes and strides
 from torch tensors and allocates the outputs. ``mla_cache8_append``,
 ``mla_cache8_read``, ``mla_cache8_decode`` and ``mla_rope`` (cache8.py) work on an
-8-bit latent cache.
+8-bit latent cache; ``mla_cache8_pages_update``, ``mla_cache8_pages_compact`` and
+``mla_cache8_pages_copy`` (cache8_pages.py) on the pages of one.
 """
 from __future__ import annotations
 
@@ -31,8 +32,12 @@ from ._binding import (DCP_DTYPE_BF16, DCP_DTYPE_F16, DCP_FLAG_LSE_FIRST, DCP_FL
                        dcp_mla_decode_workspace_bytes, library_path, load,
                        DCP_DTYPE_F32, DCP_MLA_CACHE8_BLOCK_MAX, DCP_MLA_CACHE8_CP_MAX, dcp_mla_rope,
                        dcp_mla_cache8_append, dcp_mla_cache8_read, dcp_mla_cache8_decode,
-                       dcp_mla_cache8_decode_workspace_bytes, dcp_mla_cache8_strerror)
+                       dcp_mla_cache8_decode_workspace_bytes, dcp_mla_cache8_strerror,
+                       DCP_MLA_PAGE_MAX, DCP_MLA_PAGE_MIN, DCP_MLA_PAGES_POOLS_MAX, dcp_mla_pages_update,
+                       dcp_mla_pages_update_workspace_bytes, dcp_mla_pages_compact,
+                       dcp_mla_pages_compact_workspace_bytes, dcp_mla_pages_copy)
 from .cache8 import mla_cache8_append, mla_cache8_decode, mla_cache8_read, mla_rope, mla_rope_inv_freq
+from .cache8_pages import mla_cache8_pages_compact, mla_cache8_pages_copy, mla_cache8_pages_update
 
 __all__ = ["dcp_lse_reduce", "dcp_lse_reduce_ex", "dcp_lse_reduce_strerror", "dcp_lse_reduce_version", "merge",
            "dcp_mla_decode_partial", "dcp_mla_decode_smem_bytes", "mla_decode_partial", "DCP_MLA_SPLIT_MAX",
@@ -47,7 +52,11 @@ __all__ = ["dcp_lse_reduce", "dcp_lse_reduce_ex", "dcp_lse_reduce_strerror", "dc
            "mla_rope", "mla_rope_inv_freq", "mla_cache8_append", "mla_cache8_read", "mla_cache8_decode",
            "dcp_mla_rope", "dcp_mla_cache8_append", "dcp_mla_cache8_read", "dcp_mla_cache8_decode",
            "dcp_mla_cache8_decode_workspace_bytes", "dcp_mla_cache8_strerror", "DCP_DTYPE_F32",
-           "DCP_MLA_CACHE8_BLOCK_MAX", "DCP_MLA_CACHE8_CP_MAX"]
+           "DCP_MLA_CACHE8_BLOCK_MAX", "DCP_MLA_CACHE8_CP_MAX",
+           "mla_cache8_pages_update", "mla_cache8_pages_compact", "mla_cache8_pages_copy",
+           "dcp_mla_pages_update", "dcp_mla_pages_update_workspace_bytes", "dcp_mla_pages_compact",
+           "dcp_mla_pages_compact_workspace_bytes", "dcp_mla_pages_copy",
+           "DCP_MLA_PAGE_MIN", "DCP_MLA_PAGE_MAX", "DCP_MLA_PAGES_POOLS_MAX"]
 
 
 def algorithmic_bytes(cp: int, B: int, H: int, D: int, elem: int = 2, skipped_payload_rows: int = 0) -> int:

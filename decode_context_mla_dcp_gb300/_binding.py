@@ -28,9 +28,14 @@ EXPORTED_SYMBOLS = ("dcp_lse_reduce", "dcp_lse_reduce_ex", "dcp_lse_reduce_strer
                     "dcp_mla_decode_partial", "dcp_mla_decode_smem_bytes", "dcp_mla_decode_workspace_bytes",
                     "dcp_mla_decode", "dcp_mla_decode_noalloc", "dcp_mla_decode_kernel", "dcp_mla_decode_pick_split",
                     "dcp_mla_rope", "dcp_mla_cache8_append", "dcp_mla_cache8_read", "dcp_mla_cache8_decode",
-                    "dcp_mla_cache8_decode_workspace_bytes", "dcp_mla_cache8_strerror")
+                    "dcp_mla_cache8_decode_workspace_bytes", "dcp_mla_cache8_strerror",
+                    "dcp_mla_pages_update", "dcp_mla_pages_update_workspace_bytes", "dcp_mla_pages_compact",
+                    "dcp_mla_pages_compact_workspace_bytes", "dcp_mla_pages_copy")
 DCP_MLA_CACHE8_BLOCK_MAX = 128
 DCP_MLA_CACHE8_CP_MAX = 16
+DCP_MLA_PAGE_MIN = 32
+DCP_MLA_PAGE_MAX = 4096
+DCP_MLA_PAGES_POOLS_MAX = 128
 DCP_MLA_NOALLOC_SCRATCH_BYTES = 32 << 20
 DCP_MLA_SPLIT_MAX = 16
 DCP_MLA_FLAG_MMA_SYNC = 2
@@ -120,6 +125,17 @@ def load(path: str | None = None):
         lib.dcp_mla_cache8_decode.restype = ci
         lib.dcp_mla_cache8_decode_workspace_bytes.argtypes = [ci, i64, ci, i64, i64, i64, ci]
         lib.dcp_mla_cache8_decode_workspace_bytes.restype = i64
+        lib.dcp_mla_pages_update.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, ci, ci, ci, ci, vp, vp, vp, vp, vp, i64,
+                                             vp]
+        lib.dcp_mla_pages_update.restype = ci
+        lib.dcp_mla_pages_update_workspace_bytes.argtypes = [i64, i64, i64, ci]
+        lib.dcp_mla_pages_update_workspace_bytes.restype = i64
+        lib.dcp_mla_pages_compact.argtypes = [vp, vp, i64, i64, i64, vp, vp, vp, vp, i64, vp]
+        lib.dcp_mla_pages_compact.restype = ci
+        lib.dcp_mla_pages_compact_workspace_bytes.argtypes = [i64]
+        lib.dcp_mla_pages_compact_workspace_bytes.restype = i64
+        lib.dcp_mla_pages_copy.argtypes = [pv, pv, ci, i64, ci, ci, ci, vp, i64, vp]
+        lib.dcp_mla_pages_copy.restype = ci
         lib.dcp_mla_cache8_strerror.argtypes = [ci]
         lib.dcp_mla_cache8_strerror.restype = ctypes.c_char_p
         if path is None:
@@ -301,6 +317,39 @@ def dcp_mla_cache8_decode_workspace_bytes(cp: int, B: int, H: int, T: int, windo
     """Bytes of workspace a decode of these sizes needs, 0 for none (host only)."""
     return int(load().dcp_mla_cache8_decode_workspace_bytes(int(cp), int(B), int(H), int(T), int(window), int(sinks),
                                                             int(num_sms)))
+
+
+def dcp_mla_pages_update(tables, refs, parents, keeps, wants, B: int, M: int, P: int, page: int, tables_out, refs_out,
+                         copies, missing, workspace, workspace_bytes: int, cp: int = 1, shard: int = 0,
+                         interleave: int = 1, stream=None) -> None:
+    """One step of the tables of a paged cache (see include/dcp_mla_pages.h)."""
+    _check8(load().dcp_mla_pages_update(_ptr(tables), _ptr(refs), _ptr(parents), _ptr(keeps), _ptr(wants), int(B),
+                                        int(M), int(P), int(page), int(cp), int(shard), int(interleave),
+                                        _ptr(tables_out), _ptr(refs_out), _ptr(copies), _ptr(missing),
+                                        _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def dcp_mla_pages_update_workspace_bytes(B: int, M: int, P: int, in_place: bool) -> int:
+    return int(load().dcp_mla_pages_update_workspace_bytes(int(B), int(M), int(P), 1 if in_place else 0))
+
+
+def dcp_mla_pages_compact(tables, refs, B: int, M: int, P: int, tables_out, refs_out, copies, workspace,
+                          workspace_bytes: int, stream=None) -> None:
+    """Move the pages in use to the front of the pool (see include/dcp_mla_pages.h)."""
+    _check8(load().dcp_mla_pages_compact(_ptr(tables), _ptr(refs), int(B), int(M), int(P), _ptr(tables_out),
+                                         _ptr(refs_out), _ptr(copies), _ptr(workspace), int(workspace_bytes),
+                                         _stream(stream)))
+
+
+def dcp_mla_pages_compact_workspace_bytes(P: int) -> int:
+    return int(load().dcp_mla_pages_compact_workspace_bytes(int(P)))
+
+
+def dcp_mla_pages_copy(kv_ptrs, scale_ptrs, pools: int, P: int, page: int, Dk: int, block: int, copies, n: int,
+                       stream=None) -> None:
+    """Copy pages inside each of several pools (see include/dcp_mla_pages.h)."""
+    _check8(load().dcp_mla_pages_copy(_ptr_array(kv_ptrs, pools), _ptr_array(scale_ptrs, pools), int(pools), int(P),
+                                      int(page), int(Dk), int(block), _ptr(copies), int(n), _stream(stream)))
 
 
 def dcp_mla_cache8_strerror(status: int) -> str:

@@ -16,9 +16,10 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", name)
-           for name in ("dcp_lse_reduce.cu", "mla_decode_partial.cu", "mla_cache8.cu", "mla_cache8_decode.cu")]
+           for name in ("dcp_lse_reduce.cu", "mla_decode_partial.cu", "mla_cache8.cu", "mla_cache8_decode.cu",
+                       "mla_pages.cu")]
 HEADERS = [os.path.join(ROOT, "include", name)
-           for name in ("dcp_lse_reduce.h", "dcp_mla_decode.h", "dcp_mla_cache8.h")]
+           for name in ("dcp_lse_reduce.h", "dcp_mla_decode.h", "dcp_mla_cache8.h", "dcp_mla_pages.h")]
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libdcp_lse_reduce.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)

@@ -27,6 +27,7 @@
 
 #include "dcp_lse_reduce.h"
 #include "dcp_mla_cache8.h"
+#include "dcp_mla_pages.h"
 
 namespace {
 
@@ -951,9 +952,12 @@ extern "C" const char* dcp_mla_cache8_strerror(int status) {
         case DCP_MLA_CACHE8_ERR_BAD_DTYPE: return "a dtype that the call does not take";
         case DCP_MLA_CACHE8_ERR_BAD_FLAGS: return "unknown flag bits";
         case DCP_MLA_CACHE8_ERR_WORKSPACE:
-            return "the workspace is NULL, not 256-byte aligned, or smaller than dcp_mla_cache8_decode_workspace_bytes";
+            return "the workspace is NULL, not 256-byte aligned, or smaller than the call's workspace_bytes";
         case DCP_MLA_CACHE8_ERR_BAD_WINDOW: return "window and sinks must not be negative, and sinks need a window";
         case DCP_MLA_CACHE8_ERR_TENSOR_MAP: return "a TMA tensor map of a cache could not be encoded";
+        case DCP_MLA_CACHE8_ERR_BAD_PAGE: return "page must be a power of two in [32, 4096] and a multiple of block";
+        case DCP_MLA_CACHE8_ERR_ALIAS:
+            return "outputs overlap inputs other than in place, or one pool is given twice";
         default: return dcp_lse_reduce_strerror(status);
     }
 }

@@ -1,0 +1,106 @@
+/*
+ * The 8-bit latent cache in pages (dcp_mla_cache8.h has the format of a token,
+ * of scales and of context shards): rows share pages, take over each other's,
+ * and give them back; append, read-back and attention go through a table.
+ *
+ * The pool. A page is `page` tokens of one row of one shard, a power of two in
+ * [DCP_MLA_PAGE_MIN, DCP_MLA_PAGE_MAX], and a multiple of `block`.
+ *   kv     [P, page, Dk] e4m3 codes, contiguous, 16-byte aligned
+ *   scales [P, page / block] fp32, contiguous
+ * The tables, per shard, the same for all layers.
+ *   tables [B, M] int32, contiguous: entry (b, i) is the page of tokens
+ *          i * page .. of row b on this shard. An entry outside [0, P) is no
+ *          page, and a row's pages are its entries before the first such one.
+ *   refs   [P] int32: how many rows hold a page; 0 is a free page. A program
+ *          that wants to keep a page without a row adds 1 of its own.
+ *
+ * Asynchrony, ownership, errors: as for dcp_mla_cache8_decode. All counts stay
+ * on the device, so that a step (update, copy, append, attend) can be captured.
+ */
+#ifndef DCP_MLA_PAGES_H
+#define DCP_MLA_PAGES_H
+
+#include <stdint.h>
+
+#include "dcp_mla_cache8.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define DCP_MLA_PAGE_MIN 32
+#define DCP_MLA_PAGE_MAX 4096
+#define DCP_MLA_PAGES_POOLS_MAX 128
+
+enum {
+    DCP_MLA_CACHE8_ERR_BAD_PAGE = -211,  /* page not a power of two in range, or not a multiple of block */
+    DCP_MLA_CACHE8_ERR_ALIAS = -212      /* outputs that overlap inputs in a way that the call does not take */
+};
+
+/*
+ * One step of the tables: rows take over other rows' pages, are cut back, end,
+ * begin and grow, all at once. For row b, with the tables as they are on entry:
+ *   it takes the pages of the first keeps[b] positions from row parents[b] (b
+ *   itself to go on; outside [0, B): from none, and keeps[b] counts as 0), and
+ *   gets fresh pages for what it lacks below max(keeps[b], wants[b]) positions.
+ * What it held besides is released: refs goes down by 1 for each page that a row
+ * held and up by 1 for each that it holds. So {parents -1, wants 0} ends a row,
+ * {b, n, n + k} makes room for k tokens behind n, {a, n, n + 1} forks row a.
+ *   Positions are those of a sequence over all cp shards; this shard's share is
+ *   what counts here (cp 1: all of them). They are at most M pages of the shard.
+ * Copy on write. Where wants[b] > keeps[b] and the kept tokens end inside a page
+ * that another row (or a program's own count) holds too, row b gets a fresh page
+ * in its place, and copies[b] = (that page, the fresh one); otherwise copies[b] =
+ * (-1, -1). If all who hold it are such rows, the last of them keeps it.
+ * Fresh pages are those with refs 0 after all releases, the lowest first, dealt to
+ * rows in order, in a row the copy's first and then by slot. Where they run out the
+ * entry is -1 (and there is no copy), and *missing counts these; else it is 0.
+ *   tables_out, refs_out  either tables and refs themselves (in place), or buffers
+ *            that overlap neither
+ *   copies   [B, 2] int32, 8-byte aligned; missing: one int32
+ *   parents, keeps, wants  [B] int32 (negative positions: 0)
+ *   workspace at least dcp_mla_pages_update_workspace_bytes(...) bytes, 256-byte
+ *            aligned; its contents do not matter. Calls that share one are ordered.
+ *   shapes   0 <= B <= 65535, 1 <= M, B * (M + 1) < 2^31, 1 <= P < 2^31, 0 <= shard < cp
+ */
+int dcp_mla_pages_update(const int32_t* tables, const int32_t* refs, const int32_t* parents, const int32_t* keeps,
+                         const int32_t* wants, int64_t B, int64_t M, int64_t P, int page, int cp, int shard,
+                         int interleave, int32_t* tables_out, int32_t* refs_out, int32_t* copies, int32_t* missing,
+                         void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace for dcp_mla_pages_update; -1 for sizes out of range. Host only. */
+int64_t dcp_mla_pages_update_workspace_bytes(int64_t B, int64_t M, int64_t P, int in_place);
+
+/*
+ * Move the pages in use to the front of the pool. With n pages of refs > 0, those
+ * at n and beyond go, in ascending order, to the free ones below n in ascending
+ * order: copies[i] = (page, its new place) for the i-th of them and (-1, -1) behind
+ * the last. Entries of tables and refs are changed to match; an entry that is no
+ * page, or a page that does not move, stays as it is. Nothing is copied here.
+ *   copies   [P / 2, 2] int32, 8-byte aligned (more than P / 2 pages never move)
+ *   tables_out, refs_out, workspace, shapes as above (B = 0 is allowed)
+ */
+int dcp_mla_pages_compact(const int32_t* tables, const int32_t* refs, int64_t B, int64_t M, int64_t P,
+                          int32_t* tables_out, int32_t* refs_out, int32_t* copies, void* workspace,
+                          int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace for dcp_mla_pages_compact; -1 for sizes out of range. Host only. */
+int64_t dcp_mla_pages_compact_workspace_bytes(int64_t P);
+
+/*
+ * Copy pages, codes and scales, inside each of several pools (layers) of one
+ * geometry: for each pair copies[i] = (src, dst), i < n, page src to page dst. A
+ * pair with an entry outside [0, P) is passed over. No page may be the dst of two
+ * pairs, or both dst and src.
+ *   kv_ptrs, scale_ptrs  [pools] host arrays, pools <= DCP_MLA_PAGES_POOLS_MAX; no
+ *            pool twice
+ *   shapes   0 <= n < 2^31, 1 <= P < 2^31, Dk 512 or 576
+ */
+int dcp_mla_pages_copy(void* const* kv_ptrs, float* const* scale_ptrs, int pools, int64_t P, int page, int Dk,
+                       int block, const int32_t* copies, int64_t n, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* DCP_MLA_PAGES_H */

@@ -1,0 +1,147 @@
+"""What the calls on pages refuse, on the host, and what their plain forms (oracle/pages.py) say of small cases that can
+be worked out by hand. Nothing is launched."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import decode_context_mla_dcp_gb300 as dcp
+from decode_context_mla_dcp_gb300 import build as dcp_build
+from oracle import pages as ref
+
+A = 1 << 20  # an aligned address that is never dereferenced
+NULL, SHAPE, BLOCK, CP, ALIGN = range(-201, -206, -1)
+WS, PAGE, ALIAS = -208, -211, -212
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    dcp_build.build()
+
+
+def refused(code, fn, base, **change):
+    with pytest.raises(dcp.DcpError) as e:
+        fn(**{**base, **change})
+    assert e.value.status == code
+    assert dcp.dcp_mla_cache8_strerror(code) in str(e.value)
+
+
+UPDATE = dict(tables=A, refs=2 * A, parents=A, keeps=A, wants=A, B=4, M=8, P=16, page=64, tables_out=A,
+              refs_out=2 * A, copies=A, missing=A, workspace=A, workspace_bytes=1 << 40, stream=0)
+COMPACT = dict(tables=A, refs=2 * A, B=4, M=8, P=16, tables_out=A, refs_out=2 * A, copies=A, workspace=A,
+               workspace_bytes=1 << 40, stream=0)
+COPY = dict(kv_ptrs=[A], scale_ptrs=[2 * A], pools=1, P=16, page=64, Dk=576, block=16, copies=A, n=4, stream=0)
+
+TABLES = [(SHAPE, dict(B=-1)), (SHAPE, dict(B=65536)), (SHAPE, dict(M=0)), (SHAPE, dict(P=0)),
+          (SHAPE, dict(P=1 << 31)), (SHAPE, dict(B=65535, M=1 << 15)), (SHAPE, dict(M=1 << 31)),
+          (NULL, dict(tables=None)), (NULL, dict(refs=None)), (NULL, dict(tables_out=None)),
+          (NULL, dict(refs_out=None)), (NULL, dict(copies=None)), (ALIGN, dict(tables=A + 1)),
+          (ALIGN, dict(refs=A + 2)), (ALIGN, dict(copies=A + 4)), (WS, dict(workspace=None)),
+          (WS, dict(workspace=A + 128)), (WS, dict(workspace_bytes=100)),
+          # one in place and the other not; outputs that overlap inputs or each other
+          (ALIAS, dict(tables_out=4 * A)), (ALIAS, dict(refs_out=4 * A)),
+          (ALIAS, dict(tables_out=A + 64, refs_out=4 * A)), (ALIAS, dict(tables_out=4 * A, refs_out=2 * A + 32)),
+          (ALIAS, dict(tables_out=2 * A, refs_out=4 * A)), (ALIAS, dict(tables_out=4 * A, refs_out=A)),
+          (ALIAS, dict(tables_out=4 * A, refs_out=4 * A)), (ALIAS, dict(refs=A, refs_out=A))]
+
+
+@pytest.mark.parametrize("code,change", TABLES + [
+    (PAGE, dict(page=16)), (PAGE, dict(page=48)), (PAGE, dict(page=8192)), (PAGE, dict(page=0)),
+    (CP, dict(cp=0)), (CP, dict(cp=17)), (CP, dict(cp=2, shard=2)), (CP, dict(shard=-1)), (CP, dict(interleave=0)),
+    (CP, dict(interleave=(1 << 24) + 1)), (NULL, dict(parents=None)), (NULL, dict(keeps=None)),
+    (NULL, dict(wants=None)), (NULL, dict(missing=None)), (ALIGN, dict(parents=A + 2)), (ALIGN, dict(missing=A + 2))])
+def test_update(code, change):
+    refused(code, dcp.dcp_mla_pages_update, UPDATE, **change)
+
+
+@pytest.mark.parametrize("code,change", TABLES)
+def test_compact(code, change):
+    refused(code, dcp.dcp_mla_pages_compact, COMPACT, **change)
+
+
+@pytest.mark.parametrize("code,change", [
+    (SHAPE, dict(n=-1)), (SHAPE, dict(n=1 << 31)), (SHAPE, dict(P=0)), (SHAPE, dict(Dk=640)), (SHAPE, dict(pools=0)),
+    (SHAPE, dict(pools=129, kv_ptrs=[A] * 129, scale_ptrs=[A] * 129)), (BLOCK, dict(block=3)), (BLOCK, dict(block=0)),
+    (BLOCK, dict(block=256, page=256)), (PAGE, dict(page=16)), (PAGE, dict(page=96)), (PAGE, dict(page=32, block=64)),
+    (NULL, dict(kv_ptrs=[None])), (NULL, dict(scale_ptrs=[None])), (NULL, dict(copies=None)),
+    (ALIGN, dict(kv_ptrs=[A + 8])), (ALIGN, dict(scale_ptrs=[A + 2])), (ALIGN, dict(copies=A + 4)),
+    (ALIAS, dict(pools=2, kv_ptrs=[A, A], scale_ptrs=[A, 2 * A])),
+    (ALIAS, dict(pools=2, kv_ptrs=[A, 3 * A], scale_ptrs=[2 * A, 2 * A]))])
+def test_copy(code, change):
+    refused(code, dcp.dcp_mla_pages_copy, COPY, **change)
+
+
+def test_copy_of_no_pairs_is_nothing():
+    dcp.dcp_mla_pages_copy(**{**COPY, "n": 0, "copies": None})
+
+
+def test_workspace_bytes():
+    up, co = dcp.dcp_mla_pages_update_workspace_bytes, dcp.dcp_mla_pages_compact_workspace_bytes
+    assert up(4, 100, 50, True) >= up(4, 100, 50, False) + 4 * 100 * 4
+    assert up(256, 1, 1000, False) >= 256 * 24 + 3 * 4000 and co(1000) >= 8000
+    for bad in ((-1, 1, 1), (65536, 1, 1), (1, 0, 1), (1, 1, 0), (65535, 1 << 15, 1)):
+        assert up(*bad, False) == -1
+    assert co(0) == co(1 << 31) == -1
+
+
+def test_wrappers():
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    t, r, row = i32(2, 4), i32(8), i32(2)
+    up = lambda t=t, r=r, a=row, b=row, c=row, page=64, **k: dcp.mla_cache8_pages_update(t, r, a, b, c, page=page, **k)
+    with pytest.raises(ValueError, match="CUDA"):
+        up()
+    with pytest.raises(ValueError, match="CUDA"):
+        dcp.mla_cache8_pages_compact(t, r)
+    for kw in (dict(t=t.long()), dict(t=i32(4, 2).T), dict(t=row), dict(r=r.long()), dict(r=t), dict(r=i32(0)),
+               dict(t=i32(2, 0)), dict(a=i32(3)), dict(b=row.long()), dict(c=None), dict(page=16), dict(page=100),
+               dict(page=1 << 33), dict(cp=0), dict(cp=2, shard=2), dict(interleave=0), dict(out=(t, i32(9))),
+               dict(out=(t.long(), r))):
+        with pytest.raises(ValueError):
+            up(**kw)
+    kv, sc = torch.zeros((4, 64, 576), dtype=torch.uint8), torch.ones((4, 4))
+    pairs = i32(3, 2)
+    copy = dcp.mla_cache8_pages_copy
+    with pytest.raises(ValueError, match="CUDA"):
+        copy([kv], [sc], pairs)
+    for c, s, p in [([], [], pairs), ([kv], [sc, sc], pairs), ([kv[..., :500]], [sc], pairs), ([kv[0]], [sc], pairs),
+                    ([kv], [sc[:3]], pairs), ([kv], [torch.ones((4, 5))], pairs), ([kv, kv[:3]], [sc, sc], pairs),
+                    ([kv[:, ::2]], [sc[:, ::2]], pairs), ([kv], [sc], pairs.long()), ([kv], [sc], i32(3, 3)),
+                    ([kv], [sc], i32(2, 3).T), ([kv] * 129, [sc] * 129, pairs)]:
+        with pytest.raises(ValueError):
+            copy(c, s, p)
+    with pytest.raises(TypeError):
+        copy([kv.float()], [sc], pairs)
+    with pytest.raises(TypeError):
+        copy([kv], [sc.double()], pairs)
+
+
+# ---- the plain forms, by hand ---------------------------------------------------------
+
+
+def test_a_fork_shares_whole_pages_and_copies_the_one_that_is_written():
+    # row 0: 70 tokens on pages 3, 5; row 1 becomes its twin, and both write their next token
+    t, r, c, m = ref.update([[3, 5, -1], [-1, -1, -1]], [0, 0, 0, 1, 0, 1], [0, 0], [70, 70], [71, 71], 64)
+    assert (t, r, c, m) == ([[3, 0, -1], [3, 5, -1]], [1, 0, 0, 2, 0, 1], [[5, 0], [-1, -1]], 0)
+    # only row 1 writes: row 0 keeps the page
+    t, r, c, m = ref.update([[3, 5, -1], [-1, -1, -1]], [0, 0, 0, 1, 0, 1], [0, 0], [70, 70], [70, 71], 64)
+    assert (t, r, c, m) == ([[3, 5, -1], [3, 0, -1]], [1, 0, 0, 2, 0, 1], [[-1, -1], [5, 0]], 0)
+    # at a page's end nothing is copied
+    t, r, c, m = ref.update([[3, -1], [-1, -1]], [0, 0, 0, 1], [0, 0], [64, 64], [65, 65], 64)
+    assert (t, r, c, m) == ([[3, 0], [3, 1]], [1, 1, 0, 2], [[-1, -1], [-1, -1]], 0)
+
+
+def test_rows_end_and_their_pages_are_dealt_in_the_same_step():
+    t, r, c, m = ref.update([[0, 1], [2, -1]], [1, 1, 1], [-1, 1], [0, 64], [0, 128], 64)
+    assert (t, r, c, m) == ([[-1, -1], [2, 0]], [1, 0, 1], [[-1, -1]] * 2, 0)
+    # rows change places
+    t, r, c, m = ref.update([[0, 1], [2, -1]], [1, 1, 1], [1, 0], [64, 100], [64, 100], 64)
+    assert (t, r, c, m) == ([[2, -1], [0, 1]], [1, 1, 1], [[-1, -1]] * 2, 0)
+
+
+def test_a_pool_that_runs_out():
+    t, r, c, m = ref.update([[0, -1, -1]], [1, 0], [0], [10], [190], 64)
+    assert (t, r, c, m) == ([[0, 1, -1]], [1, 1], [[-1, -1]], 1)
+
+
+def test_compaction_by_hand():
+    t, r, c = ref.compact([[5, 1], [5, -1]], [0, 1, 0, 0, 0, 2])
+    assert (t, r, c) == ([[0, 1], [0, -1]], [2, 1, 0, 0, 0, 0], [[5, 0]])
