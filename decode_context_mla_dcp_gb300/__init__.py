@@ -35,7 +35,8 @@ from ._binding import (DCP_DTYPE_BF16, DCP_DTYPE_F16, DCP_FLAG_LSE_FIRST, DCP_FL
                        dcp_mla_cache8_decode_workspace_bytes, dcp_mla_cache8_strerror,
                        DCP_MLA_PAGE_MAX, DCP_MLA_PAGE_MIN, DCP_MLA_PAGES_POOLS_MAX, dcp_mla_pages_update,
                        dcp_mla_pages_update_workspace_bytes, dcp_mla_pages_compact,
-                       dcp_mla_pages_compact_workspace_bytes, dcp_mla_pages_copy)
+                       dcp_mla_pages_compact_workspace_bytes, dcp_mla_pages_copy,
+                       dcp_mla_cache8_append_paged, dcp_mla_cache8_read_paged)
 from .cache8 import mla_cache8_append, mla_cache8_decode, mla_cache8_read, mla_rope, mla_rope_inv_freq
 from .cache8_pages import mla_cache8_pages_compact, mla_cache8_pages_copy, mla_cache8_pages_update
 
@@ -56,6 +57,7 @@ __all__ = ["dcp_lse_reduce", "dcp_lse_reduce_ex", "dcp_lse_reduce_strerror", "dc
            "mla_cache8_pages_update", "mla_cache8_pages_compact", "mla_cache8_pages_copy",
            "dcp_mla_pages_update", "dcp_mla_pages_update_workspace_bytes", "dcp_mla_pages_compact",
            "dcp_mla_pages_compact_workspace_bytes", "dcp_mla_pages_copy",
+           "dcp_mla_cache8_append_paged", "dcp_mla_cache8_read_paged",
            "DCP_MLA_PAGE_MIN", "DCP_MLA_PAGE_MAX", "DCP_MLA_PAGES_POOLS_MAX"]
 
 

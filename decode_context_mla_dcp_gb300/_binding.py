@@ -30,7 +30,8 @@ EXPORTED_SYMBOLS = ("dcp_lse_reduce", "dcp_lse_reduce_ex", "dcp_lse_reduce_strer
                     "dcp_mla_rope", "dcp_mla_cache8_append", "dcp_mla_cache8_read", "dcp_mla_cache8_decode",
                     "dcp_mla_cache8_decode_workspace_bytes", "dcp_mla_cache8_strerror",
                     "dcp_mla_pages_update", "dcp_mla_pages_update_workspace_bytes", "dcp_mla_pages_compact",
-                    "dcp_mla_pages_compact_workspace_bytes", "dcp_mla_pages_copy")
+                    "dcp_mla_pages_compact_workspace_bytes", "dcp_mla_pages_copy",
+                    "dcp_mla_cache8_append_paged", "dcp_mla_cache8_read_paged")
 DCP_MLA_CACHE8_BLOCK_MAX = 128
 DCP_MLA_CACHE8_CP_MAX = 16
 DCP_MLA_PAGE_MIN = 32
@@ -136,6 +137,12 @@ def load(path: str | None = None):
         lib.dcp_mla_pages_compact_workspace_bytes.restype = i64
         lib.dcp_mla_pages_copy.argtypes = [pv, pv, ci, i64, ci, ci, ci, vp, i64, vp]
         lib.dcp_mla_pages_copy.restype = ci
+        lib.dcp_mla_cache8_append_paged.argtypes = [vp, i64, vp, i64, ci, i64, i64, ci, vp, vp, pv, pv, pv, ci, i64, ci,
+                                                    i64, ci, ci, vp, ci, cf, vp]
+        lib.dcp_mla_cache8_append_paged.restype = ci
+        lib.dcp_mla_cache8_read_paged.argtypes = [pv, pv, pv, ci, i64, i64, ci, i64, ci, ci, ci, vp, vp, i64, vp, i64,
+                                                  ci, vp]
+        lib.dcp_mla_cache8_read_paged.restype = ci
         lib.dcp_mla_cache8_strerror.argtypes = [ci]
         lib.dcp_mla_cache8_strerror.restype = ctypes.c_char_p
         if path is None:
@@ -317,6 +324,29 @@ def dcp_mla_cache8_decode_workspace_bytes(cp: int, B: int, H: int, T: int, windo
     """Bytes of workspace a decode of these sizes needs, 0 for none (host only)."""
     return int(load().dcp_mla_cache8_decode_workspace_bytes(int(cp), int(B), int(H), int(T), int(window), int(sinks),
                                                             int(num_sms)))
+
+
+def dcp_mla_cache8_append_paged(latent, latent_row: int, k_rope, rope_row: int, dtype: int, N: int, B: int, Dk: int,
+                                cu_new, seq_lens, kv_ptrs, scale_ptrs, table_ptrs, cp: int, P: int, page: int, M: int,
+                                block: int = 1, interleave: int = 1, inv_freq=None, interleaved: bool = True,
+                                mscale: float = 1.0, stream=None) -> None:
+    """Quantise new tokens into the pages of an 8-bit cache (see include/dcp_mla_pages.h)."""
+    _check8(load().dcp_mla_cache8_append_paged(_ptr(latent), int(latent_row), _ptr(k_rope), int(rope_row), int(dtype),
+                                               int(N), int(B), int(Dk), _ptr(cu_new), _ptr(seq_lens),
+                                               _ptr_array(kv_ptrs, cp), _ptr_array(scale_ptrs, cp),
+                                               _ptr_array(table_ptrs, cp), int(cp), int(P), int(page), int(M),
+                                               int(block), int(interleave), _ptr(inv_freq), 1 if interleaved else 0,
+                                               float(mscale), _stream(stream)))
+
+
+def dcp_mla_cache8_read_paged(kv_ptrs, scale_ptrs, table_ptrs, cp: int, B: int, P: int, page: int, M: int, Dk: int,
+                              block: int, interleave: int, starts, cu, N: int, out, out_row: int, dtype: int,
+                              stream=None) -> None:
+    """Read cached tokens back from pages (see include/dcp_mla_pages.h)."""
+    _check8(load().dcp_mla_cache8_read_paged(_ptr_array(kv_ptrs, cp), _ptr_array(scale_ptrs, cp),
+                                             _ptr_array(table_ptrs, cp), int(cp), int(B), int(P), int(page), int(M),
+                                             int(Dk), int(block), int(interleave), _ptr(starts), _ptr(cu), int(N),
+                                             _ptr(out), int(out_row), int(dtype), _stream(stream)))
 
 
 def dcp_mla_pages_update(tables, refs, parents, keeps, wants, B: int, M: int, P: int, page: int, tables_out, refs_out,

@@ -133,6 +133,33 @@ def _shards(caches, scales, block, interleave):
     return index, B, T, dk, kv, sc
 
 
+def _tables(tables, caches, page, block, index):
+    """Check a paged cache's tables; (B, M, table pointers)."""
+    cp = len(caches)
+    if len(tables) != cp:
+        raise ValueError("need a table for each cache (None for a shard that is not held)")
+    if page < _b.DCP_MLA_PAGE_MIN or page > _b.DCP_MLA_PAGE_MAX or page & (page - 1) or page % block:
+        raise ValueError(f"a page must be a power of two in [{_b.DCP_MLA_PAGE_MIN}, {_b.DCP_MLA_PAGE_MAX}] and a "
+                         "multiple of block")
+    shape, i32 = None, _torch.int32
+    tb = (ctypes.c_void_p * cp)()
+    for j in range(cp):
+        t = tables[j]
+        if t is None or caches[j] is None:
+            if t is not caches[j]:
+                raise ValueError("a shard has both a cache and tables, or neither")
+            continue
+        if shape is None:
+            shape = t.shape
+        if len(shape) != 2 or t.shape != shape or t.dtype != i32 or t.get_device() != index or not t.is_contiguous():
+            raise ValueError("tables must be contiguous int32 tensors [B, M] of one shape on the caches' device")
+        tb[j] = t.data_ptr()
+    B, M = shape
+    if M < 1 or M * page >= 1 << 31:
+        raise ValueError("tables need a column, and M * page must be below 2^31")
+    return B, M, tb
+
+
 def mla_rope_inv_freq(rot: int = 64, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
                       original_len: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,
                       mscale: float = 1.0, mscale_all_dim: float = 0.0, device="cuda"):
@@ -248,7 +275,8 @@ def mla_rope(x, positions, inv_freq, *, start: int = 0, interleaved: bool = True
 
 
 def mla_cache8_append(latent, k_rope, caches, scales, seq_lens, *, cu_new=None, block: int = 1, interleave: int = 1,
-                      inv_freq=None, interleaved: bool = True, mscale: float = 1.0, stream=None) -> None:
+                      inv_freq=None, interleaved: bool = True, mscale: float = 1.0, tables=None,
+                      stream=None) -> None:
     """Quantise new tokens into the caches, in place.
 
     latent: bf16 or fp16 [N, 512]; k_rope: [N, 64] of the same type, or None for
@@ -257,9 +285,13 @@ def mla_cache8_append(latent, k_rope, caches, scales, seq_lens, *, cu_new=None, 
     at positions seq_lens[b], ... (int32 [B]: the lengths before the call). With
     inv_freq (float64 [32]) k_rope is rotated on the way. A block's scale is the
     smallest power of two that holds its values; a block that already holds
-    tokens is requantised where its scale grows."""
+    tokens is requantised where its scale grows. tables (int32 [B, M] per shard):
+    the caches are pools of pages [P, page, Dk] (cache8_pages.py), B is theirs."""
     lib, torch = _ready()
     index, B, T, dk, kv, sc = _shards(caches, scales, block, interleave)
+    if tables is not None:
+        P, page = B, T
+        B, M, tb = _tables(tables, caches, page, block, index)
     dtype = _DTYPES.get(latent.dtype)
     if dtype is None or dtype == _b.DCP_DTYPE_F32:
         raise TypeError("latent must be bf16 or fp16")
@@ -291,24 +323,34 @@ def mla_cache8_append(latent, k_rope, caches, scales, seq_lens, *, cu_new=None, 
     if inside is not None:
         with inside:
             return mla_cache8_append(latent, k_rope, caches, scales, seq_lens, cu_new=cu_new, block=block,
-                                     interleave=interleave, inv_freq=inv_freq, interleaved=interleaved, mscale=mscale)
-    rc = lib.dcp_mla_cache8_append(latent.data_ptr(), row, rope_ptr, rope_row, dtype, n, B, dk, cu, lens, kv, sc,
-                                   len(caches), T, block, interleave, freq_ptr, interleaved, mscale, raw)
+                                     interleave=interleave, inv_freq=inv_freq, interleaved=interleaved, mscale=mscale,
+                                     tables=tables)
+    if tables is None:
+        rc = lib.dcp_mla_cache8_append(latent.data_ptr(), row, rope_ptr, rope_row, dtype, n, B, dk, cu, lens, kv, sc,
+                                       len(caches), T, block, interleave, freq_ptr, interleaved, mscale, raw)
+    else:
+        rc = lib.dcp_mla_cache8_append_paged(latent.data_ptr(), row, rope_ptr, rope_row, dtype, n, B, dk, cu, lens,
+                                             kv, sc, tb, len(caches), P, page, M, block, interleave, freq_ptr,
+                                             interleaved, mscale, raw)
     if rc:
         _b._check8(rc)
 
 
 def mla_cache8_read(caches, scales, total: int, *, starts=None, cu=None, block: int = 1, interleave: int = 1,
-                    dtype=None, out=None, stream=None):
+                    dtype=None, out=None, tables=None, stream=None):
     """Cached tokens as numbers: out[cu[b] + i] is position starts[b] + i of row b.
 
     total: packed tokens in all; cu: int32 [B + 1] (None: total / B each); starts:
     int32 [B] (None: 0). dtype: bf16 (default), fp16 or fp32. out: None allocates
     [total, Dk]; or a tensor of that shape, unit inner stride, rows and base on
     16-byte boundaries. Tokens that no held shard has are left as they were (in
-    a tensor that the call allocates: undefined). Returns out."""
+    a tensor that the call allocates: undefined). tables: as for the append.
+    Returns out."""
     lib, torch = _ready()
     index, B, T, dk, kv, sc = _shards(caches, scales, block, interleave)
+    if tables is not None:
+        P, page = B, T
+        B, M, tb = _tables(tables, caches, page, block, index)
     if total < 0:
         raise ValueError("total must not be negative")
     dtype = (torch.bfloat16 if out is None else out.dtype) if dtype is None else dtype
@@ -320,7 +362,7 @@ def mla_cache8_read(caches, scales, total: int, *, starts=None, cu=None, block: 
     if inside is not None:
         with inside:
             return mla_cache8_read(caches, scales, total, starts=starts, cu=cu, block=block, interleave=interleave,
-                                   dtype=dtype, out=out)
+                                   dtype=dtype, out=out, tables=tables)
     row = dk
     if out is None:
         out = torch.empty((total, dk), dtype=dtype, device=_cuda(index))
@@ -330,8 +372,12 @@ def mla_cache8_read(caches, scales, total: int, *, starts=None, cu=None, block: 
         row = out.stride(0)
         if row < dk and total > 1:
             raise ValueError("out's rows overlap each other")
-    rc = lib.dcp_mla_cache8_read(kv, sc, len(caches), B, T, dk, block, interleave, start_ptr, cu_ptr, total,
-                                 out.data_ptr(), row, code, raw)
+    if tables is None:
+        rc = lib.dcp_mla_cache8_read(kv, sc, len(caches), B, T, dk, block, interleave, start_ptr, cu_ptr, total,
+                                     out.data_ptr(), row, code, raw)
+    else:
+        rc = lib.dcp_mla_cache8_read_paged(kv, sc, tb, len(caches), B, P, page, M, dk, block, interleave, start_ptr,
+                                           cu_ptr, total, out.data_ptr(), row, code, raw)
     if rc:
         _b._check8(rc)
     return out

@@ -369,6 +369,43 @@ struct AppendParams {
     float mscale;
 };
 
+// A cache in pages: tables, and the pool's sizes. T is what a row's table has room for.
+struct Tables {
+    const int32_t* of[kCpMax];
+    int64_t M;
+    int P, page_log2;
+};
+struct PagedAppendParams : AppendParams {
+    Tables tables;
+};
+
+// The place of token `loc` of a row in shard j's cache, in tokens; negative: it has none.
+template <class P>
+__device__ __forceinline__ int64_t row_place(const P& p, int, int row, uint32_t loc) {
+    return (int64_t)row * p.T + loc;
+}
+__device__ __forceinline__ int64_t table_place(const Tables& t, int j, int row, uint32_t loc) {
+    const int e = t.of[j][row * t.M + (loc >> t.page_log2)];
+    return e >= 0 && e < t.P ? ((int64_t)e << t.page_log2) + (loc & ((1u << t.page_log2) - 1)) : -1;
+}
+__device__ __forceinline__ int64_t token_place(const AppendParams& p, int j, int row, uint32_t loc) {
+    return row_place(p, j, row, loc);
+}
+__device__ __forceinline__ int64_t token_place(const PagedAppendParams& p, int j, int row, uint32_t loc) {
+    return table_place(p.tables, j, row, loc);
+}
+// That of its block's scale (a page is whole blocks; a row's last block may be a part of one).
+template <class P>
+__device__ __forceinline__ int64_t row_scale(const P& p, int row, int64_t, uint32_t loc) {
+    return (int64_t)row * p.blocks + (loc >> p.block_log2);
+}
+__device__ __forceinline__ int64_t scale_place(const AppendParams& p, int row, int64_t at, uint32_t loc) {
+    return row_scale(p, row, at, loc);
+}
+__device__ __forceinline__ int64_t scale_place(const PagedAppendParams& p, int, int64_t at, uint32_t) {
+    return at >> p.block_log2;
+}
+
 // A token in a warp's registers: lane l holds latent dims 8l .. 8l+7 and
 // 256 + 8l .. 256 + 8l + 7 as they are, and the rotated rotary pair l.
 struct Token {
@@ -499,8 +536,8 @@ __device__ __forceinline__ bool place_of(const AppendParams& p, const int32_t* c
 
 // Each token its own scale: a warp takes a token, one round trip for its data. (One token 1.9 us, 256 x 4 tokens over
 // four shards 3.7, 16,385 tokens 7.5; the kernel of blocks took 3.0, 5.0 and 59 for them.)
-template <class E>
-__global__ void __launch_bounds__(128) append_token_kernel(const __grid_constant__ AppendParams p) {
+template <class E, class Q>
+__global__ void __launch_bounds__(128) append_token_kernel(const __grid_constant__ Q p) {
     const int lane = threadIdx.x & 31;
     const int64_t n = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     if (n >= p.N) return;
@@ -513,13 +550,14 @@ __global__ void __launch_bounds__(128) append_token_kernel(const __grid_constant
     if (!place_of(p, p.cu, n, &w) || (int64_t)w.loc >= p.T) return;
     uint8_t* const kv = p.kv[w.shard];
     if (kv == nullptr) return;
+    const int64_t at = token_place(p, w.shard, w.row, w.loc);
+    if (at < 0) return;
     turn_token<E>(p, rope, rotate, turns_of(f), (int64_t)w.pos, &t);
     bool odd = false;
     float top = lane_top<E>(t, &odd);
     odd = __any_sync(0xffffffffu, odd);
     if (odd) top = lane_finite_top<E>(t);
     const int k = scale_exp(warp_top(top));
-    const int64_t at = (int64_t)w.row * p.T + w.loc;
     store_token<E>(p, t, odd, kv + at * p.Dk, lane, pow2(-k));
     if (lane == 0) p.scales[w.shard][at] = pow2(k);
 }
@@ -600,9 +638,9 @@ __device__ __forceinline__ int lane_sums(int x, int lane) {
     return x;
 }
 
-template <class E, int kWarps, bool kCounted>
+template <class E, int kWarps, bool kCounted, class Q>
 __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps)
-append_block_kernel(const __grid_constant__ AppendParams p) {
+append_block_kernel(const __grid_constant__ Q p) {
     __shared__ int32_t cu_s[kCounted ? kCountedRows / 32 : kCuShared + 1];
     __shared__ Place list[kCounted ? 1 : 32 * kWarps];
     __shared__ int found;
@@ -680,9 +718,11 @@ append_block_kernel(const __grid_constant__ AppendParams p) {
         }
         for (int i = 0; i < nfound; ++i) {  // (in any order: blocks are independent of each other)
             if constexpr (!kCounted) w = list[i];
-            uint8_t* const kv = p.kv[w.shard] + (int64_t)w.row * p.T * p.Dk;
-            float* const scale = p.scales[w.shard] + (int64_t)w.row * p.blocks + (w.loc >> p.block_log2);
             const uint32_t b0 = w.loc & ~(block - 1);
+            const int64_t at = token_place(p, w.shard, w.row, b0);
+            if (at < 0) continue;  // (the same in every thread)
+            uint8_t* const kv = p.kv[w.shard] + (at - b0) * p.Dk;  // as if of token 0
+            float* const scale = p.scales[w.shard] + scale_place(p, w.row, at, b0);
             const uint32_t end = w.end < b0 + block ? w.end : b0 + block;
             Token t[kTok];
             uint32_t rope[kTok], pos[kTok];
@@ -757,6 +797,21 @@ struct ReadParams {
     uint32_t cp, interleave;
     int tokens;       // tokens of a CTA
 };
+struct PagedReadParams : ReadParams {
+    Tables tables;
+};
+__device__ __forceinline__ int64_t token_place(const ReadParams& p, int j, int row, uint32_t loc) {
+    return row_place(p, j, row, loc);
+}
+__device__ __forceinline__ int64_t token_place(const PagedReadParams& p, int j, int row, uint32_t loc) {
+    return table_place(p.tables, j, row, loc);
+}
+__device__ __forceinline__ int64_t scale_place(const ReadParams& p, int row, int64_t at, uint32_t loc) {
+    return row_scale(p, row, at, loc);
+}
+__device__ __forceinline__ int64_t scale_place(const PagedReadParams& p, int, int64_t at, uint32_t) {
+    return at >> p.block_log2;
+}
 
 constexpr int kReadThreads = 256;
 constexpr int kReadTokens = 32;
@@ -769,8 +824,8 @@ __device__ __forceinline__ uint2 load_once(const uint8_t* src) {
 
 // A CTA finds its tokens' places once, then moves 8 codes a thread: 8-byte
 // loads, 16-byte stores of 16-bit values, both contiguous over the token.
-template <class E, int kDk>
-__global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadParams p) {
+template <class E, int kDk, class Q>
+__global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ Q p) {
     using T = typename E::T;
     constexpr int kUnits = kDk / 8;  // 8 codes: 72 or 64 a token, a whole number of sweeps for 32 tokens
     __shared__ const uint8_t* src_s[kReadTokens];
@@ -803,8 +858,11 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
                     loc = q * p.interleave + (pos - turn * p.interleave);
                 }
                 if ((int64_t)loc < p.T && p.kv[shard] != nullptr) {
-                    src = p.kv[shard] + ((int64_t)row * p.T + loc) * kDk;
-                    s = p.scales[shard][(int64_t)row * p.blocks + (loc >> p.block_log2)];
+                    const int64_t at = token_place(p, shard, row, loc);
+                    if (at >= 0) {
+                        src = p.kv[shard] + at * kDk;
+                        s = p.scales[shard][scale_place(p, row, at, loc)];
+                    }
                 }
             }
         }
@@ -908,35 +966,164 @@ int launch_rope(RopeParams& p, int D, int64_t esize, cudaStream_t st) {
     return launched();
 }
 
-template <class E>
-int launch_append(const AppendParams& p, int block, cudaStream_t st) {
+template <class E, class Q>
+int launch_append(const Q& p, int block, cudaStream_t st) {
     if (block == 1) {
-        append_token_kernel<E><<<(unsigned)((p.N + 3) / 4), 128, 0, st>>>(p);
+        append_token_kernel<E, Q><<<(unsigned)((p.N + 3) / 4), 128, 0, st>>>(p);
         return launched();
     }
     // about as many CTAs as are resident at once (32 warps a multiprocessor), an odd number
     const int warps = block <= 16 ? 4 : block / 4, resident = kSms * (32 / warps) + 1;
     const unsigned grid = (unsigned)(p.N < resident ? p.N : resident);
     if (p.N > resident && p.B <= kCountedRows) {
-        if (warps == 4) append_block_kernel<E, 4, true><<<grid, 128, 0, st>>>(p);
-        else if (warps == 8) append_block_kernel<E, 8, true><<<grid, 256, 0, st>>>(p);
-        else if (warps == 16) append_block_kernel<E, 16, true><<<grid, 512, 0, st>>>(p);
-        else append_block_kernel<E, 32, true><<<grid, 1024, 0, st>>>(p);
+        if (warps == 4) append_block_kernel<E, 4, true, Q><<<grid, 128, 0, st>>>(p);
+        else if (warps == 8) append_block_kernel<E, 8, true, Q><<<grid, 256, 0, st>>>(p);
+        else if (warps == 16) append_block_kernel<E, 16, true, Q><<<grid, 512, 0, st>>>(p);
+        else append_block_kernel<E, 32, true, Q><<<grid, 1024, 0, st>>>(p);
     } else {
-        if (warps == 4) append_block_kernel<E, 4, false><<<grid, 128, 0, st>>>(p);
-        else if (warps == 8) append_block_kernel<E, 8, false><<<grid, 256, 0, st>>>(p);
-        else if (warps == 16) append_block_kernel<E, 16, false><<<grid, 512, 0, st>>>(p);
-        else append_block_kernel<E, 32, false><<<grid, 1024, 0, st>>>(p);
+        if (warps == 4) append_block_kernel<E, 4, false, Q><<<grid, 128, 0, st>>>(p);
+        else if (warps == 8) append_block_kernel<E, 8, false, Q><<<grid, 256, 0, st>>>(p);
+        else if (warps == 16) append_block_kernel<E, 16, false, Q><<<grid, 512, 0, st>>>(p);
+        else append_block_kernel<E, 32, false, Q><<<grid, 1024, 0, st>>>(p);
     }
     return launched();
 }
 
-template <class E>
-int launch_read(const ReadParams& p, int Dk, cudaStream_t st) {
+template <class E, class Q>
+int launch_read(const Q& p, int Dk, cudaStream_t st) {
     const unsigned grid = (unsigned)((p.N + p.tokens - 1) / p.tokens);
-    if (Dk == 576) read_kernel<E, 576><<<grid, kReadThreads, 0, st>>>(p);
-    else read_kernel<E, 512><<<grid, kReadThreads, 0, st>>>(p);
+    if (Dk == 576) read_kernel<E, 576, Q><<<grid, kReadThreads, 0, st>>>(p);
+    else read_kernel<E, 512, Q><<<grid, kReadThreads, 0, st>>>(p);
     return launched();
+}
+
+// The checks and parameters that both forms of the append share; `room` tokens of a row on a shard, `blocks` scales.
+int append_params(const void* latent, int64_t latent_row, const void* k_rope, int64_t rope_row, int dtype, int64_t N,
+                  int64_t B, int Dk, const int32_t* cu_new, const int32_t* seq_lens, void* const* kv_ptrs,
+                  float* const* scale_ptrs, int cp, int64_t T, int block, int interleave, const double* inv_freq,
+                  int interleaved, float mscale, bool empty, AppendParams* p, bool* nothing) {
+    *nothing = false;
+    if (N < 0 || N > 0x7fffffff || B < 0 || B > 65535 || T < 0 || T > 0x7fffffff || (Dk != 512 && Dk != 576) ||
+        (cu_new == nullptr && B > 0 && N % B != 0) || (B == 0 && N > 0))
+        return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
+    if (dtype != DCP_DTYPE_BF16 && dtype != DCP_DTYPE_F16) return DCP_MLA_CACHE8_ERR_BAD_DTYPE;
+    const int lg = log2_of(block);
+    if (lg < 0) return DCP_MLA_CACHE8_ERR_BAD_BLOCK;
+    if (const int rc = check_shards(kv_ptrs, scale_ptrs, cp, interleave)) return rc;
+    // (a cache that stands for two shards would be written by both at once)
+    for (int j = 0; j < cp; ++j)
+        for (int k = 0; k < j; ++k)
+            if (!empty && kv_ptrs[j] != nullptr && (kv_ptrs[j] == kv_ptrs[k] || scale_ptrs[j] == scale_ptrs[k]))
+                return DCP_MLA_CACHE8_ERR_BAD_CP;
+    if (N == 0 || empty) {
+        *nothing = true;
+        return 0;
+    }
+    if (latent == nullptr || seq_lens == nullptr || (Dk == 576 && k_rope == nullptr))
+        return DCP_MLA_CACHE8_ERR_NULL_POINTER;
+    if (!aligned(latent, 16) || !aligned(k_rope, 16) || latent_row % 8 != 0 || (Dk == 576 && rope_row % 8 != 0) ||
+        !aligned(seq_lens, 4) || !aligned(cu_new, 4) || !aligned(inv_freq, 8))
+        return DCP_MLA_CACHE8_ERR_MISALIGNED;
+    p->latent = static_cast<const uint8_t*>(latent);
+    p->k_rope = static_cast<const uint8_t*>(k_rope);
+    p->latent_row = latent_row * 2;
+    p->rope_row = rope_row * 2;
+    p->cu = cu_new;
+    p->seq_lens = seq_lens;
+    p->inv_freq = Dk == 576 ? inv_freq : nullptr;
+    for (int j = 0; j < cp; ++j) {
+        p->kv[j] = static_cast<uint8_t*>(kv_ptrs[j]);
+        p->scales[j] = scale_ptrs[j];
+    }
+    p->N = N;
+    p->T = T;
+    p->blocks = (T + block - 1) / block;
+    p->B = (int)B;
+    p->Dk = Dk;
+    p->even = cu_new == nullptr ? (int)(N / B) : 0;
+    p->cp = (uint32_t)cp;
+    p->interleave = (uint32_t)interleave;
+    p->block_log2 = lg;
+    p->interleaved = interleaved != 0;
+    p->mscale = mscale;
+    return 0;
+}
+
+// The same for the read-back.
+int read_params(const void* const* kv_ptrs, const float* const* scale_ptrs, int cp, int64_t B, int64_t T, int Dk,
+                int block, int interleave, const int32_t* starts, const int32_t* cu, int64_t N, void* out,
+                int64_t out_row, int dtype, bool empty, ReadParams* p, bool* nothing) {
+    *nothing = false;
+    if (N < 0 || N > 0x7fffffff || B < 0 || B > 65535 || T < 0 || T > 0x7fffffff || (Dk != 512 && Dk != 576) ||
+        (cu == nullptr && B > 0 && N % B != 0) || (B == 0 && N > 0))
+        return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
+    if (dtype != DCP_DTYPE_BF16 && dtype != DCP_DTYPE_F16 && dtype != DCP_DTYPE_F32)
+        return DCP_MLA_CACHE8_ERR_BAD_DTYPE;
+    const int lg = log2_of(block);
+    if (lg < 0) return DCP_MLA_CACHE8_ERR_BAD_BLOCK;
+    if (const int rc = check_shards(kv_ptrs, scale_ptrs, cp, interleave)) return rc;
+    if (N == 0 || empty) {
+        *nothing = true;
+        return 0;
+    }
+    if (out == nullptr) return DCP_MLA_CACHE8_ERR_NULL_POINTER;
+    const int64_t esize = dtype == DCP_DTYPE_F32 ? 4 : 2;
+    if (!aligned(out, 16) || (out_row * esize) % 16 != 0 || !aligned(starts, 4) || !aligned(cu, 4))
+        return DCP_MLA_CACHE8_ERR_MISALIGNED;
+    for (int j = 0; j < cp; ++j) {
+        p->kv[j] = static_cast<const uint8_t*>(kv_ptrs[j]);
+        p->scales[j] = scale_ptrs[j];
+    }
+    p->starts = starts;
+    p->cu = cu;
+    p->out = static_cast<uint8_t*>(out);
+    p->out_row = out_row * esize;
+    p->N = N;
+    p->T = T;
+    p->blocks = (T + block - 1) / block;
+    p->B = (int)B;
+    p->even = cu == nullptr ? (int)(N / B) : 0;
+    p->block_log2 = lg;
+    p->cp = (uint32_t)cp;
+    p->interleave = (uint32_t)interleave;
+    // 32 tokens a CTA, 8 where that would leave multiprocessors idle (2,047 tokens: 3.0 us with 8, 3.6 with 32; 8,192
+    // tokens: 5.3 and 4.5; 262,144: 99 and 69)
+    p->tokens = N >= kSms * kReadTokens ? kReadTokens : 8;
+    return 0;
+}
+
+template <class Q>
+int run_append(const Q& p, int dtype, int block, cudaStream_t st) {
+    return dtype == DCP_DTYPE_BF16 ? launch_append<Bf16>(p, block, st) : launch_append<F16>(p, block, st);
+}
+template <class Q>
+int run_read(const Q& p, int dtype, int Dk, cudaStream_t st) {
+    if (dtype == DCP_DTYPE_BF16) return launch_read<Bf16>(p, Dk, st);
+    if (dtype == DCP_DTYPE_F16) return launch_read<F16>(p, Dk, st);
+    return launch_read<F32>(p, Dk, st);
+}
+
+// The tables of the shards that are held.
+int tables_of(const void* const* kv_ptrs, const int32_t* const* table_ptrs, int cp, int64_t B, int64_t M, int64_t P,
+              int page, int block, Tables* t) {
+    if (M < 1 || P < 0 || P > 0x7fffffff || M > 0x7fffffff || B < 0 || B > 65535 || B * M > 0x7fffffff)
+        return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
+    t->page_log2 = -1;
+    for (int k = 0; (1 << k) <= DCP_MLA_PAGE_MAX; ++k)
+        if (page == 1 << k) t->page_log2 = k;
+    if (log2_of(block) < 0) return DCP_MLA_CACHE8_ERR_BAD_BLOCK;
+    if (page < DCP_MLA_PAGE_MIN || t->page_log2 < 0 || page % block != 0) return DCP_MLA_CACHE8_ERR_BAD_PAGE;
+    if (M * page > 0x7fffffff) return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
+    if (cp < 1 || cp > kCpMax) return DCP_MLA_CACHE8_ERR_BAD_CP;
+    if (kv_ptrs == nullptr || table_ptrs == nullptr) return DCP_MLA_CACHE8_ERR_NULL_POINTER;
+    for (int j = 0; j < cp; ++j) {
+        if (kv_ptrs[j] != nullptr && table_ptrs[j] == nullptr && B > 0) return DCP_MLA_CACHE8_ERR_NULL_POINTER;
+        if (!aligned(table_ptrs[j], 4)) return DCP_MLA_CACHE8_ERR_MISALIGNED;
+        t->of[j] = table_ptrs[j];
+    }
+    t->M = M;
+    t->P = (int)P;
+    return 0;
 }
 
 }  // namespace
@@ -1005,90 +1192,51 @@ extern "C" int dcp_mla_cache8_append(const void* latent, int64_t latent_row, con
                                      const int32_t* seq_lens, void* const* kv_ptrs, float* const* scale_ptrs, int cp,
                                      int64_t T, int block, int interleave, const double* inv_freq, int interleaved,
                                      float mscale, void* stream) {
-    if (N < 0 || N > 0x7fffffff || B < 0 || B > 65535 || T < 0 || T > 0x7fffffff || (Dk != 512 && Dk != 576) ||
-        (cu_new == nullptr && B > 0 && N % B != 0) || (B == 0 && N > 0))
-        return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
-    if (dtype != DCP_DTYPE_BF16 && dtype != DCP_DTYPE_F16) return DCP_MLA_CACHE8_ERR_BAD_DTYPE;
-    const int lg = log2_of(block);
-    if (lg < 0) return DCP_MLA_CACHE8_ERR_BAD_BLOCK;
-    if (const int rc = check_shards(kv_ptrs, scale_ptrs, cp, interleave)) return rc;
-    // (a cache that stands for two shards would be written by both at once)
-    for (int j = 0; j < cp; ++j)
-        for (int k = 0; k < j; ++k)
-            if (T > 0 && kv_ptrs[j] != nullptr && (kv_ptrs[j] == kv_ptrs[k] || scale_ptrs[j] == scale_ptrs[k]))
-                return DCP_MLA_CACHE8_ERR_BAD_CP;
-    if (N == 0 || T == 0) return 0;
-    if (latent == nullptr || seq_lens == nullptr || (Dk == 576 && k_rope == nullptr))
-        return DCP_MLA_CACHE8_ERR_NULL_POINTER;
-    if (!aligned(latent, 16) || !aligned(k_rope, 16) || latent_row % 8 != 0 || (Dk == 576 && rope_row % 8 != 0) ||
-        !aligned(seq_lens, 4) || !aligned(cu_new, 4) || !aligned(inv_freq, 8))
-        return DCP_MLA_CACHE8_ERR_MISALIGNED;
     AppendParams p = {};
-    p.latent = static_cast<const uint8_t*>(latent);
-    p.k_rope = static_cast<const uint8_t*>(k_rope);
-    p.latent_row = latent_row * 2;
-    p.rope_row = rope_row * 2;
-    p.cu = cu_new;
-    p.seq_lens = seq_lens;
-    p.inv_freq = Dk == 576 ? inv_freq : nullptr;
-    for (int j = 0; j < cp; ++j) {
-        p.kv[j] = static_cast<uint8_t*>(kv_ptrs[j]);
-        p.scales[j] = scale_ptrs[j];
-    }
-    p.N = N;
-    p.T = T;
-    p.blocks = (T + block - 1) / block;
-    p.B = (int)B;
-    p.Dk = Dk;
-    p.even = cu_new == nullptr ? (int)(N / B) : 0;
-    p.cp = (uint32_t)cp;
-    p.interleave = (uint32_t)interleave;
-    p.block_log2 = lg;
-    p.interleaved = interleaved != 0;
-    p.mscale = mscale;
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return dtype == DCP_DTYPE_BF16 ? launch_append<Bf16>(p, block, st) : launch_append<F16>(p, block, st);
+    bool nothing;
+    const int rc = append_params(latent, latent_row, k_rope, rope_row, dtype, N, B, Dk, cu_new, seq_lens, kv_ptrs,
+                                 scale_ptrs, cp, T, block, interleave, inv_freq, interleaved, mscale, T == 0, &p,
+                                 &nothing);
+    return rc != 0 || nothing ? rc : run_append(p, dtype, block, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int dcp_mla_cache8_append_paged(const void* latent, int64_t latent_row, const void* k_rope,
+                                           int64_t rope_row, int dtype, int64_t N, int64_t B, int Dk,
+                                           const int32_t* cu_new, const int32_t* seq_lens, void* const* kv_ptrs,
+                                           float* const* scale_ptrs, const int32_t* const* table_ptrs, int cp,
+                                           int64_t P, int page, int64_t M, int block, int interleave,
+                                           const double* inv_freq, int interleaved, float mscale, void* stream) {
+    PagedAppendParams p = {};
+    bool nothing;
+    int rc = tables_of(kv_ptrs, table_ptrs, cp, B, M, P, page, block, &p.tables);
+    if (rc == 0)
+        rc = append_params(latent, latent_row, k_rope, rope_row, dtype, N, B, Dk, cu_new, seq_lens, kv_ptrs,
+                           scale_ptrs, cp, M * page, block, interleave, inv_freq, interleaved, mscale, P == 0, &p,
+                           &nothing);
+    return rc != 0 || nothing ? rc : run_append(p, dtype, block, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int dcp_mla_cache8_read(const void* const* kv_ptrs, const float* const* scale_ptrs, int cp, int64_t B,
                                    int64_t T, int Dk, int block, int interleave, const int32_t* starts,
                                    const int32_t* cu, int64_t N, void* out, int64_t out_row, int dtype,
                                    void* stream) {
-    if (N < 0 || N > 0x7fffffff || B < 0 || B > 65535 || T < 0 || T > 0x7fffffff || (Dk != 512 && Dk != 576) ||
-        (cu == nullptr && B > 0 && N % B != 0) || (B == 0 && N > 0))
-        return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
-    if (dtype != DCP_DTYPE_BF16 && dtype != DCP_DTYPE_F16 && dtype != DCP_DTYPE_F32)
-        return DCP_MLA_CACHE8_ERR_BAD_DTYPE;
-    const int lg = log2_of(block);
-    if (lg < 0) return DCP_MLA_CACHE8_ERR_BAD_BLOCK;
-    if (const int rc = check_shards(kv_ptrs, scale_ptrs, cp, interleave)) return rc;
-    if (N == 0 || T == 0) return 0;
-    if (out == nullptr) return DCP_MLA_CACHE8_ERR_NULL_POINTER;
-    const int64_t esize = dtype == DCP_DTYPE_F32 ? 4 : 2;
-    if (!aligned(out, 16) || (out_row * esize) % 16 != 0 || !aligned(starts, 4) || !aligned(cu, 4))
-        return DCP_MLA_CACHE8_ERR_MISALIGNED;
     ReadParams p = {};
-    for (int j = 0; j < cp; ++j) {
-        p.kv[j] = static_cast<const uint8_t*>(kv_ptrs[j]);
-        p.scales[j] = scale_ptrs[j];
-    }
-    p.starts = starts;
-    p.cu = cu;
-    p.out = static_cast<uint8_t*>(out);
-    p.out_row = out_row * esize;
-    p.N = N;
-    p.T = T;
-    p.blocks = (T + block - 1) / block;
-    p.B = (int)B;
-    p.even = cu == nullptr ? (int)(N / B) : 0;
-    p.block_log2 = lg;
-    p.cp = (uint32_t)cp;
-    p.interleave = (uint32_t)interleave;
-    // 32 tokens a CTA, 8 where that would leave multiprocessors idle (2,047 tokens: 3.0 us with 8, 3.6 with 32; 8,192
-    // tokens: 5.3 and 4.5; 262,144: 99 and 69)
-    p.tokens = N >= kSms * kReadTokens ? kReadTokens : 8;
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == DCP_DTYPE_BF16) return launch_read<Bf16>(p, Dk, st);
-    if (dtype == DCP_DTYPE_F16) return launch_read<F16>(p, Dk, st);
-    return launch_read<F32>(p, Dk, st);
+    bool nothing;
+    const int rc = read_params(kv_ptrs, scale_ptrs, cp, B, T, Dk, block, interleave, starts, cu, N, out, out_row,
+                               dtype, T == 0, &p, &nothing);
+    return rc != 0 || nothing ? rc : run_read(p, dtype, Dk, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int dcp_mla_cache8_read_paged(const void* const* kv_ptrs, const float* const* scale_ptrs,
+                                         const int32_t* const* table_ptrs, int cp, int64_t B, int64_t P, int page,
+                                         int64_t M, int Dk, int block, int interleave, const int32_t* starts,
+                                         const int32_t* cu, int64_t N, void* out, int64_t out_row, int dtype,
+                                         void* stream) {
+    PagedReadParams p = {};
+    bool nothing;
+    int rc = tables_of(kv_ptrs, table_ptrs, cp, B, M, P, page, block, &p.tables);
+    if (rc == 0)
+        rc = read_params(kv_ptrs, scale_ptrs, cp, B, M * page, Dk, block, interleave, starts, cu, N, out, out_row,
+                         dtype, P == 0, &p, &nothing);
+    return rc != 0 || nothing ? rc : run_read(p, dtype, Dk, static_cast<cudaStream_t>(stream));
 }

@@ -99,6 +99,25 @@ int64_t dcp_mla_pages_compact_workspace_bytes(int64_t P);
 int dcp_mla_pages_copy(void* const* kv_ptrs, float* const* scale_ptrs, int pools, int64_t P, int page, int Dk,
                        int block, const int32_t* copies, int64_t n, void* stream);
 
+/*
+ * dcp_mla_cache8_append and dcp_mla_cache8_read over pages: the same calls, with a
+ * token of row b that is number t of shard j at token t mod page of page
+ * tables[j][b, t / page] of shard j's pool. A token whose entry is no page, or that
+ * lies past M pages, has no place: it is not written, and not read. Two rows must
+ * not append to one page in one call (dcp_mla_pages_update sees to it); nor may two
+ * shards share a pool. table_ptrs: a pointer per shard, as kv_ptrs.
+ *   shapes   0 <= B <= 65535, 0 <= P < 2^31, 1 <= M, B * M < 2^31, M * page < 2^31
+ */
+int dcp_mla_cache8_append_paged(const void* latent, int64_t latent_row, const void* k_rope, int64_t rope_row, int dtype,
+                                int64_t N, int64_t B, int Dk, const int32_t* cu_new, const int32_t* seq_lens,
+                                void* const* kv_ptrs, float* const* scale_ptrs, const int32_t* const* table_ptrs,
+                                int cp, int64_t P, int page, int64_t M, int block, int interleave,
+                                const double* inv_freq, int interleaved, float mscale, void* stream);
+int dcp_mla_cache8_read_paged(const void* const* kv_ptrs, const float* const* scale_ptrs,
+                              const int32_t* const* table_ptrs, int cp, int64_t B, int64_t P, int page, int64_t M,
+                              int Dk, int block, int interleave, const int32_t* starts, const int32_t* cu, int64_t N,
+                              void* out, int64_t out_row, int dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -7,6 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import decode_context_mla_dcp_gb300 as dcp
+from oracle import cache8
 from oracle import pages as ref
 
 pytestmark = pytest.mark.gpu
@@ -232,3 +233,127 @@ def test_update_and_copy_in_a_graph_on_another_stream():
         assert t.tolist() == tables and f.tolist() == refs and copies.tolist() == pairs and missing.tolist() == [short]
     for x, y in zip(kv + sc, plain):
         assert torch.equal(x, y)
+
+
+# ---- tokens in pages ------------------------------------------------------------------
+
+
+def randn(g, *shape):
+    return torch.randn(shape, generator=g, device=DEV)
+
+
+def make_paged(g, cp, B, M, page, dk, block, spare=3):
+    """Pools of finite codes, with tables of distinct pages in random order."""
+    P = B * M + spare
+    kv = [(randn(g, P, page, dk) * 100).clamp(-448, 448).to(torch.float8_e4m3fn) for _ in range(cp)]
+    sc = [torch.exp2(torch.randint(-8, 3, (P, page // block), generator=g, device=DEV).float()) for _ in range(cp)]
+    tb = [torch.randperm(P, generator=g, device=DEV)[:B * M].view(B, M).int() for _ in range(cp)]
+    return kv, sc, tb
+
+
+def as_rows(kv, sc, tb):
+    """The same rows, one after the other."""
+    rows = [c.view(torch.uint8)[t.long()].flatten(1, 2) for c, t in zip(kv, tb)]
+    return [r.view(torch.float8_e4m3fn) for r in rows], [s[t.long()].flatten(1, 2) for s, t in zip(sc, tb)]
+
+
+APPENDS = [
+    # B, counts, starts, cp, interleave, block, page, M, dk, dtype
+    (1, [1], [0], 1, 1, 1, 32, 1, 576, torch.bfloat16),
+    (1, [1], [31], 1, 1, 32, 32, 2, 576, torch.bfloat16),
+    (3, [4, 0, 90], [60, 5, 0], 1, 1, 1, 32, 4, 576, torch.float16),
+    (3, [4, 0, 90], [60, 5, 0], 1, 1, 16, 64, 2, 576, torch.bfloat16),
+    (2, [131, 64], [1, 127], 1, 1, 128, 128, 2, 512, torch.bfloat16),
+    (4, [300, 17, 1, 200], [13, 100, 255, 0], 4, 16, 64, 64, 2, 576, torch.bfloat16),
+    (3, [90, 5, 0], [13, 44, 7], 3, 5, 2, 32, 2, 576, torch.bfloat16),
+    (2, [50, 60], [100, 30], 1, 1, 8, 64, 2, 576, torch.bfloat16),  # past the last page
+    (2, [5000, 17], [60, 5000], 1, 1, 64, 4096, 2, 576, torch.bfloat16),
+    (700, None, None, 1, 1, 16, 32, 3, 512, torch.bfloat16),
+    (300, None, None, 2, 1, 32, 64, 2, 576, torch.float16),
+]
+
+
+@pytest.mark.parametrize("case", APPENDS, ids=lambda c: f"B{c[0]}cp{c[3]}i{c[4]}b{c[5]}p{c[6]}M{c[7]}d{c[8]}")
+def test_paged_append_and_read_are_those_of_the_rows(case):
+    """The contiguous forms have tests against 64 bits; over pages the same codes, scales and numbers, and no page is
+    touched besides."""
+    B, counts, starts, cp, il, block, page, M, dk, dtype = case
+    r = random.Random(B)
+    counts = counts or [r.choice([0, 1, 2, 7, 40]) for _ in range(B)]
+    starts = starts or [r.randrange(M * page * cp - 40) for _ in range(B)]
+    g = torch.Generator(device=DEV)
+    g.manual_seed(B + page)
+    n = sum(counts)
+    kv, sc, tb = make_paged(g, cp, B, M, page, dk, block)
+    if cp == 3:  # a shard that is not held
+        kv[1] = sc[1] = tb[1] = None
+    held = [j for j in range(cp) if kv[j] is not None]
+    pick = lambda x: [x[j] for j in held]
+    rows, rscales = as_rows(pick(kv), pick(sc), pick(tb))
+    full = lambda x: [x[held.index(j)] if j in held else None for j in range(cp)]
+    rows, rscales = full(rows), full(rscales)
+    before = [None if c is None else c.view(torch.uint8).clone() for c in kv]
+    latent = (randn(g, n + 1, 512) * torch.exp2(torch.randint(-9, 9, (n + 1, 1), generator=g, device=DEV).float())).to(dtype)
+    rope = randn(g, n + 1, 64).to(dtype) if dk == 576 else None
+    inv_freq = dcp.mla_rope_inv_freq(64)[0] if dk == 576 else None
+    cu = ints([0] + counts).cumsum(0).int()
+    lens = ints(starts)
+    kw = dict(cu_new=cu, block=block, interleave=il, inv_freq=inv_freq, mscale=1.25)
+    dcp.mla_cache8_append(latent, rope, rows, rscales, lens, **kw)
+    dcp.mla_cache8_append(latent, rope, kv, sc, lens, tables=tb, **kw)
+    got, gscales = as_rows(pick(kv), pick(sc), pick(tb))
+    for a, b, c, d in zip(got, pick(rows), gscales, pick(rscales)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)) and torch.equal(c, d)
+    for j in held:
+        spare = torch.ones((kv[j].shape[0],), dtype=torch.bool, device=DEV)
+        spare[tb[j].long().flatten()] = False
+        assert torch.equal(kv[j].view(torch.uint8)[spare], before[j][spare])
+    for out_dtype in (torch.bfloat16, torch.float16, torch.float32):
+        a, b = (torch.full((n + 1, dk), 7.0, dtype=out_dtype, device=DEV) for _ in range(2))
+        kw = dict(starts=lens, cu=cu, block=block, interleave=il)
+        dcp.mla_cache8_read(rows, rscales, n + 1, out=a, **kw)
+        dcp.mla_cache8_read(kv, sc, n + 1, out=b, tables=tb, **kw)
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("block", [1, 16])
+def test_tokens_without_a_page(block):
+    """They are not written and not read; entries that are no page may be any number."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(block)
+    page, dk = 32, 576
+    kv, sc, _ = make_paged(g, 1, 1, 4, page, dk, block, 0)
+    tb = [ints([[2, -1, 0, 4], [1 << 30, 1, -(1 << 31), 3]], 2, 4)]
+    n = 2 * 128
+    latent, rope = randn(g, n, 512).bfloat16(), randn(g, n, 64).bfloat16()
+    lens = ints([0, 0])
+    dcp.mla_cache8_append(latent, rope, kv, sc, lens, block=block, tables=tb)
+    out = torch.full((n, dk), 7.0, device=DEV)
+    dcp.mla_cache8_read(kv, sc, n, block=block, out=out, tables=tb)
+    x = torch.cat((latent, rope), 1).double().view(2, 4, page, dk)
+    got = out.double().view(2, 4, page, dk)
+    for b, i in ((0, 0), (0, 2), (1, 1), (1, 3)):
+        # half a step of e4m3, or of its subnormals (2^-10 of a scale that is at most 2 / 448 of a block's peak)
+        peak = x[b, i].abs().amax()
+        assert ((got[b, i] - x[b, i]).abs() <= torch.maximum(2.0 ** -4 * x[b, i].abs(), 2.0 ** -10 * peak * 2 / 448)).all()
+    for b, i in ((0, 1), (0, 3), (1, 0), (1, 2)):
+        assert (got[b, i] == 7).all()
+
+
+def test_pages_past_32_bits():
+    """Tokens whose bytes, and whose numbers, lie far into a pool of 8 GB."""
+    P, page = 230000, 64
+    kv = [torch.zeros((P, page, 576), dtype=torch.uint8, device=DEV)]
+    sc = [torch.ones((P, 1), device=DEV)]
+    tb = [ints([[P - 1, 116509], [3, P - 2]], 2, 2)]
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    latent, rope = randn(g, 200, 512).bfloat16(), randn(g, 200, 64).bfloat16()
+    dcp.mla_cache8_append(latent, rope, kv, sc, ints([0, 20]), block=64, tables=tb)
+    got = dcp.mla_cache8_read(kv, sc, 200, starts=ints([0, 20]), block=64, tables=tb, dtype=torch.float32).double()
+    x = torch.cat((latent, rope), 1).double()
+    # half a step of e4m3, or of its subnormals: 2^-10 of the block's scale, which is the one that 5 sigma need or, where
+    # row 1 begins inside a block that holds tokens, the 1 that stands there (a scale never shrinks)
+    assert ((got - x).abs() <= torch.clamp(2.0 ** -4 * x.abs(), min=2.0 ** -10)).all()
+    touched = kv[0].view(P, -1).any(1).nonzero()[:, 0].tolist()
+    assert touched == [3, 116509, P - 2, P - 1]

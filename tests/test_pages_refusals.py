@@ -74,6 +74,42 @@ def test_copy_of_no_pairs_is_nothing():
     dcp.dcp_mla_pages_copy(**{**COPY, "n": 0, "copies": None})
 
 
+PAGED = dict(latent=A, latent_row=512, k_rope=A, rope_row=64, dtype=0, N=4, B=2, Dk=576, cu_new=A, seq_lens=A,
+             kv_ptrs=[A], scale_ptrs=[2 * A], table_ptrs=[A], cp=1, P=8, page=64, M=4, stream=0)
+READ = dict(kv_ptrs=[A], scale_ptrs=[A], table_ptrs=[A], cp=1, B=2, P=8, page=64, M=4, Dk=576, block=1, interleave=1,
+            starts=A, cu=A, N=4, out=A, out_row=576, dtype=0, stream=0)
+DTYPE = -206
+POOLS = [(SHAPE, dict(B=-1)), (SHAPE, dict(B=65536)), (SHAPE, dict(P=-1)), (SHAPE, dict(P=1 << 31)),
+         (SHAPE, dict(M=0)), (SHAPE, dict(M=1 << 25)), (SHAPE, dict(B=65535, M=1 << 16)), (PAGE, dict(page=16)),
+         (PAGE, dict(page=65)), (PAGE, dict(page=8192)), (PAGE, dict(page=32, block=64)), (BLOCK, dict(block=3)),
+         (CP, dict(cp=0)), (CP, dict(cp=17, kv_ptrs=[A] * 17, scale_ptrs=[A] * 17, table_ptrs=[A] * 17)),
+         (CP, dict(interleave=0)), (NULL, dict(table_ptrs=[None])),
+         (NULL, dict(kv_ptrs=[None], scale_ptrs=[None])), (NULL, dict(scale_ptrs=[None])),
+         (ALIGN, dict(table_ptrs=[A + 2])), (ALIGN, dict(kv_ptrs=[A + 8])), (ALIGN, dict(scale_ptrs=[A + 2])),
+         (SHAPE, dict(Dk=640))]
+
+
+@pytest.mark.parametrize("code,change", POOLS + [
+    (SHAPE, dict(N=-1)), (SHAPE, dict(cu_new=None, N=3)), (SHAPE, dict(B=0)), (DTYPE, dict(dtype=2)),
+    (NULL, dict(latent=None)), (NULL, dict(k_rope=None)), (NULL, dict(seq_lens=None)), (ALIGN, dict(latent_row=516)),
+    (CP, dict(cp=2, kv_ptrs=[A, A], scale_ptrs=[A, 2 * A], table_ptrs=[A, A]))])
+def test_paged_append(code, change):
+    refused(code, dcp.dcp_mla_cache8_append_paged, PAGED, **change)
+
+
+@pytest.mark.parametrize("code,change", POOLS + [
+    (SHAPE, dict(N=-1)), (SHAPE, dict(cu=None, N=3)), (DTYPE, dict(dtype=5)), (NULL, dict(out=None)),
+    (ALIGN, dict(out=A + 8)), (ALIGN, dict(out_row=580)), (ALIGN, dict(starts=A + 2))])
+def test_paged_read(code, change):
+    refused(code, dcp.dcp_mla_cache8_read_paged, READ, **change)
+
+
+def test_paged_calls_of_nothing():
+    dcp.dcp_mla_cache8_append_paged(**{**PAGED, "N": 0})
+    dcp.dcp_mla_cache8_append_paged(**{**PAGED, "P": 0})
+    dcp.dcp_mla_cache8_read_paged(**{**READ, "N": 0, "out": None})
+
+
 def test_workspace_bytes():
     up, co = dcp.dcp_mla_pages_update_workspace_bytes, dcp.dcp_mla_pages_compact_workspace_bytes
     assert up(4, 100, 50, True) >= up(4, 100, 50, False) + 4 * 100 * 4
@@ -112,6 +148,28 @@ def test_wrappers():
         copy([kv.float()], [sc], pairs)
     with pytest.raises(TypeError):
         copy([kv], [sc.double()], pairs)
+
+
+def test_wrappers_check_tables():
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    kv, sc, t = torch.zeros((4, 64, 576), dtype=torch.uint8), torch.ones((4, 64)), i32(2, 3)
+    lat, pe, lens = torch.zeros((2, 512), dtype=torch.bfloat16), torch.zeros((2, 64), dtype=torch.bfloat16), i32(2)
+    kv48, sc48 = torch.zeros((4, 48, 576), dtype=torch.uint8), torch.ones((4, 48))
+    calls = (lambda c, s, tables, **k: dcp.mla_cache8_append(lat, pe, c, s, lens, tables=tables, **k),
+             lambda c, s, tables, **k: dcp.mla_cache8_read(c, s, 2, tables=tables, **k))
+    for call in calls:
+        with pytest.raises(ValueError, match="CUDA"):
+            call([kv], [sc], [t])
+        for c, s, tables, kw in [([kv], [sc], [], {}), ([kv], [sc], [t, t], {}), ([kv], [sc], [None], {}),
+                                 ([kv, None], [sc, None], [t, t], {}), ([kv], [sc], [t.long()], {}),
+                                 ([kv], [sc], [lens], {}), ([kv], [sc], [i32(3, 2).T], {}),
+                                 ([kv, kv.clone()], [sc, sc.clone()], [t, i32(2, 4)], {}), ([kv48], [sc48], [t], {}),
+                                 ([kv], [sc], [i32(2, 0)], {}),
+                                 ([kv[:, :32].contiguous()], [torch.ones((4, 1))], [t], dict(block=64))]:
+            with pytest.raises(ValueError):
+                call(c, s, tables, **kw)
+    with pytest.raises(ValueError, match="seq_lens"):  # rows are the tables', not the pool's
+        dcp.mla_cache8_append(lat, pe, [kv], [sc], i32(4), tables=[t])
 
 
 # ---- the plain forms, by hand ---------------------------------------------------------
