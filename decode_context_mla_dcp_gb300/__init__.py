@@ -36,9 +36,10 @@ from ._binding import (DCP_DTYPE_BF16, DCP_DTYPE_F16, DCP_FLAG_LSE_FIRST, DCP_FL
                        DCP_MLA_PAGE_MAX, DCP_MLA_PAGE_MIN, DCP_MLA_PAGES_POOLS_MAX, dcp_mla_pages_update,
                        dcp_mla_pages_update_workspace_bytes, dcp_mla_pages_compact,
                        dcp_mla_pages_compact_workspace_bytes, dcp_mla_pages_copy,
-                       dcp_mla_cache8_append_paged, dcp_mla_cache8_read_paged)
+                       dcp_mla_cache8_append_paged, dcp_mla_cache8_read_paged, dcp_mla_cache8_decode_paged,
+                       dcp_mla_cache8_decode_paged_workspace_bytes)
 from .cache8 import mla_cache8_append, mla_cache8_decode, mla_cache8_read, mla_rope, mla_rope_inv_freq
-from .cache8_pages import mla_cache8_pages_compact, mla_cache8_pages_copy, mla_cache8_pages_update
+from .cache8_pages import mla_cache8_groups, mla_cache8_pages_compact, mla_cache8_pages_copy, mla_cache8_pages_update
 
 __all__ = ["dcp_lse_reduce", "dcp_lse_reduce_ex", "dcp_lse_reduce_strerror", "dcp_lse_reduce_version", "merge",
            "dcp_mla_decode_partial", "dcp_mla_decode_smem_bytes", "mla_decode_partial", "DCP_MLA_SPLIT_MAX",
@@ -57,7 +58,8 @@ __all__ = ["dcp_lse_reduce", "dcp_lse_reduce_ex", "dcp_lse_reduce_strerror", "dc
            "mla_cache8_pages_update", "mla_cache8_pages_compact", "mla_cache8_pages_copy",
            "dcp_mla_pages_update", "dcp_mla_pages_update_workspace_bytes", "dcp_mla_pages_compact",
            "dcp_mla_pages_compact_workspace_bytes", "dcp_mla_pages_copy",
-           "dcp_mla_cache8_append_paged", "dcp_mla_cache8_read_paged",
+           "dcp_mla_cache8_append_paged", "dcp_mla_cache8_read_paged", "dcp_mla_cache8_decode_paged",
+           "dcp_mla_cache8_decode_paged_workspace_bytes", "mla_cache8_groups",
            "DCP_MLA_PAGE_MIN", "DCP_MLA_PAGE_MAX", "DCP_MLA_PAGES_POOLS_MAX"]
 
 

@@ -31,7 +31,8 @@ EXPORTED_SYMBOLS = ("dcp_lse_reduce", "dcp_lse_reduce_ex", "dcp_lse_reduce_strer
                     "dcp_mla_cache8_decode_workspace_bytes", "dcp_mla_cache8_strerror",
                     "dcp_mla_pages_update", "dcp_mla_pages_update_workspace_bytes", "dcp_mla_pages_compact",
                     "dcp_mla_pages_compact_workspace_bytes", "dcp_mla_pages_copy",
-                    "dcp_mla_cache8_append_paged", "dcp_mla_cache8_read_paged")
+                    "dcp_mla_cache8_append_paged", "dcp_mla_cache8_read_paged", "dcp_mla_cache8_decode_paged",
+                    "dcp_mla_cache8_decode_paged_workspace_bytes")
 DCP_MLA_CACHE8_BLOCK_MAX = 128
 DCP_MLA_CACHE8_CP_MAX = 16
 DCP_MLA_PAGE_MIN = 32
@@ -143,6 +144,12 @@ def load(path: str | None = None):
         lib.dcp_mla_cache8_read_paged.argtypes = [pv, pv, pv, ci, i64, i64, ci, i64, ci, ci, ci, vp, vp, i64, vp, i64,
                                                   ci, vp]
         lib.dcp_mla_cache8_read_paged.restype = ci
+        lib.dcp_mla_cache8_decode_paged.argtypes = [vp, i64, i64, pv, pv, pv, vp, vp, vp, ci, i64, ci, ci, ci, i64, ci,
+                                                    i64, ci, ci, i64, i64, cf, ci, vp, i64, vp, vp, vp,
+                                                    ctypes.c_uint, vp]
+        lib.dcp_mla_cache8_decode_paged.restype = ci
+        lib.dcp_mla_cache8_decode_paged_workspace_bytes.argtypes = [ci, i64, ci, ci, i64, i64, i64, ci, ci]
+        lib.dcp_mla_cache8_decode_paged_workspace_bytes.restype = i64
         lib.dcp_mla_cache8_strerror.argtypes = [ci]
         lib.dcp_mla_cache8_strerror.restype = ctypes.c_char_p
         if path is None:
@@ -347,6 +354,29 @@ def dcp_mla_cache8_read_paged(kv_ptrs, scale_ptrs, table_ptrs, cp: int, B: int, 
                                              _ptr_array(table_ptrs, cp), int(cp), int(B), int(P), int(page), int(M),
                                              int(Dk), int(block), int(interleave), _ptr(starts), _ptr(cu), int(N),
                                              _ptr(out), int(out_row), int(dtype), _stream(stream)))
+
+
+def dcp_mla_cache8_decode_paged(q, q_row: int, q_head: int, kv_ptrs, scale_ptrs, table_ptrs, seq_lens, cp: int, B: int,
+                                H: int, Dk: int, Dv: int, P: int, page: int, M: int, block: int, interleave: int,
+                                window: int, sinks: int, scale: float, lse_base_e: bool, workspace,
+                                workspace_bytes: int, out, lse=None, groups=None, shared=None, status=None,
+                                flags: int = 0, stream=None) -> None:
+    """Single-token attention over the pages of an 8-bit cache (see include/dcp_mla_pages.h)."""
+    _check8(load().dcp_mla_cache8_decode_paged(_ptr(q), int(q_row), int(q_head), _ptr_array(kv_ptrs, cp),
+                                               _ptr_array(scale_ptrs, cp), _ptr_array(table_ptrs, cp),
+                                               _ptr(seq_lens), _ptr(groups), _ptr(shared), int(cp), int(B), int(H),
+                                               int(Dk), int(Dv), int(P), int(page), int(M), int(block),
+                                               int(interleave), int(window), int(sinks), float(scale),
+                                               1 if lse_base_e else 0, _ptr(workspace), int(workspace_bytes),
+                                               _ptr(out), _ptr(lse), _ptr(status), int(flags), _stream(stream)))
+
+
+def dcp_mla_cache8_decode_paged_workspace_bytes(cp: int, B: int, H: int, page: int, M: int, window: int, sinks: int,
+                                                grouped: bool, num_sms: int) -> int:
+    """Bytes of workspace a decode over pages needs, 0 for none (host only)."""
+    return int(load().dcp_mla_cache8_decode_paged_workspace_bytes(int(cp), int(B), int(H), int(page), int(M),
+                                                                  int(window), int(sinks), 1 if grouped else 0,
+                                                                  int(num_sms)))
 
 
 def dcp_mla_pages_update(tables, refs, parents, keeps, wants, B: int, M: int, P: int, page: int, tables_out, refs_out,

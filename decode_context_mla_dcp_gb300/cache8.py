@@ -385,7 +385,7 @@ def mla_cache8_read(caches, scales, total: int, *, starts=None, cu=None, block: 
 
 def mla_cache8_decode(q, caches, scales, seq_lens, scale: float, *, block: int = 1, interleave: int = 1,
                       window: int = 0, sinks: int = 0, lse_base_e: bool = True, out=None, lse=None, workspace=None,
-                      status=None, flags: int = 0, stream=None):
+                      status=None, flags: int = 0, tables=None, groups=None, shared=None, stream=None):
     """Single-token attention over the cached positions of each row.
 
     q: CUDA bf16 [B, H, Dk] (unit stride along Dk, even row and head strides);
@@ -396,9 +396,30 @@ def mla_cache8_decode(q, caches, scales, seq_lens, scale: float, *, block: int =
     None the result is the partial over the held ones, for ``merge``. workspace: a
     contiguous CUDA tensor of at least dcp_mla_cache8_decode_workspace_bytes bytes,
     256-byte aligned, allocated when not given and needed. status: None, or an
-    int32 CUDA tensor (see the C header)."""
+    int32 CUDA tensor (see the C header).
+
+    tables: as for the append (workspace then: dcp_mla_cache8_decode_paged_workspace_bytes).
+    With tables, groups (int32 [B, 2]: first row and rows of each row's group of
+    consecutive rows) and shared (int32 [B]: positions that a group's rows have in
+    common, in the same pages) let rows attend to a common prefix together;
+    mla_cache8_groups makes both. The result is the same without."""
     lib, torch = _ready()
     index, B, T, dk, kv, sc = _shards(caches, scales, block, interleave)
+    if tables is not None:
+        P, page = B, T
+        B, M, tb = _tables(tables, caches, page, block, index)
+        group_ptr = shared_ptr = None
+        if groups is not None:
+            if groups.dtype != torch.int32 or groups.shape != (B, 2) or groups.get_device() != index or \
+                    not groups.is_contiguous():
+                raise ValueError("groups must be a contiguous int32 tensor [B, 2] on the caches' device")
+            if window > 0:
+                raise ValueError("groups do not go together with a window")
+            group_ptr, shared_ptr = groups.data_ptr(), _ints("shared", shared, B, index)
+        if (groups is None) != (shared is None):
+            raise ValueError("groups and shared come together")
+    elif groups is not None or shared is not None:
+        raise ValueError("groups need a paged cache: tables")
     if q.dim() != 3 or q.dtype != torch.bfloat16 or q.get_device() != index:
         raise ValueError("q must be bf16 [B, H, Dk] with unit inner stride, on the caches' device")
     qb, H, qd = q.shape
@@ -416,7 +437,8 @@ def mla_cache8_decode(q, caches, scales, seq_lens, scale: float, *, block: int =
         with inside:
             return mla_cache8_decode(q, caches, scales, seq_lens, scale, block=block, interleave=interleave,
                                      window=window, sinks=sinks, lse_base_e=lse_base_e, out=out, lse=lse,
-                                     workspace=workspace, status=status, flags=flags)
+                                     workspace=workspace, status=status, flags=flags, tables=tables, groups=groups,
+                                     shared=shared)
     if out is None:
         out = torch.empty((B, H, 512), dtype=torch.bfloat16, device=q.device)
     elif out.shape != (B, H, 512) or out.dtype != torch.bfloat16 or out.get_device() != index or \
@@ -428,12 +450,16 @@ def mla_cache8_decode(q, caches, scales, seq_lens, scale: float, *, block: int =
         raise ValueError("lse must be a contiguous fp32 tensor [B, H] on the caches' device")
     room = None
     if workspace is None:
-        size = _ROOM.get((cp, B, H, T, window, sinks, index))
+        key = (cp, B, H, T, window, sinks, index) if tables is None else \
+            (cp, B, H, T, window, sinks, index, M, groups is None)
+        size = _ROOM.get(key)
         if size is None:
             if len(_ROOM) > 4096:
                 _ROOM.clear()
-            size = lib.dcp_mla_cache8_decode_workspace_bytes(cp, B, H, T, window, sinks, _sms(index))
-            _ROOM[cp, B, H, T, window, sinks, index] = size
+            size = lib.dcp_mla_cache8_decode_workspace_bytes(cp, B, H, T, window, sinks, _sms(index)) \
+                if tables is None else lib.dcp_mla_cache8_decode_paged_workspace_bytes(
+                    cp, B, H, page, M, window, sinks, groups is not None, _sms(index))
+            _ROOM[key] = size
         if size > 0:
             workspace = torch.empty((size,), dtype=torch.uint8, device=q.device)
             room = workspace.data_ptr()
@@ -445,9 +471,15 @@ def mla_cache8_decode(q, caches, scales, seq_lens, scale: float, *, block: int =
         if status.dtype != torch.int32 or status.get_device() != index or status.numel() < 1:
             raise ValueError("status must be an int32 tensor on the caches' device")
         status = status.data_ptr()
-    rc = lib.dcp_mla_cache8_decode(q.data_ptr(), row, head, kv, sc, lens, cp, B, H, dk, 512, T, block, interleave,
-                                   window, sinks, scale, lse_base_e, room, size, out.data_ptr(), lse.data_ptr(),
-                                   status, flags, raw)
+    if tables is None:
+        rc = lib.dcp_mla_cache8_decode(q.data_ptr(), row, head, kv, sc, lens, cp, B, H, dk, 512, T, block, interleave,
+                                       window, sinks, scale, lse_base_e, room, size, out.data_ptr(), lse.data_ptr(),
+                                       status, flags, raw)
+    else:
+        rc = lib.dcp_mla_cache8_decode_paged(q.data_ptr(), row, head, kv, sc, tb, lens, group_ptr, shared_ptr, cp, B,
+                                             H, dk, 512, P, page, M, block, interleave, window, sinks, scale,
+                                             lse_base_e, room, size, out.data_ptr(), lse.data_ptr(), status, flags,
+                                             raw)
     if rc:
         _b._check8(rc)
     return out, lse

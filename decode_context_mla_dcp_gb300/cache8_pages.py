@@ -73,6 +73,23 @@ def _space(workspace, key, ask, index):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
+def mla_cache8_groups(rows, shared, device="cuda"):
+    """The groups of a batch for mla_cache8_decode, from the host: rows[g] consecutive
+    rows of the batch begin with the same shared[g] positions, in the same pages (a row
+    alone is a group of 1). Returns (groups int32 [B, 2], shared int32 [B])."""
+    import torch
+    rows, shared = [int(n) for n in rows], [int(n) for n in shared]
+    if len(rows) != len(shared) or min(rows + shared, default=0) < 0 or max(shared, default=0) >= 1 << 31:
+        raise ValueError("rows and shared must be counts of the same groups")
+    pairs, common, first = [], [], 0
+    for n, s in zip(rows, shared):
+        pairs += [(first, n)] * n
+        common += [s] * n
+        first += n
+    return torch.tensor(pairs, dtype=torch.int32, device=device).view(first, 2), \
+        torch.tensor(common, dtype=torch.int32, device=device)
+
+
 def mla_cache8_pages_update(tables, refs, parents, keeps, wants, *, page: int, cp: int = 1, shard: int = 0,
                             interleave: int = 1, out=None, copies=None, missing=None, workspace=None, stream=None):
     """Rows take over other rows' pages, are cut back, end, begin and grow, all at once.

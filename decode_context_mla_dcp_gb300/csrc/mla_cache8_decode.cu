@@ -69,6 +69,7 @@
 #include "dcp_lse_reduce.h"
 #include "dcp_mla_cache8.h"
 #include "dcp_mla_decode.h"
+#include "dcp_mla_pages.h"
 
 namespace {
 
@@ -112,10 +113,23 @@ struct DecodeBase {
 };
 template <int kShards>
 struct DecodeParams : DecodeBase {
+    static constexpr bool kPaged = false;
     CUtensorMap tm_latent[kShards];        // boxes of 128 dims x 128 tokens, 128-byte swizzle
     CUtensorMap tm_rope[kShards];          // boxes of 64 dims x 128 tokens, 64-byte swizzle
     const float* scales[kShards];
     __device__ __forceinline__ uint32_t shards() const { return kShards == 1 ? 1u : cp; }
+};
+// A cache in pages (the maps are [P, page, Dk], their boxes a page's tokens where a page has fewer than 128), and rows
+// that share a prefix. T is what a row's table has room for.
+template <int kShards>
+struct PagedParams : DecodeParams<kShards> {
+    static constexpr bool kPaged = true;
+    const int* tables[kShards];
+    const int2* groups;                    // [B] first row and rows of the row's group, or NULL
+    const int* shared;                     // [B] positions that they have in common
+    int* lead;                             // [B] for the join: the group's first row if the row uses the prefix, or -1
+    int64_t M;
+    int P, page_log2;
 };
 
 // ---- PTX helpers -------------------------------------------------------------
@@ -291,28 +305,91 @@ __device__ __forceinline__ uint32_t share(const P& p, Prefix x, uint32_t j) {
 }
 struct RowView {
     Prefix len, win, sink;
+    bool prefix;  // (of a group: whole tiles)
 };
 __device__ __forceinline__ uint32_t row_length(const DecodeBase& p, int b) {
     const int n = p.seq_lens[b];
     return n < 0 ? 0u : (uint32_t)n;
 }
+// What is walked through. Without groups there is a line for each row, all of its positions. With groups there are 2 B:
+// line b < B is the prefix of row b's group for the b-th set of that group's heads (a set is head_blocks blocks of kNH
+// heads of the group's rows, one row's behind the other's), of no tile where the group has fewer sets; line B + b is
+// what row b has behind the prefix. A prefix ends at a whole tile of each shard, and the rest belongs to the rows. A row
+// that is shorter than its prefix takes no part, and has all its tokens in its own line.
+struct Line {
+    uint32_t length;  // positions [base, length)
+    uint32_t base;
+    uint32_t source;  // kPrefix and the set, or 0; and the heads of this CTA's block (kHeadsAt)
+};
+constexpr uint32_t kPrefix = 1u << 31, kHeadsAt = 16, kSetMask = 0xffffu;
 template <class P>
-__device__ __forceinline__ RowView row_view(const P& p, uint32_t L) {
+__device__ __forceinline__ int line_count(const P& p) {
+    if constexpr (P::kPaged)
+        if (p.groups != nullptr) return 2 * p.B;
+    return p.B;
+}
+// The row that a line's tokens are of.
+template <class P>
+__device__ __forceinline__ int line_row(const P& p, int v, uint32_t source) {
+    if constexpr (P::kPaged) {
+        if (p.groups == nullptr) return v;
+        return source & kPrefix ? v - (int)(source & kSetMask) : v - p.B;
+    }
+    return v;
+}
+template <class P>
+__device__ __forceinline__ Line line_of(const P& p, int v, int hblk, int block_heads) {
+    Line r = {0u, 0u, 0u};
+    if constexpr (P::kPaged) {
+        const int h0 = hblk * block_heads, own = p.H - h0 < block_heads ? p.H - h0 : block_heads;
+        r.source = (uint32_t)own << kHeadsAt;
+        if (p.groups != nullptr) {
+            const int b = v < p.B ? v : v - p.B;
+            const int2 g = p.groups[b];
+            const int n = p.shared[b], len = p.seq_lens[b];
+            // (groups that the call does not allow have no prefix, or another one: nothing is read out of place)
+            const bool is = g.x >= 0 && g.x <= b && g.y >= 2 && b - g.x < g.y && g.y <= p.B - g.x && n > 0;
+            const uint32_t common = is ? (uint32_t)n : 0u;
+            if (v >= p.B) {
+                r.length = len < 0 ? 0u : (uint32_t)len;
+                r.base = r.length >= common ? common : 0u;
+                return r;
+            }
+            const int set = b - g.x, first = (set * p.head_blocks + hblk) * block_heads;
+            const int left = is ? g.y * p.H - first : 0;
+            if (is && set * p.head_blocks * block_heads < g.y * p.H) r.length = common;
+            r.source = kPrefix | (uint32_t)set | ((uint32_t)max(0, min(left, block_heads)) << kHeadsAt);
+            return r;
+        }
+    }
+    r.length = row_length(p, v);
+    return r;
+}
+template <class P>
+__device__ __forceinline__ RowView row_view(const P& p, const Line& r) {
+    const uint32_t L = r.length;
     const uint32_t w = p.window > 0 && L > p.window ? L - p.window : 0u;
     RowView v;
     v.len = prefix_of(p, L);
     v.win = p.window > 0 ? prefix_of(p, w) : Prefix{0u, 0u};
     v.sink = p.sinks > 0 ? prefix_of(p, p.sinks < w ? p.sinks : w) : Prefix{0u, 0u};
+    if constexpr (P::kPaged) {
+        if (p.groups != nullptr) {  // (there is no window with groups)
+            v.win = prefix_of(p, r.base);
+            v.prefix = (r.source & kPrefix) != 0;
+        }
+    }
     return v;
 }
-// A shard's visible tokens: [0, first) and [start, end); tiles of the one, then of the other.
+// A shard's visible tokens: [0, first) and [start, end); tiles of the one, then of the other. Pages want tiles that
+// begin at a multiple of 128 tokens: `skip` tokens of the second part's first tile come before what is visible.
 struct ShardView {
-    uint32_t first, start, end;
+    uint32_t first, start, end, skip;
     int tiles_first, tiles;
 };
 template <class P>
 __device__ __forceinline__ ShardView shard_view(const P& p, const RowView& v, uint32_t j) {
-    ShardView s = {0u, 0u, 0u, 0, 0};
+    ShardView s = {0u, 0u, 0u, 0u, 0, 0};
     if (!((p.held >> j) & 1u)) return s;
     s.end = share(p, v.len, j);
     if (p.window > 0) {
@@ -320,13 +397,22 @@ __device__ __forceinline__ ShardView shard_view(const P& p, const RowView& v, ui
         s.first = p.sinks > 0 ? share(p, v.sink, j) : 0u;
         if (s.first == s.start) s.first = s.start = 0u;
     }
+    if constexpr (P::kPaged) {
+        if (p.groups != nullptr) {
+            s.start = share(p, v.win, j) & ~(uint32_t)(kTile - 1);
+            if (v.prefix) s.end &= ~(uint32_t)(kTile - 1);
+        } else {
+            s.skip = s.start & (kTile - 1);
+            s.start -= s.skip;
+        }
+    }
     s.tiles_first = (int)((s.first + kTile - 1) / kTile);
     s.tiles = s.tiles_first + (int)((s.end - s.start + kTile - 1) / kTile);
     return s;
 }
 template <class P>
-__device__ __forceinline__ int row_tiles(const P& p, uint32_t L) {
-    const RowView v = row_view(p, L);
+__device__ __forceinline__ int row_tiles(const P& p, const Line& r) {
+    const RowView v = row_view(p, r);
     int n = 0;
 #pragma unroll 1
     for (uint32_t j = 0; j < p.shards(); ++j) n += shard_view(p, v, j).tiles;
@@ -339,8 +425,8 @@ struct Cursor {
     uint32_t j;
     int i;  // tile of the shard
     template <class P>
-    __device__ __forceinline__ void seek(const P& p, uint32_t L, int tile) {
-        row = row_view(p, L);
+    __device__ __forceinline__ void seek(const P& p, const Line& r, int tile) {
+        row = row_view(p, r);
         j = 0;
         s = shard_view(p, row, 0);
         i = tile;
@@ -365,6 +451,7 @@ struct Cursor {
         const uint32_t n = (i < s.tiles_first ? s.first : s.end) - token();
         return n < kTile ? (int)n : kTile;
     }
+    __device__ __forceinline__ int skip() const { return i == s.tiles_first ? (int)s.skip : 0; }
 };
 
 // The CTAs' shares. All rows' tiles lie in a line that is cut evenly, but a row that begins in a share costs its CTA
@@ -376,11 +463,14 @@ __device__ __forceinline__ int places(int tiles, int change) { return tiles > 0 
 
 // What the join needs of a row: its first CTA range and its number of segments. Written by the CTA that has the
 // row's first tile (at place pre + change); for a row without a tile by the first CTA.
-__device__ __forceinline__ void tell_row(const DecodeBase& p, int b, int n, int pre, int g, int g_end, int per,
+template <class P>
+__device__ __forceinline__ void tell_row(const P& p, int b, const Line& r, int n, int pre, int g, int g_end, int per,
                                          int range, int change) {
     pre += change;
-    if (n == 0 && range == 0) p.row_info[b] = make_int2(0, 0);
-    else if (n > 0 && pre >= g && pre < g_end) p.row_info[b] = make_int2(range, (pre + n - 1) / per - range + 1);
+    const bool here = n == 0 ? range == 0 : pre >= g && pre < g_end;
+    if (here) p.row_info[b] = n == 0 ? make_int2(0, 0) : make_int2(range, (pre + n - 1) / per - range + 1);
+    if constexpr (P::kPaged)
+        if (here && p.groups != nullptr && b >= p.B) p.lead[b - p.B] = r.base > 0 ? p.groups[b - p.B].x : -1;
 }
 
 // ---- the kernel ------------------------------------------------------------------
@@ -417,13 +507,14 @@ struct Shape {
 // What the loading warp tells the others about a tile.
 struct alignas(16) TileInfo {
     uint32_t token;  // first token
-    int valid;       // tokens; 0: no more tiles
+    int valid;       // tokens; 0: no more tiles (pages: and those to skip, from bit 8 on)
     uint32_t what;   // shard, and kFirst ...
     int row;
 };
 constexpr uint32_t kFirst = 256, kLast = 512;  // the first, the last tile of a segment (a run of tiles of one row)
 constexpr uint32_t kWhole = 1024;              // the segment is the whole row
 constexpr uint32_t kStarts = 2048;             // the segment has the row's first tile
+constexpr uint32_t kFresh = 4096;              // no tile of the segment before this one has a visible token (pages)
 
 struct Shared {  // barriers and small things, behind the scale atom
     uint64_t info_full[4];    // a tile's description is there
@@ -442,8 +533,12 @@ struct Shared {  // barriers and small things, behind the scale atom
     uint32_t tmem;
     int abort;
     int find[4];              // the CTA's first row (-1: none), its first tile there, the row's tiles
-    int wsum[16];
+    union {
+        int wsum[16];
+        int pages[4][4];      // of a tile, by fours of 32 tokens at most; negative: none
+    };
     TileInfo info[4];
+    uint32_t source[4];       // of a tile's line (pages)
 };
 static_assert(sizeof(Shared) <= 512 && offsetof(Shared, s_full) == 160, "");
 
@@ -607,9 +702,10 @@ __device__ __forceinline__ void issue_values(uint32_t ka, uint32_t pa, uint32_t 
 // Shares. All rows' tiles are cut evenly over the CTAs (a row's parts are joined by
 // the second kernel), each head block for itself; a call whose rows have at most two
 // tiles gives whole rows to a CTA and needs no second kernel.
-template <int kDk, int kNH, int kShards>
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ DecodeParams<kShards> p) {
+template <int kDk, int kNH, class P>
+__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ P p) {
     using S = Shape<kDk, kNH>;
+    constexpr bool kPaged = P::kPaged;
     constexpr int kHW = S::kHW, kChange = kNH / 32;
     constexpr uint32_t kIdS = (1u << 4) | ((uint32_t)(S::kRows >> 3) << 17) | (8u << 24);
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -642,6 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         if (lane == 0) {
             *abort_flag = 0;
             sh->find[0] = p.row_mode ? range : -1;
+            if constexpr (kPaged) sh->find[3] = nh << kHeadsAt;
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -655,14 +752,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 
     pdl_wait();
     pdl_launch_dependents();
-    uint32_t length = 0;  // the loading warp's row's; with few rows, first a lane's row's
-    if (warp == kLoadWarp && lane < p.B) length = row_length(p, lane);
+    const int lines = line_count(p);
+    Line line = {0u, 0u, 0u};  // the loading warp's; with few lines, first a lane's own
+    if (warp == kLoadWarp && lane < lines) line = line_of(p, lane, hblk, kNH);
 
     // ---- this CTA's tiles: [g, g_end) of all rows' tiles, from tile `tile` of row `row` (or whole rows)
     int row = range, tile = 0, n_row = 0, g = 0, g_end = 0;
-    if (!p.row_mode && p.B <= 32) {
+    if (!p.row_mode && lines <= 32) {
         if (warp == kLoadWarp) {  // few rows: a lane a row, beside the others' set-up
-            const int n = lane < p.B ? row_tiles(p, length) : 0;
+            const int n = lane < lines ? row_tiles(p, line) : 0;
             int x = places(n, kChange);
 #pragma unroll 1
             for (int o = 1; o < 32; o <<= 1) {
@@ -678,12 +776,20 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             row = here ? __ffs(here) - 1 : 0;
             tile = g - __shfl_sync(0xffffffffu, pre, row) - kChange;
             n_row = __shfl_sync(0xffffffffu, n, row);
-            length = __shfl_sync(0xffffffffu, length, row);
-            if (lane == 0 && here) sh->find[0] = row;
-            if (hblk == 0 && lane < p.B) tell_row(p, lane, n, pre, g, g_end, per, range, kChange);
+            if (hblk == 0 && lane < lines) tell_row(p, lane, line, n, pre, g, g_end, per, range, kChange);
+            line.length = __shfl_sync(0xffffffffu, line.length, row);
+            if constexpr (kPaged) {
+                line.base = __shfl_sync(0xffffffffu, line.base, row);
+                line.source = __shfl_sync(0xffffffffu, line.source, row);
+            }
+            if (lane == 0 && here) {
+                sh->find[0] = row;
+                if constexpr (kPaged) sh->find[3] = (int)line.source;
+            }
         }
     } else if (!p.row_mode) {
         int total = 0, n_mine = 0, pre_mine = 0, per_cta = 0;
+        Line mine = {0u, 0u, 0u};
         for (int pass = 0; pass < 2; ++pass) {
             int base = 0;
             if (pass == 1) {
@@ -693,9 +799,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 g_end = hi < total ? (int)hi : total;
                 per_cta = per;
             }
-            for (int b0 = 0; b0 < p.B; b0 += kSoftThreads) {
-                if (pass == 0 || p.B > kSoftThreads) {
-                    const int n = tid < kSoftThreads && b0 + tid < p.B ? row_tiles(p, row_length(p, b0 + tid)) : 0;
+            for (int b0 = 0; b0 < lines; b0 += kSoftThreads) {
+                if (pass == 0 || lines > kSoftThreads) {
+                    const bool is = tid < kSoftThreads && b0 + tid < lines;
+                    if (is) mine = line_of(p, b0 + tid, hblk, kNH);
+                    const int n = is ? row_tiles(p, mine) : 0;
                     int x = places(n, kChange);
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
@@ -717,9 +825,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                         sh->find[0] = b0 + tid;
                         sh->find[1] = g - pre_mine - kChange;
                         sh->find[2] = n_mine;
+                        if constexpr (kPaged) sh->find[3] = (int)mine.source;
                     }
-                    if (hblk == 0 && tid < kSoftThreads && b0 + tid < p.B)
-                        tell_row(p, b0 + tid, n_mine, pre_mine, g, g_end, per_cta, range, kChange);
+                    if (hblk == 0 && tid < kSoftThreads && b0 + tid < lines)
+                        tell_row(p, b0 + tid, mine, n_mine, pre_mine, g, g_end, per_cta, range, kChange);
                 }
             }
             if (pass == 0) total = base;
@@ -732,21 +841,52 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 
     if (warp == kLoadWarp) {
         // ---- loads (the warp walks together, lane 0 issues)
-        if (!p.row_mode && p.B > 32) {
-            row = p.B;
+        if (!p.row_mode && lines > 32) {
+            row = lines;
             if (g < g_end) {  // (a range of no tiles has found no row)
                 row = sh->find[0];
                 tile = sh->find[1];
                 n_row = sh->find[2];
-                length = row_length(p, row);
+                line = line_of(p, row, hblk, kNH);
             }
         }
+        // the pages of a tile: a lane has that of its 32, 64 or 128 tokens
+        int box_log2 = 7, boxes = 1;
+        if constexpr (kPaged) {
+            box_log2 = p.page_log2 < 7 ? p.page_log2 : 7;
+            boxes = kTile >> box_log2;
+        }
+        const auto page_at = [&](const Cursor& c, int table_row) {
+            int id = -1;
+            if constexpr (kPaged) {
+                const int64_t slot = (int64_t)(c.token() >> p.page_log2) + lane;
+                if (lane < boxes && slot < p.M) id = p.tables[c.j][table_row * p.M + slot];
+                if (id >= p.P) id = -1;
+            }
+            return id < 0 ? -1 : id;
+        };
         uint32_t t = 0;
         bool ok = true, known = !p.row_mode;
-        while (ok && row < p.B && (p.row_mode || g < g_end)) {
-            if (!known) {
-                length = row_length(p, row);
-                n_row = row_tiles(p, length);
+        while (ok && row < lines && (p.row_mode || g < g_end)) {
+            if (kPaged && !p.row_mode && !known) {  // the next line with tiles: many may have none, so a lane a line
+                uint32_t some = 0;
+                for (; row < lines && !some; row += some ? 0 : 32) {
+                    n_row = 0;
+                    if (row + lane < lines) {
+                        line = line_of(p, row + lane, hblk, kNH);
+                        n_row = row_tiles(p, line);
+                    }
+                    some = __ballot_sync(0xffffffffu, n_row > 0);
+                }
+                if (!some) break;
+                const int at = __ffs(some) - 1;
+                row += at;
+                n_row = __shfl_sync(0xffffffffu, n_row, at);
+                line = {__shfl_sync(0xffffffffu, line.length, at), __shfl_sync(0xffffffffu, line.base, at),
+                        __shfl_sync(0xffffffffu, line.source, at)};
+            } else if (!known) {
+                line = line_of(p, row, hblk, kNH);
+                n_row = row_tiles(p, line);
             }
             known = false;
             if (n_row == 0 && p.row_mode) {  // a row that sees nothing
@@ -762,15 +902,30 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             const int n = p.row_mode || n_row - tile < g_end - g ? n_row - tile : g_end - g;
             if (n > 0) {
                 Cursor c;
-                c.seek(p, length, tile);
-                const uint32_t about = (tile == 0 ? kStarts : 0u) | (tile == 0 && n == n_row ? kWhole : 0u);
+                c.seek(p, line, tile);
+                const bool alone = !kPaged || (line.base == 0 && !(line.source & kPrefix));  // (nothing joins it)
+                const uint32_t about = (tile == 0 ? kStarts : 0u) | (tile == 0 && n == n_row && alone ? kWhole : 0u);
+                const int table_row = line_row(p, row, line.source);
+                int id = page_at(c, table_row);
+                bool fresh = true;
                 for (int i = 0; i < n; ++i, ++t) {
                     const uint32_t st = t & 1, par = ((t >> 1) + 1) & 1;
                     uint8_t* const kv = smem + st * S::kStage;
                     const int tok0 = (int)c.token();
+                    uint32_t what = c.j | about | (i == 0 ? kFirst : 0u) | (i == n - 1 ? kLast : 0u);
+                    int valid = c.valid();
+                    if constexpr (kPaged) {
+                        if (lane < 4) sh->pages[t & 3][lane] = id;
+                        const int lo = lane << box_log2;
+                        const bool seen = id >= 0 && lo < valid && lo + (1 << box_log2) > c.skip();
+                        what |= fresh ? kFresh : 0u;
+                        fresh = fresh && !__any_sync(0xffffffffu, seen);
+                        valid |= c.skip() << 8;
+                        __syncwarp();
+                    }
                     if (lane == 0) {
-                        sh->info[t & 3] = {(uint32_t)tok0, c.valid(),
-                                           c.j | about | (i == 0 ? kFirst : 0u) | (i == n - 1 ? kLast : 0u), row};
+                        sh->info[t & 3] = {(uint32_t)tok0, valid, what, row};
+                        if constexpr (kPaged) sh->source[t & 3] = line.source;
                         mbar_arrive(&sh->info_full[t & 3]);
                     }
                     // (q is needed first: the first tile's loads stand behind it)
@@ -786,14 +941,42 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                             uint64_t* const bar = &sh->kv_full[st][a];
                             mbar_expect_tx(bar, kSlice + (a == 3 ? S::kRopeSlice : 0) +
                                                     (p.stall && t == 0 && a == 0 ? 16 : 0));
-                            tma_load_3d(kv + a * kSlice, &p.tm_latent[c.j], a * 128, tok0, row, bar);
-                            if (S::kHasRope && a == 3)
-                                tma_load_3d(kv + 4 * kSlice, &p.tm_rope[c.j], kDv, tok0, row, bar);
+                            if constexpr (!kPaged) {
+                                tma_load_3d(kv + a * kSlice, &p.tm_latent[c.j], a * 128, tok0, row, bar);
+                                if (S::kHasRope && a == 3)
+                                    tma_load_3d(kv + 4 * kSlice, &p.tm_rope[c.j], kDv, tok0, row, bar);
+                            }
                             sh->armed[st][a] = (int)(t >> 1);
+                        }
+                        if constexpr (kPaged) {  // (a page of none lies outside the map: zeros)
+                            __syncwarp();
+                            if (lane < boxes) {
+                                uint64_t* const bar = &sh->kv_full[st][a];
+                                const int y = tok0 & ((1 << p.page_log2) - 1) & ~(kTile - 1);
+                                tma_load_3d(kv + a * kSlice + (lane << (box_log2 + 7)), &p.tm_latent[c.j], a * 128, y,
+                                            id, bar);
+                                if (S::kHasRope && a == 3)
+                                    tma_load_3d(kv + 4 * kSlice + (lane << (box_log2 + 6)), &p.tm_rope[c.j], kDv, y,
+                                                id, bar);
+                            }
+                            __syncwarp();
                         }
                     }
                     if (!ok) break;
                     c.next(p);
+                    if constexpr (kPaged) {
+                        if (i + 1 < n) {
+                            id = page_at(c, table_row);
+                            if (t >= 1 && lane < boxes && id >= 0) {
+                                const int y = (int)c.token() & ((1 << p.page_log2) - 1) & ~(kTile - 1);
+#pragma unroll 1
+                                for (int a = 0; a < 4; ++a) tma_prefetch_3d(&p.tm_latent[c.j], a * 128, y, id);
+                                if constexpr (S::kHasRope) tma_prefetch_3d(&p.tm_rope[c.j], kDv, y, id);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    if (kPaged) continue;
                     if (i + 1 < n && t >= 1 && lane == 0) {  // the next tile's stage is still in use: to L2 meanwhile
 #pragma unroll 1
                         for (int a = 0; a < 4; ++a) tma_prefetch_3d(&p.tm_latent[c.j], a * 128, (int)c.token(), row);
@@ -882,9 +1065,21 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         // either way), all of a warp's heads (a quarter of its group's) in flight at once.
         constexpr int kPer = kHW / 4;
         const int hq = hb + quad * kPer;
-        auto fetch_q = [&](int row) {
+        auto fetch_q = [&](int v, uint32_t source) {
+            const int row = line_row(p, v, source);
             const uint8_t* const src = p.q + row * p.q_row + (h0 + hq) * p.q_head;
             const uint32_t to = smem_u32(q_s);
+            const int heads = kPaged ? (int)(source >> kHeadsAt) & 127 : nh;
+            // head k of the warp's: of one row, or of a group's rows one behind the other
+            const auto head_at = [&](int k) {
+                if constexpr (kPaged) {
+                    if (source & kPrefix) {
+                        const uint32_t r = ((source & kSetMask) * p.head_blocks + hblk) * kNH + hq + k, m = r / p.H;
+                        return p.q + (int64_t)(row + (int)m) * p.q_row + (int64_t)(r - m * p.H) * p.q_head;
+                    }
+                }
+                return src + k * p.q_head;
+            };
             if (p.q_wide) {
                 constexpr int kC = kDk / 8;  // 16-byte pieces of a head
 #pragma unroll 1
@@ -893,14 +1088,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     const uint32_t dst =
                         j < 64 ? (j >> 4) * S::kQSlice + (hq + k + ((j >> 3) & 1) * kNH) * 128 + (j & 7) * 16
                                : 4 * S::kQSlice + (hq + k + ((j - 64) >> 2) * kNH) * 64 + (j & 3) * 16;
-                    const bool is = hq + k < nh;
-                    copy_16(to + dst, is ? src + k * p.q_head + 16 * j : p.q, is ? 16u : 0u);
+                    const bool is = hq + k < heads;
+                    copy_16(to + dst, is ? head_at(k) + 16 * j : p.q, is ? 16u : 0u);
                 }
             } else {
 #pragma unroll 1
                 for (int k = 0; k < kPer; ++k) {
-                    const bool is = hq + k < nh;
-                    const uint8_t* const from = is ? src + k * p.q_head + 4 * lane : p.q;
+                    const bool is = hq + k < heads;
+                    const uint8_t* const from = is ? head_at(k) + 4 * lane : p.q;
                     const uint32_t dst = to + (hq + k) * 128 + 4 * lane, step = is ? 128u : 0u, bytes = is ? 4u : 0u;
 #pragma unroll 1
                     for (int i = 0; i < 8; ++i)
@@ -973,14 +1168,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         // The next tile's description; a tile of no tokens ends the loop, and so does a wait that gave up in any
         // warp: all warps agree here.
         TileInfo ti = {0u, 0, 0u, 0};
+        uint32_t source = 0;
         auto next_segment = [&](bool good) {
             const bool ok = mbar_wait(&sh->info_full[t & 3], (t >> 2) & 1, abort_flag, p.status, p.wait_ns);
             ti = sh->info[t & 3];
+            if constexpr (kPaged) source = sh->source[t & 3];
             return !soft_any(!(ok && good)) && ti.valid > 0;
         };
         // q of the CTA's first row is asked for at once (with whole rows that row may turn out to see nothing)
         const int asked = sh->find[0];
-        if (asked >= 0) fetch_q(asked);
+        if (asked >= 0) fetch_q(asked, kPaged ? (uint32_t)sh->find[3] : 0u);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->q_asked);
         bool going = next_segment(true);
@@ -988,12 +1185,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             if (ti.row != asked) {
                 asm volatile("cp.async.wait_all;" ::: "memory");
                 __syncwarp();
-                fetch_q(ti.row);
+                fetch_q(ti.row, source);
             }
             aborted = !split_q();
         }
         while (going) {  // segments
-            const int row = ti.row;
+            const int line_now = ti.row, row = line_row(p, ti.row, source);
+            const int heads = kPaged ? (int)(source >> kHeadsAt) & 127 : nh;
             f32x2 l2[kHW / 2];
 #pragma unroll
             for (int h = 0; h < kHW / 2; ++h) l2[h] = 0ull;
@@ -1004,8 +1202,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 ti = sh->info[t & 3];
                 // this thread's token's scale, in flight beside the scores
                 float u = 1.f;
-                const int valid = ti.valid;
-                if (ok) {
+                const int valid = kPaged ? ti.valid & 255 : ti.valid;
+                bool seen = tok < valid;
+                if constexpr (kPaged) {
+                    const int at = tok >> (p.page_log2 < 7 ? p.page_log2 : 7);
+                    const int id = ok ? *(volatile int*)&sh->pages[t & 3][at] : -1;
+                    seen = seen && tok >= (ti.valid >> 8) && id >= 0;
+                    const uint32_t in_page = (ti.token + (uint32_t)tok) & ((1u << p.page_log2) - 1);
+                    if (seen)
+                        u = p.scales[ti.what & 255u][(((int64_t)id << p.page_log2) + in_page) >> p.block_log2];
+                } else if (ok) {
                     const uint32_t loc = ti.token + (uint32_t)(tok < valid ? tok : valid - 1);
                     u = p.scales[ti.what & 255u][(int64_t)row * p.blocks + (loc >> p.block_log2)];
                 }
@@ -1039,7 +1245,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                                 sv[h + 2], sv[h + 3]);
                     }
                 }
-                if (valid < kTile && tok >= valid) {
+                if (kPaged ? !seen : valid < kTile && tok >= valid) {
                     // a token that is not visible may hold anything: probability 0 (2^-kRange, and with a whole
                     // warp of them scale 2^-127), and a value row of zeros (0 x NaN)
 #pragma unroll
@@ -1093,7 +1299,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 // old one a token with a small scale can lie beyond fp32, and after a move by a large scale the sums
                 // before it can still count.
                 bool move = far > kLazy;
-                if (first && quad * 32 < valid) {
+                if (kPaged ? (ti.what & kFresh) && __any_sync(0xffffffffu, seen) : first && quad * 32 < valid) {
 #pragma unroll
                     for (int h = 0; h < kHW; ++h) move |= d[h] < -kLow;
                 }
@@ -1120,7 +1326,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 #pragma unroll 1
                         for (int k = 0; k < 4; ++k) up = max(up, red_i[k * kNH + r]);
                         // (each head by its own scores: none is rounded differently for another's)
-                        up = up > kLazy || (first && up < -kLow) ? up : 0;
+                        up = up > kLazy || ((kPaged ? (ti.what & kFresh) != 0 : first) && up < -kLow) ? up : 0;
                         const int m = m_s[r] + up;
                         // out of range, or NaN: the head's sums become NaN
                         const bool bad = m >= kMagicBits + kRange || m <= kMagicBits - kRange;
@@ -1206,7 +1412,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             // ---- the segment's end. The next one's q comes in meanwhile (this one's scores are all done: q's place
             // is free) and is split before this one's output leaves, so that its first scores run beside that.
             going = next_segment(!aborted);
-            if (going) fetch_q(ti.row);
+            if (going) fetch_q(ti.row, source);
             if (!aborted) {
                 // sums over the warp's tokens: halves of the heads to halves of the lanes until a lane has one head
                 float l[kHW];
@@ -1227,14 +1433,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 if ((lane & (32 / kHW - 1)) == 0) red[quad * kNH + hb + lane / (32 / kHW)] = l[0];
                 aborted = !meet();
                 const bool whole = (about & kWhole) != 0;  // the row's only segment
-                const int64_t slot = (int64_t)blockIdx.x * 2 + ((about & kStarts) ? 1 : 0);
+                int64_t slot = (int64_t)blockIdx.x * 2 + ((about & kStarts) ? 1 : 0);
+                if constexpr (kPaged)  // with groups a CTA can have many lines that begin here and are joined
+                    if (p.groups != nullptr)
+                        slot = (about & kStarts) ? gridDim.x + (int64_t)line_now * p.head_blocks + hblk : blockIdx.x;
                 if (quad == 0 && lane < kHW) {
                     const int r = hb + lane;
                     const float l = (red[r] + red[kNH + r]) + (red[2 * kNH + r] + red[3 * kNH + r]);
-                    a_s[r] = __fdividef(1.0f, l);
+                    a_s[r] = kPaged && l == 0.f ? 0.f : __fdividef(1.0f, l);  // (no visible token has a page)
                     const float lse2 = (float)(m_s[r] - kMagicBits) + log2f(l);
                     if (!whole) p.part_lse[slot * kNH + r] = lse2;
-                    else if (p.lse != nullptr && r < nh) p.lse[(int64_t)row * p.H + h0 + r] = lse2 * p.lse_scale;
+                    else if (p.lse != nullptr && r < heads) p.lse[(int64_t)row * p.H + h0 + r] = lse2 * p.lse_scale;
                 }
                 aborted = !meet() || aborted;
                 float inv[kHW];
@@ -1268,11 +1477,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                             reinterpret_cast<__nv_bfloat16*>(p.out) + ((int64_t)row * p.H + h0 + hb) * kDv + d;
 #pragma unroll
                         for (int h = 0; h < kHW; ++h)
-                            if (hb + h < nh) dst[h * kDv] = __float2bfloat16_rn(o[h] * inv[h]);
+                            if (hb + h < heads) dst[h * kDv] = __float2bfloat16_rn(o[h] * inv[h]);
                     } else {
                         float* const dst = p.part + slot * (kNH * kDv) + hb * kDv + d;
 #pragma unroll
-                        for (int h = 0; h < kHW; ++h) dst[h * kDv] = o[h] * inv[h];
+                        for (int h = 0; h < kHW; ++h)
+                            if (!kPaged || hb + h < heads) dst[h * kDv] = o[h] * inv[h];
                     }
                 }
                 tc_fence_before();
@@ -1304,14 +1514,20 @@ struct JoinParams {
     int H, head_blocks, block_heads;
     float lse_scale;
 };
+struct PagedJoinParams : JoinParams {
+    const int* lead;     // [B], or NULL: no groups
+    int B, ctas;
+};
 
 // One warp per (row, head), eight of them a CTA; or a CTA of kWarps warps, where there are few rows and many segments
 // of each (its 1024 CTAs for 8 rows x 128 heads are resident at once with four warps, not with eight). The segments'
 // outputs are weighted by 2^(lse - max), and the row's LSE comes of the same weights. Rows with one segment have been
 // written; rows without a tile get zeros. Bound by the partials' way from L2, so a warp asks for two segments at once,
 // together with the LSEs: two round trips, the first for what the row has.
-template <int kWarps>
-__global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 256) join_kernel(const __grid_constant__ JoinParams p) {
+// Rows with a prefix have its segments first, those of the group's set of heads that has this head, then their own.
+template <int kWarps, class Q>
+__global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 256) join_kernel(const __grid_constant__ Q p) {
+    constexpr bool kPaged = sizeof(Q) > sizeof(JoinParams);
     __shared__ float acc_s[kWarps > 1 ? kWarps : 1][kDv];
     __shared__ float sum_s[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1321,10 +1537,29 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 256) join_kernel(co
     pdl_wait();
     pdl_launch_dependents();
     if (unit >= p.units) return;
-    const int2 row = p.row_info[b];
-    if (row.y == 1) return;
+    int2 row, pre = {0, 0};
+    int pre_line = 0, pre_block = 0, pre_head = 0;
+    bool grouped = false;
+    if constexpr (kPaged) {
+        grouped = p.lead != nullptr;
+        row = p.row_info[grouped ? p.B + b : b];
+        const int lead = grouped ? p.lead[b] : -1;
+        if (lead < 0) {
+            if (row.y == 1) return;
+        } else {
+            const int r = (b - lead) * p.H + h, chunk = r / p.block_heads;
+            pre_head = r - chunk * p.block_heads;
+            pre_line = lead + chunk / p.head_blocks;
+            pre_block = chunk % p.head_blocks;
+            pre = p.row_info[pre_line];
+        }
+    } else {
+        row = p.row_info[b];
+        if (row.y == 1) return;
+    }
+    const int n = pre.y + row.y;
     uint4* const out = reinterpret_cast<uint4*>(p.out + unit * (kDv * 2));
-    if (row.y == 0) {
+    if (n == 0) {
         if (w == 0) {
             out[lane] = make_uint4(0u, 0u, 0u, 0u);
             out[32 + lane] = make_uint4(0u, 0u, 0u, 0u);
@@ -1334,6 +1569,16 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 256) join_kernel(co
     }
     // segment i of the row: the first one is its CTA's last, the others are their CTAs' first
     const auto place = [&](int i) {
+        if constexpr (kPaged) {
+            if (grouped) {
+                const bool common = i < pre.y;
+                const int at = common ? i : i - pre.y, line = common ? pre_line : p.B + b;
+                const int block = common ? pre_block : hblk, first = common ? pre.x : row.x;
+                const int64_t slot = at == 0 ? p.ctas + (int64_t)line * p.head_blocks + block
+                                             : (int64_t)(first + at) * p.head_blocks + block;
+                return slot * p.block_heads + (common ? pre_head : hh);
+            }
+        }
         return (((int64_t)(row.x + i) * p.head_blocks + hblk) * 2 + (i == 0 ? 1 : 0)) * p.block_heads + hh;
     };
     float acc[16], sum = 0.f, m = -INFINITY;
@@ -1344,9 +1589,9 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 256) join_kernel(co
 #pragma unroll
         for (int k = 0; k < 4; ++k) to[k] = src[k * 32 + lane];
     };
-    if (w < row.y) load(w, x[0]);
-    if (w + kWarps < row.y) load(w + kWarps, x[1]);
-    for (int i = lane; i < row.y; i += 32) {
+    if (w < n) load(w, x[0]);
+    if (w + kWarps < n) load(w + kWarps, x[1]);
+    for (int i = lane; i < n; i += 32) {
         const float l = p.part_lse[place(i)];
         nan |= isnan(l);
         m = fmaxf(m, l);
@@ -1354,14 +1599,16 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 256) join_kernel(co
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (__any_sync(0xffffffffu, nan)) m = __uint_as_float(0x7fffffffu);
+    const bool none = kPaged && m == -INFINITY;  // (no visible token has a page)
+    if (none) m = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.f;
 #pragma unroll 1
-    for (int i0 = w; i0 < row.y; i0 += 2 * kWarps) {
+    for (int i0 = w; i0 < n; i0 += 2 * kWarps) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int i = i0 + u * kWarps;
-            if (i >= row.y) break;
+            if (i >= n) break;
             const float f = ex2(p.part_lse[place(i)] - m);
             sum += f;
 #pragma unroll
@@ -1371,7 +1618,7 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 256) join_kernel(co
                 acc[4 * k + 2] = fmaf(f, x[u][k].z, acc[4 * k + 2]);
                 acc[4 * k + 3] = fmaf(f, x[u][k].w, acc[4 * k + 3]);
             }
-            if (i + 2 * kWarps < row.y) load(i + 2 * kWarps, x[u]);
+            if (i + 2 * kWarps < n) load(i + 2 * kWarps, x[u]);
         }
     }
     if constexpr (kWarps > 1) {
@@ -1398,7 +1645,7 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 256) join_kernel(co
         acc[2] = a.z;
         acc[3] = a.w;
     }
-    const float inv = 1.0f / sum;
+    const float inv = none ? 0.f : 1.0f / sum;
 #pragma unroll
     for (int i = 0; i < (kWarps > 1 ? 1 : 4); ++i) {
         uint2 v;
@@ -1430,14 +1677,15 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     return fn;
 }
 
-// A [B, T, Dk] byte cache read in boxes of `width` dims x 128 tokens; tokens past T read as 0.
-bool encode_cache(CUtensorMap* tm, const void* base, int Dk, int64_t T, int64_t B, uint32_t width,
+// A [B, T, Dk] byte cache (a pool: [P, page, Dk]) read in boxes of `width` dims x `tokens` tokens; tokens past T, and
+// rows outside [0, B), read as 0.
+bool encode_cache(CUtensorMap* tm, const void* base, int Dk, int64_t T, int64_t B, uint32_t width, int tokens,
                   CUtensorMapSwizzle swizzle) {
     const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (enc == nullptr) return false;
     cuuint64_t dim[3] = {(cuuint64_t)Dk, (cuuint64_t)T, (cuuint64_t)B};
     cuuint64_t stride[2] = {(cuuint64_t)Dk, (cuuint64_t)Dk * (cuuint64_t)T};
-    cuuint32_t box[3] = {width, (cuuint32_t)kTile, 1u};
+    cuuint32_t box[3] = {width, (cuuint32_t)tokens, 1u};
     cuuint32_t step[3] = {1u, 1u, 1u};
     return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dim, stride, box, step,
                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1450,8 +1698,8 @@ bool encode_cache(CUtensorMap* tm, const void* base, int Dk, int64_t T, int64_t 
 int head_block(int H) { return H <= 16 ? 16 : (H <= 32 ? 32 : 64); }
 
 // CTAs of a call: one per multiprocessor, shared out between the head blocks.
-int grid_ranges(int H, int num_sms) {
-    const int blocks = (H + head_block(H) - 1) / head_block(H);
+int grid_ranges(int H, int heads, int num_sms) {
+    const int blocks = (H + heads - 1) / heads;
     const int r = num_sms / blocks;
     return r < 1 ? 1 : r;
 }
@@ -1459,16 +1707,18 @@ int grid_ranges(int H, int num_sms) {
 int64_t round_up(int64_t x) { return (x + 255) / 256 * 256; }
 
 struct Workspace {
-    int64_t part, part_lse, row_info, bytes;
+    int64_t part, part_lse, row_info, lead, bytes;
 };
-Workspace workspace_of(int64_t B, int H, int num_sms) {
-    const int nh = head_block(H);
-    const int64_t ctas = (int64_t)grid_ranges(H, num_sms) * ((H + nh - 1) / nh);
+// heads: of a block, from head_block(). With groups each line that begins somewhere has a place, besides those that go on.
+Workspace workspace_of(int64_t B, int H, int heads, bool grouped, int num_sms) {
+    const int64_t blocks = (H + heads - 1) / heads, ctas = grid_ranges(H, heads, num_sms) * blocks;
+    const int64_t slots = grouped ? ctas + 2 * B * blocks : 2 * ctas;
     Workspace w;
     w.part = 0;
-    w.part_lse = w.part + round_up(2 * ctas * nh * kDv * 4);
-    w.row_info = w.part_lse + round_up(2 * ctas * nh * 4);
-    w.bytes = w.row_info + round_up(B * 8);
+    w.part_lse = w.part + round_up(slots * heads * kDv * 4);
+    w.row_info = w.part_lse + round_up(slots * heads * 4);
+    w.lead = w.row_info + round_up((grouped ? 2 : 1) * B * 8);
+    w.bytes = w.lead + (grouped ? round_up(B * 4) : 0);
     return w;
 }
 
@@ -1487,15 +1737,15 @@ int multiprocessors() {
     return n;
 }
 
-template <int kDk, int kNH, int kShards>
-cudaError_t launch_decode(const DecodeParams<kShards>& p, unsigned flags, cudaStream_t st) {
+template <int kDk, int kNH, class P>
+cudaError_t launch_decode(const P& p, unsigned flags, cudaStream_t st) {
     constexpr int bytes = Shape<kDk, kNH>::kSmem;
     static int configured[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE)) {
-        e = cudaFuncSetAttribute(decode_kernel<kDk, kNH, kShards>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        e = cudaFuncSetAttribute(decode_kernel<kDk, kNH, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
     }
@@ -1509,7 +1759,7 @@ cudaError_t launch_decode(const DecodeParams<kShards>& p, unsigned flags, cudaSt
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = (flags & DCP_FLAG_PDL) ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, decode_kernel<kDk, kNH, kShards>, p);
+    e = cudaLaunchKernelEx(&cfg, decode_kernel<kDk, kNH, P>, p);
     if (e != cudaSuccess || p.row_mode) return e;
     // the join overlaps its launch with the decode's tail and waits for it on the device
     const int64_t units = (int64_t)p.B * p.H;
@@ -1522,33 +1772,70 @@ cudaError_t launch_decode(const DecodeParams<kShards>& p, unsigned flags, cudaSt
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
     const JoinParams j = {p.part, p.part_lse, p.row_info, p.out, p.lse, units, p.H, p.head_blocks, kNH, p.lse_scale};
-    return few ? cudaLaunchKernelEx(&cfg, join_kernel<4>, j) : cudaLaunchKernelEx(&cfg, join_kernel<1>, j);
+    if constexpr (P::kPaged) {
+        const PagedJoinParams pj = {j, p.groups != nullptr ? p.lead : nullptr, p.B, p.ranges * p.head_blocks};
+        return few ? cudaLaunchKernelEx(&cfg, join_kernel<4, PagedJoinParams>, pj)
+                   : cudaLaunchKernelEx(&cfg, join_kernel<1, PagedJoinParams>, pj);
+    } else {
+        return few ? cudaLaunchKernelEx(&cfg, join_kernel<4, JoinParams>, j)
+                   : cudaLaunchKernelEx(&cfg, join_kernel<1, JoinParams>, j);
+    }
 }
 
-// Encode the shards' tensor maps and launch. Returns the call's status.
-template <int kShards>
-int run_decode(const DecodeBase& base, const void* const* kv, const float* const* scales, int Dk, unsigned flags,
-               cudaStream_t st) {
-    DecodeParams<kShards> p;
+template <class P>
+cudaError_t launch_heads(const P& p, int Dk, int heads, unsigned flags, cudaStream_t st) {
+    if (Dk > kDv)
+        return heads == 16 ? launch_decode<576, 16>(p, flags, st)
+                           : (heads == 32 ? launch_decode<576, 32>(p, flags, st) : launch_decode<576, 64>(p, flags, st));
+    return heads == 16 ? launch_decode<512, 16>(p, flags, st)
+                       : (heads == 32 ? launch_decode<512, 32>(p, flags, st) : launch_decode<512, 64>(p, flags, st));
+}
+
+// Encode the shards' tensor maps (of caches of `rows` rows of `tokens` tokens, in boxes of `box`) and launch. Returns the
+// call's status.
+template <int kShards, class P>
+int run_decode(P& p, const DecodeBase& base, const void* const* kv, const float* const* scales, int64_t rows,
+               int64_t tokens, int box, int Dk, int heads, unsigned flags, cudaStream_t st) {
     static_cast<DecodeBase&>(p) = base;
     for (uint32_t j = 0; j < (uint32_t)kShards; ++j) {
         p.scales[j] = j < base.cp ? scales[j] : nullptr;
         if (!((base.held >> j) & 1u)) continue;
-        if (!encode_cache(&p.tm_latent[j], kv[j], Dk, base.T, base.B, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-            (Dk > kDv && !encode_cache(&p.tm_rope[j], kv[j], Dk, base.T, base.B, 64, CU_TENSOR_MAP_SWIZZLE_64B)))
+        if (!encode_cache(&p.tm_latent[j], kv[j], Dk, tokens, rows, 128, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            (Dk > kDv && !encode_cache(&p.tm_rope[j], kv[j], Dk, tokens, rows, 64, box, CU_TENSOR_MAP_SWIZZLE_64B)))
             return DCP_MLA_CACHE8_ERR_TENSOR_MAP;
     }
-    const int nh = head_block(base.H);
-    cudaError_t e;
-    if (Dk > kDv) {
-        e = nh == 16 ? launch_decode<576, 16>(p, flags, st)
-                     : (nh == 32 ? launch_decode<576, 32>(p, flags, st) : launch_decode<576, 64>(p, flags, st));
-    } else {
-        e = nh == 16 ? launch_decode<512, 16>(p, flags, st)
-                     : (nh == 32 ? launch_decode<512, 32>(p, flags, st) : launch_decode<512, 64>(p, flags, st));
-    }
+    const cudaError_t e = launch_heads(p, Dk, heads, flags, st);
     if (e != cudaSuccess) (void)cudaGetLastError();
     return (int)e;
+}
+template <int kShards>
+int run_rows(const DecodeBase& base, const void* const* kv, const float* const* scales, int Dk, int heads,
+             unsigned flags, cudaStream_t st) {
+    DecodeParams<kShards> p;
+    return run_decode<kShards>(p, base, kv, scales, base.B, base.T, kTile, Dk, heads, flags, st);
+}
+
+// What a paged call has besides.
+struct Pages {
+    const int32_t* const* tables;
+    int64_t P, M;
+    int page, page_log2;
+    const int32_t *groups, *shared;
+    int32_t* lead;
+};
+template <int kShards>
+int run_paged(const DecodeBase& base, const Pages& pages, const void* const* kv, const float* const* scales, int Dk,
+              int heads, unsigned flags, cudaStream_t st) {
+    PagedParams<kShards> p;
+    for (uint32_t j = 0; j < (uint32_t)kShards; ++j) p.tables[j] = j < base.cp ? pages.tables[j] : nullptr;
+    p.groups = reinterpret_cast<const int2*>(pages.groups);
+    p.shared = pages.shared;
+    p.lead = pages.lead;
+    p.M = pages.M;
+    p.P = (int)pages.P;
+    p.page_log2 = pages.page_log2;
+    return run_decode<kShards>(p, base, kv, scales, pages.P, pages.page, pages.page < kTile ? pages.page : kTile, Dk,
+                               heads, flags, st);
 }
 
 // Rows of at most two tiles are not worth splitting: a join costs as much. (128 heads x 256 tokens: 12.6 us whole, 15.3
@@ -1562,6 +1849,19 @@ bool whole_rows(int cp, int64_t T, int64_t window, int64_t sinks) {
     return cp * most <= 2;
 }
 
+int page_log2_of(int page) {
+    for (int k = 0; (1 << k) <= DCP_MLA_PAGE_MAX; ++k)
+        if (page == 1 << k) return (1 << k) >= DCP_MLA_PAGE_MIN ? k : -1;
+    return -1;
+}
+
+// Groups are of use where a row's heads leave room in a block of 64: then several rows' heads fill it, and a prefix's
+// tile is multiplied for all of them at once. (A multiple of 64 heads fills its blocks alone: every block takes the
+// prefix's tiles for itself either way, and finds them in L2 without groups too.) They cost a place for partial results
+// per row, so that there is a limit.
+bool uses_groups(bool grouped, int64_t B, int H) { return grouped && B >= 2 && B <= 2048 && H % 64 != 0; }
+int group_block(int64_t B, int H) { return head_block(B * H < 64 ? (int)(B * H) : 64); }
+
 }  // namespace
 
 extern "C" int64_t dcp_mla_cache8_decode_workspace_bytes(int cp, int64_t B, int H, int64_t T, int64_t window,
@@ -1569,15 +1869,25 @@ extern "C" int64_t dcp_mla_cache8_decode_workspace_bytes(int cp, int64_t B, int 
     if (cp < 1 || cp > kCpMax || B < 0 || B > 65535 || H < 1 || H > 1024 || T < 0 || T > 0x7fffffff || window < 0 ||
         sinks < 0 || num_sms < 1 || num_sms > 4096)
         return -1;
-    return B == 0 || whole_rows(cp, T, window, sinks) ? 0 : workspace_of(B, H, num_sms).bytes;
+    return B == 0 || whole_rows(cp, T, window, sinks) ? 0 : workspace_of(B, H, head_block(H), false, num_sms).bytes;
 }
 
-extern "C" int dcp_mla_cache8_decode(const void* q, int64_t q_row, int64_t q_head, const void* const* kv_ptrs,
-                                     const float* const* scale_ptrs, const int32_t* seq_lens, int cp, int64_t B,
-                                     int H, int Dk, int Dv, int64_t T, int block, int interleave, int64_t window,
-                                     int64_t sinks, float scale, int lse_base_e, void* workspace,
-                                     int64_t workspace_bytes, void* out, float* lse, int32_t* status, unsigned flags,
-                                     void* stream) {
+extern "C" int64_t dcp_mla_cache8_decode_paged_workspace_bytes(int cp, int64_t B, int H, int page, int64_t M,
+                                                               int64_t window, int64_t sinks, int grouped,
+                                                               int num_sms) {
+    if (page_log2_of(page) < 0 || M < 1 || M > 0x7fffffff || M * page > 0x7fffffff) return -1;
+    const int64_t bytes = dcp_mla_cache8_decode_workspace_bytes(cp, B, H, M * page, window, sinks, num_sms);
+    return bytes < 0 || B == 0 || !uses_groups(grouped != 0, B, H)
+               ? bytes
+               : workspace_of(B, H, group_block(B, H), true, num_sms).bytes;
+}
+
+// Both forms. T: what a row has room for; pages: NULL for rows one after the other.
+static int decode_call(const void* q, int64_t q_row, int64_t q_head, const void* const* kv_ptrs,
+                       const float* const* scale_ptrs, Pages* pages, const int32_t* seq_lens, int cp, int64_t B, int H,
+                       int Dk, int Dv, int64_t T, int block, int interleave, int64_t window, int64_t sinks, float scale,
+                       int lse_base_e, void* workspace, int64_t workspace_bytes, void* out, float* lse, int32_t* status,
+                       unsigned flags, void* stream) {
     if (B < 0 || B > 65535 || H < 1 || H > 1024 || (Dk != 512 && Dk != 576) || Dv != kDv || T < 0 || T > 0x7fffffff)
         return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
     int lg = -1;
@@ -1600,25 +1910,29 @@ extern "C" int dcp_mla_cache8_decode(const void* q, int64_t q_row, int64_t q_hea
         if ((kv_ptrs[j] == nullptr) != (scale_ptrs[j] == nullptr)) return DCP_MLA_CACHE8_ERR_NULL_POINTER;
         if (!aligned(kv_ptrs[j], 16) || !aligned(scale_ptrs[j], 4)) return DCP_MLA_CACHE8_ERR_MISALIGNED;
         if (kv_ptrs[j] != nullptr) {
+            if (pages != nullptr && B > 0 && pages->tables[j] == nullptr) return DCP_MLA_CACHE8_ERR_NULL_POINTER;
+            if (pages != nullptr && !aligned(pages->tables[j], 4)) return DCP_MLA_CACHE8_ERR_MISALIGNED;
             p.held |= 1u << j;
             some = j;
         }
     }
     if (some < 0) return DCP_MLA_CACHE8_ERR_NULL_POINTER;
     // every tile count stays in 32 bits
+    const bool grouped = pages != nullptr && uses_groups(pages->groups != nullptr, B, H);
     const int64_t shard_tiles = T / kTile + 2;
-    if (B * cp * shard_tiles > 0x40000000) return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
+    if (B * cp * shard_tiles * (grouped ? 2 : 1) > 0x40000000) return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
     if (B == 0) return 0;
     const int sms = multiprocessors();
     if (sms < 1) {
         (void)cudaGetLastError();
         return DCP_ERR_DEVICE;
     }
-    const Workspace ws = workspace_of(B, H, sms);
-    p.row_mode = whole_rows(cp, T, window, sinks) ? 1 : 0;
+    const int heads = grouped ? group_block(B, H) : head_block(H);
+    const Workspace ws = workspace_of(B, H, heads, grouped, sms);
+    p.row_mode = !grouped && whole_rows(cp, T, window, sinks) ? 1 : 0;
     if (!p.row_mode && (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < ws.bytes))
         return DCP_MLA_CACHE8_ERR_WORKSPACE;
-    if (T == 0) p.held = 0;  // nothing is cached: every row is empty
+    if (T == 0 || (pages != nullptr && pages->P == 0)) p.held = 0;  // nothing is cached: every row is empty
     uint8_t* const w = static_cast<uint8_t*>(workspace);
     p.q = static_cast<const uint8_t*>(q);
     p.q_row = q_row * 2;
@@ -1640,15 +1954,53 @@ extern "C" int dcp_mla_cache8_decode(const void* q, int64_t q_row, int64_t q_hea
     p.block_log2 = lg;
     p.B = (int)B;
     p.H = H;
-    p.head_blocks = (H + head_block(H) - 1) / head_block(H);
-    p.ranges = grid_ranges(H, sms);
+    p.head_blocks = (H + heads - 1) / heads;
+    p.ranges = grid_ranges(H, heads, sms);
     p.scale_log2 = scale * 1.4426950408889634f;
     p.lse_scale = lse_base_e ? 0.6931471805599453f : 1.0f;
     p.stall = (flags & DCP_MLA_FLAG_TEST_STALL) ? 1 : 0;
     p.wait_ns = p.stall ? kTestWaitLimitNs : kWaitLimitNs;
     if (p.row_mode && p.ranges > B) p.ranges = (int)B;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (cp == 1) return run_decode<1>(p, kv_ptrs, scale_ptrs, Dk, flags, st);
-    if (cp <= 4) return run_decode<4>(p, kv_ptrs, scale_ptrs, Dk, flags, st);
-    return run_decode<kCpMax>(p, kv_ptrs, scale_ptrs, Dk, flags, st);
+    if (pages != nullptr) {
+        if (grouped) pages->lead = reinterpret_cast<int32_t*>(w + ws.lead);
+        else pages->groups = nullptr;
+        return cp == 1 ? run_paged<1>(p, *pages, kv_ptrs, scale_ptrs, Dk, heads, flags, st)
+                       : run_paged<kCpMax>(p, *pages, kv_ptrs, scale_ptrs, Dk, heads, flags, st);
+    }
+    if (cp == 1) return run_rows<1>(p, kv_ptrs, scale_ptrs, Dk, heads, flags, st);
+    if (cp <= 4) return run_rows<4>(p, kv_ptrs, scale_ptrs, Dk, heads, flags, st);
+    return run_rows<kCpMax>(p, kv_ptrs, scale_ptrs, Dk, heads, flags, st);
+}
+
+extern "C" int dcp_mla_cache8_decode(const void* q, int64_t q_row, int64_t q_head, const void* const* kv_ptrs,
+                                     const float* const* scale_ptrs, const int32_t* seq_lens, int cp, int64_t B,
+                                     int H, int Dk, int Dv, int64_t T, int block, int interleave, int64_t window,
+                                     int64_t sinks, float scale, int lse_base_e, void* workspace,
+                                     int64_t workspace_bytes, void* out, float* lse, int32_t* status, unsigned flags,
+                                     void* stream) {
+    return decode_call(q, q_row, q_head, kv_ptrs, scale_ptrs, nullptr, seq_lens, cp, B, H, Dk, Dv, T, block, interleave,
+                       window, sinks, scale, lse_base_e, workspace, workspace_bytes, out, lse, status, flags, stream);
+}
+
+extern "C" int dcp_mla_cache8_decode_paged(const void* q, int64_t q_row, int64_t q_head, const void* const* kv_ptrs,
+                                           const float* const* scale_ptrs, const int32_t* const* table_ptrs,
+                                           const int32_t* seq_lens, const int32_t* groups, const int32_t* shared,
+                                           int cp, int64_t B, int H, int Dk, int Dv, int64_t P, int page, int64_t M,
+                                           int block, int interleave, int64_t window, int64_t sinks, float scale,
+                                           int lse_base_e, void* workspace, int64_t workspace_bytes, void* out,
+                                           float* lse, int32_t* status, unsigned flags, void* stream) {
+    Pages pages = {table_ptrs, P, M, page, page_log2_of(page), groups, shared, nullptr};
+    if (P < 0 || P > 0x7fffffff || M < 1 || M > 0x7fffffff || B < 0 || B > 65535 || B * M > 0x7fffffff)
+        return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
+    if (block < 1 || block > DCP_MLA_CACHE8_BLOCK_MAX || (block & (block - 1)) != 0)
+        return DCP_MLA_CACHE8_ERR_BAD_BLOCK;
+    if (pages.page_log2 < 0 || page % block != 0) return DCP_MLA_CACHE8_ERR_BAD_PAGE;
+    if (M * page > 0x7fffffff) return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
+    if (table_ptrs == nullptr || (groups == nullptr) != (shared == nullptr)) return DCP_MLA_CACHE8_ERR_NULL_POINTER;
+    if (!aligned(groups, 8) || !aligned(shared, 4)) return DCP_MLA_CACHE8_ERR_MISALIGNED;
+    if (groups != nullptr && window > 0) return DCP_MLA_CACHE8_ERR_BAD_WINDOW;
+    return decode_call(q, q_row, q_head, kv_ptrs, scale_ptrs, &pages, seq_lens, cp, B, H, Dk, Dv, M * page, block,
+                       interleave, window, sinks, scale, lse_base_e, workspace, workspace_bytes, out, lse, status,
+                       flags, stream);
 }

@@ -118,6 +118,39 @@ int dcp_mla_cache8_read_paged(const void* const* kv_ptrs, const float* const* sc
                               int Dk, int block, int interleave, const int32_t* starts, const int32_t* cu, int64_t N,
                               void* out, int64_t out_row, int dtype, void* stream);
 
+/*
+ * dcp_mla_cache8_decode over pages: the same call and numerics, with the tokens'
+ * places as above. A visible position without a page is not attended to (it counts in
+ * the length); a row that sees no token gives out = 0 and lse = -inf.
+ *
+ * Rows that share a prefix. groups (or NULL) and shared say that consecutive rows
+ * have their first positions in the same pages: row b belongs to the groups[b][1]
+ * rows from row groups[b][0] on, and positions p < shared[b] of all of them are those
+ * of row groups[b][0], whose table alone is used for them. Every row of a group has
+ * the same entries in groups and shared. A row whose length is below shared takes no
+ * part and is looked up in its own table. The result is that of the call without
+ * groups (but for the order of sums); what is saved is work: tiles of the prefix are
+ * multiplied with several rows' heads at a time where a row's heads do not fill the
+ * kernel's blocks of 64. With H a multiple of 64, or more than 2048 rows, groups make
+ * no difference. Groups do not go together with a window.
+ *   groups   [B, 2] int32, 8-byte aligned; shared [B] int32 (below 1: nothing is
+ *            shared). Entries that break these rules give undefined results in the
+ *            rows concerned.
+ *   workspace at least dcp_mla_cache8_decode_paged_workspace_bytes(...) bytes
+ *   shapes   as for both
+ */
+int dcp_mla_cache8_decode_paged(const void* q, int64_t q_row, int64_t q_head, const void* const* kv_ptrs,
+                                const float* const* scale_ptrs, const int32_t* const* table_ptrs,
+                                const int32_t* seq_lens, const int32_t* groups, const int32_t* shared, int cp,
+                                int64_t B, int H, int Dk, int Dv, int64_t P, int page, int64_t M, int block,
+                                int interleave, int64_t window, int64_t sinks, float scale, int lse_base_e,
+                                void* workspace, int64_t workspace_bytes, void* out, float* lse, int32_t* status,
+                                unsigned flags, void* stream);
+
+/* Bytes of workspace for it, `grouped` with groups; 0 for none, -1 for sizes out of range. Host only. */
+int64_t dcp_mla_cache8_decode_paged_workspace_bytes(int cp, int64_t B, int H, int page, int64_t M, int64_t window,
+                                                    int64_t sinks, int grouped, int num_sms);
+
 #ifdef __cplusplus
 }
 #endif

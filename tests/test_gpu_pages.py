@@ -9,6 +9,7 @@ torch = pytest.importorskip("torch")
 import decode_context_mla_dcp_gb300 as dcp
 from oracle import cache8
 from oracle import pages as ref
+from .test_gpu_cache8 import check_decode
 
 pytestmark = pytest.mark.gpu
 
@@ -357,3 +358,438 @@ def test_pages_past_32_bits():
     assert ((got - x).abs() <= torch.clamp(2.0 ** -4 * x.abs(), min=2.0 ** -10)).all()
     touched = kv[0].view(P, -1).any(1).nonzero()[:, 0].tolist()
     assert touched == [3, 116509, P - 2, P - 1]
+
+
+# ---- attention over pages ----------------------------------------------------------------
+# The tolerances are those of test_gpu_cache8.py (derived there): the kernel is the same one, and how a row is cut into
+# segments, and whether some of them are of a prefix, changes the order of fp32 sums only.
+
+SCALE = 192 ** -0.5
+
+
+def make_pool(g, P, page, dk, block):
+    x = randn(g, P, page, dk) * torch.exp(0.4 * randn(g, P, page, 1))
+    s = torch.exp2(torch.randint(-8, -6, (P, page // block), generator=g, device=DEV).float())
+    s = s * (1 + 0.5 * torch.rand((P, page // block), generator=g, device=DEV))  # not only powers of two
+    return (x / s.repeat_interleave(block, 1)[..., None]).clamp(-448, 448).to(torch.float8_e4m3fn), s
+
+
+def check_paged(q, kv, sc, tb, lens, cp, il, block, window, sinks, out, lse, base_e=True, held=None, rows=None,
+                scale=SCALE):
+    """Each row's visible tokens that have a page, one after the other, as a cache of one row and one shard."""
+    P, page, dk = next(c.shape for c in kv if c is not None)
+    for b in (range(q.shape[0]) if rows is None else rows):
+        toks = []
+        for p in cache8.visible(max(int(lens[b]), 0), window, sinks):
+            j, t = cache8.place(p, cp, il)
+            if (held is None or j in held) and t < tb[j].shape[1] * page:
+                toks.append((j, t))
+        codes, us = torch.zeros((0, dk), device=DEV), torch.zeros((0,), device=DEV)
+        if toks:
+            j, t = torch.tensor(toks, device=DEV).T
+            parts, scales = [], []
+            for k in range(cp):
+                at = t[j == k]
+                if not len(at):
+                    continue
+                e = tb[k][b, at // page].long()
+                ok = (e >= 0) & (e < P)
+                parts.append(kv[k][e[ok], at[ok] % page].float())
+                scales.append(sc[k][e[ok], at[ok] % page // block])
+            codes, us = torch.cat(parts), torch.cat(scales)
+        n = codes.shape[0]
+        check_decode(q[b:b + 1], [codes[None]], [us[None]], [n], scale, 1, 1, 1, 0, 0, out[b:b + 1], lse[b:b + 1],
+                     base_e)
+
+
+DECODES = [
+    # H, dk, cp, interleave, block, page, M, lengths, window, sinks
+    (16, 576, 1, 1, 1, 32, 1, [1, 0, 32], 0, 0),
+    (16, 576, 1, 1, 1, 32, 7, [0, 1, 31, 32, 33, 127, 128, 129, 199, 224], 0, 0),
+    (64, 576, 1, 1, 1, 64, 5, [0, 1, 127, 128, 129, 256, 257, 300], 0, 0),
+    (32, 576, 1, 1, 16, 64, 5, [0, 5, 128, 299], 0, 0),
+    (128, 576, 1, 1, 64, 128, 9, [1030, 0, 999, 64], 0, 0),
+    (128, 512, 1, 1, 1, 256, 3, [700, 3, 513], 0, 0),
+    (16, 512, 1, 1, 128, 1024, 1, [700, 3, 513], 0, 0),
+    (32, 512, 2, 1, 4, 64, 5, [600, 3, 513], 0, 0),
+    (8, 576, 2, 16, 16, 64, 3, [259, 100, 16, 17], 0, 0),
+    (24, 576, 4, 1, 1, 32, 3, [360, 1, 2, 3, 0], 0, 0),
+    (65, 576, 3, 7, 8, 64, 5, [700, 41], 0, 0),
+    (48, 576, 16, 1, 2, 32, 2, [640, 7, 600], 0, 0),
+    (64, 576, 1, 1, 1, 64, 8, [500, 130, 129, 100, 0], 128, 0),
+    (64, 576, 1, 1, 1, 32, 30, [900, 600, 40], 300, 4),
+    (16, 576, 1, 1, 16, 128, 8, [900, 600, 404, 403], 400, 3),
+    (128, 576, 2, 1, 1, 64, 8, [1000, 700, 9], 333, 8),
+    (32, 576, 4, 16, 32, 32, 10, [1200, 900, 77, 0], 100, 130),
+    (64, 512, 1, 1, 1, 64, 11, [700, 640], 1, 0),
+    (64, 576, 1, 1, 1, 64, 11, [700, 640], 5, 1000),
+    (64, 576, 1, 1, 1, 512, 2, [900, 640], 130, 131),
+    (16, 576, 1, 1, 1, 64, 8, [10000, -5, 499], 0, 0),  # beyond the table, negative
+]
+
+
+@pytest.mark.parametrize("case", DECODES, ids=lambda c: f"H{c[0]}d{c[1]}cp{c[2]}i{c[3]}b{c[4]}p{c[5]}M{c[6]}w{c[8]}s{c[9]}")
+def test_paged_decode(case):
+    H, dk, cp, il, block, page, M, lengths, window, sinks = case
+    g = torch.Generator(device=DEV)
+    g.manual_seed(H + M + window)
+    B = len(lengths)
+    P = B * M + 2
+    kv, sc = map(list, zip(*[make_pool(g, P, page, dk, block) for _ in range(cp)]))
+    tb = [torch.randperm(P, generator=g, device=DEV)[:B * M].view(B, M).int() for _ in range(cp)]
+    q = randn(g, B, H, dk).bfloat16()
+    lens = ints(lengths)
+    # what no row sees may hold anything: NaN codes, NaN scales where a whole block is unseen, entries that are no page
+    for j in range(cp):
+        seen = torch.zeros((P, page), dtype=torch.bool, device=DEV)
+        for b, n in enumerate(lengths):
+            for p in cache8.visible(max(n, 0), window, sinks):
+                k, t = cache8.place(p, cp, il)
+                if k == j and t < M * page:
+                    seen[int(tb[j][b, t // page]), t % page] = True
+        kv[j].view(torch.uint8)[~seen] = 0x7F
+        sc[j][~seen.view(P, -1, block).any(2)] = float("nan")
+        used = seen.any(1)[tb[j].long()]
+        tb[j] = torch.where(used, tb[j], torch.randint(-2, 2, (B, M), generator=g, device=DEV).int() * (1 << 29))
+    kw = dict(block=block, interleave=il, window=window, sinks=sinks, lse_base_e=H % 3 != 0)
+    status = torch.zeros((1,), dtype=torch.int32, device=DEV)
+    out, lse = dcp.mla_cache8_decode(q, kv, sc, lens, SCALE, tables=tb, status=status, **kw)
+    assert int(status) == 0
+    check_paged(q, kv, sc, tb, lens, cp, il, block, window, sinks, out, lse, kw["lse_base_e"])
+    again = dcp.mla_cache8_decode(q, kv, sc, lens, SCALE, tables=tb, flags=dcp.DCP_FLAG_PDL, **kw)
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("H,B,M,page,cp", [(16, 1, 700, 64, 1), (128, 1, 200, 64, 1), (64, 2, 70, 128, 2),
+                                           (128, 37, 6, 128, 1), (32, 600, 13, 32, 1)])
+def test_paged_decode_is_that_of_the_rows(H, B, M, page, cp):
+    """Bit for bit, where tiles begin at the same tokens (no window)."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(M)
+    P = B * M + 1
+    kv, sc = map(list, zip(*[make_pool(g, P, page, 576, 16) for _ in range(cp)]))
+    tb = [torch.randperm(P, generator=g, device=DEV)[:B * M].view(B, M).int() for _ in range(cp)]
+    rows, rscales = as_rows(kv, sc, tb)
+    q = randn(g, B, H, 576).bfloat16()
+    lens = (torch.rand((B,), generator=g, device=DEV) * cp * M * page).int()
+    lens[0] = cp * M * page
+    a = dcp.mla_cache8_decode(q, rows, rscales, lens, SCALE, block=16)
+    b = dcp.mla_cache8_decode(q, kv, sc, lens, SCALE, block=16, tables=tb)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("H", [16, 64, 128])
+@pytest.mark.parametrize("page", [32, 64, 128, 256])
+@pytest.mark.parametrize("loud", [1.0, 40.0])
+def test_paged_decode_of_tokens_without_a_page(H, page, loud):
+    """Anywhere in a row: its first tiles, its last, all of them, a few. (Loud keys give scores far from zero.)"""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(H + page)
+    n = 1024
+    M, B = n // page, 8
+    P = B * M
+    kv, sc = make_pool(g, P, page, 576, 1)
+    sc *= loud
+    tb = torch.randperm(P, generator=g, device=DEV).view(B, M).int()
+    slot = torch.arange(M, device=DEV)
+    bad = torch.rand((B, M), generator=g, device=DEV) < 0.4
+    bad[0] = slot < M - 1          # the last page alone
+    bad[1] = slot >= 1             # the first alone
+    bad[2] = True
+    bad[3] = (slot * page >= 200) & (slot * page < 700)
+    bad[4] = False
+    bad[5, :max(1, 512 // page)] = True
+    tb = torch.where(bad, ints([-1, P, 1 << 30, -(1 << 31)])[torch.randint(0, 4, (B, M), generator=g, device=DEV)], tb)
+    q = randn(g, B, H, 576).bfloat16()
+    lens = ints([n, n - 3, n, 1000, n, n, 900, 40])
+    for kw in ({}, dict(window=300, sinks=5)):
+        out, lse = dcp.mla_cache8_decode(q, [kv], [sc], lens, SCALE, tables=[tb], **kw)
+        check_paged(q, [kv], [sc], [tb], lens, 1, 1, 1, kw.get("window", 0), kw.get("sinks", 0), out, lse)
+        assert (out[2] == 0).all() and (lse[2] == -float("inf")).all()
+    groups, shared = dcp.mla_cache8_groups([B], [512])
+    same = tb.clone()
+    same[:, :512 // page] = tb[5, :512 // page] if page <= 512 else same[:, :0]
+    out, lse = dcp.mla_cache8_decode(q, [kv], [sc], lens, SCALE, tables=[same], groups=groups, shared=shared)
+    check_paged(q, [kv], [sc], [same], lens, 1, 1, 1, 0, 0, out, lse)
+
+
+GROUPS = [
+    # H, cp, interleave, block, page, rows of the groups, their shared positions, most tokens of a row's own
+    (16, 1, 1, 1, 64, [2], [128], 1),
+    (16, 1, 1, 1, 64, [4], [1000], 300),
+    (16, 1, 1, 64, 64, [9, 1, 3], [1500, 700, 129], 200),
+    (16, 1, 1, 1, 32, [1, 1, 1, 1], [300, 0, 400, 128], 100),
+    (8, 1, 1, 1, 64, [20], [640], 130),
+    (1, 1, 1, 1, 64, [70], [513], 20),
+    (40, 1, 1, 1, 128, [5, 2], [900, 1111], 500),
+    (100, 1, 1, 16, 64, [3, 6], [777, 640], 150),
+    (24, 2, 1, 1, 64, [4, 3], [1000, 300], 100),
+    (16, 4, 16, 16, 32, [6], [3000], 70),
+    (48, 3, 5, 1, 64, [2, 2, 4], [500, 2000, 100], 90),
+    (16, 1, 1, 1, 64, [2] * 20, [256] * 20, 300),
+    (12, 1, 1, 1, 64, [3, 1] * 90, [256, 0] * 90, 150),
+    (32, 1, 1, 1, 256, [300], [384], 64),
+    (64, 1, 1, 1, 64, [3], [600], 100),      # (groups make no difference)
+    (20, 1, 1, 1, 64, [3, 4], [100, 127], 300),  # shorter than a tile
+    (16, 1, 1, 1, 64, [6], [1 << 30], 300),  # beyond every row
+    (16, 16, 1, 1, 32, [5], [4000], 300),
+]
+
+
+@pytest.mark.parametrize("case", GROUPS, ids=lambda c: f"H{c[0]}cp{c[1]}i{c[2]}b{c[3]}p{c[4]}g{len(c[5])}n{sum(c[5])}s{c[6][0]}")
+@pytest.mark.parametrize("dk", [576, 512])
+def test_groups(case, dk):
+    """Rows behind shared prefixes; among them rows of nothing of their own, of no token, and shorter than the prefix
+    (with pages of their own)."""
+    H, cp, il, block, page, counts, shared, most = case
+    if dk == 512 and H not in (16, 40, 100):
+        pytest.skip("one width is enough")
+    B = sum(counts)
+    r = random.Random(B + H)
+    lens, first, alone = [], [], []
+    for n, s in zip(counts, shared):
+        f = len(lens)
+        for i in range(n):
+            base = s if s < 1 << 29 else 400
+            kind = r.random() if n > 2 else 1.0
+            cut = kind < 0.12 and s < 1 << 29
+            lens.append(r.randint(0, max(base - 1, 0)) if cut else base + (0 if kind < 0.25 else r.randint(1, most)))
+            first.append(f)
+            alone.append(cut)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(B * H)
+    M = -(-(max(lens) // (cp * il) + 1) * il // page) + 1
+    P = B * M + 1
+    kv, sc = map(list, zip(*[make_pool(g, P, page, dk, block) for _ in range(cp)]))
+    tb = [torch.randperm(P, generator=g, device=DEV)[:B * M].view(B, M).int() for _ in range(cp)]
+    for j in range(cp):
+        for b in range(B):
+            s = shared[[b >= sum(counts[:k]) and b < sum(counts[:k + 1]) for k in range(len(counts))].index(True)]
+            if b == first[b] or alone[b] or s >= 1 << 29:
+                continue
+            have = ref.share(s, cp, j, il)
+            whole = have // page
+            tb[j][b, :whole] = tb[j][first[b], :whole]
+            if have % page:  # the page that the prefix ends in: a copy, as the step of the tables leaves it
+                a, z = int(tb[j][first[b], whole]), int(tb[j][b, whole])
+                n = have % page
+                kv[j].view(torch.uint8)[z, :n] = kv[j].view(torch.uint8)[a, :n]
+                sc[j][z, :-(-n // block)] = sc[j][a, :-(-n // block)]
+    q = randn(g, B, H, dk).bfloat16()
+    n = ints(lens)
+    groups, common = dcp.mla_cache8_groups(counts, shared)
+    kw = dict(block=block, interleave=il, lse_base_e=H % 3 != 0, tables=tb)
+    status = torch.zeros((1,), dtype=torch.int32, device=DEV)
+    out, lse = dcp.mla_cache8_decode(q, kv, sc, n, SCALE, groups=groups, shared=common, status=status, **kw)
+    assert int(status) == 0
+    check_paged(q, kv, sc, tb, n, cp, il, block, 0, 0, out, lse, kw["lse_base_e"],
+                rows=range(B) if B < 60 else list(range(0, B, 7)) + [B - 1])
+    plain = dcp.mla_cache8_decode(q, kv, sc, n, SCALE, **kw)
+    # two results within 2^-8 of one value each, and the sums' orders
+    assert ((out.float() - plain[0].float()).abs() <= 2.0 ** -6 * plain[0].float().abs().amax(-1, keepdim=True)).all()
+    if H % 64 == 0:
+        assert torch.equal(out, plain[0]) and torch.equal(lse, plain[1])
+    again = dcp.mla_cache8_decode(q, kv, sc, n, SCALE, groups=groups, shared=common, flags=dcp.DCP_FLAG_PDL, **kw)
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
+def test_groups_of_a_long_prefix():
+    """Prefixes that are cut over many CTAs, offset by one long row alone."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(2)
+    H, page, counts, shared = 16, 64, [30, 1, 33], [12000, 0, 7000]
+    B = sum(counts)
+    own = torch.randint(1, 400, (B,), generator=g, device=DEV).tolist()
+    own[30] = 20000
+    lens = [s + own[i] for i, s in enumerate([12000] * 30 + [0] + [7000] * 33)]
+    M = -(-20000 // page)
+    P = 2 * M + B * 8
+    kv, sc = make_pool(g, P + 320, page, 576, 64)
+    free = iter(torch.randperm(P + 320, generator=g, device=DEV).tolist())
+    take = lambda n: [next(free) for _ in range(n)]
+    heads = {0: take(12000 // page), 30: take(M), 31: take(7000 // page)}
+    tb = []
+    for i in range(B):
+        row = list(heads[0 if i < 30 else 30 if i == 30 else 31])
+        row += take(-(-lens[i] // page) - len(row))
+        tb.append(row + [-1] * (M - len(row)))
+    # (a page of the prefix's last, partial page is the row's own, with tokens of its own: shared ends at whole pages)
+    groups, common = dcp.mla_cache8_groups(counts, [s // page * page for s in shared])
+    q, n, tb = randn(g, B, H, 576).bfloat16(), ints(lens), [ints(tb, B, M)]
+    out, lse = dcp.mla_cache8_decode(q, [kv], [sc], n, SCALE, block=64, tables=tb, groups=groups, shared=common)
+    check_paged(q, [kv], [sc], tb, n, 1, 1, 64, 0, 0, out, lse, rows=[0, 1, 7, 29, 30, 31, 40, 63])
+
+
+def test_groups_that_break_the_rules_read_nothing_out_of_place():
+    """Whatever stands in groups and shared, rows that are grouped rightly keep their results."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(4)
+    B, M, page, H = 12, 8, 64, 16
+    P = B * M
+    kv, sc = make_pool(g, P, page, 576, 1)
+    tb = torch.randperm(P, generator=g, device=DEV).view(B, M).int()
+    tb[1:4, :4] = tb[0, :4]
+    q, lens = randn(g, B, H, 576).bfloat16(), ints([400, 300, 256, 500, 100, 512, 0, 17, 129, 300, 64, 511])
+    groups, shared = dcp.mla_cache8_groups([4] + [1] * 8, [256] + [0] * 8)
+    for b, (first, count, common) in enumerate([(-1, 9, 200), (3, 4, 100), (4, 100, 256), (1 << 30, 2, 128),
+                                                (4, -5, 300), (-(1 << 31), 1 << 30, 256), (11, 3, 999),
+                                                ((1 << 31) - 1, (1 << 31) - 1, (1 << 31) - 1)], start=4):
+        groups[b, 0], groups[b, 1], shared[b] = first, count, common
+    out, lse = dcp.mla_cache8_decode(q, [kv], [sc], lens, SCALE, tables=[tb], groups=groups, shared=shared)
+    check_paged(q, [kv], [sc], [tb], lens, 1, 1, 1, 0, 0, out, lse, rows=range(4))
+
+
+def test_paged_decode_partials_of_shards_merge_to_the_whole():
+    """Each shard alone, with a prefix, then the merge: the whole."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(6)
+    cp, B, H, page, M = 4, 6, 16, 64, 4
+    kv, sc = map(list, zip(*[make_pool(g, B * M, page, 576, 1) for _ in range(cp)]))
+    tb = [torch.randperm(B * M, generator=g, device=DEV).view(B, M).int() for _ in range(cp)]
+    for t in tb:
+        t[1:, :2] = t[0, :2]
+    q, lens = randn(g, B, H, 576).bfloat16(), ints([600, 512, 1000, 700, 513, 3])
+    groups, shared = dcp.mla_cache8_groups([B], [512])
+    kw = dict(groups=groups, shared=shared)
+    whole, wl = dcp.mla_cache8_decode(q, kv, sc, lens, SCALE, tables=tb, **kw)
+    check_paged(q, kv, sc, tb, lens, cp, 1, 1, 0, 0, whole, wl)
+    srcs, lses = [], []
+    for j in range(cp):
+        only = lambda x: [x[k] if k == j else None for k in range(cp)]
+        o, l = dcp.mla_cache8_decode(q, only(kv), only(sc), lens, SCALE, tables=only(tb), **kw)
+        check_paged(q, kv, sc, tb, lens, cp, 1, 1, 0, 0, o, l, held=[j])
+        srcs.append(o)
+        lses.append(l)
+    outs, louts = dcp.merge(srcs, lses, True, seq_lens=lens)
+    # each partial is rounded to bf16 (2^-9 of itself), and so is the merged one
+    merged = torch.cat(outs, 1).double()
+    size = torch.stack(srcs).double().abs().amax(0)
+    assert ((merged - whole.double()).abs() <= 2.0 ** -7 * torch.maximum(size, whole.double().abs())).all()
+    assert ((torch.cat(louts, 1) - wl).abs() <= 1e-4).all()
+
+
+def test_a_serving_run():
+    """Prompt, fork, decode steps in a captured graph, an end, a compaction: every step's attention against 64 bits over
+    what the tables say, and the tables against the plain form."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(8)
+    B, M, P, page, H, block = 6, 12, 60, 64, 16, 16
+    tables, refs = [[-1] * M for _ in range(B)], [0] * P
+    t, f = ints(tables, B, M), ints(refs)
+    kv = torch.zeros((P, page, 576), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    sc = torch.ones((P, page // block), device=DEV)
+    inv_freq, _ = dcp.mla_rope_inv_freq(64)
+    rows = [ints([0] * B) for _ in range(3)]
+
+    def plan(parents, keeps, wants):
+        nonlocal tables, refs
+        for x, y in zip(rows, (parents, keeps, wants)):
+            x.copy_(ints(y))
+        tables, refs, _, short = ref.update(tables, refs, parents, keeps, wants, page)
+        assert short == 0
+
+    def step():
+        _, _, copies, missing = dcp.mla_cache8_pages_update(t, f, *rows, page=page)
+        dcp.mla_cache8_pages_copy([kv], [sc], copies)
+        return missing
+
+    # a prompt of 300 tokens in row 0, one of 77 in row 4
+    plan(list(range(B)), [0] * B, [300, 0, 0, 0, 77, 0])
+    step()
+    latent, rope = randn(g, 377, 512).bfloat16(), randn(g, 377, 64).bfloat16()
+    dcp.mla_cache8_append(latent, rope, [kv], [sc], ints([0] * B), cu_new=ints([0, 300, 300, 300, 300, 377, 377]),
+                          block=block, inv_freq=inv_freq, tables=[t])
+    # rows 0 to 3 go on from row 0, each with tokens of its own; row 5 from row 4
+    lens = [300, 300, 300, 300, 77, 77]
+    n = ints(lens)
+    groups, shared = dcp.mla_cache8_groups([4, 2], [300, 77])
+    q = torch.empty((B, H, 576), dtype=torch.bfloat16, device=DEV)
+    new, pe = torch.empty((B, 512), dtype=torch.bfloat16, device=DEV), torch.empty((B, 64), dtype=torch.bfloat16, device=DEV)
+    plan([0, 0, 0, 0, 4, 4], lens, [x + 1 for x in lens])
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        missing = step()
+        dcp.mla_rope(q[..., 512:], n, inv_freq, out=q[..., 512:])
+        dcp.mla_cache8_append(new, pe, [kv], [sc], n, block=block, inv_freq=inv_freq, tables=[t])
+        n.add_(1)
+        out, lse = dcp.mla_cache8_decode(q, [kv], [sc], n, SCALE, block=block, tables=[t], groups=groups, shared=shared)
+    for i in range(70):
+        q.copy_(randn(g, B, H, 576))
+        new.copy_(randn(g, B, 512))
+        pe.copy_(randn(g, B, 64))
+        if i:
+            plan(list(range(B)), lens, [x + 1 for x in lens])
+        graph.replay()
+        torch.cuda.synchronize()
+        lens = [x + 1 for x in lens]
+        assert t.tolist() == tables and f.tolist() == refs and n.tolist() == lens and int(missing) == 0
+        if i % 23 == 0 or i == 69:
+            check_paged(q, [kv], [sc], [t], n, 1, 1, block, 0, 0, out, lse)
+    # rows 0 and 3 end, and the pool shrinks to what is in use
+    plan([-1, 1, 2, -1, 4, 5], lens, [0 if b in (0, 3) else x for b, x in enumerate(lens)])
+    step()
+    before = dcp.mla_cache8_decode(q, [kv], [sc], n, SCALE, block=block, tables=[t])
+    _, _, copies = dcp.mla_cache8_pages_compact(t, f)
+    dcp.mla_cache8_pages_copy([kv], [sc], copies)
+    tables, refs, _ = ref.compact(tables, refs)
+    assert t.tolist() == tables and f.tolist() == refs
+    used = sum(r > 0 for r in refs)
+    assert max(max(r) for r in tables) == used - 1
+    after = dcp.mla_cache8_decode(q, [kv[:used]], [sc[:used]], n, SCALE, block=block, tables=[t])
+    assert torch.equal(before[0], after[0]) and torch.equal(before[1], after[1])
+    assert (after[0][0] == 0).all() and (after[1][3] == -float("inf")).all()
+
+
+@pytest.mark.parametrize("B,H,M,grouped", [(1, 16, 3, False), (8, 16, 40, True), (8, 128, 40, False)])
+def test_paged_decode_after_waits_that_gave_up(B, H, M, grouped):
+    """As for the rows: a wait that runs out sets the status, and the next call is right."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(B)
+    page = 64
+    kv, sc = make_pool(g, B * M, page, 576, 1)
+    tb = [torch.randperm(B * M, generator=g, device=DEV).view(B, M).int()]
+    tb[0][1:, :8] = tb[0][0, :8]
+    q = randn(g, B, H, 576).bfloat16()
+    lens = torch.full((B,), M * page - 5, dtype=torch.int32, device=DEV)
+    groups, shared = dcp.mla_cache8_groups([B], [512])
+    kw = dict(groups=groups, shared=shared) if grouped else {}
+    status = torch.zeros((1,), dtype=torch.int32, device=DEV)
+    dcp.mla_cache8_decode(q, [kv], [sc], lens, SCALE, tables=tb, status=status, flags=dcp.DCP_MLA_FLAG_TEST_STALL, **kw)
+    torch.cuda.synchronize()
+    assert int(status) == 1
+    status.zero_()
+    out, lse = dcp.mla_cache8_decode(q, [kv], [sc], lens, SCALE, tables=tb, status=status, **kw)
+    check_paged(q, [kv], [sc], tb, lens, 1, 1, 1, 0, 0, out, lse, rows=[0, B - 1])
+    assert int(status) == 0
+
+
+def test_paged_decode_far_into_a_pool():
+    """Pages whose bytes lie past 2^32 and past 2^33."""
+    P, page = 240000, 64
+    kv = torch.zeros((P, page, 576), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    sc = torch.zeros((P, page // 16), device=DEV)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    at = [P - 1, 116509, 3, 233017, 120000, P - 7]
+    x, s = make_pool(g, len(at), page, 576, 16)
+    for i, e in enumerate(at):
+        kv.view(torch.uint8)[e], sc[e] = x.view(torch.uint8)[i], s[i]
+    tb = [ints([[P - 1, 116509, 3], [233017, 120000, P - 7]], 2, 3)]
+    q, lens = randn(g, 2, 16, 576).bfloat16(), ints([190, 180])
+    out, lse = dcp.mla_cache8_decode(q, [kv], [sc], lens, SCALE, block=16, tables=tb)
+    check_paged(q, [kv], [sc], tb, lens, 1, 1, 16, 0, 0, out, lse)
+
+
+def test_paged_calls_of_no_rows():
+    kv, sc = torch.zeros((4, 64, 576), dtype=torch.uint8, device=DEV), torch.ones((4, 64), device=DEV)
+    none, zero = torch.empty((0,), dtype=torch.int32, device=DEV), ints([0])
+    tb = [torch.empty((0, 3), dtype=torch.int32, device=DEV)]
+    latent, rope = (torch.empty((0, w), dtype=torch.bfloat16, device=DEV) for w in (512, 64))
+    dcp.mla_cache8_append(latent, rope, [kv], [sc], none, cu_new=zero, tables=tb)
+    assert dcp.mla_cache8_read([kv], [sc], 0, tables=tb).shape == (0, 576)
+    q = torch.empty((0, 16, 576), dtype=torch.bfloat16, device=DEV)
+    groups, shared = dcp.mla_cache8_groups([], [])
+    for kw in ({}, dict(groups=groups, shared=shared)):
+        out, lse = dcp.mla_cache8_decode(q, [kv], [sc], none, SCALE, tables=tb, **kw)
+        assert out.shape == (0, 16, 512) and lse.shape == (0, 16)

@@ -104,7 +104,67 @@ def test_paged_read(code, change):
     refused(code, dcp.dcp_mla_cache8_read_paged, READ, **change)
 
 
+DECODE = dict(q=A, q_row=576 * 16, q_head=576, kv_ptrs=[A], scale_ptrs=[A], table_ptrs=[A], seq_lens=A, cp=1, B=2, H=16,
+              Dk=576, Dv=512, P=8, page=64, M=40, block=1, interleave=1, window=0, sinks=0, scale=1.0, lse_base_e=True,
+              workspace=A, workspace_bytes=1 << 40, out=A, lse=A, stream=0)
+FLAGS, WINDOW = -207, -209
+
+
+@pytest.mark.parametrize("code,change", POOLS + [
+    (SHAPE, dict(H=0)), (SHAPE, dict(H=1025)), (SHAPE, dict(Dv=256)), (WINDOW, dict(window=-1)),
+    (WINDOW, dict(sinks=4)), (WINDOW, dict(groups=A, shared=A, window=4)), (FLAGS, dict(flags=2)),
+    (NULL, dict(q=None)), (NULL, dict(out=None)), (NULL, dict(seq_lens=None)), (NULL, dict(groups=A)),
+    (NULL, dict(shared=A)), (ALIGN, dict(q=A + 2)), (ALIGN, dict(q_row=577)), (ALIGN, dict(out=A + 8)),
+    (ALIGN, dict(groups=A + 4, shared=A)), (ALIGN, dict(groups=A, shared=A + 2)), (ALIGN, dict(status=A + 2)),
+    (SHAPE, dict(B=65535, M=32767, page=64, cp=16, kv_ptrs=[A] * 16, scale_ptrs=[A] * 16, table_ptrs=[A] * 16))])
+def test_paged_decode(code, change):
+    refused(code, dcp.dcp_mla_cache8_decode_paged, DECODE, **change)
+
+
+def test_paged_decode_workspace_bytes():
+    ws = dcp.dcp_mla_cache8_decode_paged_workspace_bytes
+    rows = dcp.dcp_mla_cache8_decode_workspace_bytes
+    assert ws(1, 8, 16, 64, 100, 0, 0, False, 152) == rows(1, 8, 16, 6400, 0, 0, 152) > 0
+    assert ws(1, 8, 16, 64, 4, 0, 0, False, 152) == 0  # two tiles a row: no row is split
+    # with groups a place for each row's own part and for each set of a group's heads, in blocks of 64
+    assert ws(1, 8, 16, 64, 4, 0, 0, True, 152) >= (152 + 16) * 64 * 513 * 4
+    assert ws(1, 2, 16, 64, 100, 0, 0, True, 152) < ws(1, 4, 16, 64, 100, 0, 0, True, 152)  # blocks of 32, of 64
+    # groups make no difference with whole blocks of 64 heads, many rows, or one
+    for B, H in ((8, 64), (8, 128), (2049, 16), (1, 16)):
+        assert ws(1, B, H, 64, 100, 0, 0, True, 152) == ws(1, B, H, 64, 100, 0, 0, False, 152)
+    assert ws(1, 0, 16, 64, 100, 0, 0, True, 152) == 0
+    for bad in (dict(page=16), dict(page=96), dict(M=0), dict(M=1 << 26), dict(B=-1), dict(H=0), dict(sms=0)):
+        a = {**dict(B=8, H=16, page=64, M=100, sms=152), **bad}
+        assert ws(1, a["B"], a["H"], a["page"], a["M"], 0, 0, True, a["sms"]) == -1
+
+
+def test_groups_on_the_host():
+    groups, shared = dcp.mla_cache8_groups([2, 0, 1, 3], [40, 7, 0, 9], device="cpu")
+    assert groups.tolist() == [[0, 2], [0, 2], [2, 1], [3, 3], [3, 3], [3, 3]]
+    assert shared.tolist() == [40, 40, 0, 9, 9, 9] and groups.dtype == shared.dtype == torch.int32
+    assert dcp.mla_cache8_groups([], [], device="cpu")[0].shape == (0, 2)
+    for bad in (([1], []), ([-1], [0]), ([1], [-1]), ([1], [1 << 31])):
+        with pytest.raises(ValueError):
+            dcp.mla_cache8_groups(*bad, device="cpu")
+
+
+def test_decode_wrapper_checks_groups():
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    kv, sc, t = torch.zeros((4, 64, 576), dtype=torch.uint8), torch.ones((4, 64)), i32(2, 3)
+    q = torch.zeros((2, 4, 576), dtype=torch.bfloat16)
+    call = lambda tables=[t], **k: dcp.mla_cache8_decode(q, [kv], [sc], i32(2), 1.0, tables=tables, **k)
+    with pytest.raises(ValueError, match="CUDA"):
+        call(groups=i32(2, 2), shared=i32(2))
+    for kw in (dict(groups=i32(2, 2)), dict(shared=i32(2)), dict(groups=i32(3, 2), shared=i32(2)),
+               dict(groups=i32(2, 2).long(), shared=i32(2)), dict(groups=i32(2, 2), shared=i32(3)),
+               dict(groups=i32(2, 2), shared=i32(2), window=5), dict(tables=None, groups=i32(2, 2), shared=i32(2)),
+               dict(groups=i32(2, 4)[:, ::2], shared=i32(2)), dict(tables=[None]), dict(tables=[t.long()])):
+        with pytest.raises(ValueError):
+            call(**kw)
+
+
 def test_paged_calls_of_nothing():
+    dcp.dcp_mla_cache8_decode_paged(**{**DECODE, "B": 0, "workspace": None})
     dcp.dcp_mla_cache8_append_paged(**{**PAGED, "N": 0})
     dcp.dcp_mla_cache8_append_paged(**{**PAGED, "P": 0})
     dcp.dcp_mla_cache8_read_paged(**{**READ, "N": 0, "out": None})
