@@ -128,6 +128,16 @@ def test_update_of_a_large_table():
     check_update(tables, refs, [b if b % 2 else -1 for b in range(B)], [most // 2 + 1] * B, [most] * B, 32)
 
 
+def test_update_of_a_pool_that_shared_memory_does_not_hold():
+    """262,144 pages are kept on chip; and more rows than are."""
+    r = random.Random(3)
+    for B, M, P in ((50, 60, 300_001), (20_000, 2, 50_000), (20, 60, 150_000)):
+        tables, refs = make_tables(r, B, M, P, 0.5)
+        parents = [r.choice([b, b, -1, r.randrange(B)]) for b in range(B)]
+        keeps = [r.randint(0, M * 32) for _ in range(B)]
+        check_update(tables, refs, parents, keeps, [k + r.choice([0, 1, 40]) for k in keeps], 32)
+
+
 def test_update_of_no_rows():
     t, f = torch.empty((0, 4), dtype=torch.int32, device=DEV), ints([0, 2, 0])
     e = torch.empty((0,), dtype=torch.int32, device=DEV)

@@ -173,7 +173,7 @@ def test_paged_calls_of_nothing():
 def test_workspace_bytes():
     up, co = dcp.dcp_mla_pages_update_workspace_bytes, dcp.dcp_mla_pages_compact_workspace_bytes
     assert up(4, 100, 50, True) >= up(4, 100, 50, False) + 4 * 100 * 4
-    assert up(256, 1, 1000, False) >= 256 * 24 + 3 * 4000 and co(1000) >= 8000
+    assert up(20000, 1, 300000, False) >= 20000 * 16 + 300000 * 12 and co(100000) >= 2 * 12500
     for bad in ((-1, 1, 1), (65536, 1, 1), (1, 0, 1), (1, 1, 0), (65535, 1 << 15, 1)):
         assert up(*bad, False) == -1
     assert co(0) == co(1 << 31) == -1
