@@ -79,6 +79,11 @@ constexpr int kSlice = kTile * 128;        // bytes of a 128-dim slice of a tile
 constexpr int kSoftWarps = 16, kSoftThreads = 32 * kSoftWarps;
 constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
 constexpr int kThreads = kSoftThreads + 64;
+// With pages three warps load, the first slice, the next two, and the last with the rope slice (the second and third warp
+// stand behind the MMA warp): a request takes its warp some 150 cycles, a tile has up to 20 of them, and a slice's place
+// is free only shortly before its next tokens are wanted. (A fourth would leave 80 registers a thread. 64 ragged rows x 16K
+// x 128 heads, pages of 32, 64, 128 tokens: 157, 147 and 141 us with one, 132, 129 and 128 with three)
+constexpr int kPagedThreads = kThreads + 64;
 constexpr int kCpMax = DCP_MLA_CACHE8_CP_MAX;
 constexpr int64_t kMaxInterleave = 1 << 24;
 constexpr long long kWaitLimitNs = 2000000000LL;  // every wait gives up after this,
@@ -124,6 +129,7 @@ struct DecodeParams : DecodeBase {
 template <int kShards>
 struct PagedParams : DecodeParams<kShards> {
     static constexpr bool kPaged = true;
+    const uint8_t* kv[kShards];
     const int* tables[kShards];
     const int2* groups;                    // [B] first row and rows of the row's group, or NULL
     const int* shared;                     // [B] positions that they have in common
@@ -203,6 +209,10 @@ __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* tm, int x, in
     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(tm)),
                  "r"(x), "r"(y), "r"(z)
                  : "memory");
+}
+// `bytes` (a multiple of 16) from a 16-byte boundary to L2
+__device__ __forceinline__ void prefetch_bulk(const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 constexpr uint32_t kSwizzle128 = 2, kSwizzle64 = 4, kSwizzle32 = 6, kSwizzleNone = 0;
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
@@ -703,7 +713,7 @@ __device__ __forceinline__ void issue_values(uint32_t ka, uint32_t pa, uint32_t 
 // the second kernel), each head block for itself; a call whose rows have at most two
 // tiles gives whole rows to a CTA and needs no second kernel.
 template <int kDk, int kNH, class P>
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ P p) {
+__global__ void __launch_bounds__(P::kPaged ? kPagedThreads : kThreads, 1) decode_kernel(const __grid_constant__ P p) {
     using S = Shape<kDk, kNH>;
     constexpr bool kPaged = P::kPaged;
     constexpr int kHW = S::kHW, kChange = kNH / 32;
@@ -722,6 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     volatile int* const abort_flag = &sh->abort;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool loads = warp == kLoadWarp || (kPaged && warp > kMmaWarp);
     const int hblk = blockIdx.x % p.head_blocks, range = blockIdx.x / p.head_blocks;
     const int h0 = hblk * kNH;
     const int nh = p.H - h0 < kNH ? p.H - h0 : kNH;
@@ -754,12 +765,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     pdl_launch_dependents();
     const int lines = line_count(p);
     Line line = {0u, 0u, 0u};  // the loading warp's; with few lines, first a lane's own
-    if (warp == kLoadWarp && lane < lines) line = line_of(p, lane, hblk, kNH);
+    if (loads && lane < lines) line = line_of(p, lane, hblk, kNH);
 
     // ---- this CTA's tiles: [g, g_end) of all rows' tiles, from tile `tile` of row `row` (or whole rows)
     int row = range, tile = 0, n_row = 0, g = 0, g_end = 0;
     if (!p.row_mode && lines <= 32) {
-        if (warp == kLoadWarp) {  // few rows: a lane a row, beside the others' set-up
+        if (loads) {  // few rows: a lane a row, beside the others' set-up
             const int n = lane < lines ? row_tiles(p, line) : 0;
             int x = places(n, kChange);
 #pragma unroll 1
@@ -782,12 +793,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 line.base = __shfl_sync(0xffffffffu, line.base, row);
                 line.source = __shfl_sync(0xffffffffu, line.source, row);
             }
-            if (lane == 0 && here) {
+            if (lane == 0 && here && warp == kLoadWarp) {
                 sh->find[0] = row;
                 if constexpr (kPaged) sh->find[3] = (int)line.source;
             }
             // (told before the shuffles, the rows' kernel of 64 heads spills: 145.6 us for 64 ragged rows x 16K, not 142)
-            if (hblk == 0 && lane < lines) tell_row(p, lane, own, n, pre, g, g_end, per, range, kChange);
+            if (hblk == 0 && lane < lines && warp == kLoadWarp) tell_row(p, lane, own, n, pre, g, g_end, per, range, kChange);
         }
     } else if (!p.row_mode) {
         int total = 0, n_mine = 0, pre_mine = 0, per_cta = 0;
@@ -841,8 +852,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
 
-    if (warp == kLoadWarp) {
-        // ---- loads (the warp walks together, lane 0 issues)
+    if (loads) {
+        // ---- loads (the warp walks together, lane 0 issues; with pages this warp's slice only, a lane a page)
+        const int my_slice = kPaged && warp > kMmaWarp ? 2 * (warp - kMmaWarp) - 1 : 0;
+        const int end_slice = kPaged ? (my_slice == 1 ? 3 : my_slice + 1) : 4;
         if (!p.row_mode && lines > 32) {
             row = lines;
             if (g < g_end) {  // (a range of no tiles has found no row)
@@ -854,7 +867,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         }
         // the pages of a tile: a lane has that of its 32, 64 or 128 tokens
         int box_log2 = 7, boxes = 1;
+        uint32_t page_mask = ~0u;
         if constexpr (kPaged) {
+            page_mask = (1u << p.page_log2) - 1;
             box_log2 = p.page_log2 < 7 ? p.page_log2 : 7;
             boxes = kTile >> box_log2;
         }
@@ -891,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 n_row = row_tiles(p, line);
             }
             known = false;
-            if (n_row == 0 && p.row_mode) {  // a row that sees nothing
+            if (n_row == 0 && p.row_mode && my_slice == 0) {  // a row that sees nothing
                 uint4* const o = reinterpret_cast<uint4*>(p.out + ((int64_t)row * p.H + h0) * (kDv * 2));
                 for (int i = lane; i < nh * (kDv / 8); i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
                 if (p.lse != nullptr)
@@ -916,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     const int tok0 = (int)c.token();
                     uint32_t what = c.j | about | (i == 0 ? kFirst : 0u) | (i == n - 1 ? kLast : 0u);
                     int valid = c.valid();
-                    if constexpr (kPaged) {
+                    if (kPaged && my_slice == 0) {
                         if (lane < 4) sh->pages[t & 3][lane] = id;
                         const int lo = lane << box_log2;
                         const bool seen = id >= 0 && lo < valid && lo + (1 << box_log2) > c.skip();
@@ -925,7 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                         valid |= c.skip() << 8;
                         __syncwarp();
                     }
-                    if (lane == 0) {
+                    if (lane == 0 && my_slice == 0) {
                         sh->info[t & 3] = {(uint32_t)tok0, valid, what, row};
                         if constexpr (kPaged) sh->source[t & 3] = line.source;
                         mbar_arrive(&sh->info_full[t & 3]);
@@ -934,31 +949,31 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     if (t == 0)
                         ok = __all_sync(0xffffffffu, mbar_wait(&sh->q_asked, 0, abort_flag, p.status, p.wait_ns));
                     if (!ok) break;
+                    const int id0 = kPaged ? __shfl_sync(0xffffffffu, id, 0) : row, y = tok0 & (int)page_mask;
 #pragma unroll 1
-                    for (int a = 0; a < 4; ++a) {
+                    for (int a = my_slice; a < end_slice; ++a) {
                         if (t >= 2) ok = mbar_wait(&sh->kv_free[st][a], par, abort_flag, p.status, p.wait_ns);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
+                        uint64_t* const bar = &sh->kv_full[st][a];
                         if (lane == 0) {
-                            uint64_t* const bar = &sh->kv_full[st][a];
                             mbar_expect_tx(bar, kSlice + (a == 3 ? S::kRopeSlice : 0) +
                                                     (p.stall && t == 0 && a == 0 ? 16 : 0));
-                            if constexpr (!kPaged) {
-                                tma_load_3d(kv + a * kSlice, &p.tm_latent[c.j], a * 128, tok0, row, bar);
+                            if (!kPaged || boxes == 1) {  // (what is the same in every lane is cheaper)
+                                tma_load_3d(kv + a * kSlice, &p.tm_latent[c.j], a * 128, y, id0, bar);
                                 if (S::kHasRope && a == 3)
-                                    tma_load_3d(kv + 4 * kSlice, &p.tm_rope[c.j], kDv, tok0, row, bar);
+                                    tma_load_3d(kv + 4 * kSlice, &p.tm_rope[c.j], kDv, y, id0, bar);
                             }
                             sh->armed[st][a] = (int)(t >> 1);
                         }
-                        if constexpr (kPaged) {  // (a page of none lies outside the map: zeros)
-                            __syncwarp();
-                            if (lane < boxes) {
-                                uint64_t* const bar = &sh->kv_full[st][a];
-                                const int y = tok0 & ((1 << p.page_log2) - 1) & ~(kTile - 1);
-                                tma_load_3d(kv + a * kSlice + (lane << (box_log2 + 7)), &p.tm_latent[c.j], a * 128, y,
+                        if constexpr (kPaged) {
+                            // a lane a page (of none, it lies outside the map: zeros), in no order with lane 0's arrival:
+                            // the phase waits for that and for all of its bytes
+                            if (boxes > 1 && lane < boxes) {
+                                tma_load_3d(kv + a * kSlice + (lane << (box_log2 + 7)), &p.tm_latent[c.j], a * 128, 0,
                                             id, bar);
                                 if (S::kHasRope && a == 3)
-                                    tma_load_3d(kv + 4 * kSlice + (lane << (box_log2 + 6)), &p.tm_rope[c.j], kDv, y,
+                                    tma_load_3d(kv + 4 * kSlice + (lane << (box_log2 + 6)), &p.tm_rope[c.j], kDv, 0,
                                                 id, bar);
                             }
                             __syncwarp();
@@ -969,11 +984,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     if constexpr (kPaged) {
                         if (i + 1 < n) {
                             id = page_at(c, table_row);
-                            if (t >= 1 && lane < boxes && id >= 0) {
-                                const int y = (int)c.token() & ((1 << p.page_log2) - 1) & ~(kTile - 1);
-#pragma unroll 1
-                                for (int a = 0; a < 4; ++a) tma_prefetch_3d(&p.tm_latent[c.j], a * 128, y, id);
-                                if constexpr (S::kHasRope) tma_prefetch_3d(&p.tm_rope[c.j], kDv, y, id);
+                            // the next tile's stage is still in use: to L2 meanwhile (a page's tokens lie side by side,
+                            // so one request a page instead of one a slice)
+                            if (my_slice == 3 && t >= 1 && lane < boxes && id >= 0) {
+                                const int64_t at = ((int64_t)id << p.page_log2) + (boxes == 1 ? c.token() & page_mask : 0u);
+                                prefetch_bulk(p.kv[c.j] + at * kDk, (uint32_t)kDk << box_log2);
                             }
                             __syncwarp();
                         }
@@ -990,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             row += p.row_mode ? p.ranges : 1;
             tile = p.row_mode ? 0 : -kChange;
         }
-        if (lane == 0) {
+        if (lane == 0 && my_slice == 0) {
             if (ok) {  // no more tiles: a tile of no tokens
                 if (t >= 4) ok = mbar_wait(&sh->kv_free[t & 1][3], ((t >> 1) + 1) & 1, abort_flag, p.status, p.wait_ns);
                 sh->info[t & 3] = {0u, 0, 0u, 0};
@@ -1739,6 +1754,12 @@ int multiprocessors() {
     return n;
 }
 
+template <class P>
+bool grouped_rows(const P& p) {
+    if constexpr (P::kPaged) return p.groups != nullptr;
+    return false;
+}
+
 template <int kDk, int kNH, class P>
 cudaError_t launch_decode(const P& p, unsigned flags, cudaStream_t st) {
     constexpr int bytes = Shape<kDk, kNH>::kSmem;
@@ -1753,7 +1774,7 @@ cudaError_t launch_decode(const P& p, unsigned flags, cudaStream_t st) {
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.ranges * p.head_blocks));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(P::kPaged ? kPagedThreads : kThreads);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -1767,8 +1788,9 @@ cudaError_t launch_decode(const P& p, unsigned flags, cudaStream_t st) {
     const int64_t units = (int64_t)p.B * p.H;
     // four warps a (row, head) where a row has four segments or more on average and the CTAs of all (row, head) are
     // resident in about one turn, else one (128 heads: 8 rows x 4096 23.4 us with four, 25.7 with one; 19 rows 38.2 and
-    // 36.5; 64 ragged rows x 16K 152 and 145; 16 heads, 32 rows x 4096 26.2 and 27.3)
-    const bool few = p.ranges >= 4 * p.B && units <= 8 * (int64_t)p.ranges * p.head_blocks;
+    // 36.5; 64 ragged rows x 16K 152 and 145; 16 heads, 32 rows x 4096 26.2 and 27.3), and with groups, whose prefixes
+    // have many (64 rows of 16 heads behind two prefixes of 16K: 61.6 and 63.4)
+    const bool few = (p.ranges >= 4 * p.B || grouped_rows(p)) && units <= 8 * (int64_t)p.ranges * p.head_blocks;
     cfg.gridDim = dim3((unsigned)(few ? units : (units + 7) / 8));
     cfg.blockDim = dim3(few ? 128 : 256);
     cfg.dynamicSmemBytes = 0;
@@ -1829,7 +1851,10 @@ template <int kShards>
 int run_paged(const DecodeBase& base, const Pages& pages, const void* const* kv, const float* const* scales, int Dk,
               int heads, unsigned flags, cudaStream_t st) {
     PagedParams<kShards> p;
-    for (uint32_t j = 0; j < (uint32_t)kShards; ++j) p.tables[j] = j < base.cp ? pages.tables[j] : nullptr;
+    for (uint32_t j = 0; j < (uint32_t)kShards; ++j) {
+        p.kv[j] = j < base.cp ? static_cast<const uint8_t*>(kv[j]) : nullptr;
+        p.tables[j] = j < base.cp ? pages.tables[j] : nullptr;
+    }
     p.groups = reinterpret_cast<const int2*>(pages.groups);
     p.shared = pages.shared;
     p.lead = pages.lead;
@@ -1859,9 +1884,14 @@ int page_log2_of(int page) {
 
 // Groups are of use where a row's heads leave room in a block of 64: then several rows' heads fill it, and a prefix's
 // tile is multiplied for all of them at once. (A multiple of 64 heads fills its blocks alone: every block takes the
-// prefix's tiles for itself either way, and finds them in L2 without groups too.) They cost a place for partial results
-// per row, so that there is a limit.
-bool uses_groups(bool grouped, int64_t B, int H) { return grouped && B >= 2 && B <= 2048 && H % 64 != 0; }
+// prefix's tiles for itself either way, and finds them in L2 without groups too.) And where there are tiles enough: blocks
+// of 64 heads, places and a join cost some 5 us more than 16 heads a row alone. (16 heads, one group, with groups and
+// without: 8 rows x 2,048 tokens, 144 tiles, 18.8 us and 12.9; 16 x 8,192, 1,056 tiles, 24.0 and 22.8; 8 x 32,768, 2,064
+// tiles, 31.2 and 33.5; 32 x 32,768, 8,256 tiles, 51.4 and 93.1. 40 heads, 16 x 8,192: 30.4 and 31.4.) What is known here is
+// what rows have room for, not their lengths. Each row takes places for partial results, so that there is a limit.
+bool uses_groups(bool grouped, int cp, int64_t B, int H, int64_t T) {
+    return grouped && B >= 2 && B <= 2048 && H % 64 != 0 && B * cp * ((T + kTile - 1) / kTile) >= 1024;
+}
 int group_block(int64_t B, int H) { return head_block(B * H < 64 ? (int)(B * H) : 64); }
 
 }  // namespace
@@ -1879,7 +1909,7 @@ extern "C" int64_t dcp_mla_cache8_decode_paged_workspace_bytes(int cp, int64_t B
                                                                int num_sms) {
     if (page_log2_of(page) < 0 || M < 1 || M > 0x7fffffff || M * page > 0x7fffffff) return -1;
     const int64_t bytes = dcp_mla_cache8_decode_workspace_bytes(cp, B, H, M * page, window, sinks, num_sms);
-    return bytes < 0 || B == 0 || !uses_groups(grouped != 0, B, H)
+    return bytes < 0 || B == 0 || !uses_groups(grouped != 0, cp, B, H, M * page)
                ? bytes
                : workspace_of(B, H, group_block(B, H), true, num_sms).bytes;
 }
@@ -1920,7 +1950,7 @@ static int decode_call(const void* q, int64_t q_row, int64_t q_head, const void*
     }
     if (some < 0) return DCP_MLA_CACHE8_ERR_NULL_POINTER;
     // every tile count stays in 32 bits
-    const bool grouped = pages != nullptr && uses_groups(pages->groups != nullptr, B, H);
+    const bool grouped = pages != nullptr && uses_groups(pages->groups != nullptr, cp, B, H, T);
     const int64_t shard_tiles = T / kTile + 2;
     if (B * cp * shard_tiles * (grouped ? 2 : 1) > 0x40000000) return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
     if (B == 0) return 0;

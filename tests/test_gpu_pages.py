@@ -517,10 +517,17 @@ def test_paged_decode_of_tokens_without_a_page(H, page, loud):
         check_paged(q, [kv], [sc], [tb], lens, 1, 1, 1, kw.get("window", 0), kw.get("sinks", 0), out, lse)
         assert (out[2] == 0).all() and (lse[2] == -float("inf")).all()
     groups, shared = dcp.mla_cache8_groups([B], [512])
-    same = tb.clone()
-    same[:, :512 // page] = tb[5, :512 // page] if page <= 512 else same[:, :0]
+    same = roomy(tb, 1, page)
+    same[:, :512 // page] = tb[5, :512 // page]
     out, lse = dcp.mla_cache8_decode(q, [kv], [sc], lens, SCALE, tables=[same], groups=groups, shared=shared)
     check_paged(q, [kv], [sc], [same], lens, 1, 1, 1, 0, 0, out, lse)
+
+
+def roomy(t, cp, page):
+    """Tables with room for the 1024 tiles from which on groups are used: entries of -1 behind the others."""
+    B, M = t.shape
+    more = max(0, -(-1024 * 128 // (B * cp * page)) - M)
+    return torch.cat((t, torch.full((B, more), -1, dtype=torch.int32, device=DEV)), 1)
 
 
 GROUPS = [
@@ -572,6 +579,7 @@ def test_groups(case, dk):
     P = B * M + 1
     kv, sc = map(list, zip(*[make_pool(g, P, page, dk, block) for _ in range(cp)]))
     tb = [torch.randperm(P, generator=g, device=DEV)[:B * M].view(B, M).int() for _ in range(cp)]
+    tb = [roomy(t, cp, page) for t in tb]
     for j in range(cp):
         for b in range(B):
             s = shared[[b >= sum(counts[:k]) and b < sum(counts[:k + 1]) for k in range(len(counts))].index(True)]
@@ -637,7 +645,7 @@ def test_groups_that_break_the_rules_read_nothing_out_of_place():
     B, M, page, H = 12, 8, 64, 16
     P = B * M
     kv, sc = make_pool(g, P, page, 576, 1)
-    tb = torch.randperm(P, generator=g, device=DEV).view(B, M).int()
+    tb = roomy(torch.randperm(P, generator=g, device=DEV).view(B, M).int(), 1, page)
     tb[1:4, :4] = tb[0, :4]
     q, lens = randn(g, B, H, 576).bfloat16(), ints([400, 300, 256, 500, 100, 512, 0, 17, 129, 300, 64, 511])
     groups, shared = dcp.mla_cache8_groups([4] + [1] * 8, [256] + [0] * 8)
@@ -655,7 +663,7 @@ def test_paged_decode_partials_of_shards_merge_to_the_whole():
     g.manual_seed(6)
     cp, B, H, page, M = 4, 6, 16, 64, 4
     kv, sc = map(list, zip(*[make_pool(g, B * M, page, 576, 1) for _ in range(cp)]))
-    tb = [torch.randperm(B * M, generator=g, device=DEV).view(B, M).int() for _ in range(cp)]
+    tb = [roomy(torch.randperm(B * M, generator=g, device=DEV).view(B, M).int(), cp, page) for _ in range(cp)]
     for t in tb:
         t[1:, :2] = t[0, :2]
     q, lens = randn(g, B, H, 576).bfloat16(), ints([600, 512, 1000, 700, 513, 3])
@@ -683,7 +691,7 @@ def test_a_serving_run():
     what the tables say, and the tables against the plain form."""
     g = torch.Generator(device=DEV)
     g.manual_seed(8)
-    B, M, P, page, H, block = 6, 12, 60, 64, 16, 16
+    B, M, P, page, H, block = 6, 360, 60, 64, 16, 16  # (room for 1024 tiles: groups are used)
     tables, refs = [[-1] * M for _ in range(B)], [0] * P
     t, f = ints(tables, B, M), ints(refs)
     kv = torch.zeros((P, page, 576), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
@@ -759,7 +767,9 @@ def test_paged_decode_after_waits_that_gave_up(B, H, M, grouped):
     page = 64
     kv, sc = make_pool(g, B * M, page, 576, 1)
     tb = [torch.randperm(B * M, generator=g, device=DEV).view(B, M).int()]
-    tb[0][1:, :8] = tb[0][0, :8]
+    if grouped:
+        tb = [roomy(tb[0], 1, page)]
+        tb[0][1:, :8] = tb[0][0, :8]
     q = randn(g, B, H, 576).bfloat16()
     lens = torch.full((B,), M * page - 5, dtype=torch.int32, device=DEV)
     groups, shared = dcp.mla_cache8_groups([B], [512])

@@ -127,11 +127,13 @@ def test_paged_decode_workspace_bytes():
     assert ws(1, 8, 16, 64, 100, 0, 0, False, 152) == rows(1, 8, 16, 6400, 0, 0, 152) > 0
     assert ws(1, 8, 16, 64, 4, 0, 0, False, 152) == 0  # two tiles a row: no row is split
     # with groups a place for each row's own part and for each set of a group's heads, in blocks of 64
-    assert ws(1, 8, 16, 64, 4, 0, 0, True, 152) >= (152 + 16) * 64 * 513 * 4
-    assert ws(1, 2, 16, 64, 100, 0, 0, True, 152) < ws(1, 4, 16, 64, 100, 0, 0, True, 152)  # blocks of 32, of 64
-    # groups make no difference with whole blocks of 64 heads, many rows, or one
-    for B, H in ((8, 64), (8, 128), (2049, 16), (1, 16)):
-        assert ws(1, B, H, 64, 100, 0, 0, True, 152) == ws(1, B, H, 64, 100, 0, 0, False, 152)
+    assert ws(1, 8, 16, 64, 256, 0, 0, True, 152) >= (152 + 16) * 64 * 513 * 4
+    assert ws(1, 2, 16, 64, 1024, 0, 0, True, 152) < ws(1, 4, 16, 64, 1024, 0, 0, True, 152)  # blocks of 32, of 64
+    # groups make no difference with whole blocks of 64 heads, many rows, one, or fewer than 1024 tiles of room
+    for B, H, M in ((8, 64, 1024), (8, 128, 1024), (2049, 16, 1024), (1, 16, 4096), (8, 16, 254)):
+        assert ws(1, B, H, 64, M, 0, 0, True, 152) == ws(1, B, H, 64, M, 0, 0, False, 152)
+    assert ws(1, 8, 16, 64, 256, 0, 0, True, 152) == ws(4, 8, 16, 64, 64, 0, 0, True, 152) != \
+        ws(1, 8, 16, 64, 256, 0, 0, False, 152)
     assert ws(1, 0, 16, 64, 100, 0, 0, True, 152) == 0
     for bad in (dict(page=16), dict(page=96), dict(M=0), dict(M=1 << 26), dict(B=-1), dict(H=0), dict(sms=0)):
         a = {**dict(B=8, H=16, page=64, M=100, sms=152), **bad}
