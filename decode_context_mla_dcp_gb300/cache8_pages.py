@@ -66,7 +66,10 @@ def _space(workspace, key, ask, index):
             if len(_ROOM) > 4096:
                 _ROOM.clear()
             size = _ROOM[key] = ask()
-        workspace = _c._torch.empty((max(size, 1),), dtype=_c._torch.uint8, device=_c._cuda(index))
+        if size <= 0:
+            return None, size, None
+        torch = _c._torch
+        workspace = torch.empty((size,), dtype=torch.uint8, device=_c._cuda(index))
         return workspace.data_ptr(), size, workspace
     if workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the tables' device")

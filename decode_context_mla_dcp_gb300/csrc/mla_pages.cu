@@ -626,7 +626,7 @@ extern "C" int dcp_mla_pages_update(const int32_t* tables, const int32_t* refs, 
     if (check_alias(tables, refs, tables_out, refs_out, B * M, P)) return DCP_MLA_CACHE8_ERR_ALIAS;
     const bool in_place = refs == refs_out;
     const UpdateSpace ws = update_space(B, M, P, in_place);
-    if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < ws.bytes)
+    if (ws.bytes > 0 && (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < ws.bytes))
         return DCP_MLA_CACHE8_ERR_WORKSPACE;
     uint8_t* const w = static_cast<uint8_t*>(workspace);
     UpdateParams p;

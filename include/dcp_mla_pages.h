@@ -60,7 +60,9 @@ enum {
  *   copies   [B, 2] int32, 8-byte aligned; missing: one int32
  *   parents, keeps, wants  [B] int32 (negative positions: 0)
  *   workspace at least dcp_mla_pages_update_workspace_bytes(...) bytes, 256-byte
- *            aligned; its contents do not matter. Calls that share one are ordered.
+ *            aligned (NULL where that is 0: out of place, with up to 16,384 rows and
+ *            262,144 pages); its contents do not matter. Calls that share one are
+ *            ordered.
  *   shapes   0 <= B <= 65535, 1 <= M, B * (M + 1) < 2^31, 1 <= P < 2^31, 0 <= shard < cp
  */
 int dcp_mla_pages_update(const int32_t* tables, const int32_t* refs, const int32_t* parents, const int32_t* keeps,
@@ -68,7 +70,7 @@ int dcp_mla_pages_update(const int32_t* tables, const int32_t* refs, const int32
                          int interleave, int32_t* tables_out, int32_t* refs_out, int32_t* copies, int32_t* missing,
                          void* workspace, int64_t workspace_bytes, void* stream);
 
-/* Bytes of workspace for dcp_mla_pages_update; -1 for sizes out of range. Host only. */
+/* Bytes of workspace for dcp_mla_pages_update, 0 for none; -1 for sizes out of range. Host only. */
 int64_t dcp_mla_pages_update_workspace_bytes(int64_t B, int64_t M, int64_t P, int in_place);
 
 /*

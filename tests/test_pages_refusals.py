@@ -59,7 +59,7 @@ def test_compact(code, change):
 
 
 @pytest.mark.parametrize("code,change", [
-    (SHAPE, dict(n=-1)), (SHAPE, dict(n=1 << 31)), (SHAPE, dict(P=0)), (SHAPE, dict(Dk=640)), (SHAPE, dict(pools=0)),
+    (SHAPE, dict(n=-1)), (SHAPE, dict(n=1 << 31)), (SHAPE, dict(n=1 << 29, page=4096)), (SHAPE, dict(P=0)), (SHAPE, dict(Dk=640)), (SHAPE, dict(pools=0)),
     (SHAPE, dict(pools=129, kv_ptrs=[A] * 129, scale_ptrs=[A] * 129)), (BLOCK, dict(block=3)), (BLOCK, dict(block=0)),
     (BLOCK, dict(block=256, page=256)), (PAGE, dict(page=16)), (PAGE, dict(page=96)), (PAGE, dict(page=32, block=64)),
     (NULL, dict(kv_ptrs=[None])), (NULL, dict(scale_ptrs=[None])), (NULL, dict(copies=None)),
@@ -179,6 +179,9 @@ def test_workspace_bytes():
     for bad in ((-1, 1, 1), (65536, 1, 1), (1, 0, 1), (1, 1, 0), (65535, 1 << 15, 1)):
         assert up(*bad, False) == -1
     assert co(0) == co(1 << 31) == -1
+    assert up(16384, 100, 262144, False) == 0 < up(16385, 100, 262144, False)
+    assert up(1, 1, 262145, False) > 0 and up(1, 1, 1, True) > 0
+    assert up(0, 4, 8, True) == 0
 
 
 def test_wrappers():
