@@ -1271,9 +1271,10 @@ __global__ void __launch_bounds__(P::kPaged ? kPagedThreads : kThreads, 1) decod
 #pragma unroll
                     for (int k = 0; k < 8; ++k) r[(k + tok) & 7] = make_uint4(0u, 0u, 0u, 0u);
                 }
-                // E, the 32 tokens' largest score rounded to an integer, per head; how far it lies from the reference;
-                // and P = 2^(s - E + 8) in (0, 2^8.5], which does not depend on the reference
-                int d[kHW], far = INT_MIN;
+                // E, the 32 tokens' largest score rounded to an integer, per head, and P = 2^(s - E + 8) in (0, 2^8.5],
+                // which does not depend on the reference
+                int* const mine = red_i + quad * kNH + hb;  // this warp's words
+                int top[kHW];
                 uint32_t wh[kHW / 4], wl[kHW / 4];
                 const f32x2 neg = pack2(-1.f, -1.f);
 #pragma unroll
@@ -1285,13 +1286,9 @@ __global__ void __launch_bounds__(P::kPaged ? kPagedThreads : kThreads, 1) decod
                         const f32x2 s2 = pack2(sv[h + k], sv[h + k + 1]);
                         float e0, e1;
                         unpack2(add2(s2, pack2(kMagic, kMagic)), e0, e1);
-                        const int i0 = __reduce_max_sync(0xffffffffu, __float_as_int(e0));
-                        const int i1 = __reduce_max_sync(0xffffffffu, __float_as_int(e1));
-                        const int2 m = *reinterpret_cast<const int2*>(m_s + hb + h + k);
-                        d[h + k] = i0 - m.x;
-                        d[h + k + 1] = i1 - m.y;
-                        far = max(far, max(d[h + k], d[h + k + 1]));
-                        const f32x2 e8 = fma2(pack2(__int_as_float(i0), __int_as_float(i1)), neg,
+                        top[h + k] = __reduce_max_sync(0xffffffffu, __float_as_int(e0));
+                        top[h + k + 1] = __reduce_max_sync(0xffffffffu, __float_as_int(e1));
+                        const f32x2 e8 = fma2(pack2(__int_as_float(top[h + k]), __int_as_float(top[h + k + 1])), neg,
                                               pack2(kMagic + 8.f, kMagic + 8.f));
                         float x, y;
                         unpack2(add2(s2, e8), x, y);
@@ -1315,27 +1312,27 @@ __global__ void __launch_bounds__(P::kPaged ? kPagedThreads : kThreads, 1) decod
                 // sums waits for the reference that holds: M follows s + log2 u and the sums s alone, so that at the
                 // old one a token with a small scale can lie beyond fp32, and after a move by a large scale the sums
                 // before it can still count.
-                bool move = far > kLazy;
-                if (kPaged ? (ti.what & kFresh) && __any_sync(0xffffffffu, seen) : first && quad * 32 < valid) {
+                // (How far E lies from the reference, `d`, and what follows from it is the same for the whole warp: a lane a
+                // head, through the warp's words, instead of all heads in every lane.)
+                if (lane == 0) {
 #pragma unroll
-                    for (int h = 0; h < kHW; ++h) move |= d[h] < -kLow;
+                    for (int h = 0; h < kHW; h += 4)
+                        *reinterpret_cast<int4*>(mine + h) = make_int4(top[h], top[h + 1], top[h + 2], top[h + 3]);
                 }
+                __syncwarp();
+                int d = lane < kHW ? mine[lane] - m_s[hb + lane] : INT_MIN;
+                bool move = __reduce_max_sync(0xffffffffu, d) > kLazy;
+                if (kPaged ? (ti.what & kFresh) && __any_sync(0xffffffffu, seen) : first && quad * 32 < valid)
+                    move |= __reduce_min_sync(0xffffffffu, lane < kHW ? d : INT_MAX) < -kLow;
                 if (lane == 0) {
                     if (move) sh->moved[group][t & 1] = 1;
                     mbar_arrive(&sh->voted[group]);
                 }
-                int* const mine = red_i + quad * kNH + hb;  // this warp's words
-                if (lane == 0) {
-#pragma unroll
-                    for (int h = 0; h < kHW; h += 4)
-                        *reinterpret_cast<int4*>(mine + h) = make_int4(d[h], d[h + 1], d[h + 2], d[h + 3]);
-                }
-                __syncwarp();
-                int sf = lane < kHW ? mine[lane] : 0;
                 const bool heard =
                     __all_sync(0xffffffffu, mbar_wait(&sh->voted[group], t & 1, abort_flag, p.status, p.wait_ns));
                 ok = ok && heard;
                 if (heard && *(volatile int*)&sh->moved[group][t & 1]) {
+                    if (lane < kHW) mine[lane] = d;
                     ok = meet() && ok;
                     if (quad == 0 && lane < kHW) {
                         const int r = hb + lane;
@@ -1353,7 +1350,7 @@ __global__ void __launch_bounds__(P::kPaged ? kPagedThreads : kThreads, 1) decod
                         if (lane == 0) sh->moved[group][t & 1] = 0;
                     }
                     ok = meet() && ok;
-                    if (lane < kHW) sf -= up_s[hb + lane];
+                    if (lane < kHW) d -= up_s[hb + lane];
 #pragma unroll
                     for (int h = 0; h < kHW; h += 2) {
                         // in two factors, for sums can be 2^93 and a move more than 2^126; a_s adds a NaN, or nothing
@@ -1364,8 +1361,6 @@ __global__ void __launch_bounds__(P::kPaged ? kPagedThreads : kThreads, 1) decod
                         l2[h / 2] = fma2(pack2(f.x, f.y), 0ull,
                                          mul2(mul2(l2[h / 2], pack2(down_by(x >> 1), down_by(y >> 1))),
                                               pack2(down_by(x - (x >> 1)), down_by(y - (y >> 1)))));
-                        d[h] -= up.x;
-                        d[h + 1] -= up.y;
                     }
                     if (!first) {  // O as well, once the values before are added
                         ok = mbar_wait(&sh->o_done, (t - 1) & 1, abort_flag, p.status, p.wait_ns) && ok;
@@ -1388,10 +1383,15 @@ __global__ void __launch_bounds__(P::kPaged ? kPagedThreads : kThreads, 1) decod
                         tmem_wait_st();
                     }
                 }
+                float* const weight = reinterpret_cast<float*>(mine);
+                if (lane < kHW) weight[lane] = weight_of(d);
+                __syncwarp();
 #pragma unroll
-                for (int h = 0; h < kHW; h += 2)
-                    l2[h / 2] = fma2(mul2(pack2(sv[h], sv[h + 1]), ru2), pack2(weight_of(d[h]), weight_of(d[h + 1])),
-                                     l2[h / 2]);
+                for (int h = 0; h < kHW; h += 4) {
+                    const float4 w = *reinterpret_cast<const float4*>(weight + h);
+                    l2[h / 2] = fma2(mul2(pack2(sv[h], sv[h + 1]), ru2), pack2(w.x, w.y), l2[h / 2]);
+                    l2[h / 2 + 1] = fma2(mul2(pack2(sv[h + 2], sv[h + 3]), ru2), pack2(w.z, w.w), l2[h / 2 + 1]);
+                }
                 // the buffer of P is free once the values before are added
                 if (t > 0) ok = mbar_wait(&sh->o_done, (t - 1) & 1, abort_flag, p.status, p.wait_ns) && ok;
                 // (warps of a group leave at one place: at the end of a tile, when a wait gave up anywhere)
@@ -1414,7 +1414,7 @@ __global__ void __launch_bounds__(P::kPaged ? kPagedThreads : kThreads, 1) decod
                 }
                 if (lane < kHW) {
                     const int r = hb + lane;
-                    sf = max(sf + kBias, 0);
+                    const int sf = max(d + kBias, 0);
                     sf_s[(r & 31) * 16 + (r >> 5) * 4 + quad] = (uint8_t)sf;
                     sf_s[((r + kNH) & 31) * 16 + ((r + kNH) >> 5) * 4 + quad] = (uint8_t)sf;
                 }
