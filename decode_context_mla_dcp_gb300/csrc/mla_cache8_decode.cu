@@ -1214,25 +1214,29 @@ __global__ void __launch_bounds__(P::kPaged ? kPagedThreads : kThreads, 1) decod
             for (int h = 0; h < kHW / 2; ++h) l2[h] = 0ull;
 
             const uint32_t about = ti.what;  // (of the first tile: how the segment lies in its row)
-            for (bool first = true;; first = false, ++t) {
-                bool ok = mbar_wait(&sh->info_full[t & 3], (t >> 2) & 1, abort_flag, p.status, p.wait_ns);
-                ti = sh->info[t & 3];
-                // this thread's token's scale, in flight beside the scores
+            // Of a tile: whether this thread's token is visible, and its block's scale, which is asked for one tile ahead.
+            const auto look = [&](const TileInfo& i, uint32_t at, bool ok, bool* visible) {
+                const int valid = kPaged ? i.valid & 255 : i.valid;
                 float u = 1.f;
-                const int valid = kPaged ? ti.valid & 255 : ti.valid;
-                bool seen = tok < valid;
+                bool is = tok < valid;
                 if constexpr (kPaged) {
-                    const int at = tok >> (p.page_log2 < 7 ? p.page_log2 : 7);
-                    const int id = ok ? *(volatile int*)&sh->pages[t & 3][at] : -1;
-                    seen = seen && tok >= (ti.valid >> 8) && id >= 0;
-                    const uint32_t in_page = (ti.token + (uint32_t)tok) & ((1u << p.page_log2) - 1);
-                    if (seen)
-                        u = p.scales[ti.what & 255u][(((int64_t)id << p.page_log2) + in_page) >> p.block_log2];
+                    const int box = tok >> (p.page_log2 < 7 ? p.page_log2 : 7);
+                    const int id = ok ? *(volatile int*)&sh->pages[at & 3][box] : -1;
+                    is = is && tok >= (i.valid >> 8) && id >= 0;
+                    const uint32_t in_page = (i.token + (uint32_t)tok) & ((1u << p.page_log2) - 1);
+                    if (is) u = p.scales[i.what & 255u][(((int64_t)id << p.page_log2) + in_page) >> p.block_log2];
                 } else if (ok) {
-                    const uint32_t loc = ti.token + (uint32_t)(tok < valid ? tok : valid - 1);
-                    u = p.scales[ti.what & 255u][(int64_t)row * p.blocks + (loc >> p.block_log2)];
+                    const uint32_t loc = i.token + (uint32_t)(is ? tok : valid - 1);
+                    u = p.scales[i.what & 255u][(int64_t)row * p.blocks + (loc >> p.block_log2)];
                 }
-                ok = ok && mbar_wait(&sh->s_full, t & 1, abort_flag, p.status, p.wait_ns);
+                *visible = is;
+                return u;
+            };
+            bool seen;
+            float u = look(ti, t, true, &seen);
+            for (bool first = true;; first = false, ++t) {
+                const int valid = kPaged ? ti.valid & 255 : ti.valid;
+                bool ok = mbar_wait(&sh->s_full, t & 1, abort_flag, p.status, p.wait_ns);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
                 float sv[kHW];
@@ -1328,6 +1332,38 @@ __global__ void __launch_bounds__(P::kPaged ? kPagedThreads : kThreads, 1) decod
                     if (move) sh->moved[group][t & 1] = 1;
                     mbar_arrive(&sh->voted[group]);
                 }
+                // Beside the vote: the next tile's description, and P, whose place is free once the values before are
+                // added. (Both after it, and the scale asked for with its tile's scores: ORDER_MEASURED)
+                TileInfo next = ti;
+                float next_u = 1.f;
+                bool next_seen = false;
+                if (!(ti.what & kLast)) {
+                    const uint32_t n = t + 1;
+                    const bool is = mbar_wait(&sh->info_full[n & 3], (n >> 2) & 1, abort_flag, p.status, p.wait_ns);
+                    ok = ok && is;
+                    next = sh->info[n & 3];
+                    next_u = look(next, n, is, &next_seen);
+                }
+                if (t > 0) ok = mbar_wait(&sh->o_done, (t - 1) & 1, abort_flag, p.status, p.wait_ns) && ok;
+                {
+                    // A token's heads side by side, as they lie in this thread (the MMA reads P along the heads).
+                    uint8_t* const p_lo = S::kLoInRope ? smem + (t & 1) * S::kStage + 4 * kSlice
+                                                       : p_s + (S::kStacked ? 0 : kTile * S::kPRow);
+                    const int swz = S::kPRow == 64 ? (tok >> 1) & 3 : (tok >> 2) & 1;
+                    const int at_h = tok * S::kPRow + (((hb >> 4) ^ swz) << 4) + (hb & 15);
+                    const int lo_c = (S::kStacked ? kNH >> 4 : 0) + (hb >> 4);
+                    const int at_l = tok * S::kPRow + ((lo_c ^ swz) << 4) + (hb & 15);
+                    if constexpr (kHW == 16) {
+                        *reinterpret_cast<uint4*>(p_s + at_h) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+                        *reinterpret_cast<uint4*>(p_lo + at_l) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
+                    } else if constexpr (kHW == 8) {
+                        *reinterpret_cast<uint2*>(p_s + at_h) = make_uint2(wh[0], wh[1]);
+                        *reinterpret_cast<uint2*>(p_lo + at_l) = make_uint2(wl[0], wl[1]);
+                    } else {
+                        *reinterpret_cast<uint32_t*>(p_s + at_h) = wh[0];
+                        *reinterpret_cast<uint32_t*>(p_lo + at_l) = wl[0];
+                    }
+                }
                 const bool heard =
                     __all_sync(0xffffffffu, mbar_wait(&sh->voted[group], t & 1, abort_flag, p.status, p.wait_ns));
                 ok = ok && heard;
@@ -1362,8 +1398,7 @@ __global__ void __launch_bounds__(P::kPaged ? kPagedThreads : kThreads, 1) decod
                                          mul2(mul2(l2[h / 2], pack2(down_by(x >> 1), down_by(y >> 1))),
                                               pack2(down_by(x - (x >> 1)), down_by(y - (y >> 1)))));
                     }
-                    if (!first) {  // O as well, once the values before are added
-                        ok = mbar_wait(&sh->o_done, (t - 1) & 1, abort_flag, p.status, p.wait_ns) && ok;
+                    if (!first) {  // O as well (the values before are added)
                         __syncwarp();
                         tc_fence_after();
 #pragma unroll 1
@@ -1392,26 +1427,7 @@ __global__ void __launch_bounds__(P::kPaged ? kPagedThreads : kThreads, 1) decod
                     l2[h / 2] = fma2(mul2(pack2(sv[h], sv[h + 1]), ru2), pack2(w.x, w.y), l2[h / 2]);
                     l2[h / 2 + 1] = fma2(mul2(pack2(sv[h + 2], sv[h + 3]), ru2), pack2(w.z, w.w), l2[h / 2 + 1]);
                 }
-                // the buffer of P is free once the values before are added
-                if (t > 0) ok = mbar_wait(&sh->o_done, (t - 1) & 1, abort_flag, p.status, p.wait_ns) && ok;
                 // (warps of a group leave at one place: at the end of a tile, when a wait gave up anywhere)
-                // A token's heads side by side, as they lie in this thread (the MMA reads P along the heads).
-                uint8_t* const p_lo =
-                    S::kLoInRope ? smem + (t & 1) * S::kStage + 4 * kSlice : p_s + (S::kStacked ? 0 : kTile * S::kPRow);
-                const int swz = S::kPRow == 64 ? (tok >> 1) & 3 : (tok >> 2) & 1;
-                const int at_h = tok * S::kPRow + (((hb >> 4) ^ swz) << 4) + (hb & 15);
-                const int lo_c = (S::kStacked ? kNH >> 4 : 0) + (hb >> 4);
-                const int at_l = tok * S::kPRow + ((lo_c ^ swz) << 4) + (hb & 15);
-                if constexpr (kHW == 16) {
-                    *reinterpret_cast<uint4*>(p_s + at_h) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
-                    *reinterpret_cast<uint4*>(p_lo + at_l) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
-                } else if constexpr (kHW == 8) {
-                    *reinterpret_cast<uint2*>(p_s + at_h) = make_uint2(wh[0], wh[1]);
-                    *reinterpret_cast<uint2*>(p_lo + at_l) = make_uint2(wl[0], wl[1]);
-                } else {
-                    *reinterpret_cast<uint32_t*>(p_s + at_h) = wh[0];
-                    *reinterpret_cast<uint32_t*>(p_lo + at_l) = wl[0];
-                }
                 if (lane < kHW) {
                     const int r = hb + lane;
                     const int sf = max(d + kBias, 0);
@@ -1424,6 +1440,9 @@ __global__ void __launch_bounds__(P::kPaged ? kPagedThreads : kThreads, 1) decod
                 if (lane == 0) mbar_arrive(&sh->p_full);
                 aborted = aborted || __any_sync(0xffffffffu, !ok);
                 if (aborted || (ti.what & kLast)) break;
+                ti = next;
+                u = next_u;
+                seen = next_seen;
             }
             ++t;
             // ---- the segment's end. The next one's q comes in meanwhile (this one's scores are all done: q's place
