@@ -163,6 +163,16 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// The same without waiting (try_wait may suspend the thread for a while).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ long long global_ns() {
     long long t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -655,7 +665,8 @@ __device__ __forceinline__ void issue_scores(uint32_t ka, uint32_t qa, uint32_t 
 
 // Its values: per 128 latent dims 4 MMAs with both parts of P side by side, or 8 with one part each (the cached tile
 // then stays in the collector for the second); each slice of the tile is given back as soon as it has been used.
-template <class S>
+// (Blocks kM0 to kM1 of the four.)
+template <class S, int kM0, int kM1>
 __device__ __forceinline__ void issue_values(uint32_t ka, uint32_t pa, uint32_t tmem, uint32_t go_on,
                                              uint64_t* slice_free, uint64_t* done) {
     // ue8m0 scales, A read M-major, B N-major
@@ -670,9 +681,9 @@ __device__ __forceinline__ void issue_values(uint32_t ka, uint32_t pa, uint32_t 
         const uint64_t hi = smem_desc(pa, 16, 8 * S::kPRow, kSw), b1 = smem_desc(lo, 16, 8 * S::kPRow, kSw);
         const uint64_t both = S::kStacked ? hi : (S::kLoInRope ? smem_desc(lo, pa - lo, 8 * S::kPRow, kSw)
                                                                : smem_desc(pa, lo - pa, 8 * S::kPRow, kSw));
-        copy_scales(tmem + S::kSf + 4, pa + S::kPBytes);
+        if (kM0 == 0) copy_scales(tmem + S::kSf + 4, pa + S::kPBytes);
 #pragma unroll 1
-        for (int m = 0; m < 4; ++m) {
+        for (int m = kM0; m < kM1; ++m) {
             const uint32_t d = tmem + S::col(m);
             const uint64_t am = a0 + (uint32_t)(m * (kSlice >> 4));
             if (S::wide(m)) {
@@ -693,7 +704,7 @@ __device__ __forceinline__ void issue_values(uint32_t ka, uint32_t pa, uint32_t 
             }
             mma_commit(slice_free + m);
         }
-        mma_commit(done);
+        if (kM1 == 4) mma_commit(done);
     }
     __syncwarp();
 }
@@ -1006,8 +1017,10 @@ __global__ void __launch_bounds__(P::kPaged ? kPagedThreads : kThreads, 1) decod
             tile = p.row_mode ? 0 : -kChange;
         }
         if (lane == 0 && my_slice == 0) {
-            if (ok) {  // no more tiles: a tile of no tokens
-                if (t >= 4) ok = mbar_wait(&sh->kv_free[t & 1][3], ((t >> 1) + 1) & 1, abort_flag, p.status, p.wait_ns);
+            // no more tiles: a tile of no tokens. (A description's place is free as soon as any slice of the tile three
+            // before has been used: the softmax warps are then done with the one before that. The MMA warp looks for the
+            // next tile while it has half of the values before to issue, so that no description waits for those.)
+            if (ok) {
                 sh->info[t & 3] = {0u, 0, 0u, 0};
                 mbar_arrive(&sh->info_full[t & 3]);
             }
@@ -1017,44 +1030,60 @@ __global__ void __launch_bounds__(P::kPaged ? kPagedThreads : kThreads, 1) decod
         // The whole warp walks the loop on values that are the same in every lane (so that descriptors live in
         // uniform registers, and an MMA costs one instruction), and one elected lane issues.
         uint32_t t = 0, segs = 0;
-        bool more = true;
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), base = smem_u32(smem);
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, p.wait_ns));
         };
         bool began = false;  // tile t - 1 is the first of a segment
-        auto values = [&](uint32_t v) {
-            if (!wait(&sh->p_full, v & 1)) return false;
-            tc_fence_after();
-            issue_values<S>(base + (v & 1) * S::kStage, base + 2 * S::kStage + S::kQBytes, tm, began ? 0u : 1u,
-                            sh->kv_free[v & 1], &sh->o_done);
+        // What tile n is: the first of a segment, one at all.
+        auto describe = [&](uint32_t n, bool* first, bool* is) {
+            if (!wait(&sh->info_full[n & 3], (n >> 2) & 1)) return false;
+            *first = (__shfl_sync(0xffffffffu, sh->info[n & 3].what, 0) & kFirst) != 0;
+            *is = __shfl_sync(0xffffffffu, sh->info[n & 3].valid, 0) != 0;
             return true;
         };
-        while (more) {
-            if (!wait(&sh->info_full[t & 3], (t >> 2) & 1)) break;
-            const bool first = (__shfl_sync(0xffffffffu, sh->info[t & 3].what, 0) & kFirst) != 0;
-            more = __shfl_sync(0xffffffffu, sh->info[t & 3].valid, 0) != 0;
+        // The values of tile v, and `beside`, what the next tile is: with pages and blocks of 16 or 32 heads that is asked
+        // for between their halves, while the first one is at work. (64 ragged rows x 16K in pages of 64: 16 heads 63 us,
+        // 66 with it behind; 32 heads 64 and 70; where the tiles come from L2, 64 rows behind two prefixes of 16K alone, 102
+        // and 98; 8 rows x 4096 14.0 and 13.7. 128 heads 132 us, and 124 behind: there the second half comes too late.
+        // Rows one after the other gain nothing, 64 and 63.)
+        auto values = [&](uint32_t v, auto beside) {
+            if (!wait(&sh->p_full, v & 1)) return false;
+            tc_fence_after();
+            constexpr int kHalf = kPaged && S::kStacked ? 2 : 4;
+            const uint32_t ka = base + (v & 1) * S::kStage, pa = base + 2 * S::kStage + S::kQBytes;
+            issue_values<S, 0, kHalf>(ka, pa, tm, began ? 0u : 1u, sh->kv_free[v & 1], &sh->o_done);
+            const bool ok = beside();
+            if (kHalf < 4) issue_values<S, kHalf, 4>(ka, pa, tm, began ? 0u : 1u, sh->kv_free[v & 1], &sh->o_done);
+            return ok;
+        };
+        bool first = true, more = false, going = describe(0, &first, &more);
+        while (going) {
             // (a new segment's q comes after the sums of the last one, and they after its values)
             const bool turn = t > 0 && (first || !more);
-            if (turn && !values(t - 1)) break;
-            if (more) {
-                if (t > 0 && !wait(&sh->s_free, (t - 1) & 1)) break;
-                if (first && !wait(&sh->q_full, segs++ & 1)) break;
-                // (whether the next slice is there is asked before this one's MMAs are issued)
-                uint64_t* const full = sh->kv_full[t & 1];
-                const uint32_t par = (t >> 1) & 1;
-                bool ok = true, there = mbar_try_wait(full, par);
+            if (turn && !values(t - 1, [] { return true; })) break;
+            if (!more) break;
+            if (t > 0 && !wait(&sh->s_free, (t - 1) & 1)) break;
+            if (first && !wait(&sh->q_full, segs++ & 1)) break;
+            // (whether the next slice is there is asked before this one's MMAs are issued)
+            uint64_t* const full = sh->kv_full[t & 1];
+            const uint32_t par = (t >> 1) & 1;
+            bool ok = true, there = mbar_test(full, par);
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    if (!__all_sync(0xffffffffu, there)) ok = wait(full + s, par);
-                    if (!ok) break;
-                    if (s < 3) there = mbar_try_wait(full + s + 1, par);
-                    tc_fence_after();
-                    issue_scores<S>(base + (t & 1) * S::kStage, base + 2 * S::kStage, tm, kIdS, s, &sh->s_full);
-                }
-                if (!ok || (t > 0 && !turn && !values(t - 1))) break;
+            for (int s = 0; s < 4; ++s) {
+                if (!__all_sync(0xffffffffu, there)) ok = wait(full + s, par);
+                if (!ok) break;
+                if (s < 3) there = mbar_test(full + s + 1, par);
+                tc_fence_after();
+                issue_scores<S>(base + (t & 1) * S::kStage, base + 2 * S::kStage, tm, kIdS, s, &sh->s_full);
             }
+            if (!ok) break;
+            bool next_first = false, next_more = false;
+            const auto next = [&] { return describe(t + 1, &next_first, &next_more); };
+            going = t > 0 && !turn ? values(t - 1, next) : next();
             began = first;
+            first = next_first;
+            more = next_more;
             ++t;
         }
         if (elect_one()) mma_commit(&sh->drained);
@@ -1333,7 +1362,8 @@ __global__ void __launch_bounds__(P::kPaged ? kPagedThreads : kThreads, 1) decod
                     mbar_arrive(&sh->voted[group]);
                 }
                 // Beside the vote: the next tile's description, and P, whose place is free once the values before are
-                // added. (Both after it, and the scale asked for with its tile's scores: ORDER_MEASURED)
+                // added. (Both behind it, and the scale asked for with its tile's scores: 64 ragged rows x
+                // 16K x 128 heads in pages of 64 125.2 us, 123.6 so.)
                 TileInfo next = ti;
                 float next_u = 1.f;
                 bool next_seen = false;
