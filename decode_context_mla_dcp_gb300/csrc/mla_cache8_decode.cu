@@ -1,5 +1,6 @@
-// Single-token MLA attention over the 8-bit latent cache, sm_103a. What it
-// computes is stated in include/dcp_mla_cache8.h.
+// Single-token MLA attention over the 8-bit latent cache, in rows or in pages,
+// sm_103a. What it computes is stated in include/dcp_mla_cache8.h and
+// include/dcp_mla_pages.h.
 //
 // The mathematics. A tile is 128 cached tokens; the cached e4m3 codes go to the
 // tensor cores as they lie in the cache. With c_t = scale * log2(e) * (scale of
@@ -39,19 +40,36 @@
 // of 64 heads takes 4,230 cycles at the 1.94 GHz that the call runs at. Its MMAs
 // alone take 2,958 (1,393 the scores, N = 128; 1,565 the values: N = 64 costs 55
 // to 59 cycles and N = 128 77, so both parts of P go into one MMA where TMEM has room
-// for them, the first 128 dims). Shared memory's port is what they wait for: the
-// operands take 2,150 of its cycles a tile, the tile itself 580, the softmax some
-// 900. Two tiles, q and P fill shared memory, S, O and the scales TMEM (456 of 512
-// columns), so there is no third stage and one CTA a multiprocessor.
-//   measured, 128 heads: 64 ragged rows of up to 16K tokens 142 to 151 us with their
-//   lengths, 280 to 286 us for 10^6 tokens (146.3 us, 1.00 PFLOP/s as the operator
-//   counts them, twice that on the tensor cores, over three sets of lengths; 148 for
-//   seconds on end, at the power limit); 8 rows x 4096 tokens 23.5 us, of which 16.4
+// for them, the first 128 dims). Shared memory's port serves them all: the operands
+// take 2,150 of its cycles a tile, the tile itself 580, the softmax some 900. Two
+// tiles, q and P fill shared memory, S, O and the scales TMEM (456 of 512 columns), so
+// there is no third stage and one CTA a multiprocessor. By the clock of the MMA warp a
+// tile's turn is 930 cycles to issue the scores and 1,460 the values; the others are
+// waits, each some 100 to 300: for P, for slices, for the scores' place, for what comes.
+//   measured, 128 heads: 64 ragged rows of up to 16K tokens 140 to 149 us with their
+//   lengths, 276 to 282 us for 10^6 tokens; 8 rows x 4096 tokens 23.2 us, of which 16
 //   are the main kernel (4 tiles a CTA between 10,000 cycles to begin and 6,000 to
-//   end) and 6 the join; 16 heads, 200 tokens: 8.1 to 8.4 us. One shard of 8 held,
+//   end) and 6 the join; 16 heads, 200 tokens: 8.5 to 8.9 us. One shard of 8 held,
 //   8 rows x 4096 of its tokens: 24.0 us.
-// With 16 and 32 heads 64 ragged rows x 16K take 67 and 71 us against 45 of their
-// bytes; where the rest goes has not been measured.
+// With 16 and 32 heads 64 ragged rows x 16K take 63 and 65 us against 45 of their
+// bytes: some 16 us are the beginning, the end and the join, and the MMA warp's turn
+// (46 cycles an MMA whatever its N, and the waits between) is near the rest.
+//
+// Pages. A tile is 128 tokens at a multiple of 128, from 1 to 4 pages: a TMA box a page
+// into the tile's place (the swizzle goes by address, so that the tile is the same), and
+// zeros where there is no page. The loading warps bring the tile's page numbers with its
+// description; a token without a page is masked like one that is not visible. Three
+// loading warps and one L2 request a page make this faster than rows: the 64 ragged
+// rows x 16K x 128 heads 124 us in pages of 64 (the same lengths in rows 130); with one
+// loading warp and a request a slice 150.
+//
+// Groups. Rows that share a prefix have their heads side by side in blocks of 64 over
+// the prefix's tiles, so that 16 heads a row cost a quarter of the tiles' turns; what a
+// row has behind the prefix, whole tiles of which are the prefix's, is a line of its own,
+// and the join weighs both. 64 rows of 16 heads behind two prefixes of 16K with up to
+// 1,024 tokens of their own: 55.6 us, 101 without groups; floor 20 (the products at the
+// bf16 rate). Bound as above, at 2.0 us a tile: 2,464 tiles and changes of line are 16 a
+// CTA, 33 us of it, and the beginning, the end and the join are the rest.
 //
 // Rounding to fewer bits: q's and P's parts as above. log2 u, exp2 and the division by u
 // are the hardware's (two units of the last place, 2^-22, two units), far below P's
@@ -713,7 +731,7 @@ __device__ __forceinline__ void issue_values(uint32_t ka, uint32_t pa, uint32_t 
 // quarter of the heads, a warp of it 32 of the tile's tokens (its TMEM lanes), a
 // thread one token. One warp walks the tiles and loads them (TMA, two stages, each
 // slice as soon as the values of the tile before last have used it, and the tile
-// after next into L2), one issues the MMAs in a fixed turn: a tile's scores, slice
+// after next into L2; with pages three warps share the slices), one issues the MMAs in a fixed turn: a tile's scores, slice
 // by slice, then the values of the tile before, so that scores and softmax of one
 // tile run beside the values of another. (Polling for whichever was ready first
 // was slower, 170 against 164 us at 64 ragged rows x 16K; so was a slice of values
@@ -1571,6 +1589,7 @@ __global__ void __launch_bounds__(P::kPaged ? kPagedThreads : kThreads, 1) decod
 // ---- the rows that were split ---------------------------------------------------------
 
 struct JoinParams {
+    static constexpr bool kPaged = false;
     const float* part;
     const float* part_lse;
     const int2* row_info;
@@ -1581,6 +1600,7 @@ struct JoinParams {
     float lse_scale;
 };
 struct PagedJoinParams : JoinParams {
+    static constexpr bool kPaged = true;
     const int* lead;     // [B], or NULL: no groups
     int B, ctas;
 };
@@ -1593,7 +1613,7 @@ struct PagedJoinParams : JoinParams {
 // Rows with a prefix have its segments first, those of the group's set of heads that has this head, then their own.
 template <int kWarps, class Q>
 __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 256) join_kernel(const __grid_constant__ Q p) {
-    constexpr bool kPaged = sizeof(Q) > sizeof(JoinParams);
+    constexpr bool kPaged = Q::kPaged;
     __shared__ float acc_s[kWarps > 1 ? kWarps : 1][kDv];
     __shared__ float sum_s[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

@@ -10,7 +10,8 @@
  * The tables, per shard, the same for all layers.
  *   tables [B, M] int32, contiguous: entry (b, i) is the page of tokens
  *          i * page .. of row b on this shard. An entry outside [0, P) is no
- *          page, and a row's pages are its entries before the first such one.
+ *          page. A row's pages are its entries before the first such one; the
+ *          append, the read-back and the attention look at each entry by itself.
  *   refs   [P] int32: how many rows hold a page; 0 is a free page. A program
  *          that wants to keep a page without a row adds 1 of its own.
  *
