@@ -553,14 +553,13 @@ GROUPS = [
 ]
 
 
-@pytest.mark.parametrize("case", GROUPS, ids=lambda c: f"H{c[0]}cp{c[1]}i{c[2]}b{c[3]}p{c[4]}g{len(c[5])}n{sum(c[5])}s{c[6][0]}")
-@pytest.mark.parametrize("dk", [576, 512])
+@pytest.mark.parametrize("case,dk", [(c, 576) for c in GROUPS] + [(c, 512) for c in GROUPS if c[0] in (16, 40, 100)],
+                         ids=lambda c: c if isinstance(c, int) else
+                         f"H{c[0]}cp{c[1]}i{c[2]}b{c[3]}p{c[4]}g{len(c[5])}n{sum(c[5])}s{c[6][0]}")
 def test_groups(case, dk):
     """Rows behind shared prefixes; among them rows of nothing of their own, of no token, and shorter than the prefix
     (with pages of their own)."""
     H, cp, il, block, page, counts, shared, most = case
-    if dk == 512 and H not in (16, 40, 100):
-        pytest.skip("one width is enough")
     B = sum(counts)
     r = random.Random(B + H)
     lens, first, alone = [], [], []
@@ -813,3 +812,154 @@ def test_paged_calls_of_no_rows():
     for kw in ({}, dict(groups=groups, shared=shared)):
         out, lse = dcp.mla_cache8_decode(q, [kv], [sc], none, SCALE, tables=tb, **kw)
         assert out.shape == (0, 16, 512) and lse.shape == (0, 16)
+
+
+def grouped_batch(g, B, H, prefix, own, page=64, block=1, dk=576):
+    """One group behind `prefix` positions (whole pages), with room for groups to be used: pool, tables, q, lengths."""
+    M = -(-(prefix + max(own)) // page)
+    P = B * M
+    kv, sc = make_pool(g, P, page, dk, block)
+    tb = roomy(torch.randperm(P, generator=g, device=DEV).view(B, M).int(), 1, page)
+    tb[1:, :prefix // page] = tb[0, :prefix // page]
+    return kv, sc, tb, randn(g, B, H, dk).bfloat16(), ints([prefix + n for n in own])
+
+
+def test_groups_take_what_a_call_may_bring():
+    """A workspace of just the size, full of NaN; outputs given; q with odd strides; another stream; bits that stay."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(11)
+    B, H = 7, 24
+    kv, sc, tb, q, lens = grouped_batch(g, B, H, 640, [1, 0, 130, 200, 127, 128, 300], block=16)
+    groups, shared = dcp.mla_cache8_groups([B], [640])
+    kw = dict(block=16, tables=[tb], groups=groups, shared=shared)
+    want = dcp.mla_cache8_decode(q, [kv], [sc], lens, SCALE, **kw)
+    check_paged(q, [kv], [sc], [tb], lens, 1, 1, 16, 0, 0, *want)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    size = dcp.dcp_mla_cache8_decode_paged_workspace_bytes(1, B, H, 64, tb.shape[1], 0, 0, True, sms)
+    assert size > dcp.dcp_mla_cache8_decode_paged_workspace_bytes(1, B, H, 64, tb.shape[1], 0, 0, False, sms)
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device=DEV)
+    wide = torch.zeros((B, H + 1, 600), dtype=torch.bfloat16, device=DEV)
+    odd = wide[:, 1:, 2:578]  # heads and rows on 4-byte boundaries only
+    odd.copy_(q)
+    out, lse = torch.full((B, H, 512), 7.0, dtype=torch.bfloat16, device=DEV), torch.full((B, H), 7.0, device=DEV)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    got = dcp.mla_cache8_decode(odd, [kv], [sc], lens, SCALE, out=out, lse=lse, workspace=ws, stream=stream, **kw)
+    stream.synchronize()
+    assert got[0] is out and got[1] is lse
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    with pytest.raises(dcp.DcpError):
+        dcp.mla_cache8_decode(q, [kv], [sc], lens, SCALE, workspace=ws[:size - 256], **kw)
+
+
+@pytest.mark.parametrize("loud", [(1.0, 30.0), (30.0, 1.0), (0.01, 30.0), (60.0, 60.0)])
+def test_groups_whose_prefix_and_rows_lie_far_apart(loud):
+    """Scores of the prefix and of the rows' own tokens of very different sizes: the join's weights."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(12)
+    B, H = 9, 16
+    kv, sc, tb, q, lens = grouped_batch(g, B, H, 1280, [300, 5, 0, 129, 64, 1, 200, 256, 17])
+    common = tb[0, :20].long()
+    sc *= loud[1]
+    sc[common] *= loud[0] / loud[1]
+    groups, shared = dcp.mla_cache8_groups([B], [1280])
+    out, lse = dcp.mla_cache8_decode(q, [kv], [sc], lens, SCALE, tables=[tb], groups=groups, shared=shared)
+    check_paged(q, [kv], [sc], [tb], lens, 1, 1, 1, 0, 0, out, lse)
+
+
+def test_groups_keep_nan_to_its_row_and_head():
+    """Heads of several rows stand in one block: a NaN or an infinity in one row's q stays there; one in a token of the
+    prefix reaches every row, one behind it its own row alone."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(13)
+    B, H = 6, 16
+    kv, sc, tb, q, lens = grouped_batch(g, B, H, 640, [100, 200, 1, 50, 300, 128])
+    groups, shared = dcp.mla_cache8_groups([B], [640])
+    kw = dict(tables=[tb], groups=groups, shared=shared)
+    want = dcp.mla_cache8_decode(q, [kv], [sc], lens, SCALE, **kw)
+    bad = q.clone()
+    bad[1, 3, 17], bad[4, 15, 570] = float("nan"), float("inf")
+    out, lse = dcp.mla_cache8_decode(bad, [kv], [sc], lens, SCALE, **kw)
+    hit = torch.zeros((B, H), dtype=torch.bool, device=DEV)
+    hit[1, 3] = hit[4, 15] = True
+    assert out[hit].isnan().all() and lse[hit].isnan().all()
+    assert torch.equal(out[~hit], want[0][~hit]) and torch.equal(lse[~hit], want[1][~hit])
+    own = sc.clone()
+    own[tb[3, 10].long(), 5] = float("nan")  # position 645 of row 3
+    out, lse = dcp.mla_cache8_decode(q, [kv], [own], lens, SCALE, **kw)
+    rows = torch.arange(B, device=DEV) == 3
+    assert out[rows].isnan().all() and torch.equal(out[~rows], want[0][~rows]) and torch.equal(lse[~rows], want[1][~rows])
+    all_ = sc.clone()
+    all_[tb[0, 2].long(), 5] = float("nan")  # position 133 of the prefix
+    out, lse = dcp.mla_cache8_decode(q, [kv], [all_], lens, SCALE, **kw)
+    assert out.isnan().all() and lse.isnan().all()
+
+
+def test_two_graphs_over_one_workspace_in_turn():
+    """Two captured calls that share a workspace, replayed one after the other, in either order."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(14)
+    B, H = 5, 16
+    kv, sc, tb, q, lens = grouped_batch(g, B, H, 640, [100, 200, 1, 50, 300])
+    groups, shared = dcp.mla_cache8_groups([B], [640])
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    ws = torch.empty((dcp.dcp_mla_cache8_decode_paged_workspace_bytes(1, B, H, 64, tb.shape[1], 0, 0, True, sms),),
+                     dtype=torch.uint8, device=DEV)
+    calls = [(q, lens), (randn(g, B, H, 576).bfloat16(), lens - 30)]
+    want = [dcp.mla_cache8_decode(a, [kv], [sc], n, SCALE, tables=[tb], groups=groups, shared=shared) for a, n in calls]
+    graphs, got = [], []
+    for a, n in calls:
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got.append(dcp.mla_cache8_decode(a, [kv], [sc], n, SCALE, tables=[tb], groups=groups, shared=shared,
+                                             workspace=ws))
+        graphs.append(graph)
+    for order in ((0, 1), (1, 0), (0, 0, 1, 1)):
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for (o, l), (wo, wl) in zip(got, want):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_paged_decode_random(seed):
+    """Random sizes: heads, shards, blocks, pages, windows or groups, pages that are missing."""
+    r = random.Random(seed)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    H, dk = r.choice([1, 7, 16, 20, 32, 48, 64, 100, 128]), r.choice([576, 576, 512])
+    cp, page = r.choice([1, 1, 2, 5]), r.choice([32, 64, 128, 512])
+    il, block = r.choice([1, 16, 24]) if cp > 1 else 1, r.choice([1, 8, 32])
+    B, M = r.choice([1, 3, 10, 40]), r.randint(1, 6)
+    most = min(M * page, 900) * cp
+    lens = [r.choice([0, 1, r.randint(0, most), r.randint(0, most), most + 50]) for _ in range(B)]
+    P = B * M + 1
+    kv, sc = map(list, zip(*[make_pool(g, P, page, dk, block) for _ in range(cp)]))
+    tb = [torch.randperm(P, generator=g, device=DEV)[:B * M].view(B, M).int() for _ in range(cp)]
+    kw = {}
+    window = sinks = 0
+    if r.random() < 0.4:
+        window, sinks = r.randint(1, most), r.choice([0, 3, 200])
+        kw = dict(window=window, sinks=sinks)
+    else:
+        counts = []
+        while sum(counts) < B:
+            counts.append(min(r.randint(1, 6), B - sum(counts)))
+        common = [r.randint(0, most) // (page * cp * il) * (page * cp * il) for _ in counts]
+        groups, shared = dcp.mla_cache8_groups(counts, common)
+        tb = [roomy(t, cp, page) for t in tb]
+        for b in range(B):
+            first, s = int(groups[b, 0]), int(shared[b])
+            if lens[b] >= s:
+                for j in range(cp):
+                    n = ref.share(s, cp, j, il) // page
+                    tb[j][b, :n] = tb[j][first, :n]
+        kw = dict(groups=groups, shared=shared)
+    if r.random() < 0.3:  # (the same entry in every row, so that prefixes stay common)
+        for t in tb:
+            t[:, r.randrange(M)] = r.choice([-1, P, 1 << 30])
+    q = randn(g, B, H, dk).bfloat16()
+    out, lse = dcp.mla_cache8_decode(q, kv, sc, ints(lens), SCALE, block=block, interleave=il, tables=tb, **kw)
+    check_paged(q, kv, sc, tb, ints(lens), cp, il, block, window, sinks, out, lse)
