@@ -1623,8 +1623,11 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 256) join_kernel(co
     pdl_wait();
     pdl_launch_dependents();
     if (unit >= p.units) return;
+    // the places of its segments, in heads: the first prefix one, then from `pre_at` on; the first own one, then from
+    // `own_at` on (with `step` each)
+    const int step = p.head_blocks * p.block_heads;
     int2 row, pre = {0, 0};
-    int pre_line = 0, pre_block = 0, pre_head = 0;
+    int pre_first = 0, pre_at = 0, own_first = 0, own_at = 0;
     bool grouped = false;
     if constexpr (kPaged) {
         grouped = p.lead != nullptr;
@@ -1633,12 +1636,14 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 256) join_kernel(co
         if (lead < 0) {
             if (row.y == 1) return;
         } else {
-            const int r = (b - lead) * p.H + h, chunk = r / p.block_heads;
-            pre_head = r - chunk * p.block_heads;
-            pre_line = lead + chunk / p.head_blocks;
-            pre_block = chunk % p.head_blocks;
-            pre = p.row_info[pre_line];
+            const int r = (b - lead) * p.H + h, chunk = r / p.block_heads, head = r - chunk * p.block_heads;
+            const int set = chunk / p.head_blocks, block = chunk - set * p.head_blocks;
+            pre = p.row_info[lead + set];
+            pre_first = (p.ctas + (lead + set) * p.head_blocks + block) * p.block_heads + head;
+            pre_at = (pre.x * p.head_blocks + block) * p.block_heads + head;
         }
+        own_first = (p.ctas + (p.B + b) * p.head_blocks + hblk) * p.block_heads + hh;
+        own_at = ((row.x - pre.y) * p.head_blocks + hblk) * p.block_heads + hh;
     } else {
         row = p.row_info[b];
         if (row.y == 1) return;
@@ -1657,12 +1662,8 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 256) join_kernel(co
     const auto place = [&](int i) {
         if constexpr (kPaged) {
             if (grouped) {
-                const bool common = i < pre.y;
-                const int at = common ? i : i - pre.y, line = common ? pre_line : p.B + b;
-                const int block = common ? pre_block : hblk, first = common ? pre.x : row.x;
-                const int64_t slot = at == 0 ? p.ctas + (int64_t)line * p.head_blocks + block
-                                             : (int64_t)(first + at) * p.head_blocks + block;
-                return slot * p.block_heads + (common ? pre_head : hh);
+                if (i < pre.y) return (int64_t)(i == 0 ? pre_first : pre_at + i * step);
+                return (int64_t)(i == pre.y ? own_first : own_at + i * step);
             }
         }
         return (((int64_t)(row.x + i) * p.head_blocks + hblk) * 2 + (i == 0 ? 1 : 0)) * p.block_heads + hh;
