@@ -3,7 +3,8 @@
  * positions, the quantising append, the read-back, and single-token attention
  * over the cache (with an optional sliding window and a few first tokens that
  * stay visible). They chain as a serving step does: rotate the queries, append
- * the new tokens, attend.
+ * the new tokens, attend. (dcp_mla_pages.h has the same cache in pages that rows
+ * share.)
  *
  * The cache. A row (sequence) holds at most T tokens a shard. A token is Dk
  * e4m3 values, 512 latent dims (key and value) and, with Dk = 576, 64 rotary
