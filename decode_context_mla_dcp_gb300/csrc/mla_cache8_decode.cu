@@ -37,7 +37,7 @@
 // What bounds it. A CTA has up to 64 heads: 2 x 64 x (576 + 512) x 2 operations a
 // token (q's and P's two parts) against 576 bytes, so with 64 heads and more it is
 // the tensor cores and what feeds them, with 16 the cache's way from DRAM. A tile
-// of 64 heads takes 4,230 cycles at the 1.94 GHz that the call runs at. Its MMAs
+// of 64 heads takes some 4,150 cycles at the 1.94 GHz that the call runs at, with pages 3,900. Its MMAs
 // alone take 2,958 (1,393 the scores, N = 128; 1,565 the values: N = 64 costs 55
 // to 59 cycles and N = 128 77, so both parts of P go into one MMA where TMEM has room
 // for them, the first 128 dims). Shared memory's port serves them all: the operands
@@ -1940,10 +1940,16 @@ int run_paged(const DecodeBase& base, const Pages& pages, const void* const* kv,
 // the lengths are on the device, and a call with uneven ones wants the split.) Shards that are not held count too: one
 // of 8 with 256 tokens a row is split, 16.2 us for 8 rows and 41.9 for 200, where the same tokens alone take 12.0 and
 // 33.1.
-bool whole_rows(int cp, int64_t T, int64_t window, int64_t sinks) {
+int64_t most_tiles(int cp, int64_t T, int64_t window, int64_t sinks) {
     const int64_t seen = window > 0 && window < T ? window : T, first = sinks < T ? sinks : T;
-    const int64_t most = (seen + kTile - 1) / kTile + (window > 0 ? (first + kTile - 1) / kTile : 0);
-    return cp * most <= 2;
+    return cp * ((seen + kTile - 1) / kTile + (window > 0 ? (first + kTile - 1) / kTile : 0));
+}
+bool whole_rows(int cp, int64_t T, int64_t window, int64_t sinks) { return most_tiles(cp, T, window, sinks) <= 2; }
+// With pages three tiles neither: it saves a workspace and a second launch as well. (Pages of 64, whole and split. Three
+// tiles: 16 heads, 1 row 10.6 and 10.4 us, 128 rows 11.6 and 13.7; 128 heads, 8 rows 14.6 and 16.6. Four tiles: 16 heads, 8
+// rows 12.2 and 11.1, 32 rows 12.5 and 11.8; 128 heads, 8 rows 16.6 and 17.0.)
+bool whole_paged_rows(int cp, int64_t T, int64_t window, int64_t sinks) {
+    return most_tiles(cp, T, window, sinks) <= 3;
 }
 
 int page_log2_of(int page) {
@@ -1979,9 +1985,10 @@ extern "C" int64_t dcp_mla_cache8_decode_paged_workspace_bytes(int cp, int64_t B
                                                                int num_sms) {
     if (page_log2_of(page) < 0 || M < 1 || M > 0x7fffffff || M * page > 0x7fffffff) return -1;
     const int64_t bytes = dcp_mla_cache8_decode_workspace_bytes(cp, B, H, M * page, window, sinks, num_sms);
-    return bytes < 0 || B == 0 || !uses_groups(grouped != 0, cp, B, H, M * page)
-               ? bytes
-               : workspace_of(B, H, group_block(B, H), true, num_sms).bytes;
+    if (bytes < 0 || B == 0) return bytes;
+    if (uses_groups(grouped != 0, cp, B, H, M * page))
+        return workspace_of(B, H, group_block(B, H), true, num_sms).bytes;
+    return whole_paged_rows(cp, M * page, window, sinks) ? 0 : bytes;
 }
 
 // Both forms. T: what a row has room for; pages: NULL for rows one after the other.
@@ -2031,7 +2038,9 @@ static int decode_call(const void* q, int64_t q_row, int64_t q_head, const void*
     }
     const int heads = grouped ? group_block(B, H) : head_block(H);
     const Workspace ws = workspace_of(B, H, heads, grouped, sms);
-    p.row_mode = !grouped && whole_rows(cp, T, window, sinks) ? 1 : 0;
+    p.row_mode = grouped            ? 0
+                 : pages != nullptr ? whole_paged_rows(cp, T, window, sinks)
+                                    : whole_rows(cp, T, window, sinks);
     if (!p.row_mode && (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < ws.bytes))
         return DCP_MLA_CACHE8_ERR_WORKSPACE;
     if (T == 0 || (pages != nullptr && pages->P == 0)) p.held = 0;  // nothing is cached: every row is empty

@@ -125,7 +125,9 @@ def test_paged_decode_workspace_bytes():
     ws = dcp.dcp_mla_cache8_decode_paged_workspace_bytes
     rows = dcp.dcp_mla_cache8_decode_workspace_bytes
     assert ws(1, 8, 16, 64, 100, 0, 0, False, 152) == rows(1, 8, 16, 6400, 0, 0, 152) > 0
-    assert ws(1, 8, 16, 64, 4, 0, 0, False, 152) == 0  # two tiles a row: no row is split
+    # up to three tiles a row: no row is split
+    assert ws(1, 8, 16, 64, 4, 0, 0, False, 152) == ws(1, 8, 16, 64, 6, 0, 0, False, 152) == 0
+    assert ws(1, 8, 16, 64, 7, 0, 0, False, 152) > 0 == ws(3, 8, 16, 64, 2, 0, 0, False, 152)
     # with groups a place for each row's own part and for each set of a group's heads, in blocks of 64
     assert ws(1, 8, 16, 64, 256, 0, 0, True, 152) >= (152 + 16) * 64 * 513 * 4
     assert ws(1, 2, 16, 64, 1024, 0, 0, True, 152) < ws(1, 4, 16, 64, 1024, 0, 0, True, 152)  # blocks of 32, of 64
