@@ -37,7 +37,7 @@
 // What bounds it. A CTA has up to 64 heads: 2 x 64 x (576 + 512) x 2 operations a
 // token (q's and P's two parts) against 576 bytes, so with 64 heads and more it is
 // the tensor cores and what feeds them, with 16 the cache's way from DRAM. A tile
-// of 64 heads takes some 4,150 cycles at the 1.94 GHz that the call runs at, with pages 3,900. Its MMAs
+// of 64 heads takes some 3,800 cycles at the 1.94 GHz that the call runs at. Its MMAs
 // alone take 2,958 (1,393 the scores, N = 128; 1,565 the values: N = 64 costs 55
 // to 59 cycles and N = 128 77, so both parts of P go into one MMA where TMEM has room
 // for them, the first 128 dims). Shared memory's port serves them all: the operands
@@ -46,22 +46,21 @@
 // there is no third stage and one CTA a multiprocessor. By the clock of the MMA warp a
 // tile's turn is 930 cycles to issue the scores and 1,460 the values; the others are
 // waits, each some 100 to 300: for P, for slices, for the scores' place, for what comes.
-//   measured, 128 heads: 64 ragged rows of up to 16K tokens 140 to 149 us with their
-//   lengths, 276 to 282 us for 10^6 tokens; 8 rows x 4096 tokens 23.2 us, of which 16
+//   measured, 128 heads: 64 ragged rows of up to 16K tokens 128 to 137 us with their
+//   lengths, 252 to 258 us for 10^6 tokens; 8 rows x 4096 tokens 22.9 us, of which 16
 //   are the main kernel (4 tiles a CTA between 10,000 cycles to begin and 6,000 to
-//   end) and 6 the join; 16 heads, 200 tokens: 8.5 to 8.9 us. One shard of 8 held,
-//   8 rows x 4096 of its tokens: 24.0 us.
-// With 16 and 32 heads 64 ragged rows x 16K take 63 and 65 us against 45 of their
+//   end) and 6 the join; 16 heads, 200 tokens: 8.3 us. One shard of 8 held, 8 rows x
+//   4096 of its tokens: 24 us.
+// With 16 and 32 heads 64 ragged rows x 16K take 63 and 66 us against 45 of their
 // bytes: some 16 us are the beginning, the end and the join, and the MMA warp's turn
 // (46 cycles an MMA whatever its N, and the waits between) is near the rest.
 //
 // Pages. A tile is 128 tokens at a multiple of 128, from 1 to 4 pages: a TMA box a page
 // into the tile's place (the swizzle goes by address, so that the tile is the same), and
 // zeros where there is no page. The loading warps bring the tile's page numbers with its
-// description; a token without a page is masked like one that is not visible. Three
-// loading warps and one L2 request a page make this faster than rows: the 64 ragged
-// rows x 16K x 128 heads 124 us in pages of 64 (the same lengths in rows 130); with one
-// loading warp and a request a slice 150.
+// description; a token without a page is masked like one that is not visible. One bulk
+// request a page brings the tile after next to L2. 64 ragged rows x 16K x 128 heads take
+// 124 us in pages of 64 and 123 in pages of 128, the same lengths in rows 119.5.
 //
 // Groups. Rows that share a prefix have their heads side by side in blocks of 64 over
 // the prefix's tiles, so that 16 heads a row cost a quarter of the tiles' turns; what a
@@ -96,12 +95,11 @@ constexpr int kTile = 128;                 // tokens of a tile: the MMA's M
 constexpr int kSlice = kTile * 128;        // bytes of a 128-dim slice of a tile
 constexpr int kSoftWarps = 16, kSoftThreads = 32 * kSoftWarps;
 constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
-constexpr int kThreads = kSoftThreads + 64;
-// With pages three warps load, the first slice, the next two, and the last with the rope slice (the second and third warp
-// stand behind the MMA warp): a request takes its warp some 150 cycles, a tile has up to 20 of them, and a slice's place
-// is free only shortly before its next tokens are wanted. (A fourth would leave 80 registers a thread. 64 ragged rows x 16K
-// x 128 heads, pages of 32, 64, 128 tokens: 157, 147 and 141 us with one, 132, 129 and 128 with three)
-constexpr int kPagedThreads = kThreads + 64;
+// Three warps load: the first slice, the next two, and the last with the rope slice (the second and third warp stand behind
+// the MMA warp). A request takes its warp some 150 cycles, a tile has 5 of them, in pages up to 20, and a slice's place is
+// free only shortly before its next tokens are wanted. (A fourth would leave 80 registers a thread. 64 ragged rows x 16K x
+// 128 heads: rows 130.5 us with one, 119.5 with three; in pages of 32, 64, 128 tokens 157, 147 and 141, and 132, 129, 128.)
+constexpr int kThreads = kSoftThreads + 128;
 constexpr int kCpMax = DCP_MLA_CACHE8_CP_MAX;
 constexpr int64_t kMaxInterleave = 1 << 24;
 constexpr long long kWaitLimitNs = 2000000000LL;  // every wait gives up after this,
@@ -729,9 +727,9 @@ __device__ __forceinline__ void issue_values(uint32_t ka, uint32_t pa, uint32_t 
 
 // Roles. Sixteen warps do the softmax, in four groups of four: a group has a
 // quarter of the heads, a warp of it 32 of the tile's tokens (its TMEM lanes), a
-// thread one token. One warp walks the tiles and loads them (TMA, two stages, each
+// thread one token. Three warps walk the tiles and load them (TMA, two stages, each
 // slice as soon as the values of the tile before last have used it, and the tile
-// after next into L2; with pages three warps share the slices), one issues the MMAs in a fixed turn: a tile's scores, slice
+// after next into L2), one issues the MMAs in a fixed turn: a tile's scores, slice
 // by slice, then the values of the tile before, so that scores and softmax of one
 // tile run beside the values of another. (Polling for whichever was ready first
 // was slower, 170 against 164 us at 64 ragged rows x 16K; so was a slice of values
@@ -742,7 +740,7 @@ __device__ __forceinline__ void issue_values(uint32_t ka, uint32_t pa, uint32_t 
 // the second kernel), each head block for itself; a call whose rows have at most two
 // tiles gives whole rows to a CTA and needs no second kernel.
 template <int kDk, int kNH, class P>
-__global__ void __launch_bounds__(P::kPaged ? kPagedThreads : kThreads, 1) decode_kernel(const __grid_constant__ P p) {
+__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ P p) {
     using S = Shape<kDk, kNH>;
     constexpr bool kPaged = P::kPaged;
     constexpr int kHW = S::kHW, kChange = kNH / 32;
@@ -761,7 +759,7 @@ __global__ void __launch_bounds__(P::kPaged ? kPagedThreads : kThreads, 1) decod
     volatile int* const abort_flag = &sh->abort;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const bool loads = warp == kLoadWarp || (kPaged && warp > kMmaWarp);
+    const bool loads = warp == kLoadWarp || warp > kMmaWarp;
     const int hblk = blockIdx.x % p.head_blocks, range = blockIdx.x / p.head_blocks;
     const int h0 = hblk * kNH;
     const int nh = p.H - h0 < kNH ? p.H - h0 : kNH;
@@ -882,9 +880,8 @@ __global__ void __launch_bounds__(P::kPaged ? kPagedThreads : kThreads, 1) decod
     const uint32_t tmem = sh->tmem;
 
     if (loads) {
-        // ---- loads (the warp walks together, lane 0 issues; with pages this warp's slice only, a lane a page)
-        const int my_slice = kPaged && warp > kMmaWarp ? 2 * (warp - kMmaWarp) - 1 : 0;
-        const int end_slice = kPaged ? (my_slice == 1 ? 3 : my_slice + 1) : 4;
+        // ---- loads (a warp walks together over all tiles and loads its slices, lane 0, or a lane a page)
+        const int my_slice = warp > kMmaWarp ? 2 * (warp - kMmaWarp) - 1 : 0, end_slice = my_slice == 1 ? 3 : my_slice + 1;
         if (!p.row_mode && lines > 32) {
             row = lines;
             if (g < g_end) {  // (a range of no tiles has found no row)
@@ -1023,7 +1020,8 @@ __global__ void __launch_bounds__(P::kPaged ? kPagedThreads : kThreads, 1) decod
                         }
                     }
                     if (kPaged) continue;
-                    if (i + 1 < n && t >= 1 && lane == 0) {  // the next tile's stage is still in use: to L2 meanwhile
+                    // the next tile's stage is still in use: to L2 meanwhile
+                    if (my_slice == 3 && i + 1 < n && t >= 1 && lane == 0) {
 #pragma unroll 1
                         for (int a = 0; a < 4; ++a) tma_prefetch_3d(&p.tm_latent[c.j], a * 128, (int)c.token(), row);
                         if constexpr (S::kHasRope) tma_prefetch_3d(&p.tm_rope[c.j], kDv, (int)c.token(), row);
@@ -1844,7 +1842,7 @@ cudaError_t launch_decode(const P& p, unsigned flags, cudaStream_t st) {
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.ranges * p.head_blocks));
-    cfg.blockDim = dim3(P::kPaged ? kPagedThreads : kThreads);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
