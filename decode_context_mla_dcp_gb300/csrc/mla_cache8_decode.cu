@@ -49,9 +49,9 @@
 //   measured, 128 heads: 64 ragged rows of up to 16K tokens 128 to 137 us with their
 //   lengths, 252 to 258 us for 10^6 tokens; 8 rows x 4096 tokens 22.9 us, of which 16
 //   are the main kernel (4 tiles a CTA between 10,000 cycles to begin and 6,000 to
-//   end) and 6 the join; 16 heads, 200 tokens: 8.3 us. One shard of 8 held, 8 rows x
+//   end) and 6 the join; 16 heads, 200 tokens: 8.1 to 8.5 us. One shard of 8 held, 8 rows x
 //   4096 of its tokens: 24 us.
-// With 16 and 32 heads 64 ragged rows x 16K take 63 and 66 us against 45 of their
+// With 16 and 32 heads 64 ragged rows x 16K take 60 and 62 us against 45 of their
 // bytes: some 16 us are the beginning, the end and the join, and the MMA warp's turn
 // (46 cycles an MMA whatever its N, and the waits between) is near the rest.
 //
@@ -1058,15 +1058,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             *is = __shfl_sync(0xffffffffu, sh->info[n & 3].valid, 0) != 0;
             return true;
         };
-        // The values of tile v, and `beside`, what the next tile is: with pages and blocks of 16 or 32 heads that is asked
-        // for between their halves, while the first one is at work. (64 ragged rows x 16K in pages of 64: 16 heads 63 us,
-        // 66 with it behind; 32 heads 64 and 70; where the tiles come from L2, 64 rows behind two prefixes of 16K alone, 102
-        // and 98; 8 rows x 4096 14.0 and 13.7. 128 heads 132 us, and 124 behind: there the second half comes too late.
-        // Rows one after the other gain nothing, 64 and 63.)
+        // The values of tile v, and `beside`, what the next tile is: with blocks of 16 or 32 heads that is asked for between
+        // their halves, while the first one is at work. (64 ragged rows x 16K: 16 heads 59.7 us, 62.5 with it behind; 32
+        // heads 62 and 66; in pages of 64 63 and 66, 64 and 70; where the tiles come from L2, 64 rows behind two prefixes
+        // of 16K alone, 102 and 98; 8 rows x 4096 x 16 heads 13.3 and 13.2. 128 heads in pages 132 us, and 124 behind:
+        // there the second half comes too late.)
         auto values = [&](uint32_t v, auto beside) {
             if (!wait(&sh->p_full, v & 1)) return false;
             tc_fence_after();
-            constexpr int kHalf = kPaged && S::kStacked ? 2 : 4;
+            constexpr int kHalf = S::kStacked ? 2 : 4;
             const uint32_t ka = base + (v & 1) * S::kStage, pa = base + 2 * S::kStage + S::kQBytes;
             issue_values<S, 0, kHalf>(ka, pa, tm, began ? 0u : 1u, sh->kv_free[v & 1], &sh->o_done);
             const bool ok = beside();
