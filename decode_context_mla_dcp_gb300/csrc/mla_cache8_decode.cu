@@ -948,7 +948,22 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 c.seek(p, line, tile);
                 const bool alone = !kPaged || (line.base == 0 && !(line.source & kPrefix));  // (nothing joins it)
                 const uint32_t about = (tile == 0 ? kStarts : 0u) | (tile == 0 && n == n_row && alone ? kWhole : 0u);
-                const int table_row = line_row(p, row, line.source);
+                int table_row = line_row(p, row, line.source);
+                if constexpr (kPaged) {
+                    // a prefix is read through the first of the group's rows that has all of it (a shorter one may have
+                    // been cut back, or have ended)
+                    if (line.source & kPrefix) {
+                        const int rows = p.groups[row].y, first = table_row;
+                        for (int k = 0; k < rows; k += 32) {
+                            const uint32_t has = __ballot_sync(
+                                0xffffffffu, k + lane < rows && row_length(p, first + k + lane) >= line.length);
+                            if (has) {
+                                table_row = first + k + __ffs(has) - 1;
+                                break;
+                            }
+                        }
+                    }
+                }
                 int id = page_at(c, table_row);
                 bool fresh = true;
                 for (int i = 0; i < n; ++i, ++t) {

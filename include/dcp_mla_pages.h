@@ -128,9 +128,10 @@ int dcp_mla_cache8_read_paged(const void* const* kv_ptrs, const float* const* sc
  *
  * Rows that share a prefix. groups (or NULL) and shared say that consecutive rows
  * have their first positions in the same pages: row b belongs to the groups[b][1]
- * rows from row groups[b][0] on, and positions p < shared[b] of all of them are those
- * of row groups[b][0], whose table alone is used for them. Every row of a group has
- * the same entries in groups and shared. A row whose length is below shared takes no
+ * rows from row groups[b][0] on, and positions p < shared[b] of all of them are the
+ * same; they are looked up in the table of the first of these rows that is at least
+ * shared[b] long. Every row of a group has the same entries in groups and shared. A row
+ * whose length is below shared (one that has ended, say, with a length of 0) takes no
  * part and is looked up in its own table. The result is that of the call without
  * groups (but for the order of sums); what is saved is work: tiles of the prefix are
  * multiplied with several rows' heads at a time where a row's heads do not fill the
