@@ -114,6 +114,8 @@ def mla_cache8_pages_update(tables, refs, parents, keeps, wants, *, page: int, c
         raise ValueError("tables need a column and refs an entry")
     if page < _b.DCP_MLA_PAGE_MIN or page > _b.DCP_MLA_PAGE_MAX or page & (page - 1):
         raise ValueError(f"page must be a power of two in [{_b.DCP_MLA_PAGE_MIN}, {_b.DCP_MLA_PAGE_MAX}]")
+    if M * page >= 1 << 31:
+        raise ValueError("M * page must be below 2^31")
     if not 1 <= cp <= _b.DCP_MLA_CACHE8_CP_MAX or not 0 <= shard < cp or not 1 <= interleave <= 1 << 24:
         raise ValueError("cp must be in [1, 16], shard in [0, cp) and interleave in [1, 2^24]")
     rows = [_c._ints(name, t, B, index) for name, t in (("parents", parents), ("keeps", keeps), ("wants", wants))]

@@ -166,13 +166,13 @@ __global__ void __launch_bounds__(kThreads) update_kernel(const __grid_constant_
     }
     cluster.sync();
     // ---- what each row takes over, and the counts of pages that change hands
-    const int64_t room = min((int64_t)p.M << p.page_log2, (int64_t)0x7fffffff);
+    const int room = p.M << p.page_log2;
     const int page_up = (1 << p.page_log2) - 1;
     for (int b = row0 + warp; b < row1; b += kWarps) {
         const int from = p.parents[b], keeps = p.keeps[b], wants = p.wants[b];
         const bool some = from >= 0 && from < p.B, self = from == b;
-        const int keep = some ? (int)min(room, (int64_t)share_of(keeps, p.cp, p.shard, p.interleave)) : 0;
-        const int want = (int)min(room, (int64_t)share_of(wants, p.cp, p.shard, p.interleave));
+        const int keep = some ? min(room, share_of(keeps, p.cp, p.shard, p.interleave)) : 0;
+        const int want = min(room, share_of(wants, p.cp, p.shard, p.interleave));
         const int n_keep = (keep >> p.page_log2) + ((keep & page_up) != 0);
         const int n_want = (want >> p.page_log2) + ((want & page_up) != 0);
         const int edge = want > keep && (keep & page_up) ? keep >> p.page_log2 : -1;
@@ -501,8 +501,10 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 int64_t round_up(int64_t x) { return (x + 255) / 256 * 256; }
+// (a row's room, in tokens of the smallest page, is below 2^31: loops over its entries count in 32 bits)
 bool sizes_ok(int64_t B, int64_t M, int64_t P) {
-    return B >= 0 && B <= 65535 && M >= 1 && M < 0x7fffffff && B * (M + 1) <= 0x7fffffff && P >= 1 && P <= 0x7fffffff;
+    return B >= 0 && B <= 65535 && M >= 1 && M <= 0x7fffffff / DCP_MLA_PAGE_MIN && B * (M + 1) <= 0x7fffffff && P >= 1 &&
+           P <= 0x7fffffff;
 }
 int page_log2_of(int page) {
     for (int k = 0; (1 << k) <= DCP_MLA_PAGE_MAX; ++k)
@@ -616,6 +618,7 @@ extern "C" int dcp_mla_pages_update(const int32_t* tables, const int32_t* refs, 
     if (!sizes_ok(B, M, P)) return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
     const int lg = page_log2_of(page);
     if (lg < 0) return DCP_MLA_CACHE8_ERR_BAD_PAGE;
+    if (M * page > 0x7fffffff) return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
     if (cp < 1 || cp > DCP_MLA_CACHE8_CP_MAX || shard < 0 || shard >= cp || interleave < 1 || interleave > 1 << 24)
         return DCP_MLA_CACHE8_ERR_BAD_CP;
     if (refs == nullptr || refs_out == nullptr || missing == nullptr ||

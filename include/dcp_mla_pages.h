@@ -64,7 +64,8 @@ enum {
  *            aligned (NULL where that is 0: out of place, with up to 16,384 rows and
  *            262,144 pages); its contents do not matter. Calls that share one are
  *            ordered.
- *   shapes   0 <= B <= 65535, 1 <= M, B * (M + 1) < 2^31, 1 <= P < 2^31, 0 <= shard < cp
+ *   shapes   0 <= B <= 65535, 1 <= M, M * page < 2^31 (here and in the calls without a
+ *            page: M < 2^26), B * (M + 1) < 2^31, 1 <= P < 2^31, 0 <= shard < cp
  */
 int dcp_mla_pages_update(const int32_t* tables, const int32_t* refs, const int32_t* parents, const int32_t* keeps,
                          const int32_t* wants, int64_t B, int64_t M, int64_t P, int page, int cp, int shard,
