@@ -11,6 +11,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "dcp_lse_reduce.h"
 #include "dcp_mla_pages.h"
 
@@ -600,6 +602,21 @@ int check_alias(const int32_t* tables, const int32_t* refs, const int32_t* table
            overlap(tables_out, entries * 4, refs_out, P * 4);
 }
 
+struct Span {
+    const void* at;
+    int64_t bytes;
+};
+// Whether one of `written` overlaps another one, or one of `others`.
+bool meet(std::initializer_list<Span> written, std::initializer_list<Span> others) {
+    for (const Span* w = written.begin(); w != written.end(); ++w) {
+        for (const Span* v = written.begin(); v != w; ++v)
+            if (overlap(w->at, w->bytes, v->at, v->bytes)) return true;
+        for (const Span& o : others)
+            if (overlap(w->at, w->bytes, o.at, o.bytes)) return true;
+    }
+    return false;
+}
+
 }  // namespace
 
 extern "C" int64_t dcp_mla_pages_update_workspace_bytes(int64_t B, int64_t M, int64_t P, int in_place) {
@@ -633,6 +650,12 @@ extern "C" int dcp_mla_pages_update(const int32_t* tables, const int32_t* refs, 
     const UpdateSpace ws = update_space(B, M, P, in_place);
     if (ws.bytes > 0 && (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < ws.bytes))
         return DCP_MLA_CACHE8_ERR_WORKSPACE;
+    // (parents and positions are read to the end of the call, and address what is written)
+    const Span t = {tables, B * M * 4}, r = {refs, P * 4}, to = {tables_out, B * M * 4}, ro = {refs_out, P * 4},
+               parent = {parents, B * 4}, keep = {keeps, B * 4}, want = {wants, B * 4};
+    if (meet({{copies, B * 8}, {missing, 4}, {workspace, ws.bytes}}, {t, r, to, ro, parent, keep, want}) ||
+        meet({to, ro}, {parent, keep, want}))
+        return DCP_MLA_CACHE8_ERR_ALIAS;
     uint8_t* const w = static_cast<uint8_t*>(workspace);
     UpdateParams p;
     p.tables = tables;
@@ -678,6 +701,9 @@ extern "C" int dcp_mla_pages_compact(const int32_t* tables, const int32_t* refs,
     const CompactSpace ws = compact_space(P);
     if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < ws.bytes)
         return DCP_MLA_CACHE8_ERR_WORKSPACE;
+    if (meet({{copies, P / 2 * 8}, {workspace, ws.bytes}},
+             {{tables, B * M * 4}, {refs, P * 4}, {tables_out, B * M * 4}, {refs_out, P * 4}}))
+        return DCP_MLA_CACHE8_ERR_ALIAS;
     uint8_t* const w = static_cast<uint8_t*>(workspace);
     CompactParams p;
     p.tables = tables;

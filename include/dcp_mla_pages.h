@@ -60,6 +60,8 @@ enum {
  *            that overlap neither
  *   copies   [B, 2] int32, 8-byte aligned; missing: one int32
  *   parents, keeps, wants  [B] int32 (negative positions: 0)
+ *   Nothing else that is written (copies, missing, the workspace) overlaps anything
+ *   that the call takes, and tables_out and refs_out do not overlap these three.
  *   workspace at least dcp_mla_pages_update_workspace_bytes(...) bytes, 256-byte
  *            aligned (NULL where that is 0: out of place, with up to 16,384 rows and
  *            262,144 pages); its contents do not matter. Calls that share one are
@@ -82,7 +84,7 @@ int64_t dcp_mla_pages_update_workspace_bytes(int64_t B, int64_t M, int64_t P, in
  * the last. Entries of tables and refs are changed to match; an entry that is no
  * page, or a page that does not move, stays as it is. Nothing is copied here.
  *   copies   [P / 2, 2] int32, 8-byte aligned (more than P / 2 pages never move)
- *   tables_out, refs_out, workspace, shapes as above (B = 0 is allowed)
+ *   tables_out, refs_out, workspace, overlaps, shapes as above (B = 0 is allowed)
  */
 int dcp_mla_pages_compact(const int32_t* tables, const int32_t* refs, int64_t B, int64_t M, int64_t P,
                           int32_t* tables_out, int32_t* refs_out, int32_t* copies, void* workspace,

@@ -23,3 +23,27 @@ def test_the_wrapper_refuses_rows_of_2_31_tokens():
     with pytest.raises(ValueError, match="2\\^31"):
         dcp.mla_cache8_pages_update(i32(1, 1 << 19), i32(8), i32(1), i32(1), i32(1), page=4096)
     assert dcp.dcp_mla_pages_update_workspace_bytes(1, (1 << 26) - 1, 16, False) == 0
+
+
+# the step of the tables and the compaction with every buffer in a place of its own
+APART = dict(tables=A, refs=2 * A, parents=3 * A, keeps=4 * A, wants=5 * A, tables_out=6 * A, refs_out=7 * A,
+             copies=8 * A, missing=9 * A, workspace=10 * A)
+
+
+@pytest.mark.parametrize("change", [
+    dict(copies=A), dict(copies=A + 120), dict(copies=6 * A - 8), dict(copies=2 * A + 56), dict(copies=7 * A),
+    dict(copies=3 * A), dict(copies=4 * A + 8), dict(copies=5 * A), dict(missing=A), dict(missing=7 * A + 60),
+    dict(missing=4 * A), dict(missing=8 * A + 28), dict(tables_out=3 * A), dict(tables_out=4 * A - 124),
+    dict(refs_out=5 * A), dict(tables_out=A, refs_out=2 * A, copies=A + 64),
+    dict(tables_out=A, refs_out=2 * A, wants=A + 4), dict(tables_out=A, refs_out=2 * A, workspace=4 * A),
+    dict(tables_out=A, refs_out=2 * A, workspace=8 * A)])
+def test_an_update_that_would_write_over_what_it_takes(change):
+    refused(ALIAS, dcp.dcp_mla_pages_update, {**UPDATE, **APART}, **change)
+
+
+@pytest.mark.parametrize("change", [
+    dict(copies=A), dict(copies=2 * A + 56), dict(copies=6 * A + 120), dict(copies=7 * A), dict(copies=10 * A),
+    dict(workspace=A), dict(workspace=2 * A), dict(workspace=6 * A), dict(workspace=7 * A)])
+def test_a_compaction_that_would_write_over_what_it_takes(change):
+    apart = {k: APART[k] for k in ("tables", "refs", "tables_out", "refs_out", "copies", "workspace")}
+    refused(ALIAS, dcp.dcp_mla_pages_compact, {**COMPACT, **apart}, **change)
