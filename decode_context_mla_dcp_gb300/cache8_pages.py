@@ -173,7 +173,7 @@ def mla_cache8_pages_copy(caches, scales, copies, *, stream=None) -> None:
     """Copy pages, codes and scales, inside each of several pools (the layers).
 
     caches: up to 128 pools [P, page, Dk] of one shape, scales: as many [P, page /
-    block]. copies: int32 [n, 2], (from, to) as mla_cache8_pages_update and
+    block], of which no two overlap. copies: int32 [n, 2], (from, to) as mla_cache8_pages_update and
     mla_cache8_pages_compact give them; a pair with an entry outside [0, P) is passed
     over. No page may be the target of two pairs, or of one and the source of
     another."""

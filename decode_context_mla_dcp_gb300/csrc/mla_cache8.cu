@@ -1144,7 +1144,7 @@ extern "C" const char* dcp_mla_cache8_strerror(int status) {
         case DCP_MLA_CACHE8_ERR_TENSOR_MAP: return "a TMA tensor map of a cache could not be encoded";
         case DCP_MLA_CACHE8_ERR_BAD_PAGE: return "page must be a power of two in [32, 4096] and a multiple of block";
         case DCP_MLA_CACHE8_ERR_ALIAS:
-            return "outputs overlap inputs other than in place, or one pool is given twice";
+            return "outputs overlap inputs other than in place, or two pools overlap";
         default: return dcp_lse_reduce_strerror(status);
     }
 }

@@ -757,8 +757,10 @@ extern "C" int dcp_mla_pages_copy(void* const* kv_ptrs, float* const* scale_ptrs
     for (int j = 0; j < pools; ++j) {
         if (kv_ptrs[j] == nullptr || scale_ptrs[j] == nullptr) return DCP_MLA_CACHE8_ERR_NULL_POINTER;
         if (!aligned(kv_ptrs[j], 16) || !aligned(scale_ptrs[j], 4)) return DCP_MLA_CACHE8_ERR_MISALIGNED;
-        for (int k = 0; k < j; ++k)  // (a pool that came twice would be written by two CTAs)
-            if (kv_ptrs[j] == kv_ptrs[k] || scale_ptrs[j] == scale_ptrs[k]) return DCP_MLA_CACHE8_ERR_ALIAS;
+        for (int k = 0; k < j; ++k)  // (what two pools have in common would be written by two CTAs)
+            if (overlap(kv_ptrs[j], P * page * Dk, kv_ptrs[k], P * page * Dk) ||
+                overlap(scale_ptrs[j], P * (page / block) * 4, scale_ptrs[k], P * (page / block) * 4))
+                return DCP_MLA_CACHE8_ERR_ALIAS;
         p.kv[j] = static_cast<uint8_t*>(kv_ptrs[j]);
         p.scales[j] = scale_ptrs[j];
     }

@@ -99,8 +99,9 @@ int64_t dcp_mla_pages_compact_workspace_bytes(int64_t P);
  * pair with an entry outside [0, P) is passed over. No page may be the dst of two
  * pairs, or both dst and src.
  *   kv_ptrs, scale_ptrs  [pools] host arrays, pools <= DCP_MLA_PAGES_POOLS_MAX; no
- *            pool twice
- *   shapes   0 <= n < 2^31, 1 <= P < 2^31, Dk 512 or 576
+ *            two pools overlap
+ *   shapes   n >= 0, n times the parts of 36 KiB of a page below 2^31, 1 <= P < 2^31,
+ *            Dk 512 or 576
  */
 int dcp_mla_pages_copy(void* const* kv_ptrs, float* const* scale_ptrs, int pools, int64_t P, int page, int Dk,
                        int block, const int32_t* copies, int64_t n, void* stream);

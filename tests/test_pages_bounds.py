@@ -47,3 +47,17 @@ def test_an_update_that_would_write_over_what_it_takes(change):
 def test_a_compaction_that_would_write_over_what_it_takes(change):
     apart = {k: APART[k] for k in ("tables", "refs", "tables_out", "refs_out", "copies", "workspace")}
     refused(ALIAS, dcp.dcp_mla_pages_compact, {**COMPACT, **apart}, **change)
+
+
+POOL, ROOM = 16 * 64 * 576, 16 * 4 * 4  # bytes of COPY's pool and of its scales
+
+
+@pytest.mark.parametrize("kv,scales", [
+    ([A, A + 64 * 576], [4 * A, 5 * A]), ([A + POOL - 16, A], [4 * A, 5 * A]), ([A, 2 * A], [4 * A, 4 * A + 16]),
+    ([A, 2 * A], [4 * A + ROOM - 4, 4 * A]), ([A, 2 * A, 3 * A, A + POOL // 2 // 16 * 16], [5 * A, 6 * A, 7 * A, 8 * A])])
+def test_pools_that_overlap(kv, scales):
+    refused(ALIAS, dcp.dcp_mla_pages_copy, COPY, pools=len(kv), kv_ptrs=kv, scale_ptrs=scales)
+
+
+def test_pools_side_by_side():
+    dcp.dcp_mla_pages_copy(**{**COPY, "n": 0, "pools": 2, "kv_ptrs": [A, A + POOL], "scale_ptrs": [4 * A + ROOM, 4 * A]})
