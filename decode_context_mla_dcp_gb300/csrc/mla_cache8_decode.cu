@@ -1948,6 +1948,9 @@ int run_paged(const DecodeBase& base, const Pages& pages, const void* const* kv,
                                heads, flags, st);
 }
 
+// Every count of tiles stays in 32 bits, for `lines` lines of T tokens a shard (with groups there are two a row).
+bool few_tiles(int cp, int64_t lines, int64_t T) { return lines * cp * (T / kTile + 2) <= 1 << 30; }
+
 // Rows of at most two tiles are not worth splitting: a join costs as much. (128 heads x 256 tokens: 12.6 us whole, 15.3
 // split for 8 rows, 34 and 41 for 200. Of four tiles: 16.6 whole and 15.7 split for 8 rows x 512, 17.8 and 20.4 for 64;
 // the lengths are on the device, and a call with uneven ones wants the split.) Shards that are not held count too: one
@@ -1977,9 +1980,11 @@ int page_log2_of(int page) {
 // of 64 heads, places and a join cost some 5 us more than 16 heads a row alone. (16 heads, one group, with groups and
 // without: 8 rows x 2,048 tokens, 144 tiles, 18.8 us and 12.9; 16 x 8,192, 1,056 tiles, 24.0 and 22.8; 8 x 32,768, 2,064
 // tiles, 31.2 and 33.5; 32 x 32,768, 8,256 tiles, 51.4 and 93.1. 40 heads, 16 x 8,192: 30.4 and 31.4.) What is known here is
-// what rows have room for, not their lengths. Each row takes places for partial results, so that there is a limit.
+// what rows have room for, not their lengths. Each row takes places for partial results, so that there is a limit; and
+// where the tiles of twice as many lines could not be counted, a call goes without.
 bool uses_groups(bool grouped, int cp, int64_t B, int H, int64_t T) {
-    return grouped && B >= 2 && B <= 2048 && H % 64 != 0 && B * cp * ((T + kTile - 1) / kTile) >= 1024;
+    return grouped && B >= 2 && B <= 2048 && H % 64 != 0 && B * cp * ((T + kTile - 1) / kTile) >= 1024 &&
+           few_tiles(cp, 2 * B, T);
 }
 int group_block(int64_t B, int H) { return head_block(B * H < 64 ? (int)(B * H) : 64); }
 
@@ -1988,7 +1993,7 @@ int group_block(int64_t B, int H) { return head_block(B * H < 64 ? (int)(B * H) 
 extern "C" int64_t dcp_mla_cache8_decode_workspace_bytes(int cp, int64_t B, int H, int64_t T, int64_t window,
                                                          int64_t sinks, int num_sms) {
     if (cp < 1 || cp > kCpMax || B < 0 || B > 65535 || H < 1 || H > 1024 || T < 0 || T > 0x7fffffff || window < 0 ||
-        sinks < 0 || num_sms < 1 || num_sms > 4096)
+        sinks < 0 || num_sms < 1 || num_sms > 4096 || !few_tiles(cp, B, T))
         return -1;
     return B == 0 || whole_rows(cp, T, window, sinks) ? 0 : workspace_of(B, H, head_block(H), false, num_sms).bytes;
 }
@@ -2039,10 +2044,8 @@ static int decode_call(const void* q, int64_t q_row, int64_t q_head, const void*
         }
     }
     if (some < 0) return DCP_MLA_CACHE8_ERR_NULL_POINTER;
-    // every tile count stays in 32 bits
+    if (!few_tiles(cp, B, T)) return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
     const bool grouped = pages != nullptr && uses_groups(pages->groups != nullptr, cp, B, H, T);
-    const int64_t shard_tiles = T / kTile + 2;
-    if (B * cp * shard_tiles * (grouped ? 2 : 1) > 0x40000000) return DCP_MLA_CACHE8_ERR_BAD_SHAPE;
     if (B == 0) return 0;
     const int sms = multiprocessors();
     if (sms < 1) {

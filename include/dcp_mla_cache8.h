@@ -161,7 +161,7 @@ int dcp_mla_cache8_read(const void* const* kv_ptrs, const float* const* scale_pt
  *            DCP_MLA_FLAG_TEST_STALL (32; see dcp_mla_decode.h: the first tile
  *            of each CTA never counts as landed, waits give up after 20 ms)
  *   shapes   0 <= B <= 65535, 1 <= H <= 1024, Dk 512 or 576, Dv 512,
- *            0 <= T < 2^31, window and sinks >= 0
+ *            0 <= T < 2^31, B * cp * (T / 128 + 2) <= 2^30, window and sinks >= 0
  * Numerics. The codes go to the tensor cores as they are. q is split into two
  * e4m3 parts at a power-of-two scale per head, which holds every value above
  * 2^-9 of the head's largest exactly (and the others to 2^-16 of it).

@@ -140,15 +140,15 @@ int dcp_mla_cache8_read_paged(const void* const* kv_ptrs, const float* const* sc
  * groups (but for the order of sums); what is saved is work: tiles of the prefix are
  * multiplied with several rows' heads at a time where a row's heads do not fill the
  * kernel's blocks of 64. With H a multiple of 64, more than 2048 rows, or tables with
- * room for fewer than 1024 tiles of 128 tokens in all (B * cp * M * page / 128), groups
- * make no difference; with long tables and short prefixes they cost some microseconds
- * (16 heads: they pay from about 2000 tiles of rows times prefix on). Groups do not go
- * together with a window.
+ * room for fewer than 1024 tiles of 128 tokens in all (B * cp * M * page / 128) or for
+ * more than 2^29 (B * cp * (M * page / 128 + 2)), groups make no difference; with long
+ * tables and short prefixes they cost some microseconds (16 heads: they pay from about
+ * 2000 tiles of rows times prefix on). Groups do not go together with a window.
  *   groups   [B, 2] int32, 8-byte aligned; shared [B] int32 (below 1: nothing is
  *            shared). Entries that break these rules give undefined results in the
  *            rows concerned.
  *   workspace at least dcp_mla_cache8_decode_paged_workspace_bytes(...) bytes
- *   shapes   as for both
+ *   shapes   as for both, T being M * page
  */
 int dcp_mla_cache8_decode_paged(const void* q, int64_t q_row, int64_t q_head, const void* const* kv_ptrs,
                                 const float* const* scale_ptrs, const int32_t* const* table_ptrs,

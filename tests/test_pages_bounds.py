@@ -4,7 +4,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import decode_context_mla_dcp_gb300 as dcp
-from .test_pages_refusals import A, ALIAS, COMPACT, COPY, DECODE, SHAPE, UPDATE, built, refused  # noqa: F401
+from .test_pages_refusals import A, ALIAS, COMPACT, COPY, DECODE, SHAPE, UPDATE, WS, built, refused  # noqa: F401
 
 
 @pytest.mark.parametrize("M,page", [(1 << 26, 32), (1 << 19, 4096), (1 << 25, 64), ((1 << 31) - 2, 32),
@@ -61,3 +61,32 @@ def test_pools_that_overlap(kv, scales):
 
 def test_pools_side_by_side():
     dcp.dcp_mla_pages_copy(**{**COPY, "n": 0, "pools": 2, "kv_ptrs": [A, A + POOL], "scale_ptrs": [4 * A + ROOM, 4 * A]})
+
+
+SHARDS = lambda cp: dict(cp=cp, kv_ptrs=[A] * cp, scale_ptrs=[A] * cp, table_ptrs=[A] * cp)
+TILES = [(2048, 16, 1 << 15), (40, 1, (1 << 25) - 1), (65, 1, 1 << 24)]  # rows, shards, pages of 64
+
+
+@pytest.mark.parametrize("B,cp,M", TILES)
+def test_groups_with_room_for_more_tiles_than_can_be_counted_twice(B, cp, M):
+    """Groups make no difference there: what a call without them takes, one with them takes too."""
+    ws = dcp.dcp_mla_cache8_decode_paged_workspace_bytes
+    size = ws(cp, B, 16, 64, M, 0, 0, False, 152)
+    assert size == ws(cp, B, 16, 64, M, 0, 0, True, 152) > 0
+    assert ws(cp, B // 2, 16, 64, M, 0, 0, True, 152) > size  # (where they are used there are more places)
+    for kw in ({}, dict(groups=A, shared=A)):
+        with pytest.raises(dcp.DcpError) as e:
+            dcp.dcp_mla_cache8_decode_paged(**{**DECODE, **SHARDS(cp), **kw, "B": B, "M": M, "workspace": None})
+        assert e.value.status in (WS, -10)  # (without a GPU the workspace is not come to)
+
+
+@pytest.mark.parametrize("B,cp,M", [(2 * B + 2, cp, M) for B, cp, M in TILES if 2 * B * M < 1 << 31] + [(63, 16, 1 << 22)])
+def test_tiles_that_cannot_be_counted(B, cp, M):
+    refused(SHAPE, dcp.dcp_mla_cache8_decode_paged, DECODE, **SHARDS(cp), B=B, M=M)
+    for grouped in (False, True):
+        assert dcp.dcp_mla_cache8_decode_paged_workspace_bytes(cp, B, 16, 64, M, 0, 0, grouped, 152) == -1
+    assert dcp.dcp_mla_cache8_decode_workspace_bytes(cp, B, 16, M * 64, 0, 0, 152) == -1
+    rows = dict(q=A, q_row=576 * 16, q_head=576, kv_ptrs=[A] * cp, scale_ptrs=[A] * cp, seq_lens=A, cp=cp, B=B, H=16,
+                Dk=576, Dv=512, T=M * 64, block=1, interleave=1, window=0, sinks=0, scale=1.0, lse_base_e=True,
+                workspace=A, workspace_bytes=1 << 40, out=A, lse=A, stream=0)
+    refused(SHAPE, dcp.dcp_mla_cache8_decode, rows)
