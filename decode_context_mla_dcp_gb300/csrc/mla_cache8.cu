@@ -1145,6 +1145,8 @@ extern "C" const char* dcp_mla_cache8_strerror(int status) {
         case DCP_MLA_CACHE8_ERR_BAD_PAGE: return "page must be a power of two in [32, 4096] and a multiple of block";
         case DCP_MLA_CACHE8_ERR_ALIAS:
             return "outputs overlap inputs other than in place, or two pools overlap";
+        case DCP_MLA_CACHE8_ERR_CLUSTER:
+            return "the device or context cannot hold a cluster of 16 blocks, a multiprocessor each";
         default: return dcp_lse_reduce_strerror(status);
     }
 }

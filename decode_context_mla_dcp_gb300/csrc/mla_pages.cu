@@ -558,14 +558,15 @@ CompactSpace compact_space(int64_t P) {
 
 // CTAs of a step of the tables: one where a row a warp and few entries and pages a thread are, else a cluster of 16. (4
 // beams, 256 pages: 6.5 us with one, 7.5 with 8; 256 rows, 16,384 pages: 9.8 with 8, 9.3 with 16; 512 rows x 512, 120,000
-// pages: 21.4 with 8, 16.0 with 16.)
+// pages: 21.4 with 8, 16.0 with 16.) A cluster of 16 takes 16 whole multiprocessors of one group of them; where a device or
+// a context has none that large, the call says so (a cluster of 8 would need a larger workspace than callers bring).
 int cluster_of(int64_t rows, int64_t entries, int64_t P) {
     return rows <= kWarps && entries <= 8 * kThreads && P <= 8 * kThreads ? 1 : kClusterMax;
 }
 
 template <bool kShared>
 int launch_update(const UpdateParams& p, int ctas, int shared_bytes, cudaStream_t st) {
-    static int configured[64] = {};
+    static int configured[64] = {}, holds[64] = {};  // (holds: a cluster of kClusterMax can be resident)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && (dev < 0 || dev >= 64 || !__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE))) {
@@ -587,7 +588,16 @@ int launch_update(const UpdateParams& p, int ctas, int shared_bytes, cudaStream_
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, update_kernel<kShared>, p);
+        if (ctas > 1 && (dev < 0 || dev >= 64 || !__atomic_load_n(&holds[dev], __ATOMIC_ACQUIRE))) {
+            int n = 0;
+            e = cudaOccupancyMaxActiveClusters(&n, update_kernel<kShared>, &cfg);
+            if (e == cudaErrorInvalidClusterSize || (e == cudaSuccess && n < 1)) {
+                (void)cudaGetLastError();
+                return DCP_MLA_CACHE8_ERR_CLUSTER;
+            }
+            if (e == cudaSuccess && dev >= 0 && dev < 64) __atomic_store_n(&holds[dev], 1, __ATOMIC_RELEASE);
+        }
+        if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, update_kernel<kShared>, p);
     }
     if (e != cudaSuccess) (void)cudaGetLastError();
     return (int)e;

@@ -35,7 +35,8 @@ extern "C" {
 
 enum {
     DCP_MLA_CACHE8_ERR_BAD_PAGE = -211,  /* page not a power of two in range, or not a multiple of block */
-    DCP_MLA_CACHE8_ERR_ALIAS = -212      /* outputs that overlap inputs in a way that the call does not take */
+    DCP_MLA_CACHE8_ERR_ALIAS = -212,     /* outputs that overlap inputs in a way that the call does not take */
+    DCP_MLA_CACHE8_ERR_CLUSTER = -213    /* the device or context cannot hold a cluster of 16 blocks */
 };
 
 /*
@@ -66,6 +67,9 @@ enum {
  *            aligned (NULL where that is 0: out of place, with up to 16,384 rows and
  *            262,144 pages); its contents do not matter. Calls that share one are
  *            ordered.
+ *   Beyond 32 rows, 8,192 entries or 8,192 pages the call is one cluster of 16 blocks,
+ *   each a multiprocessor of its own: a whole GB300 has room for it, a smaller part (a
+ *   context with few multiprocessors) may not, and returns DCP_MLA_CACHE8_ERR_CLUSTER.
  *   shapes   0 <= B <= 65535, 1 <= M, M * page < 2^31 (here and in the calls without a
  *            page: M < 2^26), B * (M + 1) < 2^31, 1 <= P < 2^31, 0 <= shard < cp
  */

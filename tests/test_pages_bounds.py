@@ -90,3 +90,9 @@ def test_tiles_that_cannot_be_counted(B, cp, M):
                 Dk=576, Dv=512, T=M * 64, block=1, interleave=1, window=0, sinks=0, scale=1.0, lse_base_e=True,
                 workspace=A, workspace_bytes=1 << 40, out=A, lse=A, stream=0)
     refused(SHAPE, dcp.dcp_mla_cache8_decode, rows)
+
+
+def test_the_messages_of_pages():
+    seen = {dcp.dcp_mla_cache8_strerror(c) for c in (-211, -212, -213)}
+    assert len(seen) == 3 and "cluster of 16" in dcp.dcp_mla_cache8_strerror(-213)
+    assert dcp.dcp_mla_cache8_strerror(-214) not in seen
