@@ -643,6 +643,7 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps)
 append_block_kernel(const __grid_constant__ Q p) {
     __shared__ int32_t cu_s[kCounted ? kCountedRows / 32 : kCuShared + 1];
     __shared__ Place list[kCounted ? 1 : 32 * kWarps];
+    __shared__ int64_t at_s[kCounted ? 1 : 32 * kWarps];  // the listed blocks' places
     __shared__ int found;
     __shared__ float peak_s[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -710,7 +711,13 @@ append_block_kernel(const __grid_constant__ Q p) {
                 if (w.loc == held || (w.loc & (block - 1)) == 0) {
                     w.end = held_tokens(w.len + w.count, w.shard, p.cp, p.interleave);
                     if ((int64_t)w.end > p.T) w.end = (uint32_t)p.T;
-                    list[atomicAdd(&found, 1)] = w;
+                    // (only what has a place is listed: for each of those the CTA meets, before `found` begins again)
+                    const int64_t at = token_place(p, w.shard, w.row, w.loc & ~(block - 1));
+                    if (at >= 0) {
+                        const int k = atomicAdd(&found, 1);
+                        list[k] = w;
+                        at_s[k] = at;
+                    }
                 }
             }
             __syncthreads();
@@ -719,8 +726,13 @@ append_block_kernel(const __grid_constant__ Q p) {
         for (int i = 0; i < nfound; ++i) {  // (in any order: blocks are independent of each other)
             if constexpr (!kCounted) w = list[i];
             const uint32_t b0 = w.loc & ~(block - 1);
-            const int64_t at = token_place(p, w.shard, w.row, b0);
-            if (at < 0) continue;  // (the same in every thread)
+            int64_t at;
+            if constexpr (kCounted) {
+                at = token_place(p, w.shard, w.row, b0);
+                if (at < 0) continue;  // (the same in every thread, and nothing else is shared between turns)
+            } else {
+                at = at_s[i];
+            }
             uint8_t* const kv = p.kv[w.shard] + (at - b0) * p.Dk;  // as if of token 0
             float* const scale = p.scales[w.shard] + scale_place(p, w.row, at, b0);
             const uint32_t end = w.end < b0 + block ? w.end : b0 + block;
