@@ -6,14 +6,17 @@ each ``page`` tokens of a row; -1: none) and refs [P] int32 (how many rows hold 
 page; 0: free). Tables and refs are the same for all layers. It starts as tables
 of -1 and refs of 0, and a serving step chains
 
-    tables, refs, copies, missing = mla_cache8_pages_update(tables, refs, parents, lens, lens + 1, page=64)
+    wants = torch.where(parents < 0, 0, lens + 1)  # (a row ends with parents -1, lens 0 and wants 0)
+    tables, refs, copies, missing = mla_cache8_pages_update(tables, refs, parents, lens, wants, page=64)
     mla_cache8_pages_copy(caches_of_all_layers, scales_of_all_layers, copies)
     mla_cache8_append(latent, k_pe, [cache], [scale], lens, tables=[tables], ...)
-    out, lse = mla_cache8_decode(q, [cache], [scale], lens + 1, scale, tables=[tables], ...)
+    out, lse = mla_cache8_decode(q, [cache], [scale], wants, scale, tables=[tables], ...)
 
 Streams, errors and what a call allocates: as in cache8.py. Nothing is read back to
 the host, so that a step can be captured into a graph (``missing`` tells a program
-that looks at it that the pool ran out).
+that looks at it that the pool ran out; rows then lack pages, and one whose copy could
+not be made has lost the tokens that it kept in that page: a program that wants to go
+back keeps the state before, with ``out``).
 """
 from __future__ import annotations
 
@@ -98,13 +101,15 @@ def mla_cache8_pages_update(tables, refs, parents, keeps, wants, *, page: int, c
     """Rows take over other rows' pages, are cut back, end, begin and grow, all at once.
 
     Row b keeps the first keeps[b] positions of what row parents[b] held (b itself to
-    go on; -1: nothing) and gets pages for wants[b] positions (all int32 [B]; positions
-    of the whole sequence, of which shard ``shard`` of ``cp`` has its part). Pages are
+    go on; -1: nothing, and with wants[b] 0 the row ends) and gets pages for wants[b]
+    positions (all int32 [B]; positions of the whole sequence, of which shard ``shard``
+    of ``cp`` has its part; keeps[b] is a length of row parents[b]). Pages are
     shared, not copied, but for one that row b is about to write (wants[b] > keeps[b])
     behind kept tokens while another row holds it: row b gets a fresh one in its place
     and copies[b] = (old, new), for mla_cache8_pages_copy; other rows of copies are -1.
     Fresh pages are the free ones with the lowest numbers, dealt in row order; where
-    they run out the entry is -1 and missing counts it. out: None changes tables and
+    they run out the entry is -1 and missing counts it (where that was to be a copy, the
+    row has let go of the old page and of its tokens there). out: None changes tables and
     refs in place, or a pair of other tensors of their shapes. copies: int32 [B, 2],
     missing: int32 [1] (allocated when not given). Returns (tables, refs, copies,
     missing)."""

@@ -56,7 +56,9 @@ enum {
  * (-1, -1). If all who hold it are such rows, the last of them keeps it.
  * Fresh pages are those with refs 0 after all releases, the lowest first, dealt to
  * rows in order, in a row the copy's first and then by slot. Where they run out the
- * entry is -1 (and there is no copy), and *missing counts these; else it is 0.
+ * entry is -1, and *missing counts these; else it is 0. Where that was to be a copy's
+ * page there is no copy, and the row has let go of the old one and of its tokens there:
+ * a program that wants to go back to the state before writes to other buffers.
  *   tables_out, refs_out  either tables and refs themselves (in place), or buffers
  *            that overlap neither
  *   copies   [B, 2] int32, 8-byte aligned; missing: one int32
