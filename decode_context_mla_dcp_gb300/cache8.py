@@ -403,7 +403,9 @@ def mla_cache8_decode(q, caches, scales, seq_lens, scale: float, *, block: int =
     consecutive rows) and shared (int32 [B]: positions that a group's rows have in
     common, in the same pages) let rows attend to a common prefix together;
     mla_cache8_groups makes both. A row that is shorter than that (length 0: it has
-    ended) takes no part, the first one neither. The result is the same without."""
+    ended) takes no part, the first one neither. The result is the same without: groups
+    save time where the prefix is long beside the rows' own tokens, and cost some where
+    it is short (see the C header)."""
     lib, torch = _ready()
     index, B, T, dk, kv, sc = _shards(caches, scales, block, interleave)
     if tables is not None:

@@ -82,7 +82,8 @@ def _space(workspace, key, ask, index):
 def mla_cache8_groups(rows, shared, device="cuda"):
     """The groups of a batch for mla_cache8_decode, from the host: rows[g] consecutive
     rows of the batch begin with the same shared[g] positions, in the same pages (a row
-    alone is a group of 1). Returns (groups int32 [B, 2], shared int32 [B])."""
+    alone is a group of 1). Worth it where shared is long beside the rows' own tokens
+    (dcp_mla_pages.h says how long). Returns (groups int32 [B, 2], shared int32 [B])."""
     import torch
     rows, shared = [int(n) for n in rows], [int(n) for n in shared]
     if len(rows) != len(shared) or min(rows + shared, default=0) < 0 or max(shared, default=0) >= 1 << 31:

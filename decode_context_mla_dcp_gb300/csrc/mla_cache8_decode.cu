@@ -46,11 +46,12 @@
 // there is no third stage and one CTA a multiprocessor. By the clock of the MMA warp a
 // tile's turn is 930 cycles to issue the scores and 1,460 the values; the others are
 // waits, each some 100 to 300: for P, for slices, for the scores' place, for what comes.
-//   measured, 128 heads: 64 ragged rows of up to 16K tokens 128 to 137 us with their
-//   lengths, 252 to 258 us for 10^6 tokens; 8 rows x 4096 tokens 22.9 us, of which 16
+//   measured, 128 heads: 64 ragged rows of up to 16K tokens 119 to 138 us with their
+//   lengths (six sets of 465,318 to 547,763 tokens), 251 to 260 us for 10^6 tokens, 512
+//   wide 111 to 128 and 232 to 242; 8 rows x 4096 tokens 22.6 to 22.9 us, of which 16
 //   are the main kernel (4 tiles a CTA between 10,000 cycles to begin and 6,000 to
 //   end) and 6 the join; 16 heads, 200 tokens: 8.1 to 8.5 us. One shard of 8 held, 8 rows x
-//   4096 of its tokens: 24 us.
+//   4096 of its tokens: 24.3 us.
 // With 16 and 32 heads 64 ragged rows x 16K take 60 and 62 us against 45 of their
 // bytes: some 16 us are the beginning, the end and the join, and the MMA warp's turn
 // (46 cycles an MMA whatever its N, and the waits between) is near the rest.
@@ -60,13 +61,15 @@
 // zeros where there is no page. The loading warps bring the tile's page numbers with its
 // description; a token without a page is masked like one that is not visible. One bulk
 // request a page brings the tile after next to L2. 64 ragged rows x 16K x 128 heads take
-// 124 us in pages of 64 and 123 in pages of 128, the same lengths in rows 119.5.
+// 124 us in pages of 64 and 123 in pages of 128, the same lengths in rows 119.5 (six sets
+// of lengths: pages of 64 cost 4 to 5% more than rows).
 //
 // Groups. Rows that share a prefix have their heads side by side in blocks of 64 over
 // the prefix's tiles, so that 16 heads a row cost a quarter of the tiles' turns; what a
 // row has behind the prefix, whole tiles of which are the prefix's, is a line of its own,
 // and the join weighs both. 64 rows of 16 heads behind two prefixes of 16K with up to
-// 1,024 tokens of their own: 55.6 us, 101 without groups; floor 20 (the products at the
+// 1,024 tokens of their own: 55.6 us, 101 without groups; 64 rows of 16 heads behind 128
+// shared tokens with up to 16K of their own 94 us, 66 without; floor of the first 20 (the products at the
 // bf16 rate). Bound as above, at 2.0 us a tile: 2,464 tiles and changes of line are 16 a
 // CTA, 33 us of it, and the beginning, the end and the join are the rest.
 //
@@ -98,7 +101,8 @@ constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
 // Three warps load: the first slice, the next two, and the last with the rope slice (the second and third warp stand behind
 // the MMA warp). A request takes its warp some 150 cycles, a tile has 5 of them, in pages up to 20, and a slice's place is
 // free only shortly before its next tokens are wanted. (A fourth would leave 80 registers a thread. 64 ragged rows x 16K x
-// 128 heads: rows 130.5 us with one, 119.5 with three; in pages of 32, 64, 128 tokens 157, 147 and 141, and 132, 129, 128.)
+// 128 heads, when this was changed: rows 130.5 us with one, 119.5 with three; in pages of 32, 64, 128 tokens 157, 147 and
+// 141, and 132, 129, 128.)
 constexpr int kThreads = kSoftThreads + 128;
 constexpr int kCpMax = DCP_MLA_CACHE8_CP_MAX;
 constexpr int64_t kMaxInterleave = 1 << 24;
@@ -1979,8 +1983,11 @@ int page_log2_of(int page) {
 // prefix's tiles for itself either way, and finds them in L2 without groups too.) And where there are tiles enough: blocks
 // of 64 heads, places and a join cost some 5 us more than 16 heads a row alone. (16 heads, one group, with groups and
 // without: 8 rows x 2,048 tokens, 144 tiles, 18.8 us and 12.9; 16 x 8,192, 1,056 tiles, 24.0 and 22.8; 8 x 32,768, 2,064
-// tiles, 31.2 and 33.5; 32 x 32,768, 8,256 tiles, 51.4 and 93.1. 40 heads, 16 x 8,192: 30.4 and 31.4.) What is known here is
-// what rows have room for, not their lengths. Each row takes places for partial results, so that there is a limit; and
+// tiles, 31.2 and 33.5; 32 x 32,768, 8,256 tiles, 51.4 and 93.1. 40 heads, 16 x 8,192: 30.4 and 31.4.) The rows' own tokens
+// are in blocks of 64 heads then too, and long ones cost what is saved and more: 64 rows of 16 heads behind 128, 4,096 and
+// 8,192 shared tokens with up to 16,384, 12,288 and 8,192 of their own 93.8, 77.1 and 64.6 us with groups, 66.0, 74.4 and
+// 82.9 without; of 32 heads 102.8, 82.1, 80.4, and 69.0, 78.0, 88.4. What is known here is what rows have room for, not
+// their lengths nor the prefix's: the header says when a caller should leave groups out. Each row takes places for partial results, so that there is a limit; and
 // where the tiles of twice as many lines could not be counted, a call goes without.
 bool uses_groups(bool grouped, int cp, int64_t B, int H, int64_t T) {
     return grouped && B >= 2 && B <= 2048 && H % 64 != 0 && B * cp * ((T + kTile - 1) / kTile) >= 1024 &&

@@ -472,7 +472,8 @@ constexpr int kCopyVecs = 9;  // 16-byte pieces of a thread: a part is 36 KiB, a
 // A CTA copies a part of a page of one pool, every load in flight before the first store; one with an empty pair has
 // nothing to do. Bound by DRAM: 3,605 of 8,192 pairs, pages of 64 tokens, 266 MB read and written, 41.6 us, 6.4 TB/s
 // (43.7 with stores that stay in L2; 45.4 with as many CTAs as are resident, each going over the list: a CTA's loads
-// then wait for its stores); a few pages 2.6 us.
+// then wait for its stores); a few pages 2.6 us. Empty pairs cost their CTAs: ten pages of 8,192 pairs 7.4 us in one
+// pool, 263 in 60 (3,605 pages in 20 and in 60 pools: 782 and 2,339).
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyParams p) {
     const int part = (int)(blockIdx.x % (unsigned)p.parts);
     const int2 c = p.copies[blockIdx.x / (unsigned)p.parts];

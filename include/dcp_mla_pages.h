@@ -147,9 +147,12 @@ int dcp_mla_cache8_read_paged(const void* const* kv_ptrs, const float* const* sc
  * multiplied with several rows' heads at a time where a row's heads do not fill the
  * kernel's blocks of 64. With H a multiple of 64, more than 2048 rows, or tables with
  * room for fewer than 1024 tiles of 128 tokens in all (B * cp * M * page / 128) or for
- * more than 2^29 (B * cp * (M * page / 128 + 2)), groups make no difference; with long
- * tables and short prefixes they cost some microseconds (16 heads: they pay from about
- * 2000 tiles of rows times prefix on). Groups do not go together with a window.
+ * more than 2^29 (B * cp * (M * page / 128 + 2)), groups make no difference. Elsewhere
+ * they are for prefixes that are long beside the rows' own tokens: they pay from about
+ * 2000 tiles of rows times prefix on, where the prefix is about as long as what rows
+ * have behind it, or longer; short of that they cost time, up to half of the call
+ * without them (64 rows of 16 heads, 128 shared tokens and up to 16K of their own: 94
+ * us, 66 without), and a caller leaves them out. Groups do not go together with a window.
  *   groups   [B, 2] int32, 8-byte aligned; shared [B] int32 (below 1: nothing is
  *            shared). Entries that break these rules give undefined results in the
  *            rows concerned.
